@@ -358,6 +358,280 @@ int m3_rope_angles_cumsum(const float* theta, const float* phi0, float* phi,
                           int32_t Bt, int32_t L, int32_t H, int32_t npairs,
                           void* stream);
 
+/*
+ * ---------------------------------------------------------------- layer operators
+ * The operators that stand around a selective state-space core in a layer: the
+ * short causal convolution in front of it, the selective scan itself with a
+ * decay per channel and state (the two-term recurrence of "La dualita:
+ * Mamba-2 e Mamba-3", sec. "State Space Duality", with a diagonal A per
+ * channel), the gated norm behind it and the residual norm in front of the
+ * next block ("Mamba-3: un modello a spazio di stato progettato per
+ * l'inferenza" (cartesia.ai), "Normalizzazioni" and "Addio convoluzione
+ * corta", names them as the parts around the core).
+ *
+ * Common to all of them:
+ *   - Types: in_dtype M3_BF16 or M3_F32 for the activations; parameters
+ *     (taps, biases, A, D, gains, scales), states of the scan and the
+ *     gradients of parameters are float32.  All arithmetic is fp32; an output
+ *     is rounded once.
+ *   - Strides: a tensor with a field `*_ld` may be a slice of wider rows: ld
+ *     is the number of elements from one token (row) to the next, 0 meaning
+ *     dense; rows of all batch items follow each other at that distance, and
+ *     the elements within a row are dense.  Everything else is dense
+ *     row-major.  Pointers need the alignment of their elements only (rows
+ *     whose addresses allow it are read 16 bytes at a time).
+ *   - lengths [Bt] int32 or NULL: item b holds lengths[b] tokens (taken
+ *     into [0, L] on the device); what lies behind them is never used, whatever
+ *     it holds.  Forward outputs behind them are left as they were, gradients
+ *     of inputs behind them are set to zero, states end with the last token
+ *     held (lengths[b] = 0: the state passes through).
+ *   - Outputs do not alias inputs or each other, except where noted.
+ */
+
+/* Short causal depthwise convolution over the token axis:
+ *   y[b,t,d] = act(bias[d] + sum_{k<W} w[d,k] x[b, t-(W-1)+k, d]),
+ * act = SiLU with silu = 1, identity with 0.
+ *   x [Bt, L, D] (x_ld), w [D, W], bias [D] or NULL, y [Bt, L, D].
+ *   state [Bt, W-1, D] in_dtype or NULL (zeros): the inputs before the first
+ *   token, oldest first; state_out (nullable): the W-1 inputs that end with the
+ *   last token, may be `state` itself.  W in {2, 3, 4}. */
+typedef struct m3_conv_args {
+  int32_t Bt, L, D, W;
+  int32_t in_dtype; /* m3_dtype */
+  int32_t silu;     /* 0 or 1 */
+  const void* x;
+  int64_t x_ld;
+  const float* w;
+  const float* bias;
+  const int32_t* lengths;
+  const void* state;
+  void* y;
+  void* state_out;
+} m3_conv_args;
+int m3_causal_conv(const m3_conv_args* args, void* stream);
+
+/* One token of it: x [Bt, D] (x_ld between the batch rows), state [Bt, W-1, D]
+ * updated in place, or read only when state_out is given (which may be `state`
+ * too); y [Bt, D]. */
+typedef struct m3_conv_step_args {
+  int32_t Bt, D, W;
+  int32_t in_dtype;
+  int32_t silu;
+  const void* x;
+  int64_t x_ld;
+  const float* w;
+  const float* bias;
+  void* state;
+  void* state_out; /* NULL: state */
+  void* y;
+} m3_conv_step_args;
+int m3_causal_conv_step(const m3_conv_step_args* args, void* stream);
+
+/* Gradients of the convolution for dy [Bt, L, D] (dense): dx [Bt, L, D], dw
+ * [D, W], dbias [D] (nullable), dstate [Bt, W-1, D] in_dtype (nullable;
+ * gradient of the carry-in).  The carry-out is not differentiated.
+ * workspace: m3_causal_conv_backward_workspace_size bytes, 256-byte aligned
+ * (partial sums of dw and dbias, joined in a fixed order). */
+typedef struct m3_conv_backward_args {
+  int32_t Bt, L, D, W;
+  int32_t in_dtype;
+  int32_t silu;
+  const void* x;
+  int64_t x_ld;
+  const float* w;
+  const float* bias;
+  const int32_t* lengths;
+  const void* state;
+  const void* dy;
+  void* dx;
+  float* dw;
+  float* dbias;
+  void* dstate;
+  void* workspace;
+  size_t workspace_bytes;
+} m3_conv_backward_args;
+size_t m3_causal_conv_backward_workspace_size(const m3_conv_backward_args* args);
+int m3_causal_conv_backward(const m3_conv_backward_args* args, void* stream);
+
+/* Selective scan, a diagonal state per channel:
+ *   delta = softplus(dt + dt_bias[d]) with dt_softplus = 1 (dt_bias nullable),
+ *           dt itself with 0 (dt_bias must then be NULL);
+ *   h_t[d,n] = exp(delta_t[d] A[d,n]) h_{t-1}[d,n] + delta_t[d] x_t[d] B_t[g,n];
+ *   o_t[d] = sum_n C_t[g,n] h_t[d,n] + D[d] x_t[d];
+ *   y_t[d] = o_t[d] silu(z_t[d])   (z NULL: y = o),  g = d / (D / G).
+ *   x, dt, z [Bt, L, D] (x_ld, dt_ld, z_ld), B, C [Bt, L, G, N] (B_ld, C_ld),
+ *   A [D, N], D_skip [D] or NULL; h0 [Bt, D, N] or NULL (zeros); y [Bt, L, D];
+ *   h_final [Bt, D, N] (nullable).
+ * Sizes: N in 1..64, G divides D.
+ * workspace: optional; with few (batch, channel) pairs the token axis is cut
+ * into segments scanned at once, whose states are joined, when a workspace of
+ * m3_selective_scan_workspace_size bytes (256-byte aligned; 0: not used) is
+ * given.  It is overwritten by every call; the size depends on the shape. */
+typedef struct m3_scan_args {
+  int32_t Bt, L, D, N, G;
+  int32_t in_dtype;
+  int32_t dt_softplus;
+  const void* x;
+  int64_t x_ld;
+  const void* dt;
+  int64_t dt_ld;
+  const float* A;
+  const void* B;
+  int64_t B_ld;
+  const void* C;
+  int64_t C_ld;
+  const float* D_skip;
+  const void* z;
+  int64_t z_ld;
+  const float* dt_bias;
+  const float* h0;
+  const int32_t* lengths;
+  void* y;
+  float* h_final;
+  void* workspace;
+  size_t workspace_bytes;
+} m3_scan_args;
+size_t m3_selective_scan_workspace_size(const m3_scan_args* args);
+int m3_selective_scan(const m3_scan_args* args, void* stream);
+
+/* One token of it: x, dt, z [Bt, D], B, C [Bt, G, N] (each `*_ld` between the
+ * batch rows), h [Bt, D, N] updated in place, or read only when h_out is given
+ * (which may be h too); y [Bt, D]. */
+typedef struct m3_scan_step_args {
+  int32_t Bt, D, N, G;
+  int32_t in_dtype;
+  int32_t dt_softplus;
+  const void* x;
+  int64_t x_ld;
+  const void* dt;
+  int64_t dt_ld;
+  const float* A;
+  const void* B;
+  int64_t B_ld;
+  const void* C;
+  int64_t C_ld;
+  const float* D_skip;
+  const void* z;
+  int64_t z_ld;
+  const float* dt_bias;
+  float* h;
+  float* h_out; /* NULL: h */
+  void* y;
+} m3_scan_step_args;
+int m3_selective_scan_step(const m3_scan_step_args* args, void* stream);
+
+/* Gradients of the scan for dy [Bt, L, D] (dense) and dh_final [Bt, D, N]
+ * (nullable).  Outputs: dx, ddt [Bt, L, D], dB, dC [Bt, L, G, N] in in_dtype;
+ * dA [D, N]; dD [D] (required iff D_skip), dz [Bt, L, D] (required iff z),
+ * ddt_bias [D] (required iff dt_bias), dh0 [Bt, D, N] (nullable).  ddt is the
+ * gradient of dt as given (before the softplus).  workspace:
+ * m3_selective_scan_backward_workspace_size bytes, 256-byte aligned. */
+typedef struct m3_scan_backward_args {
+  m3_scan_args fwd; /* the forward's inputs; y, h_final, workspace are not read */
+  const void* dy;
+  const float* dh_final;
+  void* dx;
+  void* ddt;
+  float* dA;
+  void* dB;
+  void* dC;
+  float* dD;
+  void* dz;
+  float* ddt_bias;
+  float* dh0;
+  void* workspace;
+  size_t workspace_bytes;
+} m3_scan_backward_args;
+size_t m3_selective_scan_backward_workspace_size(const m3_scan_backward_args* args);
+int m3_selective_scan_backward(const m3_scan_backward_args* args, void* stream);
+
+/* Gated group RMS norm over rows of D = G groups of D / G:
+ *   gate_first = 1: v = x silu(z),  y = v rsqrt(mean_group(v^2) + eps) w;
+ *   gate_first = 0: y = x rsqrt(mean_group(x^2) + eps) w silu(z).
+ * x, z [M, D] (x_ld, z_ld; z NULL: no gate), w [D] or NULL (ones), y [M, D]
+ * (may be x or z themselves where those are dense).  eps >= 0; a group of zeros
+ * with eps = 0 gives NaN. */
+typedef struct m3_gated_norm_args {
+  int64_t M;
+  int32_t D, G;
+  int32_t in_dtype;
+  int32_t gate_first;
+  float eps;
+  const void* x;
+  int64_t x_ld;
+  const void* z;
+  int64_t z_ld;
+  const float* w;
+  void* y;
+} m3_gated_norm_args;
+int m3_gated_norm(const m3_gated_norm_args* args, void* stream);
+
+/* Its gradients for dy [M, D] (dense): dx, dz [M, D] (dz required iff z), dw [D]
+ * (required iff w). */
+typedef struct m3_gated_norm_backward_args {
+  m3_gated_norm_args fwd; /* y is not read */
+  const void* dy;
+  void* dx;
+  void* dz;
+  float* dw;
+  void* workspace;
+  size_t workspace_bytes;
+} m3_gated_norm_backward_args;
+size_t m3_gated_norm_backward_workspace_size(const m3_gated_norm_backward_args* args);
+int m3_gated_norm_backward(const m3_gated_norm_backward_args* args, void* stream);
+
+/* Residual sum and RMS norm over rows of D:
+ *   h = residual + scale x (residual NULL: 0; scale [D], NULL: 1),
+ *   residual_out = h (nullable; may be `residual` itself),
+ *   y = h rsqrt(mean(h^2) + eps) w   (w [D], NULL: ones; h unrounded).
+ * x [M, D] (x_ld), y [M, D] in_dtype; residual, residual_out [M, D] res_dtype:
+ * in_dtype or M3_F32. */
+typedef struct m3_residual_norm_args {
+  int64_t M;
+  int32_t D;
+  int32_t in_dtype;
+  int32_t res_dtype;
+  float eps;
+  const void* x;
+  int64_t x_ld;
+  const void* residual;
+  const float* scale;
+  const float* w;
+  void* y;
+  void* residual_out;
+} m3_residual_norm_args;
+int m3_residual_norm(const m3_residual_norm_args* args, void* stream);
+
+/* Its gradients at the stored sum h = residual_out [M, D] res_dtype, for dy
+ * [M, D] in_dtype and dresidual_out [M, D] res_dtype (nullable: gradient that
+ * reaches h along the residual stream):
+ *   dh = dresidual_out + d(norm)/dh,  dresidual = dh (nullable),
+ *   dx = scale dh (nullable, in_dtype), dw [D] (required iff w), dscale [D]
+ *   (required iff scale) = sum_rows dh x.
+ * x (x_ld) is read for dscale only.  dresidual may be dresidual_out itself. */
+typedef struct m3_residual_norm_backward_args {
+  int64_t M;
+  int32_t D;
+  int32_t in_dtype;
+  int32_t res_dtype;
+  float eps;
+  const void* h;
+  const void* x;
+  int64_t x_ld;
+  const float* scale;
+  const float* w;
+  const void* dy;
+  const void* dresidual_out;
+  void* dx;
+  void* dresidual;
+  float* dw;
+  float* dscale;
+  void* workspace;
+  size_t workspace_bytes;
+} m3_residual_norm_backward_args;
+size_t m3_residual_norm_backward_workspace_size(const m3_residual_norm_backward_args* args);
+int m3_residual_norm_backward(const m3_residual_norm_backward_args* args, void* stream);
+
 /* Static description of a status code (never NULL). */
 const char* m3_status_string(int status);
 

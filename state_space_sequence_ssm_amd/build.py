@@ -19,7 +19,8 @@ LIB = os.path.join(PKG, "libm3ssm.so")
 SOURCES = ["prefill_bf16_n128.hip", "prefill_bf16_n128_pro.hip", "prefill_bf16_n64.hip", "prefill_bf16_n64_pro.hip",
            "prefill_bf16_n32.hip", "prefill_bf16_n32_pro.hip", "prefill_bf16_n16.hip", "prefill_bf16_n16_pro.hip",
            "backward_main.hip", "backward.hip", "backward_pre.hip", "prefill_f32.hip", "decode.hip", "decode_mma.hip",
-           "api.hip", "angles.hip", "split.hip", "prefill_bf16.hip"]
+           "scan_backward.hip", "norms.hip", "scan.hip", "conv.hip", "api.hip", "api_layer.hip", "angles.hip", "split.hip",
+           "prefill_bf16.hip"]
 ARCH = "gfx950"
 
 
@@ -68,7 +69,8 @@ def build(verbose: bool = False) -> str:
 
 SAN_DIR = os.path.join(OBJ, "hostsan")
 SAN_LIB = os.path.join(SAN_DIR, "libm3ssm_hostsan.so")
-# host-side sanitizers only: each flag goes to the host compilation of api.hip
+# host-side sanitizers only: each flag goes to the host compilation of the API layer
+SAN_SOURCES = ["api.hip", "api_layer.hip"]
 SAN_FLAGS = ["-Xarch_host", "-fsanitize=address", "-Xarch_host", "-fsanitize=undefined",
              "-Xarch_host", "-fno-sanitize-recover=all", "-Xarch_host", "-fno-omit-frame-pointer",
              "-Xarch_host", "-g"]
@@ -87,26 +89,28 @@ def asan_runtime() -> str:
 
 
 def build_hostsan(verbose: bool = False) -> str:
-    """libm3ssm_hostsan.so: the host-side C-ABI layer (api.hip: argument
-    validation and dispatch) built with AddressSanitizer and UBSan, linked
-    with the regular kernel objects of the last build().  For host-only
+    """libm3ssm_hostsan.so: the host-side C-ABI layer (api.hip, api_layer.hip:
+    argument validation and dispatch) built with AddressSanitizer and UBSan,
+    linked with the regular kernel objects of the last build().  For host-only
     tests of the validation paths (no kernel is launched)."""
     os.makedirs(SAN_DIR, exist_ok=True)
-    objs = [os.path.join(OBJ, os.path.splitext(x)[0] + ".o") for x in SOURCES if x != "api.hip"]
+    objs = [os.path.join(OBJ, os.path.splitext(x)[0] + ".o") for x in SOURCES if x not in SAN_SOURCES]
     missing = [o for o in objs if not os.path.exists(o)]
     if missing:
         raise RuntimeError(f"run build() first: missing {missing}")
-    api_o = os.path.join(SAN_DIR, "api_hostsan.o")
-    cmd = [hipcc(), *cflags(), *SAN_FLAGS, "-c", os.path.join(CSRC, "api.hip"), "-o", api_o]
-    r = subprocess.run(cmd, capture_output=True, text=True)
-    if r.returncode != 0:
-        raise RuntimeError("hipcc (host sanitizers) failed:\n" + r.stdout + r.stderr)
+    api_os = []
+    for src in SAN_SOURCES:
+        api_os.append(os.path.join(SAN_DIR, os.path.splitext(src)[0] + "_hostsan.o"))
+        cmd = [hipcc(), *cflags(), *SAN_FLAGS, "-c", os.path.join(CSRC, src), "-o", api_os[-1]]
+        r = subprocess.run(cmd, capture_output=True, text=True)
+        if r.returncode != 0:
+            raise RuntimeError("hipcc (host sanitizers) failed:\n" + r.stdout + r.stderr)
     # a plain host link: the objects already embed their device code
     llvm = os.path.join(os.environ.get("ROCM_PATH", "/opt/rocm"), "llvm")
     rocm_lib = os.path.join(os.environ.get("ROCM_PATH", "/opt/rocm"), "lib")
     tmp = SAN_LIB + ".tmp"
     cmd = [os.path.join(llvm, "bin", "clang++"), "-shared", "-fPIC", "-shared-libsan", "-fsanitize=address,undefined",
-           "-o", tmp, api_o, *objs, "-L" + rocm_lib, "-Wl,-rpath," + rocm_lib, "-lamdhip64"]
+           "-o", tmp, *api_os, *objs, "-L" + rocm_lib, "-Wl,-rpath," + rocm_lib, "-lamdhip64"]
     if verbose:
         print(" ".join(cmd), flush=True)
     r = subprocess.run(cmd, capture_output=True, text=True)

@@ -1,0 +1,417 @@
+// Short causal depthwise convolution: prompts, single tokens and backward.
+//
+//   y[t,d] = act(bias[d] + sum_k w[d,k] x[t-(W-1)+k, d])
+//
+// Memory bound: 2 W + 4 operations per element against 2 elements moved.
+#include "layer_internal.hpp"
+
+namespace m3 {
+namespace {
+
+constexpr int kRows = 4;  // token rows loaded together by one thread
+
+struct ConvP {
+  const void* x;
+  int64_t ld;
+  const float* w;
+  const float* bias;
+  const int32_t* lengths;
+  const void* state;
+  void* state_out;
+  void* y;
+  int L, D, tt;
+  uint32_t nv, ntiles, total;
+  int silu;
+};
+
+// One thread: V channels (one 16-byte word per row) down a tile of `tt`
+// tokens, the last W - 1 inputs held in registers, so that a row is read once
+// per tile and W - 1 rows again at its start.
+template <typename T, int W, int V>
+__global__ __launch_bounds__(256) void conv_kernel(ConvP p) {
+  const uint32_t idx = blockIdx.x * 256u + threadIdx.x;
+  if (idx >= p.total) return;
+  const uint32_t cv = idx % p.nv, r = idx / p.nv;
+  const int tile = int(r % p.ntiles), b = int(r / p.ntiles);
+  const int d0 = int(cv) * V;
+  const int len = item_length(p.lengths, b, p.L);
+  const int t0 = tile * p.tt;
+  const int t1 = t0 + p.tt < len ? t0 + p.tt : len;
+  const T* x = static_cast<const T*>(p.x) + int64_t(b) * p.L * p.ld + d0;
+  const T* state = static_cast<const T*>(p.state);
+  if (state != nullptr) state += int64_t(b) * (W - 1) * p.D + d0;
+
+  float xs[W - 1 + kRows][V];
+#pragma unroll
+  for (int j = 0; j < W - 1; ++j) {
+    if (tile > 0 && t0 < len) {
+      unpack<T, V>(load_pack<T, V>(x + int64_t(t0 - (W - 1) + j) * p.ld), xs[j]);
+    } else if (tile == 0 && state != nullptr) {
+      unpack<T, V>(load_pack<T, V>(state + int64_t(j) * p.D), xs[j]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < V; ++i) xs[j][i] = 0.f;
+    }
+  }
+  if (tile == 0 && p.state_out != nullptr) {
+    // inputs len - (W-1) .. len - 1; rows of `state` are read in ascending
+    // order ahead of the row written, so the carry may be updated in place
+    T* so = static_cast<T*>(p.state_out) + int64_t(b) * (W - 1) * p.D + d0;
+#pragma unroll
+    for (int j = 0; j < W - 1; ++j) {
+      const int t = len - (W - 1) + j;
+      Pack<T, V> q{};
+      if (t >= 0) q = load_pack<T, V>(x + int64_t(t) * p.ld);
+      else if (state != nullptr) q = load_pack<T, V>(state + int64_t(len + j) * p.D);
+      *reinterpret_cast<Pack<T, V>*>(so + int64_t(j) * p.D) = q;
+    }
+  }
+  if (t0 >= t1) return;
+
+  float w[W][V], bias[V];
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    bias[i] = p.bias != nullptr ? p.bias[d0 + i] : 0.f;
+#pragma unroll
+    for (int k = 0; k < W; ++k) w[k][i] = p.w[int64_t(d0 + i) * W + k];
+  }
+  T* y = static_cast<T*>(p.y) + int64_t(b) * p.L * p.D + d0;
+  // rows past the tile's end re-read its last row (no branch around the loads)
+  Pack<T, V> q[kRows];
+#pragma unroll
+  for (int i = 0; i < kRows; ++i) q[i] = load_pack<T, V>(x + int64_t(t0 + i < t1 ? t0 + i : t1 - 1) * p.ld);
+  for (int t = t0; t < t1; t += kRows) {
+#pragma unroll
+    for (int i = 0; i < kRows; ++i) unpack<T, V>(q[i], xs[W - 1 + i]);
+    if (t + kRows < t1) {
+#pragma unroll
+      for (int i = 0; i < kRows; ++i) {
+        const int tn = t + kRows + i;
+        q[i] = load_pack<T, V>(x + int64_t(tn < t1 ? tn : t1 - 1) * p.ld);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < kRows; ++i) {
+      float o[V];
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        float a = bias[v];
+#pragma unroll
+        for (int k = 0; k < W; ++k) a = fmaf(w[k][v], xs[i + k][v], a);
+        o[v] = p.silu ? silu_f(a) : a;
+      }
+      if (t + i < t1) store_pack<T, V>(y + int64_t(t + i) * p.D, o);
+    }
+#pragma unroll
+    for (int j = 0; j < W - 1; ++j)
+#pragma unroll
+      for (int v = 0; v < V; ++v) xs[j][v] = xs[j + kRows][v];
+  }
+}
+
+struct ConvStepP {
+  const void* x;
+  int64_t ld;
+  const float* w;
+  const float* bias;
+  const void* state;
+  void* state_out;
+  void* y;
+  int D;
+  uint32_t nv, total;
+  int silu;
+};
+
+// One token: a thread holds V channels of one item, reads their W - 1 carried
+// inputs and the new one, writes y and the carry moved up by one row.
+template <typename T, int W, int V>
+__global__ __launch_bounds__(64) void conv_step_kernel(ConvStepP p) {
+  const uint32_t idx = blockIdx.x * 64u + threadIdx.x;
+  if (idx >= p.total) return;
+  const uint32_t cv = idx % p.nv, b = idx / p.nv;
+  const int d0 = int(cv) * V;
+  const T* st = static_cast<const T*>(p.state) + int64_t(b) * (W - 1) * p.D + d0;
+  T* so = static_cast<T*>(p.state_out) + int64_t(b) * (W - 1) * p.D + d0;
+  Pack<T, V> q[W];
+#pragma unroll
+  for (int j = 0; j < W - 1; ++j) q[j] = load_pack<T, V>(st + int64_t(j) * p.D);
+  q[W - 1] = load_pack<T, V>(static_cast<const T*>(p.x) + int64_t(b) * p.ld + d0);
+  float o[V];
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    float a = p.bias != nullptr ? p.bias[d0 + v] : 0.f;
+#pragma unroll
+    for (int k = 0; k < W; ++k) a = fmaf(p.w[int64_t(d0 + v) * W + k], to_f32(q[k].e[v]), a);
+    o[v] = p.silu ? silu_f(a) : a;
+  }
+  store_pack<T, V>(static_cast<T*>(p.y) + int64_t(b) * p.D + d0, o);
+#pragma unroll
+  for (int j = 0; j < W - 1; ++j) *reinterpret_cast<Pack<T, V>*>(so + int64_t(j) * p.D) = q[j + 1];
+}
+
+struct ConvBwP {
+  const void* x;
+  int64_t ld;
+  const float* w;
+  const float* bias;
+  const int32_t* lengths;
+  const void* state;
+  const void* dy;
+  void* dx;
+  void* dstate;
+  float* part;  // [Bt * ngroups][W + 1][D]
+  int L, D, tt;
+  uint32_t nv, ncb, ngroups;
+  int lgcx;
+  int silu;
+};
+
+// dpre[t] = dy[t] act'(pre[t]);  dx[t] = sum_j dpre[t+j] w[W-1-j];
+// dw[k] = sum_t dpre[t] x[t-(W-1)+k];  dbias = sum_t dpre[t].
+// One thread: V channels down `tt` tokens and the W - 1 after them, whose dpre
+// its last dx need; a block is CX columns times 256 / CX tiles, whose sums of
+// dw and dbias are joined in LDS before they go to the workspace.
+template <typename T, int W, int V>
+__global__ __launch_bounds__(256) void conv_backward_kernel(ConvBwP p) {
+  __shared__ float red[256 * (W + 1) * V];
+  const int CX = 1 << p.lgcx, RY = 256 >> p.lgcx;
+  const int col = threadIdx.x & (CX - 1), row = threadIdx.x >> p.lgcx;
+  const uint32_t cb = blockIdx.x % p.ncb, rest = blockIdx.x / p.ncb;
+  const uint32_t grp = rest % p.ngroups, b = rest / p.ngroups;
+  const uint32_t cv = (cb << p.lgcx) + col;
+  const int t0 = (int(grp) * RY + row) * p.tt;
+  const int len = item_length(p.lengths, int(b), p.L);
+  const bool on = cv < p.nv && t0 < p.L;
+  const int d0 = int(cv) * V;
+  float dw[W + 1][V];
+#pragma unroll
+  for (int k = 0; k <= W; ++k)
+#pragma unroll
+    for (int v = 0; v < V; ++v) dw[k][v] = 0.f;
+  if (on) {
+    const T* x = static_cast<const T*>(p.x) + int64_t(b) * p.L * p.ld + d0;
+    const T* dy = static_cast<const T*>(p.dy) + int64_t(b) * p.L * p.D + d0;
+    T* dx = static_cast<T*>(p.dx) + int64_t(b) * p.L * p.D + d0;
+    const T* state = static_cast<const T*>(p.state);
+    if (state != nullptr) state += int64_t(b) * (W - 1) * p.D + d0;
+    T* dst = static_cast<T*>(p.dstate);
+    if (dst != nullptr) dst += int64_t(b) * (W - 1) * p.D + d0;
+    float w[W][V], bias[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      bias[i] = p.bias != nullptr ? p.bias[d0 + i] : 0.f;
+#pragma unroll
+      for (int k = 0; k < W; ++k) w[k][i] = p.w[int64_t(d0 + i) * W + k];
+    }
+    const int tend = t0 + p.tt < p.L ? t0 + p.tt : p.L;  // dx rows [t0, tend)
+    float xs[W][V], dp[W][V];
+#pragma unroll
+    for (int j = 0; j < W - 1; ++j) {
+      const int t = t0 - (W - 1) + j;
+#pragma unroll
+      for (int v = 0; v < V; ++v) xs[j + 1][v] = 0.f, dp[j + 1][v] = 0.f;
+      if (t >= 0) {
+        if (t < len) unpack<T, V>(load_pack<T, V>(x + int64_t(t) * p.ld), xs[j + 1]);
+      } else if (state != nullptr) {
+        unpack<T, V>(load_pack<T, V>(state + int64_t(t + W - 1) * p.D), xs[j + 1]);
+      }
+    }
+    for (int t = t0; t < tend + W - 1; ++t) {
+      // windows move up: xs[W-1] = x[t], dp[W-1] = dpre[t]
+#pragma unroll
+      for (int j = 0; j < W - 1; ++j)
+#pragma unroll
+        for (int v = 0; v < V; ++v) xs[j][v] = xs[j + 1][v], dp[j][v] = dp[j + 1][v];
+      float g[V];
+#pragma unroll
+      for (int v = 0; v < V; ++v) xs[W - 1][v] = 0.f, dp[W - 1][v] = 0.f;
+      if (t < len) {
+        unpack<T, V>(load_pack<T, V>(x + int64_t(t) * p.ld), xs[W - 1]);
+        unpack<T, V>(load_pack<T, V>(dy + int64_t(t) * p.D), g);
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+          float a = bias[v];
+#pragma unroll
+          for (int k = 0; k < W; ++k) a = fmaf(w[k][v], xs[k][v], a);
+          dp[W - 1][v] = p.silu ? g[v] * dsilu_f(a, sigmoid_f(a)) : g[v];
+        }
+        if (t < tend) {
+#pragma unroll
+          for (int v = 0; v < V; ++v) {
+#pragma unroll
+            for (int k = 0; k < W; ++k) dw[k][v] = fmaf(dp[W - 1][v], xs[k][v], dw[k][v]);
+            dw[W][v] += dp[W - 1][v];
+          }
+        }
+      }
+      const int q = t - (W - 1);  // dx row whose window is complete
+      float o[V];
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        o[v] = 0.f;
+#pragma unroll
+        for (int j = 0; j < W; ++j) o[v] = fmaf(dp[j][v], w[W - 1 - j][v], o[v]);
+      }
+      if (q >= t0) store_pack<T, V>(dx + int64_t(q) * p.D, o);
+      else if (q < 0 && dst != nullptr) store_pack<T, V>(dst + int64_t(q + W - 1) * p.D, o);
+    }
+  }
+#pragma unroll
+  for (int k = 0; k <= W; ++k)
+#pragma unroll
+    for (int v = 0; v < V; ++v) red[((row * (W + 1) + k) * V + v) * CX + col] = dw[k][v];
+  __syncthreads();
+  float* part = p.part + (int64_t(b) * p.ngroups + grp) * (W + 1) * p.D;
+  for (int i = threadIdx.x; i < (W + 1) * V * CX; i += 256) {
+    const int c = i & (CX - 1), kv = i >> p.lgcx, k = kv / V, v = kv % V;
+    const uint32_t ch = ((cb << p.lgcx) + c) * V + v;
+    float s = 0.f;
+    for (int r = 0; r < RY; ++r) s += red[((r * (W + 1) + k) * V + v) * CX + c];
+    if (ch < uint32_t(p.D)) part[int64_t(k) * p.D + ch] = s;
+  }
+}
+
+// Column sums: a block takes 64 columns, its 4 waves every fourth partial row.
+__global__ __launch_bounds__(256) void colsum_kernel(ColSum c) {
+  __shared__ float red[4][64];
+  const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6;
+  const int64_t col = int64_t(blockIdx.x) * 64 + lane;
+  float s = 0.f;
+  if (col < c.ncols) {
+#pragma unroll 8
+    for (int64_t r = wv; r < c.P; r += 4) s += c.part[r * c.ncols + col];
+  }
+  red[wv][lane] = s;
+  __syncthreads();
+  if (wv != 0 || col >= c.ncols) return;
+  s = (red[0][lane] + red[1][lane]) + (red[2][lane] + red[3][lane]);
+  int64_t k = col;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if (k < c.n[i]) {
+      if (c.dst[i] != nullptr) c.dst[i][i == 0 && c.taps > 0 ? (k % c.D) * c.taps + k / c.D : k] = s;
+      return;
+    }
+    k -= c.n[i];
+  }
+}
+
+// V channels per thread: a whole 16-byte word where width and addresses allow.
+template <typename T>
+constexpr int vec() {
+  return 16 / int(sizeof(T));
+}
+
+// Tokens per tile.  Long tiles read fewer rows twice (W - 1 of tt + W - 1),
+// short ones give more threads: halved while the card (256 CUs of 2048 lanes)
+// would hold fewer than a quarter of its lanes.
+int conv_tile(int64_t Bt, int L, int64_t nv, int most) {
+  int tt = most;
+  while (tt > 8 && Bt * ((L + tt - 1) / tt) * nv < 131072) tt /= 2;
+  return tt;
+}
+
+template <typename T, int W, int V>
+hipError_t run_conv(const m3_conv_args& a, hipStream_t s) {
+  const int64_t nv = a.D / V;
+  ConvP p{a.x, a.x_ld, a.w, a.bias, a.lengths, a.state, a.state_out, a.y, a.L, a.D, 0, 0, 0, 0, a.silu};
+  p.tt = conv_tile(a.Bt, a.L, nv, 32);
+  p.nv = uint32_t(nv);
+  p.ntiles = uint32_t((a.L + p.tt - 1) / p.tt);
+  p.total = uint32_t(nv * p.ntiles * a.Bt);
+  conv_kernel<T, W, V><<<(p.total + 255) / 256, 256, 0, s>>>(p);
+  return hipGetLastError();
+}
+template <typename T, int W, int V>
+hipError_t run_step(const m3_conv_step_args& a, hipStream_t s) {
+  const int64_t nv = a.D / V;
+  ConvStepP p{a.x, a.x_ld, a.w, a.bias, a.state, a.state_out, a.y, a.D, uint32_t(nv), uint32_t(nv * a.Bt), a.silu};
+  conv_step_kernel<T, W, V><<<(p.total + 63) / 64, 64, 0, s>>>(p);
+  return hipGetLastError();
+}
+
+struct BwGeom {
+  int lgcx, tt;
+  int64_t nv, ncb, ngroups;
+};
+BwGeom bw_geom(const m3_conv_backward_args& a, int V) {
+  BwGeom g;
+  g.nv = a.D / V;
+  g.lgcx = 3;
+  while (g.lgcx < 6 && (int64_t(1) << g.lgcx) < g.nv) ++g.lgcx;
+  g.ncb = (g.nv + (int64_t(1) << g.lgcx) - 1) >> g.lgcx;
+  g.tt = conv_tile(a.Bt, a.L, g.nv, 64);
+  const int64_t per = int64_t(g.tt) * (256 >> g.lgcx);
+  g.ngroups = (a.L + per - 1) / per;
+  return g;
+}
+bool bw_vec(const m3_conv_backward_args& a) {
+  const size_t e = a.in_dtype == M3_BF16 ? 2 : 4;
+  return rows_aligned(a.x, a.x_ld, e, 16) && rows_aligned(a.dy, a.D, e, 16) && rows_aligned(a.dx, a.D, e, 16) &&
+         rows_aligned(a.state, a.D, e, 16) && rows_aligned(a.dstate, a.D, e, 16);
+}
+template <typename T, int W, int V>
+hipError_t run_bw(const m3_conv_backward_args& a, hipStream_t s) {
+  const BwGeom g = bw_geom(a, V);
+  ConvBwP p{a.x, a.x_ld, a.w, a.bias, a.lengths, a.state, a.dy, a.dx, a.dstate, static_cast<float*>(a.workspace),
+            a.L, a.D, g.tt, uint32_t(g.nv), uint32_t(g.ncb), uint32_t(g.ngroups), g.lgcx, a.silu};
+  conv_backward_kernel<T, W, V><<<uint32_t(g.ncb * g.ngroups * a.Bt), 256, 0, s>>>(p);
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  ColSum c{};
+  c.part = p.part;
+  c.P = g.ngroups * a.Bt;
+  c.ncols = int64_t(W + 1) * a.D;
+  c.dst[0] = a.dw;
+  c.n[0] = int64_t(W) * a.D;
+  c.dst[1] = a.dbias;
+  c.n[1] = a.D;
+  c.taps = W;
+  c.D = a.D;
+  return launch_colsum(c, s);
+}
+
+#define M3_CONV_DISPATCH(FN, VECOK)                                                                              \
+  const bool bf = a.in_dtype == M3_BF16;                                                                         \
+  if (VECOK) {                                                                                                   \
+    if (a.W == 2) return bf ? FN<bf16_t, 2, vec<bf16_t>()>(a, s) : FN<float, 2, vec<float>()>(a, s);             \
+    if (a.W == 3) return bf ? FN<bf16_t, 3, vec<bf16_t>()>(a, s) : FN<float, 3, vec<float>()>(a, s);             \
+    return bf ? FN<bf16_t, 4, vec<bf16_t>()>(a, s) : FN<float, 4, vec<float>()>(a, s);                           \
+  }                                                                                                              \
+  if (a.W == 2) return bf ? FN<bf16_t, 2, 1>(a, s) : FN<float, 2, 1>(a, s);                                      \
+  if (a.W == 3) return bf ? FN<bf16_t, 3, 1>(a, s) : FN<float, 3, 1>(a, s);                                      \
+  return bf ? FN<bf16_t, 4, 1>(a, s) : FN<float, 4, 1>(a, s);
+
+}  // namespace
+
+hipError_t launch_colsum(const ColSum& c, hipStream_t s) {
+  colsum_kernel<<<uint32_t((c.ncols + 63) / 64), 256, 0, s>>>(c);
+  return hipGetLastError();
+}
+
+hipError_t launch_conv(const m3_conv_args& a, hipStream_t s) {
+  const size_t e = a.in_dtype == M3_BF16 ? 2 : 4;
+  const bool ok = rows_aligned(a.x, a.x_ld, e, 16) && rows_aligned(a.y, a.D, e, 16) && rows_aligned(a.state, a.D, e, 16) &&
+                  rows_aligned(a.state_out, a.D, e, 16);
+  M3_CONV_DISPATCH(run_conv, ok)
+}
+hipError_t launch_conv_step(const m3_conv_step_args& a, hipStream_t s) {
+  const size_t e = a.in_dtype == M3_BF16 ? 2 : 4;
+  const bool ok = rows_aligned(a.x, a.x_ld, e, 16) && rows_aligned(a.y, a.D, e, 16) && rows_aligned(a.state, a.D, e, 16) &&
+                  rows_aligned(a.state_out, a.D, e, 16);
+  M3_CONV_DISPATCH(run_step, ok)
+}
+// The size covers both widths of the threads (the addresses are not known here).
+size_t conv_backward_workspace(const m3_conv_backward_args& a) {
+  const int64_t cols = int64_t(a.W + 1) * a.D;
+  const int V = a.in_dtype == M3_BF16 ? 8 : 4;
+  int64_t rows = bw_geom(a, 1).ngroups;
+  if (a.D % V == 0) {
+    const int64_t r = bw_geom(a, V).ngroups;
+    if (r > rows) rows = r;
+  }
+  return round256(size_t(rows) * a.Bt * cols * 4);
+}
+hipError_t launch_conv_backward(const m3_conv_backward_args& a, hipStream_t s) { M3_CONV_DISPATCH(run_bw, bw_vec(a)) }
+
+}  // namespace m3

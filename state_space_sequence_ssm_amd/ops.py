@@ -6,6 +6,7 @@ and the current stream.
 from __future__ import annotations
 
 import ctypes
+import functools
 
 import torch
 
@@ -278,3 +279,384 @@ def m3_rope_angles_cumsum(theta, phi0=None, *, phi=None, stream=None):
     if rc != _lib.M3_OK:
         raise M3Error(rc, "m3_rope_angles_cumsum")
     return phi
+
+
+# ---------------------------------------------------------------- layer operators
+def _scoped(fn):
+    """Run a call on its first tensor's device and on `stream`: outputs and
+    workspaces are then allocated for that stream as well."""
+    @functools.wraps(fn)
+    def call(first, *args, stream=None, **kw):
+        if not isinstance(first, torch.Tensor):
+            raise TypeError("the first argument must be a torch.Tensor")
+        if not first.is_cuda:
+            raise ValueError("the first argument must be a device tensor")
+        if stream is None and first.device.index == torch.cuda.current_device():
+            return fn(first, *args, **kw)
+        if stream is None:
+            stream = torch.cuda.current_stream(first.device)
+        elif stream.device != first.device:
+            raise ValueError(f"stream is on {stream.device}, the tensors are on {first.device}")
+        with torch.cuda.stream(stream):
+            return fn(first, *args, **kw)
+    return call
+
+
+def _dense(t, dtype, shape, name, dev):
+    """Address of a dense tensor (None: NULL) after checking it."""
+    if t is None:
+        return None
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if t.device != dev:
+        raise ValueError(f"{name} is on {t.device}, expected {dev}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
+
+
+def _rows(t, dtype, lead, inner, name, dev):
+    """Address of a tensor of shape lead + inner and the elements from one of
+    its rows to the next: dense rows, the same distance apart throughout."""
+    if t is None:
+        return None, 0
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.shape != lead + inner:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(lead + inner)}")
+    if t.device != dev:
+        raise ValueError(f"{name} is on {t.device}, expected {dev}")
+    if t.is_contiguous():
+        return t.data_ptr(), 0
+    strides = t.stride()
+    width = 1
+    for n, st in zip(reversed(inner), reversed(strides[len(lead):])):
+        if n > 1 and st != width:
+            raise ValueError(f"{name}: the elements of a row must be dense")
+        width *= n
+    ld, rows = 0, 1
+    for n, st in zip(reversed(lead), reversed(strides[:len(lead)])):
+        if n == 1:
+            continue
+        if ld == 0:
+            ld = st
+            if st < width:
+                raise ValueError(f"{name}: rows must not overlap")
+        elif st != ld * rows:
+            raise ValueError(f"{name}: all rows must be the same distance apart")
+        rows *= n
+    return t.data_ptr(), ld
+
+
+def _new(given, shape, like, dtype=None):
+    if given is not None:
+        return given
+    return torch.empty(shape, device=like.device, dtype=dtype or like.dtype)
+
+
+def _run_layer(name, args):
+    rc = getattr(_lib.load(), name)(ctypes.byref(args), torch.cuda.current_stream().cuda_stream)
+    if rc != _lib.M3_OK:
+        raise M3Error(rc, name)
+
+
+def _take_workspace(name, args, given, dev):
+    """Put a workspace of the size the library asks for into the arguments: the
+    given uint8 tensor, or a new one.  Returns it (it must outlive the call)."""
+    need = getattr(_lib.load(), name + "_workspace_size")(ctypes.byref(args))
+    if given is None:
+        if need == 0:
+            return None
+        given = torch.empty(need, dtype=torch.uint8, device=dev)
+    args.workspace = _dense(given, torch.uint8, given.shape, "workspace", dev)
+    args.workspace_bytes = given.numel()
+    return given
+
+
+_F32 = torch.float32
+
+
+@_scoped
+def m3_causal_conv(x, w, bias=None, state=None, *, lengths=None, silu=True, y=None, state_out=None, want_state=False):
+    """Short causal depthwise convolution over the tokens:
+    y[t, d] = act(bias[d] + sum_k w[d, k] x[t - (W - 1) + k, d]), act = SiLU or
+    identity.  x [Bt, L, D] (bf16 or fp32; rows may be slices of wider ones), w
+    [D, W] fp32, W in 2..4, bias [D] fp32; state [Bt, W-1, D]: the inputs before
+    the first token (None: zeros); lengths [Bt] int32: tokens held per item.
+    Returns a dict with y [Bt, L, D] (rows behind an item's length are left as
+    they were) and, with want_state or state_out (may be `state`), state: the
+    last W - 1 inputs.  `stream`: the stream to run on (default: the current
+    one), for this and the following operators."""
+    Bt, L, D = x.shape
+    W = w.shape[-1]
+    dev, t = x.device, x.dtype
+    y = _new(y, (Bt, L, D), x)
+    if want_state:
+        state_out = _new(state_out, (Bt, W - 1, D), x)
+    a = _lib.ConvArgs()
+    a.Bt, a.L, a.D, a.W, a.in_dtype, a.silu = Bt, L, D, W, _dtype_code(x), 1 if silu else 0
+    a.x, a.x_ld = _rows(x, t, (Bt, L), (D,), "x", dev)
+    a.w = _dense(w, _F32, (D, W), "w", dev)
+    a.bias = _dense(bias, _F32, (D,), "bias", dev)
+    a.lengths = _dense(lengths, torch.int32, (Bt,), "lengths", dev)
+    a.state = _dense(state, t, (Bt, W - 1, D), "state", dev)
+    a.y = _dense(y, t, (Bt, L, D), "y", dev)
+    a.state_out = _dense(state_out, t, (Bt, W - 1, D), "state_out", dev)
+    _run_layer("m3_causal_conv", a)
+    return dict(y=y, state=state_out)
+
+
+@_scoped
+def m3_causal_conv_step(state, x, w, bias=None, *, silu=True, y=None, state_out=None):
+    """One token of m3_causal_conv: x [Bt, D], state [Bt, W-1, D] updated in
+    place (or read only, the new one going to state_out).  Returns y [Bt, D]."""
+    Bt, D = x.shape
+    W = w.shape[-1]
+    dev, t = state.device, x.dtype
+    y = _new(y, (Bt, D), x)
+    a = _lib.ConvStepArgs()
+    a.Bt, a.D, a.W, a.in_dtype, a.silu = Bt, D, W, _dtype_code(x), 1 if silu else 0
+    a.x, a.x_ld = _rows(x, t, (Bt,), (D,), "x", dev)
+    a.w = _dense(w, _F32, (D, W), "w", dev)
+    a.bias = _dense(bias, _F32, (D,), "bias", dev)
+    a.state = _dense(state, t, (Bt, W - 1, D), "state", dev)
+    a.state_out = _dense(state_out, t, (Bt, W - 1, D), "state_out", dev)
+    a.y = _dense(y, t, (Bt, D), "y", dev)
+    _run_layer("m3_causal_conv_step", a)
+    return y
+
+
+@_scoped
+def m3_causal_conv_backward(x, w, bias=None, state=None, *, dy, lengths=None, silu=True, want_state_grad=False,
+                            workspace=None, out=None):
+    """Gradients of m3_causal_conv for dy [Bt, L, D] (dense).  Returns a dict
+    with dx, dw [D, W], dbias [D] (None without bias) and, with
+    want_state_grad, dstate.  `out`: optional dict of preallocated tensors."""
+    Bt, L, D = x.shape
+    W = w.shape[-1]
+    dev, t = x.device, x.dtype
+    got = out or {}
+    out = dict(dx=_new(got.get("dx"), (Bt, L, D), x), dw=_new(got.get("dw"), (D, W), x, _F32),
+               dbias=_new(got.get("dbias"), (D,), x, _F32) if bias is not None else None,
+               dstate=_new(got.get("dstate"), (Bt, W - 1, D), x) if want_state_grad or "dstate" in got else None)
+    a = _lib.ConvBackwardArgs()
+    a.Bt, a.L, a.D, a.W, a.in_dtype, a.silu = Bt, L, D, W, _dtype_code(x), 1 if silu else 0
+    a.x, a.x_ld = _rows(x, t, (Bt, L), (D,), "x", dev)
+    a.w = _dense(w, _F32, (D, W), "w", dev)
+    a.bias = _dense(bias, _F32, (D,), "bias", dev)
+    a.lengths = _dense(lengths, torch.int32, (Bt,), "lengths", dev)
+    a.state = _dense(state, t, (Bt, W - 1, D), "state", dev)
+    a.dy = _dense(dy, t, (Bt, L, D), "dy", dev)
+    a.dx = _dense(out["dx"], t, (Bt, L, D), "dx", dev)
+    a.dw = _dense(out["dw"], _F32, (D, W), "dw", dev)
+    a.dbias = _dense(out["dbias"], _F32, (D,), "dbias", dev)
+    a.dstate = _dense(out["dstate"], t, (Bt, W - 1, D), "dstate", dev)
+    workspace = _take_workspace("m3_causal_conv_backward", a, workspace, dev)
+    _run_layer("m3_causal_conv_backward", a)
+    return out
+
+
+def _scan_inputs(a, lead, x, dt, A, B, C, D, z, dt_softplus, dt_bias):
+    """The inputs that the scan, its backward and its step share."""
+    width = x.shape[-1]
+    G, N = B.shape[-2:]
+    dev, t = x.device, x.dtype
+    a.D, a.N, a.G, a.in_dtype, a.dt_softplus = width, N, G, _dtype_code(x), 1 if dt_softplus else 0
+    a.x, a.x_ld = _rows(x, t, lead, (width,), "x", dev)
+    a.dt, a.dt_ld = _rows(dt, t, lead, (width,), "dt", dev)
+    a.z, a.z_ld = _rows(z, t, lead, (width,), "z", dev)
+    a.B, a.B_ld = _rows(B, t, lead, (G, N), "B", dev)
+    a.C, a.C_ld = _rows(C, t, lead, (G, N), "C", dev)
+    a.A = _dense(A, _F32, (width, N), "A", dev)
+    a.D_skip = _dense(D, _F32, (width,), "D", dev)
+    a.dt_bias = _dense(dt_bias, _F32, (width,), "dt_bias", dev)
+
+
+@_scoped
+def m3_selective_scan(x, dt, A, B, C, D=None, z=None, h0=None, *, lengths=None, dt_softplus=False, dt_bias=None, y=None,
+                      h_final=None, want_state=True, workspace=None):
+    """Selective scan with a diagonal state per channel:
+    h_t = exp(delta_t A) h_{t-1} + delta_t x_t B_t,  y_t = (C_t . h_t + D x_t)
+    silu(z_t), delta = softplus(dt + dt_bias) or dt itself.  x, dt, z
+    [Bt, L, D], B, C [Bt, L, G, N] (bf16 or fp32; rows may be slices of wider
+    ones); A [D, N], D [D], dt_bias [D], h0 [Bt, D, N] fp32; lengths [Bt] int32;
+    N in 1..64.  workspace: a uint8 device tensor, None to allocate one when the
+    library asks for it, or False to run without (token axis not cut).
+    Returns a dict with y [Bt, L, D] (rows behind an item's length are left as
+    they were) and h: the last state [Bt, D, N]."""
+    Bt, L, width = x.shape
+    N = A.shape[-1]
+    dev, t = x.device, x.dtype
+    y = _new(y, (Bt, L, width), x)
+    if want_state:
+        h_final = _new(h_final, (Bt, width, N), x, _F32)
+    a = _lib.ScanArgs()
+    a.Bt, a.L = Bt, L
+    _scan_inputs(a, (Bt, L), x, dt, A, B, C, D, z, dt_softplus, dt_bias)
+    a.h0 = _dense(h0, _F32, (Bt, width, N), "h0", dev)
+    a.lengths = _dense(lengths, torch.int32, (Bt,), "lengths", dev)
+    a.y = _dense(y, t, (Bt, L, width), "y", dev)
+    a.h_final = _dense(h_final, _F32, (Bt, width, N), "h_final", dev)
+    if workspace is not False:
+        workspace = _take_workspace("m3_selective_scan", a, workspace, dev)
+    _run_layer("m3_selective_scan", a)
+    return dict(y=y, h=h_final)
+
+
+@_scoped
+def m3_selective_scan_step(h, x, dt, A, B, C, D=None, z=None, *, dt_softplus=False, dt_bias=None, y=None, h_out=None):
+    """One token of m3_selective_scan: x, dt, z [Bt, D], B, C [Bt, G, N], h
+    [Bt, D, N] fp32 updated in place (or read only, the new state going to
+    h_out).  Returns y [Bt, D]."""
+    Bt, width = x.shape
+    N = A.shape[-1]
+    dev = h.device
+    y = _new(y, (Bt, width), x)
+    a = _lib.ScanStepArgs()
+    a.Bt = Bt
+    _scan_inputs(a, (Bt,), x, dt, A, B, C, D, z, dt_softplus, dt_bias)
+    a.h = _dense(h, _F32, (Bt, width, N), "h", x.device)
+    a.h_out = _dense(h_out, _F32, (Bt, width, N), "h_out", dev)
+    a.y = _dense(y, x.dtype, (Bt, width), "y", dev)
+    _run_layer("m3_selective_scan_step", a)
+    return y
+
+
+@_scoped
+def m3_selective_scan_backward(x, dt, A, B, C, D=None, z=None, h0=None, *, dy, dh_final=None, lengths=None,
+                               dt_softplus=False, dt_bias=None, want_carry_grads=False, workspace=None, out=None):
+    """Gradients of m3_selective_scan for dy [Bt, L, D] (dense) and dh_final
+    [Bt, D, N].  Returns a dict with dx, ddt, dA, dB, dC, dD, dz, ddt_bias
+    (None where the input is) and, with want_carry_grads, dh0.  `out`:
+    optional dict of preallocated tensors."""
+    Bt, L, width = x.shape
+    G, N = B.shape[-2:]
+    dev, t = x.device, x.dtype
+    got = out or {}
+    shapes = dict(dx=((Bt, L, width), t), ddt=((Bt, L, width), t), dA=((width, N), _F32), dB=((Bt, L, G, N), t),
+                  dC=((Bt, L, G, N), t), dD=((width,), _F32), dz=((Bt, L, width), t), ddt_bias=((width,), _F32),
+                  dh0=((Bt, width, N), _F32))
+    absent = dict(dD=D is None, dz=z is None, ddt_bias=dt_bias is None, dh0=not want_carry_grads and "dh0" not in got)
+    a = _lib.ScanBackwardArgs()
+    out = {}
+    for k, (shape, ty) in shapes.items():
+        out[k] = None if absent.get(k) else _new(got.get(k), shape, x, ty)
+        setattr(a, k, _dense(out[k], ty, shape, k, dev))
+    a.fwd.Bt, a.fwd.L = Bt, L
+    _scan_inputs(a.fwd, (Bt, L), x, dt, A, B, C, D, z, dt_softplus, dt_bias)
+    a.fwd.h0 = _dense(h0, _F32, (Bt, width, N), "h0", dev)
+    a.fwd.lengths = _dense(lengths, torch.int32, (Bt,), "lengths", dev)
+    a.dy = _dense(dy, t, (Bt, L, width), "dy", dev)
+    a.dh_final = _dense(dh_final, _F32, (Bt, width, N), "dh_final", dev)
+    workspace = _take_workspace("m3_selective_scan_backward", a, workspace, dev)
+    _run_layer("m3_selective_scan_backward", a)
+    return out
+
+
+def _gated_inputs(a, x, z, w, groups, eps, gate_first):
+    lead, width = x.shape[:-1], x.shape[-1]
+    a.M, a.D, a.G, a.in_dtype = x.numel() // width if width else 0, width, groups, _dtype_code(x)
+    a.gate_first, a.eps = 1 if gate_first else 0, eps
+    a.x, a.x_ld = _rows(x, x.dtype, lead, (width,), "x", x.device)
+    a.z, a.z_ld = _rows(z, x.dtype, lead, (width,), "z", x.device)
+    a.w = _dense(w, _F32, (width,), "w", x.device)
+
+
+@_scoped
+def m3_gated_norm(x, z=None, w=None, *, groups=1, eps=1e-6, gate_first=True, y=None):
+    """Group RMS norm of rows with a SiLU gate: with gate_first v = x silu(z),
+    y = v rsqrt(mean_group(v^2) + eps) w, else y = x rsqrt(mean_group(x^2) +
+    eps) w silu(z).  x, z [..., D] (bf16 or fp32; rows may be slices of wider
+    ones), w [D] fp32 (None: ones), `groups` equal groups.  Returns y (dense;
+    may be given as x or z themselves where those are dense)."""
+    y = _new(y, x.shape, x)
+    a = _lib.GatedNormArgs()
+    _gated_inputs(a, x, z, w, groups, eps, gate_first)
+    a.y = _dense(y, x.dtype, x.shape, "y", x.device)
+    _run_layer("m3_gated_norm", a)
+    return y
+
+
+@_scoped
+def m3_gated_norm_backward(x, z=None, w=None, *, dy, groups=1, eps=1e-6, gate_first=True, workspace=None, out=None):
+    """Gradients of m3_gated_norm for dy (dense): a dict with dx, dz (None
+    without gate) and dw (None without gain)."""
+    dev, t = x.device, x.dtype
+    got = out or {}
+    out = dict(dx=_new(got.get("dx"), x.shape, x), dz=None if z is None else _new(got.get("dz"), x.shape, x),
+               dw=None if w is None else _new(got.get("dw"), (x.shape[-1],), x, _F32))
+    a = _lib.GatedNormBackwardArgs()
+    _gated_inputs(a.fwd, x, z, w, groups, eps, gate_first)
+    a.dy = _dense(dy, t, x.shape, "dy", dev)
+    a.dx = _dense(out["dx"], t, x.shape, "dx", dev)
+    a.dz = _dense(out["dz"], t, x.shape, "dz", dev)
+    a.dw = _dense(out["dw"], _F32, (x.shape[-1],), "dw", dev)
+    workspace = _take_workspace("m3_gated_norm_backward", a, workspace, dev)
+    _run_layer("m3_gated_norm_backward", a)
+    return out
+
+
+@_scoped
+def m3_residual_norm(x, residual=None, w=None, scale=None, *, eps=1e-6, y=None, residual_out=None, want_residual=True):
+    """Residual sum and RMS norm: h = residual + scale x, y = h rsqrt(mean(h^2)
+    + eps) w over rows of D.  x [..., D] (bf16 or fp32; rows may be slices of
+    wider ones), residual of x's shape in x's type or fp32 (None: zeros), w and
+    scale [D] fp32 (None: ones).  Returns a dict with y (x's type) and residual:
+    h in the residual's type (residual_out may be `residual` itself)."""
+    dev, t = x.device, x.dtype
+    lead, width = x.shape[:-1], x.shape[-1]
+    rt = residual.dtype if residual is not None else residual_out.dtype if residual_out is not None else t
+    y = _new(y, x.shape, x)
+    if want_residual:
+        residual_out = _new(residual_out, x.shape, x, rt)
+    a = _lib.ResidualNormArgs()
+    a.M, a.D, a.in_dtype = x.numel() // width if width else 0, width, _dtype_code(x)
+    a.res_dtype, a.eps = _lib.M3_F32 if rt == _F32 else _lib.M3_BF16, eps
+    a.x, a.x_ld = _rows(x, t, lead, (width,), "x", dev)
+    a.residual = _dense(residual, rt, x.shape, "residual", dev)
+    a.scale = _dense(scale, _F32, (width,), "scale", dev)
+    a.w = _dense(w, _F32, (width,), "w", dev)
+    a.y = _dense(y, t, x.shape, "y", dev)
+    a.residual_out = _dense(residual_out, rt, x.shape, "residual_out", dev)
+    _run_layer("m3_residual_norm", a)
+    return dict(y=y, residual=residual_out)
+
+
+@_scoped
+def m3_residual_norm_backward(h, x=None, w=None, scale=None, *, dy, dresidual=None, eps=1e-6, workspace=None, out=None):
+    """Gradients of m3_residual_norm at the stored sum h (its `residual`
+    output) for dy and dresidual (the gradient that reaches h along the
+    residual stream, h's type; None: zeros).  x is needed with scale only.
+    Returns a dict with dresidual (h's type), dx (dy's type; the same tensor
+    where scale is None and the types agree), dw and dscale (None where the
+    parameter is).  out["dresidual"] may be `dresidual` itself."""
+    dev, t = h.device, dy.dtype
+    lead, width = h.shape[:-1], h.shape[-1]
+    got = out or {}
+    dres = _new(got.get("dresidual"), h.shape, h)
+    own_dx = scale is not None or t != h.dtype or got.get("dx") is not None
+    dx = _new(got.get("dx"), h.shape, dy) if own_dx else None
+    out = dict(dresidual=dres, dx=dx if own_dx else dres, dw=None if w is None else _new(got.get("dw"), (width,), h, _F32),
+               dscale=None if scale is None else _new(got.get("dscale"), (width,), h, _F32))
+    a = _lib.ResidualNormBackwardArgs()
+    a.M, a.D, a.in_dtype = h.numel() // width if width else 0, width, _dtype_code(dy)
+    a.res_dtype, a.eps = _dtype_code(h), eps
+    a.h = _dense(h, h.dtype, h.shape, "h", dev)
+    a.x, a.x_ld = _rows(x, t, lead, (width,), "x", dev)
+    a.scale = _dense(scale, _F32, (width,), "scale", dev)
+    a.w = _dense(w, _F32, (width,), "w", dev)
+    a.dy = _dense(dy, t, h.shape, "dy", dev)
+    a.dresidual_out = _dense(dresidual, h.dtype, h.shape, "dresidual", dev)
+    a.dx = _dense(dx, t, h.shape, "dx", dev)
+    a.dresidual = _dense(dres, h.dtype, h.shape, "dresidual", dev)
+    a.dw = _dense(out["dw"], _F32, (width,), "dw", dev)
+    a.dscale = _dense(out["dscale"], _F32, (width,), "dscale", dev)
+    workspace = _take_workspace("m3_residual_norm_backward", a, workspace, dev)
+    _run_layer("m3_residual_norm_backward", a)
+    return out
