@@ -65,7 +65,7 @@ __global__ __launch_bounds__(kThreads) void states_kernel(BwP p) {
   __shared__ __align__(16) float dos[SEG ? TT : 1][CH];
 
   const int tid = threadIdx.x, s = tid % S, chl = tid / S;
-  int blk = blockIdx.x;
+  int blk = block_on_xcd();
   const int64_t blocks = int64_t(p.Bt) * p.G * p.nblk;
   const int seg = int(blk / blocks);
   blk = int(blk - seg * blocks);
@@ -131,7 +131,7 @@ __global__ __launch_bounds__(kThreads) void states_kernel(BwP p) {
   for (int t0 = tbeg; t0 < tend; t0 += TT) {
 #pragma unroll
     for (int v = 0; v < VE; ++v) {
-      const float dl_ = delta_of(to_f32(qd.e[v]), p.softplus != 0, bias[v], t0 + r < tend);
+      const float dl_ = step_of(to_f32(qd.e[v]), p.softplus != 0, bias[v], t0 + r < tend);
       du[r][c0 + v] = float2{dl_, dl_ * to_f32(qx.e[v])};
       if constexpr (SEG) dos[r][c0 + v] = to_f32(qy.e[v]) * (zp != nullptr ? silu_f(to_f32(qz.e[v])) : 1.f);
     }
@@ -216,7 +216,7 @@ __global__ __launch_bounds__(kThreads) void reverse_kernel(BwP p) {
   __shared__ __align__(16) float wp[4][TB][2][NP];
 
   const int tid = threadIdx.x, s = tid % S, chl = tid / S, lane = tid & 63, wv = tid >> 6;
-  int blk = blockIdx.x;
+  int blk = block_on_xcd();
   const int64_t blocks = int64_t(p.Bt) * p.G * p.nblk;
   const int seg = int(blk / blocks);
   blk = int(blk - seg * blocks);
@@ -323,7 +323,7 @@ __global__ __launch_bounds__(kThreads) void reverse_kernel(BwP p) {
     unpack<T, VE>(qz, zv);
 #pragma unroll
     for (int v = 0; v < VE; ++v) {
-      const float dl_ = delta_of(raw[v], p.softplus != 0, bias[v], row);
+      const float dl_ = step_of(raw[v], p.softplus != 0, bias[v], row);
       du[r][c0 + v] = float2{dl_, dl_ * xv[v]};
       dov[v] = yv[v] * (zp != nullptr ? silu_f(zv[v]) : 1.f);
       dos[r][c0 + v] = dov[v];
@@ -488,16 +488,16 @@ __global__ __launch_bounds__(256) void join_bc_kernel(const float* bc, T* dB, T*
 }
 
 struct Plan {
-  Split q;
-  int nseg, seglen;
+  int S, nblk, nseg, seglen;
   int64_t tiles, blocks;
   size_t oCk, oCd, oHe, oGs, oSd, oBc, oPart, bytes;
 };
 // Segments as in the forward, at least 128 tokens each, multiples of the tiles.
 Plan plan_of(const m3_scan_args& f) {
   Plan p;
-  p.q = split_of(f.D, f.N, f.G);
-  p.blocks = int64_t(f.Bt) * f.G * p.q.nblk;
+  p.S = lanes_for(f.N);
+  p.nblk = blocks_per_group(f.D / f.G, p.S);
+  p.blocks = int64_t(f.Bt) * f.G * p.nblk;
   p.nseg = 1;
   p.seglen = (f.L + 31) / 32 * 32;
   if (p.blocks < 512) {
@@ -509,7 +509,7 @@ Plan plan_of(const m3_scan_args& f) {
     }
   }
   p.tiles = (f.L + TB - 1) / TB;
-  const int CH = kThreads / p.q.S, NP = 4 * p.q.S;
+  const int CH = kThreads / p.S, NP = 4 * p.S;
   const size_t seg = p.nseg > 1 ? size_t(p.nseg) * f.Bt * f.D : 0;
   p.oCk = 0;
   p.oCd = round256(p.oCk + size_t(p.tiles) * p.blocks * kThreads * 16);
@@ -517,7 +517,7 @@ Plan plan_of(const m3_scan_args& f) {
   p.oGs = round256(p.oHe + seg * f.N * 4);
   p.oSd = round256(p.oGs + seg * f.N * 4);
   p.oBc = round256(p.oSd + seg * 4);
-  p.oPart = round256(p.oBc + size_t(p.q.nblk) * f.Bt * f.L * f.G * 2 * NP * 4);
+  p.oPart = round256(p.oBc + size_t(p.nblk) * f.Bt * f.L * f.G * 2 * NP * 4);
   p.bytes = round256(p.oPart + size_t(p.nseg) * f.Bt * f.D * (f.N + 2) * 4);
   return p;
 }
@@ -530,7 +530,7 @@ hipError_t run(const m3_scan_backward_args& a, hipStream_t st) {
   auto at = [&](size_t o) { return reinterpret_cast<float*>(ws + o); };
   const BwP p{f.x, f.dt, f.z, f.B, f.C, a.dy, f.x_ld, f.dt_ld, f.z_ld, f.B_ld, f.C_ld, f.A, f.D_skip, f.dt_bias, f.h0,
               a.dh_final, f.lengths, a.dx, a.ddt, a.dz, a.dh0, at(pl.oCk), at(pl.oCd), at(pl.oHe), at(pl.oGs), at(pl.oSd),
-              at(pl.oBc), at(pl.oPart), f.Bt, f.L, f.D, f.N, f.G, f.D / f.G, pl.q.nblk, pl.nseg, pl.seglen, f.dt_softplus};
+              at(pl.oBc), at(pl.oPart), f.Bt, f.L, f.D, f.N, f.G, f.D / f.G, pl.nblk, pl.nseg, pl.seglen, f.dt_softplus};
   const uint32_t grid = uint32_t(pl.blocks * pl.nseg);
   if (pl.nseg > 1) states_kernel<T, S, VEC, true><<<grid, kThreads, 0, st>>>(p);
   else states_kernel<T, S, VEC, false><<<grid, kThreads, 0, st>>>(p);
@@ -541,7 +541,7 @@ hipError_t run(const m3_scan_backward_args& a, hipStream_t st) {
   if (e != hipSuccess) return e;
   const int64_t rows = int64_t(f.Bt) * f.L, items = rows * f.G * 2 * 4 * S;
   join_bc_kernel<T, 4 * S><<<uint32_t((items + 255) / 256), 256, 0, st>>>(p.bc, static_cast<T*>(a.dB), static_cast<T*>(a.dC),
-                                                                        f.lengths, rows, f.L, f.G, f.N, pl.q.nblk);
+                                                                        f.lengths, rows, f.L, f.G, f.N, pl.nblk);
   e = hipGetLastError();
   if (e != hipSuccess) return e;
   ColSum c{};
