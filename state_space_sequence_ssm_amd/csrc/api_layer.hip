@@ -40,6 +40,8 @@ bool set_ld(int64_t& ld, int64_t width) {
   if (ld == 0) ld = width;
   return ld >= width && ld < (int64_t(1) << 31);
 }
+// The scan's tiles address their rows with 32 bits.
+bool scan_ld(int64_t& ld, int64_t width) { return set_ld(ld, width) && ld < (int64_t(1) << 24); }
 bool ok_eps(float e) { return e >= 0.f && e <= 3.0e38f; }
 int hip_status(hipError_t e) { return e == hipSuccess ? M3_OK : M3_ERR_HIP; }
 hipStream_t str(void* s) { return static_cast<hipStream_t>(s); }
@@ -72,7 +74,7 @@ int check_scan_inputs(m3_scan_args& f) {
   if (rc != M3_OK) return rc;
   if (!all_set({f.x, f.dt, f.A, f.B, f.C}) || (f.dt_bias != nullptr && !f.dt_softplus)) return M3_ERR_INVALID_ARG;
   const int64_t GN = int64_t(f.G) * f.N;
-  if (!set_ld(f.x_ld, f.D) || !set_ld(f.dt_ld, f.D) || !set_ld(f.z_ld, f.D) || !set_ld(f.B_ld, GN) || !set_ld(f.C_ld, GN))
+  if (!scan_ld(f.x_ld, f.D) || !scan_ld(f.dt_ld, f.D) || !scan_ld(f.z_ld, f.D) || !scan_ld(f.B_ld, GN) || !scan_ld(f.C_ld, GN))
     return M3_ERR_INVALID_ARG;
   if (!all_at({f.x, f.dt, f.B, f.C, f.z}, elem(f.in_dtype)) || !all_at({f.A, f.D_skip, f.dt_bias, f.h0, f.lengths}, 4))
     return M3_ERR_INVALID_ARG;

@@ -1,4 +1,6 @@
 // Selective scan over prompts and single tokens (see scan_common.hpp).
+#include <type_traits>
+
 #include "scan_common.hpp"
 
 namespace m3 {
@@ -24,22 +26,24 @@ struct ScanP {
   int Bt, L, D, N, G, Dg, nblk, nseg, seglen, softplus;
 };
 
-constexpr int tile(int S) { return S >= 4 ? 32 : 16; }  // tokens per tile
+constexpr int tile(int NB) { return NB == 4 ? 16 : 32; }  // tokens per tile
 
 // Four tokens' values of one lane, in registers.
-template <int K, bool FULL>
+template <int NB, bool FULL>
 struct Four {
-  float2 du[4];
-  float B[4][K], C[4][K];
-  template <int TT, int DS, int NP>
-  __device__ __forceinline__ void load(int t, const float2 (&d)[TT][DS], const float (&bc)[2][TT][NP], int dcol, int s) {
+  float delta[4], u[4];
+  f32x4 B[4][NB], C[4][NB];
+  // at this lane's channel of delta and u, and its states of B and C
+  template <int DS, int NP>
+  __device__ __forceinline__ void load(const float* pd, const float* pu, const float* pB, const float* pC) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      du[i] = d[t + i][dcol];
+    for (int j = 0; j < 4; ++j) {
+      delta[j] = pd[j * DS];
+      u[j] = pu[j * CH];
 #pragma unroll
-      for (int k = 0; k < K; ++k) {
-        B[i][k] = bc[0][t + i][s * K + k];
-        if (FULL) C[i][k] = bc[1][t + i][s * K + k];
+      for (int i = 0; i < NB; ++i) {
+        B[j][i] = *reinterpret_cast<const f32x4*>(pB + j * NP + 16 * i);
+        if (FULL) C[j][i] = *reinterpret_cast<const f32x4*>(pC + j * NP + 16 * i);
       }
     }
   }
@@ -48,20 +52,19 @@ struct Four {
 // FULL: y and the last state, segment s starting from the join of the states
 // before it.  Otherwise the states and sums of delta of the segments alone.
 //
-// A block is eight waves of two kinds, one of each per SIMD: four scan, 256 / S
-// channels of S lanes; four stage, that is, they load the next tile, form delta
-// and u and put them into the other half of LDS, and gate and store the tile
-// before.  So the loads' latency and the exponentials of softplus and SiLU lie
-// beside the recurrence and not between its tiles, with one barrier per tile.
-template <typename T, int K, int S, bool VEC, bool FULL>
+// A block is eight waves of two kinds, one of each per SIMD: four scan, 16
+// channels each; four stage, that is, they load the next tile, form delta and u
+// and put them into the other half of LDS, and gate and store the tile before.
+// So the loads' latency and the exponentials of softplus and SiLU lie beside the
+// recurrence and not between its tiles, with one barrier per tile.
+template <typename T, int NB, bool VEC, bool FULL>
 __global__ __launch_bounds__(2 * kThreads) void scan_kernel(ScanP p) {
-  constexpr int CH = kThreads / S, TT = tile(S), VE = TT / S, NP = K * S;
-  constexpr int NQ = (TT * NP / 2 + kThreads - 1) / kThreads;  // quads of B and C per thread
-  constexpr int YS = CH + 64 / S;                              // the S rows written together lie on different banks
-  constexpr int DS = CH + CH / 32 * 2;  // 16 bytes more every 32 channels: staging's words on different banks
-  __shared__ __align__(16) float2 du[2][TT][DS];
+  constexpr int TT = tile(NB), VE = TT * CH / kThreads, NP = 16 * NB, K = 4 * NB;
+  constexpr int NQ = (TT * NP / 2 + kThreads - 1) / kThreads;  // quads of B and C per staging thread
+  constexpr int DS = CH + 16;  // rows of delta, then of y, whose four tokens are written together: on different banks
+  __shared__ __align__(16) float dl[2][TT + 1][DS];
+  __shared__ __align__(16) float us[2][TT][CH];
   __shared__ __align__(16) float bc[2][2][TT][NP];
-  __shared__ __align__(16) float ys[FULL ? 2 : 1][FULL ? TT : 1][YS];
 
   const int tid = threadIdx.x % kThreads;
   const bool scanner = threadIdx.x < kThreads;
@@ -77,16 +80,15 @@ __global__ __launch_bounds__(2 * kThreads) void scan_kernel(ScanP p) {
   const int tiles = tend > tbeg ? (tend - tbeg + TT - 1) / TT : 0;
 
   if (scanner) {
-    const int s = tid % S, chl = tid / S;
-    const int dl = cb * CH + chl;
-    const bool live = dl < p.Dg;
-    const int d = g * p.Dg + (live ? dl : 0);
-    const int dcol = chl + chl / 32 * 2;
-    const uint32_t odd = s & 1 ? ~0u : 0u, two = s & 2 ? ~0u : 0u;
+    const int lane = tid & 63, s = lane >> 4, chl = (tid >> 6) * 16 + (lane & 15);
+    const int dloc = cb * CH + chl;
+    const bool live = dloc < p.Dg;
+    const int d = g * p.Dg + (live ? dloc : 0);
     float A2[K], h[K], sum_delta = 0.f;
+    auto state = [&](int k) { return 16 * (k / 4) + 4 * s + k % 4; };
 #pragma unroll
     for (int k = 0; k < K; ++k) {
-      const int n = s * K + k;
+      const int n = state(k);
       const bool on = live && n < p.N;
       A2[k] = on ? p.A[int64_t(d) * p.N + n] * kLog2e : 0.f;
       h[k] = on && p.h0 != nullptr && (FULL || seg == 0) ? p.h0[(int64_t(b) * p.D + d) * p.N + n] : 0.f;
@@ -97,57 +99,65 @@ __global__ __launch_bounds__(2 * kThreads) void scan_kernel(ScanP p) {
         const float sd = p.sdel[at];
 #pragma unroll
         for (int k = 0; k < K; ++k) {
-          const int n = s * K + k;
-          const float e = n < p.N ? p.hend[at * p.N + n] : 0.f;
+          const float e = state(k) < p.N ? p.hend[at * p.N + state(k)] : 0.f;
           h[k] = q == 0 ? e : fmaf(decay(sd, A2[k]), h[k], e);
         }
       }
     }
     __syncthreads();
-    for (int i = 0; i < tiles; ++i) {
-      const int left = tend - tbeg - i * TT, o = i & 1;
+    for (int t = 0; t < tiles; ++t) {
+      const int left = tend - tbeg - t * TT, o = t & 1;
+      float* pd = &dl[o][0][chl];
+      const float* pu = &us[o][0][chl];
+      const float* pB = &bc[o][0][0][4 * s];
+      const float* pC = &bc[o][1][0][4 * s];
       // four tokens at a time, the next four on their way from LDS meanwhile; two
       // register sets in turn.  Tokens past the end have delta = u = B = C = 0 and
-      // leave the state alone.
-      auto four = [&](int tq, const Four<K, FULL>& q) {
-        float a[4][K], w[4][K], y[4];
+      // leave the state alone.  y takes the place of its channel's delta.
+      // The sums over states of four tokens wait for the next four's exponentials,
+      // which cover their latency; row TT takes those in front of the first.
+      float y[4] = {0.f, 0.f, 0.f, 0.f};
+      auto four = [&](int to, const Four<NB, FULL>& q) {
+        constexpr int AT = 4 / NB;
+        if constexpr (FULL) pd[to * DS] = rows_sum4(y);
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
+        for (int j0 = 0; j0 < 4; j0 += AT) {
+          float a[AT][K], w[AT][K];
 #pragma unroll
-          for (int k = 0; k < K; ++k) {
-            a[j][k] = decay(q.du[j].x, A2[k]);
-            w[j][k] = q.du[j].y * q.B[j][k];
+          for (int j = 0; j < AT; ++j)
+#pragma unroll
+            for (int k = 0; k < K; ++k) {
+              a[j][k] = decay(q.delta[j0 + j], A2[k]);
+              w[j][k] = q.u[j0 + j] * q.B[j0 + j][k / 4][k % 4];
+            }
+          __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+          for (int j = 0; j < AT; ++j) {
+            y[j0 + j] = 0.f;
+#pragma unroll
+            for (int k = 0; k < K; ++k) {
+              h[k] = fmaf(a[j][k], h[k], w[j][k]);
+              if (FULL) y[j0 + j] = fmaf(q.C[j0 + j][k / 4][k % 4], h[k], y[j0 + j]);
+            }
+            if (!FULL) sum_delta += q.delta[j0 + j];
           }
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          y[j] = 0.f;
-#pragma unroll
-          for (int k = 0; k < K; ++k) {
-            h[k] = fmaf(a[j][k], h[k], w[j][k]);
-            if (FULL) y[j] = fmaf(q.C[j][k], h[k], y[j]);
-          }
-          if (!FULL) sum_delta += q.du[j].x;
-        }
-        if constexpr (FULL) {
-          float r0, r1;
-          lanes_sum4<S>(y, odd, two, r0, r1);
-          if constexpr (S >= 4) {
-            if (s < 4) ys[o][tq + s][chl] = r0;
-          } else {
-            ys[o][tq + s][chl] = r0;
-            ys[o][tq + 2 + s][chl] = r1;
-          }
+          __builtin_amdgcn_sched_barrier(0);
         }
       };
       const int nt = left < TT ? (left + 7) & ~7 : TT;
-      Four<K, FULL> q0, q1;
-      q0.load(0, du[o], bc[o], dcol, s);
-      for (int tq = 0; tq < nt; tq += 8) {
-        q1.load(tq + 4, du[o], bc[o], dcol, s);
-        four(tq, q0);
-        q0.load(tq + 8 < TT ? tq + 8 : 0, du[o], bc[o], dcol, s);
-        four(tq + 4, q1);
+      const int rv = row_value(s);
+      Four<NB, FULL> q0, q1;
+      q0.template load<DS, NP>(pd, pu, pB, pC);
+#pragma unroll
+      for (int tq = 0; tq < TT; tq += 8) {
+        if (tq >= nt) break;
+        q1.template load<DS, NP>(pd + (tq + 4) * DS, pu + (tq + 4) * CH, pB + (tq + 4) * NP, pC + (tq + 4) * NP);
+        four(tq > 0 ? tq - 4 + rv : TT, q0);
+        const int tn = tq + 8 < TT ? tq + 8 : tq;
+        q0.template load<DS, NP>(pd + tn * DS, pu + tn * CH, pB + tn * NP, pC + tn * NP);
+        four(tq + rv, q1);
       }
+      if constexpr (FULL) pd[(nt - 4 + rv) * DS] = rows_sum4(y);
       __syncthreads();
     }
     if (!live) return;
@@ -155,12 +165,12 @@ __global__ __launch_bounds__(2 * kThreads) void scan_kernel(ScanP p) {
       if (p.hfin == nullptr || seg != p.nseg - 1) return;
 #pragma unroll
       for (int k = 0; k < K; ++k)
-        if (s * K + k < p.N) p.hfin[(int64_t(b) * p.D + d) * p.N + s * K + k] = h[k];
+        if (state(k) < p.N) p.hfin[(int64_t(b) * p.D + d) * p.N + state(k)] = h[k];
     } else {
       const int64_t at = (int64_t(seg) * p.Bt + b) * p.D + d;
 #pragma unroll
       for (int k = 0; k < K; ++k)
-        if (s * K + k < p.N) p.hend[at * p.N + s * K + k] = h[k];
+        if (state(k) < p.N) p.hend[at * p.N + state(k)] = h[k];
       if (s == 0) p.sdel[at] = sum_delta;
     }
     return;
@@ -168,92 +178,153 @@ __global__ __launch_bounds__(2 * kThreads) void scan_kernel(ScanP p) {
 
   // staging: token r of the tile, channels c0 ..
   const int r = tid / (CH / VE), c0 = (tid % (CH / VE)) * VE;
-  const int ncol = p.Dg - (cb * CH + c0) < VE ? p.Dg - (cb * CH + c0) : VE;
-  const int dc = g * p.Dg + cb * CH + c0;
+  const int ncol = p.Dg - (cb * CH + c0) < VE ? p.Dg - (cb * CH + c0) : VE;  // to be stored; none past the group
+  const int cin = ncol > 0 ? cb * CH + c0 : 0, nin = ncol > 0 ? ncol : 1;      // to be read
+  const int dc = g * p.Dg + cin;
   const int64_t row0 = int64_t(b) * p.L;
-  const T* xp = static_cast<const T*>(p.x) + row0 * p.xld + dc;
-  const T* dtp = static_cast<const T*>(p.dt) + row0 * p.dtld + dc;
-  const T* zp = p.z == nullptr ? nullptr : static_cast<const T*>(p.z) + row0 * p.zld + dc;
-  T* yp = FULL ? static_cast<T*>(p.y) + row0 * p.D + dc : nullptr;
+  const bool gated = p.z != nullptr;
+  const int64_t zld = gated ? p.zld : p.xld;
+  // rows of the item (the same for all lanes) and this thread's place in a tile
+  const T* xp = static_cast<const T*>(p.x) + row0 * p.xld + g * p.Dg;
+  const T* dtp = static_cast<const T*>(p.dt) + row0 * p.dtld + g * p.Dg;
+  const T* zp = gated ? static_cast<const T*>(p.z) + row0 * zld + g * p.Dg : xp;
+  const T* bp = static_cast<const T*>(p.B) + row0 * p.Bld + int64_t(g) * p.N;
+  const T* cp = static_cast<const T*>(p.C) + row0 * p.Cld + int64_t(g) * p.N;
+  T* yp = FULL ? static_cast<T*>(p.y) + row0 * p.D + g * p.Dg : nullptr;
   float bias[VE], dsk[VE];
 #pragma unroll
   for (int v = 0; v < VE; ++v) {
-    bias[v] = p.dtb != nullptr && v < ncol ? p.dtb[dc + v] : 0.f;
-    dsk[v] = FULL && p.Dsk != nullptr && v < ncol ? p.Dsk[dc + v] : 0.f;
+    const int dc = g * p.Dg + cin + v;
+    bias[v] = p.dtb != nullptr && v < ncol ? p.dtb[dc] : 0.f;
+    dsk[v] = FULL && p.Dsk != nullptr && v < ncol ? p.Dsk[dc] : 0.f;
   }
-  const bool bcvec = VEC && p.N % 4 == 0;
+  // this thread's quads of B and C: token, first state, which of the two
+  int qt[NQ], qn[NQ];
+  bool qc[NQ];
+#pragma unroll
+  for (int i = 0; i < NQ; ++i) {
+    const int e = (tid + i * kThreads) % (TT * NP / 2);
+    qt[i] = (e / (NP / 4)) % TT;
+    qn[i] = e % (NP / 4) * 4;
+    qc[i] = e / (NP / 4 * TT) == 1;
+  }
+  struct Place {
+    uint32_t x, dt, z, q[NQ];
+  };
+  auto place = [&](int last) {  // rows behind the tile's last one are read from it
+    Place o;
+    const uint32_t rr = r < last ? r : last;
+    o.x = rr * uint32_t(p.xld) + cin;
+    o.dt = rr * uint32_t(p.dtld) + cin;
+    o.z = rr * uint32_t(zld) + cin;
+#pragma unroll
+    for (int i = 0; i < NQ; ++i)
+      o.q[i] = uint32_t(qt[i] < last ? qt[i] : last) * uint32_t(qc[i] ? p.Cld : p.Bld) + (qn[i] < p.N ? qn[i] : 0);
+    return o;
+  };
+  const Place whole_tile = place(TT - 1);
 
   Pack<T, VE> qx{}, qd{}, qz{};
   Pack<T, 4> qb[NQ];
   auto fetch = [&](int t0) {
-    const int t = t0 + r;
-    const bool row = t < tend;
-    qx = load_cols<T, VE, VEC>(xp + int64_t(t) * p.xld, row, ncol);
-    qd = load_cols<T, VE, VEC>(dtp + int64_t(t) * p.dtld, row, ncol);
-    if (FULL && zp != nullptr) qz = load_cols<T, VE, VEC>(zp + int64_t(t) * p.zld, row, ncol);
+    const int64_t tb = t0 < tend ? t0 : tend - 1;
+    Place o = whole_tile;
+    if (tend - 1 - tb < TT - 1) o = place(int(tend - 1 - tb));
+    qx = fetch_cols<T, VE, VEC>(xp + tb * p.xld + o.x, nin);
+    qd = fetch_cols<T, VE, VEC>(dtp + tb * p.dtld + o.dt, nin);
+    if constexpr (FULL) qz = fetch_cols<T, VE, VEC>(zp + tb * zld + o.z, nin);
 #pragma unroll
     for (int i = 0; i < NQ; ++i) {
-      const int e = tid + i * kThreads, q = e % (NP / 4), tt = (e / (NP / 4)) % TT, which = e / (NP / 4 * TT);
-      qb[i] = Pack<T, 4>{};
-      if (which < (FULL ? 2 : 1) && t0 + tt < tend && 4 * q < p.N) {
-        const int64_t ld = which ? p.Cld : p.Bld;
-        const T* src = static_cast<const T*>(which ? p.C : p.B) + (row0 + t0 + tt) * ld + int64_t(g) * p.N + 4 * q;
-        qb[i] = bcvec ? load_pack<T, 4>(src) : load_some<T, 4>(src, p.N - 4 * q);
-      }
+      const int n = p.N - qn[i] < 1 ? 1 : p.N - qn[i];
+      qb[i] = fetch_cols<T, 4, VEC>((qc[i] ? cp + tb * p.Cld : bp + tb * p.Bld) + o.q[i], n);
     }
   };
-  auto stage = [&](int t0, int o) {
+  // skip[o], gate[o]: D x and silu(z) of the tile in half o, for its y
+  float skip[2][VE], gate[2][VE];
+  auto stage = [&](int t0, auto half) {
+    constexpr int o = decltype(half)::value;
+    const bool whole = t0 + TT <= tend;
+    float de[VE], u[VE];
+    unpack<T, VE>(qd, de);
+    unpack<T, VE>(qx, u);
+    if (p.softplus) {
 #pragma unroll
-    for (int v = 0; v < VE; ++v) {
-      const float dl_ = step_of(to_f32(qd.e[v]), p.softplus != 0, bias[v], t0 + r < tend);
-      du[o][r][c0 + c0 / 32 * 2 + v] = float2{dl_, dl_ * to_f32(qx.e[v])};
+      for (int v = 0; v < VE; ++v) de[v] = softplus_fast(de[v] + bias[v]);
     }
+    if constexpr (FULL) {
+      unpack<T, VE>(qz, gate[o]);
+      if (gated) {
+#pragma unroll
+        for (int v = 0; v < VE; ++v) gate[o][v] = silu_f(gate[o][v]);
+      } else {
+#pragma unroll
+        for (int v = 0; v < VE; ++v) gate[o][v] = 1.f;
+      }
+#pragma unroll
+      for (int v = 0; v < VE; ++v) skip[o][v] = dsk[v] * u[v];
+    }
+#pragma unroll
+    for (int v = 0; v < VE; ++v) u[v] *= de[v];
+    if (!whole || ncol < VE) {  // tokens past the end and channels past the group
+#pragma unroll
+      for (int v = 0; v < VE; ++v) {
+        const bool on = t0 + r < tend && v < ncol;
+        de[v] = on ? de[v] : 0.f;
+        u[v] = on ? u[v] : 0.f;
+      }
+    }
+    store_pack<float, VE>(&dl[o][r][c0], de);
+    store_pack<float, VE>(&us[o][r][c0], u);
 #pragma unroll
     for (int i = 0; i < NQ; ++i) {
-      const int e = tid + i * kThreads, q = e % (NP / 4), tt = (e / (NP / 4)) % TT, which = e / (NP / 4 * TT);
-      if (which < 2) {
-        float f[4];
-        unpack<T, 4>(qb[i], f);
-        *reinterpret_cast<f32x4*>(&bc[o][which][tt][4 * q]) = f32x4{f[0], f[1], f[2], f[3]};
+      float f[4];
+      unpack<T, 4>(qb[i], f);
+      if (!whole || p.N < NP) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) f[k] = qn[i] + k < p.N && t0 + qt[i] < tend ? f[k] : 0.f;
       }
+      store_pack<float, 4>(&bc[o][qc[i]][qt[i]][qn[i]], f);
     }
   };
-  auto finish = [&](int t0, int o, const Pack<T, VE>& x, const Pack<T, VE>& z) {
-    float out[VE];
+  // y of a tile, read from where this thread put delta (and puts the next one's)
+  float out[VE];
+  auto finish = [&](auto half) {
+    constexpr int o = decltype(half)::value;
+    unpack<float, VE>(load_pack<float, VE>(&dl[o][r][c0]), out);
 #pragma unroll
     for (int v = 0; v < VE; ++v) {
-      out[v] = fmaf(dsk[v], to_f32(x.e[v]), ys[o][r][c0 + v]);
-      if (zp != nullptr) out[v] *= silu_f(to_f32(z.e[v]));
+      out[v] = (out[v] + skip[o][v]) * gate[o][v];
     }
-    store_cols<T, VE, VEC>(yp + int64_t(t0 + r) * p.D, out, t0 + r < tend, ncol);
   };
-  // x and z of the tile staged last and of the one before it
-  Pack<T, VE> x1{}, z1{}, x2{}, z2{};
+  auto store = [&](int t0) { store_cols<T, VE, VEC>(yp + int64_t(t0) * p.D + (uint32_t(r) * uint32_t(p.D) + cin), out, t0 + r < tend, ncol); };
+  auto step = [&](int i, auto half, auto other) {
+    const int t0 = tbeg + i * TT;
+    if (FULL && i > 0) finish(other);
+    if (i + 1 < tiles) {
+      stage(t0 + TT, other);
+      fetch(t0 + 2 * TT);
+    }
+    // last, so that no wait for the loads above waits for it as well
+    if (FULL && i > 0) store(t0 - TT);
+    __syncthreads();
+  };
+  const std::integral_constant<int, 0> even;
+  const std::integral_constant<int, 1> odd;
   if (tiles > 0) {
     fetch(tbeg);
-    stage(tbeg, 0);
-    x1 = qx;
-    z1 = qz;
-    if (tiles > 1) fetch(tbeg + TT);
+    stage(tbeg, even);
+    fetch(tbeg + TT);
   }
   __syncthreads();
-  for (int i = 0; i < tiles; ++i) {
-    const int t0 = tbeg + i * TT;
-    const Pack<T, VE> xo = x2, zo = z2;  // tile i - 1
-    x2 = x1;
-    z2 = z1;
-    if (i + 1 < tiles) {
-      stage(t0 + TT, (i + 1) & 1);
-      x1 = qx;
-      z1 = qz;
-      if (i + 2 < tiles) fetch(t0 + 2 * TT);
-    }
-    if constexpr (FULL)
-      if (i > 0) finish(t0 - TT, (i - 1) & 1, xo, zo);
-    __syncthreads();
+  for (int i = 0; i < tiles; i += 2) {
+    step(i, even, odd);
+    if (i + 1 < tiles) step(i + 1, odd, even);
   }
-  if constexpr (FULL)
-    if (tiles > 0) finish(tbeg + (tiles - 1) * TT, (tiles - 1) & 1, x2, z2);
+  if (FULL && tiles > 0) {
+    if (tiles % 2) finish(even);
+    else finish(odd);
+    store(tbeg + (tiles - 1) * TT);
+  }
 }
 
 struct StepP {
@@ -271,6 +342,16 @@ struct StepP {
   void* y;
   int Bt, D, N, G, Dg, softplus, nb;
 };
+
+// Sum over S neighbouring lanes, in each of them.
+template <int S>
+__device__ __forceinline__ float lanes_sum(float v) {
+  if constexpr (S >= 2) v += dpp<0xB1, 0xF, true>(v);    // lane ^ 1
+  if constexpr (S >= 4) v += dpp<0x4E, 0xF, true>(v);    // lane ^ 2
+  if constexpr (S >= 8) v += dpp<0x141, 0xF, true>(v);   // mirrored within 8
+  if constexpr (S >= 16) v += dpp<0x140, 0xF, true>(v);  // mirrored within 16
+  return v;
+}
 
 // One token: S lanes per (item, channel), 4 states each in one 16-byte word;
 // the state is read and written once, everything else is small beside it.
@@ -321,18 +402,14 @@ __global__ __launch_bounds__(kThreads) void scan_step_kernel(StepP p) {
 }
 
 struct Plan {
-  int K, S, nblk, nseg, seglen;
+  int NB, nblk, nseg, seglen;
 };
 // Segments of the token axis: with fewer blocks than two per compute unit the
 // axis is cut, at least 128 tokens to a segment.
 Plan plan_of(const m3_scan_args& a) {
   Plan p;
-  p.K = 4;
-  p.S = lanes_for(a.N);
-#ifdef M3_K2
-  if (a.N > 8 && a.N <= 16) p.K = 2, p.S = 8;
-#endif
-  p.nblk = blocks_per_group(a.D / a.G, p.S);
+  p.NB = state_blocks(a.N);
+  p.nblk = blocks_per_group(a.D / a.G);
   p.nseg = 1;
   p.seglen = a.L;
   const int64_t blocks = int64_t(a.Bt) * a.G * p.nblk;
@@ -345,7 +422,7 @@ Plan plan_of(const m3_scan_args& a) {
   return p;
 }
 
-template <typename T, int K, int S, bool VEC>
+template <typename T, int NB, bool VEC>
 hipError_t run(const m3_scan_args& a, Plan pl, hipStream_t st) {
   if (a.workspace == nullptr) pl.nseg = 1, pl.seglen = a.L;
   ScanP p{a.x, a.dt, a.z, a.B, a.C, a.x_ld, a.dt_ld, a.z_ld, a.B_ld, a.C_ld, a.A, a.D_skip, a.dt_bias, a.h0, a.lengths, a.y,
@@ -354,11 +431,11 @@ hipError_t run(const m3_scan_args& a, Plan pl, hipStream_t st) {
   if (pl.nseg > 1) {
     p.hend = static_cast<float*>(a.workspace);
     p.sdel = p.hend + int64_t(pl.nseg - 1) * a.Bt * a.D * a.N;
-    scan_kernel<T, K, S, VEC, false><<<uint32_t(per * (pl.nseg - 1)), 2 * kThreads, 0, st>>>(p);
+    scan_kernel<T, NB, VEC, false><<<uint32_t(per * (pl.nseg - 1)), 2 * kThreads, 0, st>>>(p);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
-  scan_kernel<T, K, S, VEC, true><<<uint32_t(per * pl.nseg), 2 * kThreads, 0, st>>>(p);
+  scan_kernel<T, NB, VEC, true><<<uint32_t(per * pl.nseg), 2 * kThreads, 0, st>>>(p);
   return hipGetLastError();
 }
 template <typename T, int S, bool VEC>
@@ -371,23 +448,16 @@ hipError_t run_step(const m3_scan_step_args& a, hipStream_t st) {
 }
 
 template <typename T, bool VEC>
-hipError_t by_lanes(const m3_scan_args& a, const Plan& p, hipStream_t st) {
-  switch (p.S) {
-    case 2: return run<T, 4, 2, VEC>(a, p, st);
-    case 4: return run<T, 4, 4, VEC>(a, p, st);
-    case 8: return p.K == 2 ? run<T, 2, 8, VEC>(a, p, st) : run<T, 4, 8, VEC>(a, p, st);
-    default: return run<T, 4, 16, VEC>(a, p, st);
-  }
+hipError_t by_states(const m3_scan_args& a, const Plan& p, hipStream_t st) {
+  if (p.NB == 1) return run<T, 1, VEC>(a, p, st);
+  return p.NB == 2 ? run<T, 2, VEC>(a, p, st) : run<T, 4, VEC>(a, p, st);
 }
 template <typename T, bool VEC>
 hipError_t step_by_lanes(const m3_scan_step_args& a, hipStream_t st) {
   if (a.N <= 4) return run_step<T, 1, VEC>(a, st);
-  switch (lanes_for(a.N)) {
-    case 2: return run_step<T, 2, VEC>(a, st);
-    case 4: return run_step<T, 4, VEC>(a, st);
-    case 8: return run_step<T, 8, VEC>(a, st);
-    default: return run_step<T, 16, VEC>(a, st);
-  }
+  if (a.N <= 8) return run_step<T, 2, VEC>(a, st);
+  if (a.N <= 16) return run_step<T, 4, VEC>(a, st);
+  return a.N <= 32 ? run_step<T, 8, VEC>(a, st) : run_step<T, 16, VEC>(a, st);
 }
 
 }  // namespace
@@ -402,13 +472,13 @@ hipError_t launch_scan(const m3_scan_args& a, hipStream_t s) {
   const size_t e = bf ? 2 : 4;
   // a staging thread's channels, and four values of B or C, as whole words
   const scan::Plan p = scan::plan_of(a);
-  const int ve = scan::tile(p.S) / p.S;
+  const int ve = scan::tile(p.NB) * scan::CH / scan::kThreads;
   const size_t word = e * ve < 16 ? e * ve : 16;
   const bool vec = (a.D / a.G) % ve == 0 && rows_aligned(a.x, a.x_ld, e, word) && rows_aligned(a.dt, a.dt_ld, e, word) &&
                    rows_aligned(a.z, a.z_ld, e, word) && rows_aligned(a.y, a.D, e, word) &&
-                   (a.N % 4 != 0 || (rows_aligned(a.B, a.B_ld, e, 4 * e) && rows_aligned(a.C, a.C_ld, e, 4 * e)));
-  if (bf) return vec ? scan::by_lanes<bf16_t, true>(a, p, s) : scan::by_lanes<bf16_t, false>(a, p, s);
-  return vec ? scan::by_lanes<float, true>(a, p, s) : scan::by_lanes<float, false>(a, p, s);
+                   a.N % 4 == 0 && rows_aligned(a.B, a.B_ld, e, 4 * e) && rows_aligned(a.C, a.C_ld, e, 4 * e);
+  if (bf) return vec ? scan::by_states<bf16_t, true>(a, p, s) : scan::by_states<bf16_t, false>(a, p, s);
+  return vec ? scan::by_states<float, true>(a, p, s) : scan::by_states<float, false>(a, p, s);
 }
 hipError_t launch_scan_step(const m3_scan_step_args& a, hipStream_t s) {
   const bool bf = a.in_dtype == M3_BF16;

@@ -26,6 +26,16 @@ namespace scan {
 namespace {
 
 constexpr int TB = 16;  // tokens per tile of the reverse walk
+inline int lanes_for(int N) { return N <= 8 ? 2 : N <= 16 ? 4 : N <= 32 ? 8 : 16; }  // of 4 states each
+inline int blocks_per_group(int Dg, int S) { return (Dg + kThreads / S - 1) / (kThreads / S); }
+template <int S>
+__device__ __forceinline__ float lanes_sum(float v) {
+  if constexpr (S >= 2) v += dpp<0xB1, 0xF, true>(v);    // lane ^ 1
+  if constexpr (S >= 4) v += dpp<0x4E, 0xF, true>(v);    // lane ^ 2
+  if constexpr (S >= 8) v += dpp<0x141, 0xF, true>(v);   // mirrored within 8
+  if constexpr (S >= 16) v += dpp<0x140, 0xF, true>(v);  // mirrored within 16
+  return v;
+}
 
 struct BwP {
   const void* x;

@@ -4,13 +4,17 @@
 //   h_t[d,n] = exp(delta_t[d] A[d,n]) h_{t-1}[d,n] + u_t[d] B_t[n],  u = delta x
 //
 // With a decay of its own for every (channel, state) pair the recurrence has no
-// matrix-product form: it is one exponential, two multiplies and a multiply-add
-// per (token, channel, state), and one more multiply-add for the readout.  So
-// the vector ALUs bound it.  A channel's N states lie in S neighbouring lanes,
-// K each; a block of 256 lanes owns 256 / S channels of one group and walks the
-// token axis in tiles.  What is shared by a channel's lanes (delta, u, the
-// gate) or by all channels (B, C) is computed or converted once per tile by the
-// block and passed on in LDS.
+// matrix-product form: per (token, channel, state) it is a multiply, an
+// exponential and a multiply-add, and one more multiply-add for the readout.  So
+// the vector ALUs bound it, the exponentials (half rate) for two fifths.
+//
+// A wave holds 16 channels, lane = 16 s + channel, with the states 16 i + 4 s ..
+// + 3 (i < NB) of its channel in registers: a token's sum over the states of
+// four tokens takes three lane swaps and three additions.  What is shared by a
+// channel's lanes (delta, u, the gate) or by all channels (B, C) is computed or
+// converted once per tile and passed on in LDS.  (This is also the layout of a
+// 16 x 16 fp32 matrix product's result; forming u_t B_t^T on the matrix cores
+// saved a ninth of the vector instructions and made the scan a quarter slower.)
 #pragma once
 #include "layer_internal.hpp"
 
@@ -46,47 +50,28 @@ __device__ __forceinline__ int block_on_xcd() {
   return n % 8 == 0 ? (i & 7) * (n >> 3) + (i >> 3) : i;
 }
 
-// Sum over the S neighbouring lanes of a channel, in each of them.
-template <int S>
-__device__ __forceinline__ float lanes_sum(float v) {
-  if constexpr (S >= 2) v += dpp<0xB1, 0xF, true>(v);    // lane ^ 1
-  if constexpr (S >= 4) v += dpp<0x4E, 0xF, true>(v);    // lane ^ 2
-  if constexpr (S >= 8) v += dpp<0x141, 0xF, true>(v);   // mirrored within 8
-  if constexpr (S >= 16) v += dpp<0x140, 0xF, true>(v);  // mirrored within 16
-  return v;
+// Sums over the four lanes of a channel of four values, one left in each lane:
+// row q of 16 lanes ends with the sum of v[row_value(q)].
+__device__ __forceinline__ int row_value(int q) { return (q & 1) << 1 | q >> 1; }  // 0, 2, 1, 3
+__device__ __forceinline__ float rows_sum4(const float* v) {
+  const auto a = __builtin_amdgcn_permlane32_swap(__float_as_uint(v[0]), __float_as_uint(v[1]), false, false);
+  const auto b = __builtin_amdgcn_permlane32_swap(__float_as_uint(v[2]), __float_as_uint(v[3]), false, false);
+  const float lo = __uint_as_float(a[0]) + __uint_as_float(a[1]), hi = __uint_as_float(b[0]) + __uint_as_float(b[1]);
+  const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(lo), __float_as_uint(hi), false, false);
+  return __uint_as_float(r[0]) + __uint_as_float(r[1]);
 }
-
-// m ? a : b for an all-ones or all-zeros m, as one bit-field instruction (a
-// ternary of sums becomes a branch around them).
-__device__ __forceinline__ float pick(uint32_t m, float a, float b) {
-  return __uint_as_float((__float_as_uint(a) & m) | (__float_as_uint(b) & ~m));
-}
-// Sums over a channel's S lanes of four values, one value left in each lane:
-// lane s ends with the sum of v[s & 3] (S = 2: v[s] and v[2 + s]).  Halving the
-// values with the lanes takes 9 instructions at S = 4 instead of 8 for four
-// full sums and the selection after them.  odd, two: all ones where s & 1, s & 2.
-template <int S>
-__device__ __forceinline__ void lanes_sum4(const float (&v)[4], uint32_t odd, uint32_t two, float& r0, float& r1) {
-  float t[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    t[i] = v[i];
-    if constexpr (S >= 16) t[i] += dpp<0x140, 0xF, true>(t[i]);
-    if constexpr (S >= 8) t[i] += dpp<0x141, 0xF, true>(t[i]);
-  }
-  const float a = pick(odd, t[1], t[0]) + dpp<0xB1, 0xF, true>(pick(odd, t[0], t[1]));
-  const float b = pick(odd, t[3], t[2]) + dpp<0xB1, 0xF, true>(pick(odd, t[2], t[3]));
-  if constexpr (S >= 4) {
-    r0 = pick(two, b, a) + dpp<0x4E, 0xF, true>(pick(two, a, b));
-    r1 = 0.f;
-  } else {
-    r0 = a;
-    r1 = b;
-  }
-}
-
 // One tile's share of a row-major [token][channel] tensor: this thread's VE
-// neighbouring channels of one token.
+// neighbouring channels of one token.  The loads have no branch around them (a
+// branch makes the compiler wait for the values at its end): rows and columns
+// past the edge are read from the nearest ones inside and dropped by the user.
+template <typename T, int VE, bool VEC>
+__device__ __forceinline__ Pack<T, VE> fetch_cols(const T* p, int ncol) {
+  if constexpr (VEC) return load_pack<T, VE>(p);
+  Pack<T, VE> q;
+#pragma unroll
+  for (int v = 0; v < VE; ++v) q.e[v] = p[v < ncol ? v : ncol - 1];
+  return q;
+}
 template <typename T, int VE, bool VEC>
 __device__ __forceinline__ Pack<T, VE> load_cols(const T* p, bool row, int ncol) {
   Pack<T, VE> q{};
@@ -107,8 +92,9 @@ __device__ __forceinline__ void store_cols(T* p, const float* v, bool row, int n
 }
 
 // Blocks of channels never straddle two groups.
-inline int lanes_for(int N) { return N <= 8 ? 2 : N <= 16 ? 4 : N <= 32 ? 8 : 16; }  // of 4 states each
-inline int blocks_per_group(int Dg, int S) { return (Dg + kThreads / S - 1) / (kThreads / S); }
+constexpr int CH = 64;  // channels of a block: 16 for each of its four scanning waves
+inline int state_blocks(int N) { return N <= 16 ? 1 : N <= 32 ? 2 : 4; }  // of 16 states
+inline int blocks_per_group(int Dg) { return (Dg + CH - 1) / CH; }
 
 }  // namespace scan
 }  // namespace m3
