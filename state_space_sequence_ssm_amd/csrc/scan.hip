@@ -8,22 +8,15 @@ namespace scan {
 namespace {
 
 struct ScanP {
-  const void* x;
-  const void* dt;
-  const void* z;
-  const void* B;
-  const void* C;
-  int64_t xld, dtld, zld, Bld, Cld;
+  Inputs in;
   const float* A;
-  const float* Dsk;
-  const float* dtb;
   const float* h0;
   const int32_t* lengths;
   void* y;
   float* hfin;
   float* hend;  // [nseg - 1][Bt][D][N] states of the segments from zero (segment 0: from h0)
   float* sdel;  // [nseg - 1][Bt][D] sums of delta
-  int Bt, L, D, N, G, Dg, nblk, nseg, seglen, softplus;
+  int Bt, nblk, nseg, seglen, softplus;
 };
 
 constexpr int tile(int NB) { return NB == 4 ? 16 : 32; }  // tokens per tile
@@ -60,7 +53,6 @@ struct Four {
 template <typename T, int NB, bool VEC, bool FULL>
 __global__ __launch_bounds__(2 * kThreads) void scan_kernel(ScanP p) {
   constexpr int TT = tile(NB), VE = TT * CH / kThreads, NP = 16 * NB, K = 4 * NB;
-  constexpr int NQ = (TT * NP / 2 + kThreads - 1) / kThreads;  // quads of B and C per staging thread
   constexpr int DS = CH + 16;  // rows of delta, then of y, whose four tokens are written together: on different banks
   __shared__ __align__(16) float dl[2][TT + 1][DS];
   __shared__ __align__(16) float us[2][TT][CH];
@@ -71,10 +63,10 @@ __global__ __launch_bounds__(2 * kThreads) void scan_kernel(ScanP p) {
   int blk = block_on_xcd();
   const int cb = blk % p.nblk;
   blk /= p.nblk;
-  const int g = blk % p.G;
-  blk /= p.G;
+  const int g = blk % p.in.G;
+  blk /= p.in.G;
   const int b = blk % p.Bt, seg = blk / p.Bt;
-  const int len = item_length(p.lengths, b, p.L);
+  const int len = item_length(p.lengths, b, p.in.L);
   const int tbeg = seg * p.seglen;
   const int tend = tbeg + p.seglen < len ? tbeg + p.seglen : len;
   const int tiles = tend > tbeg ? (tend - tbeg + TT - 1) / TT : 0;
@@ -82,24 +74,24 @@ __global__ __launch_bounds__(2 * kThreads) void scan_kernel(ScanP p) {
   if (scanner) {
     const int lane = tid & 63, s = lane >> 4, chl = (tid >> 6) * 16 + (lane & 15);
     const int dloc = cb * CH + chl;
-    const bool live = dloc < p.Dg;
-    const int d = g * p.Dg + (live ? dloc : 0);
+    const bool live = dloc < p.in.Dg;
+    const int d = g * p.in.Dg + (live ? dloc : 0);
     float A2[K], h[K], sum_delta = 0.f;
     auto state = [&](int k) { return 16 * (k / 4) + 4 * s + k % 4; };
 #pragma unroll
     for (int k = 0; k < K; ++k) {
       const int n = state(k);
-      const bool on = live && n < p.N;
-      A2[k] = on ? p.A[int64_t(d) * p.N + n] * kLog2e : 0.f;
-      h[k] = on && p.h0 != nullptr && (FULL || seg == 0) ? p.h0[(int64_t(b) * p.D + d) * p.N + n] : 0.f;
+      const bool on = live && n < p.in.N;
+      A2[k] = on ? p.A[int64_t(d) * p.in.N + n] * kLog2e : 0.f;
+      h[k] = on && p.h0 != nullptr && (FULL || seg == 0) ? p.h0[(int64_t(b) * p.in.D + d) * p.in.N + n] : 0.f;
     }
     if constexpr (FULL) {
       for (int q = 0; q < seg; ++q) {
-        const int64_t at = (int64_t(q) * p.Bt + b) * p.D + d;
+        const int64_t at = (int64_t(q) * p.Bt + b) * p.in.D + d;
         const float sd = p.sdel[at];
 #pragma unroll
         for (int k = 0; k < K; ++k) {
-          const float e = state(k) < p.N ? p.hend[at * p.N + state(k)] : 0.f;
+          const float e = state(k) < p.in.N ? p.hend[at * p.in.N + state(k)] : 0.f;
           h[k] = q == 0 ? e : fmaf(decay(sd, A2[k]), h[k], e);
         }
       }
@@ -165,95 +157,42 @@ __global__ __launch_bounds__(2 * kThreads) void scan_kernel(ScanP p) {
       if (p.hfin == nullptr || seg != p.nseg - 1) return;
 #pragma unroll
       for (int k = 0; k < K; ++k)
-        if (state(k) < p.N) p.hfin[(int64_t(b) * p.D + d) * p.N + state(k)] = h[k];
+        if (state(k) < p.in.N) p.hfin[(int64_t(b) * p.in.D + d) * p.in.N + state(k)] = h[k];
     } else {
-      const int64_t at = (int64_t(seg) * p.Bt + b) * p.D + d;
+      const int64_t at = (int64_t(seg) * p.Bt + b) * p.in.D + d;
 #pragma unroll
       for (int k = 0; k < K; ++k)
-        if (state(k) < p.N) p.hend[at * p.N + state(k)] = h[k];
+        if (state(k) < p.in.N) p.hend[at * p.in.N + state(k)] = h[k];
       if (s == 0) p.sdel[at] = sum_delta;
     }
     return;
   }
 
-  // staging: token r of the tile, channels c0 ..
-  const int r = tid / (CH / VE), c0 = (tid % (CH / VE)) * VE;
-  const int ncol = p.Dg - (cb * CH + c0) < VE ? p.Dg - (cb * CH + c0) : VE;  // to be stored; none past the group
-  const int cin = ncol > 0 ? cb * CH + c0 : 0, nin = ncol > 0 ? ncol : 1;      // to be read
-  const int dc = g * p.Dg + cin;
-  const int64_t row0 = int64_t(b) * p.L;
-  const bool gated = p.z != nullptr;
-  const int64_t zld = gated ? p.zld : p.xld;
-  // rows of the item (the same for all lanes) and this thread's place in a tile
-  const T* xp = static_cast<const T*>(p.x) + row0 * p.xld + g * p.Dg;
-  const T* dtp = static_cast<const T*>(p.dt) + row0 * p.dtld + g * p.Dg;
-  const T* zp = gated ? static_cast<const T*>(p.z) + row0 * zld + g * p.Dg : xp;
-  const T* bp = static_cast<const T*>(p.B) + row0 * p.Bld + int64_t(g) * p.N;
-  const T* cp = static_cast<const T*>(p.C) + row0 * p.Cld + int64_t(g) * p.N;
-  T* yp = FULL ? static_cast<T*>(p.y) + row0 * p.D + g * p.Dg : nullptr;
+  Stager<T, TT, CH, NP, VEC, FULL, false, FULL> st;
+  st.init(p.in, b, g, cb, tid, tend);
+  const int r = st.r, c0 = st.c0;
+  T* yp = FULL ? static_cast<T*>(p.y) + int64_t(b) * p.in.L * p.in.D + g * p.in.Dg : nullptr;
   float bias[VE], dsk[VE];
 #pragma unroll
   for (int v = 0; v < VE; ++v) {
-    const int dc = g * p.Dg + cin + v;
-    bias[v] = p.dtb != nullptr && v < ncol ? p.dtb[dc] : 0.f;
-    dsk[v] = FULL && p.Dsk != nullptr && v < ncol ? p.Dsk[dc] : 0.f;
+    const int dc = g * p.in.Dg + st.cin + v;
+    bias[v] = p.in.dtb != nullptr && v < st.ncol ? p.in.dtb[dc] : 0.f;
+    dsk[v] = FULL && p.in.Dsk != nullptr && v < st.ncol ? p.in.Dsk[dc] : 0.f;
   }
-  // this thread's quads of B and C: token, first state, which of the two
-  int qt[NQ], qn[NQ];
-  bool qc[NQ];
-#pragma unroll
-  for (int i = 0; i < NQ; ++i) {
-    const int e = (tid + i * kThreads) % (TT * NP / 2);
-    qt[i] = (e / (NP / 4)) % TT;
-    qn[i] = e % (NP / 4) * 4;
-    qc[i] = e / (NP / 4 * TT) == 1;
-  }
-  struct Place {
-    uint32_t x, dt, z, q[NQ];
-  };
-  auto place = [&](int last) {  // rows behind the tile's last one are read from it
-    Place o;
-    const uint32_t rr = r < last ? r : last;
-    o.x = rr * uint32_t(p.xld) + cin;
-    o.dt = rr * uint32_t(p.dtld) + cin;
-    o.z = rr * uint32_t(zld) + cin;
-#pragma unroll
-    for (int i = 0; i < NQ; ++i)
-      o.q[i] = uint32_t(qt[i] < last ? qt[i] : last) * uint32_t(qc[i] ? p.Cld : p.Bld) + (qn[i] < p.N ? qn[i] : 0);
-    return o;
-  };
-  const Place whole_tile = place(TT - 1);
-
-  Pack<T, VE> qx{}, qd{}, qz{};
-  Pack<T, 4> qb[NQ];
-  auto fetch = [&](int t0) {
-    const int64_t tb = t0 < tend ? t0 : tend - 1;
-    Place o = whole_tile;
-    if (tend - 1 - tb < TT - 1) o = place(int(tend - 1 - tb));
-    qx = fetch_cols<T, VE, VEC>(xp + tb * p.xld + o.x, nin);
-    qd = fetch_cols<T, VE, VEC>(dtp + tb * p.dtld + o.dt, nin);
-    if constexpr (FULL) qz = fetch_cols<T, VE, VEC>(zp + tb * zld + o.z, nin);
-#pragma unroll
-    for (int i = 0; i < NQ; ++i) {
-      const int n = p.N - qn[i] < 1 ? 1 : p.N - qn[i];
-      qb[i] = fetch_cols<T, 4, VEC>((qc[i] ? cp + tb * p.Cld : bp + tb * p.Bld) + o.q[i], n);
-    }
-  };
   // skip[o], gate[o]: D x and silu(z) of the tile in half o, for its y
   float skip[2][VE], gate[2][VE];
   auto stage = [&](int t0, auto half) {
     constexpr int o = decltype(half)::value;
-    const bool whole = t0 + TT <= tend;
     float de[VE], u[VE];
-    unpack<T, VE>(qd, de);
-    unpack<T, VE>(qx, u);
+    unpack<T, VE>(st.qd, de);
+    unpack<T, VE>(st.qx, u);
     if (p.softplus) {
 #pragma unroll
       for (int v = 0; v < VE; ++v) de[v] = softplus_fast(de[v] + bias[v]);
     }
     if constexpr (FULL) {
-      unpack<T, VE>(qz, gate[o]);
-      if (gated) {
+      unpack<T, VE>(st.qz, gate[o]);
+      if (st.gated) {
 #pragma unroll
         for (int v = 0; v < VE; ++v) gate[o][v] = silu_f(gate[o][v]);
       } else {
@@ -265,26 +204,17 @@ __global__ __launch_bounds__(2 * kThreads) void scan_kernel(ScanP p) {
     }
 #pragma unroll
     for (int v = 0; v < VE; ++v) u[v] *= de[v];
-    if (!whole || ncol < VE) {  // tokens past the end and channels past the group
+    if (st.edge(t0)) {  // tokens past the end and channels past the group
 #pragma unroll
       for (int v = 0; v < VE; ++v) {
-        const bool on = t0 + r < tend && v < ncol;
+        const bool on = st.inside(t0, v);
         de[v] = on ? de[v] : 0.f;
         u[v] = on ? u[v] : 0.f;
       }
     }
     store_pack<float, VE>(&dl[o][r][c0], de);
     store_pack<float, VE>(&us[o][r][c0], u);
-#pragma unroll
-    for (int i = 0; i < NQ; ++i) {
-      float f[4];
-      unpack<T, 4>(qb[i], f);
-      if (!whole || p.N < NP) {
-#pragma unroll
-        for (int k = 0; k < 4; ++k) f[k] = qn[i] + k < p.N && t0 + qt[i] < tend ? f[k] : 0.f;
-      }
-      store_pack<float, 4>(&bc[o][qc[i]][qt[i]][qn[i]], f);
-    }
+    st.put_bc(t0, &bc[o][0][0][0]);
   };
   // y of a tile, read from where this thread put delta (and puts the next one's)
   float out[VE];
@@ -296,13 +226,13 @@ __global__ __launch_bounds__(2 * kThreads) void scan_kernel(ScanP p) {
       out[v] = (out[v] + skip[o][v]) * gate[o][v];
     }
   };
-  auto store = [&](int t0) { store_cols<T, VE, VEC>(yp + int64_t(t0) * p.D + (uint32_t(r) * uint32_t(p.D) + cin), out, t0 + r < tend, ncol); };
+  auto store = [&](int t0) { store_cols<T, VE, VEC>(yp + int64_t(t0) * p.in.D + (uint32_t(r) * uint32_t(p.in.D) + st.cin), out, t0 + r < tend, st.ncol); };
   auto step = [&](int i, auto half, auto other) {
     const int t0 = tbeg + i * TT;
     if (FULL && i > 0) finish(other);
     if (i + 1 < tiles) {
       stage(t0 + TT, other);
-      fetch(t0 + 2 * TT);
+      st.fetch(t0 + 2 * TT);
     }
     // last, so that no wait for the loads above waits for it as well
     if (FULL && i > 0) store(t0 - TT);
@@ -311,9 +241,9 @@ __global__ __launch_bounds__(2 * kThreads) void scan_kernel(ScanP p) {
   const std::integral_constant<int, 0> even;
   const std::integral_constant<int, 1> odd;
   if (tiles > 0) {
-    fetch(tbeg);
+    st.fetch(tbeg);
     stage(tbeg, even);
-    fetch(tbeg + TT);
+    st.fetch(tbeg + TT);
   }
   __syncthreads();
   for (int i = 0; i < tiles; i += 2) {
@@ -425,8 +355,9 @@ Plan plan_of(const m3_scan_args& a) {
 template <typename T, int NB, bool VEC>
 hipError_t run(const m3_scan_args& a, Plan pl, hipStream_t st) {
   if (a.workspace == nullptr) pl.nseg = 1, pl.seglen = a.L;
-  ScanP p{a.x, a.dt, a.z, a.B, a.C, a.x_ld, a.dt_ld, a.z_ld, a.B_ld, a.C_ld, a.A, a.D_skip, a.dt_bias, a.h0, a.lengths, a.y,
-          a.h_final, nullptr, nullptr, a.Bt, a.L, a.D, a.N, a.G, a.D / a.G, pl.nblk, pl.nseg, pl.seglen, a.dt_softplus};
+  const Inputs in{a.x, a.dt, a.z, a.B, a.C, nullptr, a.x_ld, a.dt_ld, a.z_ld, a.B_ld, a.C_ld, a.D_skip, a.dt_bias, a.L, a.D, a.N,
+                  a.G, a.D / a.G};
+  ScanP p{in, a.A, a.h0, a.lengths, a.y, a.h_final, nullptr, nullptr, a.Bt, pl.nblk, pl.nseg, pl.seglen, a.dt_softplus};
   const int64_t per = int64_t(a.Bt) * a.G * pl.nblk;
   if (pl.nseg > 1) {
     p.hend = static_cast<float*>(a.workspace);

@@ -1,4 +1,4 @@
-// Backward of the selective scan (see scan_common.hpp for the forward's layout).
+// Backward of the selective scan (see scan_common.hpp for the forward).
 //
 // With do_t = dy_t silu(z_t) and g_t the gradient of the state after token t:
 //   g_t = C_t do_t + a_{t+1} g_{t+1},      a_t = exp(delta_t A)
@@ -12,42 +12,31 @@
 // to the first: it computes a tile's decays and states again, keeps them in
 // registers (2 x 16 x 4 per lane) and runs the reverse recurrence over them, so
 // each decay is computed twice in all and no state goes to memory per token.
-// dB and dC are summed over a wave's channels by lane swaps, over the block's
-// waves in LDS and over the blocks from a workspace in a fixed order.
+// dB and dC are summed over a wave's 16 channels in registers, over the block's
+// waves in LDS and over the blocks from a workspace, in a fixed order.
 // The token axis can be cut into segments walked at once: the first walk then
 // starts every segment from zero and also forms, in the same forward pass, what
 // the segment contributes to the gradient in front of it,
 //   sum_t (prod_{r<=t} a_r) C_t do_t,
 // and the second walk joins states from the left and gradients from the right.
+//
+// A wave holds 16 channels and one block of 16 states, lane = 16 s + channel
+// with the states 4 s .. + 3; a block of eight waves (four scan, four stage) is
+// 64 / NB channels of NB state blocks, whose sums over the states the staging
+// waves join.
+#include <type_traits>
+
 #include "scan_common.hpp"
 
 namespace m3 {
 namespace scan {
 namespace {
 
-constexpr int TB = 16;  // tokens per tile of the reverse walk
-inline int lanes_for(int N) { return N <= 8 ? 2 : N <= 16 ? 4 : N <= 32 ? 8 : 16; }  // of 4 states each
-inline int blocks_per_group(int Dg, int S) { return (Dg + kThreads / S - 1) / (kThreads / S); }
-template <int S>
-__device__ __forceinline__ float lanes_sum(float v) {
-  if constexpr (S >= 2) v += dpp<0xB1, 0xF, true>(v);    // lane ^ 1
-  if constexpr (S >= 4) v += dpp<0x4E, 0xF, true>(v);    // lane ^ 2
-  if constexpr (S >= 8) v += dpp<0x141, 0xF, true>(v);   // mirrored within 8
-  if constexpr (S >= 16) v += dpp<0x140, 0xF, true>(v);  // mirrored within 16
-  return v;
-}
+constexpr int TB = 16;  // tokens per tile of the reverse walk, and between two kept states
 
 struct BwP {
-  const void* x;
-  const void* dt;
-  const void* z;
-  const void* B;
-  const void* C;
-  const void* dy;
-  int64_t xld, dtld, zld, Bld, Cld;
+  Inputs in;
   const float* A;
-  const float* Dsk;
-  const float* dtb;
   const float* h0;
   const float* dhf;
   const int32_t* lengths;
@@ -56,425 +45,529 @@ struct BwP {
   void* dz;
   float* dh0;
   float* ck;    // [tiles][blocks][256][4] state in front of each tile (of its segment from zero)
-  float* cd;    // [tiles][blocks][CH] sum of delta from the segment's start to the tile
+  float* cd;    // [tiles][blocks][CHB] sum of delta from the segment's start to the tile
   float* hend;  // [nseg][Bt][D][N] state of a segment from zero (segment 0: from h0)
   float* gsum;  // [nseg][Bt][D][N] a segment's contribution to the gradient in front of it
   float* sdel;  // [nseg][Bt][D] sum of delta
   float* bc;    // [nblk][Bt * L][G][2][NP] sums of dB and dC over a block's channels
   float* part;  // [nseg * Bt][D * N + D + D] sums of dA, dD, ddt_bias
-  int Bt, L, D, N, G, Dg, nblk, nseg, seglen, softplus;
+  int Bt, nblk, nseg, seglen, softplus;
+};
+
+// Where a block and a scanning lane are.
+template <int NB>
+struct Where {
+  static constexpr int CHB = CH / NB;
+  int64_t blocks, unit;
+  int seg, cb, g, b, tbeg, tlim, tend;
+  __device__ __forceinline__ explicit Where(const BwP& p) {
+    int blk = block_on_xcd();
+    blocks = int64_t(p.Bt) * p.in.G * p.nblk;
+    seg = int(blk / blocks);
+    blk = int(blk - seg * blocks);
+    unit = blk;
+    cb = blk % p.nblk;
+    blk /= p.nblk;
+    g = blk % p.in.G;
+    b = blk / p.in.G;
+    const int len = item_length(p.lengths, b, p.in.L);
+    tbeg = seg * p.seglen;
+    tlim = tbeg + p.seglen < p.in.L ? tbeg + p.seglen : p.in.L;
+    tend = tlim < len ? tlim : len;
+  }
+};
+template <int NB>
+struct Lane {
+  int s, chl, n0, d, nleft;  // state group, channel in the block, first state, channel, states left from n0
+  bool live;
+  __device__ __forceinline__ Lane(const BwP& p, const Where<NB>& w, int tid) {
+    const int wave = tid >> 6;
+    s = (tid & 63) >> 4;
+    chl = (wave / NB) * 16 + (tid & 15);
+    n0 = (wave % NB) * 16 + 4 * s;
+    nleft = p.in.N - n0;
+    const int dl = w.cb * Where<NB>::CHB + chl;
+    live = dl < p.in.Dg;
+    d = w.g * p.in.Dg + (live ? dl : 0);
+  }
+};
+
+// Four tokens' values of one lane, in registers.
+template <bool DO, bool CC>
+struct Four {
+  float delta[4], u[4], go[4];
+  f32x4 B[4], C[4];
+  template <int CHB, int NP>
+  __device__ __forceinline__ void load(const float* pd, const float* pu, const float* po, const float* pB, const float* pC) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      delta[j] = pd[j * CHB];
+      u[j] = pu[j * CHB];
+      if (DO) go[j] = po[j * CHB];
+      B[j] = *reinterpret_cast<const f32x4*>(pB + j * NP);
+      if (CC) C[j] = *reinterpret_cast<const f32x4*>(pC + j * NP);
+    }
+  }
 };
 
 // First walk: states in front of the tiles, and with SEG the segments' ends.
-template <typename T, int S, bool VEC, bool SEG>
-__global__ __launch_bounds__(kThreads) void states_kernel(BwP p) {
-  constexpr int K = 4, CH = kThreads / S, TT = S >= 4 ? 32 : 16, VE = TT / S, NP = K * S;
-  constexpr int NQ = (TT * NP / 2 + kThreads - 1) / kThreads;
-  __shared__ __align__(16) float2 du[TT][CH];
-  __shared__ __align__(16) float bc[SEG ? 2 : 1][TT][NP];
-  __shared__ __align__(16) float dos[SEG ? TT : 1][CH];
+template <typename T, int NB, bool VEC, bool SEG>
+__global__ __launch_bounds__(2 * kThreads) void states_kernel(BwP p) {
+  constexpr int TT = 32, CHB = CH / NB, VE = TT * CHB / kThreads, NP = 16 * NB;
+  __shared__ __align__(16) float dl[2][TT][CHB];
+  __shared__ __align__(16) float us[2][TT][CHB];
+  __shared__ __align__(16) float ds[SEG ? 2 : 1][SEG ? TT : 1][CHB];
+  __shared__ __align__(16) float bc[2][SEG ? 2 : 1][TT][NP];
+  const int tid = threadIdx.x % kThreads;
+  const Where<NB> w(p);
+  const int tiles = w.tend > w.tbeg ? (w.tend - w.tbeg + TT - 1) / TT : 0;
 
-  const int tid = threadIdx.x, s = tid % S, chl = tid / S;
-  int blk = block_on_xcd();
-  const int64_t blocks = int64_t(p.Bt) * p.G * p.nblk;
-  const int seg = int(blk / blocks);
-  blk = int(blk - seg * blocks);
-  const int64_t unit = blk;
-  const int cb = blk % p.nblk;
-  blk /= p.nblk;
-  const int g = blk % p.G, b = blk / p.G;
-  const int len = item_length(p.lengths, b, p.L);
-  const int tbeg = seg * p.seglen;
-  const int tend = tbeg + p.seglen < len ? tbeg + p.seglen : len;
-
-  const int dl = cb * CH + chl;
-  const bool live = dl < p.Dg;
-  const int d = g * p.Dg + (live ? dl : 0);
-  float A2[K], h[K], P[K], gs[K];
+  if (threadIdx.x < kThreads) {
+    const Lane<NB> l(p, w, tid);
+    float A2[4], h[4], P[4], gs[4], sum_delta = 0.f;
 #pragma unroll
-  for (int k = 0; k < K; ++k) {
-    const int n = s * K + k;
-    const bool on = live && n < p.N;
-    A2[k] = on ? p.A[int64_t(d) * p.N + n] * kLog2e : 0.f;
-    h[k] = on && p.h0 != nullptr && seg == 0 ? p.h0[(int64_t(b) * p.D + d) * p.N + n] : 0.f;
-    P[k] = 1.f;
-    gs[k] = 0.f;
+    for (int k = 0; k < 4; ++k) {
+      const bool on = l.live && k < l.nleft;
+      A2[k] = on ? p.A[int64_t(l.d) * p.in.N + l.n0 + k] * kLog2e : 0.f;
+      h[k] = on && p.h0 != nullptr && w.seg == 0 ? p.h0[(int64_t(w.b) * p.in.D + l.d) * p.in.N + l.n0 + k] : 0.f;
+      P[k] = 1.f;
+      gs[k] = 0.f;
+    }
+    __syncthreads();
+    for (int t = 0; t < tiles; ++t) {
+      const int left = w.tend - w.tbeg - t * TT, o = t & 1;
+      const float* pd = &dl[o][0][l.chl];
+      const float* pu = &us[o][0][l.chl];
+      const float* po = &ds[SEG ? o : 0][0][l.chl];
+      const float* pB = &bc[o][0][0][l.n0];
+      const float* pC = &bc[o][SEG ? 1 : 0][0][l.n0];
+      auto keep = [&](int tq) {
+        const int64_t at = int64_t((w.tbeg + t * TT + tq) / TB) * w.blocks + w.unit;
+        store_pack<float, 4>(p.ck + (at * kThreads + tid) * 4, h);
+        if (SEG && l.s == 0 && l.n0 == 0) p.cd[at * CHB + l.chl] = sum_delta;
+      };
+      auto four = [&](const Four<SEG, SEG>& q) {
+        float a[4][4], u[4][4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            a[j][k] = decay(q.delta[j], A2[k]);
+            u[j][k] = q.u[j] * q.B[j][k];
+          }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            h[k] = fmaf(a[j][k], h[k], u[j][k]);
+            if constexpr (SEG) {
+              P[k] *= a[j][k];
+              gs[k] = fmaf(P[k], q.C[j][k] * q.go[j], gs[k]);
+            }
+          }
+          if (SEG) sum_delta += q.delta[j];
+        }
+      };
+      // the next four tokens on their way from LDS meanwhile
+      Four<SEG, SEG> q0, q1;
+      q0.template load<CHB, NP>(pd, pu, po, pB, pC);
+#pragma unroll
+      for (int tq = 0; tq < TT; tq += 8) {
+        if (tq >= left) break;
+        if (tq % TB == 0) keep(tq);
+        q1.template load<CHB, NP>(pd + (tq + 4) * CHB, pu + (tq + 4) * CHB, po + (tq + 4) * CHB, pB + (tq + 4) * NP, pC + (tq + 4) * NP);
+        four(q0);
+        const int tn = tq + 8 < TT ? tq + 8 : tq;
+        q0.template load<CHB, NP>(pd + tn * CHB, pu + tn * CHB, po + tn * CHB, pB + tn * NP, pC + tn * NP);
+        four(q1);
+      }
+      __syncthreads();
+    }
+    if (!SEG || !l.live) return;
+    const int64_t at = (int64_t(w.seg) * p.Bt + w.b) * p.in.D + l.d;
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      if (k < l.nleft) {
+        p.hend[at * p.in.N + l.n0 + k] = h[k];
+        p.gsum[at * p.in.N + l.n0 + k] = gs[k];
+      }
+    if (l.s == 0 && l.n0 == 0) p.sdel[at] = sum_delta;
+    return;
   }
-  float sum_delta = 0.f;
 
-  const int r = tid / (CH / VE), c0 = (tid % (CH / VE)) * VE;
-  const int ncol = p.Dg - (cb * CH + c0) < VE ? p.Dg - (cb * CH + c0) : VE;
-  const int dc = g * p.Dg + cb * CH + c0;
-  const int64_t row0 = int64_t(b) * p.L;
-  const T* xp = static_cast<const T*>(p.x) + row0 * p.xld + dc;
-  const T* dtp = static_cast<const T*>(p.dt) + row0 * p.dtld + dc;
-  const T* zp = p.z == nullptr ? nullptr : static_cast<const T*>(p.z) + row0 * p.zld + dc;
-  const T* dyp = static_cast<const T*>(p.dy) + row0 * p.D + dc;
+  Stager<T, TT, CHB, NP, VEC, SEG, SEG, SEG> st;
+  st.init(p.in, w.b, w.g, w.cb, tid, w.tend);
   float bias[VE];
 #pragma unroll
-  for (int v = 0; v < VE; ++v) bias[v] = p.dtb != nullptr && v < ncol ? p.dtb[dc + v] : 0.f;
-  const bool bcvec = VEC && p.N % 4 == 0;
-
-  Pack<T, VE> qx{}, qd{}, qz{}, qy{};
-  Pack<T, 4> qb[NQ];
-  auto fetch = [&](int t0) {
-    const int t = t0 + r;
-    const bool row = t < tend;
-    qx = load_cols<T, VE, VEC>(xp + int64_t(t) * p.xld, row, ncol);
-    qd = load_cols<T, VE, VEC>(dtp + int64_t(t) * p.dtld, row, ncol);
+  for (int v = 0; v < VE; ++v) bias[v] = p.in.dtb != nullptr && v < st.ncol ? p.in.dtb[w.g * p.in.Dg + st.cin + v] : 0.f;
+  auto stage = [&](int t0, int o) {
+    float de[VE], u[VE], go[VE];
+    unpack<T, VE>(st.qd, de);
+    unpack<T, VE>(st.qx, u);
+    if (p.softplus) {
+#pragma unroll
+      for (int v = 0; v < VE; ++v) de[v] = softplus_fast(de[v] + bias[v]);
+    }
+#pragma unroll
+    for (int v = 0; v < VE; ++v) u[v] *= de[v];
     if constexpr (SEG) {
-      qy = load_cols<T, VE, VEC>(dyp + int64_t(t) * p.D, row, ncol);
-      if (zp != nullptr) qz = load_cols<T, VE, VEC>(zp + int64_t(t) * p.zld, row, ncol);
-    }
+      float zv[VE];
+      unpack<T, VE>(st.qy, go);
+      unpack<T, VE>(st.qz, zv);
+      if (st.gated) {
 #pragma unroll
-    for (int i = 0; i < NQ; ++i) {
-      const int e = tid + i * kThreads, q = e % (NP / 4), tt = (e / (NP / 4)) % TT, which = e / (NP / 4 * TT);
-      qb[i] = Pack<T, 4>{};
-      if (which < (SEG ? 2 : 1) && t0 + tt < tend && 4 * q < p.N) {
-        const int64_t ld = which ? p.Cld : p.Bld;
-        const T* src = static_cast<const T*>(which ? p.C : p.B) + (row0 + t0 + tt) * ld + int64_t(g) * p.N + 4 * q;
-        qb[i] = bcvec ? load_pack<T, 4>(src) : load_some<T, 4>(src, p.N - 4 * q);
+        for (int v = 0; v < VE; ++v) go[v] *= silu_f(zv[v]);
       }
     }
+    if (st.edge(t0)) {
+#pragma unroll
+      for (int v = 0; v < VE; ++v) {
+        const bool on = st.inside(t0, v);
+        de[v] = on ? de[v] : 0.f;
+        u[v] = on ? u[v] : 0.f;
+        if (SEG) go[v] = on ? go[v] : 0.f;
+      }
+    }
+    store_pack<float, VE>(&dl[o][st.r][st.c0], de);
+    store_pack<float, VE>(&us[o][st.r][st.c0], u);
+    if constexpr (SEG) store_pack<float, VE>(&ds[o][st.r][st.c0], go);
+    st.put_bc(t0, &bc[o][0][0][0]);
   };
-  if (tbeg < tend) fetch(tbeg);
-  for (int t0 = tbeg; t0 < tend; t0 += TT) {
-#pragma unroll
-    for (int v = 0; v < VE; ++v) {
-      const float dl_ = step_of(to_f32(qd.e[v]), p.softplus != 0, bias[v], t0 + r < tend);
-      du[r][c0 + v] = float2{dl_, dl_ * to_f32(qx.e[v])};
-      if constexpr (SEG) dos[r][c0 + v] = to_f32(qy.e[v]) * (zp != nullptr ? silu_f(to_f32(qz.e[v])) : 1.f);
-    }
-#pragma unroll
-    for (int i = 0; i < NQ; ++i) {
-      const int e = tid + i * kThreads, q = e % (NP / 4), tt = (e / (NP / 4)) % TT, which = e / (NP / 4 * TT);
-      if (which < (SEG ? 2 : 1)) {
-        float f[4];
-        unpack<T, 4>(qb[i], f);
-        *reinterpret_cast<f32x4*>(&bc[which][tt][4 * q]) = f32x4{f[0], f[1], f[2], f[3]};
-      }
-    }
-    __syncthreads();
-    if (t0 + TT < tend) fetch(t0 + TT);
-    const int nt = tend - t0 < TT ? (tend - t0 + 3) & ~3 : TT;
-    for (int tq = 0; tq < nt; tq += 4) {
-      if (tq % TB == 0) {
-        const int64_t at = int64_t((t0 + tq) / TB) * blocks + unit;
-        store_pack<float, 4>(p.ck + (at * kThreads + tid) * 4, h);
-        if (SEG && s == 0) p.cd[at * CH + chl] = sum_delta;
-      }
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int t = tq + i;
-        const float2 q = du[t][chl];
-        if constexpr (SEG) sum_delta += q.x;
-#pragma unroll
-        for (int k = 0; k < K; ++k) {
-          const float a = decay(q.x, A2[k]);
-          h[k] = fmaf(a, h[k], q.y * bc[0][t][s * K + k]);
-          if constexpr (SEG) {
-            P[k] *= a;
-            gs[k] = fmaf(P[k], bc[1][t][s * K + k] * dos[t][chl], gs[k]);
-          }
-        }
-      }
-    }
-    __syncthreads();
+  if (tiles > 0) {
+    st.fetch(w.tbeg);
+    stage(w.tbeg, 0);
+    st.fetch(w.tbeg + TT);
   }
-  if constexpr (SEG) {
-    if (!live) return;
-    const int64_t at = (int64_t(seg) * p.Bt + b) * p.D + d;
-#pragma unroll
-    for (int k = 0; k < K; ++k)
-      if (s * K + k < p.N) {
-        p.hend[at * p.N + s * K + k] = h[k];
-        p.gsum[at * p.N + s * K + k] = gs[k];
-      }
-    if (s == 0) p.sdel[at] = sum_delta;
+  __syncthreads();
+  for (int i = 0; i < tiles; ++i) {
+    if (i + 1 < tiles) {
+      stage(w.tbeg + (i + 1) * TT, (i + 1) & 1);
+      st.fetch(w.tbeg + (i + 2) * TT);
+    }
+    __syncthreads();
   }
 }
 
-// Sum of v[0..3] over a wave's channels (the lanes equal modulo S).  Row q of
-// 16 lanes ends with the sums of v[{0, 2, 1, 3}[q]], in every one of its lanes
-// of the same state group.
-template <int S>
-__device__ __forceinline__ float channels_sum(const float* v) {
-  auto swap32 = [](float a, float b) {
-    const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(a), __float_as_uint(b), false, false);
-    return __uint_as_float(r[0]) + __uint_as_float(r[1]);
-  };
-  const float lo = swap32(v[0], v[1]), hi = swap32(v[2], v[3]);
-  const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(lo), __float_as_uint(hi), false, false);
-  float t = __uint_as_float(r[0]) + __uint_as_float(r[1]);
-  if constexpr (S <= 8) t += dpp<0x128, 0xF, true>(t);  // rotated by 8 within 16
-  if constexpr (S <= 4) t += dpp<0x124, 0xF, true>(t);  // by 4
-  if constexpr (S <= 2) t += dpp<0x122, 0xF, true>(t);  // by 2
+// m ? a : b for an all-ones or all-zeros m, as one bit-field instruction (a
+// ternary of sums becomes a branch around them).
+__device__ __forceinline__ float pick(uint32_t m, float a, float b) {
+  return __uint_as_float((__float_as_uint(a) & m) | (__float_as_uint(b) & ~m));
+}
+// Sum of v[0..3] over the 16 channels of a row of lanes: lane c of the row ends
+// with the sum of v[c & 3].  odd, two: all ones where c & 1, c & 2.
+__device__ __forceinline__ float channels_sum(const float* v, uint32_t odd, uint32_t two) {
+  const float a = pick(odd, v[1], v[0]) + dpp<0xB1, 0xF, true>(pick(odd, v[0], v[1]));
+  const float b = pick(odd, v[3], v[2]) + dpp<0xB1, 0xF, true>(pick(odd, v[2], v[3]));
+  float t = pick(two, b, a) + dpp<0x4E, 0xF, true>(pick(two, a, b));
+  t += dpp<0x124, 0xF, true>(t);  // rotated by 4 within 16
+  t += dpp<0x128, 0xF, true>(t);  // by 8
   return t;
 }
 
+// LDS of the reverse walk; everything twice, a tile being staged, and the one
+// before finished, while one is walked.
+template <int NB>
+struct Shared {
+  static constexpr int CHB = CH / NB, NP = 16 * NB;
+  float dl[2][TB][CHB], us[2][TB][CHB], ds[2][TB][CHB];  // delta, u, do
+  float bc[2][2][TB][NP];
+  float o[2][NB][TB][CHB], gB[2][NB][TB][CHB], gA[2][NB][TB][CHB];  // sums over a block's 16 states
+  float wp[2][4 / NB][TB][2][NP];                                   // dB and dC of a wave's 16 channels
+};
+
 // Second walk.
-template <typename T, int S, bool VEC>
-__global__ __launch_bounds__(kThreads) void reverse_kernel(BwP p) {
-  constexpr int K = 4, CH = kThreads / S, VE = TB / S, NP = K * S;
-  constexpr int NQ = (TB * NP / 2 + kThreads - 1) / kThreads;
-  constexpr int YS = CH + 64 / S;
-  __shared__ __align__(16) float2 du[TB][CH];
-  __shared__ __align__(16) float dos[TB][CH];
-  __shared__ __align__(16) float bc[2][TB][NP];
-  __shared__ __align__(16) float os[TB][YS];
-  __shared__ __align__(16) float gb[2][TB][YS];
-  __shared__ __align__(16) float wp[4][TB][2][NP];
+template <typename T, int NB, bool VEC>
+__global__ __launch_bounds__(2 * kThreads) void reverse_kernel(BwP p) {
+  constexpr int CHB = CH / NB, VE = TB * CHB / kThreads, NP = 16 * NB;
+  extern __shared__ __align__(16) unsigned char smem[];
+  Shared<NB>& sh = *reinterpret_cast<Shared<NB>*>(smem);
+  const int tid = threadIdx.x % kThreads;
+  const Where<NB> w(p);
+  const int tiles = w.tend > w.tbeg ? (w.tend - w.tbeg + TB - 1) / TB : 0;
+  const int64_t ncols = int64_t(p.in.D) * (p.in.N + 2);
+  float* part = p.part + (int64_t(w.seg) * p.Bt + w.b) * ncols;
 
-  const int tid = threadIdx.x, s = tid % S, chl = tid / S, lane = tid & 63, wv = tid >> 6;
-  int blk = block_on_xcd();
-  const int64_t blocks = int64_t(p.Bt) * p.G * p.nblk;
-  const int seg = int(blk / blocks);
-  blk = int(blk - seg * blocks);
-  const int64_t unit = blk;
-  const int cb = blk % p.nblk;
-  blk /= p.nblk;
-  const int g = blk % p.G, b = blk / p.G;
-  const int len = item_length(p.lengths, b, p.L);
-  const int tbeg = seg * p.seglen;
-  const int tlim = tbeg + p.seglen < p.L ? tbeg + p.seglen : p.L;
-  const int tend = tlim < len ? tlim : len;
+  if (threadIdx.x < kThreads) {
+    const Lane<NB> l(p, w, tid);
+    const int wave = tid >> 6, blk = wave % NB;
+    const int64_t at0 = int64_t(w.b) * p.in.D + l.d, per = int64_t(p.Bt) * p.in.D;
+    const uint32_t odd = tid & 1 ? ~0u : 0u, two = tid & 2 ? ~0u : 0u, four = tid & 4 ? ~0u : 0u, eight = tid & 8 ? ~0u : 0u;
+    const int rv = row_value(l.s);
+    float A2[4], gg[4], hin[4], dA[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const bool on = l.live && k < l.nleft;
+      A2[k] = on ? p.A[int64_t(l.d) * p.in.N + l.n0 + k] * kLog2e : 0.f;
+      gg[k] = on && p.dhf != nullptr ? p.dhf[at0 * p.in.N + l.n0 + k] : 0.f;
+      hin[k] = 0.f;
+      dA[k] = 0.f;
+    }
+    for (int q = 0; q < w.seg; ++q) {  // state in front of the segment
+      const float sd = p.sdel[q * per + at0];
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        hin[k] = fmaf(decay(sd, A2[k]), hin[k], k < l.nleft ? p.hend[(q * per + at0) * p.in.N + l.n0 + k] : 0.f);
+    }
+    for (int q = p.nseg - 1; q > w.seg; --q) {  // gradient behind it
+      const float sd = p.sdel[q * per + at0];
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        gg[k] = fmaf(decay(sd, A2[k]), gg[k], k < l.nleft ? p.gsum[(q * per + at0) * p.in.N + l.n0 + k] : 0.f);
+    }
+    Pack<float, 4> qh{};
+    float qcd = 0.f;
+    auto fetch = [&](int tile) {
+      const int64_t at = int64_t(w.tbeg / TB + (tile > 0 ? tile : 0)) * w.blocks + w.unit;
+      qh = load_pack<float, 4>(p.ck + (at * kThreads + tid) * 4);
+      if (w.seg > 0) qcd = p.cd[at * CHB + l.chl];
+    };
+    if (tiles > 0) fetch(tiles - 1);
+    __syncthreads();
+    for (int i = 0; i < tiles; ++i) {
+      const int o = i & 1;
+      float h[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) h[k] = w.seg > 0 ? fmaf(decay(qcd, A2[k]), hin[k], qh.e[k]) : qh.e[k];
+      fetch(tiles - 2 - i);
+      const float* pd = &sh.dl[o][0][l.chl];
+      const float* pu = &sh.us[o][0][l.chl];
+      const float* po = &sh.ds[o][0][l.chl];
+      const float* pB = &sh.bc[o][0][0][l.n0];
+      const float* pC = &sh.bc[o][1][0][l.n0];
+      // ---- decays and states of the tile, forward
+      float a[TB][4], ah[TB][4];
+      Four<true, true> q[2];
+      q[0].template load<CHB, NP>(pd, pu, po, pB, pC);
+#pragma unroll
+      for (int tq = 0; tq < TB; tq += 4) {
+        const Four<true, true>& f = q[tq / 4 & 1];
+        if (tq + 4 < TB)
+          q[tq / 4 + 1 & 1].template load<CHB, NP>(pd + (tq + 4) * CHB, pu + (tq + 4) * CHB, po + (tq + 4) * CHB, pB + (tq + 4) * NP,
+                                                   pC + (tq + 4) * NP);
+        float y[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+#pragma unroll
+          for (int k = 0; k < 4; ++k) a[tq + j][k] = decay(f.delta[j], A2[k]);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          y[j] = 0.f;
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            ah[tq + j][k] = a[tq + j][k] * h[k];
+            h[k] = fmaf(f.u[j], f.B[j][k], ah[tq + j][k]);
+            y[j] = fmaf(f.C[j][k], h[k], y[j]);
+          }
+        }
+        sh.o[o][blk][tq + rv][l.chl] = rows_sum4(y);
+      }
+      // ---- gradients, backward; the last four tokens' values are at hand
+      float dAt[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int tq = TB - 4; tq >= 0; tq -= 4) {
+        const Four<true, true>& f = q[tq / 4 & 1];
+        if (tq > 0)
+          q[tq / 4 + 1 & 1].template load<CHB, NP>(pd + (tq - 4) * CHB, pu + (tq - 4) * CHB, po + (tq - 4) * CHB, pB + (tq - 4) * NP,
+                                                   pC + (tq - 4) * NP);
+        float sB[4], sA[4], rB[4], rC[4];
+#pragma unroll
+        for (int j = 3; j >= 0; --j) {
+          float gu[4], dh[4];
+          sB[j] = sA[j] = 0.f;
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const float gk = fmaf(f.C[j][k], f.go[j], gg[k]);
+            dh[k] = f.go[j] * fmaf(f.u[j], f.B[j][k], ah[tq + j][k]);
+            gu[k] = gk * f.u[j];
+            sB[j] = fmaf(gk, f.B[j][k], sB[j]);
+            const float m = gk * ah[tq + j][k];
+            sA[j] = fmaf(m, A2[k], sA[j]);
+            dAt[k] = fmaf(m, f.delta[j], dAt[k]);
+            gg[k] = gk * a[tq + j][k];
+          }
+          rB[j] = channels_sum(gu, odd, two);
+          rC[j] = channels_sum(dh, odd, two);
+        }
+        sh.gB[o][blk][tq + rv][l.chl] = rows_sum4(sB);
+        sh.gA[o][blk][tq + rv][l.chl] = rows_sum4(sA);
+        // lane c of a row writes token c / 4, state c % 4 of its group
+        float* wp = &sh.wp[o][wave / NB][tq + (tid >> 2 & 3)][0][l.n0 + (tid & 3)];
+        wp[0] = pick(eight, pick(four, rB[3], rB[2]), pick(four, rB[1], rB[0]));
+        wp[NP] = pick(eight, pick(four, rC[3], rC[2]), pick(four, rC[1], rC[0]));
+      }
+#pragma unroll
+      for (int k = 0; k < 4; ++k) dA[k] += dAt[k];
+      __syncthreads();
+    }
+    if (l.live) {
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        if (k < l.nleft) {
+          part[int64_t(l.d) * p.in.N + l.n0 + k] = dA[k];
+          if (w.seg == 0 && p.dh0 != nullptr) p.dh0[at0 * p.in.N + l.n0 + k] = gg[k];
+        }
+    }
+    __syncthreads();
+    return;
+  }
 
-  const int dl = cb * CH + chl;
-  const bool live = dl < p.Dg;
-  const int d = g * p.Dg + (live ? dl : 0);
-  const int64_t at0 = int64_t(b) * p.D + d;
-  float A2[K], gg[K], hin[K], dA[K];
-#pragma unroll
-  for (int k = 0; k < K; ++k) {
-    const int n = s * K + k;
-    const bool on = live && n < p.N;
-    A2[k] = on ? p.A[int64_t(d) * p.N + n] * kLog2e : 0.f;
-    gg[k] = on && p.dhf != nullptr ? p.dhf[at0 * p.N + n] : 0.f;
-    hin[k] = 0.f;
-    dA[k] = 0.f;
-  }
-  const int64_t per = int64_t(p.Bt) * p.D;
-  for (int q = 0; q < seg; ++q) {  // state in front of the segment
-    const float sd = p.sdel[q * per + at0];
-#pragma unroll
-    for (int k = 0; k < K; ++k)
-      hin[k] = fmaf(decay(sd, A2[k]), hin[k], s * K + k < p.N ? p.hend[(q * per + at0) * p.N + s * K + k] : 0.f);
-  }
-  for (int q = p.nseg - 1; q > seg; --q) {  // gradient behind it
-    const float sd = p.sdel[q * per + at0];
-#pragma unroll
-    for (int k = 0; k < K; ++k)
-      gg[k] = fmaf(decay(sd, A2[k]), gg[k], s * K + k < p.N ? p.gsum[(q * per + at0) * p.N + s * K + k] : 0.f);
-  }
-
-  const int r = tid / (CH / VE), c0 = (tid % (CH / VE)) * VE;
-  const int ncol = p.Dg - (cb * CH + c0) < VE ? p.Dg - (cb * CH + c0) : VE;
-  const int dc = g * p.Dg + cb * CH + c0;
-  const int64_t row0 = int64_t(b) * p.L;
-  const T* xp = static_cast<const T*>(p.x) + row0 * p.xld + dc;
-  const T* dtp = static_cast<const T*>(p.dt) + row0 * p.dtld + dc;
-  const T* zp = p.z == nullptr ? nullptr : static_cast<const T*>(p.z) + row0 * p.zld + dc;
-  const T* dyp = static_cast<const T*>(p.dy) + row0 * p.D + dc;
-  T* dxp = static_cast<T*>(p.dx) + row0 * p.D + dc;
-  T* ddtp = static_cast<T*>(p.ddt) + row0 * p.D + dc;
-  T* dzp = p.dz == nullptr ? nullptr : static_cast<T*>(p.dz) + row0 * p.D + dc;
+  Stager<T, TB, CHB, NP, VEC, true, true, true> st;
+  st.init(p.in, w.b, w.g, w.cb, tid, w.tend);
+  const int r = st.r, c0 = st.c0;
+  const int64_t out0 = int64_t(w.b) * p.in.L * p.in.D + w.g * p.in.Dg;
+  const uint32_t oo = uint32_t(r) * uint32_t(p.in.D) + st.cin;
+  T* dxp = static_cast<T*>(p.dx) + out0;
+  T* ddtp = static_cast<T*>(p.ddt) + out0;
+  T* dzp = p.dz == nullptr ? nullptr : static_cast<T*>(p.dz) + out0;
   float bias[VE], dsk[VE], dD[VE], dbias[VE];
 #pragma unroll
   for (int v = 0; v < VE; ++v) {
-    bias[v] = p.dtb != nullptr && v < ncol ? p.dtb[dc + v] : 0.f;
-    dsk[v] = p.Dsk != nullptr && v < ncol ? p.Dsk[dc + v] : 0.f;
+    const int dc = w.g * p.in.Dg + st.cin + v;
+    bias[v] = p.in.dtb != nullptr && v < st.ncol ? p.in.dtb[dc] : 0.f;
+    dsk[v] = p.in.Dsk != nullptr && v < st.ncol ? p.in.Dsk[dc] : 0.f;
     dD[v] = dbias[v] = 0.f;
   }
-  const bool bcvec = VEC && p.N % 4 == 0;
   // rows behind the item's length: zero gradients
-  for (int t = (tend > tbeg ? tend : tbeg) + r; t < tlim; t += TB) {
+  for (int t = (w.tend > w.tbeg ? w.tend : w.tbeg) + r; t < w.tlim; t += TB) {
     float zero[VE];
 #pragma unroll
     for (int v = 0; v < VE; ++v) zero[v] = 0.f;
-    store_cols<T, VE, VEC>(dxp + int64_t(t) * p.D, zero, true, ncol);
-    store_cols<T, VE, VEC>(ddtp + int64_t(t) * p.D, zero, true, ncol);
-    if (dzp != nullptr) store_cols<T, VE, VEC>(dzp + int64_t(t) * p.D, zero, true, ncol);
+    const int64_t at = int64_t(t) * p.in.D + st.cin;
+    store_cols<T, VE, VEC>(dxp + at, zero, true, st.ncol);
+    store_cols<T, VE, VEC>(ddtp + at, zero, true, st.ncol);
+    if (dzp != nullptr) store_cols<T, VE, VEC>(dzp + at, zero, true, st.ncol);
   }
-
-  Pack<T, VE> qx{}, qd{}, qz{}, qy{};
-  Pack<T, 4> qb[NQ];
-  Pack<float, 4> qh{};
-  float qcd = 0.f;
-  auto fetch = [&](int t0) {
-    const int t = t0 + r;
-    const bool row = t < tend;
-    qx = load_cols<T, VE, VEC>(xp + int64_t(t) * p.xld, row, ncol);
-    qd = load_cols<T, VE, VEC>(dtp + int64_t(t) * p.dtld, row, ncol);
-    qy = load_cols<T, VE, VEC>(dyp + int64_t(t) * p.D, row, ncol);
-    if (zp != nullptr) qz = load_cols<T, VE, VEC>(zp + int64_t(t) * p.zld, row, ncol);
+  // of the tile in each half: x, delta, sigmoid(dt), do, dy silu'(z)
+  float kx[2][VE], kd[2][VE], ks[2][VE], kg[2][VE], kz[2][VE];
+  auto stage = [&](int t0, auto half) {
+    constexpr int o = decltype(half)::value;
+    float u[VE], zv[VE];
+    unpack<T, VE>(st.qx, kx[o]);
+    unpack<T, VE>(st.qd, kd[o]);
+    unpack<T, VE>(st.qy, kg[o]);
+    unpack<T, VE>(st.qz, zv);
+    if (p.softplus) {
 #pragma unroll
-    for (int i = 0; i < NQ; ++i) {
-      const int e = tid + i * kThreads, q = e % (NP / 4), tt = (e / (NP / 4)) % TB, which = e / (NP / 4 * TB);
-      qb[i] = Pack<T, 4>{};
-      if (which < 2 && t0 + tt < tend && 4 * q < p.N) {
-        const int64_t ld = which ? p.Cld : p.Bld;
-        const T* src = static_cast<const T*>(which ? p.C : p.B) + (row0 + t0 + tt) * ld + int64_t(g) * p.N + 4 * q;
-        qb[i] = bcvec ? load_pack<T, 4>(src) : load_some<T, 4>(src, p.N - 4 * q);
+      for (int v = 0; v < VE; ++v) kd[o][v] = softplus_sigmoid(kd[o][v] + bias[v], ks[o][v]);
+    } else {
+#pragma unroll
+      for (int v = 0; v < VE; ++v) ks[o][v] = 1.f;
+    }
+    if (st.gated) {
+#pragma unroll
+      for (int v = 0; v < VE; ++v) {
+        const float sg = sigmoid_f(zv[v]);
+        kz[o][v] = kg[o][v] * dsilu_f(zv[v], sg);
+        kg[o][v] *= zv[v] * sg;
+      }
+    } else {
+#pragma unroll
+      for (int v = 0; v < VE; ++v) kz[o][v] = 0.f;
+    }
+#pragma unroll
+    for (int v = 0; v < VE; ++v) u[v] = kd[o][v] * kx[o][v];
+    if (st.edge(t0)) {
+#pragma unroll
+      for (int v = 0; v < VE; ++v) {
+        const bool on = st.inside(t0, v);
+        kx[o][v] = on ? kx[o][v] : 0.f;
+        kd[o][v] = on ? kd[o][v] : 0.f;
+        ks[o][v] = on ? ks[o][v] : 0.f;
+        kg[o][v] = on ? kg[o][v] : 0.f;
+        u[v] = on ? u[v] : 0.f;
       }
     }
-    const int64_t at = int64_t(t0 / TB) * blocks + unit;
-    qh = load_pack<float, 4>(p.ck + (at * kThreads + tid) * 4);
-    if (seg > 0) qcd = p.cd[at * CH + chl];
+    store_pack<float, VE>(&sh.dl[o][r][c0], kd[o]);
+    store_pack<float, VE>(&sh.us[o][r][c0], u);
+    store_pack<float, VE>(&sh.ds[o][r][c0], kg[o]);
+    st.put_bc(t0, &sh.bc[o][0][0][0]);
   };
-  const int tlast = tend > tbeg ? tbeg + (tend - tbeg - 1) / TB * TB : tbeg - TB;
-  if (tlast >= tbeg) fetch(tlast);
-  for (int t0 = tlast; t0 >= tbeg; t0 -= TB) {
-    // ---- stage the tile
-    const bool row = t0 + r < tend;
-    float xv[VE], raw[VE], dov[VE], yv[VE], zv[VE];
-    unpack<T, VE>(qx, xv);
-    unpack<T, VE>(qd, raw);
-    unpack<T, VE>(qy, yv);
-    unpack<T, VE>(qz, zv);
+  float ox[VE], od[VE], oz[VE];
+  auto finish = [&](auto half) {
+    constexpr int o = decltype(half)::value;
+    float y[VE], gB[VE], gA[VE];
+#pragma unroll
+    for (int v = 0; v < VE; ++v) y[v] = gB[v] = gA[v] = 0.f;
+#pragma unroll
+    for (int i = 0; i < NB; ++i) {
+      const Pack<float, VE> q0 = load_pack<float, VE>(&sh.o[o][i][r][c0]), q1 = load_pack<float, VE>(&sh.gB[o][i][r][c0]),
+                            q2 = load_pack<float, VE>(&sh.gA[o][i][r][c0]);
+#pragma unroll
+      for (int v = 0; v < VE; ++v) {
+        y[v] += q0.e[v];
+        gB[v] += q1.e[v];
+        gA[v] += q2.e[v];
+      }
+    }
 #pragma unroll
     for (int v = 0; v < VE; ++v) {
-      const float dl_ = step_of(raw[v], p.softplus != 0, bias[v], row);
-      du[r][c0 + v] = float2{dl_, dl_ * xv[v]};
-      dov[v] = yv[v] * (zp != nullptr ? silu_f(zv[v]) : 1.f);
-      dos[r][c0 + v] = dov[v];
+      ox[v] = fmaf(dsk[v], kg[o][v], kd[o][v] * gB[v]);
+      od[v] = fmaf(kx[o][v], gB[v], gA[v] * kLn2) * ks[o][v];
+      oz[v] = kz[o][v] * fmaf(dsk[v], kx[o][v], y[v]);
+      dD[v] = fmaf(kg[o][v], kx[o][v], dD[v]);
+      dbias[v] += od[v];
     }
+  };
+  auto store = [&](int t0, int o) {
+    const bool row = t0 + r < w.tend;
+    const int64_t at = int64_t(t0) * p.in.D;
+    store_cols<T, VE, VEC>(dxp + at + oo, ox, row, st.ncol);
+    store_cols<T, VE, VEC>(ddtp + at + oo, od, row, st.ncol);
+    if (dzp != nullptr) store_cols<T, VE, VEC>(dzp + at + oo, oz, row, st.ncol);
 #pragma unroll
-    for (int i = 0; i < NQ; ++i) {
-      const int e = tid + i * kThreads, q = e % (NP / 4), tt = (e / (NP / 4)) % TB, which = e / (NP / 4 * TB);
-      if (which < 2) {
-        float f[4];
-        unpack<T, 4>(qb[i], f);
-        *reinterpret_cast<f32x4*>(&bc[which][tt][4 * q]) = f32x4{f[0], f[1], f[2], f[3]};
-      }
+    for (int e = 4 * tid; e < TB * 2 * NP; e += 4 * kThreads) {
+      const int t = e / (2 * NP), c = e % (2 * NP);
+      f32x4 v = *reinterpret_cast<const f32x4*>(&sh.wp[o][0][0][0][0] + e);
+#pragma unroll
+      for (int i = 1; i < 4 / NB; ++i) v += *reinterpret_cast<const f32x4*>(&sh.wp[o][i][0][0][0] + e);
+      if (t0 + t < w.tend)
+        *reinterpret_cast<f32x4*>(p.bc + (((int64_t(w.cb) * p.Bt + w.b) * p.in.L + t0 + t) * p.in.G + w.g) * (2 * NP) + c) = v;
     }
-    float h[K];
-#pragma unroll
-    for (int k = 0; k < K; ++k) h[k] = seg > 0 ? fmaf(decay(qcd, A2[k]), hin[k], qh.e[k]) : qh.e[k];
+  };
+  const std::integral_constant<int, 0> even;
+  const std::integral_constant<int, 1> odd;
+  auto start = [&](int i) { return w.tbeg + (tiles - 1 - i) * TB; };  // first token of the tile of step i
+  auto step = [&](int i, auto half, auto other) {
+    if (i > 0) finish(other);
+    if (i + 1 < tiles) {
+      stage(start(i + 1), other);
+      st.fetch(start(i + 2));
+    }
+    if (i > 0) store(start(i - 1), decltype(other)::value);
     __syncthreads();
-    if (t0 - TB >= tbeg) fetch(t0 - TB);
-    // ---- decays and states of the tile, forward
-    float a[TB][K], ah[TB][K];
-    float keep = 0.f;
-#pragma unroll
-    for (int t = 0; t < TB; ++t) {
-      const float2 q = du[t][chl];
-      float o = 0.f;
-#pragma unroll
-      for (int k = 0; k < K; ++k) {
-        a[t][k] = decay(q.x, A2[k]);
-        ah[t][k] = a[t][k] * h[k];
-        h[k] = fmaf(q.y, bc[0][t][s * K + k], ah[t][k]);
-        o = fmaf(bc[1][t][s * K + k], h[k], o);
-      }
-      o = lanes_sum<S>(o);
-      if (s == (S >= 4 ? t & 3 : t & 1)) keep = o;
-      if (S >= 4 ? (t & 3) == 3 : (t & 1)) {
-        if (s < 4) os[S >= 4 ? t - 3 + s : t - 1 + s][chl] = keep;
-      }
-    }
-    // ---- gradients, backward
-    float dAt[K] = {0.f, 0.f, 0.f, 0.f};
-    float keepB = 0.f, keepA = 0.f;
-#pragma unroll
-    for (int t = TB - 1; t >= 0; --t) {
-      const float2 q = du[t][chl];
-      const float dot = dos[t][chl];
-      float gu[K], dh[K], sB = 0.f, sA = 0.f;
-#pragma unroll
-      for (int k = 0; k < K; ++k) {
-        const float Bv = bc[0][t][s * K + k], Cv = bc[1][t][s * K + k];
-        const float gk = fmaf(Cv, dot, gg[k]);
-        const float hk = fmaf(q.y, Bv, ah[t][k]);
-        dh[k] = dot * hk;
-        gu[k] = gk * q.y;
-        sB = fmaf(gk, Bv, sB);
-        const float w = gk * ah[t][k];
-        sA = fmaf(w, A2[k], sA);
-        dAt[k] = fmaf(w, q.x, dAt[k]);
-        gg[k] = gk * a[t][k];
-      }
-      sB = lanes_sum<S>(sB);
-      sA = lanes_sum<S>(sA);
-      if (s == (S >= 4 ? t & 3 : t & 1)) {
-        keepB = sB;
-        keepA = sA;
-      }
-      if (S >= 4 ? (t & 3) == 0 : (t & 1) == 0) {
-        if (s < 4) {
-          gb[0][t + s][chl] = keepB;
-          gb[1][t + s][chl] = keepA;
-        }
-      }
-      const float rB = channels_sum<S>(gu), rC = channels_sum<S>(dh);
-      const int rowq = lane >> 4, n = s * 4 + ((rowq & 1) << 1 | rowq >> 1);
-      if constexpr (S <= 8) {
-        const int which = (lane & 15) / S;
-        if (which < 2) wp[wv][t][which][n] = which ? rC : rB;
-      } else {
-        wp[wv][t][0][n] = rB;
-        wp[wv][t][1][n] = rC;
-      }
-    }
-#pragma unroll
-    for (int k = 0; k < K; ++k) dA[k] += dAt[k];
-    __syncthreads();
-    // ---- outputs of the tile
-    float ox[VE], od[VE], oz[VE];
-#pragma unroll
-    for (int v = 0; v < VE; ++v) {
-      const float gB = gb[0][r][c0 + v], gA = gb[1][r][c0 + v];
-      const float dl_ = du[r][c0 + v].x;
-      ox[v] = fmaf(dsk[v], dov[v], dl_ * gB);
-      od[v] = fmaf(xv[v], gB, gA * kLn2);
-      if (p.softplus) od[v] *= sigmoid_f(raw[v] + bias[v]);
-      if (row) {
-        dD[v] = fmaf(dov[v], xv[v], dD[v]);
-        dbias[v] += od[v];
-      }
-      oz[v] = zp != nullptr ? yv[v] * fmaf(dsk[v], xv[v], os[r][c0 + v]) * dsilu_f(zv[v], sigmoid_f(zv[v])) : 0.f;
-    }
-    store_cols<T, VE, VEC>(dxp + int64_t(t0 + r) * p.D, ox, row, ncol);
-    store_cols<T, VE, VEC>(ddtp + int64_t(t0 + r) * p.D, od, row, ncol);
-    if (dzp != nullptr) store_cols<T, VE, VEC>(dzp + int64_t(t0 + r) * p.D, oz, row, ncol);
-    for (int i = tid; i < TB * 2 * NP; i += kThreads) {
-      const int t = i / (2 * NP), e = i % (2 * NP);
-      const float* w0 = &wp[0][t][0][0] + e;
-      const float v = (w0[0] + w0[TB * 2 * NP]) + (w0[2 * TB * 2 * NP] + w0[3 * TB * 2 * NP]);
-      if (t0 + t < tend)
-        p.bc[((int64_t(cb) * p.Bt * p.L + row0 + t0 + t) * p.G + g) * (2 * NP) + e] = v;
-    }
-    __syncthreads();  // du is read above and written by the next tile
-  }
-  // ---- sums over the tokens
-  const int64_t ncols = int64_t(p.D) * (p.N + 2);
-  float* part = p.part + (int64_t(seg) * p.Bt + b) * ncols;
-  if (live) {
-#pragma unroll
-    for (int k = 0; k < K; ++k) {
-      const int n = s * K + k;
-      if (n < p.N) {
-        part[int64_t(d) * p.N + n] = dA[k];
-        if (seg == 0 && p.dh0 != nullptr) p.dh0[at0 * p.N + n] = gg[k];
-      }
-    }
+  };
+  if (tiles > 0) {
+    st.fetch(start(0));
+    stage(start(0), even);
+    st.fetch(start(1));
   }
   __syncthreads();
+  for (int i = 0; i < tiles; i += 2) {
+    step(i, even, odd);
+    if (i + 1 < tiles) step(i + 1, odd, even);
+  }
+  if (tiles > 0) {
+    if (tiles % 2) finish(even);
+    else finish(odd);
+    store(start(tiles - 1), (tiles - 1) & 1);
+  }
+  // ---- sums over the tokens: this thread's rows, then the 16 of each column
 #pragma unroll
   for (int v = 0; v < VE; ++v) {
-    os[r][c0 + v] = dD[v];
-    gb[0][r][c0 + v] = dbias[v];
+    sh.dl[0][r][c0 + v] = dD[v];
+    sh.us[0][r][c0 + v] = dbias[v];
   }
   __syncthreads();
-  if (tid < CH && cb * CH + tid < p.Dg) {
+  if (tid < CHB && w.cb * CHB + tid < p.in.Dg) {
     float sd = 0.f, sb = 0.f;
 #pragma unroll
     for (int q = 0; q < TB; ++q) {
-      sd += os[q][tid];
-      sb += gb[0][q][tid];
+      sd += sh.dl[0][q][tid];
+      sb += sh.us[0][q][tid];
     }
-    const int dd = g * p.Dg + cb * CH + tid;
-    part[int64_t(p.D) * p.N + dd] = sd;
-    part[int64_t(p.D) * (p.N + 1) + dd] = sb;
+    const int dd = w.g * p.in.Dg + w.cb * CHB + tid;
+    part[int64_t(p.in.D) * p.in.N + dd] = sd;
+    part[int64_t(p.in.D) * (p.in.N + 1) + dd] = sb;
   }
 }
 
@@ -498,19 +591,20 @@ __global__ __launch_bounds__(256) void join_bc_kernel(const float* bc, T* dB, T*
 }
 
 struct Plan {
-  int S, nblk, nseg, seglen;
+  int NB, nblk, nseg, seglen;
   int64_t tiles, blocks;
   size_t oCk, oCd, oHe, oGs, oSd, oBc, oPart, bytes;
 };
 // Segments as in the forward, at least 128 tokens each, multiples of the tiles.
 Plan plan_of(const m3_scan_args& f) {
   Plan p;
-  p.S = lanes_for(f.N);
-  p.nblk = blocks_per_group(f.D / f.G, p.S);
+  p.NB = state_blocks(f.N);
+  const int CHB = CH / p.NB, NP = 16 * p.NB;
+  p.nblk = (f.D / f.G + CHB - 1) / CHB;
   p.blocks = int64_t(f.Bt) * f.G * p.nblk;
   p.nseg = 1;
   p.seglen = (f.L + 31) / 32 * 32;
-  if (p.blocks < 512) {
+  if (p.blocks < 256) {
     int64_t n = (512 + p.blocks - 1) / p.blocks;
     if (n > f.L / 128) n = f.L / 128;
     if (n > 1) {
@@ -519,11 +613,10 @@ Plan plan_of(const m3_scan_args& f) {
     }
   }
   p.tiles = (f.L + TB - 1) / TB;
-  const int CH = kThreads / p.S, NP = 4 * p.S;
   const size_t seg = p.nseg > 1 ? size_t(p.nseg) * f.Bt * f.D : 0;
   p.oCk = 0;
   p.oCd = round256(p.oCk + size_t(p.tiles) * p.blocks * kThreads * 16);
-  p.oHe = round256(p.oCd + (p.nseg > 1 ? size_t(p.tiles) * p.blocks * CH * 4 : 0));
+  p.oHe = round256(p.oCd + (p.nseg > 1 ? size_t(p.tiles) * p.blocks * CHB * 4 : 0));
   p.oGs = round256(p.oHe + seg * f.N * 4);
   p.oSd = round256(p.oGs + seg * f.N * 4);
   p.oBc = round256(p.oSd + seg * 4);
@@ -532,26 +625,29 @@ Plan plan_of(const m3_scan_args& f) {
   return p;
 }
 
-template <typename T, int S, bool VEC>
-hipError_t run(const m3_scan_backward_args& a, hipStream_t st) {
+template <typename T, int NB, bool VEC>
+hipError_t run(const m3_scan_backward_args& a, const Plan& pl, hipStream_t st) {
+  static std::atomic<uint64_t> cleared{0};
   const m3_scan_args& f = a.fwd;
-  const Plan pl = plan_of(f);
   unsigned char* ws = static_cast<unsigned char*>(a.workspace);
   auto at = [&](size_t o) { return reinterpret_cast<float*>(ws + o); };
-  const BwP p{f.x, f.dt, f.z, f.B, f.C, a.dy, f.x_ld, f.dt_ld, f.z_ld, f.B_ld, f.C_ld, f.A, f.D_skip, f.dt_bias, f.h0,
-              a.dh_final, f.lengths, a.dx, a.ddt, a.dz, a.dh0, at(pl.oCk), at(pl.oCd), at(pl.oHe), at(pl.oGs), at(pl.oSd),
-              at(pl.oBc), at(pl.oPart), f.Bt, f.L, f.D, f.N, f.G, f.D / f.G, pl.nblk, pl.nseg, pl.seglen, f.dt_softplus};
+  const Inputs in{f.x, f.dt, f.z, f.B, f.C, a.dy, f.x_ld, f.dt_ld, f.z_ld, f.B_ld, f.C_ld, f.D_skip, f.dt_bias, f.L, f.D, f.N, f.G,
+                  f.D / f.G};
+  const BwP p{in, f.A, f.h0, a.dh_final, f.lengths, a.dx, a.ddt, a.dz, a.dh0, at(pl.oCk), at(pl.oCd), at(pl.oHe), at(pl.oGs),
+              at(pl.oSd), at(pl.oBc), at(pl.oPart), f.Bt, pl.nblk, pl.nseg, pl.seglen, f.dt_softplus};
   const uint32_t grid = uint32_t(pl.blocks * pl.nseg);
-  if (pl.nseg > 1) states_kernel<T, S, VEC, true><<<grid, kThreads, 0, st>>>(p);
-  else states_kernel<T, S, VEC, false><<<grid, kThreads, 0, st>>>(p);
+  if (pl.nseg > 1) states_kernel<T, NB, VEC, true><<<grid, 2 * kThreads, 0, st>>>(p);
+  else states_kernel<T, NB, VEC, false><<<grid, 2 * kThreads, 0, st>>>(p);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  reverse_kernel<T, S, VEC><<<grid, kThreads, 0, st>>>(p);
+  e = allow_lds(reinterpret_cast<const void*>(&reverse_kernel<T, NB, VEC>), sizeof(Shared<NB>), cleared);
+  if (e != hipSuccess) return e;
+  reverse_kernel<T, NB, VEC><<<grid, 2 * kThreads, sizeof(Shared<NB>), st>>>(p);
   e = hipGetLastError();
   if (e != hipSuccess) return e;
-  const int64_t rows = int64_t(f.Bt) * f.L, items = rows * f.G * 2 * 4 * S;
-  join_bc_kernel<T, 4 * S><<<uint32_t((items + 255) / 256), 256, 0, st>>>(p.bc, static_cast<T*>(a.dB), static_cast<T*>(a.dC),
-                                                                        f.lengths, rows, f.L, f.G, f.N, pl.nblk);
+  const int64_t rows = int64_t(f.Bt) * f.L, items = rows * f.G * 2 * 16 * NB;
+  join_bc_kernel<T, 16 * NB><<<uint32_t((items + 255) / 256), 256, 0, st>>>(p.bc, static_cast<T*>(a.dB), static_cast<T*>(a.dC),
+                                                                          f.lengths, rows, f.L, f.G, f.N, pl.nblk);
   e = hipGetLastError();
   if (e != hipSuccess) return e;
   ColSum c{};
@@ -568,13 +664,9 @@ hipError_t run(const m3_scan_backward_args& a, hipStream_t st) {
 }
 
 template <typename T, bool VEC>
-hipError_t by_lanes(const m3_scan_backward_args& a, hipStream_t st) {
-  switch (lanes_for(a.fwd.N)) {
-    case 2: return run<T, 2, VEC>(a, st);
-    case 4: return run<T, 4, VEC>(a, st);
-    case 8: return run<T, 8, VEC>(a, st);
-    default: return run<T, 16, VEC>(a, st);
-  }
+hipError_t by_states(const m3_scan_backward_args& a, const Plan& p, hipStream_t st) {
+  if (p.NB == 1) return run<T, 1, VEC>(a, p, st);
+  return p.NB == 2 ? run<T, 2, VEC>(a, p, st) : run<T, 4, VEC>(a, p, st);
 }
 
 }  // namespace
@@ -585,15 +677,16 @@ hipError_t launch_scan_backward(const m3_scan_backward_args& a, hipStream_t s) {
   const m3_scan_args& f = a.fwd;
   const bool bf = f.in_dtype == M3_BF16;
   const size_t e = bf ? 2 : 4;
+  const scan::Plan p = scan::plan_of(f);
   // the first walk's staging threads take the wider words
-  const int S = scan::lanes_for(f.N), ve = (S >= 4 ? 32 : 16) / S;
+  const int ve = 8 / p.NB;
   const size_t word = e * ve < 16 ? e * ve : 16;
   const bool vec = (f.D / f.G) % ve == 0 && rows_aligned(f.x, f.x_ld, e, word) && rows_aligned(f.dt, f.dt_ld, e, word) &&
                    rows_aligned(f.z, f.z_ld, e, word) && rows_aligned(a.dy, f.D, e, word) && rows_aligned(a.dx, f.D, e, word) &&
-                   rows_aligned(a.ddt, f.D, e, word) && rows_aligned(a.dz, f.D, e, word) &&
-                   (f.N % 4 != 0 || (rows_aligned(f.B, f.B_ld, e, 4 * e) && rows_aligned(f.C, f.C_ld, e, 4 * e)));
-  if (bf) return vec ? scan::by_lanes<bf16_t, true>(a, s) : scan::by_lanes<bf16_t, false>(a, s);
-  return vec ? scan::by_lanes<float, true>(a, s) : scan::by_lanes<float, false>(a, s);
+                   rows_aligned(a.ddt, f.D, e, word) && rows_aligned(a.dz, f.D, e, word) && f.N % 4 == 0 &&
+                   rows_aligned(f.B, f.B_ld, e, 4 * e) && rows_aligned(f.C, f.C_ld, e, 4 * e);
+  if (bf) return vec ? scan::by_states<bf16_t, true>(a, p, s) : scan::by_states<bf16_t, false>(a, p, s);
+  return vec ? scan::by_states<float, true>(a, p, s) : scan::by_states<float, false>(a, p, s);
 }
 
 }  // namespace m3

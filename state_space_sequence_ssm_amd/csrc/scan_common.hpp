@@ -17,6 +17,7 @@
 // saved a ninth of the vector instructions and made the scan a quarter slower.)
 #pragma once
 #include "layer_internal.hpp"
+#include "m3ssm_internal.hpp"
 
 namespace m3 {
 namespace scan {
@@ -36,6 +37,14 @@ __device__ __forceinline__ float decay(float delta, float a2) { return __builtin
 __device__ __forceinline__ float softplus_fast(float v) {
   const float u = __builtin_amdgcn_exp2f(-fabsf(v) * kLog2e);
   const float w = 1.f + u;
+  return fmaxf(v, 0.f) + fmaf(__builtin_amdgcn_logf(w), kLn2, u - (w - 1.f));
+}
+// The same, and sigmoid(v) = d softplus / dv from the same exponential.
+__device__ __forceinline__ float softplus_sigmoid(float v, float& sg) {
+  const float u = __builtin_amdgcn_exp2f(-fabsf(v) * kLog2e);
+  const float w = 1.f + u;
+  const float r = __builtin_amdgcn_rcpf(w);
+  sg = v >= 0.f ? r : u * r;
   return fmaxf(v, 0.f) + fmaf(__builtin_amdgcn_logf(w), kLn2, u - (w - 1.f));
 }
 // delta of one token: 0 behind the end.
@@ -60,26 +69,15 @@ __device__ __forceinline__ float rows_sum4(const float* v) {
   const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(lo), __float_as_uint(hi), false, false);
   return __uint_as_float(r[0]) + __uint_as_float(r[1]);
 }
-// One tile's share of a row-major [token][channel] tensor: this thread's VE
-// neighbouring channels of one token.  The loads have no branch around them (a
+// VE neighbouring values.  The loads of a tile have no branch around them (a
 // branch makes the compiler wait for the values at its end): rows and columns
-// past the edge are read from the nearest ones inside and dropped by the user.
+// past the edge are read from the nearest ones inside and dropped later.
 template <typename T, int VE, bool VEC>
 __device__ __forceinline__ Pack<T, VE> fetch_cols(const T* p, int ncol) {
   if constexpr (VEC) return load_pack<T, VE>(p);
   Pack<T, VE> q;
 #pragma unroll
   for (int v = 0; v < VE; ++v) q.e[v] = p[v < ncol ? v : ncol - 1];
-  return q;
-}
-template <typename T, int VE, bool VEC>
-__device__ __forceinline__ Pack<T, VE> load_cols(const T* p, bool row, int ncol) {
-  Pack<T, VE> q{};
-  if constexpr (VEC) {
-    if (row && ncol > 0) q = load_pack<T, VE>(p);
-  } else {
-    if (row) q = load_some<T, VE>(p, ncol);
-  }
   return q;
 }
 template <typename T, int VE, bool VEC>
@@ -90,6 +88,116 @@ __device__ __forceinline__ void store_cols(T* p, const float* v, bool row, int n
     if (row) store_some<T, VE>(p, v, ncol);
   }
 }
+
+// The tensors of a call as the kernels take them.
+struct Inputs {
+  const void* x;
+  const void* dt;
+  const void* z;
+  const void* B;
+  const void* C;
+  const void* dy;
+  int64_t xld, dtld, zld, Bld, Cld;
+  const float* Dsk;
+  const float* dtb;
+  int L, D, N, G, Dg;
+};
+
+// A staging thread's part of the tiles of one item and one block of CHB channels:
+// VE neighbouring channels of token r of each tensor, and quads of B (and C).
+// fetch() starts the loads of a tile into registers; the values are used a tile
+// later.  Z, DY, CC: whether z, dy and C are wanted.
+template <typename T, int TT, int CHB, int NP, bool VEC, bool Z, bool DY, bool CC>
+struct Stager {
+  static constexpr int VE = TT * CHB / kThreads;
+  static constexpr int kQuads = (CC ? 2 : 1) * TT * NP / 4, NQ = (kQuads + kThreads - 1) / kThreads;
+  const T *x, *dt, *z, *dy, *B, *C;
+  int64_t xld, dtld, zld, dyld, Bld, Cld;
+  int r, c0, ncol, nin, cin, tend, N;
+  int qt[NQ], qn[NQ];
+  bool qc[NQ], gated;
+  uint32_t ox, odt, oz, ody, oq[NQ];
+  Pack<T, VE> qx, qd, qz, qy;
+  Pack<T, 4> qb[NQ];
+
+  __device__ __forceinline__ void init(const Inputs& p, int b, int g, int cb, int tid, int end) {
+    r = tid / (CHB / VE);
+    c0 = (tid % (CHB / VE)) * VE;
+    const int left = p.Dg - (cb * CHB + c0);
+    ncol = left < VE ? left : VE;  // to be stored: none past the group
+    cin = ncol > 0 ? cb * CHB + c0 : 0;
+    nin = ncol > 0 ? ncol : 1;  // to be read
+    tend = end;
+    N = p.N;
+    gated = p.z != nullptr;
+    xld = p.xld;
+    dtld = p.dtld;
+    zld = gated ? p.zld : p.xld;
+    dyld = p.D;
+    Bld = p.Bld;
+    Cld = p.Cld;
+    const int64_t row0 = int64_t(b) * p.L;
+    x = static_cast<const T*>(p.x) + row0 * xld + g * p.Dg;
+    dt = static_cast<const T*>(p.dt) + row0 * dtld + g * p.Dg;
+    z = gated ? static_cast<const T*>(p.z) + row0 * zld + g * p.Dg : x;
+    dy = DY ? static_cast<const T*>(p.dy) + row0 * dyld + g * p.Dg : x;
+    B = static_cast<const T*>(p.B) + row0 * Bld + int64_t(g) * p.N;
+    C = static_cast<const T*>(p.C) + row0 * Cld + int64_t(g) * p.N;
+#pragma unroll
+    for (int i = 0; i < NQ; ++i) {
+      const int e = (tid + i * kThreads) % kQuads;
+      qt[i] = (e / (NP / 4)) % TT;
+      qn[i] = e % (NP / 4) * 4;
+      qc[i] = e / (NP / 4 * TT) == 1;
+    }
+    place(TT - 1, ox, odt, oz, ody, oq);
+    qx = qd = qz = qy = Pack<T, VE>{};
+  }
+  // this thread's offsets in a tile whose last row is `last`
+  __device__ __forceinline__ void place(int last, uint32_t& px, uint32_t& pdt, uint32_t& pz, uint32_t& pdy, uint32_t (&pq)[NQ]) const {
+    const uint32_t rr = r < last ? r : last;
+    px = rr * uint32_t(xld) + cin;
+    pdt = rr * uint32_t(dtld) + cin;
+    pz = rr * uint32_t(zld) + cin;
+    pdy = rr * uint32_t(dyld) + cin;
+#pragma unroll
+    for (int i = 0; i < NQ; ++i)
+      pq[i] = uint32_t(qt[i] < last ? qt[i] : last) * uint32_t(qc[i] ? Cld : Bld) + (qn[i] < N ? qn[i] : 0);
+  }
+  // tend > 0; a tile past the end reads its last row
+  __device__ __forceinline__ void fetch(int t0) {
+    const int64_t tb = t0 < 0 ? 0 : t0 < tend ? t0 : tend - 1;
+    uint32_t px = ox, pdt = odt, pz = oz, pdy = ody, pq[NQ];
+#pragma unroll
+    for (int i = 0; i < NQ; ++i) pq[i] = oq[i];
+    if (tend - 1 - tb < TT - 1) place(int(tend - 1 - tb), px, pdt, pz, pdy, pq);
+    qx = fetch_cols<T, VE, VEC>(x + tb * xld + px, nin);
+    qd = fetch_cols<T, VE, VEC>(dt + tb * dtld + pdt, nin);
+    if constexpr (Z) qz = fetch_cols<T, VE, VEC>(z + tb * zld + pz, nin);
+    if constexpr (DY) qy = fetch_cols<T, VE, VEC>(dy + tb * dyld + pdy, nin);
+#pragma unroll
+    for (int i = 0; i < NQ; ++i) {
+      const int n = N - qn[i] < 1 ? 1 : N - qn[i];
+      qb[i] = fetch_cols<T, 4, VEC>((qc[i] ? C + tb * Cld : B + tb * Bld) + pq[i], n);
+    }
+  }
+  // B and C of the fetched tile to LDS [2][TT][NP]; zeros past the end and past N
+  __device__ __forceinline__ void put_bc(int t0, float* bc) const {
+#pragma unroll
+    for (int i = 0; i < NQ; ++i) {
+      float f[4];
+      unpack<T, 4>(qb[i], f);
+      if (t0 + TT > tend || N < NP) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) f[k] = qn[i] + k < N && t0 + qt[i] < tend ? f[k] : 0.f;
+      }
+      store_pack<float, 4>(bc + ((qc[i] ? TT : 0) + qt[i]) * NP + qn[i], f);
+    }
+  }
+  // whether value v of the fetched tile lies inside
+  __device__ __forceinline__ bool edge(int t0) const { return t0 + TT > tend || ncol < VE; }
+  __device__ __forceinline__ bool inside(int t0, int v) const { return t0 + r < tend && v < ncol; }
+};
 
 // Blocks of channels never straddle two groups.
 constexpr int CH = 64;  // channels of a block: 16 for each of its four scanning waves
