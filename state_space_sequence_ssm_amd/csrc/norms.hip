@@ -12,6 +12,13 @@ namespace {
 // words of V elements.  BLK = 0: teams of 2^lgteam <= 64 lanes inside waves,
 // 256-thread blocks; BLK > 0: one block of BLK lanes per unit.  NV = 0: any
 // width, columns walked in a loop and read twice.
+//
+// A team keeps its group and walks rows `walkers` apart: gains, and in the
+// backward the sums of their gradients, stay in registers, and the next row is
+// on its way while one is computed.  In all but the last turn every team has a
+// row, so loads and stores have no branch around them (a branch would make each
+// wait for a load wait for the stores as well).  Lanes past the width repeat the
+// team's first word and leave the sums alone.
 struct Geom {
   bool vec;
   int nv, blk, lgteam;
@@ -21,8 +28,12 @@ struct Geom {
 template <int BLK>
 __device__ __forceinline__ float team_sum(float v, int lgteam, float* red) {
   if constexpr (BLK == 0) {
-    if (lgteam == 6) return wave_sum(v);
-    for (int m = 1; m < (1 << lgteam); m <<= 1) v += __shfl_xor(v, m);
+    if (lgteam >= 1) v += dpp<0xB1, 0xF, true>(v);   // lane ^ 1
+    if (lgteam >= 2) v += dpp<0x4E, 0xF, true>(v);   // lane ^ 2
+    if (lgteam >= 3) v += dpp<0x141, 0xF, true>(v);  // mirrored within 8
+    if (lgteam >= 4) v += dpp<0x140, 0xF, true>(v);  // mirrored within 16
+    if (lgteam >= 5) v = add_x16(v);
+    if (lgteam >= 6) v = add_x32(v);
     return v;
   } else {
     v = wave_sum(v);
@@ -35,20 +46,68 @@ __device__ __forceinline__ float team_sum(float v, int lgteam, float* red) {
   }
 }
 
+// Two at once, with one barrier.
+template <int BLK>
+__device__ __forceinline__ void team_sum2(float& a, float& b, int lgteam, float (&red)[2][16]) {
+  if constexpr (BLK == 0) {
+    a = team_sum<0>(a, lgteam, nullptr);
+    b = team_sum<0>(b, lgteam, nullptr);
+  } else {
+    a = wave_sum(a);
+    b = wave_sum(b);
+    if ((threadIdx.x & 63) == 0) {
+      red[0][threadIdx.x >> 6] = a;
+      red[1][threadIdx.x >> 6] = b;
+    }
+    __syncthreads();
+    a = b = 0.f;
+#pragma unroll
+    for (int i = 0; i < BLK / 64; ++i) {
+      a += red[0][i];
+      b += red[1][i];
+    }
+  }
+}
+
 template <int BLK>
 constexpr int threads() {
   return BLK == 0 ? 256 : BLK;
 }
 
-template <int BLK>
-__device__ __forceinline__ int64_t team_index(int lgteam) {
-  if constexpr (BLK == 0) return (int64_t(blockIdx.x) * 256 + threadIdx.x) >> lgteam;
-  return blockIdx.x;
-}
-template <int BLK>
-__device__ __forceinline__ int team_lane(int lgteam) {
-  if constexpr (BLK == 0) return int(threadIdx.x) & ((1 << lgteam) - 1);
-  return int(threadIdx.x);
+// Where a lane is: its team's first row and group, and its words' columns.
+template <int V, int NV, int BLK>
+struct Place {
+  static constexpr int NR = NV > 0 ? NV : 1;
+  int lane, team, g0, width, c[NR];
+  int64_t walker;
+  bool in[NR];
+  __device__ __forceinline__ Place(int lgteam, int G, int Dg) {
+    team = BLK ? BLK : 1 << lgteam;
+    const uint32_t slot = BLK ? blockIdx.x : (blockIdx.x * 256u + threadIdx.x) >> lgteam;
+    lane = BLK ? int(threadIdx.x) : int(threadIdx.x) & (team - 1);
+    walker = slot / uint32_t(G);
+    g0 = int(slot % uint32_t(G)) * Dg;
+    width = Dg;
+#pragma unroll
+    for (int i = 0; i < NR; ++i) {
+      c[i] = (i * team + lane) * V;
+      in[i] = c[i] < Dg;
+      c[i] = in[i] ? c[i] : 0;
+    }
+  }
+};
+// A gain's values at a lane's words (1 without one).
+template <int V, int NR>
+__device__ __forceinline__ void gain(const float* w, const int (&c)[NR], float (&o)[NR][V]) {
+#pragma unroll
+  for (int i = 0; i < NR; ++i) {
+    if (w != nullptr) {
+      unpack<float, V>(load_pack<float, V>(w + c[i]), o[i]);
+    } else {
+#pragma unroll
+      for (int j = 0; j < V; ++j) o[i][j] = 1.f;
+    }
+  }
 }
 
 struct GatedP {
@@ -56,73 +115,92 @@ struct GatedP {
   const void* z;
   const float* w;
   void* y;
-  int64_t xld, zld, units;
+  int64_t xld, zld, M, walkers;
   int D, G, Dg, lgteam, gate_first;
   float eps, inv;
 };
 
 template <typename T, int V, int NV, int BLK>
 __global__ __launch_bounds__(threads<BLK>()) void gated_kernel(GatedP p) {
-  __shared__ float red[16];
-  const int64_t unit = team_index<BLK>(p.lgteam);
-  const int lane = team_lane<BLK>(p.lgteam), team = BLK ? BLK : 1 << p.lgteam;
-  const bool live = unit < p.units;
-  const int64_t row = live ? unit / p.G : 0;
-  const int g0 = live ? int(unit - row * p.G) * p.Dg : 0;
-  const T* x = static_cast<const T*>(p.x) + row * p.xld + g0;
-  const T* z = p.z == nullptr ? nullptr : static_cast<const T*>(p.z) + row * p.zld + g0;
-  T* y = static_cast<T*>(p.y) + row * p.D + g0;
-  const float* w = p.w == nullptr ? nullptr : p.w + g0;
-  const bool first = p.gate_first != 0;
+  __shared__ float red[2][16];
+  const Place<V, NV, BLK> at(p.lgteam, p.G, p.Dg);
+  const T* x = static_cast<const T*>(p.x) + at.g0;
+  const bool gated = p.z != nullptr, first = p.gate_first != 0;
+  const T* z = gated ? static_cast<const T*>(p.z) + at.g0 : nullptr;
+  T* y = static_cast<T*>(p.y) + at.g0;
+  const float* w = p.w == nullptr ? nullptr : p.w + at.g0;
+  const int64_t whole = p.M / p.walkers;
   if constexpr (NV > 0) {
-    float v[NV][V], gate[NV][V];
-    float s = 0.f;
+    float wr[NV][V];
+    gain<V, NV>(w, at.c, wr);
     Pack<T, V> qx[NV], qz[NV];
+    auto fetch = [&](int64_t k) {
+      int64_t row = at.walker + k * p.walkers;
+      row = row < p.M ? row : p.M - 1;
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int c = (i * team + lane) * V;
-      qx[i] = Pack<T, V>{};
-      qz[i] = Pack<T, V>{};
-      if (live && c < p.Dg) {
-        qx[i] = load_pack<T, V>(x + c);
-        if (z != nullptr) qz[i] = load_pack<T, V>(z + c);
+      for (int i = 0; i < NV; ++i) {
+        qx[i] = load_pack<T, V>(x + row * p.xld + at.c[i]);
+        if (gated) qz[i] = load_pack<T, V>(z + row * p.zld + at.c[i]);
       }
-    }
+    };
+    auto turn = [&](int64_t k, bool last) {
+      float v[NV][V], gate[NV][V];
+      float s = 0.f;
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      unpack<T, V>(qx[i], v[i]);
-      unpack<T, V>(qz[i], gate[i]);
+      for (int i = 0; i < NV; ++i) {
+        unpack<T, V>(qx[i], v[i]);
+        if (gated) {
+          unpack<T, V>(qz[i], gate[i]);
 #pragma unroll
-      for (int j = 0; j < V; ++j) {
-        gate[i][j] = z != nullptr ? silu_f(gate[i][j]) : 1.f;
-        if (first) v[i][j] *= gate[i][j];
-        s = fmaf(v[i][j], v[i][j], s);
+          for (int j = 0; j < V; ++j) gate[i][j] = silu_f(gate[i][j]);
+        } else {
+#pragma unroll
+          for (int j = 0; j < V; ++j) gate[i][j] = 1.f;
+        }
+        if (first) {
+#pragma unroll
+          for (int j = 0; j < V; ++j) v[i][j] *= gate[i][j];
+        }
+        float t = 0.f;
+#pragma unroll
+        for (int j = 0; j < V; ++j) t = fmaf(v[i][j], v[i][j], t);
+        s += at.in[i] ? t : 0.f;
       }
-    }
-    const float r = rsqrtf(team_sum<BLK>(s, p.lgteam, red) * p.inv + p.eps);
+      if (!last) fetch(k + 1);
+      const float r = rsqrtf(team_sum<BLK>(s, p.lgteam, red[k & 1]) * p.inv + p.eps);
+      const int64_t row = at.walker + k * p.walkers;
+      if (last && row >= p.M) return;
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int c = (i * team + lane) * V;
-      if (!live || c >= p.Dg) continue;
-      float o[V];
+      for (int i = 0; i < NV; ++i) {
+        float o[V];
+        if (first) {
 #pragma unroll
-      for (int j = 0; j < V; ++j) {
-        o[j] = v[i][j] * r * (w != nullptr ? w[c + j] : 1.f);
-        if (!first) o[j] *= gate[i][j];
+          for (int j = 0; j < V; ++j) o[j] = v[i][j] * r * wr[i][j];
+        } else {
+#pragma unroll
+          for (int j = 0; j < V; ++j) o[j] = v[i][j] * r * wr[i][j] * gate[i][j];
+        }
+        store_pack<T, V>(y + row * p.D + at.c[i], o);
       }
-      store_pack<T, V>(y + c, o);
-    }
+    };
+    fetch(0);
+    for (int64_t k = 0; k < whole; ++k) turn(k, false);
+    if (whole * p.walkers < p.M) turn(whole, true);
   } else {
-    float s = 0.f;
-    for (int c = lane; c < p.Dg; c += team) {
-      float v = to_f32(x[c]);
-      if (first && z != nullptr) v *= silu_f(to_f32(z[c]));
-      s = fmaf(v, v, s);
-    }
-    const float r = rsqrtf(team_sum<BLK>(s, p.lgteam, red) * p.inv + p.eps);
-    for (int c = lane; c < p.Dg; c += team) {
-      const float gate = z != nullptr ? silu_f(to_f32(z[c])) : 1.f;
-      from_f32(to_f32(x[c]) * gate * r * (w != nullptr ? w[c] : 1.f), y[c]);
+    for (int64_t row = at.walker, k = 0; row < p.M; row += p.walkers, ++k) {
+      const T* xr = x + row * p.xld;
+      const T* zr = gated ? z + row * p.zld : nullptr;
+      float s = 0.f;
+      for (int c = at.lane; c < p.Dg; c += at.team) {
+        float v = to_f32(xr[c]);
+        if (first && gated) v *= silu_f(to_f32(zr[c]));
+        s = fmaf(v, v, s);
+      }
+      const float r = rsqrtf(team_sum<BLK>(s, p.lgteam, red[k & 1]) * p.inv + p.eps);
+      for (int c = at.lane; c < p.Dg; c += at.team) {
+        const float gate = gated ? silu_f(to_f32(zr[c])) : 1.f;
+        from_f32(to_f32(xr[c]) * gate * r * (w != nullptr ? w[c] : 1.f), y[row * p.D + c]);
+      }
     }
   }
 }
@@ -142,121 +220,121 @@ struct GatedBwP {
 
 // With v = x silu(z) (or x), n = v r, r = rsqrt(mean(v^2) + eps), u = dy (or dy
 // silu(z)) and e = u w:  dv = r (e - n mean(e n)), dw = sum u n.  Both sums of
-// a row, v^2 and e v, go through one reduction.  A team keeps its group and
-// walks rows `walkers` apart, so that its part of dw stays in registers.
+// a row, v^2 and e v, are known before its outputs are formed.
 template <typename T, int V, int NV, int BLK>
 __global__ __launch_bounds__(threads<BLK>()) void gated_backward_kernel(GatedBwP p) {
   __shared__ float red[2][2][16];
-  const int64_t slot = team_index<BLK>(p.lgteam);
-  const int lane = team_lane<BLK>(p.lgteam), team = BLK ? BLK : 1 << p.lgteam;
-  const int64_t walker = slot / p.G;
-  const int g0 = int(slot - walker * p.G) * p.Dg;
-  const bool live = walker < p.walkers;
+  const Place<V, NV, BLK> at(p.lgteam, p.G, p.Dg);
   const bool first = p.gate_first != 0, gated = p.z != nullptr;
-  const float* w = p.w == nullptr ? nullptr : p.w + g0;
-  float* part = p.part == nullptr ? nullptr : p.part + walker * p.D + g0;
-  constexpr int NR = NV > 0 ? NV : 1;
-  float dw[NR][V], wr[NR][V];
+  const T* x = static_cast<const T*>(p.x) + at.g0;
+  const T* z = gated ? static_cast<const T*>(p.z) + at.g0 : nullptr;
+  const T* dy = static_cast<const T*>(p.dy) + at.g0;
+  T* dx = static_cast<T*>(p.dx) + at.g0;
+  T* dz = gated ? static_cast<T*>(p.dz) + at.g0 : nullptr;
+  const float* w = p.w == nullptr ? nullptr : p.w + at.g0;
+  float* part = p.part == nullptr ? nullptr : p.part + at.walker * p.D + at.g0;
+  const int64_t whole = p.M / p.walkers;
+  if constexpr (NV > 0) {
+    float dw[NV][V], wr[NV][V];
+    gain<V, NV>(w, at.c, wr);
 #pragma unroll
-  for (int i = 0; i < NR; ++i) {
-    const int c = (i * team + lane) * V;
+    for (int i = 0; i < NV; ++i)
 #pragma unroll
-    for (int j = 0; j < V; ++j) {
-      dw[i][j] = 0.f;
-      wr[i][j] = NV > 0 && w != nullptr && live && c < p.Dg ? w[c + j] : 1.f;
-    }
-  }
-  if constexpr (NV == 0) {
-    if (part != nullptr && live)
-      for (int c = lane; c < p.Dg; c += team) part[c] = 0.f;
-  }
-  // every team of a block makes the same number of turns (the block's barriers)
-  const int64_t turns = (p.M + p.walkers - 1) / p.walkers;
-  for (int64_t k = 0; k < turns; ++k) {
-    const int64_t row = walker + k * p.walkers;
-    const bool on = live && row < p.M;
-    const T* x = static_cast<const T*>(p.x) + (on ? row : 0) * p.xld + g0;
-    const T* z = gated ? static_cast<const T*>(p.z) + (on ? row : 0) * p.zld + g0 : nullptr;
-    const T* dy = static_cast<const T*>(p.dy) + (on ? row : 0) * p.D + g0;
-    T* dx = static_cast<T*>(p.dx) + (on ? row : 0) * p.D + g0;
-    T* dz = static_cast<T*>(p.dz) + (on ? row : 0) * p.D + g0;
-    float s1 = 0.f, s2 = 0.f;
-    if constexpr (NV > 0) {
-      Pack<T, V> qx[NV], qz[NV], qd[NV];
+      for (int j = 0; j < V; ++j) dw[i][j] = 0.f;
+    Pack<T, V> qx[NV], qz[NV], qd[NV];
+    auto fetch = [&](int64_t k) {
+      int64_t row = at.walker + k * p.walkers;
+      row = row < p.M ? row : p.M - 1;
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
-        const int c = (i * team + lane) * V;
-        qx[i] = qz[i] = qd[i] = Pack<T, V>{};
-        if (on && c < p.Dg) {
-          qx[i] = load_pack<T, V>(x + c);
-          qd[i] = load_pack<T, V>(dy + c);
-          if (gated) qz[i] = load_pack<T, V>(z + c);
-        }
+        qx[i] = load_pack<T, V>(x + row * p.xld + at.c[i]);
+        qd[i] = load_pack<T, V>(dy + row * p.D + at.c[i]);
+        if (gated) qz[i] = load_pack<T, V>(z + row * p.zld + at.c[i]);
       }
+    };
+    auto turn = [&](int64_t k, bool last) {
+      float xv[NV][V], zv[NV][V], d[NV][V], sg[NV][V];
+      float s1 = 0.f, s2 = 0.f;
 #pragma unroll
-      for (int i = 0; i < NV; ++i)
+      for (int i = 0; i < NV; ++i) {
+        unpack<T, V>(qx[i], xv[i]);
+        unpack<T, V>(qd[i], d[i]);
+        if (gated) {
+          unpack<T, V>(qz[i], zv[i]);
+#pragma unroll
+          for (int j = 0; j < V; ++j) sg[i][j] = sigmoid_f(zv[i][j]);
+        } else {
+#pragma unroll
+          for (int j = 0; j < V; ++j) zv[i][j] = sg[i][j] = 1.f;
+        }
+        float t1 = 0.f, t2 = 0.f;
 #pragma unroll
         for (int j = 0; j < V; ++j) {
-          const float gate = gated ? silu_f(to_f32(qz[i].e[j])) : 1.f;
-          const float xv = to_f32(qx[i].e[j]), u = to_f32(qd[i].e[j]) * wr[i][j];
-          const float v = first ? xv * gate : xv;
-          s1 = fmaf(v, v, s1);
-          s2 = fmaf(first ? u : u * gate, v, s2);
+          const float gate = zv[i][j] * sg[i][j];
+          const float v = first ? xv[i][j] * gate : xv[i][j];
+          const float e = d[i][j] * wr[i][j];
+          t1 = fmaf(v, v, t1);
+          t2 = fmaf(first ? e : e * gate, v, t2);
         }
-      s1 = team_sum<BLK>(s1, p.lgteam, red[k & 1][0]);
-      s2 = team_sum<BLK>(s2, p.lgteam, red[k & 1][1]);
+        s1 += at.in[i] ? t1 : 0.f;
+        s2 += at.in[i] ? t2 : 0.f;
+      }
+      if (!last) fetch(k + 1);
+      team_sum2<BLK>(s1, s2, p.lgteam, red[k & 1]);
       const float r = rsqrtf(s1 * p.inv + p.eps), m = s2 * r * p.inv;
+      const int64_t row = at.walker + k * p.walkers;
+      if (last && row >= p.M) return;
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
-        const int c = (i * team + lane) * V;
-        if (!on || c >= p.Dg) continue;
         float ox[V], oz[V];
 #pragma unroll
         for (int j = 0; j < V; ++j) {
-          const float zv = to_f32(qz[i].e[j]), xv = to_f32(qx[i].e[j]), d = to_f32(qd[i].e[j]);
-          const float sg = gated ? sigmoid_f(zv) : 1.f, gate = gated ? zv * sg : 1.f;
-          const float n = (first ? xv * gate : xv) * r;
-          const float u = first ? d : d * gate;
+          const float gate = zv[i][j] * sg[i][j];
+          const float n = (first ? xv[i][j] * gate : xv[i][j]) * r;
+          const float u = first ? d[i][j] : d[i][j] * gate;
           const float dv = r * (u * wr[i][j] - n * m);
           ox[j] = first ? dv * gate : dv;
-          oz[j] = (first ? dv * xv : d * n * wr[i][j]) * dsilu_f(zv, sg);
+          oz[j] = (first ? dv * xv[i][j] : d[i][j] * n * wr[i][j]) * dsilu_f(zv[i][j], sg[i][j]);
           dw[i][j] = fmaf(u, n, dw[i][j]);
         }
-        store_pack<T, V>(dx + c, ox);
-        if (gated) store_pack<T, V>(dz + c, oz);
+        store_pack<T, V>(dx + row * p.D + at.c[i], ox);
+        if (gated) store_pack<T, V>(dz + row * p.D + at.c[i], oz);
       }
-    } else {
-      for (int c = lane; on && c < p.Dg; c += team) {
-        const float gate = gated ? silu_f(to_f32(z[c])) : 1.f;
-        const float xv = to_f32(x[c]), u = to_f32(dy[c]) * (w != nullptr ? w[c] : 1.f);
+    };
+    fetch(0);
+    for (int64_t k = 0; k < whole; ++k) turn(k, false);
+    if (whole * p.walkers < p.M) turn(whole, true);
+    if (part == nullptr) return;
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+      if (at.in[i]) store_pack<float, V>(part + at.c[i], dw[i]);
+  } else {
+    if (part != nullptr)
+      for (int c = at.lane; c < p.Dg; c += at.team) part[c] = 0.f;
+    for (int64_t row = at.walker, k = 0; row < p.M; row += p.walkers, ++k) {
+      const T* xr = x + row * p.xld;
+      const T* zr = gated ? z + row * p.zld : nullptr;
+      const T* dr = dy + row * p.D;
+      float s1 = 0.f, s2 = 0.f;
+      for (int c = at.lane; c < p.Dg; c += at.team) {
+        const float gate = gated ? silu_f(to_f32(zr[c])) : 1.f;
+        const float xv = to_f32(xr[c]), e = to_f32(dr[c]) * (w != nullptr ? w[c] : 1.f);
         const float v = first ? xv * gate : xv;
         s1 = fmaf(v, v, s1);
-        s2 = fmaf(first ? u : u * gate, v, s2);
+        s2 = fmaf(first ? e : e * gate, v, s2);
       }
-      s1 = team_sum<BLK>(s1, p.lgteam, red[k & 1][0]);
-      s2 = team_sum<BLK>(s2, p.lgteam, red[k & 1][1]);
+      team_sum2<BLK>(s1, s2, p.lgteam, red[k & 1]);
       const float r = rsqrtf(s1 * p.inv + p.eps), m = s2 * r * p.inv;
-      for (int c = lane; on && c < p.Dg; c += team) {
-        const float zv = gated ? to_f32(z[c]) : 0.f, xv = to_f32(x[c]), d = to_f32(dy[c]);
-        const float sg = gated ? sigmoid_f(zv) : 1.f, gate = gated ? zv * sg : 1.f;
-        const float wc = w != nullptr ? w[c] : 1.f;
+      for (int c = at.lane; c < p.Dg; c += at.team) {
+        const float zv = gated ? to_f32(zr[c]) : 1.f, xv = to_f32(xr[c]), d = to_f32(dr[c]);
+        const float sg = gated ? sigmoid_f(zv) : 1.f, gate = zv * sg, wc = w != nullptr ? w[c] : 1.f;
         const float n = (first ? xv * gate : xv) * r;
         const float u = first ? d : d * gate;
         const float dv = r * (u * wc - n * m);
-        from_f32(first ? dv * gate : dv, dx[c]);
-        if (gated) from_f32((first ? dv * xv : d * n * wc) * dsilu_f(zv, sg), dz[c]);
+        from_f32(first ? dv * gate : dv, dx[row * p.D + c]);
+        if (gated) from_f32((first ? dv * xv : d * n * wc) * dsilu_f(zv, sg), dz[row * p.D + c]);
         if (part != nullptr) part[c] = fmaf(u, n, part[c]);
       }
-    }
-  }
-  if constexpr (NV > 0) {
-    if (part == nullptr || !live) return;
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int c = (i * team + lane) * V;
-#pragma unroll
-      for (int j = 0; j < V; ++j)
-        if (c + j < p.Dg) part[c + j] = dw[i][j];
     }
   }
 }
@@ -268,72 +346,82 @@ struct ResP {
   const float* w;
   void* y;
   void* res_out;
-  int64_t xld, M;
+  int64_t xld, M, walkers;
   int D, lgteam;
   float eps, inv;
 };
 
 template <typename T, typename R, int V, int NV, int BLK>
 __global__ __launch_bounds__(threads<BLK>()) void residual_kernel(ResP p) {
-  __shared__ float red[16];
-  const int64_t unit = team_index<BLK>(p.lgteam);
-  const int lane = team_lane<BLK>(p.lgteam), team = BLK ? BLK : 1 << p.lgteam;
-  const bool live = unit < p.M;
-  const int64_t row = live ? unit : 0;
-  const T* x = static_cast<const T*>(p.x) + row * p.xld;
-  const R* res = p.res == nullptr ? nullptr : static_cast<const R*>(p.res) + row * p.D;
-  R* out = p.res_out == nullptr ? nullptr : static_cast<R*>(p.res_out) + row * p.D;
-  T* y = static_cast<T*>(p.y) + row * p.D;
+  __shared__ float red[2][16];
+  const Place<V, NV, BLK> at(p.lgteam, 1, p.D);
+  const T* x = static_cast<const T*>(p.x);
+  const R* res = static_cast<const R*>(p.res);
+  R* out = static_cast<R*>(p.res_out);
+  T* y = static_cast<T*>(p.y);
+  const int64_t whole = p.M / p.walkers;
   if constexpr (NV > 0) {
-    float h[NV][V];
-    float s = 0.f;
     Pack<T, V> qx[NV];
     Pack<R, V> qr[NV];
+    auto fetch = [&](int64_t k) {
+      int64_t row = at.walker + k * p.walkers;
+      row = row < p.M ? row : p.M - 1;
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int c = (i * team + lane) * V;
-      qx[i] = Pack<T, V>{};
-      qr[i] = Pack<R, V>{};
-      if (live && c < p.D) {
-        qx[i] = load_pack<T, V>(x + c);
-        if (res != nullptr) qr[i] = load_pack<R, V>(res + c);
+      for (int i = 0; i < NV; ++i) {
+        qx[i] = load_pack<T, V>(x + row * p.xld + at.c[i]);
+        if (res != nullptr) qr[i] = load_pack<R, V>(res + row * p.D + at.c[i]);
+        else qr[i] = Pack<R, V>{};
       }
-    }
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int c = (i * team + lane) * V;
-#pragma unroll
-      for (int j = 0; j < V; ++j) {
-        const float sc = p.scale != nullptr && c < p.D ? p.scale[c + j] : 1.f;
-        h[i][j] = fmaf(sc, to_f32(qx[i].e[j]), to_f32(qr[i].e[j]));
-        s = fmaf(h[i][j], h[i][j], s);
-      }
-      if (out != nullptr && live && c < p.D) store_pack<R, V>(out + c, h[i]);
-    }
-    const float r = rsqrtf(team_sum<BLK>(s, p.lgteam, red) * p.inv + p.eps);
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int c = (i * team + lane) * V;
-      if (!live || c >= p.D) continue;
-      float o[V];
-#pragma unroll
-      for (int j = 0; j < V; ++j) o[j] = h[i][j] * r * (p.w != nullptr ? p.w[c + j] : 1.f);
-      store_pack<T, V>(y + c, o);
-    }
-  } else {
-    auto sum = [&](int c) {
-      return fmaf(p.scale != nullptr ? p.scale[c] : 1.f, to_f32(x[c]), res != nullptr ? to_f32(res[c]) : 0.f);
     };
-    float s = 0.f;
-    for (int c = lane; c < p.D; c += team) {
-      const float h = sum(c);
-      s = fmaf(h, h, s);
-    }
-    const float r = rsqrtf(team_sum<BLK>(s, p.lgteam, red) * p.inv + p.eps);
-    for (int c = lane; c < p.D; c += team) {
-      const float h = sum(c);
-      if (out != nullptr) from_f32(h, out[c]);
-      from_f32(h * r * (p.w != nullptr ? p.w[c] : 1.f), y[c]);
+    fetch(0);
+    float wr[NV][V], sr[NV][V];
+    gain<V, NV>(p.w, at.c, wr);
+    gain<V, NV>(p.scale, at.c, sr);
+    auto turn = [&](int64_t k, bool last) {
+      float h[NV][V];
+      float s = 0.f;
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        float t = 0.f;
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+          h[i][j] = fmaf(sr[i][j], to_f32(qx[i].e[j]), to_f32(qr[i].e[j]));
+          t = fmaf(h[i][j], h[i][j], t);
+        }
+        s += at.in[i] ? t : 0.f;
+      }
+      if (!last) fetch(k + 1);
+      const float r = rsqrtf(team_sum<BLK>(s, p.lgteam, red[k & 1]) * p.inv + p.eps);
+      const int64_t row = at.walker + k * p.walkers;
+      if (last && row >= p.M) return;
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        float o[V];
+        if (out != nullptr) store_pack<R, V>(out + row * p.D + at.c[i], h[i]);
+#pragma unroll
+        for (int j = 0; j < V; ++j) o[j] = h[i][j] * r * wr[i][j];
+        store_pack<T, V>(y + row * p.D + at.c[i], o);
+      }
+    };
+    for (int64_t k = 0; k < whole; ++k) turn(k, false);
+    if (whole * p.walkers < p.M) turn(whole, true);
+  } else {
+    for (int64_t row = at.walker, k = 0; row < p.M; row += p.walkers, ++k) {
+      auto sum = [&](int c) {
+        return fmaf(p.scale != nullptr ? p.scale[c] : 1.f, to_f32(x[row * p.xld + c]),
+                    res != nullptr ? to_f32(res[row * p.D + c]) : 0.f);
+      };
+      float s = 0.f;
+      for (int c = at.lane; c < p.D; c += at.team) {
+        const float h = sum(c);
+        s = fmaf(h, h, s);
+      }
+      const float r = rsqrtf(team_sum<BLK>(s, p.lgteam, red[k & 1]) * p.inv + p.eps);
+      for (int c = at.lane; c < p.D; c += at.team) {
+        const float h = sum(c);
+        if (out != nullptr) from_f32(h, out[row * p.D + c]);
+        from_f32(h * r * (p.w != nullptr ? p.w[c] : 1.f), y[row * p.D + c]);
+      }
     }
   }
 }
@@ -358,145 +446,141 @@ struct ResBwP {
 template <typename T, typename R, int V, int NV, int BLK>
 __global__ __launch_bounds__(threads<BLK>()) void residual_backward_kernel(ResBwP p) {
   __shared__ float red[2][2][16];
-  const int64_t walker = team_index<BLK>(p.lgteam);
-  const int lane = team_lane<BLK>(p.lgteam), team = BLK ? BLK : 1 << p.lgteam;
-  const bool live = walker < p.walkers;
-  float* pw = nullptr;
-  float* ps = nullptr;
-  if (live) {
-    float* row = p.part + walker * (p.has_dw + p.has_ds) * p.D;
-    if (p.has_dw) pw = row;
-    if (p.has_ds) ps = row + (p.has_dw ? p.D : 0);
-  }
-  constexpr int NR = NV > 0 ? NV : 1;
-  float dw[NR][V], ds[NR][V], wr[NR][V], sr[NR][V];
-#pragma unroll
-  for (int i = 0; i < NR; ++i) {
-    const int c = (i * team + lane) * V;
-#pragma unroll
-    for (int j = 0; j < V; ++j) {
-      dw[i][j] = ds[i][j] = 0.f;
-      wr[i][j] = NV > 0 && p.w != nullptr && c < p.D ? p.w[c + j] : 1.f;
-      sr[i][j] = NV > 0 && p.scale != nullptr && c < p.D ? p.scale[c + j] : 1.f;
-    }
-  }
-  if constexpr (NV == 0) {
-    for (int c = lane; c < p.D; c += team) {
-      if (pw != nullptr) pw[c] = 0.f;
-      if (ps != nullptr) ps[c] = 0.f;
-    }
-  }
-  const int64_t turns = (p.M + p.walkers - 1) / p.walkers;
-  for (int64_t k = 0; k < turns; ++k) {
-    const bool on = live && walker + k * p.walkers < p.M;
-    const int64_t row = on ? walker + k * p.walkers : 0;
-    const R* h = static_cast<const R*>(p.h) + row * p.D;
-    const T* x = static_cast<const T*>(p.x) + row * p.xld;
-    const T* dy = static_cast<const T*>(p.dy) + row * p.D;
-    const R* dro = p.dro == nullptr ? nullptr : static_cast<const R*>(p.dro) + row * p.D;
-    T* dx = p.dx == nullptr ? nullptr : static_cast<T*>(p.dx) + row * p.D;
-    R* dres = p.dres == nullptr ? nullptr : static_cast<R*>(p.dres) + row * p.D;
-    float s1 = 0.f, s2 = 0.f;
-    if constexpr (NV > 0) {
-      Pack<R, V> qh[NV], qr[NV];
-      Pack<T, V> qd[NV], qx[NV];
+  const Place<V, NV, BLK> at(p.lgteam, 1, p.D);
+  float* prow = p.part + at.walker * (p.has_dw + p.has_ds) * p.D;
+  float* pw = p.has_dw ? prow : nullptr;
+  float* ps = p.has_ds ? prow + (p.has_dw ? p.D : 0) : nullptr;
+  const R* h = static_cast<const R*>(p.h);
+  const T* x = static_cast<const T*>(p.x);
+  const T* dy = static_cast<const T*>(p.dy);
+  const R* dro = static_cast<const R*>(p.dro);
+  T* dx = static_cast<T*>(p.dx);
+  R* dres = static_cast<R*>(p.dres);
+  const int64_t whole = p.M / p.walkers;
+  if constexpr (NV > 0) {
+    Pack<R, V> qh[NV], qr[NV];
+    Pack<T, V> qd[NV], qx[NV];
+    auto fetch = [&](int64_t k) {
+      int64_t row = at.walker + k * p.walkers;
+      row = row < p.M ? row : p.M - 1;
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
-        const int c = (i * team + lane) * V;
-        qh[i] = qr[i] = Pack<R, V>{};
-        qd[i] = qx[i] = Pack<T, V>{};
-        if (on && c < p.D) {
-          qh[i] = load_pack<R, V>(h + c);
-          qd[i] = load_pack<T, V>(dy + c);
-          if (dro != nullptr) qr[i] = load_pack<R, V>(dro + c);
-          if (p.has_ds) qx[i] = load_pack<T, V>(x + c);
-        }
+        qh[i] = load_pack<R, V>(h + row * p.D + at.c[i]);
+        qd[i] = load_pack<T, V>(dy + row * p.D + at.c[i]);
+        if (dro != nullptr) qr[i] = load_pack<R, V>(dro + row * p.D + at.c[i]);
+        else qr[i] = Pack<R, V>{};
+        if (p.has_ds) qx[i] = load_pack<T, V>(x + row * p.xld + at.c[i]);
+        else qx[i] = Pack<T, V>{};
       }
+    };
+    fetch(0);
+    float dw[NV][V], ds[NV][V], wr[NV][V], sr[NV][V];
+    gain<V, NV>(p.w, at.c, wr);
+    gain<V, NV>(p.scale, at.c, sr);
 #pragma unroll
-      for (int i = 0; i < NV; ++i)
+    for (int i = 0; i < NV; ++i)
+#pragma unroll
+      for (int j = 0; j < V; ++j) dw[i][j] = ds[i][j] = 0.f;
+    auto turn = [&](int64_t k, bool last) {
+      // the row as it came, so that it takes half the registers
+      Pack<R, V> ch[NV], cr[NV];
+      Pack<T, V> cd[NV], cx[NV];
+      float s1 = 0.f, s2 = 0.f;
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        ch[i] = qh[i];
+        cr[i] = qr[i];
+        cd[i] = qd[i];
+        cx[i] = qx[i];
+        float t1 = 0.f, t2 = 0.f;
 #pragma unroll
         for (int j = 0; j < V; ++j) {
-          const float hv = to_f32(qh[i].e[j]);
-          s1 = fmaf(hv, hv, s1);
-          s2 = fmaf(to_f32(qd[i].e[j]) * wr[i][j], hv, s2);
+          const float hv = to_f32(ch[i].e[j]);
+          t1 = fmaf(hv, hv, t1);
+          t2 = fmaf(to_f32(cd[i].e[j]) * wr[i][j], hv, t2);
         }
-      s1 = team_sum<BLK>(s1, p.lgteam, red[k & 1][0]);
-      s2 = team_sum<BLK>(s2, p.lgteam, red[k & 1][1]);
+        s1 += at.in[i] ? t1 : 0.f;
+        s2 += at.in[i] ? t2 : 0.f;
+      }
+      if (!last) fetch(k + 1);
+      team_sum2<BLK>(s1, s2, p.lgteam, red[k & 1]);
       const float r = rsqrtf(s1 * p.inv + p.eps), m = s2 * r * p.inv;
+      const int64_t row = at.walker + k * p.walkers;
+      if (last && row >= p.M) return;
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
-        const int c = (i * team + lane) * V;
-        if (!on || c >= p.D) continue;
         float o[V], ox[V];
 #pragma unroll
         for (int j = 0; j < V; ++j) {
-          const float n = to_f32(qh[i].e[j]) * r, d = to_f32(qd[i].e[j]);
-          o[j] = to_f32(qr[i].e[j]) + r * (d * wr[i][j] - n * m);
+          const float n = to_f32(ch[i].e[j]) * r, d = to_f32(cd[i].e[j]);
+          o[j] = to_f32(cr[i].e[j]) + r * (d * wr[i][j] - n * m);
           ox[j] = sr[i][j] * o[j];
           dw[i][j] = fmaf(d, n, dw[i][j]);
-          ds[i][j] = fmaf(o[j], to_f32(qx[i].e[j]), ds[i][j]);
+          ds[i][j] = fmaf(o[j], to_f32(cx[i].e[j]), ds[i][j]);
         }
-        if (dres != nullptr) store_pack<R, V>(dres + c, o);
-        if (dx != nullptr) store_pack<T, V>(dx + c, ox);
+        if (dres != nullptr) store_pack<R, V>(dres + row * p.D + at.c[i], o);
+        if (dx != nullptr) store_pack<T, V>(dx + row * p.D + at.c[i], ox);
       }
-    } else {
-      for (int c = lane; on && c < p.D; c += team) {
-        const float hv = to_f32(h[c]);
-        s1 = fmaf(hv, hv, s1);
-        s2 = fmaf(to_f32(dy[c]) * (p.w != nullptr ? p.w[c] : 1.f), hv, s2);
-      }
-      s1 = team_sum<BLK>(s1, p.lgteam, red[k & 1][0]);
-      s2 = team_sum<BLK>(s2, p.lgteam, red[k & 1][1]);
-      const float r = rsqrtf(s1 * p.inv + p.eps), m = s2 * r * p.inv;
-      for (int c = lane; on && c < p.D; c += team) {
-        const float n = to_f32(h[c]) * r, d = to_f32(dy[c]);
-        const float o = (dro != nullptr ? to_f32(dro[c]) : 0.f) + r * (d * (p.w != nullptr ? p.w[c] : 1.f) - n * m);
-        if (dres != nullptr) from_f32(o, dres[c]);
-        if (dx != nullptr) from_f32((p.scale != nullptr ? p.scale[c] : 1.f) * o, dx[c]);
-        if (pw != nullptr) pw[c] = fmaf(d, n, pw[c]);
-        if (ps != nullptr) ps[c] = fmaf(o, to_f32(x[c]), ps[c]);
-      }
-    }
-  }
-  if constexpr (NV > 0) {
+    };
+    for (int64_t k = 0; k < whole; ++k) turn(k, false);
+    if (whole * p.walkers < p.M) turn(whole, true);
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      const int c = (i * team + lane) * V;
-#pragma unroll
-      for (int j = 0; j < V; ++j)
-        if (c + j < p.D) {
-          if (pw != nullptr) pw[c + j] = dw[i][j];
-          if (ps != nullptr) ps[c + j] = ds[i][j];
-        }
+      if (!at.in[i]) continue;
+      if (pw != nullptr) store_pack<float, V>(pw + at.c[i], dw[i]);
+      if (ps != nullptr) store_pack<float, V>(ps + at.c[i], ds[i]);
+    }
+  } else {
+    for (int c = at.lane; c < p.D; c += at.team) {
+      if (pw != nullptr) pw[c] = 0.f;
+      if (ps != nullptr) ps[c] = 0.f;
+    }
+    for (int64_t row = at.walker, k = 0; row < p.M; row += p.walkers, ++k) {
+      const int64_t r0 = row * p.D;
+      float s1 = 0.f, s2 = 0.f;
+      for (int c = at.lane; c < p.D; c += at.team) {
+        const float hv = to_f32(h[r0 + c]);
+        s1 = fmaf(hv, hv, s1);
+        s2 = fmaf(to_f32(dy[r0 + c]) * (p.w != nullptr ? p.w[c] : 1.f), hv, s2);
+      }
+      team_sum2<BLK>(s1, s2, p.lgteam, red[k & 1]);
+      const float r = rsqrtf(s1 * p.inv + p.eps), m = s2 * r * p.inv;
+      for (int c = at.lane; c < p.D; c += at.team) {
+        const float n = to_f32(h[r0 + c]) * r, d = to_f32(dy[r0 + c]);
+        const float o = (dro != nullptr ? to_f32(dro[r0 + c]) : 0.f) + r * (d * (p.w != nullptr ? p.w[c] : 1.f) - n * m);
+        if (dres != nullptr) from_f32(o, dres[r0 + c]);
+        if (dx != nullptr) from_f32((p.scale != nullptr ? p.scale[c] : 1.f) * o, dx[r0 + c]);
+        if (pw != nullptr) pw[c] = fmaf(d, n, pw[c]);
+        if (ps != nullptr) ps[c] = fmaf(o, to_f32(x[row * p.xld + c]), ps[c]);
+      }
     }
   }
 }
 
-// Lanes for a unit of `width` elements.  Up to 64 words: one wave or a part of
-// it.  Up to 256 words: four words per lane of a wave where the units fill the
-// card (2048 waves or more), else a block of 256 lanes; then wider blocks, and
-// the loop for what no block holds in registers.
-Geom pick(int64_t units, int width, int V, bool vec) {
+// Lanes for a unit of `width` elements: a part of a wave up to 64 words, wider
+// ones over several words per lane or several waves, the loop for what a block
+// does not hold in registers (2048 words, 16384 bf16 values).  Forward, a unit of
+// 65 to 256 words is one wave's where the units fill the card (2048 or more), a
+// block's otherwise; the backward holds four times the registers per word and
+// takes a block at once (rows of 2048 bf16, 4 words per lane of one wave: 216
+// registers and 216 us for 32768 rows; one word per lane of four: see the kernel).
+Geom pick(int64_t units, int width, int V, bool vec, bool backward) {
   Geom g{vec, 1, 0, 6};
   const int64_t words = (int64_t(width) + V - 1) / V;
   if (words <= 64) {
     g.lgteam = 0;
     while ((1 << g.lgteam) < words) ++g.lgteam;
-  } else if (words <= 128 && units >= 2048) {
-    g.nv = 2;
-  } else if (words <= 256 && units >= 2048) {
-    g.nv = 4;
-  } else if (words <= 256) {
-    g.blk = 256;
+  } else if (words <= 256 && units >= 2048 && !backward) {
+    g.nv = words <= 128 ? 2 : 4;
   } else if (words <= 512) {
     g.blk = 256;
-    g.nv = 2;
+    g.nv = words <= 256 ? 1 : 2;
   } else if (words <= 1024) {
-    g.blk = 256;
-    g.nv = 4;
-  } else if (words <= 4096) {
+    g.blk = backward ? 1024 : 256;
+    g.nv = backward ? 1 : 4;
+  } else if (words <= 2048) {
     g.blk = 1024;
-    g.nv = 4;
+    g.nv = 2;
   } else {
     g.vec = false;
     g.blk = 1024;
@@ -505,56 +589,58 @@ Geom pick(int64_t units, int width, int V, bool vec) {
   return g;
 }
 
-// Rows a team of the backward kernels walks: enough teams for 2048 waves, but
-// at least 32 rows each once the card is full (the partial sums of a team cost
-// as much as four rows).
-int64_t pick_walkers(int64_t M, int G, const Geom& g) {
+// Teams of a group, each walking rows that far apart: `waves` waves in all on the
+// card's 1024 SIMDs, whole blocks of teams, at most one team per row (rounded up to
+// a block's worth).
+int64_t pick_walkers(int64_t M, int G, const Geom& g, int64_t waves) {
   const int64_t lanes = g.blk ? g.blk : int64_t(1) << g.lgteam;
-  int64_t w = (int64_t(2048) * 64 + lanes * G - 1) / (lanes * G);
-  if (w < (M + 31) / 32) w = (M + 31) / 32;
-  const int64_t most = (int64_t(16384) * 64 + lanes * G - 1) / (lanes * G);
-  if (w > most) w = most;
-  return w < M ? w : M;
+  const int64_t per = g.blk ? 1 : 256 >> g.lgteam;  // teams of a block
+  int64_t w = waves * 64 / (lanes * G);
+  if (w > M) w = M;
+  if (w < 1) w = 1;
+  return (w + per - 1) / per * per;
 }
+constexpr int64_t kForwardWaves = 8192, kBackwardWaves = 4096;
 
-// The kernel instance for a geometry: F<V, NV, BLK>(...).
-#define M3_NORM_DISPATCH(g, VV, CALL)                      \
-  if ((g).nv == 0) return CALL(1, 0, 1024);                \
-  if ((g).vec) {                                           \
-    if ((g).blk == 1024) return CALL(VV, 4, 1024);         \
-    if ((g).blk == 256) {                                  \
-      if ((g).nv == 1) return CALL(VV, 1, 256);            \
-      if ((g).nv == 2) return CALL(VV, 2, 256);            \
-      return CALL(VV, 4, 256);                             \
-    }                                                      \
-    if ((g).nv == 1) return CALL(VV, 1, 0);                \
-    if ((g).nv == 2) return CALL(VV, 2, 0);                \
-    return CALL(VV, 4, 0);                                 \
-  }                                                        \
-  if ((g).blk == 1024) return CALL(1, 4, 1024);            \
-  if ((g).blk == 256) {                                    \
-    if ((g).nv == 1) return CALL(1, 1, 256);               \
-    if ((g).nv == 2) return CALL(1, 2, 256);               \
-    return CALL(1, 4, 256);                                \
-  }                                                        \
-  if ((g).nv == 1) return CALL(1, 1, 0);                   \
-  if ((g).nv == 2) return CALL(1, 2, 0);                   \
-  return CALL(1, 4, 0);
+// The kernel instance for a geometry: CALL(V, NV, BLK).
+#define M3_NORM_WIDTH(g, V, CALL)            \
+  if ((g).blk == 0) {                        \
+    if ((g).nv == 1) return CALL(V, 1, 0);   \
+    if ((g).nv == 2) return CALL(V, 2, 0);   \
+    return CALL(V, 4, 0);                    \
+  }                                          \
+  if ((g).blk == 1024) return CALL(V, 2, 1024); \
+  if ((g).nv == 1) return CALL(V, 1, 256);   \
+  if ((g).nv == 2) return CALL(V, 2, 256);   \
+  return CALL(V, 4, 256);
+#define M3_NORM_BACKWARD_WIDTH(g, V, CALL)        \
+  if ((g).blk == 0) return CALL(V, 1, 0);         \
+  if ((g).blk == 256) {                           \
+    if ((g).nv == 1) return CALL(V, 1, 256);      \
+    return CALL(V, 2, 256);                       \
+  }                                               \
+  if ((g).nv == 1) return CALL(V, 1, 1024);       \
+  return CALL(V, 2, 1024);
+#define M3_NORM_DISPATCH(g, VV, WIDTH, CALL) \
+  if ((g).nv == 0) return CALL(1, 0, 1024);  \
+  if ((g).vec) {                             \
+    WIDTH(g, VV, CALL)                       \
+  }                                          \
+  WIDTH(g, 1, CALL)
 
-uint32_t grid_of(const Geom& g, int64_t teams) {
-  return uint32_t(g.blk ? teams : ((teams << g.lgteam) + 255) / 256);
-}
+uint32_t grid_of(const Geom& g, int64_t teams) { return uint32_t(g.blk ? teams : (teams << g.lgteam) / 256); }
+bool gain_aligned(const float* w) { return reinterpret_cast<uintptr_t>(w) % 16 == 0; }
 
 template <typename T>
 hipError_t run_gated(const m3_gated_norm_args& a, hipStream_t s) {
   constexpr int VV = 16 / int(sizeof(T));
   const int Dg = a.D / a.G;
   const bool vec = Dg % VV == 0 && rows_aligned(a.x, a.x_ld, sizeof(T), 16) && rows_aligned(a.z, a.z_ld, sizeof(T), 16) &&
-                   rows_aligned(a.y, a.D, sizeof(T), 16);
-  const Geom g = pick(a.M * a.G, Dg, vec ? VV : 1, vec);
-  const GatedP p{a.x, a.z, a.w, a.y, a.x_ld, a.z_ld, a.M * a.G, a.D, a.G, Dg, g.lgteam, a.gate_first, a.eps, 1.f / float(Dg)};
-#define CALL(V, NV, BLK) (gated_kernel<T, V, NV, BLK><<<grid_of(g, p.units), threads<BLK>(), 0, s>>>(p), hipGetLastError())
-  M3_NORM_DISPATCH(g, VV, CALL)
+                   rows_aligned(a.y, a.D, sizeof(T), 16) && gain_aligned(a.w);
+  const Geom g = pick(a.M * a.G, Dg, vec ? VV : 1, vec, false);
+  const GatedP p{a.x, a.z, a.w, a.y, a.x_ld, a.z_ld, a.M, pick_walkers(a.M, a.G, g, kForwardWaves), a.D, a.G, Dg, g.lgteam, a.gate_first, a.eps, 1.f / float(Dg)};
+#define CALL(V, NV, BLK) (gated_kernel<T, V, NV, BLK><<<grid_of(g, p.walkers * p.G), threads<BLK>(), 0, s>>>(p), hipGetLastError())
+  M3_NORM_DISPATCH(g, VV, M3_NORM_WIDTH, CALL)
 #undef CALL
 }
 
@@ -564,14 +650,14 @@ bool gated_bw_vec(const m3_gated_norm_backward_args& a) {
   const m3_gated_norm_args& f = a.fwd;
   return (f.D / f.G) % VV == 0 && rows_aligned(f.x, f.x_ld, sizeof(T), 16) && rows_aligned(f.z, f.z_ld, sizeof(T), 16) &&
          rows_aligned(a.dy, f.D, sizeof(T), 16) && rows_aligned(a.dx, f.D, sizeof(T), 16) &&
-         rows_aligned(a.dz, f.D, sizeof(T), 16);
+         rows_aligned(a.dz, f.D, sizeof(T), 16) && gain_aligned(f.w);
 }
 template <typename T>
 hipError_t launch_gated_bw(const GatedBwP& p, const Geom& g, hipStream_t s) {
   constexpr int VV = 16 / int(sizeof(T));
 #define CALL(V, NV, BLK) \
   (gated_backward_kernel<T, V, NV, BLK><<<grid_of(g, p.walkers * p.G), threads<BLK>(), 0, s>>>(p), hipGetLastError())
-  M3_NORM_DISPATCH(g, VV, CALL)
+  M3_NORM_DISPATCH(g, VV, M3_NORM_BACKWARD_WIDTH, CALL)
 #undef CALL
 }
 template <typename T>
@@ -580,9 +666,9 @@ hipError_t run_gated_bw(const m3_gated_norm_backward_args& a, hipStream_t s) {
   const m3_gated_norm_args& f = a.fwd;
   const int Dg = f.D / f.G;
   const bool vec = gated_bw_vec<T>(a);
-  const Geom g = pick(f.M * f.G, Dg, vec ? VV : 1, vec);
+  const Geom g = pick(f.M * f.G, Dg, vec ? VV : 1, vec, true);
   const GatedBwP p{f.x, f.z, f.w, a.dy, a.dx, a.dz, f.w != nullptr ? static_cast<float*>(a.workspace) : nullptr, f.x_ld, f.z_ld,
-                   f.M, pick_walkers(f.M, f.G, g), f.D, f.G, Dg, g.lgteam, f.gate_first, f.eps, 1.f / float(Dg)};
+                   f.M, pick_walkers(f.M, f.G, g, kBackwardWaves), f.D, f.G, Dg, g.lgteam, f.gate_first, f.eps, 1.f / float(Dg)};
   const hipError_t e = launch_gated_bw<T>(p, g, s);
   if (e != hipSuccess || f.w == nullptr) return e;
   ColSum c{};
@@ -598,11 +684,13 @@ template <typename T, typename R>
 hipError_t run_residual(const m3_residual_norm_args& a, hipStream_t s) {
   constexpr int VV = 16 / int(sizeof(T));
   const bool vec = a.D % VV == 0 && rows_aligned(a.x, a.x_ld, sizeof(T), 16) && rows_aligned(a.y, a.D, sizeof(T), 16) &&
-                   rows_aligned(a.residual, a.D, sizeof(R), 16) && rows_aligned(a.residual_out, a.D, sizeof(R), 16);
-  const Geom g = pick(a.M, a.D, vec ? VV : 1, vec);
-  const ResP p{a.x, a.residual, a.scale, a.w, a.y, a.residual_out, a.x_ld, a.M, a.D, g.lgteam, a.eps, 1.f / float(a.D)};
-#define CALL(V, NV, BLK) (residual_kernel<T, R, V, NV, BLK><<<grid_of(g, p.M), threads<BLK>(), 0, s>>>(p), hipGetLastError())
-  M3_NORM_DISPATCH(g, VV, CALL)
+                   rows_aligned(a.residual, a.D, sizeof(R), 16) && rows_aligned(a.residual_out, a.D, sizeof(R), 16) && gain_aligned(a.w) &&
+                   gain_aligned(a.scale);
+  const Geom g = pick(a.M, a.D, vec ? VV : 1, vec, false);
+  const ResP p{a.x, a.residual, a.scale, a.w, a.y, a.residual_out, a.x_ld, a.M, pick_walkers(a.M, 1, g, kForwardWaves),
+               a.D, g.lgteam, a.eps, 1.f / float(a.D)};
+#define CALL(V, NV, BLK) (residual_kernel<T, R, V, NV, BLK><<<grid_of(g, p.walkers), threads<BLK>(), 0, s>>>(p), hipGetLastError())
+  M3_NORM_DISPATCH(g, VV, M3_NORM_WIDTH, CALL)
 #undef CALL
 }
 template <typename T, typename R>
@@ -610,7 +698,7 @@ hipError_t launch_residual_bw(const ResBwP& p, const Geom& g, hipStream_t s) {
   constexpr int VV = 16 / int(sizeof(T));
 #define CALL(V, NV, BLK) \
   (residual_backward_kernel<T, R, V, NV, BLK><<<grid_of(g, p.walkers), threads<BLK>(), 0, s>>>(p), hipGetLastError())
-  M3_NORM_DISPATCH(g, VV, CALL)
+  M3_NORM_DISPATCH(g, VV, M3_NORM_BACKWARD_WIDTH, CALL)
 #undef CALL
 }
 template <typename T, typename R>
@@ -618,10 +706,10 @@ hipError_t run_residual_bw(const m3_residual_norm_backward_args& a, hipStream_t 
   constexpr int VV = 16 / int(sizeof(T));
   const bool vec = a.D % VV == 0 && rows_aligned(a.x, a.x_ld, sizeof(T), 16) && rows_aligned(a.dy, a.D, sizeof(T), 16) &&
                    rows_aligned(a.dx, a.D, sizeof(T), 16) && rows_aligned(a.h, a.D, sizeof(R), 16) &&
-                   rows_aligned(a.dresidual_out, a.D, sizeof(R), 16) && rows_aligned(a.dresidual, a.D, sizeof(R), 16);
-  const Geom g = pick(a.M, a.D, vec ? VV : 1, vec);
+                   rows_aligned(a.dresidual_out, a.D, sizeof(R), 16) && rows_aligned(a.dresidual, a.D, sizeof(R), 16) && gain_aligned(a.w) && gain_aligned(a.scale);
+  const Geom g = pick(a.M, a.D, vec ? VV : 1, vec, true);
   const ResBwP p{a.h, a.x, a.scale, a.w, a.dy, a.dresidual_out, a.dx, a.dresidual, static_cast<float*>(a.workspace), a.x_ld, a.M,
-                 pick_walkers(a.M, 1, g), a.D, g.lgteam, a.w != nullptr, a.scale != nullptr, a.eps, 1.f / float(a.D)};
+                 pick_walkers(a.M, 1, g, kBackwardWaves), a.D, g.lgteam, a.w != nullptr, a.scale != nullptr, a.eps, 1.f / float(a.D)};
   const hipError_t e = launch_residual_bw<T, R>(p, g, s);
   if (e != hipSuccess || (a.w == nullptr && a.scale == nullptr)) return e;
   ColSum c{};
@@ -643,8 +731,8 @@ size_t gated_norm_backward_workspace(const m3_gated_norm_backward_args& a) {
   const m3_gated_norm_args& f = a.fwd;
   if (f.w == nullptr) return 0;
   const int V = f.in_dtype == M3_BF16 ? 8 : 4, Dg = f.D / f.G;
-  int64_t w = pick_walkers(f.M, f.G, pick(f.M * f.G, Dg, 1, false));
-  const int64_t v = pick_walkers(f.M, f.G, pick(f.M * f.G, Dg, V, true));
+  int64_t w = pick_walkers(f.M, f.G, pick(f.M * f.G, Dg, 1, false, true), kBackwardWaves);
+  const int64_t v = pick_walkers(f.M, f.G, pick(f.M * f.G, Dg, V, true, true), kBackwardWaves);
   if (v > w) w = v;
   return round256(size_t(w) * f.D * 4);
 }
@@ -657,8 +745,8 @@ hipError_t launch_residual_norm(const m3_residual_norm_args& a, hipStream_t s) {
 }
 size_t residual_norm_backward_workspace(const m3_residual_norm_backward_args& a) {
   const int V = a.in_dtype == M3_BF16 ? 8 : 4;
-  int64_t w = pick_walkers(a.M, 1, pick(a.M, a.D, 1, false));
-  const int64_t v = pick_walkers(a.M, 1, pick(a.M, a.D, V, true));
+  int64_t w = pick_walkers(a.M, 1, pick(a.M, a.D, 1, false, true), kBackwardWaves);
+  const int64_t v = pick_walkers(a.M, 1, pick(a.M, a.D, V, true, true), kBackwardWaves);
   if (v > w) w = v;
   return round256(size_t(w) * ((a.w != nullptr) + (a.scale != nullptr)) * a.D * 4);
 }
