@@ -76,20 +76,18 @@ __global__ __launch_bounds__(256) void conv_kernel(ConvP p) {
     for (int k = 0; k < W; ++k) w[k][i] = p.w[int64_t(d0 + i) * W + k];
   }
   T* y = static_cast<T*>(p.y) + int64_t(b) * p.L * p.D + d0;
-  // rows past the tile's end re-read its last row (no branch around the loads)
+  // kRows rows at a time, the next ones on their way meanwhile; rows past the
+  // tile's end re-read its last row.  No branch around loads or stores but in the
+  // last group: one would make each wait for a load wait for the stores too.
   Pack<T, V> q[kRows];
+  auto fetch = [&](int t) {
 #pragma unroll
-  for (int i = 0; i < kRows; ++i) q[i] = load_pack<T, V>(x + int64_t(t0 + i < t1 ? t0 + i : t1 - 1) * p.ld);
-  for (int t = t0; t < t1; t += kRows) {
+    for (int i = 0; i < kRows; ++i) q[i] = load_pack<T, V>(x + int64_t(t + i < t1 ? t + i : t1 - 1) * p.ld);
+  };
+  auto rows = [&](int t, bool all) {
 #pragma unroll
     for (int i = 0; i < kRows; ++i) unpack<T, V>(q[i], xs[W - 1 + i]);
-    if (t + kRows < t1) {
-#pragma unroll
-      for (int i = 0; i < kRows; ++i) {
-        const int tn = t + kRows + i;
-        q[i] = load_pack<T, V>(x + int64_t(tn < t1 ? tn : t1 - 1) * p.ld);
-      }
-    }
+    if (all) fetch(t + kRows);
 #pragma unroll
     for (int i = 0; i < kRows; ++i) {
       float o[V];
@@ -98,15 +96,23 @@ __global__ __launch_bounds__(256) void conv_kernel(ConvP p) {
         float a = bias[v];
 #pragma unroll
         for (int k = 0; k < W; ++k) a = fmaf(w[k][v], xs[i + k][v], a);
-        o[v] = p.silu ? silu_f(a) : a;
+        o[v] = a;
       }
-      if (t + i < t1) store_pack<T, V>(y + int64_t(t + i) * p.D, o);
+      if (p.silu) {
+#pragma unroll
+        for (int v = 0; v < V; ++v) o[v] = silu_f(o[v]);
+      }
+      if (all || t + i < t1) store_pack<T, V>(y + int64_t(t + i) * p.D, o);
     }
 #pragma unroll
     for (int j = 0; j < W - 1; ++j)
 #pragma unroll
       for (int v = 0; v < V; ++v) xs[j][v] = xs[j + kRows][v];
-  }
+  };
+  fetch(t0);
+  int t = t0;
+  for (; t + kRows <= t1; t += kRows) rows(t, true);
+  if (t < t1) rows(t, false);
 }
 
 struct ConvStepP {
@@ -169,8 +175,9 @@ struct ConvBwP {
 // dpre[t] = dy[t] act'(pre[t]);  dx[t] = sum_j dpre[t+j] w[W-1-j];
 // dw[k] = sum_t dpre[t] x[t-(W-1)+k];  dbias = sum_t dpre[t].
 // One thread: V channels down `tt` tokens and the W - 1 after them, whose dpre
-// its last dx need; a block is CX columns times 256 / CX tiles, whose sums of
-// dw and dbias are joined in LDS before they go to the workspace.
+// its last dx need, four at a time with the next four on their way; a block is CX
+// columns times 256 / CX tiles, whose sums of dw and dbias are joined in LDS
+// before they go to the workspace.
 template <typename T, int W, int V>
 __global__ __launch_bounds__(256) void conv_backward_kernel(ConvBwP p) {
   __shared__ float red[256 * (W + 1) * V];
@@ -181,14 +188,13 @@ __global__ __launch_bounds__(256) void conv_backward_kernel(ConvBwP p) {
   const uint32_t cv = (cb << p.lgcx) + col;
   const int t0 = (int(grp) * RY + row) * p.tt;
   const int len = item_length(p.lengths, int(b), p.L);
-  const bool on = cv < p.nv && t0 < p.L;
   const int d0 = int(cv) * V;
   float dw[W + 1][V];
 #pragma unroll
   for (int k = 0; k <= W; ++k)
 #pragma unroll
     for (int v = 0; v < V; ++v) dw[k][v] = 0.f;
-  if (on) {
+  if (cv < p.nv && t0 < p.L) {
     const T* x = static_cast<const T*>(p.x) + int64_t(b) * p.L * p.ld + d0;
     const T* dy = static_cast<const T*>(p.dy) + int64_t(b) * p.L * p.D + d0;
     T* dx = static_cast<T*>(p.dx) + int64_t(b) * p.L * p.D + d0;
@@ -204,57 +210,94 @@ __global__ __launch_bounds__(256) void conv_backward_kernel(ConvBwP p) {
       for (int k = 0; k < W; ++k) w[k][i] = p.w[int64_t(d0 + i) * W + k];
     }
     const int tend = t0 + p.tt < p.L ? t0 + p.tt : p.L;  // dx rows [t0, tend)
-    float xs[W][V], dp[W][V];
+    const int have = len > 0 ? len - 1 : 0;               // the last row with values (row 0 stands in for none)
+    // xs[j] = x[t - (W-1) + j], dp[j] = dpre[t - (W-1) + j]
+    float xs[W - 1 + kRows][V], dp[W - 1 + kRows][V];
 #pragma unroll
     for (int j = 0; j < W - 1; ++j) {
       const int t = t0 - (W - 1) + j;
 #pragma unroll
-      for (int v = 0; v < V; ++v) xs[j + 1][v] = 0.f, dp[j + 1][v] = 0.f;
+      for (int v = 0; v < V; ++v) xs[j][v] = dp[j][v] = 0.f;
       if (t >= 0) {
-        if (t < len) unpack<T, V>(load_pack<T, V>(x + int64_t(t) * p.ld), xs[j + 1]);
+        if (t < len) unpack<T, V>(load_pack<T, V>(x + int64_t(t) * p.ld), xs[j]);
       } else if (state != nullptr) {
-        unpack<T, V>(load_pack<T, V>(state + int64_t(t + W - 1) * p.D), xs[j + 1]);
+        unpack<T, V>(load_pack<T, V>(state + int64_t(t + W - 1) * p.D), xs[j]);
       }
     }
-    for (int t = t0; t < tend + W - 1; ++t) {
-      // windows move up: xs[W-1] = x[t], dp[W-1] = dpre[t]
+    Pack<T, V> qx[kRows], qd[kRows];
+    auto fetch = [&](int t) {
 #pragma unroll
-      for (int j = 0; j < W - 1; ++j)
+      for (int i = 0; i < kRows; ++i) {
+        const int64_t at = t + i < have ? t + i : have;
+        qx[i] = load_pack<T, V>(x + at * p.ld);
+        qd[i] = load_pack<T, V>(dy + at * p.D);
+      }
+    };
+    // rows t .. t + 3; inner: all of them and the dx they complete lie in the tile
+    auto rows = [&](int t, bool inner) {
 #pragma unroll
-        for (int v = 0; v < V; ++v) xs[j][v] = xs[j + 1][v], dp[j][v] = dp[j + 1][v];
-      float g[V];
+      for (int i = 0; i < kRows; ++i) {
+        unpack<T, V>(qx[i], xs[W - 1 + i]);
+        unpack<T, V>(qd[i], dp[W - 1 + i]);
+      }
+      if (t + kRows > len) {
 #pragma unroll
-      for (int v = 0; v < V; ++v) xs[W - 1][v] = 0.f, dp[W - 1][v] = 0.f;
-      if (t < len) {
-        unpack<T, V>(load_pack<T, V>(x + int64_t(t) * p.ld), xs[W - 1]);
-        unpack<T, V>(load_pack<T, V>(dy + int64_t(t) * p.D), g);
+        for (int i = 0; i < kRows; ++i)
 #pragma unroll
-        for (int v = 0; v < V; ++v) {
-          float a = bias[v];
+          for (int v = 0; v < V; ++v) {
+            xs[W - 1 + i][v] = t + i < len ? xs[W - 1 + i][v] : 0.f;
+            dp[W - 1 + i][v] = t + i < len ? dp[W - 1 + i][v] : 0.f;
+          }
+      }
+      fetch(t + kRows);
 #pragma unroll
-          for (int k = 0; k < W; ++k) a = fmaf(w[k][v], xs[k][v], a);
-          dp[W - 1][v] = p.silu ? g[v] * dsilu_f(a, sigmoid_f(a)) : g[v];
+      for (int i = 0; i < kRows; ++i) {
+        if (p.silu) {
+#pragma unroll
+          for (int v = 0; v < V; ++v) {
+            float a = bias[v];
+#pragma unroll
+            for (int k = 0; k < W; ++k) a = fmaf(w[k][v], xs[i + k][v], a);
+            dp[W - 1 + i][v] *= dsilu_f(a, sigmoid_f(a));
+          }
         }
-        if (t < tend) {
+        if (inner || t + i < tend) {
 #pragma unroll
           for (int v = 0; v < V; ++v) {
 #pragma unroll
-            for (int k = 0; k < W; ++k) dw[k][v] = fmaf(dp[W - 1][v], xs[k][v], dw[k][v]);
-            dw[W][v] += dp[W - 1][v];
+            for (int k = 0; k < W; ++k) dw[k][v] = fmaf(dp[W - 1 + i][v], xs[i + k][v], dw[k][v]);
+            dw[W][v] += dp[W - 1 + i][v];
           }
         }
-      }
-      const int q = t - (W - 1);  // dx row whose window is complete
-      float o[V];
+        float o[V];
 #pragma unroll
-      for (int v = 0; v < V; ++v) {
-        o[v] = 0.f;
+        for (int v = 0; v < V; ++v) {
+          o[v] = 0.f;
 #pragma unroll
-        for (int j = 0; j < W; ++j) o[v] = fmaf(dp[j][v], w[W - 1 - j][v], o[v]);
+          for (int j = 0; j < W; ++j) o[v] = fmaf(dp[i + j][v], w[W - 1 - j][v], o[v]);
+        }
+        const int q = t + i - (W - 1);  // the dx row that is complete now
+        if (inner) {
+          store_pack<T, V>(dx + int64_t(q) * p.D, o);
+        } else if (q >= t0) {
+          if (q < tend) store_pack<T, V>(dx + int64_t(q) * p.D, o);
+        } else if (q < 0 && dst != nullptr) {
+          store_pack<T, V>(dst + int64_t(q + W - 1) * p.D, o);
+        }
       }
-      if (q >= t0) store_pack<T, V>(dx + int64_t(q) * p.D, o);
-      else if (q < 0 && dst != nullptr) store_pack<T, V>(dst + int64_t(q + W - 1) * p.D, o);
-    }
+#pragma unroll
+      for (int j = 0; j < W - 1; ++j)
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+          xs[j][v] = xs[j + kRows][v];
+          dp[j][v] = dp[j + kRows][v];
+        }
+    };
+    fetch(t0);
+    rows(t0, false);
+    int t = t0 + kRows;
+    for (; t + kRows <= tend; t += kRows) rows(t, true);
+    for (; t < tend + W - 1; t += kRows) rows(t, false);
   }
 #pragma unroll
   for (int k = 0; k <= W; ++k)
@@ -303,12 +346,6 @@ __global__ __launch_bounds__(1024) void colsum_kernel(ColSum c) {
   }
 }
 
-// V channels per thread: a whole 16-byte word where width and addresses allow.
-template <typename T>
-constexpr int vec() {
-  return 16 / int(sizeof(T));
-}
-
 // Tokens per tile.  Long tiles read fewer rows twice (W - 1 of tt + W - 1),
 // short ones give more threads: halved while the card (256 CUs of 2048 lanes)
 // would hold fewer than a quarter of its lanes.
@@ -354,8 +391,8 @@ BwGeom bw_geom(const m3_conv_backward_args& a, int V) {
 }
 bool bw_vec(const m3_conv_backward_args& a) {
   const size_t e = a.in_dtype == M3_BF16 ? 2 : 4;
-  return rows_aligned(a.x, a.x_ld, e, 16) && rows_aligned(a.dy, a.D, e, 16) && rows_aligned(a.dx, a.D, e, 16) &&
-         rows_aligned(a.state, a.D, e, 16) && rows_aligned(a.dstate, a.D, e, 16);
+  return rows_aligned(a.x, a.x_ld, e, 4 * e) && rows_aligned(a.dy, a.D, e, 4 * e) && rows_aligned(a.dx, a.D, e, 4 * e) &&
+         rows_aligned(a.state, a.D, e, 4 * e) && rows_aligned(a.dstate, a.D, e, 4 * e);
 }
 template <typename T, int W, int V>
 hipError_t run_bw(const m3_conv_backward_args& a, hipStream_t s) {
@@ -378,12 +415,14 @@ hipError_t run_bw(const m3_conv_backward_args& a, hipStream_t s) {
   return launch_colsum(c, s);
 }
 
-#define M3_CONV_DISPATCH(FN, VECOK)                                                                              \
+// Four channels per thread in the backward, whose windows of x and dpre are twice
+// the forward's registers.
+#define M3_CONV_DISPATCH(FN, VB, VF, VECOK)                                                                              \
   const bool bf = a.in_dtype == M3_BF16;                                                                         \
   if (VECOK) {                                                                                                   \
-    if (a.W == 2) return bf ? FN<bf16_t, 2, vec<bf16_t>()>(a, s) : FN<float, 2, vec<float>()>(a, s);             \
-    if (a.W == 3) return bf ? FN<bf16_t, 3, vec<bf16_t>()>(a, s) : FN<float, 3, vec<float>()>(a, s);             \
-    return bf ? FN<bf16_t, 4, vec<bf16_t>()>(a, s) : FN<float, 4, vec<float>()>(a, s);                           \
+    if (a.W == 2) return bf ? FN<bf16_t, 2, VB>(a, s) : FN<float, 2, VF>(a, s);             \
+    if (a.W == 3) return bf ? FN<bf16_t, 3, VB>(a, s) : FN<float, 3, VF>(a, s);             \
+    return bf ? FN<bf16_t, 4, VB>(a, s) : FN<float, 4, VF>(a, s);                           \
   }                                                                                                              \
   if (a.W == 2) return bf ? FN<bf16_t, 2, 1>(a, s) : FN<float, 2, 1>(a, s);                                      \
   if (a.W == 3) return bf ? FN<bf16_t, 3, 1>(a, s) : FN<float, 3, 1>(a, s);                                      \
@@ -401,25 +440,24 @@ hipError_t launch_conv(const m3_conv_args& a, hipStream_t s) {
   const size_t e = a.in_dtype == M3_BF16 ? 2 : 4;
   const bool ok = rows_aligned(a.x, a.x_ld, e, 16) && rows_aligned(a.y, a.D, e, 16) && rows_aligned(a.state, a.D, e, 16) &&
                   rows_aligned(a.state_out, a.D, e, 16);
-  M3_CONV_DISPATCH(run_conv, ok)
+  M3_CONV_DISPATCH(run_conv, 8, 4, ok)
 }
 hipError_t launch_conv_step(const m3_conv_step_args& a, hipStream_t s) {
   const size_t e = a.in_dtype == M3_BF16 ? 2 : 4;
   const bool ok = rows_aligned(a.x, a.x_ld, e, 16) && rows_aligned(a.y, a.D, e, 16) && rows_aligned(a.state, a.D, e, 16) &&
                   rows_aligned(a.state_out, a.D, e, 16);
-  M3_CONV_DISPATCH(run_step, ok)
+  M3_CONV_DISPATCH(run_step, 8, 4, ok)
 }
 // The size covers both widths of the threads (the addresses are not known here).
 size_t conv_backward_workspace(const m3_conv_backward_args& a) {
   const int64_t cols = int64_t(a.W + 1) * a.D;
-  const int V = a.in_dtype == M3_BF16 ? 8 : 4;
   int64_t rows = bw_geom(a, 1).ngroups;
-  if (a.D % V == 0) {
-    const int64_t r = bw_geom(a, V).ngroups;
+  if (a.D % 4 == 0) {
+    const int64_t r = bw_geom(a, 4).ngroups;
     if (r > rows) rows = r;
   }
   return round256(size_t(rows) * a.Bt * cols * 4);
 }
-hipError_t launch_conv_backward(const m3_conv_backward_args& a, hipStream_t s) { M3_CONV_DISPATCH(run_bw, bw_vec(a)) }
+hipError_t launch_conv_backward(const m3_conv_backward_args& a, hipStream_t s) { M3_CONV_DISPATCH(run_bw, 4, 4, bw_vec(a)) }
 
 }  // namespace m3

@@ -559,11 +559,12 @@ __global__ __launch_bounds__(threads<BLK>()) void residual_backward_kernel(ResBw
 
 // Lanes for a unit of `width` elements: a part of a wave up to 64 words, wider
 // ones over several words per lane or several waves, the loop for what a block
-// does not hold in registers (2048 words, 16384 bf16 values).  Forward, a unit of
-// 65 to 256 words is one wave's where the units fill the card (2048 or more), a
-// block's otherwise; the backward holds four times the registers per word and
-// takes a block at once (rows of 2048 bf16, 4 words per lane of one wave: 216
-// registers and 216 us for 32768 rows; one word per lane of four: see the kernel).
+// does not hold in registers (over 2048 words, 16384 bf16 values; in the backward
+// over 1024).  Forward, a unit of 65 to 256 words is one wave's where the units
+// fill the card (2048 or more) and a block's otherwise.  The backward holds four
+// times the registers per word and takes a block at once: 32768 rows of 2048 bf16
+// take 159 us with one word per lane of four waves, and 216 us with four words per
+// lane of one wave (216 registers).
 Geom pick(int64_t units, int width, int V, bool vec, bool backward) {
   Geom g{vec, 1, 0, 6};
   const int64_t words = (int64_t(width) + V - 1) / V;
@@ -576,9 +577,9 @@ Geom pick(int64_t units, int width, int V, bool vec, bool backward) {
     g.blk = 256;
     g.nv = words <= 256 ? 1 : 2;
   } else if (words <= 1024) {
-    g.blk = backward ? 1024 : 256;
-    g.nv = backward ? 1 : 4;
-  } else if (words <= 2048) {
+    g.blk = backward ? 512 : 256;
+    g.nv = backward ? 2 : 4;
+  } else if (words <= 2048 && !backward) {
     g.blk = 1024;
     g.nv = 2;
   } else {
@@ -615,12 +616,9 @@ constexpr int64_t kForwardWaves = 8192, kBackwardWaves = 4096;
   return CALL(V, 4, 256);
 #define M3_NORM_BACKWARD_WIDTH(g, V, CALL)        \
   if ((g).blk == 0) return CALL(V, 1, 0);         \
-  if ((g).blk == 256) {                           \
-    if ((g).nv == 1) return CALL(V, 1, 256);      \
-    return CALL(V, 2, 256);                       \
-  }                                               \
-  if ((g).nv == 1) return CALL(V, 1, 1024);       \
-  return CALL(V, 2, 1024);
+  if ((g).blk == 512) return CALL(V, 2, 512);     \
+  if ((g).nv == 1) return CALL(V, 1, 256);        \
+  return CALL(V, 2, 256);
 #define M3_NORM_DISPATCH(g, VV, WIDTH, CALL) \
   if ((g).nv == 0) return CALL(1, 0, 1024);  \
   if ((g).vec) {                             \
