@@ -100,6 +100,13 @@ __device__ __forceinline__ float silu_f(float v) { return v * sigmoid_f(v); }
 // silu'(v) = g (1 + v (1 - g)), g = sigmoid(v)
 __device__ __forceinline__ float dsilu_f(float v, float g) { return g * (1.f + v * (1.f - g)); }
 
+// The block's index with neighbours on one XCD (workgroups are dealt to the 8
+// XCDs in turn), so that lines that neighbours share are fetched into one L2.
+__device__ __forceinline__ int block_on_xcd() {
+  const int n = gridDim.x, i = blockIdx.x;
+  return n % 8 == 0 ? (i & 7) * (n >> 3) + (i >> 3) : i;
+}
+
 __device__ __forceinline__ int item_length(const int32_t* lengths, int b, int L) {
   if (lengths == nullptr) return L;
   const int n = lengths[b];

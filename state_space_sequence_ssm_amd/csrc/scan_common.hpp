@@ -52,13 +52,6 @@ __device__ __forceinline__ float step_of(float raw, bool softplus, float bias, b
   return !valid ? 0.f : softplus ? softplus_fast(raw + bias) : raw;
 }
 
-// Blocks of neighbouring channels on one XCD (workgroups are dealt to the 8 XCDs
-// in turn), so that the lines they share are fetched into one L2.
-__device__ __forceinline__ int block_on_xcd() {
-  const int n = gridDim.x, i = blockIdx.x;
-  return n % 8 == 0 ? (i & 7) * (n >> 3) + (i >> 3) : i;
-}
-
 // Sums over the four lanes of a channel of four values, one left in each lane:
 // row q of 16 lanes ends with the sum of v[row_value(q)].
 __device__ __forceinline__ int row_value(int q) { return (q & 1) << 1 | q >> 1; }  // 0, 2, 1, 3
