@@ -2,7 +2,8 @@
 //
 // With do_t = dy_t silu(z_t) and g_t the gradient of the state after token t:
 //   g_t = C_t do_t + a_{t+1} g_{t+1},      a_t = exp(delta_t A)
-//   dC_t[n] = sum_d do_t h_t,   dB_t[n] = sum_d g_t u_t
+//   dC_t[n] = sum_d do_t h_t = sum_d do_t (a_t h_{t-1}) + B_t[n] sum_d do_t u_t
+//   dB_t[n] = sum_d g_t u_t
 //   dx_t = D do_t + delta_t sum_n g_t B_t
 //   ddelta_t = x_t sum_n g_t B_t + sum_n g_t (a_t h_{t-1}) A
 //   dA = sum_t g_t (a_t h_{t-1}) delta_t,   dz_t = dy_t o_t silu'(z_t)
@@ -248,10 +249,10 @@ __global__ __launch_bounds__(2 * kThreads) void states_kernel(BwP p) {
   }
 }
 
-// m ? a : b for an all-ones or all-zeros m, as one bit-field instruction (a
-// ternary of sums becomes a branch around them).
+// m ? a : b for an all-ones or all-zeros m, in one instruction: the truth table
+// of (m & a) | (~m & b).  (A ternary of sums becomes a branch around them.)
 __device__ __forceinline__ float pick(uint32_t m, float a, float b) {
-  return __uint_as_float((__float_as_uint(a) & m) | (__float_as_uint(b) & ~m));
+  return __uint_as_float(__builtin_amdgcn_bitop3_b32(m, __float_as_uint(a), __float_as_uint(b), 0xCA));
 }
 // Sum of v[0..3] over the 16 channels of a row of lanes: lane c of the row ends
 // with the sum of v[c & 3].  odd, two: all ones where c & 1, c & 2.
@@ -272,7 +273,8 @@ struct Shared {
   float dl[2][TB][CHB], us[2][TB][CHB], ds[2][TB][CHB];  // delta, u, do
   float bc[2][2][TB][NP];
   float o[2][NB][TB][CHB], gB[2][NB][TB][CHB], gA[2][NB][TB][CHB];  // sums over a block's 16 states
-  float wp[2][4 / NB][TB][2][NP];                                   // dB and dC of a wave's 16 channels
+  float wp[2][4 / NB][TB][2][NP];                                   // dB, and dC without u B^T, of a wave's 16 channels
+  float sdu[2][TB];                                                 // sum over the block's channels of do u
 };
 
 // Second walk.
@@ -377,7 +379,7 @@ __global__ __launch_bounds__(2 * kThreads) void reverse_kernel(BwP p) {
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
             const float gk = fmaf(f.C[j][k], f.go[j], gg[k]);
-            dh[k] = f.go[j] * fmaf(f.u[j], f.B[j][k], ah[tq + j][k]);
+            dh[k] = f.go[j] * ah[tq + j][k];
             gu[k] = gk * f.u[j];
             sB[j] = fmaf(gk, f.B[j][k], sB[j]);
             const float m = gk * ah[tq + j][k];
@@ -437,6 +439,10 @@ __global__ __launch_bounds__(2 * kThreads) void reverse_kernel(BwP p) {
     store_cols<T, VE, VEC>(ddtp + at, zero, true, st.ncol);
     if (dzp != nullptr) store_cols<T, VE, VEC>(dzp + at, zero, true, st.ncol);
   }
+  // this thread's four of the tile's sums of dB and dC, those past the tile repeating it
+  constexpr int kSums = TB * 2 * NP, NS = kSums > 4 * kThreads ? kSums / (4 * kThreads) : 1;
+  float* bcp = p.bc + ((int64_t(w.cb) * p.Bt + w.b) * p.in.L * p.in.G + w.g) * (2 * NP);
+  const int64_t bcrow = int64_t(p.in.G) * (2 * NP);
   // of the tile in each half: x, delta, sigmoid(dt), do, dy silu'(z)
   float kx[2][VE], kd[2][VE], ks[2][VE], kg[2][VE], kz[2][VE];
   auto stage = [&](int t0, auto half) {
@@ -481,8 +487,18 @@ __global__ __launch_bounds__(2 * kThreads) void reverse_kernel(BwP p) {
     store_pack<float, VE>(&sh.us[o][r][c0], u);
     store_pack<float, VE>(&sh.ds[o][r][c0], kg[o]);
     st.put_bc(t0, &sh.bc[o][0][0][0]);
+    // the row's sum of do u, over its 16 threads
+    float du = 0.f;
+#pragma unroll
+    for (int v = 0; v < VE; ++v) du = fmaf(kg[o][v], u[v], du);
+    du += dpp<0xB1, 0xF, true>(du);
+    du += dpp<0x4E, 0xF, true>(du);
+    du += dpp<0x141, 0xF, true>(du);
+    du += dpp<0x140, 0xF, true>(du);
+    if ((tid & 15) == 0) sh.sdu[o][r] = du;
   };
   float ox[VE], od[VE], oz[VE];
+  f32x4 obc[NS];
   auto finish = [&](auto half) {
     constexpr int o = decltype(half)::value;
     float y[VE], gB[VE], gA[VE];
@@ -507,21 +523,30 @@ __global__ __launch_bounds__(2 * kThreads) void reverse_kernel(BwP p) {
       dD[v] = fmaf(kg[o][v], kx[o][v], dD[v]);
       dbias[v] += od[v];
     }
+#pragma unroll
+    for (int q = 0; q < NS; ++q) {
+      const int e = 4 * ((tid + q * kThreads) % (kSums / 4)), t = e / (2 * NP), c = e % (2 * NP);
+      f32x4 v = *reinterpret_cast<const f32x4*>(&sh.wp[o][0][0][0][0] + e);
+#pragma unroll
+      for (int i = 1; i < 4 / NB; ++i) v += *reinterpret_cast<const f32x4*>(&sh.wp[o][i][0][0][0] + e);
+      const float m = c < NP ? 0.f : sh.sdu[o][t];
+      const f32x4 Bv = *reinterpret_cast<const f32x4*>(&sh.bc[o][0][t][c % NP]);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) v[k] = c < NP ? v[k] : fmaf(m, Bv[k], v[k]);
+      obc[q] = v;
+    }
   };
-  auto store = [&](int t0, int o) {
+  auto store = [&](int t0) {
     const bool row = t0 + r < w.tend;
     const int64_t at = int64_t(t0) * p.in.D;
     store_cols<T, VE, VEC>(dxp + at + oo, ox, row, st.ncol);
     store_cols<T, VE, VEC>(ddtp + at + oo, od, row, st.ncol);
     if (dzp != nullptr) store_cols<T, VE, VEC>(dzp + at + oo, oz, row, st.ncol);
+    float* bt = bcp + t0 * bcrow;
 #pragma unroll
-    for (int e = 4 * tid; e < TB * 2 * NP; e += 4 * kThreads) {
-      const int t = e / (2 * NP), c = e % (2 * NP);
-      f32x4 v = *reinterpret_cast<const f32x4*>(&sh.wp[o][0][0][0][0] + e);
-#pragma unroll
-      for (int i = 1; i < 4 / NB; ++i) v += *reinterpret_cast<const f32x4*>(&sh.wp[o][i][0][0][0] + e);
-      if (t0 + t < w.tend)
-        *reinterpret_cast<f32x4*>(p.bc + (((int64_t(w.cb) * p.Bt + w.b) * p.in.L + t0 + t) * p.in.G + w.g) * (2 * NP) + c) = v;
+    for (int q = 0; q < NS; ++q) {
+      const int i = tid + q * kThreads, e = 4 * i, t = e / (2 * NP), c = e % (2 * NP);
+      if (i < kSums / 4 && t0 + t < w.tend) *reinterpret_cast<f32x4*>(bt + (t * bcrow + c)) = obc[q];
     }
   };
   const std::integral_constant<int, 0> even;
@@ -533,7 +558,7 @@ __global__ __launch_bounds__(2 * kThreads) void reverse_kernel(BwP p) {
       stage(start(i + 1), other);
       st.fetch(start(i + 2));
     }
-    if (i > 0) store(start(i - 1), decltype(other)::value);
+    if (i > 0) store(start(i - 1));
     __syncthreads();
   };
   if (tiles > 0) {
@@ -549,7 +574,7 @@ __global__ __launch_bounds__(2 * kThreads) void reverse_kernel(BwP p) {
   if (tiles > 0) {
     if (tiles % 2) finish(even);
     else finish(odd);
-    store(start(tiles - 1), (tiles - 1) & 1);
+    store(start(tiles - 1));
   }
   // ---- sums over the tokens: this thread's rows, then the 16 of each column
 #pragma unroll
