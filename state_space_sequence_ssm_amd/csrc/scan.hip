@@ -19,25 +19,22 @@ struct ScanP {
   int Bt, nblk, nseg, seglen, softplus;
 };
 
-constexpr int tile(int NB) { return NB == 4 ? 16 : 32; }  // tokens per tile
+constexpr int TT = 32;  // tokens per tile
 
 // Four tokens' values of one lane, in registers.
-template <int NB, bool FULL>
+template <bool FULL>
 struct Four {
   float delta[4], u[4];
-  f32x4 B[4][NB], C[4][NB];
+  f32x4 B[4], C[4];
   // at this lane's channel of delta and u, and its states of B and C
-  template <int DS, int NP>
+  template <int CHB, int NP>
   __device__ __forceinline__ void load(const float* pd, const float* pu, const float* pB, const float* pC) {
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      delta[j] = pd[j * DS];
-      u[j] = pu[j * CH];
-#pragma unroll
-      for (int i = 0; i < NB; ++i) {
-        B[j][i] = *reinterpret_cast<const f32x4*>(pB + j * NP + 16 * i);
-        if (FULL) C[j][i] = *reinterpret_cast<const f32x4*>(pC + j * NP + 16 * i);
-      }
+      delta[j] = pd[j * CHB];
+      u[j] = pu[j * CHB];
+      B[j] = *reinterpret_cast<const f32x4*>(pB + j * NP);
+      if (FULL) C[j] = *reinterpret_cast<const f32x4*>(pC + j * NP);
     }
   }
 };
@@ -46,17 +43,20 @@ struct Four {
 // before it.  Otherwise the states and sums of delta of the segments alone.
 //
 // A block is eight waves of two kinds, one of each per SIMD: four scan, 16
-// channels each; four stage, that is, they load the next tile, form delta and u
-// and put them into the other half of LDS, and gate and store the tile before.
-// So the loads' latency and the exponentials of softplus and SiLU lie beside the
-// recurrence and not between its tiles, with one barrier per tile.
+// channels and 16 states each (64 / NB channels of NB state blocks); four stage,
+// that is, they load the next tile, form delta and u and put them into the other
+// half of LDS, and join, gate and store the y of the tile before.  So the loads'
+// latency and the exponentials of softplus and SiLU lie beside the recurrence and
+// not between its tiles, with one barrier per tile.  128 registers, so that a
+// compute unit holds two blocks where there are as many.
 template <typename T, int NB, bool VEC, bool FULL>
-__global__ __launch_bounds__(2 * kThreads) void scan_kernel(ScanP p) {
-  constexpr int TT = tile(NB), VE = TT * CH / kThreads, NP = 16 * NB, K = 4 * NB;
-  constexpr int DS = CH + 16;  // rows of delta, then of y, whose four tokens are written together: on different banks
-  __shared__ __align__(16) float dl[2][TT + 1][DS];
-  __shared__ __align__(16) float us[2][TT][CH];
-  __shared__ __align__(16) float bc[2][2][TT][NP];
+__global__ __launch_bounds__(2 * kThreads, 4) void scan_kernel(ScanP p) {
+  constexpr int CHB = CH / NB, VE = TT * CHB / kThreads, NP = 16 * NB;
+  constexpr int YS = CHB == 16 ? 16 : CHB + 16;  // the four tokens' rows written together lie on different banks
+  __shared__ __align__(16) float dl[2][TT][CHB];
+  __shared__ __align__(16) float us[2][TT][CHB];
+  __shared__ __align__(16) float bc[2][FULL ? 2 : 1][TT][NP];
+  __shared__ __align__(16) float ys[FULL ? 2 : 1][FULL ? NB : 1][FULL ? TT + 1 : 1][YS];  // row TT takes what is not wanted
 
   const int tid = threadIdx.x % kThreads;
   const bool scanner = threadIdx.x < kThreads;
@@ -72,26 +72,25 @@ __global__ __launch_bounds__(2 * kThreads) void scan_kernel(ScanP p) {
   const int tiles = tend > tbeg ? (tend - tbeg + TT - 1) / TT : 0;
 
   if (scanner) {
-    const int lane = tid & 63, s = lane >> 4, chl = (tid >> 6) * 16 + (lane & 15);
-    const int dloc = cb * CH + chl;
+    const int wave = tid >> 6, s = (tid & 63) >> 4, chl = (wave / NB) * 16 + (tid & 15);
+    const int sb = wave % NB, n0 = sb * 16 + 4 * s, nleft = p.in.N - n0;
+    const int dloc = cb * CHB + chl;
     const bool live = dloc < p.in.Dg;
     const int d = g * p.in.Dg + (live ? dloc : 0);
-    float A2[K], h[K], sum_delta = 0.f;
-    auto state = [&](int k) { return 16 * (k / 4) + 4 * s + k % 4; };
+    float A2[4], h[4], sum_delta = 0.f;
 #pragma unroll
-    for (int k = 0; k < K; ++k) {
-      const int n = state(k);
-      const bool on = live && n < p.in.N;
-      A2[k] = on ? p.A[int64_t(d) * p.in.N + n] * kLog2e : 0.f;
-      h[k] = on && p.h0 != nullptr && (FULL || seg == 0) ? p.h0[(int64_t(b) * p.in.D + d) * p.in.N + n] : 0.f;
+    for (int k = 0; k < 4; ++k) {
+      const bool on = live && k < nleft;
+      A2[k] = on ? p.A[int64_t(d) * p.in.N + n0 + k] * kLog2e : 0.f;
+      h[k] = on && p.h0 != nullptr && (FULL || seg == 0) ? p.h0[(int64_t(b) * p.in.D + d) * p.in.N + n0 + k] : 0.f;
     }
     if constexpr (FULL) {
       for (int q = 0; q < seg; ++q) {
         const int64_t at = (int64_t(q) * p.Bt + b) * p.in.D + d;
         const float sd = p.sdel[at];
 #pragma unroll
-        for (int k = 0; k < K; ++k) {
-          const float e = state(k) < p.in.N ? p.hend[at * p.in.N + state(k)] : 0.f;
+        for (int k = 0; k < 4; ++k) {
+          const float e = k < nleft ? p.hend[at * p.in.N + n0 + k] : 0.f;
           h[k] = q == 0 ? e : fmaf(decay(sd, A2[k]), h[k], e);
         }
       }
@@ -99,76 +98,73 @@ __global__ __launch_bounds__(2 * kThreads) void scan_kernel(ScanP p) {
     __syncthreads();
     for (int t = 0; t < tiles; ++t) {
       const int left = tend - tbeg - t * TT, o = t & 1;
-      float* pd = &dl[o][0][chl];
+      const float* pd = &dl[o][0][chl];
       const float* pu = &us[o][0][chl];
-      const float* pB = &bc[o][0][0][4 * s];
-      const float* pC = &bc[o][1][0][4 * s];
-      // four tokens at a time, the next four on their way from LDS meanwhile; two
+      const float* pB = &bc[o][0][0][n0];
+      const float* pC = &bc[o][FULL ? 1 : 0][0][n0];
+      float* py = &ys[FULL ? o : 0][FULL ? sb : 0][0][chl];
+      // Four tokens at a time, the next four on their way from LDS meanwhile; two
       // register sets in turn.  Tokens past the end have delta = u = B = C = 0 and
-      // leave the state alone.  y takes the place of its channel's delta.
-      // The sums over states of four tokens wait for the next four's exponentials,
-      // which cover their latency; row TT takes those in front of the first.
+      // leave the state alone.  Decays and inputs of the four come ahead of their
+      // recurrence: independent work that covers the exponentials' latency and that
+      // of the sums over states of the four tokens before.
       float y[4] = {0.f, 0.f, 0.f, 0.f};
-      auto four = [&](int to, const Four<NB, FULL>& q) {
-        constexpr int AT = 4 / NB;
-        if constexpr (FULL) pd[to * DS] = rows_sum4(y);
+      auto four = [&](int to, const Four<FULL>& q) {
+        float a[4][4], w[4][4];
+        if constexpr (FULL) py[to * YS] = rows_sum4(y);
 #pragma unroll
-        for (int j0 = 0; j0 < 4; j0 += AT) {
-          float a[AT][K], w[AT][K];
+        for (int j = 0; j < 4; ++j)
 #pragma unroll
-          for (int j = 0; j < AT; ++j)
-#pragma unroll
-            for (int k = 0; k < K; ++k) {
-              a[j][k] = decay(q.delta[j0 + j], A2[k]);
-              w[j][k] = q.u[j0 + j] * q.B[j0 + j][k / 4][k % 4];
-            }
-          __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-          for (int j = 0; j < AT; ++j) {
-            y[j0 + j] = 0.f;
-#pragma unroll
-            for (int k = 0; k < K; ++k) {
-              h[k] = fmaf(a[j][k], h[k], w[j][k]);
-              if (FULL) y[j0 + j] = fmaf(q.C[j0 + j][k / 4][k % 4], h[k], y[j0 + j]);
-            }
-            if (!FULL) sum_delta += q.delta[j0 + j];
+          for (int k = 0; k < 4; ++k) {
+            a[j][k] = decay(q.delta[j], A2[k]);
+            w[j][k] = q.u[j] * q.B[j][k];
           }
-          __builtin_amdgcn_sched_barrier(0);
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          y[j] = 0.f;
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            h[k] = fmaf(a[j][k], h[k], w[j][k]);
+            if (FULL) y[j] = fmaf(q.C[j][k], h[k], y[j]);
+          }
+          if (!FULL) sum_delta += q.delta[j];
         }
+        __builtin_amdgcn_sched_barrier(0);
       };
       const int nt = left < TT ? (left + 7) & ~7 : TT;
       const int rv = row_value(s);
-      Four<NB, FULL> q0, q1;
-      q0.template load<DS, NP>(pd, pu, pB, pC);
+      Four<FULL> q0, q1;
+      q0.template load<CHB, NP>(pd, pu, pB, pC);
 #pragma unroll
       for (int tq = 0; tq < TT; tq += 8) {
         if (tq >= nt) break;
-        q1.template load<DS, NP>(pd + (tq + 4) * DS, pu + (tq + 4) * CH, pB + (tq + 4) * NP, pC + (tq + 4) * NP);
+        q1.template load<CHB, NP>(pd + (tq + 4) * CHB, pu + (tq + 4) * CHB, pB + (tq + 4) * NP, pC + (tq + 4) * NP);
         four(tq > 0 ? tq - 4 + rv : TT, q0);
         const int tn = tq + 8 < TT ? tq + 8 : tq;
-        q0.template load<DS, NP>(pd + tn * DS, pu + tn * CH, pB + tn * NP, pC + tn * NP);
+        q0.template load<CHB, NP>(pd + tn * CHB, pu + tn * CHB, pB + tn * NP, pC + tn * NP);
         four(tq + rv, q1);
       }
-      if constexpr (FULL) pd[(nt - 4 + rv) * DS] = rows_sum4(y);
+      if constexpr (FULL) py[(nt - 4 + rv) * YS] = rows_sum4(y);
       __syncthreads();
     }
     if (!live) return;
     if constexpr (FULL) {
       if (p.hfin == nullptr || seg != p.nseg - 1) return;
 #pragma unroll
-      for (int k = 0; k < K; ++k)
-        if (state(k) < p.in.N) p.hfin[(int64_t(b) * p.in.D + d) * p.in.N + state(k)] = h[k];
+      for (int k = 0; k < 4; ++k)
+        if (k < nleft) p.hfin[(int64_t(b) * p.in.D + d) * p.in.N + n0 + k] = h[k];
     } else {
       const int64_t at = (int64_t(seg) * p.Bt + b) * p.in.D + d;
 #pragma unroll
-      for (int k = 0; k < K; ++k)
-        if (state(k) < p.in.N) p.hend[at * p.in.N + state(k)] = h[k];
-      if (s == 0) p.sdel[at] = sum_delta;
+      for (int k = 0; k < 4; ++k)
+        if (k < nleft) p.hend[at * p.in.N + n0 + k] = h[k];
+      if (s == 0 && sb == 0) p.sdel[at] = sum_delta;
     }
     return;
   }
 
-  Stager<T, TT, CH, NP, VEC, FULL, false, FULL> st;
+  Stager<T, TT, CHB, NP, VEC, FULL, false, FULL> st;
   st.init(p.in, b, g, cb, tid, tend);
   const int r = st.r, c0 = st.c0;
   T* yp = FULL ? static_cast<T*>(p.y) + int64_t(b) * p.in.L * p.in.D + g * p.in.Dg : nullptr;
@@ -216,20 +212,24 @@ __global__ __launch_bounds__(2 * kThreads) void scan_kernel(ScanP p) {
     store_pack<float, VE>(&us[o][r][c0], u);
     st.put_bc(t0, &bc[o][0][0][0]);
   };
-  // y of a tile, read from where this thread put delta (and puts the next one's)
   float out[VE];
   auto finish = [&](auto half) {
     constexpr int o = decltype(half)::value;
-    unpack<float, VE>(load_pack<float, VE>(&dl[o][r][c0]), out);
+    unpack<float, VE>(load_pack<float, VE>(&ys[o][0][r][c0]), out);
 #pragma unroll
-    for (int v = 0; v < VE; ++v) {
-      out[v] = (out[v] + skip[o][v]) * gate[o][v];
+    for (int i = 1; i < NB; ++i) {
+      const Pack<float, VE> q = load_pack<float, VE>(&ys[o][i][r][c0]);
+#pragma unroll
+      for (int v = 0; v < VE; ++v) out[v] += q.e[v];
     }
+#pragma unroll
+    for (int v = 0; v < VE; ++v) out[v] = (out[v] + skip[o][v]) * gate[o][v];
   };
   auto store = [&](int t0) { store_cols<T, VE, VEC>(yp + int64_t(t0) * p.in.D + (uint32_t(r) * uint32_t(p.in.D) + st.cin), out, t0 + r < tend, st.ncol); };
   auto step = [&](int i, auto half, auto other) {
     const int t0 = tbeg + i * TT;
-    if (FULL && i > 0) finish(other);
+    if constexpr (FULL)
+      if (i > 0) finish(other);
     if (i + 1 < tiles) {
       stage(t0 + TT, other);
       st.fetch(t0 + 2 * TT);
@@ -250,7 +250,8 @@ __global__ __launch_bounds__(2 * kThreads) void scan_kernel(ScanP p) {
     step(i, even, odd);
     if (i + 1 < tiles) step(i + 1, odd, even);
   }
-  if (FULL && tiles > 0) {
+  if constexpr (FULL) {
+    if (tiles == 0) return;
     if (tiles % 2) finish(even);
     else finish(odd);
     store(tbeg + (tiles - 1) * TT);
@@ -270,7 +271,7 @@ struct StepP {
   const float* h;
   float* hout;
   void* y;
-  int Bt, D, N, G, Dg, softplus, nb;
+  int Bt, D, N, Dg, softplus, nblk;
 };
 
 // Sum over S neighbouring lanes, in each of them.
@@ -283,52 +284,61 @@ __device__ __forceinline__ float lanes_sum(float v) {
   return v;
 }
 
-// One token: S lanes per (item, channel), 4 states each in one 16-byte word;
-// the state is read and written once, everything else is small beside it.
-template <typename T, int S, bool VEC>
+// One token: S lanes per channel, 4 states each in one 16-byte word, for NI items
+// whose loads are started together; the state is read and written once,
+// everything else is small beside it.
+template <typename T, int S, int NI, bool VEC>
 __global__ __launch_bounds__(kThreads) void scan_step_kernel(StepP p) {
-  const int s = threadIdx.x % S;
-  const int64_t unit = (int64_t(blockIdx.x) * kThreads + threadIdx.x) / S;
-  const int b = int(unit / p.D), d = int(unit - int64_t(b) * p.D);
-  if (b >= p.Bt) return;
-  const int g = d / p.Dg, n0 = 4 * s;
-  const int64_t at = unit * p.N + n0;
-  Pack<float, 4> h{}, A{};
-  Pack<T, 4> B{}, C{};
-  const T* Bp = static_cast<const T*>(p.B) + int64_t(b) * p.Bld + int64_t(g) * p.N + n0;
-  const T* Cp = static_cast<const T*>(p.C) + int64_t(b) * p.Cld + int64_t(g) * p.N + n0;
-  if (n0 < p.N) {
-    if constexpr (VEC) {
-      h = load_pack<float, 4>(p.h + at);
-      A = load_pack<float, 4>(p.A + int64_t(d) * p.N + n0);
-      B = load_pack<T, 4>(Bp);
-      C = load_pack<T, 4>(Cp);
-    } else {
-      h = load_some<float, 4>(p.h + at, p.N - n0);
-      A = load_some<float, 4>(p.A + int64_t(d) * p.N + n0, p.N - n0);
-      B = load_some<T, 4>(Bp, p.N - n0);
-      C = load_some<T, 4>(Cp, p.N - n0);
+  const int s = threadIdx.x % S, n0 = 4 * s;
+  const int d = (int(blockIdx.x % uint32_t(p.nblk)) * kThreads + int(threadIdx.x)) / S;
+  const int b0 = int(blockIdx.x / uint32_t(p.nblk)) * NI;
+  if (d >= p.D) return;
+  const bool on = n0 < p.N;
+  const int g = d / p.Dg, ns = on ? n0 : 0, left = p.N - n0;  // lanes without states read the first ones
+  auto quad = [&](auto* q) {
+    using E = std::remove_const_t<std::remove_pointer_t<decltype(q)>>;
+    if constexpr (VEC) return load_pack<E, 4>(q);
+    else return load_some<E, 4>(q, left);
+  };
+  const Pack<float, 4> A = quad(p.A + int64_t(d) * p.N + ns);
+  Pack<float, 4> h[NI];
+  Pack<T, 4> B[NI], C[NI];
+  T x[NI], dt[NI], z[NI];
+#pragma unroll
+  for (int i = 0; i < NI; ++i) {
+    const int b = b0 + i < p.Bt ? b0 + i : p.Bt - 1;
+    h[i] = quad(p.h + (int64_t(b) * p.D + d) * p.N + ns);
+    B[i] = quad(static_cast<const T*>(p.B) + int64_t(b) * p.Bld + int64_t(g) * p.N + ns);
+    C[i] = quad(static_cast<const T*>(p.C) + int64_t(b) * p.Cld + int64_t(g) * p.N + ns);
+    x[i] = static_cast<const T*>(p.x)[int64_t(b) * p.xld + d];
+    dt[i] = static_cast<const T*>(p.dt)[int64_t(b) * p.dtld + d];
+    z[i] = p.z != nullptr ? static_cast<const T*>(p.z)[int64_t(b) * p.zld + d] : T{};
+  }
+  const float bias = p.dtb != nullptr ? p.dtb[d] : 0.f, dsk = p.Dsk != nullptr ? p.Dsk[d] : 0.f;
+#pragma unroll
+  for (int i = 0; i < NI; ++i) {
+    const int b = b0 + i;
+    const float xv = to_f32(x[i]);
+    const float delta = p.softplus ? softplus_fast(to_f32(dt[i]) + bias) : to_f32(dt[i]);
+    float o = 0.f, hn[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      hn[k] = fmaf(decay(delta, A.e[k] * kLog2e), h[i].e[k], delta * xv * to_f32(B[i].e[k]));
+      o = fmaf(to_f32(C[i].e[k]), hn[k], o);
+    }
+    o = lanes_sum<S>(on ? o : 0.f);
+    if (b >= p.Bt) break;
+    if (on) {
+      float* ho = p.hout + (int64_t(b) * p.D + d) * p.N + n0;
+      if constexpr (VEC) store_pack<float, 4>(ho, hn);
+      else store_some<float, 4>(ho, hn, left);
+    }
+    if (s == 0) {
+      o = fmaf(dsk, xv, o);
+      if (p.z != nullptr) o *= silu_f(to_f32(z[i]));
+      from_f32(o, static_cast<T*>(p.y)[int64_t(b) * p.D + d]);
     }
   }
-  const float x = to_f32(static_cast<const T*>(p.x)[int64_t(b) * p.xld + d]);
-  const float raw = to_f32(static_cast<const T*>(p.dt)[int64_t(b) * p.dtld + d]);
-  const float delta = step_of(raw, p.softplus != 0, p.dtb != nullptr ? p.dtb[d] : 0.f, true);
-  const float u = delta * x;
-  float o = 0.f, hn[4];
-#pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    hn[k] = fmaf(decay(delta, A.e[k] * kLog2e), h.e[k], u * to_f32(B.e[k]));
-    o = fmaf(to_f32(C.e[k]), hn[k], o);
-  }
-  if (n0 < p.N) {
-    if constexpr (VEC) store_pack<float, 4>(p.hout + at, hn);
-    else store_some<float, 4>(p.hout + at, hn, p.N - n0);
-  }
-  o = lanes_sum<S>(o);
-  if (s != 0) return;
-  if (p.Dsk != nullptr) o = fmaf(p.Dsk[d], x, o);
-  if (p.z != nullptr) o *= silu_f(to_f32(static_cast<const T*>(p.z)[int64_t(b) * p.zld + d]));
-  from_f32(o, static_cast<T*>(p.y)[unit]);
 }
 
 struct Plan {
@@ -339,7 +349,7 @@ struct Plan {
 Plan plan_of(const m3_scan_args& a) {
   Plan p;
   p.NB = state_blocks(a.N);
-  p.nblk = blocks_per_group(a.D / a.G);
+  p.nblk = blocks_per_group(a.D / a.G, p.NB);
   p.nseg = 1;
   p.seglen = a.L;
   const int64_t blocks = int64_t(a.Bt) * a.G * p.nblk;
@@ -369,13 +379,19 @@ hipError_t run(const m3_scan_args& a, Plan pl, hipStream_t st) {
   scan_kernel<T, NB, VEC, true><<<uint32_t(per * pl.nseg), 2 * kThreads, 0, st>>>(p);
   return hipGetLastError();
 }
-template <typename T, int S, bool VEC>
+template <typename T, int S, int NI, bool VEC>
 hipError_t run_step(const m3_scan_step_args& a, hipStream_t st) {
+  const int64_t nblk = (int64_t(a.D) * S + kThreads - 1) / kThreads;
   const StepP p{a.x, a.dt, a.z, a.B, a.C, a.x_ld, a.dt_ld, a.z_ld, a.B_ld, a.C_ld, a.A, a.D_skip, a.dt_bias, a.h, a.h_out, a.y,
-                a.Bt, a.D, a.N, a.G, a.D / a.G, a.dt_softplus, 1};
-  const int64_t lanes = int64_t(a.Bt) * a.D * S;
-  scan_step_kernel<T, S, VEC><<<uint32_t((lanes + kThreads - 1) / kThreads), kThreads, 0, st>>>(p);
+                a.Bt, a.D, a.N, a.D / a.G, a.dt_softplus, int(nblk)};
+  scan_step_kernel<T, S, NI, VEC><<<uint32_t(nblk * ((int64_t(a.Bt) + NI - 1) / NI)), kThreads, 0, st>>>(p);
   return hipGetLastError();
+}
+// Several items per lane once the lanes would fill the card twice (256 CUs of 2048).
+template <typename T, int S, bool VEC>
+hipError_t step_items(const m3_scan_step_args& a, hipStream_t st) {
+  if (int64_t(a.Bt) * a.D * S >= 1 << 20) return run_step<T, S, 4, VEC>(a, st);
+  return run_step<T, S, 1, VEC>(a, st);
 }
 
 template <typename T, bool VEC>
@@ -385,10 +401,10 @@ hipError_t by_states(const m3_scan_args& a, const Plan& p, hipStream_t st) {
 }
 template <typename T, bool VEC>
 hipError_t step_by_lanes(const m3_scan_step_args& a, hipStream_t st) {
-  if (a.N <= 4) return run_step<T, 1, VEC>(a, st);
-  if (a.N <= 8) return run_step<T, 2, VEC>(a, st);
-  if (a.N <= 16) return run_step<T, 4, VEC>(a, st);
-  return a.N <= 32 ? run_step<T, 8, VEC>(a, st) : run_step<T, 16, VEC>(a, st);
+  if (a.N <= 4) return step_items<T, 1, VEC>(a, st);
+  if (a.N <= 8) return step_items<T, 2, VEC>(a, st);
+  if (a.N <= 16) return step_items<T, 4, VEC>(a, st);
+  return a.N <= 32 ? step_items<T, 8, VEC>(a, st) : step_items<T, 16, VEC>(a, st);
 }
 
 }  // namespace
@@ -401,13 +417,11 @@ size_t scan_workspace(const m3_scan_args& a) {
 hipError_t launch_scan(const m3_scan_args& a, hipStream_t s) {
   const bool bf = a.in_dtype == M3_BF16;
   const size_t e = bf ? 2 : 4;
-  // a staging thread's channels, and four values of B or C, as whole words
   const scan::Plan p = scan::plan_of(a);
-  const int ve = scan::tile(p.NB) * scan::CH / scan::kThreads;
-  const size_t word = e * ve < 16 ? e * ve : 16;
-  const bool vec = (a.D / a.G) % ve == 0 && rows_aligned(a.x, a.x_ld, e, word) && rows_aligned(a.dt, a.dt_ld, e, word) &&
-                   rows_aligned(a.z, a.z_ld, e, word) && rows_aligned(a.y, a.D, e, word) &&
-                   a.N % 4 == 0 && rows_aligned(a.B, a.B_ld, e, 4 * e) && rows_aligned(a.C, a.C_ld, e, 4 * e);
+  // four channels, and four values of B or C, as whole words
+  const bool vec = (a.D / a.G) % 4 == 0 && a.N % 4 == 0 && rows_aligned(a.x, a.x_ld, e, 4 * e) &&
+                   rows_aligned(a.dt, a.dt_ld, e, 4 * e) && rows_aligned(a.z, a.z_ld, e, 4 * e) && rows_aligned(a.y, a.D, e, 4 * e) &&
+                   rows_aligned(a.B, a.B_ld, e, 4 * e) && rows_aligned(a.C, a.C_ld, e, 4 * e);
   if (bf) return vec ? scan::by_states<bf16_t, true>(a, p, s) : scan::by_states<bf16_t, false>(a, p, s);
   return vec ? scan::by_states<float, true>(a, p, s) : scan::by_states<float, false>(a, p, s);
 }

@@ -625,7 +625,7 @@ Plan plan_of(const m3_scan_args& f) {
   Plan p;
   p.NB = state_blocks(f.N);
   const int CHB = CH / p.NB, NP = 16 * p.NB;
-  p.nblk = (f.D / f.G + CHB - 1) / CHB;
+  p.nblk = blocks_per_group(f.D / f.G, p.NB);
   p.blocks = int64_t(f.Bt) * f.G * p.nblk;
   p.nseg = 1;
   p.seglen = (f.L + 31) / 32 * 32;
@@ -703,12 +703,10 @@ hipError_t launch_scan_backward(const m3_scan_backward_args& a, hipStream_t s) {
   const bool bf = f.in_dtype == M3_BF16;
   const size_t e = bf ? 2 : 4;
   const scan::Plan p = scan::plan_of(f);
-  // the first walk's staging threads take the wider words
-  const int ve = 8 / p.NB;
-  const size_t word = e * ve < 16 ? e * ve : 16;
-  const bool vec = (f.D / f.G) % ve == 0 && rows_aligned(f.x, f.x_ld, e, word) && rows_aligned(f.dt, f.dt_ld, e, word) &&
-                   rows_aligned(f.z, f.z_ld, e, word) && rows_aligned(a.dy, f.D, e, word) && rows_aligned(a.dx, f.D, e, word) &&
-                   rows_aligned(a.ddt, f.D, e, word) && rows_aligned(a.dz, f.D, e, word) && f.N % 4 == 0 &&
+  // four channels, and four values of B or C, as whole words
+  const bool vec = (f.D / f.G) % 4 == 0 && f.N % 4 == 0 && rows_aligned(f.x, f.x_ld, e, 4 * e) &&
+                   rows_aligned(f.dt, f.dt_ld, e, 4 * e) && rows_aligned(f.z, f.z_ld, e, 4 * e) && rows_aligned(a.dy, f.D, e, 4 * e) &&
+                   rows_aligned(a.dx, f.D, e, 4 * e) && rows_aligned(a.ddt, f.D, e, 4 * e) && rows_aligned(a.dz, f.D, e, 4 * e) &&
                    rows_aligned(f.B, f.B_ld, e, 4 * e) && rows_aligned(f.C, f.C_ld, e, 4 * e);
   if (bf) return vec ? scan::by_states<bf16_t, true>(a, p, s) : scan::by_states<bf16_t, false>(a, p, s);
   return vec ? scan::by_states<float, true>(a, p, s) : scan::by_states<float, false>(a, p, s);

@@ -8,9 +8,9 @@
 // exponential and a multiply-add, and one more multiply-add for the readout.  So
 // the vector ALUs bound it, the exponentials (half rate) for two fifths.
 //
-// A wave holds 16 channels, lane = 16 s + channel, with the states 16 i + 4 s ..
-// + 3 (i < NB) of its channel in registers: a token's sum over the states of
-// four tokens takes three lane swaps and three additions.  What is shared by a
+// A wave holds 16 channels and a block of 16 states, lane = 16 s + channel with the
+// states 4 s .. + 3: the sums over the states of four tokens take three lane swaps
+// and three additions.  What is shared by a
 // channel's lanes (delta, u, the gate) or by all channels (B, C) is computed or
 // converted once per tile and passed on in LDS.  (This is also the layout of a
 // 16 x 16 fp32 matrix product's result; forming u_t B_t^T on the matrix cores
@@ -63,26 +63,40 @@ __device__ __forceinline__ float rows_sum4(const float* v) {
   const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(lo), __float_as_uint(hi), false, false);
   return __uint_as_float(r[0]) + __uint_as_float(r[1]);
 }
-// VE neighbouring values.  The loads of a tile have no branch around them (a
-// branch makes the compiler wait for the values at its end): rows and columns
-// past the edge are read from the nearest ones inside and dropped later.
+// VE neighbouring values, `ncol` of them inside (any number; at least one word for
+// a load), in words of four (VEC) or one at a time.  The loads have no branch
+// around them (a branch makes the compiler wait for the values at its end): words
+// past the edge are read from the first one and dropped later.
+template <int VE, bool VEC>
+constexpr int word() {
+  return !VEC ? 1 : VE < 4 ? VE : 4;
+}
 template <typename T, int VE, bool VEC>
 __device__ __forceinline__ Pack<T, VE> fetch_cols(const T* p, int ncol) {
-  if constexpr (VEC) return load_pack<T, VE>(p);
+  constexpr int VW = word<VE, VEC>();
   Pack<T, VE> q;
 #pragma unroll
-  for (int v = 0; v < VE; ++v) q.e[v] = p[v < ncol ? v : ncol - 1];
+  for (int v = 0; v < VE; v += VW) {
+    const Pack<T, VW> o = load_pack<T, VW>(p + (v < ncol ? v : 0));
+#pragma unroll
+    for (int i = 0; i < VW; ++i) q.e[v + i] = o.e[i];
+  }
   return q;
 }
 template <typename T, int VE, bool VEC>
 __device__ __forceinline__ void store_cols(T* p, const float* v, bool row, int ncol) {
-  if constexpr (VEC) {
-    if (row && ncol > 0) store_pack<T, VE>(p, v);
-  } else {
-    if (row) store_some<T, VE>(p, v, ncol);
+  constexpr int VW = word<VE, VEC>();
+  if (row && VE <= ncol) {
+    if constexpr (VW > 1 || VE == 1) {
+#pragma unroll
+      for (int i = 0; i < VE; i += VW) store_pack<T, VW>(p + i, v + i);
+      return;
+    }
   }
+#pragma unroll
+  for (int i = 0; i < VE; i += VW)
+    if (row && i < ncol) store_pack<T, VW>(p + i, v + i);
 }
-
 // The tensors of a call as the kernels take them.
 struct Inputs {
   const void* x;
@@ -107,7 +121,7 @@ struct Stager {
   static constexpr int kQuads = (CC ? 2 : 1) * TT * NP / 4, NQ = (kQuads + kThreads - 1) / kThreads;
   const T *x, *dt, *z, *dy, *B, *C;
   int64_t xld, dtld, zld, dyld, Bld, Cld;
-  int r, c0, ncol, nin, cin, tend, N;
+  int r, c0, ncol, cin, tend, N;
   int qt[NQ], qn[NQ];
   bool qc[NQ], gated;
   uint32_t ox, odt, oz, ody, oq[NQ];
@@ -118,9 +132,8 @@ struct Stager {
     r = tid / (CHB / VE);
     c0 = (tid % (CHB / VE)) * VE;
     const int left = p.Dg - (cb * CHB + c0);
-    ncol = left < VE ? left : VE;  // to be stored: none past the group
+    ncol = left < VE ? left : VE;  // channels inside: none past the group
     cin = ncol > 0 ? cb * CHB + c0 : 0;
-    nin = ncol > 0 ? ncol : 1;  // to be read
     tend = end;
     N = p.N;
     gated = p.z != nullptr;
@@ -165,14 +178,13 @@ struct Stager {
 #pragma unroll
     for (int i = 0; i < NQ; ++i) pq[i] = oq[i];
     if (tend - 1 - tb < TT - 1) place(int(tend - 1 - tb), px, pdt, pz, pdy, pq);
-    qx = fetch_cols<T, VE, VEC>(x + tb * xld + px, nin);
-    qd = fetch_cols<T, VE, VEC>(dt + tb * dtld + pdt, nin);
-    if constexpr (Z) qz = fetch_cols<T, VE, VEC>(z + tb * zld + pz, nin);
-    if constexpr (DY) qy = fetch_cols<T, VE, VEC>(dy + tb * dyld + pdy, nin);
+    qx = fetch_cols<T, VE, VEC>(x + tb * xld + px, ncol);
+    qd = fetch_cols<T, VE, VEC>(dt + tb * dtld + pdt, ncol);
+    if constexpr (Z) qz = fetch_cols<T, VE, VEC>(z + tb * zld + pz, ncol);
+    if constexpr (DY) qy = fetch_cols<T, VE, VEC>(dy + tb * dyld + pdy, ncol);
 #pragma unroll
     for (int i = 0; i < NQ; ++i) {
-      const int n = N - qn[i] < 1 ? 1 : N - qn[i];
-      qb[i] = fetch_cols<T, 4, VEC>((qc[i] ? C + tb * Cld : B + tb * Bld) + pq[i], n);
+      qb[i] = fetch_cols<T, 4, VEC>((qc[i] ? C + tb * Cld : B + tb * Bld) + pq[i], N - qn[i]);
     }
   }
   // B and C of the fetched tile to LDS [2][TT][NP]; zeros past the end and past N
@@ -194,9 +206,9 @@ struct Stager {
 };
 
 // Blocks of channels never straddle two groups.
-constexpr int CH = 64;  // channels of a block: 16 for each of its four scanning waves
+constexpr int CH = 64;  // channels of a block with one state block: 16 for each of its four scanning waves
 inline int state_blocks(int N) { return N <= 16 ? 1 : N <= 32 ? 2 : 4; }  // of 16 states
-inline int blocks_per_group(int Dg) { return (Dg + CH - 1) / CH; }
+inline int blocks_per_group(int Dg, int NB) { return (Dg + CH / NB - 1) / (CH / NB); }
 
 }  // namespace scan
 }  // namespace m3
