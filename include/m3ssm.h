@@ -466,7 +466,8 @@ int m3_causal_conv_backward(const m3_conv_backward_args* args, void* stream);
  * workspace: optional; with few (batch, channel) pairs the token axis is cut
  * into segments scanned at once, whose states are joined, when a workspace of
  * m3_selective_scan_workspace_size bytes (256-byte aligned; 0: not used) is
- * given.  It is overwritten by every call; the size depends on the shape. */
+ * given.  It is overwritten by every call, so calls at once need their own; the
+ * size depends on the sizes and on whether lengths is given. */
 typedef struct m3_scan_args {
   int32_t Bt, L, D, N, G;
   int32_t in_dtype;

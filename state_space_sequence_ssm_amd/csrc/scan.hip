@@ -344,8 +344,15 @@ __global__ __launch_bounds__(kThreads) void scan_step_kernel(StepP p) {
 struct Plan {
   int NB, nblk, nseg, seglen;
 };
-// Segments of the token axis: with fewer blocks than two per compute unit the
-// axis is cut, at least 128 tokens to a segment.
+// Segments of the token axis.  A cut costs a second pass over nearly all tokens
+// (states alone, two thirds of the work), so it pays where the blocks leave
+// enough of the 256 compute units idle: L 4096, D 2048, N 16 bf16 with 128 blocks
+// 230 us cut and 289 us not, with 192 blocks 371 us and 290 us.  Then two blocks
+// per unit (1 item of 16384 tokens: 270 us, with four 290 us, with one 282 us),
+// but four where the items' lengths differ and blocks behind them have nothing to
+// do (5 items of 0 to 1537 tokens, 160 blocks: 85 us, with two 100 us, uncut 114
+// us); 64 tokens to a segment
+// at least (512 tokens: 24 us, with 128 29 us).
 Plan plan_of(const m3_scan_args& a) {
   Plan p;
   p.NB = state_blocks(a.N);
@@ -353,9 +360,9 @@ Plan plan_of(const m3_scan_args& a) {
   p.nseg = 1;
   p.seglen = a.L;
   const int64_t blocks = int64_t(a.Bt) * a.G * p.nblk;
-  if (blocks >= 256) return p;
-  int64_t n = (512 + blocks - 1) / blocks;
-  if (n > a.L / 128) n = a.L / 128;
+  if (blocks >= (a.lengths != nullptr ? 256 : 160)) return p;
+  int64_t n = ((a.lengths != nullptr ? 1024 : 512) + blocks - 1) / blocks;
+  if (n > a.L / 64) n = a.L / 64;
   if (n < 2) return p;
   p.seglen = int(((a.L + n - 1) / n + 31) / 32 * 32);
   p.nseg = (a.L + p.seglen - 1) / p.seglen;
