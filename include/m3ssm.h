@@ -386,6 +386,8 @@ int m3_rope_angles_cumsum(const float* theta, const float* phi0, float* phi,
  *     of inputs behind them are set to zero, states end with the last token
  *     held (lengths[b] = 0: the state passes through).
  *   - Outputs do not alias inputs or each other, except where noted.
+ *   - Sizes: Bt D and M below 2^31, 2^35 elements of one tensor, L and D up to
+ *     2^28; larger ones are M3_ERR_UNSUPPORTED.
  */
 
 /* Short causal depthwise convolution over the token axis:
@@ -462,7 +464,7 @@ int m3_causal_conv_backward(const m3_conv_backward_args* args, void* stream);
  *   x, dt, z [Bt, L, D] (x_ld, dt_ld, z_ld), B, C [Bt, L, G, N] (B_ld, C_ld),
  *   A [D, N], D_skip [D] or NULL; h0 [Bt, D, N] or NULL (zeros); y [Bt, L, D];
  *   h_final [Bt, D, N] (nullable).
- * Sizes: N in 1..64, G divides D.
+ * Sizes: N in 1..64, G divides D, row distances below 2^24 elements.
  * workspace: optional; with few (batch, channel) pairs the token axis is cut
  * into segments scanned at once, whose states are joined, when a workspace of
  * m3_selective_scan_workspace_size bytes (256-byte aligned; 0: not used) is
@@ -546,7 +548,7 @@ typedef struct m3_scan_backward_args {
 size_t m3_selective_scan_backward_workspace_size(const m3_scan_backward_args* args);
 int m3_selective_scan_backward(const m3_scan_backward_args* args, void* stream);
 
-/* Gated group RMS norm over rows of D = G groups of D / G:
+/* Gated group RMS norm over rows of D = G groups (up to 2^20) of D / G:
  *   gate_first = 1: v = x silu(z),  y = v rsqrt(mean_group(v^2) + eps) w;
  *   gate_first = 0: y = x rsqrt(mean_group(x^2) + eps) w silu(z).
  * x, z [M, D] (x_ld, z_ld; z NULL: no gate), w [D] or NULL (ones), y [M, D]

@@ -9,6 +9,7 @@ namespace {
 
 constexpr double kMaxElems = 34359738368.0;  // 2^35 elements of one tensor: thread and block counts stay in 32 bits
 constexpr double kMaxInt = 2147483647.0;
+constexpr int kMaxGroups = 1 << 20;  // of a norm's row
 
 bool ok_dtype(int t) { return t == M3_F32 || t == M3_BF16; }
 size_t elem(int t) { return t == M3_BF16 ? 2 : 4; }
@@ -87,13 +88,14 @@ bool ok_scan_size(const m3_scan_args* a) {
 
 int check_gated(m3_gated_norm_args& f) {
   if (f.M < 1 || f.D < 1 || f.G < 1 || f.D % f.G != 0 || !flag(f.gate_first) || !ok_eps(f.eps)) return M3_ERR_INVALID_ARG;
-  if (!ok_dtype(f.in_dtype) || double(f.M) * f.G > kMaxInt || double(f.M) * f.D > kMaxElems) return M3_ERR_UNSUPPORTED;
+  if (!ok_dtype(f.in_dtype) || f.G > kMaxGroups || double(f.M) * f.G > kMaxInt || double(f.M) * f.D > kMaxElems)
+    return M3_ERR_UNSUPPORTED;
   if (f.x == nullptr || !set_ld(f.x_ld, f.D) || !set_ld(f.z_ld, f.D)) return M3_ERR_INVALID_ARG;
   return all_at({f.x, f.z}, elem(f.in_dtype)) && at(f.w, 4) ? M3_OK : M3_ERR_INVALID_ARG;
 }
 bool ok_gated_size(const m3_gated_norm_args& f) {
-  return f.M >= 1 && f.D >= 1 && f.G >= 1 && f.D % f.G == 0 && ok_dtype(f.in_dtype) && double(f.M) * f.G <= kMaxInt &&
-         double(f.M) * f.D <= kMaxElems;
+  return f.M >= 1 && f.D >= 1 && f.G >= 1 && f.D % f.G == 0 && f.G <= kMaxGroups && ok_dtype(f.in_dtype) &&
+         double(f.M) * f.G <= kMaxInt && double(f.M) * f.D <= kMaxElems;
 }
 
 int check_residual_shape(int64_t M, int64_t D, int in_dtype, int res_dtype, float eps) {
@@ -169,7 +171,7 @@ int m3_selective_scan_step(const m3_scan_step_args* args, void* stream) {
   if (rc != M3_OK) return rc;
   if (!all_set({a.x, a.dt, a.A, a.B, a.C, a.h, a.y}) || (a.dt_bias != nullptr && !a.dt_softplus)) return M3_ERR_INVALID_ARG;
   const int64_t GN = int64_t(a.G) * a.N;
-  if (!set_ld(a.x_ld, a.D) || !set_ld(a.dt_ld, a.D) || !set_ld(a.z_ld, a.D) || !set_ld(a.B_ld, GN) || !set_ld(a.C_ld, GN))
+  if (!scan_ld(a.x_ld, a.D) || !scan_ld(a.dt_ld, a.D) || !scan_ld(a.z_ld, a.D) || !scan_ld(a.B_ld, GN) || !scan_ld(a.C_ld, GN))
     return M3_ERR_INVALID_ARG;
   if (a.h_out == nullptr) a.h_out = a.h;
   if (!all_at({a.x, a.dt, a.B, a.C, a.z, a.y}, elem(a.in_dtype)) || !all_at({a.A, a.D_skip, a.dt_bias, a.h, a.h_out}, 4))

@@ -302,10 +302,8 @@ def _scoped(fn):
     return call
 
 
-def _dense(t, dtype, shape, name, dev):
-    """Address of a dense tensor (None: NULL) after checking it."""
-    if t is None:
-        return None
+def _refuse(t, dtype, shape, name, dev):
+    """Say what is wrong with a tensor."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.dtype != dtype:
@@ -314,6 +312,14 @@ def _dense(t, dtype, shape, name, dev):
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
     if t.device != dev:
         raise ValueError(f"{name} is on {t.device}, expected {dev}")
+
+
+def _dense(t, dtype, shape, name, dev):
+    """Address of a dense tensor (None: NULL) after checking it."""
+    if t is None:
+        return None
+    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.device == dev):
+        _refuse(t, dtype, shape, name, dev)
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
     return t.data_ptr()
@@ -324,14 +330,8 @@ def _rows(t, dtype, lead, inner, name, dev):
     its rows to the next: dense rows, the same distance apart throughout."""
     if t is None:
         return None, 0
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a torch.Tensor")
-    if t.dtype != dtype:
-        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.shape != lead + inner:
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(lead + inner)}")
-    if t.device != dev:
-        raise ValueError(f"{name} is on {t.device}, expected {dev}")
+    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == lead + inner and t.device == dev):
+        _refuse(t, dtype, lead + inner, name, dev)
     if t.is_contiguous():
         return t.data_ptr(), 0
     strides = t.stride()
@@ -364,8 +364,14 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
     lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
-def _run_layer(name, args):
-    rc = getattr(_lib.load(), name)(ctypes.byref(args), _raw_stream(torch.cuda.current_device()))
+_calls = {}
+
+
+def _run_layer(name, args, dev):
+    call = _calls.get(name)
+    if call is None:
+        call = _calls[name] = getattr(_lib.load(), name)
+    rc = call(ctypes.byref(args), _raw_stream(dev.index))
     if rc != _lib.M3_OK:
         raise M3Error(rc, name)
 
@@ -412,7 +418,7 @@ def m3_causal_conv(x, w, bias=None, state=None, *, lengths=None, silu=True, y=No
     a.state = _dense(state, t, (Bt, W - 1, D), "state", dev)
     a.y = _dense(y, t, (Bt, L, D), "y", dev)
     a.state_out = _dense(state_out, t, (Bt, W - 1, D), "state_out", dev)
-    _run_layer("m3_causal_conv", a)
+    _run_layer("m3_causal_conv", a, dev)
     return dict(y=y, state=state_out)
 
 
@@ -432,7 +438,7 @@ def m3_causal_conv_step(state, x, w, bias=None, *, silu=True, y=None, state_out=
     a.state = _dense(state, t, (Bt, W - 1, D), "state", dev)
     a.state_out = _dense(state_out, t, (Bt, W - 1, D), "state_out", dev)
     a.y = _dense(y, t, (Bt, D), "y", dev)
-    _run_layer("m3_causal_conv_step", a)
+    _run_layer("m3_causal_conv_step", a, dev)
     return y
 
 
@@ -462,7 +468,7 @@ def m3_causal_conv_backward(x, w, bias=None, state=None, *, dy, lengths=None, si
     a.dbias = _dense(out["dbias"], _F32, (D,), "dbias", dev)
     a.dstate = _dense(out["dstate"], t, (Bt, W - 1, D), "dstate", dev)
     workspace = _take_workspace("m3_causal_conv_backward", a, workspace, dev)
-    _run_layer("m3_causal_conv_backward", a)
+    _run_layer("m3_causal_conv_backward", a, dev)
     return out
 
 
@@ -509,7 +515,7 @@ def m3_selective_scan(x, dt, A, B, C, D=None, z=None, h0=None, *, lengths=None, 
     a.h_final = _dense(h_final, _F32, (Bt, width, N), "h_final", dev)
     if workspace is not False:
         workspace = _take_workspace("m3_selective_scan", a, workspace, dev)
-    _run_layer("m3_selective_scan", a)
+    _run_layer("m3_selective_scan", a, dev)
     return dict(y=y, h=h_final)
 
 
@@ -528,7 +534,7 @@ def m3_selective_scan_step(h, x, dt, A, B, C, D=None, z=None, *, dt_softplus=Fal
     a.h = _dense(h, _F32, (Bt, width, N), "h", x.device)
     a.h_out = _dense(h_out, _F32, (Bt, width, N), "h_out", dev)
     a.y = _dense(y, x.dtype, (Bt, width), "y", dev)
-    _run_layer("m3_selective_scan_step", a)
+    _run_layer("m3_selective_scan_step", a, dev)
     return y
 
 
@@ -559,7 +565,7 @@ def m3_selective_scan_backward(x, dt, A, B, C, D=None, z=None, h0=None, *, dy, d
     a.dy = _dense(dy, t, (Bt, L, width), "dy", dev)
     a.dh_final = _dense(dh_final, _F32, (Bt, width, N), "dh_final", dev)
     workspace = _take_workspace("m3_selective_scan_backward", a, workspace, dev)
-    _run_layer("m3_selective_scan_backward", a)
+    _run_layer("m3_selective_scan_backward", a, dev)
     return out
 
 
@@ -583,7 +589,7 @@ def m3_gated_norm(x, z=None, w=None, *, groups=1, eps=1e-6, gate_first=True, y=N
     a = _lib.GatedNormArgs()
     _gated_inputs(a, x, z, w, groups, eps, gate_first)
     a.y = _dense(y, x.dtype, x.shape, "y", x.device)
-    _run_layer("m3_gated_norm", a)
+    _run_layer("m3_gated_norm", a, x.device)
     return y
 
 
@@ -602,7 +608,7 @@ def m3_gated_norm_backward(x, z=None, w=None, *, dy, groups=1, eps=1e-6, gate_fi
     a.dz = _dense(out["dz"], t, x.shape, "dz", dev)
     a.dw = _dense(out["dw"], _F32, (x.shape[-1],), "dw", dev)
     workspace = _take_workspace("m3_gated_norm_backward", a, workspace, dev)
-    _run_layer("m3_gated_norm_backward", a)
+    _run_layer("m3_gated_norm_backward", a, dev)
     return out
 
 
@@ -628,7 +634,7 @@ def m3_residual_norm(x, residual=None, w=None, scale=None, *, eps=1e-6, y=None, 
     a.w = _dense(w, _F32, (width,), "w", dev)
     a.y = _dense(y, t, x.shape, "y", dev)
     a.residual_out = _dense(residual_out, rt, x.shape, "residual_out", dev)
-    _run_layer("m3_residual_norm", a)
+    _run_layer("m3_residual_norm", a, dev)
     return dict(y=y, residual=residual_out)
 
 
@@ -662,5 +668,5 @@ def m3_residual_norm_backward(h, x=None, w=None, scale=None, *, dy, dresidual=No
     a.dw = _dense(out["dw"], _F32, (width,), "dw", dev)
     a.dscale = _dense(out["dscale"], _F32, (width,), "dscale", dev)
     workspace = _take_workspace("m3_residual_norm_backward", a, workspace, dev)
-    _run_layer("m3_residual_norm_backward", a)
+    _run_layer("m3_residual_norm_backward", a, dev)
     return out

@@ -234,6 +234,8 @@ def _bad(name):
                 (f + "dt_softplus", 0, INV), (f + "A", None, INV), (f + "B", None, INV), (f + "B_ld", 31, INV), (f + "C", BASE + 1, INV)]
     if "gated" in name:
         out += [(f + "G", 3, INV), (f + "gate_first", 2, INV)]
+    if "scan" in name:
+        out += [(f + "x_ld", 1 << 24, INV), (f + "C_ld", 1 << 24, INV)]
     if "residual" in name:
         out += [("res_dtype", 5, UNS)]
     if name.endswith("backward"):
@@ -284,6 +286,14 @@ def test_gated_norm_in_place_needs_dense_rows():
 
 
 @built
+def test_gated_norm_group_limit():
+    a = _gated()
+    a.D = a.G = 1 << 21
+    a.M = 1
+    assert _lib.load().m3_gated_norm(ctypes.byref(a), None) == UNS
+
+
+@built
 def test_layer_workspace_sizes():
     lib = _lib.load()
     for name in _lib.LAYER_SIZES:
@@ -314,7 +324,7 @@ def test_layer_validation_under_host_sanitizers():
         pytest.skip(str(e))
     env = dict(os.environ, LD_PRELOAD=rt, M3SSM_HOSTSAN_LIB=lib, ASAN_OPTIONS="detect_leaks=0:verify_asan_link_order=0")
     r = subprocess.run([sys.executable, "-m", "pytest", "-x", "-q", "-p", "no:cacheprovider", os.path.abspath(__file__), "-k",
-                        "refusals or dense_rows or workspace_sizes"], cwd=ROOT, env=env, capture_output=True, text=True)
+                        "refusals or dense_rows or workspace_sizes or group_limit"], cwd=ROOT, env=env, capture_output=True, text=True)
     assert r.returncode == 0, r.stdout[-2000:] + r.stderr[-2000:]
 
 
