@@ -111,7 +111,8 @@ struct Four {
   }
 };
 
-// First walk: states in front of the tiles, and with SEG the segments' ends.
+// First walk: states in front of the tiles, and with SEG the segments' ends.  Bt 8,
+// L 2048, D 2048, N 16 bf16, uncut: 113 us.
 template <typename T, int NB, bool VEC, bool SEG>
 __global__ __launch_bounds__(2 * kThreads) void states_kernel(BwP p) {
   constexpr int TT = 32, CHB = CH / NB, VE = TT * CHB / kThreads, NP = 16 * NB;
@@ -129,7 +130,7 @@ __global__ __launch_bounds__(2 * kThreads) void states_kernel(BwP p) {
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
       const bool on = l.live && k < l.nleft;
-      A2[k] = on ? p.A[int64_t(l.d) * p.in.N + l.n0 + k] * kLog2e : 0.f;
+      A2[k] = on ? rate(p.A[int64_t(l.d) * p.in.N + l.n0 + k]) : 0.f;
       h[k] = on && p.h0 != nullptr && w.seg == 0 ? p.h0[(int64_t(w.b) * p.in.D + l.d) * p.in.N + l.n0 + k] : 0.f;
       P[k] = 1.f;
       gs[k] = 0.f;
@@ -277,7 +278,10 @@ struct Shared {
   float sdu[2][TB];                                                 // sum over the block's channels of do u
 };
 
-// Second walk.
+// Second walk.  Bound by vector issue (86% busy): 82 instructions per token and wave
+// for the recurrences and sums, 22 of them the sums of dB and dC over channels, and
+// about 17 for staging.  250 registers leave a compute unit one block.  Bt 8, L 2048,
+// D 2048, N 16 bf16: 410-435 us.
 template <typename T, int NB, bool VEC>
 __global__ __launch_bounds__(2 * kThreads) void reverse_kernel(BwP p) {
   constexpr int CHB = CH / NB, VE = TB * CHB / kThreads, NP = 16 * NB;
@@ -299,7 +303,7 @@ __global__ __launch_bounds__(2 * kThreads) void reverse_kernel(BwP p) {
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
       const bool on = l.live && k < l.nleft;
-      A2[k] = on ? p.A[int64_t(l.d) * p.in.N + l.n0 + k] * kLog2e : 0.f;
+      A2[k] = on ? rate(p.A[int64_t(l.d) * p.in.N + l.n0 + k]) : 0.f;
       gg[k] = on && p.dhf != nullptr ? p.dhf[at0 * p.in.N + l.n0 + k] : 0.f;
       hin[k] = 0.f;
       dA[k] = 0.f;

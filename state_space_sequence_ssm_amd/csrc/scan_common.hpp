@@ -27,7 +27,13 @@ constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr int kThreads = 256;
 
-// exp(delta A) from A log2(e): the hardware exponential, 1 ulp.
+// A log2(e), kept finite: a token without a step (delta = 0, as behind an item's
+// length) leaves the state alone at A = -inf too.
+__device__ __forceinline__ float rate(float A) {
+  const float v = A * kLog2e;
+  return v < -3.402823466e38f ? -3.402823466e38f : v;
+}
+// exp(delta A) from that: the hardware exponential, 1 ulp.
 __device__ __forceinline__ float decay(float delta, float a2) { return __builtin_amdgcn_exp2f(delta * a2); }
 
 // softplus(v) = max(v, 0) + log1p(u), u = exp(-|v|), in 9 instructions.  With

@@ -353,6 +353,32 @@ def test_extreme_steps(ops):
     assert rel(got["y"], want["y"]) <= 40 * 2.0 ** -24 and rel(got["h"], want["h"]) <= 40 * 2.0 ** -24
 
 
+@pytest.mark.parametrize("L", [1, 45, 300])
+def test_rates_that_forget_at_once(ops, L):
+    """A = -inf: every state is its own token's input, and the tokens behind an
+    item's length still change nothing."""
+    m = Maker(83)
+    Bt, Dm, Ns = 2, 24, 16
+    x, dt, B, C, dy = m(Bt, L, Dm), m(Bt, L, Dm), m(Bt, L, 1, Ns), m(Bt, L, 1, Ns), m(Bt, L, Dm)
+    A = torch.full((Dm, Ns), -float("inf"), device="cuda")
+    lengths = ilen([L, (L + 1) // 2])
+    got = ops.m3_selective_scan(x, dt, A, B, C, lengths=lengths, dt_softplus=True, y=torch.zeros_like(x))
+    u = torch.nn.functional.softplus(dt.double()) * x.double()
+    y = u * (B.double() * C.double()).sum(-1)
+    last = lengths.long() - 1
+    h = torch.stack([u[b, last[b], :, None] * B.double()[b, last[b]] for b in range(Bt)])
+    # u: softplus 4 roundings and its product; u B, and 17 sums of the readout
+    k = 60 * 2.0 ** -24
+    for b, n in enumerate(lengths.tolist()):
+        assert rel(got["y"][b, :n], y[b, :n]) <= k
+    assert rel(got["h"], h) <= k
+    g = ops.m3_selective_scan_backward(x, dt, A, B, C, dy=dy, lengths=lengths, dt_softplus=True, want_carry_grads=True)
+    assert all(torch.isfinite(v).all() for v in g.values() if v is not None)
+    assert (g["dh0"] == 0).all() and (g["dA"] == 0).all()
+    step = ops.m3_selective_scan_step(got["h"], x[:, 0], dt[:, 0], A, B[:, 0], C[:, 0], dt_softplus=True)
+    assert rel(step, y[:, 0]) <= k
+
+
 def test_binding_refuses_other_places(ops):
     x, w = torch.zeros(2, 5, 16, device="cuda", dtype=BF), torch.zeros(16, 4, device="cuda")
     with pytest.raises(ValueError):
