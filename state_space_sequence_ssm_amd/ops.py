@@ -289,9 +289,10 @@ def _scoped(fn):
     def call(first, *args, stream=None, **kw):
         if not isinstance(first, torch.Tensor):
             raise TypeError("the first argument must be a torch.Tensor")
-        if not first.is_cuda:
+        index = first.get_device()
+        if index < 0:
             raise ValueError("the first argument must be a device tensor")
-        if stream is None and first.device.index == torch.cuda.current_device():
+        if stream is None and index == torch.cuda.current_device():
             return fn(first, *args, **kw)
         if stream is None:
             stream = torch.cuda.current_stream(first.device)
@@ -325,23 +326,24 @@ def _dense(t, dtype, shape, name, dev):
     return t.data_ptr()
 
 
-def _rows(t, dtype, lead, inner, name, dev):
-    """Address of a tensor of shape lead + inner and the elements from one of
-    its rows to the next: dense rows, the same distance apart throughout."""
+def _rows(t, dtype, shape, lead, name, dev):
+    """Address of a tensor whose first `lead` axes count rows, and the elements
+    from one of its rows to the next: dense rows, the same distance apart
+    throughout (0: dense)."""
     if t is None:
         return None, 0
-    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == lead + inner and t.device == dev):
-        _refuse(t, dtype, lead + inner, name, dev)
+    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.device == dev):
+        _refuse(t, dtype, shape, name, dev)
     if t.is_contiguous():
         return t.data_ptr(), 0
     strides = t.stride()
     width = 1
-    for n, st in zip(reversed(inner), reversed(strides[len(lead):])):
+    for n, st in zip(reversed(shape[lead:]), reversed(strides[lead:])):
         if n > 1 and st != width:
             raise ValueError(f"{name}: the elements of a row must be dense")
         width *= n
     ld, rows = 0, 1
-    for n, st in zip(reversed(lead), reversed(strides[:len(lead)])):
+    for n, st in zip(reversed(shape[:lead]), reversed(strides[:lead])):
         if n == 1:
             continue
         if ld == 0:
@@ -355,7 +357,13 @@ def _rows(t, dtype, lead, inner, name, dev):
 
 
 def _new(given, shape, like, dtype=None):
-    return like.new_empty(shape, dtype=dtype or like.dtype) if given is None else given
+    """An output: the given tensor or a new one.  A dense tensor of the same shape
+    and type is the fastest pattern (1.2 us instead of 1.8)."""
+    if given is not None:
+        return given
+    if (dtype is None or dtype is like.dtype) and like.shape == shape and like.is_contiguous():
+        return torch.empty_like(like)
+    return torch.empty(shape, dtype=dtype or like.dtype, device=like.device)
 
 
 # The current stream's handle without building a Stream object, which takes as
@@ -411,7 +419,7 @@ def m3_causal_conv(x, w, bias=None, state=None, *, lengths=None, silu=True, y=No
         state_out = _new(state_out, (Bt, W - 1, D), x)
     a = _lib.ConvArgs()
     a.Bt, a.L, a.D, a.W, a.in_dtype, a.silu = Bt, L, D, W, _dtype_code(x), 1 if silu else 0
-    a.x, a.x_ld = _rows(x, t, (Bt, L), (D,), "x", dev)
+    a.x, a.x_ld = _rows(x, t, x.shape, 2, "x", dev)
     a.w = _dense(w, _F32, (D, W), "w", dev)
     a.bias = _dense(bias, _F32, (D,), "bias", dev)
     a.lengths = _dense(lengths, torch.int32, (Bt,), "lengths", dev)
@@ -432,7 +440,7 @@ def m3_causal_conv_step(state, x, w, bias=None, *, silu=True, y=None, state_out=
     y = _new(y, (Bt, D), x)
     a = _lib.ConvStepArgs()
     a.Bt, a.D, a.W, a.in_dtype, a.silu = Bt, D, W, _dtype_code(x), 1 if silu else 0
-    a.x, a.x_ld = _rows(x, t, (Bt,), (D,), "x", dev)
+    a.x, a.x_ld = _rows(x, t, x.shape, 1, "x", dev)
     a.w = _dense(w, _F32, (D, W), "w", dev)
     a.bias = _dense(bias, _F32, (D,), "bias", dev)
     a.state = _dense(state, t, (Bt, W - 1, D), "state", dev)
@@ -457,7 +465,7 @@ def m3_causal_conv_backward(x, w, bias=None, state=None, *, dy, lengths=None, si
                dstate=_new(got.get("dstate"), (Bt, W - 1, D), x) if want_state_grad or "dstate" in got else None)
     a = _lib.ConvBackwardArgs()
     a.Bt, a.L, a.D, a.W, a.in_dtype, a.silu = Bt, L, D, W, _dtype_code(x), 1 if silu else 0
-    a.x, a.x_ld = _rows(x, t, (Bt, L), (D,), "x", dev)
+    a.x, a.x_ld = _rows(x, t, x.shape, 2, "x", dev)
     a.w = _dense(w, _F32, (D, W), "w", dev)
     a.bias = _dense(bias, _F32, (D,), "bias", dev)
     a.lengths = _dense(lengths, torch.int32, (Bt,), "lengths", dev)
@@ -474,15 +482,15 @@ def m3_causal_conv_backward(x, w, bias=None, state=None, *, dy, lengths=None, si
 
 def _scan_inputs(a, lead, x, dt, A, B, C, D, z, dt_softplus, dt_bias):
     """The inputs that the scan, its backward and its step share."""
-    width = x.shape[-1]
     G, N = B.shape[-2:]
-    dev, t = x.device, x.dtype
+    dev, t, shape = x.device, x.dtype, x.shape
+    width, n, bc = shape[-1], len(lead), (*lead, G, N)
     a.D, a.N, a.G, a.in_dtype, a.dt_softplus = width, N, G, _dtype_code(x), 1 if dt_softplus else 0
-    a.x, a.x_ld = _rows(x, t, lead, (width,), "x", dev)
-    a.dt, a.dt_ld = _rows(dt, t, lead, (width,), "dt", dev)
-    a.z, a.z_ld = _rows(z, t, lead, (width,), "z", dev)
-    a.B, a.B_ld = _rows(B, t, lead, (G, N), "B", dev)
-    a.C, a.C_ld = _rows(C, t, lead, (G, N), "C", dev)
+    a.x, a.x_ld = _rows(x, t, shape, n, "x", dev)
+    a.dt, a.dt_ld = _rows(dt, t, shape, n, "dt", dev)
+    a.z, a.z_ld = _rows(z, t, shape, n, "z", dev)
+    a.B, a.B_ld = _rows(B, t, bc, n, "B", dev)
+    a.C, a.C_ld = _rows(C, t, bc, n, "C", dev)
     a.A = _dense(A, _F32, (width, N), "A", dev)
     a.D_skip = _dense(D, _F32, (width,), "D", dev)
     a.dt_bias = _dense(dt_bias, _F32, (width,), "dt_bias", dev)
@@ -570,11 +578,12 @@ def m3_selective_scan_backward(x, dt, A, B, C, D=None, z=None, h0=None, *, dy, d
 
 
 def _gated_inputs(a, x, z, w, groups, eps, gate_first):
-    lead, width = x.shape[:-1], x.shape[-1]
+    shape = x.shape
+    n, width = len(shape) - 1, shape[-1]
     a.M, a.D, a.G, a.in_dtype = x.numel() // width if width else 0, width, groups, _dtype_code(x)
     a.gate_first, a.eps = 1 if gate_first else 0, eps
-    a.x, a.x_ld = _rows(x, x.dtype, lead, (width,), "x", x.device)
-    a.z, a.z_ld = _rows(z, x.dtype, lead, (width,), "z", x.device)
+    a.x, a.x_ld = _rows(x, x.dtype, shape, n, "x", x.device)
+    a.z, a.z_ld = _rows(z, x.dtype, shape, n, "z", x.device)
     a.w = _dense(w, _F32, (width,), "w", x.device)
 
 
@@ -619,21 +628,21 @@ def m3_residual_norm(x, residual=None, w=None, scale=None, *, eps=1e-6, y=None, 
     wider ones), residual of x's shape in x's type or fp32 (None: zeros), w and
     scale [D] fp32 (None: ones).  Returns a dict with y (x's type) and residual:
     h in the residual's type (residual_out may be `residual` itself)."""
-    dev, t = x.device, x.dtype
-    lead, width = x.shape[:-1], x.shape[-1]
+    dev, t, shape = x.device, x.dtype, x.shape
+    width = shape[-1]
     rt = residual.dtype if residual is not None else residual_out.dtype if residual_out is not None else t
-    y = _new(y, x.shape, x)
+    y = _new(y, shape, x)
     if want_residual:
-        residual_out = _new(residual_out, x.shape, x, rt)
+        residual_out = _new(residual_out, shape, residual if residual is not None else x, rt)
     a = _lib.ResidualNormArgs()
     a.M, a.D, a.in_dtype = x.numel() // width if width else 0, width, _dtype_code(x)
     a.res_dtype, a.eps = _lib.M3_F32 if rt == _F32 else _lib.M3_BF16, eps
-    a.x, a.x_ld = _rows(x, t, lead, (width,), "x", dev)
-    a.residual = _dense(residual, rt, x.shape, "residual", dev)
+    a.x, a.x_ld = _rows(x, t, shape, len(shape) - 1, "x", dev)
+    a.residual = _dense(residual, rt, shape, "residual", dev)
     a.scale = _dense(scale, _F32, (width,), "scale", dev)
     a.w = _dense(w, _F32, (width,), "w", dev)
-    a.y = _dense(y, t, x.shape, "y", dev)
-    a.residual_out = _dense(residual_out, rt, x.shape, "residual_out", dev)
+    a.y = _dense(y, t, shape, "y", dev)
+    a.residual_out = _dense(residual_out, rt, shape, "residual_out", dev)
     _run_layer("m3_residual_norm", a, dev)
     return dict(y=y, residual=residual_out)
 
@@ -646,8 +655,7 @@ def m3_residual_norm_backward(h, x=None, w=None, scale=None, *, dy, dresidual=No
     Returns a dict with dresidual (h's type), dx (dy's type; the same tensor
     where scale is None and the types agree), dw and dscale (None where the
     parameter is).  out["dresidual"] may be `dresidual` itself."""
-    dev, t = h.device, dy.dtype
-    lead, width = h.shape[:-1], h.shape[-1]
+    dev, t, width = h.device, dy.dtype, h.shape[-1]
     got = out or {}
     dres = _new(got.get("dresidual"), h.shape, h)
     own_dx = scale is not None or t != h.dtype or got.get("dx") is not None
@@ -658,7 +666,7 @@ def m3_residual_norm_backward(h, x=None, w=None, scale=None, *, dy, dresidual=No
     a.M, a.D, a.in_dtype = h.numel() // width if width else 0, width, _dtype_code(dy)
     a.res_dtype, a.eps = _dtype_code(h), eps
     a.h = _dense(h, h.dtype, h.shape, "h", dev)
-    a.x, a.x_ld = _rows(x, t, lead, (width,), "x", dev)
+    a.x, a.x_ld = _rows(x, t, h.shape, h.dim() - 1, "x", dev)
     a.scale = _dense(scale, _F32, (width,), "scale", dev)
     a.w = _dense(w, _F32, (width,), "w", dev)
     a.dy = _dense(dy, t, h.shape, "dy", dev)

@@ -345,7 +345,7 @@ def test_binding_refuses_host_tensors():
 def test_row_distances():
     from state_space_sequence_ssm_amd import ops
     cpu, f = torch.device("cpu"), torch.float32
-    rows = lambda t, lead, inner: ops._rows(t, f, torch.Size(lead), inner, "t", cpu)[1]  # noqa: E731
+    rows = lambda t, lead, inner: ops._rows(t, f, (*lead, *inner), len(lead), "t", cpu)[1]  # noqa: E731
     wide = torch.zeros(2, 5, 24)
     assert rows(torch.zeros(2, 5, 8), (2, 5), (8,)) == 0
     assert rows(wide[..., 8:16], (2, 5), (8,)) == 24
