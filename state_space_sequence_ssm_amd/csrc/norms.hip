@@ -19,9 +19,15 @@ namespace {
 // row, so loads and stores have no branch around them (a branch would make each
 // wait for a load wait for the stores as well).  Lanes past the width repeat the
 // team's first word and leave the sums alone.
+//
+// Words are 16 bytes of T wherever a unit holds one, also where rows are not aligned
+// to them or the width is no multiple (RAG): accesses then have the alignment of T, and
+// the last word is moved back to end with the unit, its elements in the word before it
+// left out of the sums and stored twice with the same value.  16384 rows of 2047 bf16,
+// residual backward: 109 us, with one element per word 309 us.  Units of less than a word
+// take one element per lane.
 struct Geom {
-  bool vec;
-  int nv, blk, lgteam;
+  int V, nv, blk, lgteam;
 };
 
 // Sum over the unit's team, in every lane.
@@ -75,10 +81,10 @@ constexpr int threads() {
 }
 
 // Where a lane is: its team's first row and group, and its words' columns.
-template <int V, int NV, int BLK>
+template <int V, int NV, int BLK, bool RAG>
 struct Place {
   static constexpr int NR = NV > 0 ? NV : 1;
-  int lane, team, g0, width, c[NR];
+  int lane, team, g0, c[NR], skip[NR];
   int64_t walker;
   bool in[NR];
   __device__ __forceinline__ Place(int lgteam, int G, int Dg) {
@@ -87,22 +93,52 @@ struct Place {
     lane = BLK ? int(threadIdx.x) : int(threadIdx.x) & (team - 1);
     walker = slot / uint32_t(G);
     g0 = int(slot % uint32_t(G)) * Dg;
-    width = Dg;
 #pragma unroll
     for (int i = 0; i < NR; ++i) {
       c[i] = (i * team + lane) * V;
       in[i] = c[i] < Dg;
-      c[i] = in[i] ? c[i] : 0;
+      skip[i] = RAG && in[i] ? max(c[i] + V - Dg, 0) : 0;
+      c[i] = in[i] ? c[i] - skip[i] : 0;
     }
   }
+  // whether word i's element j is the sums' to take (a lane past the width drops its
+  // sums as a whole)
+  __device__ __forceinline__ bool counts(int i, int j) const { return !RAG || j >= skip[i]; }
 };
+// A word, aligned or with the alignment of its elements.
+typedef uint32_t quad_t __attribute__((ext_vector_type(4)));  // kept whole by the compiler, unlike a struct
+typedef quad_t loose_quad_t __attribute__((aligned(2), may_alias));
+template <typename T, int V, bool RAG>
+__device__ __forceinline__ Pack<T, V> load_word(const T* p) {
+  if constexpr (!RAG) return load_pack<T, V>(p);
+  static_assert(sizeof(T) * V % 16 == 0 || !RAG, "whole quads");
+  Pack<T, V> q;
+#pragma unroll
+  for (int i = 0; i < int(sizeof(T) * V / 16); ++i) {
+    const quad_t w = reinterpret_cast<const loose_quad_t*>(p)[i];
+    __builtin_memcpy(reinterpret_cast<char*>(&q) + 16 * i, &w, 16);
+  }
+  return q;
+}
+template <typename T, int V, bool RAG>
+__device__ __forceinline__ void store_word(T* p, const float* v) {
+  if constexpr (!RAG) return store_pack<T, V>(p, v);
+  Pack<T, V> q;
+  store_pack<T, V>(q.e, v);
+#pragma unroll
+  for (int i = 0; i < int(sizeof(T) * V / 16); ++i) {
+    quad_t w;
+    __builtin_memcpy(&w, reinterpret_cast<const char*>(&q) + 16 * i, 16);
+    reinterpret_cast<loose_quad_t*>(p)[i] = w;
+  }
+}
 // A gain's values at a lane's words (1 without one).
-template <int V, int NR>
+template <int V, int NR, bool RAG>
 __device__ __forceinline__ void gain(const float* w, const int (&c)[NR], float (&o)[NR][V]) {
 #pragma unroll
   for (int i = 0; i < NR; ++i) {
     if (w != nullptr) {
-      unpack<float, V>(load_pack<float, V>(w + c[i]), o[i]);
+      unpack<float, V>(load_word<float, V, RAG>(w + c[i]), o[i]);
     } else {
 #pragma unroll
       for (int j = 0; j < V; ++j) o[i][j] = 1.f;
@@ -121,10 +157,10 @@ struct GatedP {
   float eps, inv;
 };
 
-template <typename T, int V, int NV, int BLK>
+template <typename T, int V, int NV, int BLK, bool RAG>
 __global__ __launch_bounds__(threads<BLK>()) void gated_kernel(GatedP p) {
   __shared__ float red[2][16];
-  const Place<V, NV, BLK> at(p.lgteam, p.G, p.Dg);
+  const Place<V, NV, BLK, RAG> at(p.lgteam, p.G, p.Dg);
   const T* x = static_cast<const T*>(p.x) + at.g0;
   const bool gated = p.z != nullptr, first = p.gate_first != 0;
   const T* z = gated ? static_cast<const T*>(p.z) + at.g0 : nullptr;
@@ -133,15 +169,15 @@ __global__ __launch_bounds__(threads<BLK>()) void gated_kernel(GatedP p) {
   const int64_t whole = p.M / p.walkers;
   if constexpr (NV > 0) {
     float wr[NV][V];
-    gain<V, NV>(w, at.c, wr);
+    gain<V, NV, RAG>(w, at.c, wr);
     Pack<T, V> qx[NV], qz[NV];
     auto fetch = [&](int64_t k) {
       int64_t row = at.walker + k * p.walkers;
       row = row < p.M ? row : p.M - 1;
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
-        qx[i] = load_pack<T, V>(x + row * p.xld + at.c[i]);
-        if (gated) qz[i] = load_pack<T, V>(z + row * p.zld + at.c[i]);
+        qx[i] = load_word<T, V, RAG>(x + row * p.xld + at.c[i]);
+        if (gated) qz[i] = load_word<T, V, RAG>(z + row * p.zld + at.c[i]);
       }
     };
     auto turn = [&](int64_t k, bool last) {
@@ -164,7 +200,10 @@ __global__ __launch_bounds__(threads<BLK>()) void gated_kernel(GatedP p) {
         }
         float t = 0.f;
 #pragma unroll
-        for (int j = 0; j < V; ++j) t = fmaf(v[i][j], v[i][j], t);
+        for (int j = 0; j < V; ++j) {
+          const float u = at.counts(i, j) ? v[i][j] : 0.f;
+          t = fmaf(u, u, t);
+        }
         s += at.in[i] ? t : 0.f;
       }
       if (!last) fetch(k + 1);
@@ -181,7 +220,7 @@ __global__ __launch_bounds__(threads<BLK>()) void gated_kernel(GatedP p) {
 #pragma unroll
           for (int j = 0; j < V; ++j) o[j] = v[i][j] * r * wr[i][j] * gate[i][j];
         }
-        store_pack<T, V>(y + row * p.D + at.c[i], o);
+        store_word<T, V, RAG>(y + row * p.D + at.c[i], o);
       }
     };
     fetch(0);
@@ -223,10 +262,10 @@ struct GatedBwP {
 // silu(z)) and e = u w:  dv = r (e - n mean(e n)), dw = sum u n.  Both sums of
 // a row, v^2 and e v, are known before its outputs are formed.  32768 rows of 2048
 // bf16 in 8 groups: 130 us, 5.2 TB/s, and 5 us for the join of dw.
-template <typename T, int V, int NV, int BLK>
+template <typename T, int V, int NV, int BLK, bool RAG>
 __global__ __launch_bounds__(threads<BLK>()) void gated_backward_kernel(GatedBwP p) {
   __shared__ float red[2][2][16];
-  const Place<V, NV, BLK> at(p.lgteam, p.G, p.Dg);
+  const Place<V, NV, BLK, RAG> at(p.lgteam, p.G, p.Dg);
   const bool first = p.gate_first != 0, gated = p.z != nullptr;
   const T* x = static_cast<const T*>(p.x) + at.g0;
   const T* z = gated ? static_cast<const T*>(p.z) + at.g0 : nullptr;
@@ -238,7 +277,7 @@ __global__ __launch_bounds__(threads<BLK>()) void gated_backward_kernel(GatedBwP
   const int64_t whole = p.M / p.walkers;
   if constexpr (NV > 0) {
     float dw[NV][V], wr[NV][V];
-    gain<V, NV>(w, at.c, wr);
+    gain<V, NV, RAG>(w, at.c, wr);
 #pragma unroll
     for (int i = 0; i < NV; ++i)
 #pragma unroll
@@ -249,9 +288,9 @@ __global__ __launch_bounds__(threads<BLK>()) void gated_backward_kernel(GatedBwP
       row = row < p.M ? row : p.M - 1;
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
-        qx[i] = load_pack<T, V>(x + row * p.xld + at.c[i]);
-        qd[i] = load_pack<T, V>(dy + row * p.D + at.c[i]);
-        if (gated) qz[i] = load_pack<T, V>(z + row * p.zld + at.c[i]);
+        qx[i] = load_word<T, V, RAG>(x + row * p.xld + at.c[i]);
+        qd[i] = load_word<T, V, RAG>(dy + row * p.D + at.c[i]);
+        if (gated) qz[i] = load_word<T, V, RAG>(z + row * p.zld + at.c[i]);
       }
     };
     auto turn = [&](int64_t k, bool last) {
@@ -273,10 +312,11 @@ __global__ __launch_bounds__(threads<BLK>()) void gated_backward_kernel(GatedBwP
 #pragma unroll
         for (int j = 0; j < V; ++j) {
           const float gate = zv[i][j] * sg[i][j];
-          const float v = first ? xv[i][j] * gate : xv[i][j];
           const float e = d[i][j] * wr[i][j];
+          const float v = at.counts(i, j) ? (first ? xv[i][j] * gate : xv[i][j]) : 0.f;
+          const float ev = at.counts(i, j) ? (first ? e : e * gate) : 0.f;
           t1 = fmaf(v, v, t1);
-          t2 = fmaf(first ? e : e * gate, v, t2);
+          t2 = fmaf(ev, v, t2);
         }
         s1 += at.in[i] ? t1 : 0.f;
         s2 += at.in[i] ? t2 : 0.f;
@@ -299,8 +339,8 @@ __global__ __launch_bounds__(threads<BLK>()) void gated_backward_kernel(GatedBwP
           oz[j] = (first ? dv * xv[i][j] : d[i][j] * n * wr[i][j]) * dsilu_f(zv[i][j], sg[i][j]);
           dw[i][j] = fmaf(u, n, dw[i][j]);
         }
-        store_pack<T, V>(dx + row * p.D + at.c[i], ox);
-        if (gated) store_pack<T, V>(dz + row * p.D + at.c[i], oz);
+        store_word<T, V, RAG>(dx + row * p.D + at.c[i], ox);
+        if (gated) store_word<T, V, RAG>(dz + row * p.D + at.c[i], oz);
       }
     };
     fetch(0);
@@ -309,7 +349,7 @@ __global__ __launch_bounds__(threads<BLK>()) void gated_backward_kernel(GatedBwP
     if (part == nullptr) return;
 #pragma unroll
     for (int i = 0; i < NV; ++i)
-      if (at.in[i]) store_pack<float, V>(part + at.c[i], dw[i]);
+      if (at.in[i]) store_word<float, V, RAG>(part + at.c[i], dw[i]);
   } else {
     if (part != nullptr)
       for (int c = at.lane; c < p.Dg; c += at.team) part[c] = 0.f;
@@ -354,10 +394,10 @@ struct ResP {
   float eps, inv;
 };
 
-template <typename T, typename R, int V, int NV, int BLK>
+template <typename T, typename R, int V, int NV, int BLK, bool RAG>
 __global__ __launch_bounds__(threads<BLK>()) void residual_kernel(ResP p) {
   __shared__ float red[2][16];
-  const Place<V, NV, BLK> at(p.lgteam, 1, p.D);
+  const Place<V, NV, BLK, RAG> at(p.lgteam, 1, p.D);
   const T* x = static_cast<const T*>(p.x);
   const R* res = static_cast<const R*>(p.res);
   R* out = static_cast<R*>(p.res_out);
@@ -371,15 +411,15 @@ __global__ __launch_bounds__(threads<BLK>()) void residual_kernel(ResP p) {
       row = row < p.M ? row : p.M - 1;
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
-        qx[i] = load_pack<T, V>(x + row * p.xld + at.c[i]);
-        if (res != nullptr) qr[i] = load_pack<R, V>(res + row * p.D + at.c[i]);
+        qx[i] = load_word<T, V, RAG>(x + row * p.xld + at.c[i]);
+        if (res != nullptr) qr[i] = load_word<R, V, RAG>(res + row * p.D + at.c[i]);
         else qr[i] = Pack<R, V>{};
       }
     };
     fetch(0);
     float wr[NV][V], sr[NV][V];
-    gain<V, NV>(p.w, at.c, wr);
-    gain<V, NV>(p.scale, at.c, sr);
+    gain<V, NV, RAG>(p.w, at.c, wr);
+    gain<V, NV, RAG>(p.scale, at.c, sr);
     auto turn = [&](int64_t k, bool last) {
       float h[NV][V];
       float s = 0.f;
@@ -389,7 +429,8 @@ __global__ __launch_bounds__(threads<BLK>()) void residual_kernel(ResP p) {
 #pragma unroll
         for (int j = 0; j < V; ++j) {
           h[i][j] = fmaf(sr[i][j], to_f32(qx[i].e[j]), to_f32(qr[i].e[j]));
-          t = fmaf(h[i][j], h[i][j], t);
+          const float u = at.counts(i, j) ? h[i][j] : 0.f;
+          t = fmaf(u, u, t);
         }
         s += at.in[i] ? t : 0.f;
       }
@@ -400,10 +441,10 @@ __global__ __launch_bounds__(threads<BLK>()) void residual_kernel(ResP p) {
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
         float o[V];
-        if (out != nullptr) store_pack<R, V>(out + row * p.D + at.c[i], h[i]);
+        if (out != nullptr) store_word<R, V, RAG>(out + row * p.D + at.c[i], h[i]);
 #pragma unroll
         for (int j = 0; j < V; ++j) o[j] = h[i][j] * r * wr[i][j];
-        store_pack<T, V>(y + row * p.D + at.c[i], o);
+        store_word<T, V, RAG>(y + row * p.D + at.c[i], o);
       }
     };
     for (int64_t k = 0; k < whole; ++k) turn(k, false);
@@ -447,10 +488,10 @@ struct ResBwP {
 // n = h r, e = dy w:  dh = dro + r (e - n mean(e n)), dw = sum dy n, dscale =
 // sum dh x; rows walked as in the gated norm's backward.  32768 rows of 2048 bf16:
 // 157 us, 5.1 TB/s, and 7 us for the joins.
-template <typename T, typename R, int V, int NV, int BLK>
+template <typename T, typename R, int V, int NV, int BLK, bool RAG>
 __global__ __launch_bounds__(threads<BLK>()) void residual_backward_kernel(ResBwP p) {
   __shared__ float red[2][2][16];
-  const Place<V, NV, BLK> at(p.lgteam, 1, p.D);
+  const Place<V, NV, BLK, RAG> at(p.lgteam, 1, p.D);
   float* prow = p.part + at.walker * (p.has_dw + p.has_ds) * p.D;
   float* pw = p.has_dw ? prow : nullptr;
   float* ps = p.has_ds ? prow + (p.has_dw ? p.D : 0) : nullptr;
@@ -469,18 +510,18 @@ __global__ __launch_bounds__(threads<BLK>()) void residual_backward_kernel(ResBw
       row = row < p.M ? row : p.M - 1;
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
-        qh[i] = load_pack<R, V>(h + row * p.D + at.c[i]);
-        qd[i] = load_pack<T, V>(dy + row * p.D + at.c[i]);
-        if (dro != nullptr) qr[i] = load_pack<R, V>(dro + row * p.D + at.c[i]);
+        qh[i] = load_word<R, V, RAG>(h + row * p.D + at.c[i]);
+        qd[i] = load_word<T, V, RAG>(dy + row * p.D + at.c[i]);
+        if (dro != nullptr) qr[i] = load_word<R, V, RAG>(dro + row * p.D + at.c[i]);
         else qr[i] = Pack<R, V>{};
-        if (p.has_ds) qx[i] = load_pack<T, V>(x + row * p.xld + at.c[i]);
+        if (p.has_ds) qx[i] = load_word<T, V, RAG>(x + row * p.xld + at.c[i]);
         else qx[i] = Pack<T, V>{};
       }
     };
     fetch(0);
     float dw[NV][V], ds[NV][V], wr[NV][V], sr[NV][V];
-    gain<V, NV>(p.w, at.c, wr);
-    gain<V, NV>(p.scale, at.c, sr);
+    gain<V, NV, RAG>(p.w, at.c, wr);
+    gain<V, NV, RAG>(p.scale, at.c, sr);
 #pragma unroll
     for (int i = 0; i < NV; ++i)
 #pragma unroll
@@ -499,9 +540,10 @@ __global__ __launch_bounds__(threads<BLK>()) void residual_backward_kernel(ResBw
         float t1 = 0.f, t2 = 0.f;
 #pragma unroll
         for (int j = 0; j < V; ++j) {
-          const float hv = to_f32(ch[i].e[j]);
+          const float hv = at.counts(i, j) ? to_f32(ch[i].e[j]) : 0.f;
+          const float e = at.counts(i, j) ? to_f32(cd[i].e[j]) * wr[i][j] : 0.f;
           t1 = fmaf(hv, hv, t1);
-          t2 = fmaf(to_f32(cd[i].e[j]) * wr[i][j], hv, t2);
+          t2 = fmaf(e, hv, t2);
         }
         s1 += at.in[i] ? t1 : 0.f;
         s2 += at.in[i] ? t2 : 0.f;
@@ -522,8 +564,8 @@ __global__ __launch_bounds__(threads<BLK>()) void residual_backward_kernel(ResBw
           dw[i][j] = fmaf(d, n, dw[i][j]);
           ds[i][j] = fmaf(o[j], to_f32(cx[i].e[j]), ds[i][j]);
         }
-        if (dres != nullptr) store_pack<R, V>(dres + row * p.D + at.c[i], o);
-        if (dx != nullptr) store_pack<T, V>(dx + row * p.D + at.c[i], ox);
+        if (dres != nullptr) store_word<R, V, RAG>(dres + row * p.D + at.c[i], o);
+        if (dx != nullptr) store_word<T, V, RAG>(dx + row * p.D + at.c[i], ox);
       }
     };
     for (int64_t k = 0; k < whole; ++k) turn(k, false);
@@ -531,8 +573,8 @@ __global__ __launch_bounds__(threads<BLK>()) void residual_backward_kernel(ResBw
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       if (!at.in[i]) continue;
-      if (pw != nullptr) store_pack<float, V>(pw + at.c[i], dw[i]);
-      if (ps != nullptr) store_pack<float, V>(ps + at.c[i], ds[i]);
+      if (pw != nullptr) store_word<float, V, RAG>(pw + at.c[i], dw[i]);
+      if (ps != nullptr) store_word<float, V, RAG>(ps + at.c[i], ds[i]);
     }
   } else {
     for (int c = at.lane; c < p.D; c += at.team) {
@@ -569,8 +611,9 @@ __global__ __launch_bounds__(threads<BLK>()) void residual_backward_kernel(ResBw
 // times the registers per word and takes a block at once: 32768 rows of 2048 bf16
 // take 159 us with one word per lane of four waves, and 216 us with four words per
 // lane of one wave (216 registers).
-Geom pick(int64_t units, int width, int V, bool vec, bool backward) {
-  Geom g{vec, 1, 0, 6};
+Geom pick(int64_t units, int width, int in_dtype, bool backward) {
+  const int whole = in_dtype == M3_BF16 ? 8 : 4, V = width >= whole ? whole : 1;
+  Geom g{V, 1, 0, 6};
   const int64_t words = (int64_t(width) + V - 1) / V;
   if (words <= 64) {
     g.lgteam = 0;
@@ -587,7 +630,7 @@ Geom pick(int64_t units, int width, int V, bool vec, bool backward) {
     g.blk = 1024;
     g.nv = 2;
   } else {
-    g.vec = false;
+    g.V = 1;
     g.blk = 1024;
     g.nv = 0;
   }
@@ -607,28 +650,29 @@ int64_t pick_walkers(int64_t M, int G, const Geom& g, int64_t waves) {
 }
 constexpr int64_t kForwardWaves = 8192, kBackwardWaves = 4096;
 
-// The kernel instance for a geometry: CALL(V, NV, BLK).
-#define M3_NORM_WIDTH(g, V, CALL)            \
-  if ((g).blk == 0) {                        \
-    if ((g).nv == 1) return CALL(V, 1, 0);   \
-    if ((g).nv == 2) return CALL(V, 2, 0);   \
-    return CALL(V, 4, 0);                    \
-  }                                          \
-  if ((g).blk == 1024) return CALL(V, 2, 1024); \
-  if ((g).nv == 1) return CALL(V, 1, 256);   \
-  if ((g).nv == 2) return CALL(V, 2, 256);   \
-  return CALL(V, 4, 256);
-#define M3_NORM_BACKWARD_WIDTH(g, V, CALL)        \
-  if ((g).blk == 0) return CALL(V, 1, 0);         \
-  if ((g).blk == 512) return CALL(V, 2, 512);     \
-  if ((g).nv == 1) return CALL(V, 1, 256);        \
-  return CALL(V, 2, 256);
-#define M3_NORM_DISPATCH(g, VV, WIDTH, CALL) \
-  if ((g).nv == 0) return CALL(1, 0, 1024);  \
-  if ((g).vec) {                             \
-    WIDTH(g, VV, CALL)                       \
-  }                                          \
-  WIDTH(g, 1, CALL)
+// The kernel instance for a geometry: CALL(V, NV, BLK, RAG).
+#define M3_NORM_WIDTH(g, V, RAG, CALL)            \
+  if ((g).blk == 0) {                             \
+    if ((g).nv == 1) return CALL(V, 1, 0, RAG);   \
+    if ((g).nv == 2) return CALL(V, 2, 0, RAG);   \
+    return CALL(V, 4, 0, RAG);                    \
+  }                                               \
+  if ((g).blk == 1024) return CALL(V, 2, 1024, RAG); \
+  if ((g).nv == 1) return CALL(V, 1, 256, RAG);   \
+  if ((g).nv == 2) return CALL(V, 2, 256, RAG);   \
+  return CALL(V, 4, 256, RAG);
+#define M3_NORM_BACKWARD_WIDTH(g, V, RAG, CALL)   \
+  if ((g).blk == 0) return CALL(V, 1, 0, RAG);    \
+  if ((g).blk == 512) return CALL(V, 2, 512, RAG); \
+  if ((g).nv == 1) return CALL(V, 1, 256, RAG);   \
+  return CALL(V, 2, 256, RAG);
+#define M3_NORM_DISPATCH(g, vec, VV, WIDTH, CALL) \
+  if ((g).nv == 0) return CALL(1, 0, 1024, false); \
+  if ((g).V == 1) return CALL(1, 1, 0, false);    \
+  if (vec) {                                      \
+    WIDTH(g, VV, false, CALL)                     \
+  }                                               \
+  WIDTH(g, VV, true, CALL)
 
 uint32_t grid_of(const Geom& g, int64_t teams) { return uint32_t(g.blk ? teams : (teams << g.lgteam) / 256); }
 bool gain_aligned(const float* w) { return reinterpret_cast<uintptr_t>(w) % 16 == 0; }
@@ -639,10 +683,10 @@ hipError_t run_gated(const m3_gated_norm_args& a, hipStream_t s) {
   const int Dg = a.D / a.G;
   const bool vec = Dg % VV == 0 && rows_aligned(a.x, a.x_ld, sizeof(T), 16) && rows_aligned(a.z, a.z_ld, sizeof(T), 16) &&
                    rows_aligned(a.y, a.D, sizeof(T), 16) && gain_aligned(a.w);
-  const Geom g = pick(a.M * a.G, Dg, vec ? VV : 1, vec, false);
+  const Geom g = pick(a.M * a.G, Dg, a.in_dtype, false);
   const GatedP p{a.x, a.z, a.w, a.y, a.x_ld, a.z_ld, a.M, pick_walkers(a.M, a.G, g, kForwardWaves), a.D, a.G, Dg, g.lgteam, a.gate_first, a.eps, 1.f / float(Dg)};
-#define CALL(V, NV, BLK) (gated_kernel<T, V, NV, BLK><<<grid_of(g, p.walkers * p.G), threads<BLK>(), 0, s>>>(p), hipGetLastError())
-  M3_NORM_DISPATCH(g, VV, M3_NORM_WIDTH, CALL)
+#define CALL(V, NV, BLK, RAG) (gated_kernel<T, V, NV, BLK, RAG><<<grid_of(g, p.walkers * p.G), threads<BLK>(), 0, s>>>(p), hipGetLastError())
+  M3_NORM_DISPATCH(g, vec, VV, M3_NORM_WIDTH, CALL)
 #undef CALL
 }
 
@@ -655,23 +699,21 @@ bool gated_bw_vec(const m3_gated_norm_backward_args& a) {
          rows_aligned(a.dz, f.D, sizeof(T), 16) && gain_aligned(f.w);
 }
 template <typename T>
-hipError_t launch_gated_bw(const GatedBwP& p, const Geom& g, hipStream_t s) {
+hipError_t launch_gated_bw(const GatedBwP& p, const Geom& g, bool vec, hipStream_t s) {
   constexpr int VV = 16 / int(sizeof(T));
-#define CALL(V, NV, BLK) \
-  (gated_backward_kernel<T, V, NV, BLK><<<grid_of(g, p.walkers * p.G), threads<BLK>(), 0, s>>>(p), hipGetLastError())
-  M3_NORM_DISPATCH(g, VV, M3_NORM_BACKWARD_WIDTH, CALL)
+#define CALL(V, NV, BLK, RAG) \
+  (gated_backward_kernel<T, V, NV, BLK, RAG><<<grid_of(g, p.walkers * p.G), threads<BLK>(), 0, s>>>(p), hipGetLastError())
+  M3_NORM_DISPATCH(g, vec, VV, M3_NORM_BACKWARD_WIDTH, CALL)
 #undef CALL
 }
 template <typename T>
 hipError_t run_gated_bw(const m3_gated_norm_backward_args& a, hipStream_t s) {
-  constexpr int VV = 16 / int(sizeof(T));
   const m3_gated_norm_args& f = a.fwd;
   const int Dg = f.D / f.G;
-  const bool vec = gated_bw_vec<T>(a);
-  const Geom g = pick(f.M * f.G, Dg, vec ? VV : 1, vec, true);
+  const Geom g = pick(f.M * f.G, Dg, f.in_dtype, true);
   const GatedBwP p{f.x, f.z, f.w, a.dy, a.dx, a.dz, f.w != nullptr ? static_cast<float*>(a.workspace) : nullptr, f.x_ld, f.z_ld,
                    f.M, pick_walkers(f.M, f.G, g, kBackwardWaves), f.D, f.G, Dg, g.lgteam, f.gate_first, f.eps, 1.f / float(Dg)};
-  const hipError_t e = launch_gated_bw<T>(p, g, s);
+  const hipError_t e = launch_gated_bw<T>(p, g, gated_bw_vec<T>(a), s);
   if (e != hipSuccess || f.w == nullptr) return e;
   ColSum c{};
   c.part = p.part;
@@ -688,19 +730,19 @@ hipError_t run_residual(const m3_residual_norm_args& a, hipStream_t s) {
   const bool vec = a.D % VV == 0 && rows_aligned(a.x, a.x_ld, sizeof(T), 16) && rows_aligned(a.y, a.D, sizeof(T), 16) &&
                    rows_aligned(a.residual, a.D, sizeof(R), 16) && rows_aligned(a.residual_out, a.D, sizeof(R), 16) && gain_aligned(a.w) &&
                    gain_aligned(a.scale);
-  const Geom g = pick(a.M, a.D, vec ? VV : 1, vec, false);
+  const Geom g = pick(a.M, a.D, a.in_dtype, false);
   const ResP p{a.x, a.residual, a.scale, a.w, a.y, a.residual_out, a.x_ld, a.M, pick_walkers(a.M, 1, g, kForwardWaves),
                a.D, g.lgteam, a.eps, 1.f / float(a.D)};
-#define CALL(V, NV, BLK) (residual_kernel<T, R, V, NV, BLK><<<grid_of(g, p.walkers), threads<BLK>(), 0, s>>>(p), hipGetLastError())
-  M3_NORM_DISPATCH(g, VV, M3_NORM_WIDTH, CALL)
+#define CALL(V, NV, BLK, RAG) (residual_kernel<T, R, V, NV, BLK, RAG><<<grid_of(g, p.walkers), threads<BLK>(), 0, s>>>(p), hipGetLastError())
+  M3_NORM_DISPATCH(g, vec, VV, M3_NORM_WIDTH, CALL)
 #undef CALL
 }
 template <typename T, typename R>
-hipError_t launch_residual_bw(const ResBwP& p, const Geom& g, hipStream_t s) {
+hipError_t launch_residual_bw(const ResBwP& p, const Geom& g, bool vec, hipStream_t s) {
   constexpr int VV = 16 / int(sizeof(T));
-#define CALL(V, NV, BLK) \
-  (residual_backward_kernel<T, R, V, NV, BLK><<<grid_of(g, p.walkers), threads<BLK>(), 0, s>>>(p), hipGetLastError())
-  M3_NORM_DISPATCH(g, VV, M3_NORM_BACKWARD_WIDTH, CALL)
+#define CALL(V, NV, BLK, RAG) \
+  (residual_backward_kernel<T, R, V, NV, BLK, RAG><<<grid_of(g, p.walkers), threads<BLK>(), 0, s>>>(p), hipGetLastError())
+  M3_NORM_DISPATCH(g, vec, VV, M3_NORM_BACKWARD_WIDTH, CALL)
 #undef CALL
 }
 template <typename T, typename R>
@@ -709,10 +751,10 @@ hipError_t run_residual_bw(const m3_residual_norm_backward_args& a, hipStream_t 
   const bool vec = a.D % VV == 0 && rows_aligned(a.x, a.x_ld, sizeof(T), 16) && rows_aligned(a.dy, a.D, sizeof(T), 16) &&
                    rows_aligned(a.dx, a.D, sizeof(T), 16) && rows_aligned(a.h, a.D, sizeof(R), 16) &&
                    rows_aligned(a.dresidual_out, a.D, sizeof(R), 16) && rows_aligned(a.dresidual, a.D, sizeof(R), 16) && gain_aligned(a.w) && gain_aligned(a.scale);
-  const Geom g = pick(a.M, a.D, vec ? VV : 1, vec, true);
+  const Geom g = pick(a.M, a.D, a.in_dtype, true);
   const ResBwP p{a.h, a.x, a.scale, a.w, a.dy, a.dresidual_out, a.dx, a.dresidual, static_cast<float*>(a.workspace), a.x_ld, a.M,
                  pick_walkers(a.M, 1, g, kBackwardWaves), a.D, g.lgteam, a.w != nullptr, a.scale != nullptr, a.eps, 1.f / float(a.D)};
-  const hipError_t e = launch_residual_bw<T, R>(p, g, s);
+  const hipError_t e = launch_residual_bw<T, R>(p, g, vec, s);
   if (e != hipSuccess || (a.w == nullptr && a.scale == nullptr)) return e;
   ColSum c{};
   c.part = p.part;
@@ -728,14 +770,10 @@ hipError_t run_residual_bw(const m3_residual_norm_backward_args& a, hipStream_t 
 hipError_t launch_gated_norm(const m3_gated_norm_args& a, hipStream_t s) {
   return a.in_dtype == M3_BF16 ? run_gated<bf16_t>(a, s) : run_gated<float>(a, s);
 }
-// The sizes cover both widths of the lanes (the addresses are not known here).
 size_t gated_norm_backward_workspace(const m3_gated_norm_backward_args& a) {
   const m3_gated_norm_args& f = a.fwd;
   if (f.w == nullptr) return 0;
-  const int V = f.in_dtype == M3_BF16 ? 8 : 4, Dg = f.D / f.G;
-  int64_t w = pick_walkers(f.M, f.G, pick(f.M * f.G, Dg, 1, false, true), kBackwardWaves);
-  const int64_t v = pick_walkers(f.M, f.G, pick(f.M * f.G, Dg, V, true, true), kBackwardWaves);
-  if (v > w) w = v;
+  const int64_t w = pick_walkers(f.M, f.G, pick(f.M * f.G, f.D / f.G, f.in_dtype, true), kBackwardWaves);
   return round256(size_t(w) * f.D * 4);
 }
 hipError_t launch_gated_norm_backward(const m3_gated_norm_backward_args& a, hipStream_t s) {
@@ -746,10 +784,7 @@ hipError_t launch_residual_norm(const m3_residual_norm_args& a, hipStream_t s) {
   return a.res_dtype == M3_BF16 ? run_residual<bf16_t, bf16_t>(a, s) : run_residual<bf16_t, float>(a, s);
 }
 size_t residual_norm_backward_workspace(const m3_residual_norm_backward_args& a) {
-  const int V = a.in_dtype == M3_BF16 ? 8 : 4;
-  int64_t w = pick_walkers(a.M, 1, pick(a.M, a.D, 1, false, true), kBackwardWaves);
-  const int64_t v = pick_walkers(a.M, 1, pick(a.M, a.D, V, true, true), kBackwardWaves);
-  if (v > w) w = v;
+  const int64_t w = pick_walkers(a.M, 1, pick(a.M, a.D, a.in_dtype, true), kBackwardWaves);
   return round256(size_t(w) * ((a.w != nullptr) + (a.scale != nullptr)) * a.D * 4);
 }
 hipError_t launch_residual_norm_backward(const m3_residual_norm_backward_args& a, hipStream_t s) {

@@ -380,3 +380,57 @@ def test_residual_norm(ops, c):
         d2 = dr.clone()
         b2 = ops.m3_residual_norm_backward(h, x, w, scale, dy=dy, dresidual=d2, out=dict(dresidual=d2), **kw)
         assert torch.equal(d2, bw["dresidual"]) and torch.equal(b2["dx"], bw["dx"])
+
+
+# Widths that end inside a 16-byte word and rows off its alignment, at each way that
+# units are dealt to lanes.
+UNALIGNED = [(2100, 9, 1), (2500, 49, 1), (2100, 515, 1), (2100, 1030, 1), (30, 1041, 3), (5, 2051, 1), (5, 4099, 1),
+             (4, 8209, 1), (70, 1024, 2)]
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("M,D,groups", UNALIGNED)
+def test_norms_off_alignment(ops, M, D, groups, dt):
+    for first in (True, False):
+        test_gated_norm(ops, ((M, D), groups, dt, first, True, True, False))
+    test_residual_norm(ops, ((M, D), dt, "f32", True, True, False))
+    test_residual_norm(ops, ((M, D), dt, dt, False, True, False))
+    # one element off: rows, residual, gate, gain and outputs at odd addresses
+    m, t = Maker(43), DT[dt]
+    x, z, res, w, scale, dy = m(M, D, dtype=t), m(M, D, dtype=t), m(M, D, dtype=t), m(D), m(D), m(M, D, dtype=t)
+
+    def off(v):
+        o = torch.full((v.numel() + 1,), NAN, dtype=v.dtype, device="cuda")[1:].view(v.shape)
+        return o.copy_(v)
+
+    kw, k = dict(groups=groups, eps=1e-5), D // groups + 40 + 4 * _zmax(z)
+    want, mag = ref.gated_norm(x, z, w, dy=dy, **kw), ref.gated_norm(x, z, w, dy=dy, mag=True, **kw)
+    xs, zs = wide(x, 1, 2), wide(z, 3, 2)
+    close("y", ops.m3_gated_norm(xs, zs, off(w), y=off(x), **kw), want["y"], mag["y"], k)
+    got = ops.m3_gated_norm_backward(xs, zs, off(w), dy=off(dy), out=dict(dx=off(x), dz=off(x), dw=off(w)), **kw)
+    for name, extra in (("dx", k), ("dz", k), ("dw", M)):
+        close(name, got[name], want[name], mag[name], k + extra)
+    want, mag = ref.residual_norm(x, res, w, scale, eps=1e-5), ref.residual_norm(x, res, w, scale, eps=1e-5, mag=True)
+    got = ops.m3_residual_norm(xs, off(res), off(w), off(scale), y=off(x), residual_out=off(x), eps=1e-5)
+    close("residual", got["residual"], want["residual"], mag["residual"], 2)
+    close("y", got["y"], want["y"], mag["y"], D + 20)
+    h, dr = off(got["residual"]), off(m(M, D, dtype=t))
+    want, mag = (ref.residual_norm_backward(h, x, w, scale, dy, dr, eps=1e-5, mag=q) for q in (False, True))
+    bw = ops.m3_residual_norm_backward(h, xs, off(w), off(scale), dy=off(dy), dresidual=dr, eps=1e-5,
+                                       out=dict(dx=off(x), dresidual=off(x), dw=off(w), dscale=off(w)))
+    for name, extra in (("dresidual", 0), ("dx", 0), ("dw", M), ("dscale", M)):
+        close(name, bw[name], want[name], mag[name], 2 * (D + 20) + extra)
+
+
+@pytest.mark.parametrize("at", [0, 1021, 1022, 1023, 1029])
+def test_infinity_in_a_shared_word(ops, at):
+    """A row of 1030 ends in a word that shares two elements with the one before: an
+    infinity there counts once, so the row's other outputs are zeros, not NaN."""
+    x = Maker(44)(3, 1030, dtype=torch.bfloat16)
+    x[1, at] = float("inf")
+    y = ops.m3_gated_norm(x)
+    r = ops.m3_residual_norm(x)["y"]
+    for o in (y, r):
+        keep = torch.arange(1030, device="cuda") != at
+        assert (o[1, keep] == 0).all() and o[1, at].isnan()
+        assert o[0].isfinite().all() and o[2].isfinite().all() and (o[0] != 0).any()
