@@ -69,6 +69,42 @@ __device__ __forceinline__ void store_pack(T* p, const float* v) {
   }
   *reinterpret_cast<Pack<T, V>*>(p) = o;
 }
+// The same with the alignment of T only, in the widest accesses all the same (vector
+// types, which the compiler keeps whole, unlike a struct).
+template <int BYTES>
+struct Loose {
+  typedef uint32_t whole __attribute__((ext_vector_type(BYTES / 4)));
+  typedef whole type __attribute__((aligned(2), may_alias));
+};
+template <>
+struct Loose<4> {
+  typedef uint32_t whole;
+  typedef whole type __attribute__((aligned(2), may_alias));
+};
+template <typename T, int V>
+__device__ __forceinline__ Pack<T, V> load_loose(const T* p) {
+  constexpr int kBytes = int(sizeof(T)) * V, kStep = kBytes < 16 ? kBytes : 16;
+  static_assert(kBytes >= 4, "a dword at least");
+  Pack<T, V> q;
+#pragma unroll
+  for (int i = 0; i < kBytes / kStep; ++i) {
+    const typename Loose<kStep>::whole w = reinterpret_cast<const typename Loose<kStep>::type*>(p)[i];
+    __builtin_memcpy(reinterpret_cast<char*>(&q) + kStep * i, &w, kStep);
+  }
+  return q;
+}
+template <typename T, int V>
+__device__ __forceinline__ void store_loose(T* p, const float* v) {
+  constexpr int kBytes = int(sizeof(T)) * V, kStep = kBytes < 16 ? kBytes : 16;
+  Pack<T, V> q;
+  store_pack<T, V>(q.e, v);
+#pragma unroll
+  for (int i = 0; i < kBytes / kStep; ++i) {
+    typename Loose<kStep>::whole w;
+    __builtin_memcpy(&w, reinterpret_cast<const char*>(&q) + kStep * i, kStep);
+    reinterpret_cast<typename Loose<kStep>::type*>(p)[i] = w;
+  }
+}
 template <typename T, int V>
 __device__ __forceinline__ void unpack(const Pack<T, V>& q, float* v) {
 #pragma unroll

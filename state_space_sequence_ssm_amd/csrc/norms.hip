@@ -105,32 +105,15 @@ struct Place {
   // sums as a whole)
   __device__ __forceinline__ bool counts(int i, int j) const { return !RAG || j >= skip[i]; }
 };
-// A word, aligned or with the alignment of its elements.
-typedef uint32_t quad_t __attribute__((ext_vector_type(4)));  // kept whole by the compiler, unlike a struct
-typedef quad_t loose_quad_t __attribute__((aligned(2), may_alias));
 template <typename T, int V, bool RAG>
 __device__ __forceinline__ Pack<T, V> load_word(const T* p) {
-  if constexpr (!RAG) return load_pack<T, V>(p);
-  static_assert(sizeof(T) * V % 16 == 0 || !RAG, "whole quads");
-  Pack<T, V> q;
-#pragma unroll
-  for (int i = 0; i < int(sizeof(T) * V / 16); ++i) {
-    const quad_t w = reinterpret_cast<const loose_quad_t*>(p)[i];
-    __builtin_memcpy(reinterpret_cast<char*>(&q) + 16 * i, &w, 16);
-  }
-  return q;
+  if constexpr (RAG) return load_loose<T, V>(p);
+  else return load_pack<T, V>(p);
 }
 template <typename T, int V, bool RAG>
 __device__ __forceinline__ void store_word(T* p, const float* v) {
-  if constexpr (!RAG) return store_pack<T, V>(p, v);
-  Pack<T, V> q;
-  store_pack<T, V>(q.e, v);
-#pragma unroll
-  for (int i = 0; i < int(sizeof(T) * V / 16); ++i) {
-    quad_t w;
-    __builtin_memcpy(&w, reinterpret_cast<const char*>(&q) + 16 * i, 16);
-    reinterpret_cast<loose_quad_t*>(p)[i] = w;
-  }
+  if constexpr (RAG) store_loose<T, V>(p, v);
+  else store_pack<T, V>(p, v);
 }
 // A gain's values at a lane's words (1 without one).
 template <int V, int NR, bool RAG>

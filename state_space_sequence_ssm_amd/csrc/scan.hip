@@ -51,7 +51,7 @@ struct Four {
 // compute unit holds two blocks where there are as many.  Bt 8, L 4096, D 2048, N 16
 // bf16, gated: 290-320 us with the clock, 29 vector instructions per token and wave
 // and the vector ALUs 83-87% busy; the recurrence's own instructions take 164 us.
-template <typename T, int NB, bool VEC, bool FULL>
+template <typename T, int NB, Words WD, bool FULL>
 __global__ __launch_bounds__(2 * kThreads, 4) void scan_kernel(ScanP p) {
   constexpr int CHB = CH / NB, VE = TT * CHB / kThreads, NP = 16 * NB;
   constexpr int YS = CHB == 16 ? 16 : CHB + 16;  // the four tokens' rows written together lie on different banks
@@ -166,7 +166,7 @@ __global__ __launch_bounds__(2 * kThreads, 4) void scan_kernel(ScanP p) {
     return;
   }
 
-  Stager<T, TT, CHB, NP, VEC, FULL, false, FULL> st;
+  Stager<T, TT, CHB, NP, WD, FULL, false, FULL> st;
   st.init(p.in, b, g, cb, tid, tend);
   const int r = st.r, c0 = st.c0;
   T* yp = FULL ? static_cast<T*>(p.y) + int64_t(b) * p.in.L * p.in.D + g * p.in.Dg : nullptr;
@@ -182,14 +182,14 @@ __global__ __launch_bounds__(2 * kThreads, 4) void scan_kernel(ScanP p) {
   auto stage = [&](int t0, auto half) {
     constexpr int o = decltype(half)::value;
     float de[VE], u[VE];
-    unpack<T, VE>(st.qd, de);
-    unpack<T, VE>(st.qx, u);
+    st.values(st.qd, de);
+    st.values(st.qx, u);
     if (p.softplus) {
 #pragma unroll
       for (int v = 0; v < VE; ++v) de[v] = softplus_fast(de[v] + bias[v]);
     }
     if constexpr (FULL) {
-      unpack<T, VE>(st.qz, gate[o]);
+      st.values(st.qz, gate[o]);
       if (st.gated) {
 #pragma unroll
         for (int v = 0; v < VE; ++v) gate[o][v] = silu_f(gate[o][v]);
@@ -227,7 +227,7 @@ __global__ __launch_bounds__(2 * kThreads, 4) void scan_kernel(ScanP p) {
 #pragma unroll
     for (int v = 0; v < VE; ++v) out[v] = (out[v] + skip[o][v]) * gate[o][v];
   };
-  auto store = [&](int t0) { store_cols<T, VE, VEC>(yp + int64_t(t0) * p.in.D + (uint32_t(r) * uint32_t(p.in.D) + st.cin), out, t0 + r < tend, st.ncol); };
+  auto store = [&](int t0) { store_cols<T, VE, WD>(yp + int64_t(t0) * p.in.D + (uint32_t(r) * uint32_t(p.in.D) + st.cin), out, t0 + r < tend, st.ncol); };
   auto step = [&](int i, auto half, auto other) {
     const int t0 = tbeg + i * TT;
     if constexpr (FULL)
@@ -372,7 +372,7 @@ Plan plan_of(const m3_scan_args& a) {
   return p;
 }
 
-template <typename T, int NB, bool VEC>
+template <typename T, int NB, Words WD>
 hipError_t run(const m3_scan_args& a, Plan pl, hipStream_t st) {
   if (a.workspace == nullptr) pl.nseg = 1, pl.seglen = a.L;
   const Inputs in{a.x, a.dt, a.z, a.B, a.C, nullptr, a.x_ld, a.dt_ld, a.z_ld, a.B_ld, a.C_ld, a.D_skip, a.dt_bias, a.L, a.D, a.N,
@@ -382,11 +382,11 @@ hipError_t run(const m3_scan_args& a, Plan pl, hipStream_t st) {
   if (pl.nseg > 1) {
     p.hend = static_cast<float*>(a.workspace);
     p.sdel = p.hend + int64_t(pl.nseg - 1) * a.Bt * a.D * a.N;
-    scan_kernel<T, NB, VEC, false><<<uint32_t(per * (pl.nseg - 1)), 2 * kThreads, 0, st>>>(p);
+    scan_kernel<T, NB, WD, false><<<uint32_t(per * (pl.nseg - 1)), 2 * kThreads, 0, st>>>(p);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
-  scan_kernel<T, NB, VEC, true><<<uint32_t(per * pl.nseg), 2 * kThreads, 0, st>>>(p);
+  scan_kernel<T, NB, WD, true><<<uint32_t(per * pl.nseg), 2 * kThreads, 0, st>>>(p);
   return hipGetLastError();
 }
 template <typename T, int S, int NI, bool VEC>
@@ -404,10 +404,15 @@ hipError_t step_items(const m3_scan_step_args& a, hipStream_t st) {
   return run_step<T, S, 1, VEC>(a, st);
 }
 
-template <typename T, bool VEC>
+template <typename T, Words WD>
 hipError_t by_states(const m3_scan_args& a, const Plan& p, hipStream_t st) {
-  if (p.NB == 1) return run<T, 1, VEC>(a, p, st);
-  return p.NB == 2 ? run<T, 2, VEC>(a, p, st) : run<T, 4, VEC>(a, p, st);
+  if (p.NB == 1) return run<T, 1, WD>(a, p, st);
+  return p.NB == 2 ? run<T, 2, WD>(a, p, st) : run<T, 4, WD>(a, p, st);
+}
+template <typename T>
+hipError_t by_words(const m3_scan_args& a, const Plan& p, Words w, hipStream_t st) {
+  if (w == kAligned) return by_states<T, kAligned>(a, p, st);
+  return w == kLoose ? by_states<T, kLoose>(a, p, st) : by_states<T, kSingle>(a, p, st);
 }
 template <typename T, bool VEC>
 hipError_t step_by_lanes(const m3_scan_step_args& a, hipStream_t st) {
@@ -429,11 +434,11 @@ hipError_t launch_scan(const m3_scan_args& a, hipStream_t s) {
   const size_t e = bf ? 2 : 4;
   const scan::Plan p = scan::plan_of(a);
   // four channels, and four values of B or C, as whole words
-  const bool vec = (a.D / a.G) % 4 == 0 && a.N % 4 == 0 && rows_aligned(a.x, a.x_ld, e, 4 * e) &&
+  const bool aligned = (a.D / a.G) % 4 == 0 && a.N % 4 == 0 && rows_aligned(a.x, a.x_ld, e, 4 * e) &&
                    rows_aligned(a.dt, a.dt_ld, e, 4 * e) && rows_aligned(a.z, a.z_ld, e, 4 * e) && rows_aligned(a.y, a.D, e, 4 * e) &&
                    rows_aligned(a.B, a.B_ld, e, 4 * e) && rows_aligned(a.C, a.C_ld, e, 4 * e);
-  if (bf) return vec ? scan::by_states<bf16_t, true>(a, p, s) : scan::by_states<bf16_t, false>(a, p, s);
-  return vec ? scan::by_states<float, true>(a, p, s) : scan::by_states<float, false>(a, p, s);
+  const scan::Words w = scan::words_of(a.D / a.G, a.N, aligned);
+  return bf ? scan::by_words<bf16_t>(a, p, w, s) : scan::by_words<float>(a, p, w, s);
 }
 hipError_t launch_scan_step(const m3_scan_step_args& a, hipStream_t s) {
   const bool bf = a.in_dtype == M3_BF16;

@@ -113,7 +113,7 @@ struct Four {
 
 // First walk: states in front of the tiles, and with SEG the segments' ends.  Bt 8,
 // L 2048, D 2048, N 16 bf16, uncut: 113 us.
-template <typename T, int NB, bool VEC, bool SEG>
+template <typename T, int NB, Words WD, bool SEG>
 __global__ __launch_bounds__(2 * kThreads) void states_kernel(BwP p) {
   constexpr int TT = 32, CHB = CH / NB, VE = TT * CHB / kThreads, NP = 16 * NB;
   __shared__ __align__(16) float dl[2][TT][CHB];
@@ -197,15 +197,15 @@ __global__ __launch_bounds__(2 * kThreads) void states_kernel(BwP p) {
     return;
   }
 
-  Stager<T, TT, CHB, NP, VEC, SEG, SEG, SEG> st;
+  Stager<T, TT, CHB, NP, WD, SEG, SEG, SEG> st;
   st.init(p.in, w.b, w.g, w.cb, tid, w.tend);
   float bias[VE];
 #pragma unroll
   for (int v = 0; v < VE; ++v) bias[v] = p.in.dtb != nullptr && v < st.ncol ? p.in.dtb[w.g * p.in.Dg + st.cin + v] : 0.f;
   auto stage = [&](int t0, int o) {
     float de[VE], u[VE], go[VE];
-    unpack<T, VE>(st.qd, de);
-    unpack<T, VE>(st.qx, u);
+    st.values(st.qd, de);
+    st.values(st.qx, u);
     if (p.softplus) {
 #pragma unroll
       for (int v = 0; v < VE; ++v) de[v] = softplus_fast(de[v] + bias[v]);
@@ -214,8 +214,8 @@ __global__ __launch_bounds__(2 * kThreads) void states_kernel(BwP p) {
     for (int v = 0; v < VE; ++v) u[v] *= de[v];
     if constexpr (SEG) {
       float zv[VE];
-      unpack<T, VE>(st.qy, go);
-      unpack<T, VE>(st.qz, zv);
+      st.values(st.qy, go);
+      st.values(st.qz, zv);
       if (st.gated) {
 #pragma unroll
         for (int v = 0; v < VE; ++v) go[v] *= silu_f(zv[v]);
@@ -282,7 +282,7 @@ struct Shared {
 // for the recurrences and sums, 22 of them the sums of dB and dC over channels, and
 // about 17 for staging.  250 registers leave a compute unit one block.  Bt 8, L 2048,
 // D 2048, N 16 bf16: 410-435 us.
-template <typename T, int NB, bool VEC>
+template <typename T, int NB, Words WD>
 __global__ __launch_bounds__(2 * kThreads) void reverse_kernel(BwP p) {
   constexpr int CHB = CH / NB, VE = TB * CHB / kThreads, NP = 16 * NB;
   extern __shared__ __align__(16) unsigned char smem[];
@@ -417,7 +417,7 @@ __global__ __launch_bounds__(2 * kThreads) void reverse_kernel(BwP p) {
     return;
   }
 
-  Stager<T, TB, CHB, NP, VEC, true, true, true> st;
+  Stager<T, TB, CHB, NP, WD, true, true, true> st;
   st.init(p.in, w.b, w.g, w.cb, tid, w.tend);
   const int r = st.r, c0 = st.c0;
   const int64_t out0 = int64_t(w.b) * p.in.L * p.in.D + w.g * p.in.Dg;
@@ -439,9 +439,9 @@ __global__ __launch_bounds__(2 * kThreads) void reverse_kernel(BwP p) {
 #pragma unroll
     for (int v = 0; v < VE; ++v) zero[v] = 0.f;
     const int64_t at = int64_t(t) * p.in.D + st.cin;
-    store_cols<T, VE, VEC>(dxp + at, zero, true, st.ncol);
-    store_cols<T, VE, VEC>(ddtp + at, zero, true, st.ncol);
-    if (dzp != nullptr) store_cols<T, VE, VEC>(dzp + at, zero, true, st.ncol);
+    store_cols<T, VE, WD>(dxp + at, zero, true, st.ncol);
+    store_cols<T, VE, WD>(ddtp + at, zero, true, st.ncol);
+    if (dzp != nullptr) store_cols<T, VE, WD>(dzp + at, zero, true, st.ncol);
   }
   // this thread's four of the tile's sums of dB and dC, those past the tile repeating it
   constexpr int kSums = TB * 2 * NP, NS = kSums > 4 * kThreads ? kSums / (4 * kThreads) : 1;
@@ -452,10 +452,10 @@ __global__ __launch_bounds__(2 * kThreads) void reverse_kernel(BwP p) {
   auto stage = [&](int t0, auto half) {
     constexpr int o = decltype(half)::value;
     float u[VE], zv[VE];
-    unpack<T, VE>(st.qx, kx[o]);
-    unpack<T, VE>(st.qd, kd[o]);
-    unpack<T, VE>(st.qy, kg[o]);
-    unpack<T, VE>(st.qz, zv);
+    st.values(st.qx, kx[o]);
+    st.values(st.qd, kd[o]);
+    st.values(st.qy, kg[o]);
+    st.values(st.qz, zv);
     if (p.softplus) {
 #pragma unroll
       for (int v = 0; v < VE; ++v) kd[o][v] = softplus_sigmoid(kd[o][v] + bias[v], ks[o][v]);
@@ -543,9 +543,9 @@ __global__ __launch_bounds__(2 * kThreads) void reverse_kernel(BwP p) {
   auto store = [&](int t0) {
     const bool row = t0 + r < w.tend;
     const int64_t at = int64_t(t0) * p.in.D;
-    store_cols<T, VE, VEC>(dxp + at + oo, ox, row, st.ncol);
-    store_cols<T, VE, VEC>(ddtp + at + oo, od, row, st.ncol);
-    if (dzp != nullptr) store_cols<T, VE, VEC>(dzp + at + oo, oz, row, st.ncol);
+    store_cols<T, VE, WD>(dxp + at + oo, ox, row, st.ncol);
+    store_cols<T, VE, WD>(ddtp + at + oo, od, row, st.ncol);
+    if (dzp != nullptr) store_cols<T, VE, WD>(dzp + at + oo, oz, row, st.ncol);
     float* bt = bcp + t0 * bcrow;
 #pragma unroll
     for (int q = 0; q < NS; ++q) {
@@ -668,7 +668,7 @@ Plan plan_of(const m3_scan_args& f) {
   return p;
 }
 
-template <typename T, int NB, bool VEC>
+template <typename T, int NB, Words WD>
 hipError_t run(const m3_scan_backward_args& a, const Plan& pl, hipStream_t st) {
   static std::atomic<uint64_t> cleared{0};
   const m3_scan_args& f = a.fwd;
@@ -679,13 +679,13 @@ hipError_t run(const m3_scan_backward_args& a, const Plan& pl, hipStream_t st) {
   const BwP p{in, f.A, f.h0, a.dh_final, f.lengths, a.dx, a.ddt, a.dz, a.dh0, at(pl.oCk), at(pl.oCd), at(pl.oHe), at(pl.oGs),
               at(pl.oSd), at(pl.oBc), at(pl.oPart), f.Bt, pl.nblk, pl.nseg, pl.seglen, f.dt_softplus};
   const uint32_t grid = uint32_t(pl.blocks * pl.nseg);
-  if (pl.nseg > 1) states_kernel<T, NB, VEC, true><<<grid, 2 * kThreads, 0, st>>>(p);
-  else states_kernel<T, NB, VEC, false><<<grid, 2 * kThreads, 0, st>>>(p);
+  if (pl.nseg > 1) states_kernel<T, NB, WD, true><<<grid, 2 * kThreads, 0, st>>>(p);
+  else states_kernel<T, NB, WD, false><<<grid, 2 * kThreads, 0, st>>>(p);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  e = allow_lds(reinterpret_cast<const void*>(&reverse_kernel<T, NB, VEC>), sizeof(Shared<NB>), cleared);
+  e = allow_lds(reinterpret_cast<const void*>(&reverse_kernel<T, NB, WD>), sizeof(Shared<NB>), cleared);
   if (e != hipSuccess) return e;
-  reverse_kernel<T, NB, VEC><<<grid, 2 * kThreads, sizeof(Shared<NB>), st>>>(p);
+  reverse_kernel<T, NB, WD><<<grid, 2 * kThreads, sizeof(Shared<NB>), st>>>(p);
   e = hipGetLastError();
   if (e != hipSuccess) return e;
   const int64_t rows = int64_t(f.Bt) * f.L, items = rows * f.G * 2 * 16 * NB;
@@ -706,10 +706,15 @@ hipError_t run(const m3_scan_backward_args& a, const Plan& pl, hipStream_t st) {
   return launch_colsum(c, st);
 }
 
-template <typename T, bool VEC>
+template <typename T, Words WD>
 hipError_t by_states(const m3_scan_backward_args& a, const Plan& p, hipStream_t st) {
-  if (p.NB == 1) return run<T, 1, VEC>(a, p, st);
-  return p.NB == 2 ? run<T, 2, VEC>(a, p, st) : run<T, 4, VEC>(a, p, st);
+  if (p.NB == 1) return run<T, 1, WD>(a, p, st);
+  return p.NB == 2 ? run<T, 2, WD>(a, p, st) : run<T, 4, WD>(a, p, st);
+}
+template <typename T>
+hipError_t by_words(const m3_scan_backward_args& a, const Plan& p, Words w, hipStream_t st) {
+  if (w == kAligned) return by_states<T, kAligned>(a, p, st);
+  return w == kLoose ? by_states<T, kLoose>(a, p, st) : by_states<T, kSingle>(a, p, st);
 }
 
 }  // namespace
@@ -722,12 +727,12 @@ hipError_t launch_scan_backward(const m3_scan_backward_args& a, hipStream_t s) {
   const size_t e = bf ? 2 : 4;
   const scan::Plan p = scan::plan_of(f);
   // four channels, and four values of B or C, as whole words
-  const bool vec = (f.D / f.G) % 4 == 0 && f.N % 4 == 0 && rows_aligned(f.x, f.x_ld, e, 4 * e) &&
+  const bool aligned = (f.D / f.G) % 4 == 0 && f.N % 4 == 0 && rows_aligned(f.x, f.x_ld, e, 4 * e) &&
                    rows_aligned(f.dt, f.dt_ld, e, 4 * e) && rows_aligned(f.z, f.z_ld, e, 4 * e) && rows_aligned(a.dy, f.D, e, 4 * e) &&
                    rows_aligned(a.dx, f.D, e, 4 * e) && rows_aligned(a.ddt, f.D, e, 4 * e) && rows_aligned(a.dz, f.D, e, 4 * e) &&
                    rows_aligned(f.B, f.B_ld, e, 4 * e) && rows_aligned(f.C, f.C_ld, e, 4 * e);
-  if (bf) return vec ? scan::by_states<bf16_t, true>(a, p, s) : scan::by_states<bf16_t, false>(a, p, s);
-  return vec ? scan::by_states<float, true>(a, p, s) : scan::by_states<float, false>(a, p, s);
+  const scan::Words w = scan::words_of(f.D / f.G, f.N, aligned);
+  return bf ? scan::by_words<bf16_t>(a, p, w, s) : scan::by_words<float>(a, p, w, s);
 }
 
 }  // namespace m3

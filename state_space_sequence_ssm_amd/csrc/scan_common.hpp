@@ -69,40 +69,71 @@ __device__ __forceinline__ float rows_sum4(const float* v) {
   const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(lo), __float_as_uint(hi), false, false);
   return __uint_as_float(r[0]) + __uint_as_float(r[1]);
 }
-// VE neighbouring values, `ncol` of them inside (any number; at least one word for
-// a load), in words of four (VEC) or one at a time.  The loads have no branch
-// around them (a branch makes the compiler wait for the values at its end): words
-// past the edge are read from the first one and dropped later.
-template <int VE, bool VEC>
+// How VE neighbouring values are moved: in aligned words of four; in words of four
+// with the alignment of the type (widths, state sizes or rows that are no multiples);
+// or one at a time, where there are fewer than four channels or states.  8192 tokens
+// of 2047 channels fp32 take 154 us in loose words, 253 us one at a time; aligned, 2048 take 140 us.
+enum Words { kSingle, kLoose, kAligned };
+template <int VE, Words WD>
 constexpr int word() {
-  return !VEC ? 1 : VE < 4 ? VE : 4;
+  return WD == kSingle ? 1 : VE < 4 ? VE : 4;
 }
-template <typename T, int VE, bool VEC>
+// VE neighbouring values, `ncol` of them inside (any number).  The loads have no
+// branch around them (a branch makes the compiler wait for the values at its end): words
+// past the edge are read from inside and dropped later, and a loose word across the edge
+// is moved back to end there, for unpack_cols to turn.
+template <typename T, int VE, Words WD>
 __device__ __forceinline__ Pack<T, VE> fetch_cols(const T* p, int ncol) {
-  constexpr int VW = word<VE, VEC>();
+  constexpr int VW = word<VE, WD>();
   Pack<T, VE> q;
+  if constexpr (WD == kLoose && VW > 1) asm volatile("" : "+v"(ncol));
 #pragma unroll
   for (int v = 0; v < VE; v += VW) {
-    const Pack<T, VW> o = load_pack<T, VW>(p + (v < ncol ? v : 0));
+    Pack<T, VW> o;
+    if constexpr (WD == kLoose && VW > 1) o = load_loose<T, VW>(p + (v + VW <= ncol ? v : ncol > 0 ? ncol - VW : 0));
+    else o = load_pack<T, VW>(p + (v < ncol ? v : 0));
 #pragma unroll
     for (int i = 0; i < VW; ++i) q.e[v + i] = o.e[i];
   }
   return q;
 }
-template <typename T, int VE, bool VEC>
+template <typename T, int VE, Words WD>
+__device__ __forceinline__ void unpack_cols(const Pack<T, VE>& q, float* f, int ncol) {
+  constexpr int VW = word<VE, WD>();
+  unpack<T, VE>(q, f);
+  if constexpr (WD == kLoose && VW > 1) {
+    if (ncol >= VE) return;
+    asm volatile("" : "+v"(ncol));  // computed here, not kept in registers over the tiles
+#pragma unroll
+    for (int v = 0; v < VE; v += VW) {
+      const int back = v + VW - ncol;  // values of the word before it, in front
+#pragma unroll
+      for (int k = 1; k < VW; ++k) {
+#pragma unroll
+        for (int i = v; i + 1 < v + VW; ++i) f[i] = back >= k && back < VW ? f[i + 1] : f[i];
+      }
+    }
+  }
+}
+template <typename T, int VE, Words WD>
 __device__ __forceinline__ void store_cols(T* p, const float* v, bool row, int ncol) {
-  constexpr int VW = word<VE, VEC>();
+  constexpr int VW = word<VE, WD>(), VP = WD == kLoose ? 1 : VW;  // VP: at the edge
   if (row && VE <= ncol) {
     if constexpr (VW > 1 || VE == 1) {
 #pragma unroll
-      for (int i = 0; i < VE; i += VW) store_pack<T, VW>(p + i, v + i);
+      for (int i = 0; i < VE; i += VW) {
+        if constexpr (WD == kLoose && VW > 1) store_loose<T, VW>(p + i, v + i);
+        else store_pack<T, VW>(p + i, v + i);
+      }
       return;
     }
   }
 #pragma unroll
-  for (int i = 0; i < VE; i += VW)
-    if (row && i < ncol) store_pack<T, VW>(p + i, v + i);
+  for (int i = 0; i < VE; i += VP)
+    if (row && i < ncol) store_pack<T, VP>(p + i, v + i);
 }
+// The words for widths of Dg and N; `aligned`: every row and width at whole words.
+inline Words words_of(int Dg, int N, bool aligned) { return aligned ? kAligned : Dg >= 4 && N >= 4 ? kLoose : kSingle; }
 // The tensors of a call as the kernels take them.
 struct Inputs {
   const void* x;
@@ -121,7 +152,7 @@ struct Inputs {
 // VE neighbouring channels of token r of each tensor, and quads of B (and C).
 // fetch() starts the loads of a tile into registers; the values are used a tile
 // later.  Z, DY, CC: whether z, dy and C are wanted.
-template <typename T, int TT, int CHB, int NP, bool VEC, bool Z, bool DY, bool CC>
+template <typename T, int TT, int CHB, int NP, Words WD, bool Z, bool DY, bool CC>
 struct Stager {
   static constexpr int VE = TT * CHB / kThreads;
   static constexpr int kQuads = (CC ? 2 : 1) * TT * NP / 4, NQ = (kQuads + kThreads - 1) / kThreads;
@@ -184,21 +215,22 @@ struct Stager {
 #pragma unroll
     for (int i = 0; i < NQ; ++i) pq[i] = oq[i];
     if (tend - 1 - tb < TT - 1) place(int(tend - 1 - tb), px, pdt, pz, pdy, pq);
-    qx = fetch_cols<T, VE, VEC>(x + tb * xld + px, ncol);
-    qd = fetch_cols<T, VE, VEC>(dt + tb * dtld + pdt, ncol);
-    if constexpr (Z) qz = fetch_cols<T, VE, VEC>(z + tb * zld + pz, ncol);
-    if constexpr (DY) qy = fetch_cols<T, VE, VEC>(dy + tb * dyld + pdy, ncol);
+    qx = fetch_cols<T, VE, WD>(x + tb * xld + px, ncol);
+    qd = fetch_cols<T, VE, WD>(dt + tb * dtld + pdt, ncol);
+    if constexpr (Z) qz = fetch_cols<T, VE, WD>(z + tb * zld + pz, ncol);
+    if constexpr (DY) qy = fetch_cols<T, VE, WD>(dy + tb * dyld + pdy, ncol);
 #pragma unroll
     for (int i = 0; i < NQ; ++i) {
-      qb[i] = fetch_cols<T, 4, VEC>((qc[i] ? C + tb * Cld : B + tb * Bld) + pq[i], N - qn[i]);
+      qb[i] = fetch_cols<T, 4, WD>((qc[i] ? C + tb * Cld : B + tb * Bld) + pq[i], N - qn[i]);
     }
   }
+  __device__ __forceinline__ void values(const Pack<T, VE>& q, float* f) const { unpack_cols<T, VE, WD>(q, f, ncol); }
   // B and C of the fetched tile to LDS [2][TT][NP]; zeros past the end and past N
   __device__ __forceinline__ void put_bc(int t0, float* bc) const {
 #pragma unroll
     for (int i = 0; i < NQ; ++i) {
       float f[4];
-      unpack<T, 4>(qb[i], f);
+      unpack_cols<T, 4, WD>(qb[i], f, N - qn[i]);
       if (t0 + TT > tend || N < NP) {
 #pragma unroll
         for (int k = 0; k < 4; ++k) f[k] = qn[i] + k < N && t0 + qt[i] < tend ? f[k] : 0.f;

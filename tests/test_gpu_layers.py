@@ -196,7 +196,7 @@ def _scan_inputs(c, seed):
     A = -torch.exp(torch.rand(D, N, generator=m.g) * 2.77).cuda()
     q = {k: None if v is None else spoil(v, lengths) for k, v in q.items()}
     if strided:
-        q = {k: None if v is None else wide(v) for k, v in q.items()}
+        q = {k: None if v is None else wide(v, *(strided if isinstance(strided, tuple) else ())) for k, v in q.items()}
     q["B"], q["C"] = q["B"].unflatten(-1, (G, N)), q["C"].unflatten(-1, (G, N))
     q.update(A=A, D=m(D) if hd else None, h0=m(Bt, D, N, scale=0.5) if hh else None, dt_bias=m(D, shift=-3.0) if hb else None)
     return q, m
@@ -434,3 +434,21 @@ def test_infinity_in_a_shared_word(ops, at):
         keep = torch.arange(1030, device="cuda") != at
         assert (o[1, keep] == 0).all() and o[1, at].isnan()
         assert o[0].isfinite().all() and o[2].isfinite().all() and (o[0] != 0).any()
+
+
+# Widths that leave one, two or three channels of a word, and fewer than one, in every
+# block of channels (64, 32 and 16 of them); state sizes that end inside a word; rows
+# an element or two off a word.
+SCAN_OFF = [(D, N, G, dt, off) for D, N, G, dt, off in [
+    (65, 16, 1, "bf16", (1, 2)), (66, 15, 1, "f32", (2, 1)), (67, 14, 1, "bf16", False), (71, 13, 1, "f32", False), (5, 4, 1, "bf16", (3, 0)),
+    (4, 5, 1, "f32", (1, 0)), (33, 17, 1, "bf16", (1, 2)), (35, 31, 1, "f32", False), (38, 30, 2, "bf16", (1, 1)), (17, 33, 1, "f32", (1, 0)),
+    (18, 62, 1, "bf16", False), (19, 63, 1, "f32", (1, 1)), (21, 61, 3, "bf16", (5, 2)), (64, 16, 1, "bf16", (1, 0)), (64, 16, 2, "f32", (1, 3)),
+    (3, 16, 1, "bf16", (1, 0)), (64, 3, 1, "f32", (1, 0)), (1, 1, 1, "bf16", False), (2, 2, 1, "f32", (1, 0))]]
+
+
+@pytest.mark.parametrize("D,N,G,dt,off", SCAN_OFF)
+def test_scans_off_alignment(ops, D, N, G, dt, off):
+    for Bt, L, lengths in ((1, 1, None), (2, 65, [65, 34]), (1, 290, None)):
+        c = (Bt, L, D, N, G, dt, lengths, True, True, True, True, True, off)
+        test_scan(ops, c)
+        test_scan_backward(ops, c)
