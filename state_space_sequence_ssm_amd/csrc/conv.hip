@@ -318,36 +318,10 @@ __global__ __launch_bounds__(256) void conv_backward_kernel(ConvBwP p) {
   }
 }
 
-// Column sums: a block takes COLS columns, its 1024 / COLS row groups every so
-// many-th partial row, joined in LDS.  Few columns per block for many rows, so
-// that a narrow matrix still fills the card (64-byte pieces of a row).
 template <int COLS>
 __global__ __launch_bounds__(1024) void colsum_kernel(ColSum c) {
-  constexpr int RG = 1024 / COLS;
-  __shared__ float red[RG][COLS];
-  const int lane = threadIdx.x % COLS, rg = threadIdx.x / COLS;
-  const int64_t col = int64_t(blockIdx.x) * COLS + lane;
-  float s = 0.f;
-  if (col < c.ncols) {
-#pragma unroll 4
-    for (int64_t r = rg; r < c.P; r += RG) s += c.part[r * c.ncols + col];
-  }
-  red[rg][lane] = s;
-  for (int n = RG / 2; n > 0; n /= 2) {
-    __syncthreads();
-    if (rg < n) red[rg][lane] += red[rg + n][lane];
-  }
-  if (rg != 0 || col >= c.ncols) return;
-  s = red[0][lane];
-  int64_t k = col;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    if (k < c.n[i]) {
-      if (c.dst[i] != nullptr) c.dst[i][i == 0 && c.taps > 0 ? (k % c.D) * c.taps + k / c.D : k] = s;
-      return;
-    }
-    k -= c.n[i];
-  }
+  __shared__ float red[1024];
+  colsum_block<COLS>(c, blockIdx.x, red);
 }
 
 // Tokens per tile.  Long tiles read fewer rows twice (W - 1 of tt + W - 1) and
@@ -437,8 +411,8 @@ hipError_t run_bw(const m3_conv_backward_args& a, hipStream_t s) {
 }  // namespace
 
 hipError_t launch_colsum(const ColSum& c, hipStream_t s) {
-  if (c.P > 32) colsum_kernel<16><<<uint32_t((c.ncols + 15) / 16), 1024, 0, s>>>(c);
-  else colsum_kernel<128><<<uint32_t((c.ncols + 127) / 128), 1024, 0, s>>>(c);
+  if (colsum_cols(c) == 16) colsum_kernel<16><<<colsum_blocks(c), 1024, 0, s>>>(c);
+  else colsum_kernel<128><<<colsum_blocks(c), 1024, 0, s>>>(c);
   return hipGetLastError();
 }
 

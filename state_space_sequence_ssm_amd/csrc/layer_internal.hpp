@@ -155,4 +155,38 @@ inline bool rows_aligned(const void* p, int64_t ld, size_t elem, size_t bytes) {
 }
 inline size_t round256(size_t v) { return (v + 255) & ~size_t(255); }
 
+
+// Column sums: a block of 1024 threads takes COLS columns, its 1024 / COLS row groups
+// every so many-th partial row, joined in LDS.  Few columns per block for many rows, so
+// that a narrow matrix still fills the card (64-byte pieces of a row).
+inline int colsum_cols(const ColSum& c) { return c.P > 32 ? 16 : 128; }
+inline uint32_t colsum_blocks(const ColSum& c) { return uint32_t((c.ncols + colsum_cols(c) - 1) / colsum_cols(c)); }
+template <int COLS>
+__device__ __forceinline__ void colsum_block(const ColSum& c, uint32_t block, float* red) {
+  constexpr int RG = 1024 / COLS;
+  const int lane = threadIdx.x % COLS, rg = threadIdx.x / COLS;
+  const int64_t col = int64_t(block) * COLS + lane;
+  float s = 0.f;
+  if (col < c.ncols) {
+#pragma unroll 4
+    for (int64_t r = rg; r < c.P; r += RG) s += c.part[r * c.ncols + col];
+  }
+  red[threadIdx.x] = s;
+  for (int n = RG / 2; n > 0; n /= 2) {
+    __syncthreads();
+    if (rg < n) red[threadIdx.x] += red[threadIdx.x + n * COLS];
+  }
+  if (rg != 0 || col >= c.ncols) return;
+  s = red[lane];
+  int64_t k = col;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if (k < c.n[i]) {
+      if (c.dst[i] != nullptr) c.dst[i][i == 0 && c.taps > 0 ? (k % c.D) * c.taps + k / c.D : k] = s;
+      return;
+    }
+    k -= c.n[i];
+  }
+}
+
 }  // namespace m3

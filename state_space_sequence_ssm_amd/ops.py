@@ -311,15 +311,15 @@ def _refuse(t, dtype, shape, name, dev):
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if t.shape != shape:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
-    if t.device != dev:
-        raise ValueError(f"{name} is on {t.device}, expected {dev}")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} is on {t.device}, expected cuda:{dev}")
 
 
 def _dense(t, dtype, shape, name, dev):
-    """Address of a dense tensor (None: NULL) after checking it."""
+    """Address of a dense tensor (None: NULL) on device index `dev` after checking it."""
     if t is None:
         return None
-    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.device == dev):
+    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.get_device() == dev):
         _refuse(t, dtype, shape, name, dev)
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
@@ -332,7 +332,7 @@ def _rows(t, dtype, shape, lead, name, dev):
     throughout (0: dense)."""
     if t is None:
         return None, 0
-    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.device == dev):
+    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.get_device() == dev):
         _refuse(t, dtype, shape, name, dev)
     if t.is_contiguous():
         return t.data_ptr(), 0
@@ -356,14 +356,17 @@ def _rows(t, dtype, shape, lead, name, dev):
     return t.data_ptr(), ld
 
 
-def _new(given, shape, like, dtype=None):
-    """An output: the given tensor or a new one.  A dense tensor of the same shape
-    and type is the fastest pattern (1.2 us instead of 1.8)."""
+def _out(given, dtype, shape, name, like, dev):
+    """An output and its address: the given tensor after checking it, or a new one on
+    the device of `like` (an input that is checked itself).  A dense tensor of the same
+    shape and type is the fastest pattern (1.2 us instead of 1.8)."""
     if given is not None:
-        return given
-    if (dtype is None or dtype is like.dtype) and like.shape == shape and like.is_contiguous():
-        return torch.empty_like(like)
-    return torch.empty(shape, dtype=dtype or like.dtype, device=like.device)
+        return given, _dense(given, dtype, shape, name, dev)
+    if dtype is like.dtype and like.shape == shape and like.is_contiguous():
+        given = torch.empty_like(like)
+    else:
+        given = torch.empty(shape, dtype=dtype, device=like.device)
+    return given, given.data_ptr()
 
 
 # The current stream's handle without building a Stream object, which takes as
@@ -375,11 +378,15 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
 _calls = {}
 
 
-def _run_layer(name, args, dev):
+def _call_of(name):
     call = _calls.get(name)
     if call is None:
         call = _calls[name] = getattr(_lib.load(), name)
-    rc = call(ctypes.byref(args), _raw_stream(dev.index))
+    return call
+
+
+def _run_layer(name, args, dev):
+    rc = _call_of(name)(ctypes.byref(args), _raw_stream(dev))
     if rc != _lib.M3_OK:
         raise M3Error(rc, name)
 
@@ -387,11 +394,12 @@ def _run_layer(name, args, dev):
 def _take_workspace(name, args, given, dev):
     """Put a workspace of the size the library asks for into the arguments: the
     given uint8 tensor, or a new one.  Returns it (it must outlive the call)."""
-    need = getattr(_lib.load(), name + "_workspace_size")(ctypes.byref(args))
+    need = _call_of(name + "_workspace_size")(ctypes.byref(args))
     if given is None:
-        if need == 0:
-            return None
-        given = torch.empty(need, dtype=torch.uint8, device=dev)
+        if need != 0:
+            given = torch.empty(need, dtype=torch.uint8, device=dev)
+            args.workspace, args.workspace_bytes = given.data_ptr(), need
+        return given
     args.workspace = _dense(given, torch.uint8, given.shape, "workspace", dev)
     args.workspace_bytes = given.numel()
     return given
@@ -413,19 +421,17 @@ def m3_causal_conv(x, w, bias=None, state=None, *, lengths=None, silu=True, y=No
     one), for this and the following operators."""
     Bt, L, D = x.shape
     W = w.shape[-1]
-    dev, t = x.device, x.dtype
-    y = _new(y, (Bt, L, D), x)
-    if want_state:
-        state_out = _new(state_out, (Bt, W - 1, D), x)
+    dev, t = x.get_device(), x.dtype
     a = _lib.ConvArgs()
+    y, a.y = _out(y, t, (Bt, L, D), "y", x, dev)
+    if want_state or state_out is not None:
+        state_out, a.state_out = _out(state_out, t, (Bt, W - 1, D), "state_out", x, dev)
     a.Bt, a.L, a.D, a.W, a.in_dtype, a.silu = Bt, L, D, W, _dtype_code(x), 1 if silu else 0
     a.x, a.x_ld = _rows(x, t, x.shape, 2, "x", dev)
     a.w = _dense(w, _F32, (D, W), "w", dev)
     a.bias = _dense(bias, _F32, (D,), "bias", dev)
     a.lengths = _dense(lengths, torch.int32, (Bt,), "lengths", dev)
     a.state = _dense(state, t, (Bt, W - 1, D), "state", dev)
-    a.y = _dense(y, t, (Bt, L, D), "y", dev)
-    a.state_out = _dense(state_out, t, (Bt, W - 1, D), "state_out", dev)
     _run_layer("m3_causal_conv", a, dev)
     return dict(y=y, state=state_out)
 
@@ -436,16 +442,15 @@ def m3_causal_conv_step(state, x, w, bias=None, *, silu=True, y=None, state_out=
     place (or read only, the new one going to state_out).  Returns y [Bt, D]."""
     Bt, D = x.shape
     W = w.shape[-1]
-    dev, t = state.device, x.dtype
-    y = _new(y, (Bt, D), x)
+    dev, t = state.get_device(), x.dtype
     a = _lib.ConvStepArgs()
+    y, a.y = _out(y, t, (Bt, D), "y", x, dev)
     a.Bt, a.D, a.W, a.in_dtype, a.silu = Bt, D, W, _dtype_code(x), 1 if silu else 0
     a.x, a.x_ld = _rows(x, t, x.shape, 1, "x", dev)
     a.w = _dense(w, _F32, (D, W), "w", dev)
     a.bias = _dense(bias, _F32, (D,), "bias", dev)
     a.state = _dense(state, t, (Bt, W - 1, D), "state", dev)
     a.state_out = _dense(state_out, t, (Bt, W - 1, D), "state_out", dev)
-    a.y = _dense(y, t, (Bt, D), "y", dev)
     _run_layer("m3_causal_conv_step", a, dev)
     return y
 
@@ -458,12 +463,16 @@ def m3_causal_conv_backward(x, w, bias=None, state=None, *, dy, lengths=None, si
     want_state_grad, dstate.  `out`: optional dict of preallocated tensors."""
     Bt, L, D = x.shape
     W = w.shape[-1]
-    dev, t = x.device, x.dtype
+    dev, t = x.get_device(), x.dtype
     got = out or {}
-    out = dict(dx=_new(got.get("dx"), (Bt, L, D), x), dw=_new(got.get("dw"), (D, W), x, _F32),
-               dbias=_new(got.get("dbias"), (D,), x, _F32) if bias is not None else None,
-               dstate=_new(got.get("dstate"), (Bt, W - 1, D), x) if want_state_grad or "dstate" in got else None)
     a = _lib.ConvBackwardArgs()
+    out = dict(dx=None, dw=None, dbias=None, dstate=None)
+    out["dx"], a.dx = _out(got.get("dx"), t, (Bt, L, D), "dx", x, dev)
+    out["dw"], a.dw = _out(got.get("dw"), _F32, (D, W), "dw", x, dev)
+    if bias is not None:
+        out["dbias"], a.dbias = _out(got.get("dbias"), _F32, (D,), "dbias", x, dev)
+    if want_state_grad or "dstate" in got:
+        out["dstate"], a.dstate = _out(got.get("dstate"), t, (Bt, W - 1, D), "dstate", x, dev)
     a.Bt, a.L, a.D, a.W, a.in_dtype, a.silu = Bt, L, D, W, _dtype_code(x), 1 if silu else 0
     a.x, a.x_ld = _rows(x, t, x.shape, 2, "x", dev)
     a.w = _dense(w, _F32, (D, W), "w", dev)
@@ -471,19 +480,15 @@ def m3_causal_conv_backward(x, w, bias=None, state=None, *, dy, lengths=None, si
     a.lengths = _dense(lengths, torch.int32, (Bt,), "lengths", dev)
     a.state = _dense(state, t, (Bt, W - 1, D), "state", dev)
     a.dy = _dense(dy, t, (Bt, L, D), "dy", dev)
-    a.dx = _dense(out["dx"], t, (Bt, L, D), "dx", dev)
-    a.dw = _dense(out["dw"], _F32, (D, W), "dw", dev)
-    a.dbias = _dense(out["dbias"], _F32, (D,), "dbias", dev)
-    a.dstate = _dense(out["dstate"], t, (Bt, W - 1, D), "dstate", dev)
     workspace = _take_workspace("m3_causal_conv_backward", a, workspace, dev)
     _run_layer("m3_causal_conv_backward", a, dev)
     return out
 
 
-def _scan_inputs(a, lead, x, dt, A, B, C, D, z, dt_softplus, dt_bias):
+def _scan_inputs(a, dev, lead, x, dt, A, B, C, D, z, dt_softplus, dt_bias):
     """The inputs that the scan, its backward and its step share."""
     G, N = B.shape[-2:]
-    dev, t, shape = x.device, x.dtype, x.shape
+    t, shape = x.dtype, x.shape
     width, n, bc = shape[-1], len(lead), (*lead, G, N)
     a.D, a.N, a.G, a.in_dtype, a.dt_softplus = width, N, G, _dtype_code(x), 1 if dt_softplus else 0
     a.x, a.x_ld = _rows(x, t, shape, n, "x", dev)
@@ -510,17 +515,15 @@ def m3_selective_scan(x, dt, A, B, C, D=None, z=None, h0=None, *, lengths=None, 
     they were) and h: the last state [Bt, D, N]."""
     Bt, L, width = x.shape
     N = A.shape[-1]
-    dev, t = x.device, x.dtype
-    y = _new(y, (Bt, L, width), x)
-    if want_state:
-        h_final = _new(h_final, (Bt, width, N), x, _F32)
+    dev = x.get_device()
     a = _lib.ScanArgs()
+    y, a.y = _out(y, x.dtype, (Bt, L, width), "y", x, dev)
+    if want_state or h_final is not None:
+        h_final, a.h_final = _out(h_final, _F32, (Bt, width, N), "h_final", x, dev)
     a.Bt, a.L = Bt, L
-    _scan_inputs(a, (Bt, L), x, dt, A, B, C, D, z, dt_softplus, dt_bias)
+    _scan_inputs(a, dev, (Bt, L), x, dt, A, B, C, D, z, dt_softplus, dt_bias)
     a.h0 = _dense(h0, _F32, (Bt, width, N), "h0", dev)
     a.lengths = _dense(lengths, torch.int32, (Bt,), "lengths", dev)
-    a.y = _dense(y, t, (Bt, L, width), "y", dev)
-    a.h_final = _dense(h_final, _F32, (Bt, width, N), "h_final", dev)
     if workspace is not False:
         workspace = _take_workspace("m3_selective_scan", a, workspace, dev)
     _run_layer("m3_selective_scan", a, dev)
@@ -534,14 +537,13 @@ def m3_selective_scan_step(h, x, dt, A, B, C, D=None, z=None, *, dt_softplus=Fal
     h_out).  Returns y [Bt, D]."""
     Bt, width = x.shape
     N = A.shape[-1]
-    dev = h.device
-    y = _new(y, (Bt, width), x)
+    dev = h.get_device()
     a = _lib.ScanStepArgs()
+    y, a.y = _out(y, x.dtype, (Bt, width), "y", x, dev)
     a.Bt = Bt
-    _scan_inputs(a, (Bt,), x, dt, A, B, C, D, z, dt_softplus, dt_bias)
-    a.h = _dense(h, _F32, (Bt, width, N), "h", x.device)
+    _scan_inputs(a, dev, (Bt,), x, dt, A, B, C, D, z, dt_softplus, dt_bias)
+    a.h = _dense(h, _F32, (Bt, width, N), "h", dev)
     a.h_out = _dense(h_out, _F32, (Bt, width, N), "h_out", dev)
-    a.y = _dense(y, x.dtype, (Bt, width), "y", dev)
     _run_layer("m3_selective_scan_step", a, dev)
     return y
 
@@ -555,7 +557,7 @@ def m3_selective_scan_backward(x, dt, A, B, C, D=None, z=None, h0=None, *, dy, d
     optional dict of preallocated tensors."""
     Bt, L, width = x.shape
     G, N = B.shape[-2:]
-    dev, t = x.device, x.dtype
+    dev, t = x.get_device(), x.dtype
     got = out or {}
     shapes = dict(dx=((Bt, L, width), t), ddt=((Bt, L, width), t), dA=((width, N), _F32), dB=((Bt, L, G, N), t),
                   dC=((Bt, L, G, N), t), dD=((width,), _F32), dz=((Bt, L, width), t), ddt_bias=((width,), _F32),
@@ -564,10 +566,10 @@ def m3_selective_scan_backward(x, dt, A, B, C, D=None, z=None, h0=None, *, dy, d
     a = _lib.ScanBackwardArgs()
     out = {}
     for k, (shape, ty) in shapes.items():
-        out[k] = None if absent.get(k) else _new(got.get(k), shape, x, ty)
-        setattr(a, k, _dense(out[k], ty, shape, k, dev))
+        out[k], at = (None, None) if absent.get(k) else _out(got.get(k), ty, shape, k, x, dev)
+        setattr(a, k, at)
     a.fwd.Bt, a.fwd.L = Bt, L
-    _scan_inputs(a.fwd, (Bt, L), x, dt, A, B, C, D, z, dt_softplus, dt_bias)
+    _scan_inputs(a.fwd, dev, (Bt, L), x, dt, A, B, C, D, z, dt_softplus, dt_bias)
     a.fwd.h0 = _dense(h0, _F32, (Bt, width, N), "h0", dev)
     a.fwd.lengths = _dense(lengths, torch.int32, (Bt,), "lengths", dev)
     a.dy = _dense(dy, t, (Bt, L, width), "dy", dev)
@@ -577,14 +579,14 @@ def m3_selective_scan_backward(x, dt, A, B, C, D=None, z=None, h0=None, *, dy, d
     return out
 
 
-def _gated_inputs(a, x, z, w, groups, eps, gate_first):
+def _gated_inputs(a, dev, x, z, w, groups, eps, gate_first):
     shape = x.shape
     n, width = len(shape) - 1, shape[-1]
     a.M, a.D, a.G, a.in_dtype = x.numel() // width if width else 0, width, groups, _dtype_code(x)
     a.gate_first, a.eps = 1 if gate_first else 0, eps
-    a.x, a.x_ld = _rows(x, x.dtype, shape, n, "x", x.device)
-    a.z, a.z_ld = _rows(z, x.dtype, shape, n, "z", x.device)
-    a.w = _dense(w, _F32, (width,), "w", x.device)
+    a.x, a.x_ld = _rows(x, x.dtype, shape, n, "x", dev)
+    a.z, a.z_ld = _rows(z, x.dtype, shape, n, "z", dev)
+    a.w = _dense(w, _F32, (width,), "w", dev)
 
 
 @_scoped
@@ -594,11 +596,11 @@ def m3_gated_norm(x, z=None, w=None, *, groups=1, eps=1e-6, gate_first=True, y=N
     eps) w silu(z).  x, z [..., D] (bf16 or fp32; rows may be slices of wider
     ones), w [D] fp32 (None: ones), `groups` equal groups.  Returns y (dense;
     may be given as x or z themselves where those are dense)."""
-    y = _new(y, x.shape, x)
+    dev = x.get_device()
     a = _lib.GatedNormArgs()
-    _gated_inputs(a, x, z, w, groups, eps, gate_first)
-    a.y = _dense(y, x.dtype, x.shape, "y", x.device)
-    _run_layer("m3_gated_norm", a, x.device)
+    y, a.y = _out(y, x.dtype, x.shape, "y", x, dev)
+    _gated_inputs(a, dev, x, z, w, groups, eps, gate_first)
+    _run_layer("m3_gated_norm", a, dev)
     return y
 
 
@@ -606,16 +608,17 @@ def m3_gated_norm(x, z=None, w=None, *, groups=1, eps=1e-6, gate_first=True, y=N
 def m3_gated_norm_backward(x, z=None, w=None, *, dy, groups=1, eps=1e-6, gate_first=True, workspace=None, out=None):
     """Gradients of m3_gated_norm for dy (dense): a dict with dx, dz (None
     without gate) and dw (None without gain)."""
-    dev, t = x.device, x.dtype
+    dev, t = x.get_device(), x.dtype
     got = out or {}
-    out = dict(dx=_new(got.get("dx"), x.shape, x), dz=None if z is None else _new(got.get("dz"), x.shape, x),
-               dw=None if w is None else _new(got.get("dw"), (x.shape[-1],), x, _F32))
     a = _lib.GatedNormBackwardArgs()
-    _gated_inputs(a.fwd, x, z, w, groups, eps, gate_first)
+    out = dict(dx=None, dz=None, dw=None)
+    out["dx"], a.dx = _out(got.get("dx"), t, x.shape, "dx", x, dev)
+    if z is not None:
+        out["dz"], a.dz = _out(got.get("dz"), t, x.shape, "dz", x, dev)
+    if w is not None:
+        out["dw"], a.dw = _out(got.get("dw"), _F32, x.shape[-1:], "dw", x, dev)
+    _gated_inputs(a.fwd, dev, x, z, w, groups, eps, gate_first)
     a.dy = _dense(dy, t, x.shape, "dy", dev)
-    a.dx = _dense(out["dx"], t, x.shape, "dx", dev)
-    a.dz = _dense(out["dz"], t, x.shape, "dz", dev)
-    a.dw = _dense(out["dw"], _F32, (x.shape[-1],), "dw", dev)
     workspace = _take_workspace("m3_gated_norm_backward", a, workspace, dev)
     _run_layer("m3_gated_norm_backward", a, dev)
     return out
@@ -628,21 +631,19 @@ def m3_residual_norm(x, residual=None, w=None, scale=None, *, eps=1e-6, y=None, 
     wider ones), residual of x's shape in x's type or fp32 (None: zeros), w and
     scale [D] fp32 (None: ones).  Returns a dict with y (x's type) and residual:
     h in the residual's type (residual_out may be `residual` itself)."""
-    dev, t, shape = x.device, x.dtype, x.shape
+    dev, t, shape = x.get_device(), x.dtype, x.shape
     width = shape[-1]
     rt = residual.dtype if residual is not None else residual_out.dtype if residual_out is not None else t
-    y = _new(y, shape, x)
-    if want_residual:
-        residual_out = _new(residual_out, shape, residual if residual is not None else x, rt)
     a = _lib.ResidualNormArgs()
+    y, a.y = _out(y, t, shape, "y", x, dev)
+    if want_residual or residual_out is not None:
+        residual_out, a.residual_out = _out(residual_out, rt, shape, "residual_out", residual if residual is not None else x, dev)
     a.M, a.D, a.in_dtype = x.numel() // width if width else 0, width, _dtype_code(x)
     a.res_dtype, a.eps = _lib.M3_F32 if rt == _F32 else _lib.M3_BF16, eps
     a.x, a.x_ld = _rows(x, t, shape, len(shape) - 1, "x", dev)
     a.residual = _dense(residual, rt, shape, "residual", dev)
     a.scale = _dense(scale, _F32, (width,), "scale", dev)
     a.w = _dense(w, _F32, (width,), "w", dev)
-    a.y = _dense(y, t, shape, "y", dev)
-    a.residual_out = _dense(residual_out, rt, shape, "residual_out", dev)
     _run_layer("m3_residual_norm", a, dev)
     return dict(y=y, residual=residual_out)
 
@@ -655,14 +656,19 @@ def m3_residual_norm_backward(h, x=None, w=None, scale=None, *, dy, dresidual=No
     Returns a dict with dresidual (h's type), dx (dy's type; the same tensor
     where scale is None and the types agree), dw and dscale (None where the
     parameter is).  out["dresidual"] may be `dresidual` itself."""
-    dev, t, width = h.device, dy.dtype, h.shape[-1]
+    dev, t, width = h.get_device(), dy.dtype, h.shape[-1]
     got = out or {}
-    dres = _new(got.get("dresidual"), h.shape, h)
-    own_dx = scale is not None or t != h.dtype or got.get("dx") is not None
-    dx = _new(got.get("dx"), h.shape, dy) if own_dx else None
-    out = dict(dresidual=dres, dx=dx if own_dx else dres, dw=None if w is None else _new(got.get("dw"), (width,), h, _F32),
-               dscale=None if scale is None else _new(got.get("dscale"), (width,), h, _F32))
     a = _lib.ResidualNormBackwardArgs()
+    out = dict(dresidual=None, dx=None, dw=None, dscale=None)
+    out["dresidual"], a.dresidual = _out(got.get("dresidual"), h.dtype, h.shape, "dresidual", h, dev)
+    if scale is not None or t != h.dtype or got.get("dx") is not None:
+        out["dx"], a.dx = _out(got.get("dx"), t, h.shape, "dx", dy, dev)
+    else:
+        out["dx"] = out["dresidual"]
+    if w is not None:
+        out["dw"], a.dw = _out(got.get("dw"), _F32, (width,), "dw", h, dev)
+    if scale is not None:
+        out["dscale"], a.dscale = _out(got.get("dscale"), _F32, (width,), "dscale", h, dev)
     a.M, a.D, a.in_dtype = h.numel() // width if width else 0, width, _dtype_code(dy)
     a.res_dtype, a.eps = _dtype_code(h), eps
     a.h = _dense(h, h.dtype, h.shape, "h", dev)
@@ -671,10 +677,6 @@ def m3_residual_norm_backward(h, x=None, w=None, scale=None, *, dy, dresidual=No
     a.w = _dense(w, _F32, (width,), "w", dev)
     a.dy = _dense(dy, t, h.shape, "dy", dev)
     a.dresidual_out = _dense(dresidual, h.dtype, h.shape, "dresidual", dev)
-    a.dx = _dense(dx, t, h.shape, "dx", dev)
-    a.dresidual = _dense(dres, h.dtype, h.shape, "dresidual", dev)
-    a.dw = _dense(out["dw"], _F32, (width,), "dw", dev)
-    a.dscale = _dense(out["dscale"], _F32, (width,), "dscale", dev)
     workspace = _take_workspace("m3_residual_norm_backward", a, workspace, dev)
     _run_layer("m3_residual_norm_backward", a, dev)
     return out

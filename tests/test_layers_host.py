@@ -344,7 +344,7 @@ def test_binding_refuses_host_tensors():
 @built
 def test_row_distances():
     from state_space_sequence_ssm_amd import ops
-    cpu, f = torch.device("cpu"), torch.float32
+    cpu, f = -1, torch.float32  # the device index of a host tensor
     rows = lambda t, lead, inner: ops._rows(t, f, (*lead, *inner), len(lead), "t", cpu)[1]  # noqa: E731
     wide = torch.zeros(2, 5, 24)
     assert rows(torch.zeros(2, 5, 8), (2, 5), (8,)) == 0
