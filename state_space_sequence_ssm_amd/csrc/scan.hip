@@ -22,10 +22,10 @@ struct ScanP {
 constexpr int TT = 32;  // tokens per tile
 
 // Four tokens' values of one lane, in registers.
-template <bool FULL>
+template <int S, bool FULL>
 struct Four {
   float delta[4], u[4];
-  f32x4 B[4], C[4];
+  typename States<S>::type B[4], C[4];
   // at this lane's channel of delta and u, and its states of B and C
   template <int CHB, int NP>
   __device__ __forceinline__ void load(const float* pd, const float* pu, const float* pB, const float* pC) {
@@ -33,8 +33,8 @@ struct Four {
     for (int j = 0; j < 4; ++j) {
       delta[j] = pd[j * CHB];
       u[j] = pu[j * CHB];
-      B[j] = *reinterpret_cast<const f32x4*>(pB + j * NP);
-      if (FULL) C[j] = *reinterpret_cast<const f32x4*>(pC + j * NP);
+      B[j] = *reinterpret_cast<const typename States<S>::type*>(pB + j * NP);
+      if (FULL) C[j] = *reinterpret_cast<const typename States<S>::type*>(pC + j * NP);
     }
   }
 };
@@ -43,7 +43,8 @@ struct Four {
 // before it.  Otherwise the states and sums of delta of the segments alone.
 //
 // A block is eight waves of two kinds, one of each per SIMD: four scan, 16
-// channels and 16 states each (64 / NB channels of NB state blocks); four stage,
+// channels and 4 S = 16 states each, or 8 or 4 for sizes that need no more (64 / NB
+// channels of NB state blocks); four stage,
 // that is, they load the next tile, form delta and u and put them into the other
 // half of LDS, and join, gate and store the y of the tile before.  So the loads'
 // latency and the exponentials of softplus and SiLU lie beside the recurrence and
@@ -51,9 +52,9 @@ struct Four {
 // compute unit holds two blocks where there are as many.  Bt 8, L 4096, D 2048, N 16
 // bf16, gated: 290-320 us with the clock, 29 vector instructions per token and wave
 // and the vector ALUs 83-87% busy; the recurrence's own instructions take 164 us.
-template <typename T, int NB, Words WD, bool FULL>
+template <typename T, int NB, int S, Words WD, bool FULL>
 __global__ __launch_bounds__(2 * kThreads, 4) void scan_kernel(ScanP p) {
-  constexpr int CHB = CH / NB, VE = TT * CHB / kThreads, NP = 16 * NB;
+  constexpr int CHB = CH / NB, VE = TT * CHB / kThreads, NP = 4 * S * NB;
   constexpr int YS = CHB == 16 ? 16 : CHB + 16;  // the four tokens' rows written together lie on different banks
   __shared__ __align__(16) float dl[2][TT][CHB];
   __shared__ __align__(16) float us[2][TT][CHB];
@@ -75,13 +76,13 @@ __global__ __launch_bounds__(2 * kThreads, 4) void scan_kernel(ScanP p) {
 
   if (scanner) {
     const int wave = tid >> 6, s = (tid & 63) >> 4, chl = (wave / NB) * 16 + (tid & 15);
-    const int sb = wave % NB, n0 = sb * 16 + 4 * s, nleft = p.in.N - n0;
+    const int sb = wave % NB, n0 = (sb * 4 + s) * S, nleft = p.in.N - n0;
     const int dloc = cb * CHB + chl;
     const bool live = dloc < p.in.Dg;
     const int d = g * p.in.Dg + (live ? dloc : 0);
-    float A2[4], h[4], sum_delta = 0.f;
+    float A2[S], h[S], sum_delta = 0.f;
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
+    for (int k = 0; k < S; ++k) {
       const bool on = live && k < nleft;
       A2[k] = on ? rate(p.A[int64_t(d) * p.in.N + n0 + k]) : 0.f;
       h[k] = on && p.h0 != nullptr && (FULL || seg == 0) ? p.h0[(int64_t(b) * p.in.D + d) * p.in.N + n0 + k] : 0.f;
@@ -91,7 +92,7 @@ __global__ __launch_bounds__(2 * kThreads, 4) void scan_kernel(ScanP p) {
         const int64_t at = (int64_t(q) * p.Bt + b) * p.in.D + d;
         const float sd = p.sdel[at];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
+        for (int k = 0; k < S; ++k) {
           const float e = k < nleft ? p.hend[at * p.in.N + n0 + k] : 0.f;
           h[k] = q == 0 ? e : fmaf(decay(sd, A2[k]), h[k], e);
         }
@@ -111,13 +112,13 @@ __global__ __launch_bounds__(2 * kThreads, 4) void scan_kernel(ScanP p) {
       // recurrence: independent work that covers the exponentials' latency and that
       // of the sums over states of the four tokens before.
       float y[4] = {0.f, 0.f, 0.f, 0.f};
-      auto four = [&](int to, const Four<FULL>& q) {
-        float a[4][4], w[4][4];
+      auto four = [&](int to, const Four<S, FULL>& q) {
+        float a[4][S], w[4][S];
         if constexpr (FULL) py[to * YS] = rows_sum4(y);
 #pragma unroll
         for (int j = 0; j < 4; ++j)
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
+          for (int k = 0; k < S; ++k) {
             a[j][k] = decay(q.delta[j], A2[k]);
             w[j][k] = q.u[j] * q.B[j][k];
           }
@@ -126,7 +127,7 @@ __global__ __launch_bounds__(2 * kThreads, 4) void scan_kernel(ScanP p) {
         for (int j = 0; j < 4; ++j) {
           y[j] = 0.f;
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
+          for (int k = 0; k < S; ++k) {
             h[k] = fmaf(a[j][k], h[k], w[j][k]);
             if (FULL) y[j] = fmaf(q.C[j][k], h[k], y[j]);
           }
@@ -136,7 +137,7 @@ __global__ __launch_bounds__(2 * kThreads, 4) void scan_kernel(ScanP p) {
       };
       const int nt = left < TT ? (left + 7) & ~7 : TT;
       const int rv = row_value(s);
-      Four<FULL> q0, q1;
+      Four<S, FULL> q0, q1;
       q0.template load<CHB, NP>(pd, pu, pB, pC);
 #pragma unroll
       for (int tq = 0; tq < TT; tq += 8) {
@@ -154,12 +155,12 @@ __global__ __launch_bounds__(2 * kThreads, 4) void scan_kernel(ScanP p) {
     if constexpr (FULL) {
       if (p.hfin == nullptr || seg != p.nseg - 1) return;
 #pragma unroll
-      for (int k = 0; k < 4; ++k)
+      for (int k = 0; k < S; ++k)
         if (k < nleft) p.hfin[(int64_t(b) * p.in.D + d) * p.in.N + n0 + k] = h[k];
     } else {
       const int64_t at = (int64_t(seg) * p.Bt + b) * p.in.D + d;
 #pragma unroll
-      for (int k = 0; k < 4; ++k)
+      for (int k = 0; k < S; ++k)
         if (k < nleft) p.hend[at * p.in.N + n0 + k] = h[k];
       if (s == 0 && sb == 0) p.sdel[at] = sum_delta;
     }
@@ -372,7 +373,7 @@ Plan plan_of(const m3_scan_args& a) {
   return p;
 }
 
-template <typename T, int NB, Words WD>
+template <typename T, int NB, int S, Words WD>
 hipError_t run(const m3_scan_args& a, Plan pl, hipStream_t st) {
   if (a.workspace == nullptr) pl.nseg = 1, pl.seglen = a.L;
   const Inputs in{a.x, a.dt, a.z, a.B, a.C, nullptr, a.x_ld, a.dt_ld, a.z_ld, a.B_ld, a.C_ld, a.D_skip, a.dt_bias, a.L, a.D, a.N,
@@ -382,11 +383,11 @@ hipError_t run(const m3_scan_args& a, Plan pl, hipStream_t st) {
   if (pl.nseg > 1) {
     p.hend = static_cast<float*>(a.workspace);
     p.sdel = p.hend + int64_t(pl.nseg - 1) * a.Bt * a.D * a.N;
-    scan_kernel<T, NB, WD, false><<<uint32_t(per * (pl.nseg - 1)), 2 * kThreads, 0, st>>>(p);
+    scan_kernel<T, NB, S, WD, false><<<uint32_t(per * (pl.nseg - 1)), 2 * kThreads, 0, st>>>(p);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
-  scan_kernel<T, NB, WD, true><<<uint32_t(per * pl.nseg), 2 * kThreads, 0, st>>>(p);
+  scan_kernel<T, NB, S, WD, true><<<uint32_t(per * pl.nseg), 2 * kThreads, 0, st>>>(p);
   return hipGetLastError();
 }
 template <typename T, int S, int NI, bool VEC>
@@ -406,8 +407,9 @@ hipError_t step_items(const m3_scan_step_args& a, hipStream_t st) {
 
 template <typename T, Words WD>
 hipError_t by_states(const m3_scan_args& a, const Plan& p, hipStream_t st) {
-  if (p.NB == 1) return run<T, 1, WD>(a, p, st);
-  return p.NB == 2 ? run<T, 2, WD>(a, p, st) : run<T, 4, WD>(a, p, st);
+#define CALL(NB, S) run<T, NB, S, WD>(a, p, st)
+  M3_SCAN_STATES(a.N, CALL)
+#undef CALL
 }
 template <typename T>
 hipError_t by_words(const m3_scan_args& a, const Plan& p, Words w, hipStream_t st) {

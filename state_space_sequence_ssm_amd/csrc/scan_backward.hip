@@ -45,7 +45,7 @@ struct BwP {
   void* ddt;
   void* dz;
   float* dh0;
-  float* ck;    // [tiles][blocks][256][4] state in front of each tile (of its segment from zero)
+  float* ck;    // [tiles][blocks][256][S] state in front of each tile (of its segment from zero)
   float* cd;    // [tiles][blocks][CHB] sum of delta from the segment's start to the tile
   float* hend;  // [nseg][Bt][D][N] state of a segment from zero (segment 0: from h0)
   float* gsum;  // [nseg][Bt][D][N] a segment's contribution to the gradient in front of it
@@ -77,7 +77,7 @@ struct Where {
     tend = tlim < len ? tlim : len;
   }
 };
-template <int NB>
+template <int NB, int S>
 struct Lane {
   int s, chl, n0, d, nleft;  // state group, channel in the block, first state, channel, states left from n0
   bool live;
@@ -85,7 +85,7 @@ struct Lane {
     const int wave = tid >> 6;
     s = (tid & 63) >> 4;
     chl = (wave / NB) * 16 + (tid & 15);
-    n0 = (wave % NB) * 16 + 4 * s;
+    n0 = (wave % NB * 4 + s) * S;
     nleft = p.in.N - n0;
     const int dl = w.cb * Where<NB>::CHB + chl;
     live = dl < p.in.Dg;
@@ -94,10 +94,10 @@ struct Lane {
 };
 
 // Four tokens' values of one lane, in registers.
-template <bool DO, bool CC>
+template <int S, bool DO, bool CC>
 struct Four {
   float delta[4], u[4], go[4];
-  f32x4 B[4], C[4];
+  typename States<S>::type B[4], C[4];
   template <int CHB, int NP>
   __device__ __forceinline__ void load(const float* pd, const float* pu, const float* po, const float* pB, const float* pC) {
 #pragma unroll
@@ -105,17 +105,17 @@ struct Four {
       delta[j] = pd[j * CHB];
       u[j] = pu[j * CHB];
       if (DO) go[j] = po[j * CHB];
-      B[j] = *reinterpret_cast<const f32x4*>(pB + j * NP);
-      if (CC) C[j] = *reinterpret_cast<const f32x4*>(pC + j * NP);
+      B[j] = *reinterpret_cast<const typename States<S>::type*>(pB + j * NP);
+      if (CC) C[j] = *reinterpret_cast<const typename States<S>::type*>(pC + j * NP);
     }
   }
 };
 
 // First walk: states in front of the tiles, and with SEG the segments' ends.  Bt 8,
 // L 2048, D 2048, N 16 bf16, uncut: 113 us.
-template <typename T, int NB, Words WD, bool SEG>
+template <typename T, int NB, int S, Words WD, bool SEG>
 __global__ __launch_bounds__(2 * kThreads) void states_kernel(BwP p) {
-  constexpr int TT = 32, CHB = CH / NB, VE = TT * CHB / kThreads, NP = 16 * NB;
+  constexpr int TT = 32, CHB = CH / NB, VE = TT * CHB / kThreads, NP = 4 * S * NB;
   __shared__ __align__(16) float dl[2][TT][CHB];
   __shared__ __align__(16) float us[2][TT][CHB];
   __shared__ __align__(16) float ds[SEG ? 2 : 1][SEG ? TT : 1][CHB];
@@ -125,10 +125,10 @@ __global__ __launch_bounds__(2 * kThreads) void states_kernel(BwP p) {
   const int tiles = w.tend > w.tbeg ? (w.tend - w.tbeg + TT - 1) / TT : 0;
 
   if (threadIdx.x < kThreads) {
-    const Lane<NB> l(p, w, tid);
-    float A2[4], h[4], P[4], gs[4], sum_delta = 0.f;
+    const Lane<NB, S> l(p, w, tid);
+    float A2[S], h[S], P[S], gs[S], sum_delta = 0.f;
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
+    for (int k = 0; k < S; ++k) {
       const bool on = l.live && k < l.nleft;
       A2[k] = on ? rate(p.A[int64_t(l.d) * p.in.N + l.n0 + k]) : 0.f;
       h[k] = on && p.h0 != nullptr && w.seg == 0 ? p.h0[(int64_t(w.b) * p.in.D + l.d) * p.in.N + l.n0 + k] : 0.f;
@@ -145,22 +145,22 @@ __global__ __launch_bounds__(2 * kThreads) void states_kernel(BwP p) {
       const float* pC = &bc[o][SEG ? 1 : 0][0][l.n0];
       auto keep = [&](int tq) {
         const int64_t at = int64_t((w.tbeg + t * TT + tq) / TB) * w.blocks + w.unit;
-        store_pack<float, 4>(p.ck + (at * kThreads + tid) * 4, h);
+        store_pack<float, S>(p.ck + (at * kThreads + tid) * S, h);
         if (SEG && l.s == 0 && l.n0 == 0) p.cd[at * CHB + l.chl] = sum_delta;
       };
-      auto four = [&](const Four<SEG, SEG>& q) {
-        float a[4][4], u[4][4];
+      auto four = [&](const Four<S, SEG, SEG>& q) {
+        float a[4][S], u[4][S];
 #pragma unroll
         for (int j = 0; j < 4; ++j)
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
+          for (int k = 0; k < S; ++k) {
             a[j][k] = decay(q.delta[j], A2[k]);
             u[j][k] = q.u[j] * q.B[j][k];
           }
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
+          for (int k = 0; k < S; ++k) {
             h[k] = fmaf(a[j][k], h[k], u[j][k]);
             if constexpr (SEG) {
               P[k] *= a[j][k];
@@ -171,7 +171,7 @@ __global__ __launch_bounds__(2 * kThreads) void states_kernel(BwP p) {
         }
       };
       // the next four tokens on their way from LDS meanwhile
-      Four<SEG, SEG> q0, q1;
+      Four<S, SEG, SEG> q0, q1;
       q0.template load<CHB, NP>(pd, pu, po, pB, pC);
 #pragma unroll
       for (int tq = 0; tq < TT; tq += 8) {
@@ -188,7 +188,7 @@ __global__ __launch_bounds__(2 * kThreads) void states_kernel(BwP p) {
     if (!SEG || !l.live) return;
     const int64_t at = (int64_t(w.seg) * p.Bt + w.b) * p.in.D + l.d;
 #pragma unroll
-    for (int k = 0; k < 4; ++k)
+    for (int k = 0; k < S; ++k)
       if (k < l.nleft) {
         p.hend[at * p.in.N + l.n0 + k] = h[k];
         p.gsum[at * p.in.N + l.n0 + k] = gs[k];
@@ -268,12 +268,12 @@ __device__ __forceinline__ float channels_sum(const float* v, uint32_t odd, uint
 
 // LDS of the reverse walk; everything twice, a tile being staged, and the one
 // before finished, while one is walked.
-template <int NB>
+template <int NB, int S>
 struct Shared {
-  static constexpr int CHB = CH / NB, NP = 16 * NB;
+  static constexpr int CHB = CH / NB, NP = 4 * S * NB;
   float dl[2][TB][CHB], us[2][TB][CHB], ds[2][TB][CHB];  // delta, u, do
   float bc[2][2][TB][NP];
-  float o[2][NB][TB][CHB], gB[2][NB][TB][CHB], gA[2][NB][TB][CHB];  // sums over a block's 16 states
+  float o[2][NB][TB][CHB], gB[2][NB][TB][CHB], gA[2][NB][TB][CHB];  // sums over a block's states
   float wp[2][4 / NB][TB][2][NP];                                   // dB, and dC without u B^T, of a wave's 16 channels
   float sdu[2][TB];                                                 // sum over the block's channels of do u
 };
@@ -282,11 +282,11 @@ struct Shared {
 // for the recurrences and sums, 22 of them the sums of dB and dC over channels, and
 // about 17 for staging.  250 registers leave a compute unit one block.  Bt 8, L 2048,
 // D 2048, N 16 bf16: 410-435 us.
-template <typename T, int NB, Words WD>
+template <typename T, int NB, int S, Words WD>
 __global__ __launch_bounds__(2 * kThreads) void reverse_kernel(BwP p) {
-  constexpr int CHB = CH / NB, VE = TB * CHB / kThreads, NP = 16 * NB;
+  constexpr int CHB = CH / NB, VE = TB * CHB / kThreads, NP = 4 * S * NB;
   extern __shared__ __align__(16) unsigned char smem[];
-  Shared<NB>& sh = *reinterpret_cast<Shared<NB>*>(smem);
+  Shared<NB, S>& sh = *reinterpret_cast<Shared<NB, S>*>(smem);
   const int tid = threadIdx.x % kThreads;
   const Where<NB> w(p);
   const int tiles = w.tend > w.tbeg ? (w.tend - w.tbeg + TB - 1) / TB : 0;
@@ -294,14 +294,14 @@ __global__ __launch_bounds__(2 * kThreads) void reverse_kernel(BwP p) {
   float* part = p.part + (int64_t(w.seg) * p.Bt + w.b) * ncols;
 
   if (threadIdx.x < kThreads) {
-    const Lane<NB> l(p, w, tid);
+    const Lane<NB, S> l(p, w, tid);
     const int wave = tid >> 6, blk = wave % NB;
     const int64_t at0 = int64_t(w.b) * p.in.D + l.d, per = int64_t(p.Bt) * p.in.D;
     const uint32_t odd = tid & 1 ? ~0u : 0u, two = tid & 2 ? ~0u : 0u, four = tid & 4 ? ~0u : 0u, eight = tid & 8 ? ~0u : 0u;
     const int rv = row_value(l.s);
-    float A2[4], gg[4], hin[4], dA[4];
+    float A2[S], gg[S], hin[S], dA[S];
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
+    for (int k = 0; k < S; ++k) {
       const bool on = l.live && k < l.nleft;
       A2[k] = on ? rate(p.A[int64_t(l.d) * p.in.N + l.n0 + k]) : 0.f;
       gg[k] = on && p.dhf != nullptr ? p.dhf[at0 * p.in.N + l.n0 + k] : 0.f;
@@ -311,29 +311,29 @@ __global__ __launch_bounds__(2 * kThreads) void reverse_kernel(BwP p) {
     for (int q = 0; q < w.seg; ++q) {  // state in front of the segment
       const float sd = p.sdel[q * per + at0];
 #pragma unroll
-      for (int k = 0; k < 4; ++k)
+      for (int k = 0; k < S; ++k)
         hin[k] = fmaf(decay(sd, A2[k]), hin[k], k < l.nleft ? p.hend[(q * per + at0) * p.in.N + l.n0 + k] : 0.f);
     }
     for (int q = p.nseg - 1; q > w.seg; --q) {  // gradient behind it
       const float sd = p.sdel[q * per + at0];
 #pragma unroll
-      for (int k = 0; k < 4; ++k)
+      for (int k = 0; k < S; ++k)
         gg[k] = fmaf(decay(sd, A2[k]), gg[k], k < l.nleft ? p.gsum[(q * per + at0) * p.in.N + l.n0 + k] : 0.f);
     }
-    Pack<float, 4> qh{};
+    Pack<float, S> qh{};
     float qcd = 0.f;
     auto fetch = [&](int tile) {
       const int64_t at = int64_t(w.tbeg / TB + (tile > 0 ? tile : 0)) * w.blocks + w.unit;
-      qh = load_pack<float, 4>(p.ck + (at * kThreads + tid) * 4);
+      qh = load_pack<float, S>(p.ck + (at * kThreads + tid) * S);
       if (w.seg > 0) qcd = p.cd[at * CHB + l.chl];
     };
     if (tiles > 0) fetch(tiles - 1);
     __syncthreads();
     for (int i = 0; i < tiles; ++i) {
       const int o = i & 1;
-      float h[4];
+      float h[S];
 #pragma unroll
-      for (int k = 0; k < 4; ++k) h[k] = w.seg > 0 ? fmaf(decay(qcd, A2[k]), hin[k], qh.e[k]) : qh.e[k];
+      for (int k = 0; k < S; ++k) h[k] = w.seg > 0 ? fmaf(decay(qcd, A2[k]), hin[k], qh.e[k]) : qh.e[k];
       fetch(tiles - 2 - i);
       const float* pd = &sh.dl[o][0][l.chl];
       const float* pu = &sh.us[o][0][l.chl];
@@ -341,12 +341,12 @@ __global__ __launch_bounds__(2 * kThreads) void reverse_kernel(BwP p) {
       const float* pB = &sh.bc[o][0][0][l.n0];
       const float* pC = &sh.bc[o][1][0][l.n0];
       // ---- decays and states of the tile, forward
-      float a[TB][4], ah[TB][4];
-      Four<true, true> q[2];
+      float a[TB][S], ah[TB][S];
+      Four<S, true, true> q[2];
       q[0].template load<CHB, NP>(pd, pu, po, pB, pC);
 #pragma unroll
       for (int tq = 0; tq < TB; tq += 4) {
-        const Four<true, true>& f = q[tq / 4 & 1];
+        const Four<S, true, true>& f = q[tq / 4 & 1];
         if (tq + 4 < TB)
           q[tq / 4 + 1 & 1].template load<CHB, NP>(pd + (tq + 4) * CHB, pu + (tq + 4) * CHB, po + (tq + 4) * CHB, pB + (tq + 4) * NP,
                                                    pC + (tq + 4) * NP);
@@ -354,12 +354,12 @@ __global__ __launch_bounds__(2 * kThreads) void reverse_kernel(BwP p) {
 #pragma unroll
         for (int j = 0; j < 4; ++j)
 #pragma unroll
-          for (int k = 0; k < 4; ++k) a[tq + j][k] = decay(f.delta[j], A2[k]);
+          for (int k = 0; k < S; ++k) a[tq + j][k] = decay(f.delta[j], A2[k]);
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           y[j] = 0.f;
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
+          for (int k = 0; k < S; ++k) {
             ah[tq + j][k] = a[tq + j][k] * h[k];
             h[k] = fmaf(f.u[j], f.B[j][k], ah[tq + j][k]);
             y[j] = fmaf(f.C[j][k], h[k], y[j]);
@@ -368,46 +368,57 @@ __global__ __launch_bounds__(2 * kThreads) void reverse_kernel(BwP p) {
         sh.o[o][blk][tq + rv][l.chl] = rows_sum4(y);
       }
       // ---- gradients, backward; the last four tokens' values are at hand
-      float dAt[4] = {0.f, 0.f, 0.f, 0.f};
+      float dAt[S] = {};
 #pragma unroll
       for (int tq = TB - 4; tq >= 0; tq -= 4) {
-        const Four<true, true>& f = q[tq / 4 & 1];
+        const Four<S, true, true>& f = q[tq / 4 & 1];
         if (tq > 0)
           q[tq / 4 + 1 & 1].template load<CHB, NP>(pd + (tq - 4) * CHB, pu + (tq - 4) * CHB, po + (tq - 4) * CHB, pB + (tq - 4) * NP,
                                                    pC + (tq - 4) * NP);
-        float sB[4], sA[4], rB[4], rC[4];
+        // the four tokens' S values each, four of them to a sum over the channels
+        float sB[4], sA[4], gu[4], dh[4], rB[S], rC[S];
 #pragma unroll
         for (int j = 3; j >= 0; --j) {
-          float gu[4], dh[4];
           sB[j] = sA[j] = 0.f;
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
+          for (int k = 0; k < S; ++k) {
             const float gk = fmaf(f.C[j][k], f.go[j], gg[k]);
-            dh[k] = f.go[j] * ah[tq + j][k];
-            gu[k] = gk * f.u[j];
+            dh[(j * S + k) % 4] = f.go[j] * ah[tq + j][k];
+            gu[(j * S + k) % 4] = gk * f.u[j];
             sB[j] = fmaf(gk, f.B[j][k], sB[j]);
             const float m = gk * ah[tq + j][k];
             sA[j] = fmaf(m, A2[k], sA[j]);
             dAt[k] = fmaf(m, f.delta[j], dAt[k]);
             gg[k] = gk * a[tq + j][k];
           }
-          rB[j] = channels_sum(gu, odd, two);
-          rC[j] = channels_sum(dh, odd, two);
+          if (j * S % 4 == 0) {
+            rB[j * S / 4] = channels_sum(gu, odd, two);
+            rC[j * S / 4] = channels_sum(dh, odd, two);
+          }
         }
         sh.gB[o][blk][tq + rv][l.chl] = rows_sum4(sB);
         sh.gA[o][blk][tq + rv][l.chl] = rows_sum4(sA);
-        // lane c of a row writes token c / 4, state c % 4 of its group
-        float* wp = &sh.wp[o][wave / NB][tq + (tid >> 2 & 3)][0][l.n0 + (tid & 3)];
-        wp[0] = pick(eight, pick(four, rB[3], rB[2]), pick(four, rB[1], rB[0]));
-        wp[NP] = pick(eight, pick(four, rC[3], rC[2]), pick(four, rC[1], rC[0]));
+        // lane c of a row writes value c of its 4 S: token c / S, state c % S
+        const int c = tid & (4 * S - 1);
+        float* wp = &sh.wp[o][wave / NB][tq + c / S][0][l.n0 + c % S];
+        if constexpr (S == 4) {
+          wp[0] = pick(eight, pick(four, rB[3], rB[2]), pick(four, rB[1], rB[0]));
+          wp[NP] = pick(eight, pick(four, rC[3], rC[2]), pick(four, rC[1], rC[0]));
+        } else if constexpr (S == 2) {
+          wp[0] = pick(four, rB[1], rB[0]);
+          wp[NP] = pick(four, rC[1], rC[0]);
+        } else {
+          wp[0] = rB[0];
+          wp[NP] = rC[0];
+        }
       }
 #pragma unroll
-      for (int k = 0; k < 4; ++k) dA[k] += dAt[k];
+      for (int k = 0; k < S; ++k) dA[k] += dAt[k];
       __syncthreads();
     }
     if (l.live) {
 #pragma unroll
-      for (int k = 0; k < 4; ++k)
+      for (int k = 0; k < S; ++k)
         if (k < l.nleft) {
           part[int64_t(l.d) * p.in.N + l.n0 + k] = dA[k];
           if (w.seg == 0 && p.dh0 != nullptr) p.dh0[at0 * p.in.N + l.n0 + k] = gg[k];
@@ -641,7 +652,7 @@ struct Plan {
 Plan plan_of(const m3_scan_args& f) {
   Plan p;
   p.NB = state_blocks(f.N);
-  const int CHB = CH / p.NB, NP = 16 * p.NB;
+  const int CHB = CH / p.NB, S = lane_states(f.N), NP = 4 * S * p.NB;
   p.nblk = blocks_per_group(f.D / f.G, p.NB);
   p.blocks = int64_t(f.Bt) * f.G * p.nblk;
   p.nseg = 1;
@@ -665,7 +676,7 @@ Plan plan_of(const m3_scan_args& f) {
   p.tiles = (f.L + TB - 1) / TB;
   const size_t seg = p.nseg > 1 ? size_t(p.nseg) * f.Bt * f.D : 0;
   p.oCk = 0;
-  p.oCd = round256(p.oCk + size_t(p.tiles) * p.blocks * kThreads * 16);
+  p.oCd = round256(p.oCk + size_t(p.tiles) * p.blocks * kThreads * 4 * S);
   p.oHe = round256(p.oCd + (p.nseg > 1 ? size_t(p.tiles) * p.blocks * CHB * 4 : 0));
   p.oGs = round256(p.oHe + seg * f.N * 4);
   p.oSd = round256(p.oGs + seg * f.N * 4);
@@ -675,8 +686,9 @@ Plan plan_of(const m3_scan_args& f) {
   return p;
 }
 
-template <typename T, int NB, Words WD>
+template <typename T, int NB, int S, Words WD>
 hipError_t run(const m3_scan_backward_args& a, const Plan& pl, hipStream_t st) {
+  constexpr int NP = 4 * S * NB;
   static std::atomic<uint64_t> cleared{0};
   const m3_scan_args& f = a.fwd;
   unsigned char* ws = static_cast<unsigned char*>(a.workspace);
@@ -686,13 +698,13 @@ hipError_t run(const m3_scan_backward_args& a, const Plan& pl, hipStream_t st) {
   const BwP p{in, f.A, f.h0, a.dh_final, f.lengths, a.dx, a.ddt, a.dz, a.dh0, at(pl.oCk), at(pl.oCd), at(pl.oHe), at(pl.oGs),
               at(pl.oSd), at(pl.oBc), at(pl.oPart), f.Bt, pl.nblk, pl.nseg, pl.seglen, f.dt_softplus};
   const uint32_t grid = uint32_t(pl.blocks * pl.nseg);
-  if (pl.nseg > 1) states_kernel<T, NB, WD, true><<<grid, 2 * kThreads, 0, st>>>(p);
-  else states_kernel<T, NB, WD, false><<<grid, 2 * kThreads, 0, st>>>(p);
+  if (pl.nseg > 1) states_kernel<T, NB, S, WD, true><<<grid, 2 * kThreads, 0, st>>>(p);
+  else states_kernel<T, NB, S, WD, false><<<grid, 2 * kThreads, 0, st>>>(p);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  e = allow_lds(reinterpret_cast<const void*>(&reverse_kernel<T, NB, WD>), sizeof(Shared<NB>), cleared);
+  e = allow_lds(reinterpret_cast<const void*>(&reverse_kernel<T, NB, S, WD>), sizeof(Shared<NB, S>), cleared);
   if (e != hipSuccess) return e;
-  reverse_kernel<T, NB, WD><<<grid, 2 * kThreads, sizeof(Shared<NB>), st>>>(p);
+  reverse_kernel<T, NB, S, WD><<<grid, 2 * kThreads, sizeof(Shared<NB, S>), st>>>(p);
   e = hipGetLastError();
   if (e != hipSuccess) return e;
   ColSum c{};
@@ -705,17 +717,18 @@ hipError_t run(const m3_scan_backward_args& a, const Plan& pl, hipStream_t st) {
   c.n[1] = f.D;
   c.dst[2] = a.ddt_bias;
   c.n[2] = f.D;
-  const int64_t rows = int64_t(f.Bt) * f.L, items = rows * f.G * 2 * 16 * NB;
+  const int64_t rows = int64_t(f.Bt) * f.L, items = rows * f.G * 2 * NP;
   const uint32_t sums = colsum_blocks(c), all = sums + uint32_t((items + 1023) / 1024);
-  auto* go = colsum_cols(c) == 16 ? sums_kernel<T, 16 * NB, 16> : sums_kernel<T, 16 * NB, 128>;
+  auto* go = colsum_cols(c) == 16 ? sums_kernel<T, NP, 16> : sums_kernel<T, NP, 128>;
   go<<<all, 1024, 0, st>>>(c, sums, p.bc, static_cast<T*>(a.dB), static_cast<T*>(a.dC), f.lengths, rows, f.L, f.G, f.N, pl.nblk);
   return hipGetLastError();
 }
 
 template <typename T, Words WD>
 hipError_t by_states(const m3_scan_backward_args& a, const Plan& p, hipStream_t st) {
-  if (p.NB == 1) return run<T, 1, WD>(a, p, st);
-  return p.NB == 2 ? run<T, 2, WD>(a, p, st) : run<T, 4, WD>(a, p, st);
+#define CALL(NB, S) run<T, NB, S, WD>(a, p, st)
+  M3_SCAN_STATES(a.fwd.N, CALL)
+#undef CALL
 }
 template <typename T>
 hipError_t by_words(const m3_scan_backward_args& a, const Plan& p, Words w, hipStream_t st) {
