@@ -10,6 +10,15 @@ namespace {
 
 constexpr int kRows = 4;  // token rows loaded together by one thread
 
+// First of word cv's channels.  Where words have the alignment of their elements only
+// (RAG: widths or rows that are no multiple of one) the last is moved back to end with
+// the row; the channels it shares with the word before come to the same values in both.
+template <int V, bool RAG>
+__device__ __forceinline__ int first_channel(uint32_t cv, int D) {
+  const int d0 = int(cv) * V;
+  return RAG && d0 + V > D ? D - V : d0;
+}
+
 struct ConvP {
   const void* x;
   int64_t ld;
@@ -28,13 +37,13 @@ struct ConvP {
 // tokens, the last W - 1 inputs held in registers, so that a row is read once
 // per tile and W - 1 rows again at its start.  Bt 8, L 4096, D 2048, W 4 bf16: 58 us,
 // 4.6 TB/s where a plain copy reaches 5.15.
-template <typename T, int W, int V>
+template <typename T, int W, int V, bool RAG>
 __global__ __launch_bounds__(256) void conv_kernel(ConvP p) {
   const uint32_t idx = blockIdx.x * 256u + threadIdx.x;
   if (idx >= p.total) return;
   const uint32_t cv = idx % p.nv, r = idx / p.nv;
   const int tile = int(r % p.ntiles), b = int(r / p.ntiles);
-  const int d0 = int(cv) * V;
+  const int d0 = first_channel<V, RAG>(cv, p.D);
   const int len = item_length(p.lengths, b, p.L);
   const int t0 = tile * p.tt;
   const int t1 = t0 + p.tt < len ? t0 + p.tt : len;
@@ -46,9 +55,9 @@ __global__ __launch_bounds__(256) void conv_kernel(ConvP p) {
 #pragma unroll
   for (int j = 0; j < W - 1; ++j) {
     if (tile > 0 && t0 < len) {
-      unpack<T, V>(load_pack<T, V>(x + int64_t(t0 - (W - 1) + j) * p.ld), xs[j]);
+      unpack<T, V>(load_word<T, V, RAG>(x + int64_t(t0 - (W - 1) + j) * p.ld), xs[j]);
     } else if (tile == 0 && state != nullptr) {
-      unpack<T, V>(load_pack<T, V>(state + int64_t(j) * p.D), xs[j]);
+      unpack<T, V>(load_word<T, V, RAG>(state + int64_t(j) * p.D), xs[j]);
     } else {
 #pragma unroll
       for (int i = 0; i < V; ++i) xs[j][i] = 0.f;
@@ -62,9 +71,10 @@ __global__ __launch_bounds__(256) void conv_kernel(ConvP p) {
     for (int j = 0; j < W - 1; ++j) {
       const int t = len - (W - 1) + j;
       Pack<T, V> q{};
-      if (t >= 0) q = load_pack<T, V>(x + int64_t(t) * p.ld);
-      else if (state != nullptr) q = load_pack<T, V>(state + int64_t(len + j) * p.D);
-      *reinterpret_cast<Pack<T, V>*>(so + int64_t(j) * p.D) = q;
+      if (t >= 0) q = load_word<T, V, RAG>(x + int64_t(t) * p.ld);
+      else if (state != nullptr) q = load_word<T, V, RAG>(state + int64_t(len + j) * p.D);
+      if constexpr (RAG) put_loose<T, V>(so + int64_t(j) * p.D, q);
+      else *reinterpret_cast<Pack<T, V>*>(so + int64_t(j) * p.D) = q;
     }
   }
   if (t0 >= t1) return;
@@ -83,7 +93,7 @@ __global__ __launch_bounds__(256) void conv_kernel(ConvP p) {
   Pack<T, V> q[kRows];
   auto fetch = [&](int t) {
 #pragma unroll
-    for (int i = 0; i < kRows; ++i) q[i] = load_pack<T, V>(x + int64_t(t + i < t1 ? t + i : t1 - 1) * p.ld);
+    for (int i = 0; i < kRows; ++i) q[i] = load_word<T, V, RAG>(x + int64_t(t + i < t1 ? t + i : t1 - 1) * p.ld);
   };
   auto rows = [&](int t, bool all) {
 #pragma unroll
@@ -103,7 +113,7 @@ __global__ __launch_bounds__(256) void conv_kernel(ConvP p) {
 #pragma unroll
         for (int v = 0; v < V; ++v) o[v] = silu_f(o[v]);
       }
-      if (all || t + i < t1) store_pack<T, V>(y + int64_t(t + i) * p.D, o);
+      if (all || t + i < t1) store_word<T, V, RAG>(y + int64_t(t + i) * p.D, o);
     }
 #pragma unroll
     for (int j = 0; j < W - 1; ++j)
@@ -181,7 +191,7 @@ struct ConvBwP {
 // columns times 256 / CX tiles, whose sums of dw and dbias are joined in LDS
 // before they go to the workspace.  Bt 8, L 4096, D 2048, W 4 bf16: 89 us, 4.5 TB/s,
 // and 5 us for the join.
-template <typename T, int W, int V>
+template <typename T, int W, int V, bool RAG>
 __global__ __launch_bounds__(256) void conv_backward_kernel(ConvBwP p) {
   __shared__ float red[256 * (W + 1) * V];
   const int CX = 1 << p.lgcx, RY = 256 >> p.lgcx;
@@ -192,7 +202,7 @@ __global__ __launch_bounds__(256) void conv_backward_kernel(ConvBwP p) {
   const uint32_t cv = (cb << p.lgcx) + col;
   const int t0 = (int(grp) * RY + row) * p.tt;
   const int len = item_length(p.lengths, int(b), p.L);
-  const int d0 = int(cv) * V;
+  const int d0 = first_channel<V, RAG>(cv, p.D);
   float dw[W + 1][V];
 #pragma unroll
   for (int k = 0; k <= W; ++k)
@@ -223,9 +233,9 @@ __global__ __launch_bounds__(256) void conv_backward_kernel(ConvBwP p) {
 #pragma unroll
       for (int v = 0; v < V; ++v) xs[j][v] = dp[j][v] = 0.f;
       if (t >= 0) {
-        if (t < len) unpack<T, V>(load_pack<T, V>(x + int64_t(t) * p.ld), xs[j]);
+        if (t < len) unpack<T, V>(load_word<T, V, RAG>(x + int64_t(t) * p.ld), xs[j]);
       } else if (state != nullptr) {
-        unpack<T, V>(load_pack<T, V>(state + int64_t(t + W - 1) * p.D), xs[j]);
+        unpack<T, V>(load_word<T, V, RAG>(state + int64_t(t + W - 1) * p.D), xs[j]);
       }
     }
     Pack<T, V> qx[kRows], qd[kRows];
@@ -233,8 +243,8 @@ __global__ __launch_bounds__(256) void conv_backward_kernel(ConvBwP p) {
 #pragma unroll
       for (int i = 0; i < kRows; ++i) {
         const int64_t at = t + i < have ? t + i : have;
-        qx[i] = load_pack<T, V>(x + at * p.ld);
-        qd[i] = load_pack<T, V>(dy + at * p.D);
+        qx[i] = load_word<T, V, RAG>(x + at * p.ld);
+        qd[i] = load_word<T, V, RAG>(dy + at * p.D);
       }
     };
     // rows t .. t + 3; inner: all of them and the dx they complete lie in the tile
@@ -282,11 +292,11 @@ __global__ __launch_bounds__(256) void conv_backward_kernel(ConvBwP p) {
         }
         const int q = t + i - (W - 1);  // the dx row that is complete now
         if (inner) {
-          store_pack<T, V>(dx + int64_t(q) * p.D, o);
+          store_word<T, V, RAG>(dx + int64_t(q) * p.D, o);
         } else if (q >= t0) {
-          if (q < tend) store_pack<T, V>(dx + int64_t(q) * p.D, o);
+          if (q < tend) store_word<T, V, RAG>(dx + int64_t(q) * p.D, o);
         } else if (q < 0 && dst != nullptr) {
-          store_pack<T, V>(dst + int64_t(q + W - 1) * p.D, o);
+          store_word<T, V, RAG>(dst + int64_t(q + W - 1) * p.D, o);
         }
       }
 #pragma unroll
@@ -311,10 +321,10 @@ __global__ __launch_bounds__(256) void conv_backward_kernel(ConvBwP p) {
   float* part = p.part + (int64_t(b) * p.ngroups + grp) * (W + 1) * p.D;
   for (int i = threadIdx.x; i < (W + 1) * V * CX; i += 256) {
     const int c = i & (CX - 1), kv = i >> p.lgcx, k = kv / V, v = kv % V;
-    const uint32_t ch = ((cb << p.lgcx) + c) * V + v;
+    const uint32_t cc = (cb << p.lgcx) + c;
     float s = 0.f;
     for (int r = 0; r < RY; ++r) s += red[((r * (W + 1) + k) * V + v) * CX + c];
-    if (ch < uint32_t(p.D)) part[int64_t(k) * p.D + ch] = s;
+    if (cc < p.nv) part[int64_t(k) * p.D + first_channel<V, RAG>(cc, p.D) + v] = s;
   }
 }
 
@@ -335,15 +345,15 @@ int conv_tile(int64_t Bt, int L, int64_t nv, int most) {
   return tt;
 }
 
-template <typename T, int W, int V>
+template <typename T, int W, int V, bool RAG>
 hipError_t run_conv(const m3_conv_args& a, hipStream_t s) {
-  const int64_t nv = a.D / V;
+  const int64_t nv = (a.D + V - 1) / V;
   ConvP p{a.x, a.x_ld, a.w, a.bias, a.lengths, a.state, a.state_out, a.y, a.L, a.D, 0, 0, 0, 0, a.silu};
   p.tt = conv_tile(a.Bt, a.L, nv, 64);
   p.nv = uint32_t(nv);
   p.ntiles = uint32_t((a.L + p.tt - 1) / p.tt);
   p.total = uint32_t(nv * p.ntiles * a.Bt);
-  conv_kernel<T, W, V><<<(p.total + 255) / 256, 256, 0, s>>>(p);
+  conv_kernel<T, W, V, RAG><<<(p.total + 255) / 256, 256, 0, s>>>(p);
   return hipGetLastError();
 }
 template <typename T, int W, int V>
@@ -360,7 +370,7 @@ struct BwGeom {
 };
 BwGeom bw_geom(const m3_conv_backward_args& a, int V) {
   BwGeom g;
-  g.nv = a.D / V;
+  g.nv = (a.D + V - 1) / V;
   g.lgcx = 3;
   while (g.lgcx < 6 && (int64_t(1) << g.lgcx) < g.nv) ++g.lgcx;
   g.ncb = (g.nv + (int64_t(1) << g.lgcx) - 1) >> g.lgcx;
@@ -369,17 +379,12 @@ BwGeom bw_geom(const m3_conv_backward_args& a, int V) {
   g.ngroups = (a.L + per - 1) / per;
   return g;
 }
-bool bw_vec(const m3_conv_backward_args& a) {
-  const size_t e = a.in_dtype == M3_BF16 ? 2 : 4;
-  return rows_aligned(a.x, a.x_ld, e, 4 * e) && rows_aligned(a.dy, a.D, e, 4 * e) && rows_aligned(a.dx, a.D, e, 4 * e) &&
-         rows_aligned(a.state, a.D, e, 4 * e) && rows_aligned(a.dstate, a.D, e, 4 * e);
-}
-template <typename T, int W, int V>
+template <typename T, int W, int V, bool RAG>
 hipError_t run_bw(const m3_conv_backward_args& a, hipStream_t s) {
   const BwGeom g = bw_geom(a, V);
   ConvBwP p{a.x, a.x_ld, a.w, a.bias, a.lengths, a.state, a.dy, a.dx, a.dstate, static_cast<float*>(a.workspace),
             a.L, a.D, g.tt, uint32_t(g.nv), uint32_t(g.ncb), uint32_t(g.ngroups), g.lgcx, a.silu};
-  conv_backward_kernel<T, W, V><<<uint32_t(g.ncb * g.ngroups * a.Bt), 256, 0, s>>>(p);
+  conv_backward_kernel<T, W, V, RAG><<<uint32_t(g.ncb * g.ngroups * a.Bt), 256, 0, s>>>(p);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   ColSum c{};
@@ -395,18 +400,21 @@ hipError_t run_bw(const m3_conv_backward_args& a, hipStream_t s) {
   return launch_colsum(c, s);
 }
 
-// Four channels per thread in the backward, whose windows of x and dpre are twice
-// the forward's registers.
-#define M3_CONV_DISPATCH(FN, VB, VF, VECOK)                                                                              \
-  const bool bf = a.in_dtype == M3_BF16;                                                                         \
-  if (VECOK) {                                                                                                   \
-    if (a.W == 2) return bf ? FN<bf16_t, 2, VB>(a, s) : FN<float, 2, VF>(a, s);             \
-    if (a.W == 3) return bf ? FN<bf16_t, 3, VB>(a, s) : FN<float, 3, VF>(a, s);             \
-    return bf ? FN<bf16_t, 4, VB>(a, s) : FN<float, 4, VF>(a, s);                           \
-  }                                                                                                              \
-  if (a.W == 2) return bf ? FN<bf16_t, 2, 1>(a, s) : FN<float, 2, 1>(a, s);                                      \
-  if (a.W == 3) return bf ? FN<bf16_t, 3, 1>(a, s) : FN<float, 3, 1>(a, s);                                      \
-  return bf ? FN<bf16_t, 4, 1>(a, s) : FN<float, 4, 1>(a, s);
+template <typename T, int V, bool RAG>
+hipError_t by_taps(const m3_conv_args& a, hipStream_t s) {
+  if (a.W == 2) return run_conv<T, 2, V, RAG>(a, s);
+  return a.W == 3 ? run_conv<T, 3, V, RAG>(a, s) : run_conv<T, 4, V, RAG>(a, s);
+}
+template <typename T, int V>
+hipError_t step_by_taps(const m3_conv_step_args& a, hipStream_t s) {
+  if (a.W == 2) return run_step<T, 2, V>(a, s);
+  return a.W == 3 ? run_step<T, 3, V>(a, s) : run_step<T, 4, V>(a, s);
+}
+template <typename T, int V, bool RAG>
+hipError_t bw_by_taps(const m3_conv_backward_args& a, hipStream_t s) {
+  if (a.W == 2) return run_bw<T, 2, V, RAG>(a, s);
+  return a.W == 3 ? run_bw<T, 3, V, RAG>(a, s) : run_bw<T, 4, V, RAG>(a, s);
+}
 
 }  // namespace
 
@@ -417,27 +425,39 @@ hipError_t launch_colsum(const ColSum& c, hipStream_t s) {
 }
 
 hipError_t launch_conv(const m3_conv_args& a, hipStream_t s) {
-  const size_t e = a.in_dtype == M3_BF16 ? 2 : 4;
-  const bool ok = rows_aligned(a.x, a.x_ld, e, 16) && rows_aligned(a.y, a.D, e, 16) && rows_aligned(a.state, a.D, e, 16) &&
-                  rows_aligned(a.state_out, a.D, e, 16);
-  M3_CONV_DISPATCH(run_conv, 8, 4, ok)
+  const bool bf = a.in_dtype == M3_BF16;
+  const size_t e = bf ? 2 : 4;
+  if (rows_aligned(a.x, a.x_ld, e, 16) && rows_aligned(a.y, a.D, e, 16) && rows_aligned(a.state, a.D, e, 16) &&
+      rows_aligned(a.state_out, a.D, e, 16))
+    return bf ? by_taps<bf16_t, 8, false>(a, s) : by_taps<float, 4, false>(a, s);
+  // a carry updated in place has room for one writer per channel; 8192 tokens of 2047
+  // channels bf16 take 37 us in words, 47 us one at a time
+  if (a.D >= (bf ? 8 : 4) && (a.state_out == nullptr || a.state_out != a.state))
+    return bf ? by_taps<bf16_t, 8, true>(a, s) : by_taps<float, 4, true>(a, s);
+  return bf ? by_taps<bf16_t, 1, false>(a, s) : by_taps<float, 1, false>(a, s);
 }
 hipError_t launch_conv_step(const m3_conv_step_args& a, hipStream_t s) {
-  const size_t e = a.in_dtype == M3_BF16 ? 2 : 4;
-  const bool ok = rows_aligned(a.x, a.x_ld, e, 16) && rows_aligned(a.y, a.D, e, 16) && rows_aligned(a.state, a.D, e, 16) &&
-                  rows_aligned(a.state_out, a.D, e, 16);
-  M3_CONV_DISPATCH(run_step, 8, 4, ok)
+  const bool bf = a.in_dtype == M3_BF16;
+  const size_t e = bf ? 2 : 4;
+  if (rows_aligned(a.x, a.x_ld, e, 16) && rows_aligned(a.y, a.D, e, 16) && rows_aligned(a.state, a.D, e, 16) &&
+      rows_aligned(a.state_out, a.D, e, 16))
+    return bf ? step_by_taps<bf16_t, 8>(a, s) : step_by_taps<float, 4>(a, s);
+  return bf ? step_by_taps<bf16_t, 1>(a, s) : step_by_taps<float, 1>(a, s);
 }
-// The size covers both widths of the threads (the addresses are not known here).
+// Four channels per thread in the backward, whose windows of x and dpre are twice
+// the forward's registers; 8192 tokens of 2047 channels bf16 take 54 us in words
+// and 73 us one at a time.
 size_t conv_backward_workspace(const m3_conv_backward_args& a) {
-  const int64_t cols = int64_t(a.W + 1) * a.D;
-  int64_t rows = bw_geom(a, 1).ngroups;
-  if (a.D % 4 == 0) {
-    const int64_t r = bw_geom(a, 4).ngroups;
-    if (r > rows) rows = r;
-  }
-  return round256(size_t(rows) * a.Bt * cols * 4);
+  return round256(size_t(bw_geom(a, a.D >= 4 ? 4 : 1).ngroups) * a.Bt * (a.W + 1) * a.D * 4);
 }
-hipError_t launch_conv_backward(const m3_conv_backward_args& a, hipStream_t s) { M3_CONV_DISPATCH(run_bw, 4, 4, bw_vec(a)) }
+hipError_t launch_conv_backward(const m3_conv_backward_args& a, hipStream_t s) {
+  const bool bf = a.in_dtype == M3_BF16;
+  const size_t e = bf ? 2 : 4;
+  if (rows_aligned(a.x, a.x_ld, e, 4 * e) && rows_aligned(a.dy, a.D, e, 4 * e) && rows_aligned(a.dx, a.D, e, 4 * e) &&
+      rows_aligned(a.state, a.D, e, 4 * e) && rows_aligned(a.dstate, a.D, e, 4 * e))
+    return bf ? bw_by_taps<bf16_t, 4, false>(a, s) : bw_by_taps<float, 4, false>(a, s);
+  if (a.D >= 4) return bf ? bw_by_taps<bf16_t, 4, true>(a, s) : bw_by_taps<float, 4, true>(a, s);
+  return bf ? bw_by_taps<bf16_t, 1, false>(a, s) : bw_by_taps<float, 1, false>(a, s);
+}
 
 }  // namespace m3

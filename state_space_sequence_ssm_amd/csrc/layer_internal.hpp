@@ -94,16 +94,31 @@ __device__ __forceinline__ Pack<T, V> load_loose(const T* p) {
   return q;
 }
 template <typename T, int V>
-__device__ __forceinline__ void store_loose(T* p, const float* v) {
+__device__ __forceinline__ void put_loose(T* p, const Pack<T, V>& q) {
   constexpr int kBytes = int(sizeof(T)) * V, kStep = kBytes < 16 ? kBytes : 16;
-  Pack<T, V> q;
-  store_pack<T, V>(q.e, v);
 #pragma unroll
   for (int i = 0; i < kBytes / kStep; ++i) {
     typename Loose<kStep>::whole w;
     __builtin_memcpy(&w, reinterpret_cast<const char*>(&q) + kStep * i, kStep);
     reinterpret_cast<typename Loose<kStep>::type*>(p)[i] = w;
   }
+}
+template <typename T, int V>
+__device__ __forceinline__ void store_loose(T* p, const float* v) {
+  Pack<T, V> q;
+  store_pack<T, V>(q.e, v);
+  put_loose<T, V>(p, q);
+}
+// A word, aligned or (RAG) with the alignment of its elements.
+template <typename T, int V, bool RAG>
+__device__ __forceinline__ Pack<T, V> load_word(const T* p) {
+  if constexpr (RAG) return load_loose<T, V>(p);
+  else return load_pack<T, V>(p);
+}
+template <typename T, int V, bool RAG>
+__device__ __forceinline__ void store_word(T* p, const float* v) {
+  if constexpr (RAG) store_loose<T, V>(p, v);
+  else store_pack<T, V>(p, v);
 }
 template <typename T, int V>
 __device__ __forceinline__ void unpack(const Pack<T, V>& q, float* v) {

@@ -105,16 +105,6 @@ struct Place {
   // sums as a whole)
   __device__ __forceinline__ bool counts(int i, int j) const { return !RAG || j >= skip[i]; }
 };
-template <typename T, int V, bool RAG>
-__device__ __forceinline__ Pack<T, V> load_word(const T* p) {
-  if constexpr (RAG) return load_loose<T, V>(p);
-  else return load_pack<T, V>(p);
-}
-template <typename T, int V, bool RAG>
-__device__ __forceinline__ void store_word(T* p, const float* v) {
-  if constexpr (RAG) store_loose<T, V>(p, v);
-  else store_pack<T, V>(p, v);
-}
 // A gain's values at a lane's words (1 without one).
 template <int V, int NR, bool RAG>
 __device__ __forceinline__ void gain(const float* w, const int (&c)[NR], float (&o)[NR][V]) {

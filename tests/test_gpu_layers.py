@@ -96,7 +96,7 @@ def _conv_inputs(c, seed):
     m, t = Maker(seed), DT[dt]
     x = spoil(m(Bt, L, D, dtype=t), lengths)
     w, bias, state = m(D, W, scale=0.5), m(D) if has_bias else None, m(Bt, W - 1, D, dtype=t) if has_state else None
-    return (wide(x) if strided else x), w, bias, state, m(Bt, L, D, dtype=t)
+    return (wide(x, *(strided if isinstance(strided, tuple) else ())) if strided else x), w, bias, state, m(Bt, L, D, dtype=t)
 
 
 @pytest.mark.parametrize("c", CONV, ids=str)
@@ -452,3 +452,18 @@ def test_scans_off_alignment(ops, D, N, G, dt, off):
         c = (Bt, L, D, N, G, dt, lengths, True, True, True, True, True, off)
         test_scan(ops, c)
         test_scan_backward(ops, c)
+
+
+# Widths around one word, that end inside one, and in the second block of columns; rows
+# an element or more off a word.
+CONV_OFF = [(D, W, dt, off) for D, W, dt, off in [
+    (3, 4, "bf16", (1, 0)), (4, 2, "f32", (1, 0)), (5, 3, "f32", False), (7, 4, "bf16", False), (8, 4, "bf16", (1, 1)), (9, 4, "bf16", False),
+    (15, 3, "bf16", (3, 2)), (39, 2, "bf16", False), (66, 4, "f32", (1, 0)), (257, 4, "f32", False), (513, 4, "bf16", (2, 1)), (1030, 3, "bf16", False)]]
+
+
+@pytest.mark.parametrize("D,W,dt,off", CONV_OFF)
+def test_conv_off_alignment(ops, D, W, dt, off):
+    for Bt, L, lengths in ((1, 1, None), (2, 2, None), (3, 67, [67, 0, 2]), (1, 300, None)):
+        c = (Bt, L, D, W, dt, lengths, True, True, True, off)
+        test_conv(ops, c)
+        test_conv_backward(ops, c)
