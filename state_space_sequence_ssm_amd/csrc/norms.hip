@@ -84,7 +84,8 @@ constexpr int threads() {
 template <int V, int NV, int BLK, bool RAG>
 struct Place {
   static constexpr int NR = NV > 0 ? NV : 1;
-  int lane, team, g0, c[NR], skip[NR];
+  int lane, team, g0, skip[NR];
+  uint32_t c[NR];
   int64_t walker;
   bool in[NR];
   __device__ __forceinline__ Place(int lgteam, int G, int Dg) {
@@ -95,28 +96,36 @@ struct Place {
     g0 = int(slot % uint32_t(G)) * Dg;
 #pragma unroll
     for (int i = 0; i < NR; ++i) {
-      c[i] = (i * team + lane) * V;
-      in[i] = c[i] < Dg;
-      skip[i] = RAG && in[i] ? max(c[i] + V - Dg, 0) : 0;
-      c[i] = in[i] ? c[i] - skip[i] : 0;
+      const int at = (i * team + lane) * V;
+      in[i] = at < Dg;
+      skip[i] = RAG && in[i] ? max(at + V - Dg, 0) : 0;
+      c[i] = in[i] ? at - skip[i] : 0;
     }
   }
   // whether word i's element j is the sums' to take (a lane past the width drops its
   // sums as a whole)
   __device__ __forceinline__ bool counts(int i, int j) const { return !RAG || j >= skip[i]; }
 };
-// A gain's values at a lane's words (1 without one).
-template <int V, int NR, bool RAG>
-__device__ __forceinline__ void gain(const float* w, const int (&c)[NR], float (&o)[NR][V]) {
+// Element c of a row: a 32-bit offset, beside the row's address where the whole block
+// shares it.
+template <typename T>
+__device__ __forceinline__ T* col(T* row, uint32_t c) {
+  return reinterpret_cast<T*>(reinterpret_cast<uintptr_t>(row) + c * uint32_t(sizeof(T)));
+}
+// A gain's values at a word (1 without one), and at all of a lane's words.
+template <int V, bool RAG>
+__device__ __forceinline__ void gain_word(const float* w, uint32_t c, float (&o)[V]) {
+  if (w != nullptr) {
+    unpack<float, V>(load_word<float, V, RAG>(col(w, c)), o);
+  } else {
 #pragma unroll
-  for (int i = 0; i < NR; ++i) {
-    if (w != nullptr) {
-      unpack<float, V>(load_word<float, V, RAG>(w + c[i]), o[i]);
-    } else {
-#pragma unroll
-      for (int j = 0; j < V; ++j) o[i][j] = 1.f;
-    }
+    for (int j = 0; j < V; ++j) o[j] = 1.f;
   }
+}
+template <int V, int NR, bool RAG>
+__device__ __forceinline__ void gain(const float* w, const uint32_t (&c)[NR], float (&o)[NR][V]) {
+#pragma unroll
+  for (int i = 0; i < NR; ++i) gain_word<V, RAG>(w, c[i], o[i]);
 }
 
 // Gated norm.  32768 rows of 2048 bf16 in 8 groups: 79 us, 5.1 TB/s.
@@ -149,8 +158,8 @@ __global__ __launch_bounds__(threads<BLK>()) void gated_kernel(GatedP p) {
       row = row < p.M ? row : p.M - 1;
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
-        qx[i] = load_word<T, V, RAG>(x + row * p.xld + at.c[i]);
-        if (gated) qz[i] = load_word<T, V, RAG>(z + row * p.zld + at.c[i]);
+        qx[i] = load_word<T, V, RAG>(col(x + row * p.xld, at.c[i]));
+        if (gated) qz[i] = load_word<T, V, RAG>(col(z + row * p.zld, at.c[i]));
       }
     };
     auto turn = [&](int64_t k, bool last) {
@@ -193,7 +202,7 @@ __global__ __launch_bounds__(threads<BLK>()) void gated_kernel(GatedP p) {
 #pragma unroll
           for (int j = 0; j < V; ++j) o[j] = v[i][j] * r * wr[i][j] * gate[i][j];
         }
-        store_word<T, V, RAG>(y + row * p.D + at.c[i], o);
+        store_word<T, V, RAG>(col(y + row * p.D, at.c[i]), o);
       }
     };
     fetch(0);
@@ -215,6 +224,27 @@ __global__ __launch_bounds__(threads<BLK>()) void gated_kernel(GatedP p) {
         from_f32(to_f32(xr[c]) * gate * r * (w != nullptr ? w[c] : 1.f), y[row * p.D + c]);
       }
     }
+  }
+}
+
+// The widest units of the backward, blocks of 1024 lanes with 128 registers each, read
+// gains from the cache in every row and the row when its turn comes.
+template <int BLK>
+constexpr bool lean() {
+  return BLK == 1024;
+}
+
+// Makes the compiler take a word's values from the word again, instead of keeping them
+// as floats (twice the registers, for bf16) from one pass over a row to the next.
+template <typename T, int V>
+__device__ __forceinline__ void afresh(Pack<T, V>& q) {
+  static_assert(sizeof(q) % 4 == 0, "whole dwords");
+#pragma unroll
+  for (int i = 0; i < int(sizeof(q) / 4); ++i) {
+    uint32_t w;
+    __builtin_memcpy(&w, reinterpret_cast<char*>(&q) + 4 * i, 4);
+    asm volatile("" : "+v"(w));
+    __builtin_memcpy(reinterpret_cast<char*>(&q) + 4 * i, &w, 4);
   }
 }
 
@@ -250,7 +280,7 @@ __global__ __launch_bounds__(threads<BLK>()) void gated_backward_kernel(GatedBwP
   const int64_t whole = p.M / p.walkers;
   if constexpr (NV > 0) {
     float dw[NV][V], wr[NV][V];
-    gain<V, NV, RAG>(w, at.c, wr);
+    if constexpr (!lean<BLK>()) gain<V, NV, RAG>(w, at.c, wr);
 #pragma unroll
     for (int i = 0; i < NV; ++i)
 #pragma unroll
@@ -261,12 +291,13 @@ __global__ __launch_bounds__(threads<BLK>()) void gated_backward_kernel(GatedBwP
       row = row < p.M ? row : p.M - 1;
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
-        qx[i] = load_word<T, V, RAG>(x + row * p.xld + at.c[i]);
-        qd[i] = load_word<T, V, RAG>(dy + row * p.D + at.c[i]);
-        if (gated) qz[i] = load_word<T, V, RAG>(z + row * p.zld + at.c[i]);
+        qx[i] = load_word<T, V, RAG>(col(x + row * p.xld, at.c[i]));
+        qd[i] = load_word<T, V, RAG>(col(dy + row * p.D, at.c[i]));
+        if (gated) qz[i] = load_word<T, V, RAG>(col(z + row * p.zld, at.c[i]));
       }
     };
     auto turn = [&](int64_t k, bool last) {
+      if constexpr (lean<BLK>()) fetch(k);
       float xv[NV][V], zv[NV][V], d[NV][V], sg[NV][V];
       float s1 = 0.f, s2 = 0.f;
 #pragma unroll
@@ -282,6 +313,7 @@ __global__ __launch_bounds__(threads<BLK>()) void gated_backward_kernel(GatedBwP
           for (int j = 0; j < V; ++j) zv[i][j] = sg[i][j] = 1.f;
         }
         float t1 = 0.f, t2 = 0.f;
+        if constexpr (lean<BLK>()) gain_word<V, RAG>(w, at.c[i], wr[i]);
 #pragma unroll
         for (int j = 0; j < V; ++j) {
           const float gate = zv[i][j] * sg[i][j];
@@ -294,7 +326,7 @@ __global__ __launch_bounds__(threads<BLK>()) void gated_backward_kernel(GatedBwP
         s1 += at.in[i] ? t1 : 0.f;
         s2 += at.in[i] ? t2 : 0.f;
       }
-      if (!last) fetch(k + 1);
+      if (!lean<BLK>() && !last) fetch(k + 1);
       team_sum2<BLK>(s1, s2, p.lgteam, red[k & 1]);
       const float r = rsqrtf(s1 * p.inv + p.eps), m = s2 * r * p.inv;
       const int64_t row = at.walker + k * p.walkers;
@@ -302,6 +334,19 @@ __global__ __launch_bounds__(threads<BLK>()) void gated_backward_kernel(GatedBwP
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
         float ox[V], oz[V];
+        if constexpr (lean<BLK>()) {
+          gain_word<V, RAG>(w, at.c[i], wr[i]);
+          afresh(qx[i]);
+          afresh(qd[i]);
+          unpack<T, V>(qx[i], xv[i]);
+          unpack<T, V>(qd[i], d[i]);
+          if (gated) {
+            afresh(qz[i]);
+            unpack<T, V>(qz[i], zv[i]);
+#pragma unroll
+            for (int j = 0; j < V; ++j) sg[i][j] = sigmoid_f(zv[i][j]);
+          }
+        }
 #pragma unroll
         for (int j = 0; j < V; ++j) {
           const float gate = zv[i][j] * sg[i][j];
@@ -312,17 +357,17 @@ __global__ __launch_bounds__(threads<BLK>()) void gated_backward_kernel(GatedBwP
           oz[j] = (first ? dv * xv[i][j] : d[i][j] * n * wr[i][j]) * dsilu_f(zv[i][j], sg[i][j]);
           dw[i][j] = fmaf(u, n, dw[i][j]);
         }
-        store_word<T, V, RAG>(dx + row * p.D + at.c[i], ox);
-        if (gated) store_word<T, V, RAG>(dz + row * p.D + at.c[i], oz);
+        store_word<T, V, RAG>(col(dx + row * p.D, at.c[i]), ox);
+        if (gated) store_word<T, V, RAG>(col(dz + row * p.D, at.c[i]), oz);
       }
     };
-    fetch(0);
+    if constexpr (!lean<BLK>()) fetch(0);
     for (int64_t k = 0; k < whole; ++k) turn(k, false);
     if (whole * p.walkers < p.M) turn(whole, true);
     if (part == nullptr) return;
 #pragma unroll
     for (int i = 0; i < NV; ++i)
-      if (at.in[i]) store_word<float, V, RAG>(part + at.c[i], dw[i]);
+      if (at.in[i]) store_word<float, V, RAG>(col(part, at.c[i]), dw[i]);
   } else {
     if (part != nullptr)
       for (int c = at.lane; c < p.Dg; c += at.team) part[c] = 0.f;
@@ -384,8 +429,8 @@ __global__ __launch_bounds__(threads<BLK>()) void residual_kernel(ResP p) {
       row = row < p.M ? row : p.M - 1;
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
-        qx[i] = load_word<T, V, RAG>(x + row * p.xld + at.c[i]);
-        if (res != nullptr) qr[i] = load_word<R, V, RAG>(res + row * p.D + at.c[i]);
+        qx[i] = load_word<T, V, RAG>(col(x + row * p.xld, at.c[i]));
+        if (res != nullptr) qr[i] = load_word<R, V, RAG>(col(res + row * p.D, at.c[i]));
         else qr[i] = Pack<R, V>{};
       }
     };
@@ -414,10 +459,10 @@ __global__ __launch_bounds__(threads<BLK>()) void residual_kernel(ResP p) {
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
         float o[V];
-        if (out != nullptr) store_word<R, V, RAG>(out + row * p.D + at.c[i], h[i]);
+        if (out != nullptr) store_word<R, V, RAG>(col(out + row * p.D, at.c[i]), h[i]);
 #pragma unroll
         for (int j = 0; j < V; ++j) o[j] = h[i][j] * r * wr[i][j];
-        store_word<T, V, RAG>(y + row * p.D + at.c[i], o);
+        store_word<T, V, RAG>(col(y + row * p.D, at.c[i]), o);
       }
     };
     for (int64_t k = 0; k < whole; ++k) turn(k, false);
@@ -483,23 +528,26 @@ __global__ __launch_bounds__(threads<BLK>()) void residual_backward_kernel(ResBw
       row = row < p.M ? row : p.M - 1;
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
-        qh[i] = load_word<R, V, RAG>(h + row * p.D + at.c[i]);
-        qd[i] = load_word<T, V, RAG>(dy + row * p.D + at.c[i]);
-        if (dro != nullptr) qr[i] = load_word<R, V, RAG>(dro + row * p.D + at.c[i]);
+        qh[i] = load_word<R, V, RAG>(col(h + row * p.D, at.c[i]));
+        qd[i] = load_word<T, V, RAG>(col(dy + row * p.D, at.c[i]));
+        if (dro != nullptr) qr[i] = load_word<R, V, RAG>(col(dro + row * p.D, at.c[i]));
         else qr[i] = Pack<R, V>{};
-        if (p.has_ds) qx[i] = load_word<T, V, RAG>(x + row * p.xld + at.c[i]);
+        if (p.has_ds) qx[i] = load_word<T, V, RAG>(col(x + row * p.xld, at.c[i]));
         else qx[i] = Pack<T, V>{};
       }
     };
-    fetch(0);
+    if constexpr (!lean<BLK>()) fetch(0);
     float dw[NV][V], ds[NV][V], wr[NV][V], sr[NV][V];
-    gain<V, NV, RAG>(p.w, at.c, wr);
-    gain<V, NV, RAG>(p.scale, at.c, sr);
+    if constexpr (!lean<BLK>()) {
+      gain<V, NV, RAG>(p.w, at.c, wr);
+      gain<V, NV, RAG>(p.scale, at.c, sr);
+    }
 #pragma unroll
     for (int i = 0; i < NV; ++i)
 #pragma unroll
       for (int j = 0; j < V; ++j) dw[i][j] = ds[i][j] = 0.f;
     auto turn = [&](int64_t k, bool last) {
+      if constexpr (lean<BLK>()) fetch(k);
       // the row as it came, so that it takes half the registers
       Pack<R, V> ch[NV], cr[NV];
       Pack<T, V> cd[NV], cx[NV];
@@ -511,6 +559,7 @@ __global__ __launch_bounds__(threads<BLK>()) void residual_backward_kernel(ResBw
         cd[i] = qd[i];
         cx[i] = qx[i];
         float t1 = 0.f, t2 = 0.f;
+        if constexpr (lean<BLK>()) gain_word<V, RAG>(p.w, at.c[i], wr[i]);
 #pragma unroll
         for (int j = 0; j < V; ++j) {
           const float hv = at.counts(i, j) ? to_f32(ch[i].e[j]) : 0.f;
@@ -521,7 +570,7 @@ __global__ __launch_bounds__(threads<BLK>()) void residual_backward_kernel(ResBw
         s1 += at.in[i] ? t1 : 0.f;
         s2 += at.in[i] ? t2 : 0.f;
       }
-      if (!last) fetch(k + 1);
+      if (!lean<BLK>() && !last) fetch(k + 1);
       team_sum2<BLK>(s1, s2, p.lgteam, red[k & 1]);
       const float r = rsqrtf(s1 * p.inv + p.eps), m = s2 * r * p.inv;
       const int64_t row = at.walker + k * p.walkers;
@@ -529,6 +578,12 @@ __global__ __launch_bounds__(threads<BLK>()) void residual_backward_kernel(ResBw
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
         float o[V], ox[V];
+        if constexpr (lean<BLK>()) {
+          gain_word<V, RAG>(p.w, at.c[i], wr[i]);
+          gain_word<V, RAG>(p.scale, at.c[i], sr[i]);
+          afresh(ch[i]);
+          afresh(cd[i]);
+        }
 #pragma unroll
         for (int j = 0; j < V; ++j) {
           const float n = to_f32(ch[i].e[j]) * r, d = to_f32(cd[i].e[j]);
@@ -537,8 +592,8 @@ __global__ __launch_bounds__(threads<BLK>()) void residual_backward_kernel(ResBw
           dw[i][j] = fmaf(d, n, dw[i][j]);
           ds[i][j] = fmaf(o[j], to_f32(cx[i].e[j]), ds[i][j]);
         }
-        if (dres != nullptr) store_word<R, V, RAG>(dres + row * p.D + at.c[i], o);
-        if (dx != nullptr) store_word<T, V, RAG>(dx + row * p.D + at.c[i], ox);
+        if (dres != nullptr) store_word<R, V, RAG>(col(dres + row * p.D, at.c[i]), o);
+        if (dx != nullptr) store_word<T, V, RAG>(col(dx + row * p.D, at.c[i]), ox);
       }
     };
     for (int64_t k = 0; k < whole; ++k) turn(k, false);
@@ -546,8 +601,8 @@ __global__ __launch_bounds__(threads<BLK>()) void residual_backward_kernel(ResBw
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       if (!at.in[i]) continue;
-      if (pw != nullptr) store_word<float, V, RAG>(pw + at.c[i], dw[i]);
-      if (ps != nullptr) store_word<float, V, RAG>(ps + at.c[i], ds[i]);
+      if (pw != nullptr) store_word<float, V, RAG>(col(pw, at.c[i]), dw[i]);
+      if (ps != nullptr) store_word<float, V, RAG>(col(ps, at.c[i]), ds[i]);
     }
   } else {
     for (int c = at.lane; c < p.D; c += at.team) {
@@ -578,12 +633,14 @@ __global__ __launch_bounds__(threads<BLK>()) void residual_backward_kernel(ResBw
 
 // Lanes for a unit of `width` elements: a part of a wave up to 64 words, wider
 // ones over several words per lane or several waves, the loop for what a block
-// does not hold in registers (over 2048 words, 16384 bf16 values; in the backward
-// over 1024).  Forward, a unit of 65 to 256 words is one wave's where the units
+// does not hold in registers (over 2048 words: 16384 bf16 values, 8192 fp32).
+// Forward, a unit of 65 to 256 words is one wave's where the units
 // fill the card (2048 or more) and a block's otherwise.  The backward holds four
 // times the registers per word and takes a block at once: 32768 rows of 2048 bf16
 // take 159 us with one word per lane of four waves, and 216 us with four words per
-// lane of one wave (216 registers).
+// lane of one wave (216 registers).  Its widest units spill some of them: 4096 rows of
+// 8192 fp32 take 135 us gated and 164 us residual, in the loop 310 and 428 us; of
+// 16384 bf16 255 and 317 us, in the loop 583 and 777 us.
 Geom pick(int64_t units, int width, int in_dtype, bool backward) {
   const int whole = in_dtype == M3_BF16 ? 8 : 4, V = width >= whole ? whole : 1;
   Geom g{V, 1, 0, 6};
@@ -599,7 +656,7 @@ Geom pick(int64_t units, int width, int in_dtype, bool backward) {
   } else if (words <= 1024) {
     g.blk = backward ? 512 : 256;
     g.nv = backward ? 2 : 4;
-  } else if (words <= 2048 && !backward) {
+  } else if (words <= 2048) {
     g.blk = 1024;
     g.nv = 2;
   } else {
@@ -637,6 +694,7 @@ constexpr int64_t kForwardWaves = 8192, kBackwardWaves = 4096;
 #define M3_NORM_BACKWARD_WIDTH(g, V, RAG, CALL)   \
   if ((g).blk == 0) return CALL(V, 1, 0, RAG);    \
   if ((g).blk == 512) return CALL(V, 2, 512, RAG); \
+  if ((g).blk == 1024) return CALL(V, 2, 1024, RAG); \
   if ((g).nv == 1) return CALL(V, 1, 256, RAG);   \
   return CALL(V, 2, 256, RAG);
 #define M3_NORM_DISPATCH(g, vec, VV, WIDTH, CALL) \

@@ -297,6 +297,10 @@ GATED = [
     ((3, 20008), 1, "f32", False, True, True, False),
     ((2, 40001), 1, "bf16", True, True, True, False),
     ((2, 36002), 1, "f32", False, True, True, True),
+    ((5, 8192), 1, "f32", True, True, True, False),
+    ((270, 6000), 1, "f32", False, False, True, True),
+    ((300, 8448), 1, "bf16", False, True, True, False),
+    ((5, 16384), 1, "bf16", True, True, False, True),
 ]
 
 
@@ -340,6 +344,9 @@ RESIDUAL = [
     ((2100, 1000), "f32", "f32", True, True, True),
     ((4, 8200), "bf16", "bf16", True, True, False),
     ((3, 40001), "bf16", "f32", True, True, True),
+    ((270, 8192), "f32", "f32", True, True, False),
+    ((300, 8448), "bf16", "bf16", False, True, True),
+    ((5, 16384), "bf16", "f32", True, True, False),
 ]
 
 
@@ -385,7 +392,7 @@ def test_residual_norm(ops, c):
 # Widths that end inside a 16-byte word and rows off its alignment, at each way that
 # units are dealt to lanes.
 UNALIGNED = [(2100, 9, 1), (2500, 49, 1), (2100, 515, 1), (2100, 1030, 1), (30, 1041, 3), (5, 2051, 1), (5, 4099, 1),
-             (4, 8209, 1), (70, 1024, 2)]
+             (5, 6001, 1), (4, 8209, 1), (70, 1024, 2)]
 
 
 @pytest.mark.parametrize("dt", ["bf16", "f32"])
