@@ -337,6 +337,14 @@ def _rows(t, dtype, shape, lead, name, dev):
     if t.is_contiguous():
         return t.data_ptr(), 0
     strides = t.stride()
+    # the usual slices first (one or two axes of rows, one or two inside a row): 0.5 us
+    # instead of 2, for up to five tensors of a call
+    n, ld = len(shape), strides[lead - 1]
+    if strides[-1] == 1 and shape[lead - 1] > 1 and (
+            (n == lead + 1 and ld >= shape[-1]) or
+            (n == lead + 2 and strides[lead] == shape[-1] and ld >= shape[-2] * shape[-1])) and (
+            lead == 1 or (lead == 2 and strides[0] == ld * shape[1])):
+        return t.data_ptr(), ld
     width = 1
     for n, st in zip(reversed(shape[lead:]), reversed(strides[lead:])):
         if n > 1 and st != width:
@@ -358,12 +366,12 @@ def _rows(t, dtype, shape, lead, name, dev):
 
 def _out(given, dtype, shape, name, like, dev):
     """An output and its address: the given tensor after checking it, or a new one on
-    the device of `like` (an input that is checked itself).  A dense tensor of the same
-    shape and type is the fastest pattern (1.2 us instead of 1.8)."""
+    the device of `like` (an input that is checked itself).  `like` is the input of the
+    same shape and type where there is one: the fastest pattern, 1.2 us instead of 2.2."""
     if given is not None:
         return given, _dense(given, dtype, shape, name, dev)
-    if dtype is like.dtype and like.shape == shape and like.is_contiguous():
-        given = torch.empty_like(like)
+    if dtype is like.dtype and like.shape == shape:
+        given = torch.empty_like(like, memory_format=torch.contiguous_format)
     else:
         given = torch.empty(shape, dtype=dtype, device=like.device)
     return given, given.data_ptr()
@@ -423,15 +431,15 @@ def m3_causal_conv(x, w, bias=None, state=None, *, lengths=None, silu=True, y=No
     W = w.shape[-1]
     dev, t = x.get_device(), x.dtype
     a = _lib.ConvArgs()
-    y, a.y = _out(y, t, (Bt, L, D), "y", x, dev)
-    if want_state or state_out is not None:
-        state_out, a.state_out = _out(state_out, t, (Bt, W - 1, D), "state_out", x, dev)
     a.Bt, a.L, a.D, a.W, a.in_dtype, a.silu = Bt, L, D, W, _dtype_code(x), 1 if silu else 0
     a.x, a.x_ld = _rows(x, t, x.shape, 2, "x", dev)
     a.w = _dense(w, _F32, (D, W), "w", dev)
     a.bias = _dense(bias, _F32, (D,), "bias", dev)
     a.lengths = _dense(lengths, torch.int32, (Bt,), "lengths", dev)
     a.state = _dense(state, t, (Bt, W - 1, D), "state", dev)
+    y, a.y = _out(y, t, (Bt, L, D), "y", x, dev)
+    if want_state or state_out is not None:
+        state_out, a.state_out = _out(state_out, t, (Bt, W - 1, D), "state_out", x if state is None else state, dev)
     _run_layer("m3_causal_conv", a, dev)
     return dict(y=y, state=state_out)
 
@@ -444,13 +452,13 @@ def m3_causal_conv_step(state, x, w, bias=None, *, silu=True, y=None, state_out=
     W = w.shape[-1]
     dev, t = state.get_device(), x.dtype
     a = _lib.ConvStepArgs()
-    y, a.y = _out(y, t, (Bt, D), "y", x, dev)
     a.Bt, a.D, a.W, a.in_dtype, a.silu = Bt, D, W, _dtype_code(x), 1 if silu else 0
     a.x, a.x_ld = _rows(x, t, x.shape, 1, "x", dev)
     a.w = _dense(w, _F32, (D, W), "w", dev)
     a.bias = _dense(bias, _F32, (D,), "bias", dev)
     a.state = _dense(state, t, (Bt, W - 1, D), "state", dev)
     a.state_out = _dense(state_out, t, (Bt, W - 1, D), "state_out", dev)
+    y, a.y = _out(y, t, (Bt, D), "y", x, dev)
     _run_layer("m3_causal_conv_step", a, dev)
     return y
 
@@ -466,13 +474,6 @@ def m3_causal_conv_backward(x, w, bias=None, state=None, *, dy, lengths=None, si
     dev, t = x.get_device(), x.dtype
     got = out or {}
     a = _lib.ConvBackwardArgs()
-    out = dict(dx=None, dw=None, dbias=None, dstate=None)
-    out["dx"], a.dx = _out(got.get("dx"), t, (Bt, L, D), "dx", x, dev)
-    out["dw"], a.dw = _out(got.get("dw"), _F32, (D, W), "dw", x, dev)
-    if bias is not None:
-        out["dbias"], a.dbias = _out(got.get("dbias"), _F32, (D,), "dbias", x, dev)
-    if want_state_grad or "dstate" in got:
-        out["dstate"], a.dstate = _out(got.get("dstate"), t, (Bt, W - 1, D), "dstate", x, dev)
     a.Bt, a.L, a.D, a.W, a.in_dtype, a.silu = Bt, L, D, W, _dtype_code(x), 1 if silu else 0
     a.x, a.x_ld = _rows(x, t, x.shape, 2, "x", dev)
     a.w = _dense(w, _F32, (D, W), "w", dev)
@@ -480,6 +481,13 @@ def m3_causal_conv_backward(x, w, bias=None, state=None, *, dy, lengths=None, si
     a.lengths = _dense(lengths, torch.int32, (Bt,), "lengths", dev)
     a.state = _dense(state, t, (Bt, W - 1, D), "state", dev)
     a.dy = _dense(dy, t, (Bt, L, D), "dy", dev)
+    out = dict(dx=None, dw=None, dbias=None, dstate=None)
+    out["dx"], a.dx = _out(got.get("dx"), t, (Bt, L, D), "dx", x, dev)
+    out["dw"], a.dw = _out(got.get("dw"), _F32, (D, W), "dw", w, dev)
+    if bias is not None:
+        out["dbias"], a.dbias = _out(got.get("dbias"), _F32, (D,), "dbias", bias, dev)
+    if want_state_grad or "dstate" in got:
+        out["dstate"], a.dstate = _out(got.get("dstate"), t, (Bt, W - 1, D), "dstate", x if state is None else state, dev)
     workspace = _take_workspace("m3_causal_conv_backward", a, workspace, dev)
     _run_layer("m3_causal_conv_backward", a, dev)
     return out
@@ -517,13 +525,13 @@ def m3_selective_scan(x, dt, A, B, C, D=None, z=None, h0=None, *, lengths=None, 
     N = A.shape[-1]
     dev = x.get_device()
     a = _lib.ScanArgs()
-    y, a.y = _out(y, x.dtype, (Bt, L, width), "y", x, dev)
-    if want_state or h_final is not None:
-        h_final, a.h_final = _out(h_final, _F32, (Bt, width, N), "h_final", x, dev)
     a.Bt, a.L = Bt, L
     _scan_inputs(a, dev, (Bt, L), x, dt, A, B, C, D, z, dt_softplus, dt_bias)
     a.h0 = _dense(h0, _F32, (Bt, width, N), "h0", dev)
     a.lengths = _dense(lengths, torch.int32, (Bt,), "lengths", dev)
+    y, a.y = _out(y, x.dtype, (Bt, L, width), "y", x, dev)
+    if want_state or h_final is not None:
+        h_final, a.h_final = _out(h_final, _F32, (Bt, width, N), "h_final", x if h0 is None else h0, dev)
     if workspace is not False:
         workspace = _take_workspace("m3_selective_scan", a, workspace, dev)
     _run_layer("m3_selective_scan", a, dev)
@@ -539,11 +547,11 @@ def m3_selective_scan_step(h, x, dt, A, B, C, D=None, z=None, *, dt_softplus=Fal
     N = A.shape[-1]
     dev = h.get_device()
     a = _lib.ScanStepArgs()
-    y, a.y = _out(y, x.dtype, (Bt, width), "y", x, dev)
     a.Bt = Bt
     _scan_inputs(a, dev, (Bt,), x, dt, A, B, C, D, z, dt_softplus, dt_bias)
     a.h = _dense(h, _F32, (Bt, width, N), "h", dev)
     a.h_out = _dense(h_out, _F32, (Bt, width, N), "h_out", dev)
+    y, a.y = _out(y, x.dtype, (Bt, width), "y", x, dev)
     _run_layer("m3_selective_scan_step", a, dev)
     return y
 
@@ -559,21 +567,22 @@ def m3_selective_scan_backward(x, dt, A, B, C, D=None, z=None, h0=None, *, dy, d
     G, N = B.shape[-2:]
     dev, t = x.get_device(), x.dtype
     got = out or {}
-    shapes = dict(dx=((Bt, L, width), t), ddt=((Bt, L, width), t), dA=((width, N), _F32), dB=((Bt, L, G, N), t),
-                  dC=((Bt, L, G, N), t), dD=((width,), _F32), dz=((Bt, L, width), t), ddt_bias=((width,), _F32),
-                  dh0=((Bt, width, N), _F32))
-    absent = dict(dD=D is None, dz=z is None, ddt_bias=dt_bias is None, dh0=not want_carry_grads and "dh0" not in got)
     a = _lib.ScanBackwardArgs()
-    out = {}
-    for k, (shape, ty) in shapes.items():
-        out[k], at = (None, None) if absent.get(k) else _out(got.get(k), ty, shape, k, x, dev)
-        setattr(a, k, at)
     a.fwd.Bt, a.fwd.L = Bt, L
     _scan_inputs(a.fwd, dev, (Bt, L), x, dt, A, B, C, D, z, dt_softplus, dt_bias)
     a.fwd.h0 = _dense(h0, _F32, (Bt, width, N), "h0", dev)
     a.fwd.lengths = _dense(lengths, torch.int32, (Bt,), "lengths", dev)
     a.dy = _dense(dy, t, (Bt, L, width), "dy", dev)
     a.dh_final = _dense(dh_final, _F32, (Bt, width, N), "dh_final", dev)
+    out = {}
+    rows, state = (Bt, L, width), (Bt, width, N)
+    for k, like, shape, ty, wanted in (
+            ("dx", x, rows, t, True), ("ddt", dt, rows, t, True), ("dA", A, (width, N), _F32, True), ("dB", B, B.shape, t, True),
+            ("dC", C, B.shape, t, True), ("dD", D, (width,), _F32, D is not None), ("dz", z, rows, t, z is not None),
+            ("ddt_bias", dt_bias, (width,), _F32, dt_bias is not None),
+            ("dh0", x if h0 is None else h0, state, _F32, want_carry_grads or "dh0" in got)):
+        out[k], at = _out(got.get(k), ty, shape, k, like, dev) if wanted else (None, None)
+        setattr(a, k, at)
     workspace = _take_workspace("m3_selective_scan_backward", a, workspace, dev)
     _run_layer("m3_selective_scan_backward", a, dev)
     return out
@@ -598,8 +607,8 @@ def m3_gated_norm(x, z=None, w=None, *, groups=1, eps=1e-6, gate_first=True, y=N
     may be given as x or z themselves where those are dense)."""
     dev = x.get_device()
     a = _lib.GatedNormArgs()
-    y, a.y = _out(y, x.dtype, x.shape, "y", x, dev)
     _gated_inputs(a, dev, x, z, w, groups, eps, gate_first)
+    y, a.y = _out(y, x.dtype, x.shape, "y", x, dev)
     _run_layer("m3_gated_norm", a, dev)
     return y
 
@@ -611,14 +620,14 @@ def m3_gated_norm_backward(x, z=None, w=None, *, dy, groups=1, eps=1e-6, gate_fi
     dev, t = x.get_device(), x.dtype
     got = out or {}
     a = _lib.GatedNormBackwardArgs()
+    _gated_inputs(a.fwd, dev, x, z, w, groups, eps, gate_first)
+    a.dy = _dense(dy, t, x.shape, "dy", dev)
     out = dict(dx=None, dz=None, dw=None)
     out["dx"], a.dx = _out(got.get("dx"), t, x.shape, "dx", x, dev)
     if z is not None:
         out["dz"], a.dz = _out(got.get("dz"), t, x.shape, "dz", x, dev)
     if w is not None:
-        out["dw"], a.dw = _out(got.get("dw"), _F32, x.shape[-1:], "dw", x, dev)
-    _gated_inputs(a.fwd, dev, x, z, w, groups, eps, gate_first)
-    a.dy = _dense(dy, t, x.shape, "dy", dev)
+        out["dw"], a.dw = _out(got.get("dw"), _F32, x.shape[-1:], "dw", w, dev)
     workspace = _take_workspace("m3_gated_norm_backward", a, workspace, dev)
     _run_layer("m3_gated_norm_backward", a, dev)
     return out
@@ -635,15 +644,15 @@ def m3_residual_norm(x, residual=None, w=None, scale=None, *, eps=1e-6, y=None, 
     width = shape[-1]
     rt = residual.dtype if residual is not None else residual_out.dtype if residual_out is not None else t
     a = _lib.ResidualNormArgs()
-    y, a.y = _out(y, t, shape, "y", x, dev)
-    if want_residual or residual_out is not None:
-        residual_out, a.residual_out = _out(residual_out, rt, shape, "residual_out", residual if residual is not None else x, dev)
     a.M, a.D, a.in_dtype = x.numel() // width if width else 0, width, _dtype_code(x)
     a.res_dtype, a.eps = _lib.M3_F32 if rt == _F32 else _lib.M3_BF16, eps
     a.x, a.x_ld = _rows(x, t, shape, len(shape) - 1, "x", dev)
     a.residual = _dense(residual, rt, shape, "residual", dev)
     a.scale = _dense(scale, _F32, (width,), "scale", dev)
     a.w = _dense(w, _F32, (width,), "w", dev)
+    y, a.y = _out(y, t, shape, "y", x, dev)
+    if want_residual or residual_out is not None:
+        residual_out, a.residual_out = _out(residual_out, rt, shape, "residual_out", residual if residual is not None else x, dev)
     _run_layer("m3_residual_norm", a, dev)
     return dict(y=y, residual=residual_out)
 
@@ -659,16 +668,6 @@ def m3_residual_norm_backward(h, x=None, w=None, scale=None, *, dy, dresidual=No
     dev, t, width = h.get_device(), dy.dtype, h.shape[-1]
     got = out or {}
     a = _lib.ResidualNormBackwardArgs()
-    out = dict(dresidual=None, dx=None, dw=None, dscale=None)
-    out["dresidual"], a.dresidual = _out(got.get("dresidual"), h.dtype, h.shape, "dresidual", h, dev)
-    if scale is not None or t != h.dtype or got.get("dx") is not None:
-        out["dx"], a.dx = _out(got.get("dx"), t, h.shape, "dx", dy, dev)
-    else:
-        out["dx"] = out["dresidual"]
-    if w is not None:
-        out["dw"], a.dw = _out(got.get("dw"), _F32, (width,), "dw", h, dev)
-    if scale is not None:
-        out["dscale"], a.dscale = _out(got.get("dscale"), _F32, (width,), "dscale", h, dev)
     a.M, a.D, a.in_dtype = h.numel() // width if width else 0, width, _dtype_code(dy)
     a.res_dtype, a.eps = _dtype_code(h), eps
     a.h = _dense(h, h.dtype, h.shape, "h", dev)
@@ -677,6 +676,16 @@ def m3_residual_norm_backward(h, x=None, w=None, scale=None, *, dy, dresidual=No
     a.w = _dense(w, _F32, (width,), "w", dev)
     a.dy = _dense(dy, t, h.shape, "dy", dev)
     a.dresidual_out = _dense(dresidual, h.dtype, h.shape, "dresidual", dev)
+    out = dict(dresidual=None, dx=None, dw=None, dscale=None)
+    out["dresidual"], a.dresidual = _out(got.get("dresidual"), h.dtype, h.shape, "dresidual", h, dev)
+    if scale is not None or t != h.dtype or got.get("dx") is not None:
+        out["dx"], a.dx = _out(got.get("dx"), t, h.shape, "dx", dy, dev)
+    else:
+        out["dx"] = out["dresidual"]
+    if w is not None:
+        out["dw"], a.dw = _out(got.get("dw"), _F32, (width,), "dw", w, dev)
+    if scale is not None:
+        out["dscale"], a.dscale = _out(got.get("dscale"), _F32, (width,), "dscale", scale, dev)
     workspace = _take_workspace("m3_residual_norm_backward", a, workspace, dev)
     _run_layer("m3_residual_norm_backward", a, dev)
     return out
