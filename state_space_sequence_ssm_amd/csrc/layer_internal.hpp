@@ -43,7 +43,7 @@ hipError_t launch_residual_norm_backward(const m3_residual_norm_backward_args& a
 // ---------------------------------------------------------------- device helpers
 // V consecutive elements, moved as whole words (16 bytes at most per access).
 template <typename T, int V>
-struct alignas(sizeof(T) * V < 16 ? sizeof(T) * V : 16) Pack {
+struct alignas(V & (V - 1) ? sizeof(T) : sizeof(T) * V < 16 ? sizeof(T) * V : 16) Pack {
   T e[V];
 };
 __device__ __forceinline__ float to_f32(float v) { return v; }

@@ -33,8 +33,8 @@ struct Four {
     for (int j = 0; j < 4; ++j) {
       delta[j] = pd[j * CHB];
       u[j] = pu[j * CHB];
-      B[j] = *reinterpret_cast<const typename States<S>::type*>(pB + j * NP);
-      if (FULL) C[j] = *reinterpret_cast<const typename States<S>::type*>(pC + j * NP);
+      B[j] = load_states<S>(pB + j * NP);
+      if (FULL) C[j] = load_states<S>(pC + j * NP);
     }
   }
 };

@@ -105,8 +105,8 @@ struct Four {
       delta[j] = pd[j * CHB];
       u[j] = pu[j * CHB];
       if (DO) go[j] = po[j * CHB];
-      B[j] = *reinterpret_cast<const typename States<S>::type*>(pB + j * NP);
-      if (CC) C[j] = *reinterpret_cast<const typename States<S>::type*>(pC + j * NP);
+      B[j] = load_states<S>(pB + j * NP);
+      if (CC) C[j] = load_states<S>(pC + j * NP);
     }
   }
 };
@@ -376,34 +376,39 @@ __global__ __launch_bounds__(2 * kThreads) void reverse_kernel(BwP p) {
           q[tq / 4 + 1 & 1].template load<CHB, NP>(pd + (tq - 4) * CHB, pu + (tq - 4) * CHB, po + (tq - 4) * CHB, pB + (tq - 4) * NP,
                                                    pC + (tq - 4) * NP);
         // the four tokens' S values each, four of them to a sum over the channels
-        float sB[4], sA[4], gu[4], dh[4], rB[S], rC[S];
+        float sB[4], sA[4], gu[4 * S], dh[4 * S], rB[S], rC[S];
 #pragma unroll
         for (int j = 3; j >= 0; --j) {
           sB[j] = sA[j] = 0.f;
 #pragma unroll
           for (int k = 0; k < S; ++k) {
             const float gk = fmaf(f.C[j][k], f.go[j], gg[k]);
-            dh[(j * S + k) % 4] = f.go[j] * ah[tq + j][k];
-            gu[(j * S + k) % 4] = gk * f.u[j];
+            dh[j * S + k] = f.go[j] * ah[tq + j][k];
+            gu[j * S + k] = gk * f.u[j];
             sB[j] = fmaf(gk, f.B[j][k], sB[j]);
             const float m = gk * ah[tq + j][k];
             sA[j] = fmaf(m, A2[k], sA[j]);
             dAt[k] = fmaf(m, f.delta[j], dAt[k]);
             gg[k] = gk * a[tq + j][k];
           }
-          if (j * S % 4 == 0) {
-            rB[j * S / 4] = channels_sum(gu, odd, two);
-            rC[j * S / 4] = channels_sum(dh, odd, two);
+#pragma unroll
+          for (int q = 0; q < S; ++q) {
+            if (4 * q / S != j) continue;  // the four that this token completes
+            rB[q] = channels_sum(gu + 4 * q, odd, two);
+            rC[q] = channels_sum(dh + 4 * q, odd, two);
           }
         }
         sh.gB[o][blk][tq + rv][l.chl] = rows_sum4(sB);
         sh.gA[o][blk][tq + rv][l.chl] = rows_sum4(sA);
         // lane c of a row writes value c of its 4 S: token c / S, state c % S
-        const int c = tid & (4 * S - 1);
+        const int c = S == 3 ? ((tid & 15) < 12 ? tid & 15 : (tid & 15) - 4) : tid & (4 * S - 1);
         float* wp = &sh.wp[o][wave / NB][tq + c / S][0][l.n0 + c % S];
         if constexpr (S == 4) {
           wp[0] = pick(eight, pick(four, rB[3], rB[2]), pick(four, rB[1], rB[0]));
           wp[NP] = pick(eight, pick(four, rC[3], rC[2]), pick(four, rC[1], rC[0]));
+        } else if constexpr (S == 3) {
+          wp[0] = pick(eight, rB[2], pick(four, rB[1], rB[0]));
+          wp[NP] = pick(eight, rC[2], pick(four, rC[1], rC[0]));
         } else if constexpr (S == 2) {
           wp[0] = pick(four, rB[1], rB[0]);
           wp[NP] = pick(four, rC[1], rC[0]);
@@ -455,7 +460,7 @@ __global__ __launch_bounds__(2 * kThreads) void reverse_kernel(BwP p) {
     if (dzp != nullptr) store_cols<T, VE, WD>(dzp + at, zero, true, st.ncol);
   }
   // this thread's four of the tile's sums of dB and dC, those past the tile repeating it
-  constexpr int kSums = TB * 2 * NP, NS = kSums > 4 * kThreads ? kSums / (4 * kThreads) : 1;
+  constexpr int kSums = TB * 2 * NP, NS = (kSums + 4 * kThreads - 1) / (4 * kThreads);
   float* bcp = p.bc + ((int64_t(w.cb) * p.Bt + w.b) * p.in.L * p.in.G + w.g) * (2 * NP);
   const int64_t bcrow = int64_t(p.in.G) * (2 * NP);
   // of the tile in each half: x, delta, sigmoid(dt), do, dy silu'(z)

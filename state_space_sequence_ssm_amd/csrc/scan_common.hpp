@@ -241,20 +241,28 @@ struct Stager {
 // Blocks of channels never straddle two groups.
 constexpr int CH = 64;  // channels of a block with one state block: 16 for each of its four scanning waves
 inline int state_blocks(int N) { return N <= 16 ? 1 : N <= 32 ? 2 : 4; }  // of 16 states
-// States of a lane, S: a channel's four lanes share a state block.  8192 tokens of 2048
-// channels bf16 with N = 4, 8, 16 take 75, 95, 130 us, the backward 209, 232, 314 us;
-// padded to 16 they all took the last.
-inline int lane_states(int N) { return N <= 4 ? 1 : N <= 8 ? 2 : 4; }
+// States of a lane, S: as many as make a block's 4 S of a channel's four lanes enough.
+// 8192 tokens of 2048 channels bf16 with N = 4, 8, 12, 16, 24, 32 take 75, 93, 115, 125,
+// 144, 153 us, the backward 208, 231, 301, 315, 527, 581 us; padded to whole blocks of 16
+// states, the first three took what 16 does and the fifth what 32 does.
+inline int lane_states(int N) { return (N + 4 * state_blocks(N) - 1) / (4 * state_blocks(N)); }
 template <int S>
 struct States {
-  typedef float type __attribute__((ext_vector_type(S)));
+  typedef float type __attribute__((ext_vector_type(S), aligned(S == 3 ? 4 : 4 * S)));
 };
+template <int S>
+__device__ __forceinline__ typename States<S>::type load_states(const float* p) {
+  return *reinterpret_cast<const typename States<S>::type*>(p);
+}
 // The kernels for a state size: CALL(NB, S).
-#define M3_SCAN_STATES(N, CALL)   \
+#define M3_SCAN_STATES(N, CALL)     \
   if ((N) <= 4) return CALL(1, 1);  \
   if ((N) <= 8) return CALL(1, 2);  \
+  if ((N) <= 12) return CALL(1, 3); \
   if ((N) <= 16) return CALL(1, 4); \
+  if ((N) <= 24) return CALL(2, 3); \
   if ((N) <= 32) return CALL(2, 4); \
+  if ((N) <= 48) return CALL(4, 3); \
   return CALL(4, 4);
 inline int blocks_per_group(int Dg, int NB) { return (Dg + CH / NB - 1) / (CH / NB); }
 

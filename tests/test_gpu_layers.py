@@ -450,7 +450,8 @@ SCAN_OFF = [(D, N, G, dt, off) for D, N, G, dt, off in [
     (65, 16, 1, "bf16", (1, 2)), (66, 15, 1, "f32", (2, 1)), (67, 14, 1, "bf16", False), (71, 13, 1, "f32", False), (5, 4, 1, "bf16", (3, 0)),
     (4, 5, 1, "f32", (1, 0)), (33, 17, 1, "bf16", (1, 2)), (35, 31, 1, "f32", False), (38, 30, 2, "bf16", (1, 1)), (17, 33, 1, "f32", (1, 0)),
     (18, 62, 1, "bf16", False), (19, 63, 1, "f32", (1, 1)), (21, 61, 3, "bf16", (5, 2)), (64, 16, 1, "bf16", (1, 0)), (64, 16, 2, "f32", (1, 3)),
-    (48, 8, 1, "bf16", False), (40, 7, 1, "f32", (1, 0)), (130, 6, 2, "bf16", (1, 1)), (3, 16, 1, "bf16", (1, 0)), (64, 3, 1, "f32", (1, 0)), (1, 1, 1, "bf16", False), (2, 2, 1, "f32", (1, 0))]]
+    (72, 12, 1, "bf16", False), (65, 9, 1, "f32", (1, 0)), (40, 24, 2, "bf16", False), (33, 20, 1, "f32", (1, 1)),
+    (36, 48, 1, "f32", False), (18, 40, 2, "bf16", (2, 1)), (48, 8, 1, "bf16", False), (40, 7, 1, "f32", (1, 0)), (130, 6, 2, "bf16", (1, 1)), (3, 16, 1, "bf16", (1, 0)), (64, 3, 1, "f32", (1, 0)), (1, 1, 1, "bf16", False), (2, 2, 1, "f32", (1, 0))]]
 
 
 @pytest.mark.parametrize("D,N,G,dt,off", SCAN_OFF)
