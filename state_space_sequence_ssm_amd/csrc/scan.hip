@@ -43,8 +43,7 @@ struct Four {
 // before it.  Otherwise the states and sums of delta of the segments alone.
 //
 // A block is eight waves of two kinds, one of each per SIMD: four scan, 16
-// channels and 4 S = 16 states each, or 8 or 4 for sizes that need no more (64 / NB
-// channels of NB state blocks); four stage,
+// channels and 4 S states each (64 / NB channels of NB state blocks); four stage,
 // that is, they load the next tile, form delta and u and put them into the other
 // half of LDS, and join, gate and store the y of the tile before.  So the loads'
 // latency and the exponentials of softplus and SiLU lie beside the recurrence and

@@ -11,7 +11,7 @@
 // Two walks.  The first runs forward over the tokens and keeps the state in
 // front of every 16th one.  The second walks these 16-token tiles from the last
 // to the first: it computes a tile's decays and states again, keeps them in
-// registers (2 x 16 x 4 per lane) and runs the reverse recurrence over them, so
+// registers (2 x 16 x S per lane) and runs the reverse recurrence over them, so
 // each decay is computed twice in all and no state goes to memory per token.
 // dB and dC are summed over a wave's 16 channels in registers, over the block's
 // waves in LDS and over the blocks from a workspace, in a fixed order.
@@ -21,8 +21,8 @@
 //   sum_t (prod_{r<=t} a_r) C_t do_t,
 // and the second walk joins states from the left and gradients from the right.
 //
-// A wave holds 16 channels and one block of 16 states, lane = 16 s + channel
-// with the states 4 s .. + 3; a block of eight waves (four scan, four stage) is
+// A wave holds 16 channels and one block of 4 S states, lane = 16 s + channel
+// with the states S s .. S s + S - 1; a block of eight waves (four scan, four stage) is
 // 64 / NB channels of NB state blocks, whose sums over the states the staging
 // waves join.
 #include <type_traits>

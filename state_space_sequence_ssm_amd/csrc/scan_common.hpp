@@ -8,9 +8,9 @@
 // exponential and a multiply-add, and one more multiply-add for the readout.  So
 // the vector ALUs bound it, the exponentials (half rate) for two fifths.
 //
-// A wave holds 16 channels and a block of 16 states, lane = 16 s + channel with the
-// states 4 s .. + 3: the sums over the states of four tokens take three lane swaps
-// and three additions.  What is shared by a
+// A wave holds 16 channels and a block of 4 S states (S = 4, fewer where the state size
+// needs no more), lane = 16 s + channel with the states S s .. S s + S - 1: the sums over
+// the states of four tokens take three lane swaps and three additions.  What is shared by a
 // channel's lanes (delta, u, the gate) or by all channels (B, C) is computed or
 // converted once per tile and passed on in LDS.  (This is also the layout of a
 // 16 x 16 fp32 matrix product's result; forming u_t B_t^T on the matrix cores
@@ -240,7 +240,7 @@ struct Stager {
 
 // Blocks of channels never straddle two groups.
 constexpr int CH = 64;  // channels of a block with one state block: 16 for each of its four scanning waves
-inline int state_blocks(int N) { return N <= 16 ? 1 : N <= 32 ? 2 : 4; }  // of 16 states
+inline int state_blocks(int N) { return N <= 16 ? 1 : N <= 32 ? 2 : 4; }  // of at most 16 states
 // States of a lane, S: as many as make a block's 4 S of a channel's four lanes enough.
 // 8192 tokens of 2048 channels bf16 with N = 4, 8, 12, 16, 24, 32 take 75, 93, 115, 125,
 // 144, 153 us, the backward 208, 231, 301, 315, 527, 581 us; padded to whole blocks of 16
