@@ -475,3 +475,43 @@ def test_conv_off_alignment(ops, D, W, dt, off):
         c = (Bt, L, D, W, dt, lengths, True, True, True, off)
         test_conv(ops, c)
         test_conv_backward(ops, c)
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+def test_shared_words_repeat(ops, dt):
+    """Channels that two words share are written twice with the same value: every call
+    gives the same bits, eager and replayed from a graph."""
+    m, t = Maker(45), DT[dt]
+    Bt, L, D, N = 3, 70, 1031, 11
+    x, z, dy, dl, C, B = (m(Bt, L, n, dtype=t) for n in (D, D, D, D, N, N))
+    B, C = B.unflatten(-1, (1, N)), C.unflatten(-1, (1, N))
+    w, b, gain, A = m(D, 4, scale=0.5), m(D), m(D), -torch.exp(m(D, N))
+
+    def calls():
+        y = ops.m3_causal_conv(x, w, b)["y"]
+        s = ops.m3_selective_scan(y, dl, A, B, C, gain, z, dt_softplus=True, dt_bias=b)
+        n = ops.m3_gated_norm(s["y"], z, gain)
+        r = ops.m3_residual_norm(n, x, gain)
+        g = ops.m3_residual_norm_backward(r["residual"], w=gain, dy=dy)
+        q = ops.m3_gated_norm_backward(s["y"], z, gain, dy=g["dx"])
+        u = ops.m3_selective_scan_backward(y, dl, A, B, C, gain, z, dy=q["dx"], dt_softplus=True, dt_bias=b)
+        v = ops.m3_causal_conv_backward(x, w, b, dy=u["dx"])
+        return [y, n] + [o for d in (s, r, g, q, u, v) for o in d.values() if o is not None]
+
+    first = calls()
+    assert all(torch.equal(p, q) for _ in range(3) for p, q in zip(first, calls()))
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        calls()
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=side):
+            held = calls()
+    for _ in range(3):
+        for o in held:
+            o.fill_(NAN)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(p, q) for p, q in zip(first, held))
+        assert all(torch.equal(p, q) for p, q in zip(first, calls()))
