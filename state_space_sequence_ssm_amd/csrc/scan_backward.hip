@@ -266,8 +266,17 @@ __device__ __forceinline__ float channels_sum(const float* v, uint32_t odd, uint
   return t;
 }
 
-// LDS of the reverse walk; everything twice, a tile being staged, and the one
-// before finished, while one is walked.
+// LDS of the reverse walk.  Between two barriers, while the scanning waves walk tile i,
+// the staging waves finish tile i - 1 and stage tile i + 1, each at its own pace.  So what
+// one of them stages has to lie apart from what another may still read, and with two
+// halves, i & 1, nothing of tile i - 1 that was staged may be read any more:
+//
+//                  tile i - 1         tile i                   tile i + 1
+//   dl, us, ds     -                  read by the scan         written
+//   bc             -                  read by the scan,        written
+//                                     B taken for the finish
+//   sdu            -                  taken for the finish     written
+//   o, gB, gA, wp  read by the finish written by the scan      -
 template <int NB, int S>
 struct Shared {
   static constexpr int CHB = CH / NB, NP = 4 * S * NB;
@@ -519,6 +528,18 @@ __global__ __launch_bounds__(2 * kThreads) void reverse_kernel(BwP p) {
   };
   float ox[VE], od[VE], oz[VE];
   f32x4 obc[NS];
+  // of the tile walked, for its finish in the next step: B, and the sums of do u (0 at dB)
+  f32x4 wB[NS];
+  float wdu[NS];
+  auto take = [&](auto half) {
+    constexpr int o = decltype(half)::value;
+#pragma unroll
+    for (int q = 0; q < NS; ++q) {
+      const int e = 4 * ((tid + q * kThreads) % (kSums / 4)), t = e / (2 * NP), c = e % (2 * NP);
+      wB[q] = *reinterpret_cast<const f32x4*>(&sh.bc[o][0][t][c % NP]);
+      wdu[q] = c < NP ? 0.f : sh.sdu[o][t];
+    }
+  };
   auto finish = [&](auto half) {
     constexpr int o = decltype(half)::value;
     float y[VE], gB[VE], gA[VE];
@@ -545,14 +566,12 @@ __global__ __launch_bounds__(2 * kThreads) void reverse_kernel(BwP p) {
     }
 #pragma unroll
     for (int q = 0; q < NS; ++q) {
-      const int e = 4 * ((tid + q * kThreads) % (kSums / 4)), t = e / (2 * NP), c = e % (2 * NP);
+      const int e = 4 * ((tid + q * kThreads) % (kSums / 4)), c = e % (2 * NP);
       f32x4 v = *reinterpret_cast<const f32x4*>(&sh.wp[o][0][0][0][0] + e);
 #pragma unroll
       for (int i = 1; i < 4 / NB; ++i) v += *reinterpret_cast<const f32x4*>(&sh.wp[o][i][0][0][0] + e);
-      const float m = c < NP ? 0.f : sh.sdu[o][t];
-      const f32x4 Bv = *reinterpret_cast<const f32x4*>(&sh.bc[o][0][t][c % NP]);
 #pragma unroll
-      for (int k = 0; k < 4; ++k) v[k] = c < NP ? v[k] : fmaf(m, Bv[k], v[k]);
+      for (int k = 0; k < 4; ++k) v[k] = c < NP ? v[k] : fmaf(wdu[q], wB[q][k], v[k]);
       obc[q] = v;
     }
   };
@@ -574,6 +593,7 @@ __global__ __launch_bounds__(2 * kThreads) void reverse_kernel(BwP p) {
   auto start = [&](int i) { return w.tbeg + (tiles - 1 - i) * TB; };  // first token of the tile of step i
   auto step = [&](int i, auto half, auto other) {
     if (i > 0) finish(other);
+    take(half);
     if (i + 1 < tiles) {
       stage(start(i + 1), other);
       st.fetch(start(i + 2));
