@@ -540,8 +540,9 @@ __global__ __launch_bounds__(2 * kThreads) void reverse_kernel(BwP p) {
       wdu[q] = c < NP ? 0.f : sh.sdu[o][t];
     }
   };
-  auto finish = [&](auto half) {
+  auto finish = [&](auto half, int t0) {
     constexpr int o = decltype(half)::value;
+    const bool row = t0 + r < w.tend;
     float y[VE], gB[VE], gA[VE];
 #pragma unroll
     for (int v = 0; v < VE; ++v) y[v] = gB[v] = gA[v] = 0.f;
@@ -562,7 +563,9 @@ __global__ __launch_bounds__(2 * kThreads) void reverse_kernel(BwP p) {
       od[v] = fmaf(kx[o][v], gB[v], gA[v] * kLn2) * ks[o][v];
       oz[v] = kz[o][v] * fmaf(dsk[v], kx[o][v], y[v]);
       dD[v] = fmaf(kg[o][v], kx[o][v], dD[v]);
-      dbias[v] += od[v];
+      // past the end A's terms are no token's: the state times the gradient behind it times
+      // A itself, which overflows for the A of a state that forgets at once
+      dbias[v] += row ? od[v] : 0.f;
     }
 #pragma unroll
     for (int q = 0; q < NS; ++q) {
@@ -592,7 +595,7 @@ __global__ __launch_bounds__(2 * kThreads) void reverse_kernel(BwP p) {
   const std::integral_constant<int, 1> odd;
   auto start = [&](int i) { return w.tbeg + (tiles - 1 - i) * TB; };  // first token of the tile of step i
   auto step = [&](int i, auto half, auto other) {
-    if (i > 0) finish(other);
+    if (i > 0) finish(other, start(i - 1));
     take(half);
     if (i + 1 < tiles) {
       stage(start(i + 1), other);
@@ -612,8 +615,8 @@ __global__ __launch_bounds__(2 * kThreads) void reverse_kernel(BwP p) {
     if (i + 1 < tiles) step(i + 1, odd, even);
   }
   if (tiles > 0) {
-    if (tiles % 2) finish(even);
-    else finish(odd);
+    if (tiles % 2) finish(even, start(tiles - 1));
+    else finish(odd, start(tiles - 1));
     store(start(tiles - 1));
   }
   // ---- sums over the tokens: this thread's rows, then the 16 of each column

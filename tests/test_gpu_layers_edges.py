@@ -3,8 +3,9 @@ import pytest
 
 torch = pytest.importorskip("torch")
 
+from tests import layer_ref as ref  # noqa: E402
 from tests import test_gpu_layers as base  # noqa: E402
-from tests.test_gpu_layers import BF  # noqa: E402
+from tests.test_gpu_layers import BF, close, ilen  # noqa: E402
 
 pytestmark = pytest.mark.gpu
 
@@ -45,3 +46,26 @@ def test_scan_backward_same_bits_beside_other_work(ops, N):
         torch.cuda.synchronize()
         for k, v in first.items():
             assert torch.equal(v, again[k]), k
+
+
+# ---------------------------------------------------------------- rows that count for nothing
+@pytest.mark.parametrize("L", [1, 45, 300])
+def test_scan_backward_rates_that_forget_at_once(ops, L):
+    """A = -inf in every other state, with a gradient of the last state: the tokens that
+    fill an item's last tile have no step, and add nothing to the bias's gradient."""
+    q, m = base._scan_inputs((2, L, 70, 16, 1, "f32", [L, (L + 1) // 2], True, True, True, True, True, False), 92)
+    lengths = [L, (L + 1) // 2]
+    dy, dhf = base.spoil(m(2, L, 70), lengths), m(2, 70, 16, scale=3.0)
+    forget = torch.zeros(70, 16, dtype=torch.bool, device="cuda")
+    forget[:, ::2] = True
+    steepest = float((torch.nn.functional.softplus(torch.nan_to_num(q["dt"]) + q["dt_bias"])[..., None] * q["A"]).abs().max())
+    args, kw = base._scan_call(dict(q, A=torch.where(forget, -float("inf"), q["A"])), True)
+    got = ops.m3_selective_scan_backward(*args, dy=dy, dh_final=dhf, lengths=ilen(lengths), want_carry_grads=True, **kw)
+    # 64 bits: -1e30 times any step here is an exponent whose power is zero too
+    q["A"] = torch.where(forget, -1e30, q["A"])
+    want, mag = (ref.scan(**q, lengths=lengths, dt_softplus=True, dy=dy, dh_final=dhf, mag=v) for v in (False, True))
+    # a decay of exactly zero has no error, so the steepest of the others counts
+    k = 2 * base.k_scan(L, 16, steepest, base._zmax(q["z"]))
+    for name, extra in (("dz", 0), ("dx", 16), ("ddt", 48), ("dB", 70), ("dC", 70), ("dh0", 0), ("dA", 2 * L), ("dD", 2 * L),
+                        ("ddt_bias", 2 * L + 32)):
+        close(name, got[name], want[name], mag[name], k + extra)
