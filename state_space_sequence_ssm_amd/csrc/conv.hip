@@ -208,14 +208,22 @@ __global__ __launch_bounds__(256) void conv_backward_kernel(ConvBwP p) {
   for (int k = 0; k <= W; ++k)
 #pragma unroll
     for (int v = 0; v < V; ++v) dw[k][v] = 0.f;
-  if (cv < p.nv && t0 < p.L) {
+  const int tend = t0 + p.tt < p.L ? t0 + p.tt : p.L;  // dx rows [t0, tend)
+  T* dx = static_cast<T*>(p.dx) + int64_t(b) * p.L * p.D + d0;
+  T* dst = static_cast<T*>(p.dstate);
+  if (dst != nullptr) dst += int64_t(b) * (W - 1) * p.D + d0;
+  if (cv < p.nv && t0 < p.L && t0 >= len) {  // behind the item's tokens
+    float zero[V];
+#pragma unroll
+    for (int v = 0; v < V; ++v) zero[v] = 0.f;
+    for (int t = t0; t < tend; ++t) store_word<T, V, RAG>(dx + int64_t(t) * p.D, zero);
+    for (int j = 0; j < W - 1; ++j)
+      if (t0 == 0 && dst != nullptr) store_word<T, V, RAG>(dst + int64_t(j) * p.D, zero);
+  } else if (cv < p.nv && t0 < p.L) {
     const T* x = static_cast<const T*>(p.x) + int64_t(b) * p.L * p.ld + d0;
     const T* dy = static_cast<const T*>(p.dy) + int64_t(b) * p.L * p.D + d0;
-    T* dx = static_cast<T*>(p.dx) + int64_t(b) * p.L * p.D + d0;
     const T* state = static_cast<const T*>(p.state);
     if (state != nullptr) state += int64_t(b) * (W - 1) * p.D + d0;
-    T* dst = static_cast<T*>(p.dstate);
-    if (dst != nullptr) dst += int64_t(b) * (W - 1) * p.D + d0;
     float w[W][V], bias[V];
 #pragma unroll
     for (int i = 0; i < V; ++i) {
@@ -223,8 +231,8 @@ __global__ __launch_bounds__(256) void conv_backward_kernel(ConvBwP p) {
 #pragma unroll
       for (int k = 0; k < W; ++k) w[k][i] = p.w[int64_t(d0 + i) * W + k];
     }
-    const int tend = t0 + p.tt < p.L ? t0 + p.tt : p.L;  // dx rows [t0, tend)
-    const int have = len > 0 ? len - 1 : 0;               // the last row with values (row 0 stands in for none)
+    const int tsum = tend < len ? tend : len;  // rows [t0, tsum) have a part in dw and dbias
+    const int have = len - 1;                  // the last row with values
     // xs[j] = x[t - (W-1) + j], dp[j] = dpre[t - (W-1) + j]
     float xs[W - 1 + kRows][V], dp[W - 1 + kRows][V];
 #pragma unroll
@@ -247,21 +255,14 @@ __global__ __launch_bounds__(256) void conv_backward_kernel(ConvBwP p) {
         qd[i] = load_word<T, V, RAG>(dy + at * p.D);
       }
     };
-    // rows t .. t + 3; inner: all of them and the dx they complete lie in the tile
+    // rows t .. t + 3; inner: all of them hold values, and they and the dx they complete
+    // lie in the tile.  A row behind the length has no part in anything: its zeros are put
+    // in place after the activation, whose argument may hold inputs that are not finite.
     auto rows = [&](int t, bool inner) {
 #pragma unroll
       for (int i = 0; i < kRows; ++i) {
         unpack<T, V>(qx[i], xs[W - 1 + i]);
         unpack<T, V>(qd[i], dp[W - 1 + i]);
-      }
-      if (t + kRows > len) {
-#pragma unroll
-        for (int i = 0; i < kRows; ++i)
-#pragma unroll
-          for (int v = 0; v < V; ++v) {
-            xs[W - 1 + i][v] = t + i < len ? xs[W - 1 + i][v] : 0.f;
-            dp[W - 1 + i][v] = t + i < len ? dp[W - 1 + i][v] : 0.f;
-          }
       }
       fetch(t + kRows);
 #pragma unroll
@@ -275,7 +276,11 @@ __global__ __launch_bounds__(256) void conv_backward_kernel(ConvBwP p) {
             dp[W - 1 + i][v] *= dsilu_f(a, sigmoid_f(a));
           }
         }
-        if (inner || t + i < tend) {
+        if (!inner) {
+#pragma unroll
+          for (int v = 0; v < V; ++v) dp[W - 1 + i][v] = t + i < len ? dp[W - 1 + i][v] : 0.f;
+        }
+        if (inner || t + i < tsum) {
 #pragma unroll
           for (int v = 0; v < V; ++v) {
 #pragma unroll
@@ -310,7 +315,7 @@ __global__ __launch_bounds__(256) void conv_backward_kernel(ConvBwP p) {
     fetch(t0);
     rows(t0, false);
     int t = t0 + kRows;
-    for (; t + kRows <= tend; t += kRows) rows(t, true);
+    for (; t + kRows <= tsum; t += kRows) rows(t, true);
     for (; t < tend + W - 1; t += kRows) rows(t, false);
   }
 #pragma unroll

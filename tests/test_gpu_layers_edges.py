@@ -5,7 +5,7 @@ torch = pytest.importorskip("torch")
 
 from tests import layer_ref as ref  # noqa: E402
 from tests import test_gpu_layers as base  # noqa: E402
-from tests.test_gpu_layers import BF, close, ilen  # noqa: E402
+from tests.test_gpu_layers import DT, BF, NAN, Maker, close, ilen  # noqa: E402
 
 pytestmark = pytest.mark.gpu
 
@@ -69,3 +69,45 @@ def test_scan_backward_rates_that_forget_at_once(ops, L):
     for name, extra in (("dz", 0), ("dx", 16), ("ddt", 48), ("dB", 70), ("dC", 70), ("dh0", 0), ("dA", 2 * L), ("dD", 2 * L),
                         ("ddt_bias", 2 * L + 32)):
         close(name, got[name], want[name], mag[name], k + extra)
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("D,W", [(24, 4), (37, 3), (3, 2)])
+def test_conv_backward_rows_behind_an_infinite_one(ops, D, W, dt):
+    """An item's last input is infinite: the gradients behind its length are zeros, and
+    without an activation only the newest tap's gradient sees it."""
+    for L, n in ((9, 1), (9, 4), (70, 3), (70, 64), (300, 8), (300, 129), (300, 297)):
+        m, t = Maker(93), DT[dt]
+        x, dy, w, bias = m(2, L, D, dtype=t), m(2, L, D, dtype=t), m(D, W, scale=0.5), m(D)
+        x[1, n - 1, D - 1] = float("inf")
+        lengths = [L, n]
+        base.spoil(dy, lengths)
+        for act in (True, False):
+            got = ops.m3_causal_conv_backward(x, w, bias, dy=dy, lengths=ilen(lengths), silu=act, want_state_grad=True)
+            assert (got["dx"][1, n:] == 0).all(), (L, n, act)
+            z = x.clone()
+            z[1, n - 1, D - 1] = 0
+            clean = ops.m3_causal_conv_backward(z, w, bias, dy=dy, lengths=ilen(lengths), silu=act, want_state_grad=True)
+            for k in ("dx", "dw", "dbias", "dstate"):
+                other = (..., slice(0, D - 1)) if k in ("dx", "dstate") else slice(0, D - 1)
+                assert torch.equal(got[k][other], clean[k][other]), (k, L, n, act)
+            if not act:
+                assert torch.equal(got["dw"][-1, :-1], clean["dw"][-1, :-1]) and not got["dw"][-1, -1].isfinite(), (L, n)
+                assert torch.equal(got["dx"], clean["dx"]) and torch.equal(got["dbias"], clean["dbias"])
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("act", [True, False])
+def test_conv_backward_carry_of_an_empty_item(ops, act, dt):
+    """An item without tokens: whatever its carry holds, it has no part in any gradient."""
+    for L in (1, 6, 200):
+        m, t = Maker(94), DT[dt]
+        x, dy, w, bias, state = m(3, L, 40, dtype=t), m(3, L, 40, dtype=t), m(40, 4, scale=0.5), m(40), m(3, 3, 40, dtype=t)
+        lengths = ilen([L, 0, L])
+        want = ops.m3_causal_conv_backward(x, w, bias, state, dy=dy, lengths=lengths, silu=act, want_state_grad=True)
+        assert (want["dstate"][1] == 0).all() and (want["dx"][1] == 0).all()
+        for bad in (NAN, float("inf")):
+            state[1] = bad
+            got = ops.m3_causal_conv_backward(x, w, bias, state, dy=dy, lengths=lengths, silu=act, want_state_grad=True)
+            for k, v in want.items():
+                assert torch.equal(v, got[k]), (k, L, bad)
