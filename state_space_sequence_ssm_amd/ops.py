@@ -7,6 +7,7 @@ from __future__ import annotations
 
 import ctypes
 import functools
+import inspect
 
 import torch
 
@@ -285,21 +286,24 @@ def m3_rope_angles_cumsum(theta, phi0=None, *, phi=None, stream=None):
 def _scoped(fn):
     """Run a call on its first tensor's device and on `stream`: outputs and
     workspaces are then allocated for that stream as well."""
+    name = next(iter(inspect.signature(fn).parameters))
+
     @functools.wraps(fn)
-    def call(first, *args, stream=None, **kw):
+    def call(*args, stream=None, **kw):
+        first = args[0] if args else kw.get(name)
         if not isinstance(first, torch.Tensor):
-            raise TypeError("the first argument must be a torch.Tensor")
+            raise TypeError(f"{name} must be a torch.Tensor")
         index = first.get_device()
         if index < 0:
-            raise ValueError("the first argument must be a device tensor")
+            raise ValueError(f"{name} must be a device tensor")
         if stream is None and index == torch.cuda.current_device():
-            return fn(first, *args, **kw)
+            return fn(*args, **kw)
         if stream is None:
             stream = torch.cuda.current_stream(first.device)
         elif stream.device != first.device:
             raise ValueError(f"stream is on {stream.device}, the tensors are on {first.device}")
         with torch.cuda.stream(stream):
-            return fn(first, *args, **kw)
+            return fn(*args, **kw)
     return call
 
 

@@ -111,3 +111,27 @@ def test_conv_backward_carry_of_an_empty_item(ops, act, dt):
             got = ops.m3_causal_conv_backward(x, w, bias, state, dy=dy, lengths=lengths, silu=act, want_state_grad=True)
             for k, v in want.items():
                 assert torch.equal(v, got[k]), (k, L, bad)
+
+
+# ---------------------------------------------------------------- arguments by their names
+def test_arguments_by_name(ops):
+    m = Maker(95)
+    Bt, L, D, N = 2, 20, 24, 8
+    x, dt, z, dy, h = (m(Bt, L, D, dtype=BF) for _ in range(5))
+    B, C = (m(Bt, L, 1, N, dtype=BF) for _ in range(2))
+    w, b, st, A, h0 = m(D, 4), m(D), m(Bt, 3, D, dtype=BF), -torch.exp(m(D, N)), m(Bt, D, N)
+    tok = dict(x=x[:, 0], dt=dt[:, 0], A=A, B=B[:, 0], C=C[:, 0], D=b, z=z[:, 0])
+    for fn, args in ((ops.m3_causal_conv, dict(x=x, w=w, bias=b, state=st)), (ops.m3_causal_conv_step, dict(state=st.clone(), x=x[:, 0], w=w)),
+                     (ops.m3_causal_conv_backward, dict(x=x, w=w, bias=b, state=st, dy=dy)),
+                     (ops.m3_selective_scan, dict(x=x, dt=dt, A=A, B=B, C=C, D=b, z=z, h0=h0)),
+                     (ops.m3_selective_scan_step, dict(h=h0, **tok, h_out=torch.empty_like(h0))),
+                     (ops.m3_selective_scan_backward, dict(x=x, dt=dt, A=A, B=B, C=C, D=b, z=z, h0=h0, dy=dy)),
+                     (ops.m3_gated_norm, dict(x=x, z=z, w=b)), (ops.m3_gated_norm_backward, dict(x=x, z=z, w=b, dy=dy)),
+                     (ops.m3_residual_norm, dict(x=x, residual=z, w=b, scale=b)),
+                     (ops.m3_residual_norm_backward, dict(h=h, x=x, w=b, scale=b, dy=dy))):
+        first = next(iter(args))
+        rest = {k: v.clone() if k == "state" else v for k, v in args.items() if k != first}
+        a, c = fn(args[first].clone(), **rest), fn(**args)
+        for p, q in zip(a.values(), c.values()) if isinstance(a, dict) else ((a, c),):
+            # steps of either sign overflow here: bits, since no NaN equals itself
+            assert p is None and q is None or torch.equal(p.view(torch.uint8), q.view(torch.uint8)), fn.__name__

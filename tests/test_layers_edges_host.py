@@ -4,6 +4,10 @@ import re
 
 import pytest
 
+torch = pytest.importorskip("torch")
+
+from state_space_sequence_ssm_amd import _lib  # noqa: E402
+
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 CSRC = os.path.join(ROOT, "state_space_sequence_ssm_amd", "csrc")
 
@@ -33,3 +37,25 @@ def test_what_a_step_finishes_is_not_what_it_stages(source, kernel):
     used = {k: set(re.findall(rf"&?(?:\bsh\.)?\b({names})\[", _body(text, k))) for k in ("finish", "stage")}
     assert used["stage"] >= {"dl", "us", "bc"} and used["finish"]
     assert not used["finish"] & used["stage"]
+
+
+# ---------------------------------------------------------------- the binding's arguments
+# each operator's tensors by their names, the first of them the one whose device it takes
+NAMES = {"m3_causal_conv": ("x", "w"), "m3_causal_conv_step": ("state", "x", "w"), "m3_causal_conv_backward": ("x", "w", "dy"),
+         "m3_selective_scan": ("x", "dt", "A", "B", "C"), "m3_selective_scan_step": ("h", "x", "dt", "A", "B", "C"),
+         "m3_selective_scan_backward": ("x", "dt", "A", "B", "C", "dy"), "m3_gated_norm": ("x",),
+         "m3_gated_norm_backward": ("x", "dy"), "m3_residual_norm": ("x",), "m3_residual_norm_backward": ("h", "dy")}
+
+
+def test_every_operator_is_named():
+    assert set(NAMES) == set(_lib.LAYER_CALLS)
+
+
+@pytest.mark.parametrize("name", list(NAMES))
+def test_first_argument_by_name(name):
+    from state_space_sequence_ssm_amd import ops
+    fn, t = getattr(ops, name), torch.zeros(1, 4, 8)
+    with pytest.raises(ValueError, match=f"^{NAMES[name][0]} must be a device tensor"):  # found, and on the host
+        fn(**{k: t for k in NAMES[name]})
+    with pytest.raises(TypeError, match=f"^{NAMES[name][0]} must be a torch.Tensor"):
+        fn(**{k: t for k in NAMES[name][1:]})
