@@ -646,10 +646,11 @@ def m3_residual_norm(x, residual=None, w=None, scale=None, *, eps=1e-6, y=None, 
     h in the residual's type (residual_out may be `residual` itself)."""
     dev, t, shape = x.get_device(), x.dtype, x.shape
     width = shape[-1]
-    rt = residual.dtype if residual is not None else residual_out.dtype if residual_out is not None else t
+    like = residual if residual is not None else residual_out if residual_out is not None else x
+    rt = like.dtype
     a = _lib.ResidualNormArgs()
     a.M, a.D, a.in_dtype = x.numel() // width if width else 0, width, _dtype_code(x)
-    a.res_dtype, a.eps = _lib.M3_F32 if rt == _F32 else _lib.M3_BF16, eps
+    a.res_dtype, a.eps = _dtype_code(like), eps
     a.x, a.x_ld = _rows(x, t, shape, len(shape) - 1, "x", dev)
     a.residual = _dense(residual, rt, shape, "residual", dev)
     a.scale = _dense(scale, _F32, (width,), "scale", dev)
