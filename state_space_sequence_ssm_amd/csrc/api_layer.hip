@@ -9,6 +9,7 @@ namespace {
 
 constexpr double kMaxElems = 34359738368.0;  // 2^35 elements of one tensor: thread and block counts stay in 32 bits
 constexpr double kMaxInt = 2147483647.0;
+constexpr int kMaxWidth = 1 << 28;   // L and D: an index a block's width past them stays in 32 bits
 constexpr int kMaxGroups = 1 << 20;  // of a norm's row
 
 bool ok_dtype(int t) { return t == M3_F32 || t == M3_BF16; }
@@ -49,7 +50,7 @@ hipStream_t str(void* s) { return static_cast<hipStream_t>(s); }
 
 int check_rows(int64_t Bt, int64_t L, int64_t D) {
   if (Bt < 1 || L < 1 || D < 1) return M3_ERR_INVALID_ARG;
-  if (double(Bt) * D > kMaxInt || double(Bt) * L * D > kMaxElems || L > (1 << 28) || D > (1 << 28)) return M3_ERR_UNSUPPORTED;
+  if (double(Bt) * D > kMaxInt || double(Bt) * L * D > kMaxElems || L > kMaxWidth || D > kMaxWidth) return M3_ERR_UNSUPPORTED;
   return M3_OK;
 }
 
@@ -88,20 +89,20 @@ bool ok_scan_size(const m3_scan_args* a) {
 
 int check_gated(m3_gated_norm_args& f) {
   if (f.M < 1 || f.D < 1 || f.G < 1 || f.D % f.G != 0 || !flag(f.gate_first) || !ok_eps(f.eps)) return M3_ERR_INVALID_ARG;
-  if (!ok_dtype(f.in_dtype) || f.G > kMaxGroups || double(f.M) * f.G > kMaxInt || double(f.M) * f.D > kMaxElems)
+  if (!ok_dtype(f.in_dtype) || f.G > kMaxGroups || f.D > kMaxWidth || double(f.M) * f.G > kMaxInt || double(f.M) * f.D > kMaxElems)
     return M3_ERR_UNSUPPORTED;
   if (f.x == nullptr || !set_ld(f.x_ld, f.D) || !set_ld(f.z_ld, f.D)) return M3_ERR_INVALID_ARG;
   return all_at({f.x, f.z}, elem(f.in_dtype)) && at(f.w, 4) ? M3_OK : M3_ERR_INVALID_ARG;
 }
 bool ok_gated_size(const m3_gated_norm_args& f) {
-  return f.M >= 1 && f.D >= 1 && f.G >= 1 && f.D % f.G == 0 && f.G <= kMaxGroups && ok_dtype(f.in_dtype) &&
+  return f.M >= 1 && f.D >= 1 && f.G >= 1 && f.D % f.G == 0 && f.G <= kMaxGroups && f.D <= kMaxWidth && ok_dtype(f.in_dtype) &&
          double(f.M) * f.G <= kMaxInt && double(f.M) * f.D <= kMaxElems;
 }
 
 int check_residual_shape(int64_t M, int64_t D, int in_dtype, int res_dtype, float eps) {
   if (M < 1 || D < 1 || !ok_eps(eps)) return M3_ERR_INVALID_ARG;
   if (!ok_dtype(in_dtype) || (res_dtype != in_dtype && res_dtype != M3_F32)) return M3_ERR_UNSUPPORTED;
-  if (double(M) > kMaxInt || double(M) * D > kMaxElems) return M3_ERR_UNSUPPORTED;
+  if (D > kMaxWidth || double(M) > kMaxInt || double(M) * D > kMaxElems) return M3_ERR_UNSUPPORTED;
   return M3_OK;
 }
 

@@ -1,4 +1,5 @@
 """Layer operators at the edges of what they take, without a GPU."""
+import ctypes
 import os
 import re
 
@@ -76,3 +77,45 @@ def test_residual_of_another_type(monkeypatch, bad):
     for t in (torch.bfloat16, torch.float32):
         call(x, x.to(t), residual_out=x.to(t))
     assert [a[1].res_dtype for a in ran] == [_lib.M3_BF16, _lib.M3_F32]
+
+
+# ---------------------------------------------------------------- sizes
+BASE = 0x10000000
+UNS = _lib.M3_ERR_UNSUPPORTED
+built = pytest.mark.skipif(not os.path.exists(_lib.LIB_PATH), reason="libm3ssm.so not built (run __graft_entry__.build())")
+POINTERS = {_lib.ConvBackwardArgs: "x w bias dy dx dw dbias workspace", _lib.ScanArgs: "x dt A B C y workspace",
+            _lib.ScanStepArgs: "x dt A B C h h_out y", _lib.ScanBackwardArgs: "fwd.x fwd.dt fwd.A fwd.B fwd.C dy dx ddt dA dB dC workspace",
+            _lib.GatedNormArgs: "x w y", _lib.GatedNormBackwardArgs: "fwd.x fwd.w dy dx dw workspace",
+            _lib.ResidualNormArgs: "x w y", _lib.ResidualNormBackwardArgs: "h x w scale dy dx dw dscale workspace"}
+
+
+def _put(a, path, value):
+    *front, last = path.split(".")
+    for f in front:
+        a = getattr(a, f)
+    setattr(a, last, value)
+
+
+def _refused(name, **sizes):
+    """The codes of a call of these sizes on addresses that nothing may touch, and the
+    workspace that it asks for."""
+    lib, args = _lib.load(), _lib.LAYER_CALLS[name]()
+    for i, f in enumerate(POINTERS[type(args)].split()):
+        _put(args, f, BASE + 0x100000 * i)
+    if hasattr(args, "workspace_bytes"):
+        args.workspace_bytes = (1 << 64) - 1
+    inner = args.fwd if hasattr(args, "fwd") else args
+    inner.in_dtype = _lib.M3_BF16
+    for k, v in sizes.items():
+        setattr(inner, k, v)
+    size = getattr(lib, name + "_workspace_size", None)
+    return getattr(lib, name)(ctypes.byref(args), None), None if size is None else size(ctypes.byref(args))
+
+
+@built
+@pytest.mark.parametrize("D", [(1 << 28) + 4, (1 << 31) - 1])
+def test_rows_past_the_widest_are_refused(D):
+    assert _refused("m3_gated_norm", M=1, D=D, G=1, eps=1e-6) == (UNS, None)
+    assert _refused("m3_gated_norm_backward", M=1, D=D, G=1, eps=1e-6) == (UNS, 0)
+    assert _refused("m3_residual_norm", M=1, D=D, res_dtype=_lib.M3_F32, eps=1e-6) == (UNS, None)
+    assert _refused("m3_residual_norm_backward", M=1, D=D, res_dtype=_lib.M3_F32, eps=1e-6) == (UNS, 0)
