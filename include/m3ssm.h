@@ -387,7 +387,17 @@ int m3_rope_angles_cumsum(const float* theta, const float* phi0, float* phi,
  *     held (lengths[b] = 0: the state passes through).
  *   - Outputs do not alias inputs or each other, except where noted.
  *   - Sizes: Bt D and M below 2^31, 2^35 elements of one tensor, L and D up to
- *     2^28; larger ones are M3_ERR_UNSUPPORTED.
+ *     2^28.  A launch has fewer than 2^32 work items, which bounds calls of
+ *     millions of short sequences and of very wide rows further:
+ *       scan and its backward  512 for each item, group and 64 channels of it (32
+ *                              with N > 16, 16 with N > 32)
+ *       its backward           2 N for each token and group; up to 64 D (N + 2)
+ *       its token              N / 16 for each item and channel, N rounded up to a
+ *                              power of two from 4
+ *       convolution's backward 256 for each item, 256 channels and 512 tokens; up
+ *                              to 64 (W + 1) D
+ *       norms' backwards       up to 64 D for each parameter
+ *     Larger calls are M3_ERR_UNSUPPORTED, before anything is launched.
  */
 
 /* Short causal depthwise convolution over the token axis:

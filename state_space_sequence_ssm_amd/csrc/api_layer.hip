@@ -7,7 +7,7 @@
 
 namespace {
 
-constexpr double kMaxElems = 34359738368.0;  // 2^35 elements of one tensor: thread and block counts stay in 32 bits
+constexpr double kMaxElems = 34359738368.0;  // 2^35 elements of one tensor
 constexpr double kMaxInt = 2147483647.0;
 constexpr int kMaxWidth = 1 << 28;   // L and D: an index a block's width past them stays in 32 bits
 constexpr int kMaxGroups = 1 << 20;  // of a norm's row
@@ -143,21 +143,26 @@ int m3_causal_conv_backward(const m3_conv_backward_args* args, void* stream) {
   m3_conv_backward_args a = *args;
   const int rc = check_conv_shape(a.Bt, a.L, a.D, a.W, a.in_dtype, a.silu);
   if (rc != M3_OK) return rc;
+  const size_t need = m3::conv_backward_workspace(a);
+  if (need == 0) return M3_ERR_UNSUPPORTED;
   if (!all_set({a.x, a.w, a.dy, a.dx, a.dw, a.workspace}) || !set_ld(a.x_ld, a.D)) return M3_ERR_INVALID_ARG;
   if (!all_at({a.x, a.state, a.dy, a.dx, a.dstate}, elem(a.in_dtype)) || !all_at({a.w, a.bias, a.lengths, a.dw, a.dbias}, 4))
     return M3_ERR_INVALID_ARG;
   if (clash({a.dx, a.dw, a.dbias, a.dstate, a.workspace}, {a.x, a.w, a.bias, a.lengths, a.state, a.dy})) return M3_ERR_INVALID_ARG;
-  if (!at(a.workspace, 256) || a.workspace_bytes < m3::conv_backward_workspace(a)) return M3_ERR_INVALID_ARG;
+  if (!at(a.workspace, 256) || a.workspace_bytes < need) return M3_ERR_INVALID_ARG;
   return hip_status(m3::launch_conv_backward(a, str(stream)));
 }
 
-size_t m3_selective_scan_workspace_size(const m3_scan_args* a) { return ok_scan_size(a) ? m3::scan_workspace(*a) : 0; }
+size_t m3_selective_scan_workspace_size(const m3_scan_args* a) {
+  return ok_scan_size(a) && m3::scan_fits(*a) ? m3::scan_workspace(*a) : 0;
+}
 
 int m3_selective_scan(const m3_scan_args* args, void* stream) {
   if (args == nullptr) return M3_ERR_INVALID_ARG;
   m3_scan_args a = *args;
   const int rc = check_scan_inputs(a);
   if (rc != M3_OK) return rc;
+  if (!m3::scan_fits(a)) return M3_ERR_UNSUPPORTED;
   if (a.y == nullptr || !at(a.y, elem(a.in_dtype)) || !at(a.h_final, 4)) return M3_ERR_INVALID_ARG;
   if (clash({a.y, a.h_final, a.workspace}, {a.x, a.dt, a.z, a.B, a.C, a.A, a.D_skip, a.dt_bias, a.h0, a.lengths}))
     return M3_ERR_INVALID_ARG;
@@ -170,6 +175,7 @@ int m3_selective_scan_step(const m3_scan_step_args* args, void* stream) {
   m3_scan_step_args a = *args;
   const int rc = check_scan_shape(a.Bt, 1, a.D, a.N, a.G, a.in_dtype, a.dt_softplus);
   if (rc != M3_OK) return rc;
+  if (!m3::scan_step_fits(a)) return M3_ERR_UNSUPPORTED;
   if (!all_set({a.x, a.dt, a.A, a.B, a.C, a.h, a.y}) || (a.dt_bias != nullptr && !a.dt_softplus)) return M3_ERR_INVALID_ARG;
   const int64_t GN = int64_t(a.G) * a.N;
   if (!scan_ld(a.x_ld, a.D) || !scan_ld(a.dt_ld, a.D) || !scan_ld(a.z_ld, a.D) || !scan_ld(a.B_ld, GN) || !scan_ld(a.C_ld, GN))
@@ -190,6 +196,8 @@ int m3_selective_scan_backward(const m3_scan_backward_args* args, void* stream) 
   m3_scan_backward_args a = *args;
   const int rc = check_scan_inputs(a.fwd);
   if (rc != M3_OK) return rc;
+  const size_t need = m3::scan_backward_workspace(a);
+  if (need == 0) return M3_ERR_UNSUPPORTED;
   const m3_scan_args& f = a.fwd;
   if (!all_set({a.dy, a.dx, a.ddt, a.dA, a.dB, a.dC, a.workspace})) return M3_ERR_INVALID_ARG;
   if ((f.D_skip == nullptr) != (a.dD == nullptr) || (f.z == nullptr) != (a.dz == nullptr) ||
@@ -200,7 +208,7 @@ int m3_selective_scan_backward(const m3_scan_backward_args* args, void* stream) 
   if (clash({a.dx, a.ddt, a.dA, a.dB, a.dC, a.dD, a.dz, a.ddt_bias, a.dh0, a.workspace},
             {f.x, f.dt, f.z, f.B, f.C, f.A, f.D_skip, f.dt_bias, f.h0, f.lengths, a.dy, a.dh_final}))
     return M3_ERR_INVALID_ARG;
-  if (!at(a.workspace, 256) || a.workspace_bytes < m3::scan_backward_workspace(a)) return M3_ERR_INVALID_ARG;
+  if (!at(a.workspace, 256) || a.workspace_bytes < need) return M3_ERR_INVALID_ARG;
   return hip_status(m3::launch_scan_backward(a, str(stream)));
 }
 
@@ -216,7 +224,7 @@ int m3_gated_norm(const m3_gated_norm_args* args, void* stream) {
 }
 
 size_t m3_gated_norm_backward_workspace_size(const m3_gated_norm_backward_args* a) {
-  return a != nullptr && ok_gated_size(a->fwd) ? m3::gated_norm_backward_workspace(*a) : 0;
+  return a != nullptr && ok_gated_size(a->fwd) && m3::gated_norm_backward_fits(*a) ? m3::gated_norm_backward_workspace(*a) : 0;
 }
 
 int m3_gated_norm_backward(const m3_gated_norm_backward_args* args, void* stream) {
@@ -224,6 +232,7 @@ int m3_gated_norm_backward(const m3_gated_norm_backward_args* args, void* stream
   m3_gated_norm_backward_args a = *args;
   const int rc = check_gated(a.fwd);
   if (rc != M3_OK) return rc;
+  if (!m3::gated_norm_backward_fits(a)) return M3_ERR_UNSUPPORTED;
   const m3_gated_norm_args& f = a.fwd;
   if (!all_set({a.dy, a.dx}) || (f.z == nullptr) != (a.dz == nullptr) || (f.w == nullptr) != (a.dw == nullptr))
     return M3_ERR_INVALID_ARG;
@@ -248,7 +257,7 @@ int m3_residual_norm(const m3_residual_norm_args* args, void* stream) {
 
 size_t m3_residual_norm_backward_workspace_size(const m3_residual_norm_backward_args* a) {
   if (a == nullptr || check_residual_shape(a->M, a->D, a->in_dtype, a->res_dtype, 0.f) != M3_OK) return 0;
-  return m3::residual_norm_backward_workspace(*a);
+  return m3::residual_norm_backward_fits(*a) ? m3::residual_norm_backward_workspace(*a) : 0;
 }
 
 int m3_residual_norm_backward(const m3_residual_norm_backward_args* args, void* stream) {
@@ -256,6 +265,7 @@ int m3_residual_norm_backward(const m3_residual_norm_backward_args* args, void* 
   m3_residual_norm_backward_args a = *args;
   const int rc = check_residual_shape(a.M, a.D, a.in_dtype, a.res_dtype, a.eps);
   if (rc != M3_OK) return rc;
+  if (!m3::residual_norm_backward_fits(a)) return M3_ERR_UNSUPPORTED;
   if (!all_set({a.h, a.dy}) || !set_ld(a.x_ld, a.D)) return M3_ERR_INVALID_ARG;
   if ((a.w == nullptr) != (a.dw == nullptr) || (a.scale == nullptr) != (a.dscale == nullptr)) return M3_ERR_INVALID_ARG;
   if (a.scale != nullptr && a.x == nullptr) return M3_ERR_INVALID_ARG;

@@ -424,8 +424,9 @@ hipError_t bw_by_taps(const m3_conv_backward_args& a, hipStream_t s) {
 }  // namespace
 
 hipError_t launch_colsum(const ColSum& c, hipStream_t s) {
-  if (colsum_cols(c) == 16) colsum_kernel<16><<<colsum_blocks(c), 1024, 0, s>>>(c);
-  else colsum_kernel<128><<<colsum_blocks(c), 1024, 0, s>>>(c);
+  const uint32_t blocks = uint32_t(colsum_blocks(c.P, c.ncols));
+  if (colsum_cols(c.P) == 16) colsum_kernel<16><<<blocks, 1024, 0, s>>>(c);
+  else colsum_kernel<128><<<blocks, 1024, 0, s>>>(c);
   return hipGetLastError();
 }
 
@@ -453,7 +454,9 @@ hipError_t launch_conv_step(const m3_conv_step_args& a, hipStream_t s) {
 // the forward's registers; 8192 tokens of 2047 channels bf16 take 54 us in words
 // and 73 us one at a time.
 size_t conv_backward_workspace(const m3_conv_backward_args& a) {
-  return round256(size_t(bw_geom(a, a.D >= 4 ? 4 : 1).ngroups) * a.Bt * (a.W + 1) * a.D * 4);
+  const BwGeom g = bw_geom(a, a.D >= 4 ? 4 : 1);
+  const int64_t P = g.ngroups * a.Bt, ncols = int64_t(a.W + 1) * a.D;
+  return launchable(g.ncb * P, 256) && launchable(colsum_blocks(P, ncols), 1024) ? round256(size_t(P) * ncols * 4) : 0;
 }
 hipError_t launch_conv_backward(const m3_conv_backward_args& a, hipStream_t s) {
   const bool bf = a.in_dtype == M3_BF16;

@@ -22,21 +22,31 @@ struct ColSum {
 };
 hipError_t launch_colsum(const ColSum& c, hipStream_t s);
 
+// Whether a launch's work items, blocks times threads, stay within the 32 bits in which
+// they are counted.  The *_fits functions, and for the backwards of convolution and scan a
+// workspace size other than 0, say so for all launches of a call; the calls without either
+// stay within it by the limits of their sizes.
+inline bool launchable(int64_t blocks, int threads) { return blocks * threads < (int64_t(1) << 32); }
+
 hipError_t launch_conv(const m3_conv_args& a, hipStream_t s);
 hipError_t launch_conv_step(const m3_conv_step_args& a, hipStream_t s);
 size_t conv_backward_workspace(const m3_conv_backward_args& a);
 hipError_t launch_conv_backward(const m3_conv_backward_args& a, hipStream_t s);
 
+bool scan_fits(const m3_scan_args& a);
 size_t scan_workspace(const m3_scan_args& a);
 hipError_t launch_scan(const m3_scan_args& a, hipStream_t s);
+bool scan_step_fits(const m3_scan_step_args& a);
 hipError_t launch_scan_step(const m3_scan_step_args& a, hipStream_t s);
 size_t scan_backward_workspace(const m3_scan_backward_args& a);
 hipError_t launch_scan_backward(const m3_scan_backward_args& a, hipStream_t s);
 
 hipError_t launch_gated_norm(const m3_gated_norm_args& a, hipStream_t s);
+bool gated_norm_backward_fits(const m3_gated_norm_backward_args& a);
 size_t gated_norm_backward_workspace(const m3_gated_norm_backward_args& a);
 hipError_t launch_gated_norm_backward(const m3_gated_norm_backward_args& a, hipStream_t s);
 hipError_t launch_residual_norm(const m3_residual_norm_args& a, hipStream_t s);
+bool residual_norm_backward_fits(const m3_residual_norm_backward_args& a);
 size_t residual_norm_backward_workspace(const m3_residual_norm_backward_args& a);
 hipError_t launch_residual_norm_backward(const m3_residual_norm_backward_args& a, hipStream_t s);
 
@@ -174,8 +184,8 @@ inline size_t round256(size_t v) { return (v + 255) & ~size_t(255); }
 // Column sums: a block of 1024 threads takes COLS columns, its 1024 / COLS row groups
 // every so many-th partial row, joined in LDS.  Few columns per block for many rows, so
 // that a narrow matrix still fills the card (64-byte pieces of a row).
-inline int colsum_cols(const ColSum& c) { return c.P > 32 ? 16 : 128; }
-inline uint32_t colsum_blocks(const ColSum& c) { return uint32_t((c.ncols + colsum_cols(c) - 1) / colsum_cols(c)); }
+inline int colsum_cols(int64_t P) { return P > 32 ? 16 : 128; }
+inline int64_t colsum_blocks(int64_t P, int64_t ncols) { return (ncols + colsum_cols(P) - 1) / colsum_cols(P); }
 template <int COLS>
 __device__ __forceinline__ void colsum_block(const ColSum& c, uint32_t block, float* red) {
   constexpr int RG = 1024 / COLS;

@@ -801,11 +801,14 @@ hipError_t run_residual_bw(const m3_residual_norm_backward_args& a, hipStream_t 
 hipError_t launch_gated_norm(const m3_gated_norm_args& a, hipStream_t s) {
   return a.in_dtype == M3_BF16 ? run_gated<bf16_t>(a, s) : run_gated<float>(a, s);
 }
+static int64_t gated_bw_walkers(const m3_gated_norm_args& f) {
+  return pick_walkers(f.M, f.G, pick(f.M * f.G, f.D / f.G, f.in_dtype, true), kBackwardWaves);
+}
+bool gated_norm_backward_fits(const m3_gated_norm_backward_args& a) {
+  return a.fwd.w == nullptr || launchable(colsum_blocks(gated_bw_walkers(a.fwd), a.fwd.D), 1024);
+}
 size_t gated_norm_backward_workspace(const m3_gated_norm_backward_args& a) {
-  const m3_gated_norm_args& f = a.fwd;
-  if (f.w == nullptr) return 0;
-  const int64_t w = pick_walkers(f.M, f.G, pick(f.M * f.G, f.D / f.G, f.in_dtype, true), kBackwardWaves);
-  return round256(size_t(w) * f.D * 4);
+  return a.fwd.w == nullptr ? 0 : round256(size_t(gated_bw_walkers(a.fwd)) * a.fwd.D * 4);
 }
 hipError_t launch_gated_norm_backward(const m3_gated_norm_backward_args& a, hipStream_t s) {
   return a.fwd.in_dtype == M3_BF16 ? run_gated_bw<bf16_t>(a, s) : run_gated_bw<float>(a, s);
@@ -814,9 +817,15 @@ hipError_t launch_residual_norm(const m3_residual_norm_args& a, hipStream_t s) {
   if (a.in_dtype == M3_F32) return run_residual<float, float>(a, s);
   return a.res_dtype == M3_BF16 ? run_residual<bf16_t, bf16_t>(a, s) : run_residual<bf16_t, float>(a, s);
 }
+static int64_t residual_bw_walkers(const m3_residual_norm_backward_args& a) {
+  return pick_walkers(a.M, 1, pick(a.M, a.D, a.in_dtype, true), kBackwardWaves);
+}
+bool residual_norm_backward_fits(const m3_residual_norm_backward_args& a) {
+  const int64_t ncols = int64_t((a.w != nullptr) + (a.scale != nullptr)) * a.D;
+  return launchable(colsum_blocks(residual_bw_walkers(a), ncols), 1024);
+}
 size_t residual_norm_backward_workspace(const m3_residual_norm_backward_args& a) {
-  const int64_t w = pick_walkers(a.M, 1, pick(a.M, a.D, a.in_dtype, true), kBackwardWaves);
-  return round256(size_t(w) * ((a.w != nullptr) + (a.scale != nullptr)) * a.D * 4);
+  return round256(size_t(residual_bw_walkers(a)) * ((a.w != nullptr) + (a.scale != nullptr)) * a.D * 4);
 }
 hipError_t launch_residual_norm_backward(const m3_residual_norm_backward_args& a, hipStream_t s) {
   if (a.in_dtype == M3_F32) return run_residual_bw<float, float>(a, s);

@@ -398,10 +398,10 @@ hipError_t run_step(const m3_scan_step_args& a, hipStream_t st) {
   return hipGetLastError();
 }
 // Several items per lane once the lanes would fill the card twice (256 CUs of 2048).
+int items_of(const m3_scan_step_args& a, int S) { return int64_t(a.Bt) * a.D * S >= 1 << 20 ? 4 : 1; }
 template <typename T, int S, bool VEC>
 hipError_t step_items(const m3_scan_step_args& a, hipStream_t st) {
-  if (int64_t(a.Bt) * a.D * S >= 1 << 20) return run_step<T, S, 4, VEC>(a, st);
-  return run_step<T, S, 1, VEC>(a, st);
+  return items_of(a, S) == 4 ? run_step<T, S, 4, VEC>(a, st) : run_step<T, S, 1, VEC>(a, st);
 }
 
 template <typename T, Words WD>
@@ -415,17 +415,25 @@ hipError_t by_words(const m3_scan_args& a, const Plan& p, Words w, hipStream_t s
   if (w == kAligned) return by_states<T, kAligned>(a, p, st);
   return w == kLoose ? by_states<T, kLoose>(a, p, st) : by_states<T, kSingle>(a, p, st);
 }
+int step_lanes(int N) { return N <= 4 ? 1 : N <= 8 ? 2 : N <= 16 ? 4 : N <= 32 ? 8 : 16; }
 template <typename T, bool VEC>
 hipError_t step_by_lanes(const m3_scan_step_args& a, hipStream_t st) {
-  if (a.N <= 4) return step_items<T, 1, VEC>(a, st);
-  if (a.N <= 8) return step_items<T, 2, VEC>(a, st);
-  if (a.N <= 16) return step_items<T, 4, VEC>(a, st);
-  return a.N <= 32 ? step_items<T, 8, VEC>(a, st) : step_items<T, 16, VEC>(a, st);
+  switch (step_lanes(a.N)) {
+    case 1: return step_items<T, 1, VEC>(a, st);
+    case 2: return step_items<T, 2, VEC>(a, st);
+    case 4: return step_items<T, 4, VEC>(a, st);
+    case 8: return step_items<T, 8, VEC>(a, st);
+    default: return step_items<T, 16, VEC>(a, st);
+  }
 }
 
 }  // namespace
 }  // namespace scan
 
+bool scan_fits(const m3_scan_args& a) {
+  const scan::Plan p = scan::plan_of(a);
+  return launchable(int64_t(a.Bt) * a.G * p.nblk * p.nseg, 2 * scan::kThreads);
+}
 size_t scan_workspace(const m3_scan_args& a) {
   const scan::Plan p = scan::plan_of(a);
   return p.nseg < 2 ? 0 : round256(size_t(p.nseg - 1) * a.Bt * a.D * (a.N + 1) * 4);
@@ -440,6 +448,10 @@ hipError_t launch_scan(const m3_scan_args& a, hipStream_t s) {
                    rows_aligned(a.B, a.B_ld, e, 4 * e) && rows_aligned(a.C, a.C_ld, e, 4 * e);
   const scan::Words w = scan::words_of(a.D / a.G, a.N, aligned);
   return bf ? scan::by_words<bf16_t>(a, p, w, s) : scan::by_words<float>(a, p, w, s);
+}
+bool scan_step_fits(const m3_scan_step_args& a) {
+  const int S = scan::step_lanes(a.N), NI = scan::items_of(a, S);
+  return launchable((int64_t(a.D) * S + scan::kThreads - 1) / scan::kThreads * ((int64_t(a.Bt) + NI - 1) / NI), scan::kThreads);
 }
 hipError_t launch_scan_step(const m3_scan_step_args& a, hipStream_t s) {
   const bool bf = a.in_dtype == M3_BF16;

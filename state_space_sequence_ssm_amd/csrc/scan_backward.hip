@@ -667,7 +667,7 @@ __global__ __launch_bounds__(1024) void sums_kernel(ColSum c, uint32_t sums, con
 
 struct Plan {
   int NB, nblk, nseg, seglen;
-  int64_t tiles, blocks;
+  int64_t tiles, blocks, sums, all;  // the last two: blocks of the joins, of dA, dD and ddt_bias and in all
   size_t oCk, oCd, oHe, oGs, oSd, oBc, oPart, bytes;
 };
 // Segments of the token axis.  The reverse walk's registers leave a compute unit
@@ -702,6 +702,8 @@ Plan plan_of(const m3_scan_args& f) {
     p.nseg = (f.L + p.seglen - 1) / p.seglen;
   }
   p.tiles = (f.L + TB - 1) / TB;
+  p.sums = colsum_blocks(int64_t(p.nseg) * f.Bt, int64_t(f.D) * (f.N + 2));
+  p.all = p.sums + (int64_t(f.Bt) * f.L * f.G * 2 * NP + 1023) / 1024;
   const size_t seg = p.nseg > 1 ? size_t(p.nseg) * f.Bt * f.D : 0;
   p.oCk = 0;
   p.oCd = round256(p.oCk + size_t(p.tiles) * p.blocks * kThreads * 4 * S);
@@ -745,10 +747,9 @@ hipError_t run(const m3_scan_backward_args& a, const Plan& pl, hipStream_t st) {
   c.n[1] = f.D;
   c.dst[2] = a.ddt_bias;
   c.n[2] = f.D;
-  const int64_t rows = int64_t(f.Bt) * f.L, items = rows * f.G * 2 * NP;
-  const uint32_t sums = colsum_blocks(c), all = sums + uint32_t((items + 1023) / 1024);
-  auto* go = colsum_cols(c) == 16 ? sums_kernel<T, NP, 16> : sums_kernel<T, NP, 128>;
-  go<<<all, 1024, 0, st>>>(c, sums, p.bc, static_cast<T*>(a.dB), static_cast<T*>(a.dC), f.lengths, rows, f.L, f.G, f.N, pl.nblk);
+  auto* go = colsum_cols(c.P) == 16 ? sums_kernel<T, NP, 16> : sums_kernel<T, NP, 128>;
+  go<<<uint32_t(pl.all), 1024, 0, st>>>(c, uint32_t(pl.sums), p.bc, static_cast<T*>(a.dB), static_cast<T*>(a.dC), f.lengths,
+                                        int64_t(f.Bt) * f.L, f.L, f.G, f.N, pl.nblk);
   return hipGetLastError();
 }
 
@@ -767,7 +768,10 @@ hipError_t by_words(const m3_scan_backward_args& a, const Plan& p, Words w, hipS
 }  // namespace
 }  // namespace scan
 
-size_t scan_backward_workspace(const m3_scan_backward_args& a) { return scan::plan_of(a.fwd).bytes; }
+size_t scan_backward_workspace(const m3_scan_backward_args& a) {
+  const scan::Plan p = scan::plan_of(a.fwd);
+  return launchable(p.blocks * p.nseg, 2 * scan::kThreads) && launchable(p.all, 1024) ? p.bytes : 0;
+}
 hipError_t launch_scan_backward(const m3_scan_backward_args& a, hipStream_t s) {
   const m3_scan_args& f = a.fwd;
   const bool bf = f.in_dtype == M3_BF16;

@@ -119,3 +119,26 @@ def test_rows_past_the_widest_are_refused(D):
     assert _refused("m3_gated_norm_backward", M=1, D=D, G=1, eps=1e-6) == (UNS, 0)
     assert _refused("m3_residual_norm", M=1, D=D, res_dtype=_lib.M3_F32, eps=1e-6) == (UNS, None)
     assert _refused("m3_residual_norm_backward", M=1, D=D, res_dtype=_lib.M3_F32, eps=1e-6) == (UNS, 0)
+
+
+# one launch of the call just past 2^32 work items, and what it is
+LAUNCHES = [
+    ("m3_causal_conv_backward", dict(Bt=1 << 24, L=1, D=4, W=4)),           # 256 per item
+    ("m3_causal_conv_backward", dict(Bt=64, L=1, D=1 << 24, W=4)),          # 64 per sum: 5 D of them
+    ("m3_selective_scan", dict(Bt=32768, L=1, D=4096, N=64, G=1)),          # 512 per item and 16 channels
+    ("m3_selective_scan", dict(Bt=1 << 23, L=1, D=64, N=4, G=1)),           # 512 per item
+    ("m3_selective_scan_step", dict(Bt=1 << 12, D=1 << 18, N=64, G=1)),     # 16 / 4 per item and channel
+    ("m3_selective_scan_backward", dict(Bt=1 << 23, L=1, D=64, N=4, G=1)),  # 512 per item
+    ("m3_selective_scan_backward", dict(Bt=8, L=1 << 24, D=4, N=16, G=1)),  # 32 per token
+    ("m3_selective_scan_backward", dict(Bt=64, L=1, D=1 << 20, N=64, G=1)),  # 64 per sum: 66 D of them
+    ("m3_gated_norm_backward", dict(M=64, D=1 << 26, G=1, eps=1e-6)),       # 64 per sum
+    ("m3_residual_norm_backward", dict(M=64, D=1 << 25, res_dtype=_lib.M3_BF16, eps=1e-6)),
+]
+
+
+@built
+@pytest.mark.parametrize("name,sizes", LAUNCHES, ids=lambda v: v if isinstance(v, str) else "-".join(map(str, v.values())))
+def test_launches_of_more_work_items_than_are_counted_are_refused(name, sizes):
+    """Before the first launch, and no workspace is asked for."""
+    code, size = _refused(name, **sizes)
+    assert code == UNS and not size
