@@ -474,7 +474,8 @@ int m3_causal_conv_backward(const m3_conv_backward_args* args, void* stream);
  *   x, dt, z [Bt, L, D] (x_ld, dt_ld, z_ld), B, C [Bt, L, G, N] (B_ld, C_ld),
  *   A [D, N], D_skip [D] or NULL; h0 [Bt, D, N] or NULL (zeros); y [Bt, L, D];
  *   h_final [Bt, D, N] (nullable).
- * Sizes: N in 1..64, G divides D, row distances below 2^24 elements.
+ * Sizes: N in 1..64, G divides D, row distances below 2^24 elements (for its
+ * backward and its token too; others are M3_ERR_INVALID_ARG).
  * workspace: optional; with few (batch, channel) pairs the token axis is cut
  * into segments scanned at once, whose states are joined, when a workspace of
  * m3_selective_scan_workspace_size bytes (256-byte aligned; 0: not used) is

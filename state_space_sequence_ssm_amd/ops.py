@@ -497,6 +497,11 @@ def m3_causal_conv_backward(x, w, bias=None, state=None, *, dy, lengths=None, si
     return out
 
 
+# The library's limit of the scan's row distances.  A token's rows that lie further apart
+# (one position of a batch of long sequences) are copied: they are small beside the state.
+_FAR_ROWS = 1 << 24
+
+
 def _scan_inputs(a, dev, lead, x, dt, A, B, C, D, z, dt_softplus, dt_bias):
     """The inputs that the scan, its backward and its step share."""
     G, N = B.shape[-2:]
@@ -553,6 +558,9 @@ def m3_selective_scan_step(h, x, dt, A, B, C, D=None, z=None, *, dt_softplus=Fal
     a = _lib.ScanStepArgs()
     a.Bt = Bt
     _scan_inputs(a, dev, (Bt,), x, dt, A, B, C, D, z, dt_softplus, dt_bias)
+    if max(a.x_ld, a.dt_ld, a.z_ld, a.B_ld, a.C_ld) >= _FAR_ROWS:
+        x, dt, z, B, C = (None if t is None else t.contiguous() for t in (x, dt, z, B, C))
+        _scan_inputs(a, dev, (Bt,), x, dt, A, B, C, D, z, dt_softplus, dt_bias)
     a.h = _dense(h, _F32, (Bt, width, N), "h", dev)
     a.h_out = _dense(h_out, _F32, (Bt, width, N), "h_out", dev)
     y, a.y = _out(y, x.dtype, (Bt, width), "y", x, dev)

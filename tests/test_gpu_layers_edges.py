@@ -135,3 +135,25 @@ def test_arguments_by_name(ops):
         for p, q in zip(a.values(), c.values()) if isinstance(a, dict) else ((a, c),):
             # steps of either sign overflow here: bits, since no NaN equals itself
             assert p is None and q is None or torch.equal(p.view(torch.uint8), q.view(torch.uint8)), fn.__name__
+
+
+# ---------------------------------------------------------------- far slices
+def test_scan_step_at_one_position_of_long_sequences(ops):
+    """Rows 2^24 elements apart: 8192 positions of 2048 channels, 2^20 of 16 states."""
+    m = Maker(96)
+    Bt, D, N, t = 2, 2048, 16, 17
+    x, dt, z = (torch.zeros(Bt, 8192, D, device="cuda", dtype=BF) for _ in range(3))
+    B, C = (torch.zeros(Bt, 1 << 20, 1, N, device="cuda", dtype=BF) for _ in range(2))
+    for v in (x, dt, z, B, C):
+        v[:, t] = m(*v[:, t].shape, dtype=BF)
+    A, skip, db, h0 = -torch.exp(m(D, N)), m(D), m(D, shift=-3.0), m(Bt, D, N)
+    h, ho = h0.clone(), torch.empty_like(h0)
+    kw = dict(dt_softplus=True, dt_bias=db)
+    assert x[:, t].stride(0) == B[:, t].stride(0) == 1 << 24
+    y = ops.m3_selective_scan_step(h, x[:, t], dt[:, t], A, B[:, t], C[:, t], skip, z[:, t], **kw)
+    near = [v[:, t].contiguous() for v in (x, dt, B, C, z)]
+    want = ops.m3_selective_scan_step(h0, near[0], near[1], A, near[2], near[3], skip, near[4], h_out=ho, **kw)
+    assert torch.equal(y, want) and torch.equal(h, ho)
+    st = m(Bt, 3, D, dtype=BF)
+    w = m(D, 4)
+    assert torch.equal(ops.m3_causal_conv_step(st.clone(), x[:, t], w), ops.m3_causal_conv_step(st.clone(), near[0], w))
