@@ -142,3 +142,45 @@ def test_launches_of_more_work_items_than_are_counted_are_refused(name, sizes):
     """Before the first launch, and no workspace is asked for."""
     code, size = _refused(name, **sizes)
     assert code == UNS and not size
+
+
+FAR = (1 << 32) + 5  # 5 in the structures' 32 bits
+
+
+def test_sizes_past_32_bits_are_refused(monkeypatch):
+    """The argument structures hold sizes in 32 bits, and would keep the rest of a larger one."""
+    from state_space_sequence_ssm_amd import ops
+    ran = []
+    monkeypatch.setattr(ops, "_run_layer", lambda name, a, dev: ran.append(name))
+    monkeypatch.setattr(ops, "_take_workspace", lambda *a: None)
+    monkeypatch.setattr(ops, "_dense", lambda *a: None)
+    monkeypatch.setattr(ops, "_rows", lambda *a: (None, 0))
+
+    def calls(b, l, d, n, w, g, groups):
+        t = lambda *shape: torch.zeros(()).expand(shape)  # noqa: E731
+        x, x1, A, B, out = t(b, l, d), t(b, d), t(d, n), t(b, l, g, n), dict(y=t(1))
+        grads = {k: t(1) for k in ("dx", "dw", "ddt", "dA", "dB", "dC", "dresidual")}
+        return [lambda: ops.m3_causal_conv.__wrapped__(x, t(d, w), **out),
+                lambda: ops.m3_causal_conv_step.__wrapped__(t(b, w - 1, d), x1, t(d, w), **out),
+                lambda: ops.m3_causal_conv_backward.__wrapped__(x, t(d, w), dy=x, out=grads),
+                lambda: ops.m3_selective_scan.__wrapped__(x, x, A, B, B, want_state=False, **out),
+                lambda: ops.m3_selective_scan_step.__wrapped__(t(b, d, n), x1, x1, A, B[:, 0], B[:, 0], **out),
+                lambda: ops.m3_selective_scan_backward.__wrapped__(x, x, A, B, B, dy=x, out=grads),
+                lambda: ops.m3_gated_norm.__wrapped__(x, groups=groups, **out),
+                lambda: ops.m3_gated_norm_backward.__wrapped__(x, dy=x, groups=groups, out=grads),
+                lambda: ops.m3_residual_norm.__wrapped__(x, want_residual=False, **out),
+                lambda: ops.m3_residual_norm_backward.__wrapped__(x, dy=x, out=grads)]
+
+    small = dict(b=1, l=1, d=1, n=1, w=4, g=1, groups=1)
+    for call in calls(**small):
+        call()
+    assert sorted(ran) == sorted(_lib.LAYER_CALLS)
+    conv, scan, gated, residual = (0, 1, 2), (3, 4, 5), (6, 7), (8, 9)
+    for field, wide in dict(b=conv + scan, l=(0, 2, 3, 5), d=range(10), n=scan, w=conv, g=scan, groups=gated).items():
+        for far in (FAR, 1 - (1 << 32)) if field == "groups" else (FAR,):
+            del ran[:]
+            todo = calls(**dict(small, **{field: far}))
+            for i in wide:
+                with pytest.raises(ValueError, match="2147483647"):
+                    todo[i]()
+            assert not ran
