@@ -157,3 +157,36 @@ def test_scan_step_at_one_position_of_long_sequences(ops):
     st = m(Bt, 3, D, dtype=BF)
     w = m(D, 4)
     assert torch.equal(ops.m3_causal_conv_step(st.clone(), x[:, t], w), ops.m3_causal_conv_step(st.clone(), near[0], w))
+
+
+# ---------------------------------------------------------------- captured first
+def test_first_call_of_a_kernel_is_captured(ops):
+    """Kernels that nothing has launched before, captured at once: what a launch sets up
+    the first time does not belong to the stream."""
+    m = Maker(97)
+    Bt, L, D, N = 2, 70, 3, 41
+    x, dt, z, dy = (m(Bt, L, D) for _ in range(4))
+    B, C = (m(Bt, L, 1, N) for _ in range(2))
+    A, skip, db, w, gain = -torch.exp(m(D, N)), m(D), m(D, shift=-3.0), m(D, 3), m(D)
+
+    def calls():
+        c = ops.m3_causal_conv(x, w, skip)["y"]
+        s = ops.m3_selective_scan(c, dt, A, B, C, skip, z, dt_softplus=True, dt_bias=db)
+        g = ops.m3_selective_scan_backward(c, dt, A, B, C, skip, z, dy=dy, dt_softplus=True, dt_bias=db)
+        v = ops.m3_causal_conv_backward(x, w, skip, dy=g["dx"])
+        n = ops.m3_gated_norm_backward(s["y"], z, gain, dy=dy)
+        return [c] + [o for d in (s, g, v, n) for o in d.values() if o is not None]
+
+    side, graph = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    side.wait_stream(torch.cuda.current_stream())
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side), torch.cuda.graph(graph, stream=side):
+        held = calls()
+    for _ in range(3):
+        for o in held:
+            o.fill_(NAN)
+        graph.replay()
+        torch.cuda.synchronize()
+        for p, q in zip(calls(), held):
+            assert torch.equal(p, q) and p.isfinite().all()
+        torch.cuda.synchronize()
