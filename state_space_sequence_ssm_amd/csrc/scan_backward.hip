@@ -442,7 +442,9 @@ __global__ __launch_bounds__(2 * kThreads) void reverse_kernel(BwP p) {
     return;
   }
 
-  Stager<T, TB, CHB, NP, WD, true, true, true> st;
+  // a tile that is partly past the end has its rows at its end: the last state, which may
+  // be infinite, then meets the gradients of no row but its tokens'
+  Stager<T, TB, CHB, NP, WD, true, true, true, true> st;
   st.init(p.in, w.b, w.g, w.cb, tid, w.tend);
   const int r = st.r, c0 = st.c0;
   const int64_t out0 = int64_t(w.b) * p.in.L * p.in.D + w.g * p.in.Dg;
@@ -540,9 +542,8 @@ __global__ __launch_bounds__(2 * kThreads) void reverse_kernel(BwP p) {
       wdu[q] = c < NP ? 0.f : sh.sdu[o][t];
     }
   };
-  auto finish = [&](auto half, int t0) {
+  auto finish = [&](auto half) {
     constexpr int o = decltype(half)::value;
-    const bool row = t0 + r < w.tend;
     float y[VE], gB[VE], gA[VE];
 #pragma unroll
     for (int v = 0; v < VE; ++v) y[v] = gB[v] = gA[v] = 0.f;
@@ -563,9 +564,7 @@ __global__ __launch_bounds__(2 * kThreads) void reverse_kernel(BwP p) {
       od[v] = fmaf(kx[o][v], gB[v], gA[v] * kLn2) * ks[o][v];
       oz[v] = kz[o][v] * fmaf(dsk[v], kx[o][v], y[v]);
       dD[v] = fmaf(kg[o][v], kx[o][v], dD[v]);
-      // past the end A's terms are no token's: the state times the gradient behind it times
-      // A itself, which overflows for the A of a state that forgets at once
-      dbias[v] += row ? od[v] : 0.f;
+      dbias[v] += od[v];
     }
 #pragma unroll
     for (int q = 0; q < NS; ++q) {
@@ -579,23 +578,24 @@ __global__ __launch_bounds__(2 * kThreads) void reverse_kernel(BwP p) {
     }
   };
   auto store = [&](int t0) {
-    const bool row = t0 + r < w.tend;
-    const int64_t at = int64_t(t0) * p.in.D;
+    const int64_t first = t0 < w.tend - TB ? t0 : w.tend - TB;  // the token of row 0
+    const bool row = st.token(t0, r);
+    const int64_t at = first * p.in.D;
     store_cols<T, VE, WD>(dxp + at + oo, ox, row, st.ncol);
     store_cols<T, VE, WD>(ddtp + at + oo, od, row, st.ncol);
     if (dzp != nullptr) store_cols<T, VE, WD>(dzp + at + oo, oz, row, st.ncol);
-    float* bt = bcp + t0 * bcrow;
+    float* bt = bcp + first * bcrow;
 #pragma unroll
     for (int q = 0; q < NS; ++q) {
       const int i = tid + q * kThreads, e = 4 * i, t = e / (2 * NP), c = e % (2 * NP);
-      if (i < kSums / 4 && t0 + t < w.tend) *reinterpret_cast<f32x4*>(bt + (t * bcrow + c)) = obc[q];
+      if (i < kSums / 4 && st.token(t0, t)) *reinterpret_cast<f32x4*>(bt + (t * bcrow + c)) = obc[q];
     }
   };
   const std::integral_constant<int, 0> even;
   const std::integral_constant<int, 1> odd;
   auto start = [&](int i) { return w.tbeg + (tiles - 1 - i) * TB; };  // first token of the tile of step i
   auto step = [&](int i, auto half, auto other) {
-    if (i > 0) finish(other, start(i - 1));
+    if (i > 0) finish(other);
     take(half);
     if (i + 1 < tiles) {
       stage(start(i + 1), other);
@@ -615,8 +615,8 @@ __global__ __launch_bounds__(2 * kThreads) void reverse_kernel(BwP p) {
     if (i + 1 < tiles) step(i + 1, odd, even);
   }
   if (tiles > 0) {
-    if (tiles % 2) finish(even, start(tiles - 1));
-    else finish(odd, start(tiles - 1));
+    if (tiles % 2) finish(even);
+    else finish(odd);
     store(start(tiles - 1));
   }
   // ---- sums over the tokens: this thread's rows, then the 16 of each column

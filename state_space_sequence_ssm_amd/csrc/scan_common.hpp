@@ -146,8 +146,11 @@ struct Inputs {
 // A staging thread's part of the tiles of one item and one block of CHB channels:
 // VE neighbouring channels of token r of each tensor, and quads of B (and C).
 // fetch() starts the loads of a tile into registers; the values are used a tile
-// later.  Z, DY, CC: whether z, dy and C are wanted.
-template <typename T, int TT, int CHB, int NP, Words WD, bool Z, bool DY, bool CC>
+// later.  Z, DY, CC: whether z, dy and C are wanted.  TAIL: the rows of a tile that is
+// partly past the end lie at its end and not at its start; the rows that fill it have no
+// step (delta = u = B = C = do = 0) either way, but in front of the tokens they pass on
+// the state in front of the tile, behind them the last one.
+template <typename T, int TT, int CHB, int NP, Words WD, bool Z, bool DY, bool CC, bool TAIL = false>
 struct Stager {
   static constexpr int VE = TT * CHB / kThreads;
   static constexpr int kQuads = (CC ? 2 : 1) * TT * NP / 4, NQ = (kQuads + kThreads - 1) / kThreads;
@@ -192,16 +195,22 @@ struct Stager {
     place(TT - 1, ox, odt, oz, ody, oq);
     qx = qd = qz = qy = Pack<T, VE>{};
   }
+  // row r of a full tile in one whose last row is `last`; whether it is a token's
+  static __device__ __forceinline__ int row_of(int r, int last) {
+    if (TAIL) return r > TT - 1 - last ? r - (TT - 1 - last) : 0;
+    return r < last ? r : last;
+  }
+  __device__ __forceinline__ bool token(int t0, int r) const { return TAIL ? r >= t0 + TT - tend : t0 + r < tend; }
   // this thread's offsets in a tile whose last row is `last`
   __device__ __forceinline__ void place(int last, uint32_t& px, uint32_t& pdt, uint32_t& pz, uint32_t& pdy, uint32_t (&pq)[NQ]) const {
-    const uint32_t rr = r < last ? r : last;
+    const uint32_t rr = row_of(r, last);
     px = rr * uint32_t(xld) + cin;
     pdt = rr * uint32_t(dtld) + cin;
     pz = rr * uint32_t(zld) + cin;
     pdy = rr * uint32_t(dyld) + cin;
 #pragma unroll
     for (int i = 0; i < NQ; ++i)
-      pq[i] = uint32_t(qt[i] < last ? qt[i] : last) * uint32_t(qc[i] ? Cld : Bld) + (qn[i] < N ? qn[i] : 0);
+      pq[i] = uint32_t(row_of(qt[i], last)) * uint32_t(qc[i] ? Cld : Bld) + (qn[i] < N ? qn[i] : 0);
   }
   // tend > 0; a tile past the end reads its last row
   __device__ __forceinline__ void fetch(int t0) {
@@ -228,14 +237,14 @@ struct Stager {
       unpack_cols<T, 4, WD>(qb[i], f, N - qn[i]);
       if (t0 + TT > tend || N < NP) {
 #pragma unroll
-        for (int k = 0; k < 4; ++k) f[k] = qn[i] + k < N && t0 + qt[i] < tend ? f[k] : 0.f;
+        for (int k = 0; k < 4; ++k) f[k] = qn[i] + k < N && token(t0, qt[i]) ? f[k] : 0.f;
       }
       store_pack<float, 4>(bc + ((qc[i] ? TT : 0) + qt[i]) * NP + qn[i], f);
     }
   }
   // whether value v of the fetched tile lies inside
   __device__ __forceinline__ bool edge(int t0) const { return t0 + TT > tend || ncol < VE; }
-  __device__ __forceinline__ bool inside(int t0, int v) const { return t0 + r < tend && v < ncol; }
+  __device__ __forceinline__ bool inside(int t0, int v) const { return token(t0, r) && v < ncol; }
 };
 
 // Blocks of channels never straddle two groups.

@@ -190,3 +190,29 @@ def test_first_call_of_a_kernel_is_captured(ops):
         for p, q in zip(calls(), held):
             assert torch.equal(p, q) and p.isfinite().all()
         torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("L", [1, 16, 45, 300])
+@pytest.mark.parametrize("N", [4, 12, 16, 24, 64])
+def test_scan_backward_behind_an_infinite_input(ops, L, N):
+    """An item's last input is infinite, and so is its last state.  The gradients of A
+    and of the first state, and those of the tokens before, do not depend on it: the
+    tokens that fill the last tile bring it nowhere."""
+    q, m = base._scan_inputs((2, L, 40, N, 1, "f32", [L, (L + 1) // 2], True, True, True, True, True, False), 98)
+    lengths = [L, (L + 1) // 2]
+    dy, dhf = base.spoil(m(2, L, 40), lengths), m(2, 40, N)
+    for last in (None, dhf):
+        got = []
+        for value in (0.0, float("inf")):
+            for b, n in enumerate(lengths):
+                q["x"][b, n - 1, 7] = value
+            args, kw = base._scan_call(q, True)
+            got.append(ops.m3_selective_scan_backward(*args, dy=dy, dh_final=last, lengths=ilen(lengths), want_carry_grads=True, **kw))
+        clean, bad = got
+        assert torch.equal(clean["dA"], bad["dA"]) and torch.equal(clean["dh0"], bad["dh0"]), last is None
+        for b, n in enumerate(lengths):
+            for k in ("dx", "ddt", "dz", "dB", "dC"):
+                assert torch.equal(clean[k][b, :n - 1], bad[k][b, :n - 1]) and (bad[k][b, n:] == 0).all(), k
+        keep = torch.arange(40, device="cuda") != 7
+        for k in ("dD", "ddt_bias"):
+            assert torch.equal(clean[k][keep], bad[k][keep]), k
