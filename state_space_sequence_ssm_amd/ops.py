@@ -310,11 +310,9 @@ def _scoped(fn):
 _MAX = (1 << 31) - 1
 
 
-def _sizes(*v):
-    """Sizes for the structures' 32-bit fields, which would keep the rest of a larger one."""
-    if max(v) > _MAX:
-        raise ValueError(f"sizes up to {_MAX} are taken, got {max(v)}")
-    return v
+def _too_large(*v):
+    """Refuse sizes of which the structures' 32-bit fields would keep the rest."""
+    raise ValueError(f"sizes up to {_MAX} are taken, got {max(v)}")
 
 
 def _refuse(t, dtype, shape, name, dev):
@@ -445,8 +443,9 @@ def m3_causal_conv(x, w, bias=None, state=None, *, lengths=None, silu=True, y=No
     W = w.shape[-1]
     dev, t = x.get_device(), x.dtype
     a = _lib.ConvArgs()
-    a.Bt, a.L, a.D, a.W = _sizes(Bt, L, D, W)
-    a.in_dtype, a.silu = _dtype_code(x), 1 if silu else 0
+    if Bt > _MAX or L > _MAX or D > _MAX or W > _MAX:
+        _too_large(Bt, L, D, W)
+    a.Bt, a.L, a.D, a.W, a.in_dtype, a.silu = Bt, L, D, W, _dtype_code(x), 1 if silu else 0
     a.x, a.x_ld = _rows(x, t, x.shape, 2, "x", dev)
     a.w = _dense(w, _F32, (D, W), "w", dev)
     a.bias = _dense(bias, _F32, (D,), "bias", dev)
@@ -467,8 +466,9 @@ def m3_causal_conv_step(state, x, w, bias=None, *, silu=True, y=None, state_out=
     W = w.shape[-1]
     dev, t = state.get_device(), x.dtype
     a = _lib.ConvStepArgs()
-    a.Bt, a.D, a.W = _sizes(Bt, D, W)
-    a.in_dtype, a.silu = _dtype_code(x), 1 if silu else 0
+    if Bt > _MAX or D > _MAX or W > _MAX:
+        _too_large(Bt, D, W)
+    a.Bt, a.D, a.W, a.in_dtype, a.silu = Bt, D, W, _dtype_code(x), 1 if silu else 0
     a.x, a.x_ld = _rows(x, t, x.shape, 1, "x", dev)
     a.w = _dense(w, _F32, (D, W), "w", dev)
     a.bias = _dense(bias, _F32, (D,), "bias", dev)
@@ -490,8 +490,9 @@ def m3_causal_conv_backward(x, w, bias=None, state=None, *, dy, lengths=None, si
     dev, t = x.get_device(), x.dtype
     got = out or {}
     a = _lib.ConvBackwardArgs()
-    a.Bt, a.L, a.D, a.W = _sizes(Bt, L, D, W)
-    a.in_dtype, a.silu = _dtype_code(x), 1 if silu else 0
+    if Bt > _MAX or L > _MAX or D > _MAX or W > _MAX:
+        _too_large(Bt, L, D, W)
+    a.Bt, a.L, a.D, a.W, a.in_dtype, a.silu = Bt, L, D, W, _dtype_code(x), 1 if silu else 0
     a.x, a.x_ld = _rows(x, t, x.shape, 2, "x", dev)
     a.w = _dense(w, _F32, (D, W), "w", dev)
     a.bias = _dense(bias, _F32, (D,), "bias", dev)
@@ -520,8 +521,9 @@ def _scan_inputs(a, dev, lead, x, dt, A, B, C, D, z, dt_softplus, dt_bias):
     G, N = B.shape[-2:]
     t, shape = x.dtype, x.shape
     width, n, bc = shape[-1], len(lead), (*lead, G, N)
-    a.D, a.N, a.G = _sizes(width, N, G)
-    a.in_dtype, a.dt_softplus = _dtype_code(x), 1 if dt_softplus else 0
+    if width > _MAX or N > _MAX or G > _MAX or max(lead) > _MAX:
+        _too_large(width, N, G, *lead)
+    a.D, a.N, a.G, a.in_dtype, a.dt_softplus = width, N, G, _dtype_code(x), 1 if dt_softplus else 0
     a.x, a.x_ld = _rows(x, t, shape, n, "x", dev)
     a.dt, a.dt_ld = _rows(dt, t, shape, n, "dt", dev)
     a.z, a.z_ld = _rows(z, t, shape, n, "z", dev)
@@ -548,7 +550,7 @@ def m3_selective_scan(x, dt, A, B, C, D=None, z=None, h0=None, *, lengths=None, 
     N = A.shape[-1]
     dev = x.get_device()
     a = _lib.ScanArgs()
-    a.Bt, a.L = _sizes(Bt, L)
+    a.Bt, a.L = Bt, L
     _scan_inputs(a, dev, (Bt, L), x, dt, A, B, C, D, z, dt_softplus, dt_bias)
     a.h0 = _dense(h0, _F32, (Bt, width, N), "h0", dev)
     a.lengths = _dense(lengths, torch.int32, (Bt,), "lengths", dev)
@@ -570,15 +572,19 @@ def m3_selective_scan_step(h, x, dt, A, B, C, D=None, z=None, *, dt_softplus=Fal
     N = A.shape[-1]
     dev = h.get_device()
     a = _lib.ScanStepArgs()
-    (a.Bt,) = _sizes(Bt)
+    a.Bt = Bt
     _scan_inputs(a, dev, (Bt,), x, dt, A, B, C, D, z, dt_softplus, dt_bias)
-    if max(a.x_ld, a.dt_ld, a.z_ld, a.B_ld, a.C_ld) >= _FAR_ROWS:
-        x, dt, z, B, C = (None if t is None else t.contiguous() for t in (x, dt, z, B, C))
-        _scan_inputs(a, dev, (Bt,), x, dt, A, B, C, D, z, dt_softplus, dt_bias)
     a.h = _dense(h, _F32, (Bt, width, N), "h", dev)
     a.h_out = _dense(h_out, _F32, (Bt, width, N), "h_out", dev)
     y, a.y = _out(y, x.dtype, (Bt, width), "y", x, dev)
-    _run_layer("m3_selective_scan_step", a, dev)
+    try:
+        _run_layer("m3_selective_scan_step", a, dev)
+    except M3Error:  # refused, and nothing launched: checked here, where it costs other calls nothing
+        if max(a.x_ld, a.dt_ld, a.z_ld, a.B_ld, a.C_ld) < _FAR_ROWS:
+            raise
+        x, dt, z, B, C = (None if t is None else t.contiguous() for t in (x, dt, z, B, C))
+        _scan_inputs(a, dev, (Bt,), x, dt, A, B, C, D, z, dt_softplus, dt_bias)
+        _run_layer("m3_selective_scan_step", a, dev)
     return y
 
 
@@ -594,7 +600,7 @@ def m3_selective_scan_backward(x, dt, A, B, C, D=None, z=None, h0=None, *, dy, d
     dev, t = x.get_device(), x.dtype
     got = out or {}
     a = _lib.ScanBackwardArgs()
-    a.fwd.Bt, a.fwd.L = _sizes(Bt, L)
+    a.fwd.Bt, a.fwd.L = Bt, L
     _scan_inputs(a.fwd, dev, (Bt, L), x, dt, A, B, C, D, z, dt_softplus, dt_bias)
     a.fwd.h0 = _dense(h0, _F32, (Bt, width, N), "h0", dev)
     a.fwd.lengths = _dense(lengths, torch.int32, (Bt,), "lengths", dev)
@@ -617,8 +623,9 @@ def m3_selective_scan_backward(x, dt, A, B, C, D=None, z=None, h0=None, *, dy, d
 def _gated_inputs(a, dev, x, z, w, groups, eps, gate_first):
     shape = x.shape
     n, width = len(shape) - 1, shape[-1]
-    a.D, a.G, _ = _sizes(width, groups, -groups)
-    a.M, a.in_dtype = x.numel() // width if width else 0, _dtype_code(x)
+    if width > _MAX or not -_MAX <= groups <= _MAX:
+        _too_large(width, abs(groups))
+    a.M, a.D, a.G, a.in_dtype = x.numel() // width if width else 0, width, groups, _dtype_code(x)
     a.gate_first, a.eps = 1 if gate_first else 0, eps
     a.x, a.x_ld = _rows(x, x.dtype, shape, n, "x", dev)
     a.z, a.z_ld = _rows(z, x.dtype, shape, n, "z", dev)
@@ -672,9 +679,10 @@ def m3_residual_norm(x, residual=None, w=None, scale=None, *, eps=1e-6, y=None, 
     like = residual if residual is not None else residual_out if residual_out is not None else x
     rt = like.dtype
     a = _lib.ResidualNormArgs()
-    (a.D,), a.M = _sizes(width), x.numel() // width if width else 0
-    a.in_dtype = _dtype_code(x)
-    a.res_dtype, a.eps = _dtype_code(like), eps
+    if width > _MAX:
+        _too_large(width)
+    a.M, a.D, a.in_dtype = x.numel() // width if width else 0, width, _dtype_code(x)
+    a.res_dtype, a.eps = _lib.M3_F32 if rt == _F32 else a.in_dtype if rt == t else _dtype_code(like), eps
     a.x, a.x_ld = _rows(x, t, shape, len(shape) - 1, "x", dev)
     a.residual = _dense(residual, rt, shape, "residual", dev)
     a.scale = _dense(scale, _F32, (width,), "scale", dev)
@@ -697,8 +705,9 @@ def m3_residual_norm_backward(h, x=None, w=None, scale=None, *, dy, dresidual=No
     dev, t, width = h.get_device(), dy.dtype, h.shape[-1]
     got = out or {}
     a = _lib.ResidualNormBackwardArgs()
-    (a.D,), a.M = _sizes(width), h.numel() // width if width else 0
-    a.in_dtype = _dtype_code(dy)
+    if width > _MAX:
+        _too_large(width)
+    a.M, a.D, a.in_dtype = h.numel() // width if width else 0, width, _dtype_code(dy)
     a.res_dtype, a.eps = _dtype_code(h), eps
     a.h = _dense(h, h.dtype, h.shape, "h", dev)
     a.x, a.x_ld = _rows(x, t, h.shape, h.dim() - 1, "x", dev)
