@@ -13,6 +13,7 @@ Entry points (same names as the C ABI):
                         gated group RMS norm behind the core
   m3_residual_norm, m3_residual_norm_backward
                         residual sum and RMS norm in front of the next block
+Outputs carry no gradient history; gradients come from the `_backward` entry points.
 """
 from ._lib import LAYER_CALLS, LIB_PATH, load  # noqa: F401
 

@@ -189,7 +189,7 @@ struct ConvBwP {
 // One thread: V channels down `tt` tokens and the W - 1 after them, whose dpre
 // its last dx need, four at a time with the next four on their way; a block is CX
 // columns times 256 / CX tiles, whose sums of dw and dbias are joined in LDS
-// before they go to the workspace.  Bt 8, L 4096, D 2048, W 4 bf16: 89 us, 4.5 TB/s,
+// before they go to the workspace.  Bt 8, L 4096, D 2048, W 4 bf16: 83 us, 4.8 TB/s,
 // and 5 us for the join.
 template <typename T, int W, int V, bool RAG>
 __global__ __launch_bounds__(256) void conv_backward_kernel(ConvBwP p) {
@@ -343,7 +343,7 @@ __global__ __launch_bounds__(1024) void colsum_kernel(ColSum c) {
 // write fewer partial sums, short ones give more threads: halved while the threads
 // are fewer than a quarter of the card's lanes (256 CUs of 2048).  Bt 8, L 4096, D
 // 2048 bf16: 58 us with 64 tokens, 64 us with 32; backward 89 us with 128, 103 us
-// with 64.
+// with 64 (measured with selections for padding in every row; 83 us without them).
 int conv_tile(int64_t Bt, int L, int64_t nv, int most) {
   int tt = most;
   while (tt > 8 && Bt * ((L + tt - 1) / tt) * nv < 131072) tt /= 2;
@@ -436,7 +436,7 @@ hipError_t launch_conv(const m3_conv_args& a, hipStream_t s) {
   if (rows_aligned(a.x, a.x_ld, e, 16) && rows_aligned(a.y, a.D, e, 16) && rows_aligned(a.state, a.D, e, 16) &&
       rows_aligned(a.state_out, a.D, e, 16))
     return bf ? by_taps<bf16_t, 8, false>(a, s) : by_taps<float, 4, false>(a, s);
-  // a carry updated in place has room for one writer per channel; 8192 tokens of 2047
+  // a carry updated in place has room for one writer per channel; 16384 tokens of 2047
   // channels bf16 take 37 us in words, 47 us one at a time
   if (a.D >= (bf ? 8 : 4) && (a.state_out == nullptr || a.state_out != a.state))
     return bf ? by_taps<bf16_t, 8, true>(a, s) : by_taps<float, 4, true>(a, s);
@@ -451,7 +451,7 @@ hipError_t launch_conv_step(const m3_conv_step_args& a, hipStream_t s) {
   return bf ? step_by_taps<bf16_t, 1>(a, s) : step_by_taps<float, 1>(a, s);
 }
 // Four channels per thread in the backward, whose windows of x and dpre are twice
-// the forward's registers; 8192 tokens of 2047 channels bf16 take 54 us in words
+// the forward's registers; 16384 tokens of 2047 channels bf16 take 53 us in words
 // and 73 us one at a time.
 size_t conv_backward_workspace(const m3_conv_backward_args& a) {
   const BwGeom g = bw_geom(a, a.D >= 4 ? 4 : 1);

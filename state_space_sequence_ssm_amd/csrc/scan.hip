@@ -50,7 +50,7 @@ struct Four {
 // not between its tiles, with one barrier per tile.  128 registers, so that a
 // compute unit holds two blocks where there are as many.  Bt 8, L 4096, D 2048, N 16
 // bf16, gated: 290-320 us with the clock, 29 vector instructions per token and wave
-// and the vector ALUs 83-87% busy; the recurrence's own instructions take 164 us.
+// and the vector ALUs 81-87% busy; the recurrence's own instructions take 164 us.
 template <typename T, int NB, int S, Words WD, bool FULL>
 __global__ __launch_bounds__(2 * kThreads, 4) void scan_kernel(ScanP p) {
   constexpr int CHB = CH / NB, VE = TT * CHB / kThreads, NP = 4 * S * NB;
@@ -355,7 +355,11 @@ struct Plan {
 // but four where the items' lengths differ and blocks behind them have nothing to
 // do (5 items of 0 to 1537 tokens, 160 blocks: 85 us, with two 100 us, uncut 114
 // us); 64 tokens to a segment
-// at least (512 tokens: 24 us, with 128 29 us).
+// at least (512 tokens: 24 us, with 128 29 us).  Few channels leave few blocks and many
+// segments: one item of 1024 tokens of 64 channels takes 24 us cut and 73 us uncut, of
+// 8192 tokens of 64, 128 and 256 channels 73, 74 and 132 us and 546 us, of 65536 tokens
+// 471, 283 and 237 us and 4320 us.  The last segments' joins, which read the segments in
+// front one after the other, weigh most there.
 Plan plan_of(const m3_scan_args& a) {
   Plan p;
   p.NB = state_blocks(a.N);

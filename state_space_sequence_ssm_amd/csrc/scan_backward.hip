@@ -112,7 +112,8 @@ struct Four {
 };
 
 // First walk: states in front of the tiles, and with SEG the segments' ends.  Bt 8,
-// L 2048, D 2048, N 16 bf16, uncut: 113 us.
+// L 2048, D 2048, N 16 bf16, uncut: 113-121 us, the vector ALUs 70% busy: 256 blocks
+// are one per compute unit there, two waves per SIMD.
 template <typename T, int NB, int S, Words WD, bool SEG>
 __global__ __launch_bounds__(2 * kThreads) void states_kernel(BwP p) {
   constexpr int TT = 32, CHB = CH / NB, VE = TT * CHB / kThreads, NP = 4 * S * NB;
@@ -289,8 +290,8 @@ struct Shared {
 
 // Second walk.  Bound by vector issue (86% busy): 82 instructions per token and wave
 // for the recurrences and sums, 22 of them the sums of dB and dC over channels, and
-// about 17 for staging.  250 registers leave a compute unit one block.  Bt 8, L 2048,
-// D 2048, N 16 bf16: 410-435 us.
+// about 16 for staging.  248 registers leave a compute unit one block.  Bt 8, L 2048,
+// D 2048, N 16 bf16: 410-450 us.
 template <typename T, int NB, int S, Words WD>
 __global__ __launch_bounds__(2 * kThreads) void reverse_kernel(BwP p) {
   constexpr int CHB = CH / NB, VE = TB * CHB / kThreads, NP = 4 * S * NB;

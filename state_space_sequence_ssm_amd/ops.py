@@ -1,7 +1,12 @@
-"""Thin torch binding of the C ABI: the same three entry points, marshalling
-device tensors into the argument structures.  Every step of the computation
-runs in the HIP kernels of libm3ssm.so; torch only provides device memory
-and the current stream.
+"""Thin torch binding of the C ABI: its entry points by the same names,
+marshalling device tensors into the argument structures.  Every step of the
+computation runs in the HIP kernels of libm3ssm.so; torch only provides device
+memory and the current stream (and copies a token's rows that lie too far apart
+for the library, in m3_selective_scan_step).
+
+Nothing here is recorded for automatic differentiation: outputs carry no gradient
+history, also where inputs require gradients.  Gradients come from the `_backward`
+entry points; a torch.autograd.Function around a pair of them records both.
 """
 from __future__ import annotations
 
@@ -438,7 +443,8 @@ def m3_causal_conv(x, w, bias=None, state=None, *, lengths=None, silu=True, y=No
     Returns a dict with y [Bt, L, D] (rows behind an item's length are left as
     they were) and, with want_state or state_out (may be `state`), state: the
     last W - 1 inputs.  `stream`: the stream to run on (default: the current
-    one), for this and the following operators."""
+    one), for this and the following operators.  No operator records its
+    call for automatic differentiation: gradients come from `_backward`."""
     Bt, L, D = x.shape
     W = w.shape[-1]
     dev, t = x.get_device(), x.dtype
@@ -567,7 +573,8 @@ def m3_selective_scan(x, dt, A, B, C, D=None, z=None, h0=None, *, lengths=None, 
 def m3_selective_scan_step(h, x, dt, A, B, C, D=None, z=None, *, dt_softplus=False, dt_bias=None, y=None, h_out=None):
     """One token of m3_selective_scan: x, dt, z [Bt, D], B, C [Bt, G, N], h
     [Bt, D, N] fp32 updated in place (or read only, the new state going to
-    h_out).  Returns y [Bt, D]."""
+    h_out).  Rows 2^24 elements apart and more are copied first.  Returns y
+    [Bt, D]."""
     Bt, width = x.shape
     N = A.shape[-1]
     dev = h.get_device()
