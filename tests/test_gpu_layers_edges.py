@@ -216,3 +216,10 @@ def test_scan_backward_behind_an_infinite_input(ops, L, N):
         keep = torch.arange(40, device="cuda") != 7
         for k in ("dD", "ddt_bias"):
             assert torch.equal(clean[k][keep], bad[k][keep]), k
+
+
+# ---------------------------------------------------------------- several items per lane
+@pytest.mark.parametrize("Bt,D,N,dt,strided", [(259, 1030, 13, "bf16", True), (258, 1040, 16, "f32", False), (133, 500, 61, "f32", True)])
+def test_scan_step_of_many_items(ops, Bt, D, N, dt, strided):
+    """Batches large enough that a lane takes four items, and no multiple of four."""
+    base.test_scan_step(ops, Bt, D, N, 1, dt, strided)
