@@ -68,9 +68,9 @@ def draw(rng):
         K, V = (rng.choice([32, 64, 64, 128, 128, 256, rng.randint(8, 200)]) for _ in range(2))
         if op == "attention_step":
             return dict(op=op, Bt=_log(rng, 1, max(1, min(512, (1 << 26) // (H * K * V)))), H=H, Hk=Hk, K=K, V=V, dtype=dtype)
-        most, values = (1 << 32, 1 << 25) if op == "attention" else (1 << 31, 1 << 24)
+        most, values = (1 << 32, 1 << 25) if op == "attention" else (1 << 31, 3 << 22)
         L = max(1, min(_log(rng, 1, 16384), most // (H * K * V), values // (H * max(K, V))))
-        Bt = _log(rng, 1, max(1, min(32, most // (L * H * K * V), values // (L * H * max(K, V)), (1 << 25) // (H * K * V))))
+        Bt = _log(rng, 1, max(1, min(32, most // (L * H * K * V), values // (L * H * max(K, V)), values // (H * K * V))))
         return dict(op=op, Bt=Bt, L=L, H=H, Hk=Hk, K=K, V=V, dtype=dtype, ragged=rng.random() < 0.3)
     D = rng.choice([64, 64, 128, 128, 256, 2 * rng.randint(8, 100)])
     R = rng.choice([D, D, D // 4 * 2])
