@@ -646,6 +646,143 @@ typedef struct m3_residual_norm_backward_args {
 size_t m3_residual_norm_backward_workspace_size(const m3_residual_norm_backward_args* args);
 int m3_residual_norm_backward(const m3_residual_norm_backward_args* args, void* stream);
 
+/*
+ * ---------------------------------------------------------------- linear attention
+ * The mixer beside the core: queries, keys and values against a matrix state per
+ * head with one constant decay for each head, and the norm and rotation by
+ * position of its queries and keys.  A learned decay, or one per token, is the
+ * core's (A, A_tok).  Types, row distances, lengths, aliasing and limits of
+ * launches as for the layer operators; the rows of a tensor [Bt, L, H, K] are
+ * its tokens (H * K dense elements each), row distances are below 2^24.
+ */
+
+/* Linear attention with a decay for each head:
+ *   S_t = exp(log_decay[h]) S_{t-1} + k_t v_t^T,   y_t = scale q_t^T S_t,
+ * head h of q and y with head h / (H / Hk) of k and v.
+ *   q [Bt, L, H, K] (q_ld), k [Bt, L, Hk, K] (k_ld), v [Bt, L, Hk, V] (v_ld),
+ *   y [Bt, L, H, V]; log_decay [H] float32 (0: no decay; -inf: each token alone);
+ *   h0 [Bt, H, K, V] float32 or NULL (zeros); h_final (nullable; may be h0
+ *   itself): the state after the last token.
+ * K and V in 1..256, Hk divides H.
+ * bf16 products are formed on the matrix cores with weights and states split
+ * into bf16 parts, so that the state is as good as fp32 sums make it.
+ * workspace: optional; with few (batch, head) pairs the token axis is cut into
+ * segments whose states are found first, when a workspace of
+ * m3_linear_attention_workspace_size bytes (256-byte aligned; 0: not used) is
+ * given.  It is overwritten by every call, so calls at once need their own. */
+typedef struct m3_linear_attention_args {
+  int32_t Bt, L, H, Hk, K, V;
+  int32_t in_dtype; /* m3_dtype */
+  float scale;
+  const void* q;
+  int64_t q_ld;
+  const void* k;
+  int64_t k_ld;
+  const void* v;
+  int64_t v_ld;
+  const float* log_decay;
+  const float* h0;
+  const int32_t* lengths;
+  void* y;
+  float* h_final;
+  void* workspace;
+  size_t workspace_bytes;
+} m3_linear_attention_args;
+size_t m3_linear_attention_workspace_size(const m3_linear_attention_args* args);
+int m3_linear_attention(const m3_linear_attention_args* args, void* stream);
+
+/* One token of it: q [Bt, H, K], k [Bt, Hk, K], v [Bt, Hk, V] (each `*_ld`
+ * between the batch rows), h [Bt, H, K, V] updated in place, or read only when
+ * h_out is given (which may be h too); y [Bt, H, V]. */
+typedef struct m3_linear_attention_step_args {
+  int32_t Bt, H, Hk, K, V;
+  int32_t in_dtype;
+  float scale;
+  const void* q;
+  int64_t q_ld;
+  const void* k;
+  int64_t k_ld;
+  const void* v;
+  int64_t v_ld;
+  const float* log_decay;
+  float* h;
+  float* h_out; /* NULL: h */
+  void* y;
+} m3_linear_attention_step_args;
+int m3_linear_attention_step(const m3_linear_attention_step_args* args, void* stream);
+
+/* Its gradients for dy [Bt, L, H, V] (dense) and dh_final [Bt, H, K, V]
+ * (nullable): dq [Bt, L, H, K], dk [Bt, L, Hk, K], dv [Bt, L, Hk, V] in in_dtype
+ * (shared heads: summed over the heads that share them, in a fixed order) and
+ * dh0 [Bt, H, K, V] (nullable).  log_decay is a constant.  workspace:
+ * m3_linear_attention_backward_workspace_size bytes, 256-byte aligned (0: none
+ * is needed). */
+typedef struct m3_linear_attention_backward_args {
+  m3_linear_attention_args fwd; /* the forward's inputs; y, h_final, workspace are not read */
+  const void* dy;
+  const float* dh_final;
+  void* dq;
+  void* dk;
+  void* dv;
+  float* dh0;
+  void* workspace;
+  size_t workspace_bytes;
+} m3_linear_attention_backward_args;
+size_t m3_linear_attention_backward_workspace_size(const m3_linear_attention_backward_args* args);
+int m3_linear_attention_backward(const m3_linear_attention_backward_args* args, void* stream);
+
+/* RMS norm of queries and keys for each head, and the rotation by position:
+ *   n = x rsqrt(mean(x^2) + eps) w   (norm = 0: n = x, w must be NULL);
+ *   the pair (n0, n1) of index i < R / 2, angle a = position freqs[i]:
+ *   y0 = n0 cos a - n1 sin a,  y1 = n1 cos a + n0 sin a;
+ * pairs are elements (i, i + R/2) of the head, with adjacent = 1 (2i, 2i + 1);
+ * the elements from R on are not rotated.
+ *   q [Bt, L, H, D] (q_ld), k [Bt, L, Hk, D] (k_ld) or NULL (Hk then 0), q_out,
+ *   k_out the same dense (may be q and k themselves where those are dense);
+ *   q_w, k_w [D] float32 or NULL (ones); freqs [R/2] float32 (R = 0: NULL, no
+ *   rotation), radians per position; positions [Bt, L] int32 or NULL: token t is
+ *   at `start` + t.  Angles are formed in 64 bits.  D in 1..1024, R even, R <= D.
+ *   eps >= 0; a head of zeros with eps = 0 gives NaN.  Rows behind an item's
+ *   length (lengths, as above) are left as they were. */
+typedef struct m3_qk_norm_rope_args {
+  int32_t Bt, L, H, Hk, D, R;
+  int32_t in_dtype;
+  int32_t norm;     /* 0 or 1 */
+  int32_t adjacent; /* 0 or 1 */
+  int32_t start;
+  float eps;
+  const void* q;
+  int64_t q_ld;
+  const void* k;
+  int64_t k_ld;
+  const float* q_w;
+  const float* k_w;
+  const float* freqs;
+  const int32_t* positions;
+  const int32_t* lengths;
+  void* q_out;
+  void* k_out;
+} m3_qk_norm_rope_args;
+int m3_qk_norm_rope(const m3_qk_norm_rope_args* args, void* stream);
+
+/* Its gradients for dq_out, dk_out (dense; the forward's output gradients): dq,
+ * dk dense (may be dq_out and dk_out themselves), zero behind the lengths; dq_w,
+ * dk_w [D] (required iff the gain is given).  workspace:
+ * m3_qk_norm_rope_backward_workspace_size bytes, 256-byte aligned. */
+typedef struct m3_qk_norm_rope_backward_args {
+  m3_qk_norm_rope_args fwd; /* the forward's inputs; q_out, k_out are not read */
+  const void* dq_out;
+  const void* dk_out;
+  void* dq;
+  void* dk;
+  float* dq_w;
+  float* dk_w;
+  void* workspace;
+  size_t workspace_bytes;
+} m3_qk_norm_rope_backward_args;
+size_t m3_qk_norm_rope_backward_workspace_size(const m3_qk_norm_rope_backward_args* args);
+int m3_qk_norm_rope_backward(const m3_qk_norm_rope_backward_args* args, void* stream);
+
 /* Static description of a status code (never NULL). */
 const char* m3_status_string(int status);
 

@@ -137,9 +137,52 @@ LAYER_SIZES = {
     "m3_residual_norm_backward_workspace_size": ResidualNormBackwardArgs,
 }
 
+
+
+class LinearAttentionArgs(ctypes.Structure):
+    _fields_ = [("Bt", _i32), ("L", _i32), ("H", _i32), ("Hk", _i32), ("K", _i32), ("V", _i32), ("in_dtype", _i32), ("scale", _f32),
+                ("q", _vp), ("q_ld", _i64), ("k", _vp), ("k_ld", _i64), ("v", _vp), ("v_ld", _i64), ("log_decay", _vp), ("h0", _vp),
+                ("lengths", _vp), ("y", _vp), ("h_final", _vp), ("workspace", _vp), ("workspace_bytes", _sz)]
+
+
+class LinearAttentionStepArgs(ctypes.Structure):
+    _fields_ = [("Bt", _i32), ("H", _i32), ("Hk", _i32), ("K", _i32), ("V", _i32), ("in_dtype", _i32), ("scale", _f32), ("q", _vp),
+                ("q_ld", _i64), ("k", _vp), ("k_ld", _i64), ("v", _vp), ("v_ld", _i64), ("log_decay", _vp), ("h", _vp), ("h_out", _vp),
+                ("y", _vp)]
+
+
+class LinearAttentionBackwardArgs(ctypes.Structure):
+    _fields_ = [("fwd", LinearAttentionArgs), ("dy", _vp), ("dh_final", _vp), ("dq", _vp), ("dk", _vp), ("dv", _vp), ("dh0", _vp),
+                ("workspace", _vp), ("workspace_bytes", _sz)]
+
+
+class QkNormRopeArgs(ctypes.Structure):
+    _fields_ = [("Bt", _i32), ("L", _i32), ("H", _i32), ("Hk", _i32), ("D", _i32), ("R", _i32), ("in_dtype", _i32), ("norm", _i32),
+                ("adjacent", _i32), ("start", _i32), ("eps", _f32), ("q", _vp), ("q_ld", _i64), ("k", _vp), ("k_ld", _i64),
+                ("q_w", _vp), ("k_w", _vp), ("freqs", _vp), ("positions", _vp), ("lengths", _vp), ("q_out", _vp), ("k_out", _vp)]
+
+
+class QkNormRopeBackwardArgs(ctypes.Structure):
+    _fields_ = [("fwd", QkNormRopeArgs), ("dq_out", _vp), ("dk_out", _vp), ("dq", _vp), ("dk", _vp), ("dq_w", _vp), ("dk_w", _vp),
+                ("workspace", _vp), ("workspace_bytes", _sz)]
+
+
+# linear attention and its queries' and keys' norm and rotation, likewise
+MIXER_CALLS = {
+    "m3_linear_attention": LinearAttentionArgs, "m3_linear_attention_step": LinearAttentionStepArgs,
+    "m3_linear_attention_backward": LinearAttentionBackwardArgs,
+    "m3_qk_norm_rope": QkNormRopeArgs, "m3_qk_norm_rope_backward": QkNormRopeBackwardArgs,
+}
+MIXER_SIZES = {
+    "m3_linear_attention_workspace_size": LinearAttentionArgs,
+    "m3_linear_attention_backward_workspace_size": LinearAttentionBackwardArgs,
+    "m3_qk_norm_rope_backward_workspace_size": QkNormRopeBackwardArgs,
+}
+
 EXPORTS = ("m3_ssm_prefill", "m3_ssm_prefill_workspace_size", "m3_ssm_prefill_noalloc", "m3_ssm_decode_step",
            "m3_ssm_prefill_backward", "m3_ssm_prefill_backward_workspace_size",
-           "m3_rope_angles_cumsum", "m3_status_string", "m3_version", *LAYER_CALLS, *LAYER_SIZES)
+           "m3_rope_angles_cumsum", "m3_status_string", "m3_version", *LAYER_CALLS, *LAYER_SIZES,
+           *MIXER_CALLS, *MIXER_SIZES)
 
 _lib = None
 
@@ -168,10 +211,10 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.m3_ssm_decode_step.restype = ctypes.c_int
     lib.m3_rope_angles_cumsum.argtypes = [_vp, _vp, _vp, _i32, _i32, _i32, _i32, _vp]
     lib.m3_rope_angles_cumsum.restype = ctypes.c_int
-    for name, args in LAYER_CALLS.items():
+    for name, args in (*LAYER_CALLS.items(), *MIXER_CALLS.items()):
         fn = getattr(lib, name)
         fn.argtypes, fn.restype = [ctypes.POINTER(args), _vp], ctypes.c_int
-    for name, args in LAYER_SIZES.items():
+    for name, args in (*LAYER_SIZES.items(), *MIXER_SIZES.items()):
         fn = getattr(lib, name)
         fn.argtypes, fn.restype = [ctypes.POINTER(args)], ctypes.c_size_t
     lib.m3_status_string.argtypes = [ctypes.c_int]

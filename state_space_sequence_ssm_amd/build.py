@@ -19,7 +19,8 @@ LIB = os.path.join(PKG, "libm3ssm.so")
 SOURCES = ["prefill_bf16_n128.hip", "prefill_bf16_n128_pro.hip", "prefill_bf16_n64.hip", "prefill_bf16_n64_pro.hip",
            "prefill_bf16_n32.hip", "prefill_bf16_n32_pro.hip", "prefill_bf16_n16.hip", "prefill_bf16_n16_pro.hip",
            "backward_main.hip", "backward.hip", "backward_pre.hip", "prefill_f32.hip", "decode.hip", "decode_mma.hip",
-           "scan_backward.hip", "norms.hip", "scan.hip", "conv.hip", "api.hip", "api_layer.hip", "angles.hip", "split.hip",
+           "attention_bf16.hip", "attention_f32.hip", "scan_backward.hip", "norms.hip", "scan.hip", "conv.hip", "attention.hip", "rotary.hip", "api.hip", "api_layer.hip",
+           "api_mixer.hip", "angles.hip", "split.hip",
            "prefill_bf16.hip"]
 ARCH = "gfx950"
 
@@ -70,7 +71,7 @@ def build(verbose: bool = False) -> str:
 SAN_DIR = os.path.join(OBJ, "hostsan")
 SAN_LIB = os.path.join(SAN_DIR, "libm3ssm_hostsan.so")
 # host-side sanitizers only: each flag goes to the host compilation of the API layer
-SAN_SOURCES = ["api.hip", "api_layer.hip"]
+SAN_SOURCES = ["api.hip", "api_layer.hip", "api_mixer.hip"]
 SAN_FLAGS = ["-Xarch_host", "-fsanitize=address", "-Xarch_host", "-fsanitize=undefined",
              "-Xarch_host", "-fno-sanitize-recover=all", "-Xarch_host", "-fno-omit-frame-pointer",
              "-Xarch_host", "-g"]
@@ -89,7 +90,7 @@ def asan_runtime() -> str:
 
 
 def build_hostsan(verbose: bool = False) -> str:
-    """libm3ssm_hostsan.so: the host-side C-ABI layer (api.hip, api_layer.hip:
+    """libm3ssm_hostsan.so: the host-side C-ABI layer (api.hip, api_layer.hip, api_mixer.hip:
     argument validation and dispatch) built with AddressSanitizer and UBSan,
     linked with the regular kernel objects of the last build().  For host-only
     tests of the validation paths (no kernel is launched)."""

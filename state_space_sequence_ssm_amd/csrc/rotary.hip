@@ -1,0 +1,448 @@
+// Norm of queries and keys for each head and their rotation by position, forward and
+// backward.  Memory bound: every element is read and written once.
+#include "mixer_internal.hpp"
+
+namespace m3 {
+namespace {
+
+// A wave takes one token: its cosines and sines, which all heads share, are formed once by
+// its 64 lanes and handed round through LDS.  Teams of 2^lgteam lanes then take a head each.
+// A lane holds NU units of its head, two words of V elements: with rotation the partners of
+// V pairs (words R / 2 apart, or with ADJ 2 V adjacent elements), behind R any 2 V elements.
+// RAG: words have the alignment of their elements only, and a range's last unit is moved back
+// to end with it, its first elements, which the unit before holds too, left out of the sums
+// and stored twice with the same value.
+struct RopeP {
+  const void* x[2];   // q, k
+  void* y[2];         // outputs, or in the backward dx
+  const void* dy[2];  // backward
+  const float* w[2];
+  int64_t ld[2];
+  int heads[2], its[2];  // turns of a wave over q's and k's heads
+  const float* freqs;
+  const int32_t* positions;
+  const int32_t* lengths;
+  float* part;  // backward: [blocks][2 D], or null
+  int64_t rows, walkers;
+  int L, D, R, start, norm, lgteam, units, rot_units, splits;
+  float eps, inv;
+};
+
+// cos and sin of 2 pi r, r in turns: reduced in 64 bits to an eighth of a turn around a
+// quarter, then the series of sine and cosine to x^9 and x^10 (off by 2e-9 at pi / 4).
+__device__ __forceinline__ float2 turn_of(double r) {
+  r -= __builtin_rint(r);
+  const double quarter = __builtin_rint(4.0 * r);
+  const float x = static_cast<float>((r - 0.25 * quarter) * 6.283185307179586476925);
+  const float z = x * x;
+  const float s = x * fmaf(z, fmaf(z, fmaf(z, fmaf(z, 2.7557319e-6f, -1.9841270e-4f), 8.3333333e-3f), -0.16666667f), 1.f);
+  const float c = fmaf(z, fmaf(z, fmaf(z, fmaf(z, fmaf(z, -2.7557319e-7f, 2.4801587e-5f), -1.3888889e-3f), 4.1666667e-2f), -0.5f), 1.f);
+  const int k = static_cast<int>(quarter) & 3;
+  const float a = k & 1 ? s : c, b = k & 1 ? c : s;
+  return {k == 1 || k == 2 ? -a : a, k >= 2 ? -b : b};
+}
+
+// Sum over a team of 2^lg lanes, in every lane.
+__device__ __forceinline__ float team_sum(float v, int lg) {
+  if (lg >= 1) v += dpp<0xB1, 0xF, true>(v);
+  if (lg >= 2) v += dpp<0x4E, 0xF, true>(v);
+  if (lg >= 3) v += dpp<0x141, 0xF, true>(v);
+  if (lg >= 4) v += dpp<0x140, 0xF, true>(v);
+  if (lg >= 5) v = add_x16(v);
+  if (lg >= 6) v = add_x32(v);
+  return v;
+}
+
+template <int V, int NU, bool RAG, bool ADJ>
+struct Units {
+  int a[NU], b[NU];  // the words' columns
+  int skip[NU];      // pairs (behind R: elements) at the front that another unit counts
+  int pair[NU];      // first pair, or -1 behind R
+  bool in[NU], once[NU];  // once: b repeats a
+  __device__ __forceinline__ Units(const RopeP& p, int lane, int team) {
+#pragma unroll
+    for (int i = 0; i < NU; ++i) {
+      int u = lane + i * team;
+      in[i] = u < p.units;
+      u = in[i] ? u : 0;
+      once[i] = false;
+      if (u < p.rot_units) {
+        const int half = p.R / 2, s = RAG ? min(u * V, half - V) : u * V;
+        skip[i] = u * V - s;
+        pair[i] = s;
+        a[i] = ADJ ? 2 * s : s;
+        b[i] = ADJ ? 2 * s + V : half + s;
+      } else {
+        const int rest = p.D - p.R, at = (u - p.rot_units) * 2 * V, s = RAG || V == 1 ? max(0, min(at, rest - 2 * V)) : at;
+        skip[i] = at - s;
+        pair[i] = -1;
+        a[i] = p.R + s;
+        b[i] = a[i] + V;
+        if (V == 1 && rest == 1) {
+          b[i] = a[i];
+          once[i] = true;
+        }
+      }
+    }
+  }
+  // whether element j of word a (of word b) is this unit's to count
+  __device__ __forceinline__ bool counts_a(int i, int j) const {
+    if (V > 1 && !RAG) return true;
+    return pair[i] < 0 || !ADJ ? j >= skip[i] : j / 2 >= skip[i];
+  }
+  __device__ __forceinline__ bool counts_b(int i, int j) const {
+    if (V > 1 && !RAG) return true;
+    if (once[i]) return false;
+    if (pair[i] < 0) return V + j >= skip[i];
+    return ADJ ? (V + j) / 2 >= skip[i] : j >= skip[i];
+  }
+};
+
+// (x0, x1) turned by the angle of (c, s); the transposed turn with the other sign of s
+__device__ __forceinline__ void turn2(float& x0, float& x1, float c, float s) {
+  const float y0 = fmaf(x0, c, -(x1 * s));
+  x1 = fmaf(x1, c, x0 * s);
+  x0 = y0;
+}
+template <int V, bool ADJ>
+__device__ __forceinline__ void turn_unit(float (&a)[V], float (&b)[V], const float2 (&cs)[V], float sign) {
+  if constexpr (!ADJ || V == 1) {
+#pragma unroll
+    for (int j = 0; j < V; ++j) turn2(a[j], b[j], cs[j].x, sign * cs[j].y);
+  } else {
+#pragma unroll
+    for (int j = 0; j < V / 2; ++j) {
+      turn2(a[2 * j], a[2 * j + 1], cs[j].x, sign * cs[j].y);
+      turn2(b[2 * j], b[2 * j + 1], cs[V / 2 + j].x, sign * cs[V / 2 + j].y);
+    }
+  }
+}
+template <typename T, int V, bool RAG>
+__device__ __forceinline__ Pack<T, V> fetch(const T* p) {
+  if constexpr (V == 1) {
+    Pack<T, 1> q;
+    q.e[0] = *p;
+    return q;
+  } else {
+    return load_word<T, V, RAG>(p);
+  }
+}
+template <typename T, int V, bool RAG>
+__device__ __forceinline__ void put(T* p, const float (&v)[V]) {
+  if constexpr (V == 1) from_f32(v[0], *p);
+  else store_word<T, V, RAG>(p, v);
+}
+
+// The token's cosines and sines into this wave's part of LDS; no other wave reads them.
+__device__ __forceinline__ void angles(const RopeP& p, float2* cs, int pos, int lane) {
+  for (int i = lane; i < p.R / 2; i += 64) cs[i] = turn_of(double(pos) * double(p.freqs[i]) * 0.15915494309189533577);
+  __builtin_amdgcn_wave_barrier();
+  asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+}
+template <int V, int NU, bool RAG, bool ADJ>
+__device__ __forceinline__ void angles_of(const Units<V, NU, RAG, ADJ>& u, const float2* cs, float2 (&o)[NU][V]) {
+#pragma unroll
+  for (int i = 0; i < NU; ++i)
+#pragma unroll
+    for (int j = 0; j < V; ++j) o[i][j] = u.pair[i] < 0 ? float2{1.f, 0.f} : cs[u.pair[i] + j];
+}
+
+template <typename T, int V, int NU, bool RAG, bool ADJ>
+__global__ __launch_bounds__(256) void rope_kernel(RopeP p) {
+  extern __shared__ float2 lds[];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int64_t id = int64_t(blockIdx.x) * 4 + wave, walker = id / p.splits;
+  const int split = int(id % p.splits);
+  float2* cs = lds + wave * (p.R / 2);
+  const int team = 1 << p.lgteam, teams = 64 >> p.lgteam;
+  const Units<V, NU, RAG, ADJ> u(p, lane & (team - 1), team);
+  const int all = p.its[0] + p.its[1], each = (all + p.splits - 1) / p.splits;
+  for (int64_t row = walker < p.walkers ? walker : p.rows; row < p.rows; row += p.walkers) {
+    const int t = int(row % p.L);
+    if (t >= item_length(p.lengths, int(row / p.L), p.L)) continue;
+    if (p.R > 0) angles(p, cs, p.positions == nullptr ? p.start + t : p.positions[row], lane);
+    float2 turn[NU][V];
+    angles_of<V, NU, RAG, ADJ>(u, cs, turn);
+    for (int it = split * each; it < min(all, (split + 1) * each); ++it) {
+      const int k = it >= p.its[0] ? 1 : 0;
+      const int head = min((it - (k ? p.its[0] : 0)) * teams + (lane >> p.lgteam), p.heads[k] - 1);
+      const T* x = static_cast<const T*>(p.x[k]) + row * p.ld[k] + int64_t(head) * p.D;
+      T* y = static_cast<T*>(p.y[k]) + (row * p.heads[k] + head) * p.D;
+      const float* w = p.w[k];
+      float a[NU][V], b[NU][V];
+      float s = 0.f;
+#pragma unroll
+      for (int i = 0; i < NU; ++i) {
+        unpack<T, V>(fetch<T, V, RAG>(x + u.a[i]), a[i]);
+        unpack<T, V>(fetch<T, V, RAG>(x + u.b[i]), b[i]);
+      }
+      if (p.norm) {
+#pragma unroll
+        for (int i = 0; i < NU; ++i)
+#pragma unroll
+          for (int j = 0; j < V; ++j) {
+            const float va = u.in[i] && u.counts_a(i, j) ? a[i][j] : 0.f, vb = u.in[i] && u.counts_b(i, j) ? b[i][j] : 0.f;
+            s = fmaf(va, va, fmaf(vb, vb, s));
+          }
+        const float r = rsqrtf(team_sum(s, p.lgteam) * p.inv + p.eps);
+#pragma unroll
+        for (int i = 0; i < NU; ++i)
+#pragma unroll
+          for (int j = 0; j < V; ++j) {
+            a[i][j] *= r * (w == nullptr ? 1.f : w[u.a[i] + j]);
+            b[i][j] *= r * (w == nullptr ? 1.f : w[u.b[i] + j]);
+          }
+      }
+#pragma unroll
+      for (int i = 0; i < NU; ++i) {
+        turn_unit<V, ADJ>(a[i], b[i], turn[i], 1.f);
+        if (NU == 1 || u.in[i]) {
+          put<T, V, RAG>(y + u.a[i], a[i]);
+          put<T, V, RAG>(y + u.b[i], b[i]);
+        }
+      }
+    }
+  }
+}
+
+// With n = x r, r = rsqrt(mean(x^2) + eps), d = the output's gradient turned back and
+// e = d w:  dw = sum d n,  dx = r (e - n mean(e n)).
+template <typename T, int V, int NU, bool RAG, bool ADJ>
+__global__ __launch_bounds__(256) void rope_backward_kernel(RopeP p) {
+  extern __shared__ float2 lds[];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int64_t id = int64_t(blockIdx.x) * 4 + wave, walker = id / p.splits;
+  const int split = int(id % p.splits);
+  float2* cs = lds + wave * (p.R / 2);
+  const int team = 1 << p.lgteam, teams = 64 >> p.lgteam;
+  const Units<V, NU, RAG, ADJ> u(p, lane & (team - 1), team);
+  const int all = p.its[0] + p.its[1], each = (all + p.splits - 1) / p.splits;
+  float dwa[2][NU][V], dwb[2][NU][V];
+#pragma unroll
+  for (int k = 0; k < 2; ++k)
+#pragma unroll
+    for (int i = 0; i < NU; ++i)
+#pragma unroll
+      for (int j = 0; j < V; ++j) dwa[k][i][j] = dwb[k][i][j] = 0.f;
+  for (int64_t row = walker < p.walkers ? walker : p.rows; row < p.rows; row += p.walkers) {
+    const int t = int(row % p.L);
+    const bool held = t < item_length(p.lengths, int(row / p.L), p.L);
+    float2 turn[NU][V];
+    if (held) {
+      if (p.R > 0) angles(p, cs, p.positions == nullptr ? p.start + t : p.positions[row], lane);
+      angles_of<V, NU, RAG, ADJ>(u, cs, turn);
+    }
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const int first = k ? p.its[0] : 0;
+      for (int it = max(first, split * each); it < min(first + p.its[k], (split + 1) * each); ++it) {
+        const int mine = (it - first) * teams + (lane >> p.lgteam), head = min(mine, p.heads[k] - 1);
+        const T* x = static_cast<const T*>(p.x[k]) + row * p.ld[k] + int64_t(head) * p.D;
+        const int64_t at = (row * p.heads[k] + head) * p.D;
+        const T* dy = static_cast<const T*>(p.dy[k]) + at;
+        T* dx = static_cast<T*>(p.y[k]) + at;
+        const float* w = p.w[k];
+        float a[NU][V], b[NU][V], da[NU][V], db[NU][V];
+        if (!held) {
+#pragma unroll
+          for (int j = 0; j < V; ++j) a[0][j] = 0.f;
+#pragma unroll
+          for (int i = 0; i < NU; ++i) {
+            put<T, V, RAG>(dx + u.a[i], a[0]);
+            put<T, V, RAG>(dx + u.b[i], a[0]);
+          }
+          continue;
+        }
+#pragma unroll
+        for (int i = 0; i < NU; ++i) {
+          unpack<T, V>(fetch<T, V, RAG>(x + u.a[i]), a[i]);
+          unpack<T, V>(fetch<T, V, RAG>(x + u.b[i]), b[i]);
+          unpack<T, V>(fetch<T, V, RAG>(dy + u.a[i]), da[i]);
+          unpack<T, V>(fetch<T, V, RAG>(dy + u.b[i]), db[i]);
+          turn_unit<V, ADJ>(da[i], db[i], turn[i], -1.f);
+        }
+        if (p.norm) {
+          float s = 0.f, m = 0.f;
+          float ea[NU][V], eb[NU][V];
+#pragma unroll
+          for (int i = 0; i < NU; ++i)
+#pragma unroll
+            for (int j = 0; j < V; ++j) {
+              const bool ca = u.in[i] && u.counts_a(i, j), cb = u.in[i] && u.counts_b(i, j);
+              ea[i][j] = da[i][j] * (w == nullptr ? 1.f : w[u.a[i] + j]);
+              eb[i][j] = db[i][j] * (w == nullptr ? 1.f : w[u.b[i] + j]);
+              s += (ca ? a[i][j] * a[i][j] : 0.f) + (cb ? b[i][j] * b[i][j] : 0.f);
+              m += (ca ? a[i][j] * ea[i][j] : 0.f) + (cb ? b[i][j] * eb[i][j] : 0.f);
+            }
+          const float r = rsqrtf(team_sum(s, p.lgteam) * p.inv + p.eps);
+          m = team_sum(m, p.lgteam) * p.inv * r * r;
+          const bool own = mine < p.heads[k];
+#pragma unroll
+          for (int i = 0; i < NU; ++i)
+#pragma unroll
+            for (int j = 0; j < V; ++j) {
+              dwa[k][i][j] += own && u.in[i] && u.counts_a(i, j) ? da[i][j] * (a[i][j] * r) : 0.f;
+              dwb[k][i][j] += own && u.in[i] && u.counts_b(i, j) ? db[i][j] * (b[i][j] * r) : 0.f;
+              da[i][j] = r * (ea[i][j] - a[i][j] * m);
+              db[i][j] = r * (eb[i][j] - b[i][j] * m);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < NU; ++i) {
+          if (NU == 1 || u.in[i]) {
+            put<T, V, RAG>(dx + u.a[i], da[i]);
+            put<T, V, RAG>(dx + u.b[i], db[i]);
+          }
+        }
+      }
+    }
+  }
+  if (p.part == nullptr) return;
+  // over the wave's teams, then over the block's waves, in order
+  __syncthreads();
+  float* sum = reinterpret_cast<float*>(lds);
+#pragma unroll
+  for (int k = 0; k < 2; ++k)
+#pragma unroll
+    for (int i = 0; i < NU; ++i)
+#pragma unroll
+      for (int j = 0; j < V; ++j) {
+        float va = dwa[k][i][j], vb = dwb[k][i][j];
+        for (int d = team; d < 64; d *= 2) {
+          va += __shfl_xor(va, d);
+          vb += __shfl_xor(vb, d);
+        }
+        if (lane < team && u.in[i]) {
+          if (u.counts_a(i, j)) sum[(wave * 2 + k) * p.D + u.a[i] + j] = va;
+          if (u.counts_b(i, j)) sum[(wave * 2 + k) * p.D + u.b[i] + j] = vb;
+        }
+      }
+  __syncthreads();
+  for (int c = threadIdx.x; c < 2 * p.D; c += 256)
+    p.part[int64_t(blockIdx.x) * 2 * p.D + c] = (sum[c] + sum[2 * p.D + c]) + (sum[4 * p.D + c] + sum[6 * p.D + c]);
+}
+
+// ---------------------------------------------------------------- launches
+struct Plan {
+  int V, NU;
+  bool rag;
+  RopeP p;
+  int64_t blocks;
+};
+int lg2_up(int v) {
+  int l = 0;
+  while ((1 << l) < v) ++l;
+  return l;
+}
+bool whole(const void* p, int64_t ld, size_t e) { return p == nullptr || rows_aligned(p, ld, e, 16); }
+
+// The words: 16 bytes wherever both ranges of a head hold a unit of them, else single
+// elements.  Tokens over waves; with few tokens, their heads over several.
+Plan plan_of(const m3_qk_norm_rope_args& a, bool backward) {
+  Plan h{};
+  RopeP& p = h.p;
+  const size_t e = a.in_dtype == M3_BF16 ? 2 : 4;
+  const int word = int(16 / e), rest = a.D - a.R;
+  h.V = (a.R == 0 || a.R >= 2 * word) && (rest == 0 || rest >= 2 * word) ? word : 1;
+  h.rag = (a.R / 2) % word != 0 || rest % (2 * word) != 0;
+  p.rot_units = (a.R / 2 + h.V - 1) / h.V;
+  p.units = p.rot_units + (rest + 2 * h.V - 1) / (2 * h.V);
+  p.lgteam = lg2_up(p.units < 64 ? p.units : 64);
+  h.NU = (p.units + 63) / 64;
+  p.x[0] = a.q;
+  p.x[1] = a.k;
+  p.w[0] = a.q_w;
+  p.w[1] = a.k_w;
+  p.ld[0] = a.q_ld;
+  p.ld[1] = a.k_ld;
+  p.heads[0] = a.H;
+  p.heads[1] = a.Hk;
+  const int teams = 64 >> p.lgteam;
+  for (int i = 0; i < 2; ++i) p.its[i] = (p.heads[i] + teams - 1) / teams;
+  p.freqs = a.freqs;
+  p.positions = a.positions;
+  p.lengths = a.lengths;
+  p.rows = int64_t(a.Bt) * a.L;
+  p.L = a.L;
+  p.D = a.D;
+  p.R = a.R;
+  p.start = a.start;
+  p.norm = a.norm;
+  p.eps = a.eps;
+  p.inv = 1.f / float(a.D);
+  const int all = p.its[0] + p.its[1];
+  const int64_t want = (2048 + p.rows - 1) / p.rows;
+  p.splits = int(want < all ? want : all);
+  const int64_t most = backward ? 4096 : 1 << 20;
+  p.walkers = p.rows < most ? p.rows : most;
+  h.blocks = (p.walkers * p.splits + 3) / 4;
+  return h;
+}
+template <typename T, int V, int NU, bool RAG, bool ADJ>
+hipError_t launch_one(const Plan& h, bool backward, hipStream_t s) {
+  const dim3 grid(uint32_t(h.blocks)), block(256);
+  const size_t table = size_t(4) * (h.p.R / 2) * sizeof(float2);
+  if (!backward) {
+    rope_kernel<T, V, NU, RAG, ADJ><<<grid, block, table, s>>>(h.p);
+  } else {
+    const size_t sums = size_t(8) * h.p.D * 4;
+    rope_backward_kernel<T, V, NU, RAG, ADJ><<<grid, block, table > sums ? table : sums, s>>>(h.p);
+  }
+  return hipGetLastError();
+}
+template <typename T, int W, bool ADJ>
+hipError_t launch_any(const Plan& h, bool backward, hipStream_t s) {
+  if (h.V == 1) return h.NU == 1 ? launch_one<T, 1, 1, false, ADJ>(h, backward, s) : launch_one<T, 1, 8, false, ADJ>(h, backward, s);
+  if constexpr (W == 4) {
+    if (h.NU == 2) return h.rag ? launch_one<T, W, 2, true, ADJ>(h, backward, s) : launch_one<T, W, 2, false, ADJ>(h, backward, s);
+  }
+  return h.rag ? launch_one<T, W, 1, true, ADJ>(h, backward, s) : launch_one<T, W, 1, false, ADJ>(h, backward, s);
+}
+hipError_t launch(const m3_qk_norm_rope_args& a, const Plan& h, bool backward, hipStream_t s) {
+  if (a.in_dtype == M3_BF16) return a.adjacent ? launch_any<bf16_t, 8, true>(h, backward, s) : launch_any<bf16_t, 8, false>(h, backward, s);
+  return a.adjacent ? launch_any<float, 4, true>(h, backward, s) : launch_any<float, 4, false>(h, backward, s);
+}
+
+}  // namespace
+
+hipError_t launch_rope(const m3_qk_norm_rope_args& a, hipStream_t s) {
+  Plan h = plan_of(a, false);
+  const size_t e = a.in_dtype == M3_BF16 ? 2 : 4;
+  h.p.y[0] = a.q_out;
+  h.p.y[1] = a.k_out;
+  h.rag = h.rag || (size_t(a.D) * e) % 16 != 0 || !whole(a.q, a.q_ld, e) || !whole(a.k, a.k_ld, e) || !whole(a.q_out, 0, e) ||
+          !whole(a.k_out, 0, e);
+  return launch(a, h, false, s);
+}
+
+size_t rope_backward_workspace(const m3_qk_norm_rope_backward_args& b) {
+  const m3_qk_norm_rope_args& a = b.fwd;
+  if (!a.norm) return 0;
+  return round256(size_t(plan_of(a, true).blocks) * 2 * a.D * 4);
+}
+
+hipError_t launch_rope_backward(const m3_qk_norm_rope_backward_args& b, hipStream_t s) {
+  const m3_qk_norm_rope_args& a = b.fwd;
+  Plan h = plan_of(a, true);
+  const size_t e = a.in_dtype == M3_BF16 ? 2 : 4;
+  h.p.y[0] = b.dq;
+  h.p.y[1] = b.dk;
+  h.p.dy[0] = b.dq_out;
+  h.p.dy[1] = b.dk_out;
+  const bool gains = b.dq_w != nullptr || b.dk_w != nullptr;
+  h.p.part = gains ? static_cast<float*>(b.workspace) : nullptr;
+  h.rag = h.rag || (size_t(a.D) * e) % 16 != 0 || !whole(a.q, a.q_ld, e) || !whole(a.k, a.k_ld, e) || !whole(b.dq, 0, e) ||
+          !whole(b.dk, 0, e) || !whole(b.dq_out, 0, e) || !whole(b.dk_out, 0, e);
+  const hipError_t err = launch(a, h, true, s);
+  if (err != hipSuccess || !gains) return err;
+  ColSum c{};
+  c.part = h.p.part;
+  c.P = h.blocks;
+  c.ncols = 2 * a.D;
+  c.dst[0] = b.dq_w;
+  c.dst[1] = b.dk_w;
+  c.n[0] = c.n[1] = a.D;
+  return launch_colsum(c, s);
+}
+
+}  // namespace m3

@@ -735,3 +735,168 @@ def m3_residual_norm_backward(h, x=None, w=None, scale=None, *, dy, dresidual=No
     workspace = _take_workspace("m3_residual_norm_backward", a, workspace, dev)
     _run_layer("m3_residual_norm_backward", a, dev)
     return out
+
+
+# ---------------------------------------------------------------- linear attention
+def _attention_inputs(a, dev, lead, q, k, v, log_decay, scale):
+    """The inputs that linear attention, its backward and its step share."""
+    t, n = q.dtype, len(lead)
+    H, K = q.shape[n:]
+    Hk, V = v.shape[n:]
+    if max(H, Hk, K, V, *lead) > _MAX:
+        _too_large(H, Hk, K, V, *lead)
+    a.H, a.Hk, a.K, a.V, a.in_dtype = H, Hk, K, V, _dtype_code(q)
+    a.scale = (K ** -0.5 if K else 0.0) if scale is None else scale
+    a.q, a.q_ld = _rows(q, t, (*lead, H, K), n, "q", dev)
+    a.k, a.k_ld = _rows(k, t, (*lead, Hk, K), n, "k", dev)
+    a.v, a.v_ld = _rows(v, t, (*lead, Hk, V), n, "v", dev)
+    a.log_decay = _dense(log_decay, _F32, (H,), "log_decay", dev)
+    return H, Hk, K, V
+
+
+@_scoped
+def m3_linear_attention(q, k, v, log_decay, h0=None, *, scale=None, lengths=None, y=None, h_final=None, want_state=True,
+                        workspace=None):
+    """Linear attention with a constant decay for each head:
+    S_t = exp(log_decay[h]) S_{t-1} + k_t v_t^T,  y_t = scale q_t^T S_t.
+    q [Bt, L, H, K], k [Bt, L, Hk, K], v [Bt, L, Hk, V] (bf16 or fp32; tokens may be
+    slices of wider rows; H / Hk heads of q share one of k and v), K and V in
+    1..256; log_decay [H], h0 [Bt, H, K, V] fp32; scale: K^-1/2 if None; lengths
+    [Bt] int32.  workspace: a uint8 device tensor, None to allocate one when the
+    library asks for it, or False to run without (token axis not cut).  Returns a
+    dict with y [Bt, L, H, V] (rows behind an item's length are left as they
+    were) and h: the last state [Bt, H, K, V] (h_final may be `h0` itself)."""
+    Bt, L = q.shape[:2]
+    dev, t = q.get_device(), q.dtype
+    a = _lib.LinearAttentionArgs()
+    a.Bt, a.L = min(Bt, _MAX), min(L, _MAX)
+    H, _, K, V = _attention_inputs(a, dev, (Bt, L), q, k, v, log_decay, scale)
+    a.h0 = _dense(h0, _F32, (Bt, H, K, V), "h0", dev)
+    a.lengths = _dense(lengths, torch.int32, (Bt,), "lengths", dev)
+    y, a.y = _out(y, t, (Bt, L, H, V), "y", q, dev)
+    if want_state or h_final is not None:
+        h_final, a.h_final = _out(h_final, _F32, (Bt, H, K, V), "h_final", q if h0 is None else h0, dev)
+    if workspace is not False:
+        workspace = _take_workspace("m3_linear_attention", a, workspace, dev)
+    _run_layer("m3_linear_attention", a, dev)
+    return dict(y=y, h=h_final)
+
+
+@_scoped
+def m3_linear_attention_step(h, q, k, v, log_decay, *, scale=None, y=None, h_out=None):
+    """One token of m3_linear_attention: q [Bt, H, K], k [Bt, Hk, K], v [Bt, Hk, V],
+    h [Bt, H, K, V] fp32 updated in place (or read only, the new state going to
+    h_out).  Returns y [Bt, H, V]."""
+    Bt = q.shape[0]
+    dev = h.get_device()
+    a = _lib.LinearAttentionStepArgs()
+    a.Bt = min(Bt, _MAX)
+    H, _, K, V = _attention_inputs(a, dev, (Bt,), q, k, v, log_decay, scale)
+    a.h = _dense(h, _F32, (Bt, H, K, V), "h", dev)
+    a.h_out = _dense(h_out, _F32, (Bt, H, K, V), "h_out", dev)
+    y, a.y = _out(y, q.dtype, (Bt, H, V), "y", q, dev)
+    _run_layer("m3_linear_attention_step", a, dev)
+    return y
+
+
+@_scoped
+def m3_linear_attention_backward(q, k, v, log_decay, h0=None, *, dy, dh_final=None, scale=None, lengths=None,
+                                 want_carry_grads=False, workspace=None, out=None):
+    """Gradients of m3_linear_attention for dy [Bt, L, H, V] (dense) and dh_final
+    [Bt, H, K, V].  Returns a dict with dq, dk, dv (zero behind an item's length)
+    and, with want_carry_grads, dh0.  log_decay is a constant.  `out`: optional
+    dict of preallocated tensors."""
+    Bt, L = q.shape[:2]
+    dev, t = q.get_device(), q.dtype
+    got = out or {}
+    a = _lib.LinearAttentionBackwardArgs()
+    a.fwd.Bt, a.fwd.L = min(Bt, _MAX), min(L, _MAX)
+    H, Hk, K, V = _attention_inputs(a.fwd, dev, (Bt, L), q, k, v, log_decay, scale)
+    state = (Bt, H, K, V)
+    a.fwd.h0 = _dense(h0, _F32, state, "h0", dev)
+    a.fwd.lengths = _dense(lengths, torch.int32, (Bt,), "lengths", dev)
+    a.dy = _dense(dy, t, (Bt, L, H, V), "dy", dev)
+    a.dh_final = _dense(dh_final, _F32, state, "dh_final", dev)
+    out = dict(dq=None, dk=None, dv=None, dh0=None)
+    out["dq"], a.dq = _out(got.get("dq"), t, (Bt, L, H, K), "dq", q, dev)
+    out["dk"], a.dk = _out(got.get("dk"), t, (Bt, L, Hk, K), "dk", k, dev)
+    out["dv"], a.dv = _out(got.get("dv"), t, (Bt, L, Hk, V), "dv", v, dev)
+    if want_carry_grads or "dh0" in got:
+        out["dh0"], a.dh0 = _out(got.get("dh0"), _F32, state, "dh0", q if h0 is None else h0, dev)
+    workspace = _take_workspace("m3_linear_attention_backward", a, workspace, dev)
+    _run_layer("m3_linear_attention_backward", a, dev)
+    return out
+
+
+def _rope_inputs(a, dev, q, k, q_w, k_w, freqs, positions, start, lengths, eps, norm, adjacent):
+    """The inputs that the norm and rotation and its backward share."""
+    Bt, L, H, D = q.shape
+    t, Hk = q.dtype, 0 if k is None else k.shape[2]
+    R = 0 if freqs is None else 2 * freqs.shape[0]
+    if max(Bt, L, H, Hk, D, R) > _MAX:
+        _too_large(Bt, L, H, Hk, D, R)
+    if not -_MAX <= start <= _MAX:
+        _too_large(abs(start))
+    if k is None and k_w is not None:
+        raise ValueError("k_w without k")
+    a.Bt, a.L, a.H, a.Hk, a.D, a.R, a.in_dtype = Bt, L, H, Hk, D, R, _dtype_code(q)
+    a.norm, a.adjacent, a.start, a.eps = 1 if norm else 0, 1 if adjacent else 0, start, eps
+    a.q, a.q_ld = _rows(q, t, (Bt, L, H, D), 2, "q", dev)
+    a.k, a.k_ld = _rows(k, t, (Bt, L, Hk, D), 2, "k", dev)
+    a.q_w = _dense(q_w, _F32, (D,), "q_w", dev)
+    a.k_w = _dense(k_w, _F32, (D,), "k_w", dev)
+    a.freqs = _dense(freqs, _F32, (R // 2,), "freqs", dev)
+    a.positions = _dense(positions, torch.int32, (Bt, L), "positions", dev)
+    a.lengths = _dense(lengths, torch.int32, (Bt,), "lengths", dev)
+
+
+@_scoped
+def m3_qk_norm_rope(q, k=None, q_w=None, k_w=None, *, freqs=None, positions=None, start=0, lengths=None, eps=1e-6, norm=True,
+                    adjacent=False, q_out=None, k_out=None):
+    """RMS norm of queries and keys for each head and their rotation by position, in
+    one pass: n = x rsqrt(mean(x^2) + eps) w (norm=False: n = x), then the first
+    R = 2 len(freqs) elements in pairs (i, i + R/2), with `adjacent` (2i, 2i + 1):
+    y0 = n0 cos a - n1 sin a, y1 = n1 cos a + n0 sin a, a = position freqs[i].  q
+    [Bt, L, H, D], k [Bt, L, Hk, D] or None (bf16 or fp32; tokens may be slices of
+    wider rows), D in 1..1024; q_w, k_w [D], freqs [R/2] fp32 (None: no rotation);
+    positions [Bt, L] int32 (None: start + t); lengths [Bt] int32.  Returns a dict
+    with q and k (dense; rows behind an item's length are left as they were; q_out
+    and k_out may be q and k themselves where those are dense)."""
+    dev, t = q.get_device(), q.dtype
+    a = _lib.QkNormRopeArgs()
+    _rope_inputs(a, dev, q, k, q_w, k_w, freqs, positions, start, lengths, eps, norm, adjacent)
+    q_out, a.q_out = _out(q_out, t, q.shape, "q_out", q, dev)
+    if k is not None:
+        k_out, a.k_out = _out(k_out, t, k.shape, "k_out", k, dev)
+    elif k_out is not None:
+        raise ValueError("k_out without k")
+    _run_layer("m3_qk_norm_rope", a, dev)
+    return dict(q=q_out, k=k_out)
+
+
+@_scoped
+def m3_qk_norm_rope_backward(q, k=None, q_w=None, k_w=None, *, dq_out, dk_out=None, freqs=None, positions=None, start=0,
+                             lengths=None, eps=1e-6, norm=True, adjacent=False, workspace=None, out=None):
+    """Gradients of m3_qk_norm_rope for dq_out and dk_out (dense; the gradients of
+    its outputs).  Returns a dict with dq, dk (None without k; zero behind an
+    item's length), dq_w and dk_w (None where the gain is).  `out`: optional dict
+    of preallocated tensors; its dq and dk may be dq_out and dk_out themselves."""
+    dev, t = q.get_device(), q.dtype
+    got = out or {}
+    a = _lib.QkNormRopeBackwardArgs()
+    _rope_inputs(a.fwd, dev, q, k, q_w, k_w, freqs, positions, start, lengths, eps, norm, adjacent)
+    if (k is None) != (dk_out is None):
+        raise ValueError("dk_out goes with k")
+    a.dq_out = _dense(dq_out, t, q.shape, "dq_out", dev)
+    a.dk_out = None if k is None else _dense(dk_out, t, k.shape, "dk_out", dev)
+    out = dict(dq=None, dk=None, dq_w=None, dk_w=None)
+    out["dq"], a.dq = _out(got.get("dq"), t, q.shape, "dq", q, dev)
+    if k is not None:
+        out["dk"], a.dk = _out(got.get("dk"), t, k.shape, "dk", k, dev)
+    if q_w is not None:
+        out["dq_w"], a.dq_w = _out(got.get("dq_w"), _F32, q_w.shape, "dq_w", q_w, dev)
+    if k_w is not None:
+        out["dk_w"], a.dk_w = _out(got.get("dk_w"), _F32, k_w.shape, "dk_w", k_w, dev)
+    workspace = _take_workspace("m3_qk_norm_rope_backward", a, workspace, dev)
+    _run_layer("m3_qk_norm_rope_backward", a, dev)
+    return out
