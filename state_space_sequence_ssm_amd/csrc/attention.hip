@@ -10,9 +10,21 @@ int blocks32(int k) { return k <= 32 ? 1 : k <= 64 ? 2 : k <= 128 ? 4 : 8; }
 struct Shape {
   int kb, nct;
 };
-// Blocks of 128 columns where a state of them fits the registers, of 64 otherwise.
-Shape shape_of(int b_cols, int c_cols) { return {blocks32(b_cols), c_cols > 64 && b_cols <= 128 ? 2 : 1}; }
+int64_t units(const m3_linear_attention_args& a) { return int64_t(a.Bt) * a.H; }
+// Columns of c per block: 64 where eight waves share a block (bf16, a and b of up to 128), and
+// otherwise 128 where such a state fits the registers and `blocks` of them fill the card.
+bool two_roles(const m3_linear_attention_args& a, int b_cols) { return a.in_dtype == M3_BF16 && b_cols <= 128; }
+Shape shape_of(const m3_linear_attention_args& a, int b_cols, int c_cols, int64_t blocks, bool states) {
+  const bool wide = c_cols > 64 && b_cols <= 128 && blocks >= 256 && (states || !two_roles(a, b_cols));
+  return {blocks32(b_cols), wide ? 2 : 1};
+}
+Shape walk_shape(const m3_linear_attention_args& a, int b_cols, int c_cols) { return shape_of(a, b_cols, c_cols, units(a), false); }
 int tiles(int c_cols, Shape s) { return (c_cols + 64 * s.nct - 1) / (64 * s.nct); }
+// blocks per segment of the forward, and of the backward's three walks
+int64_t forward_blocks(const m3_linear_attention_args& a) { return units(a) * tiles(a.V, walk_shape(a, a.K, a.V)); }
+int64_t backward_blocks(const m3_linear_attention_args& a) {
+  return units(a) * (2 * tiles(a.K, walk_shape(a, a.V, a.K)) + tiles(a.V, walk_shape(a, a.K, a.V)));
+}
 
 // Segments of the token axis: enough blocks for the card, each of 256 tokens at least.
 void segments(int64_t blocks, int L, int& len, int& segs) {
@@ -32,12 +44,12 @@ size_t states_bytes(const m3_linear_attention_args& a, int segs) {
 }
 Cut forward_cut(const m3_linear_attention_args& a) {
   Cut c;
-  segments(int64_t(a.Bt) * a.H * tiles(a.V, shape_of(a.K, a.V)), a.L, c.len, c.segs);
+  segments(forward_blocks(a), a.L, c.len, c.segs);
   return c;
 }
 Cut backward_cut(const m3_linear_attention_args& a) {
   Cut c;
-  segments(int64_t(a.Bt) * a.H * (2 * tiles(a.K, shape_of(a.V, a.K)) + tiles(a.V, shape_of(a.K, a.V))), a.L, c.len, c.segs);
+  segments(backward_blocks(a), a.L, c.len, c.segs);
   return c;
 }
 
@@ -66,7 +78,6 @@ WalkJob job_of(const WalkSide& x, const WalkSide& b, const WalkSide& c, bool rev
   j.s = j.u = j.w = 1.f;
   j.sn = sn;
   j.sv = sv;
-  j.blocks = tiles(c.cols, shape_of(b.cols, c.cols));
   return j;
 }
 void to(WalkJob& j, void* out, bool f32, size_t elem) {
@@ -75,9 +86,11 @@ void to(WalkJob& j, void* out, bool f32, size_t elem) {
   const size_t word = 4 * (f32 ? 4 : elem);
   j.out_words = j.c.cols % 4 == 0 && reinterpret_cast<uintptr_t>(out) % word == 0;
 }
-hipError_t run(const m3_linear_attention_args& a, const WalkPlan& p, bool states_only, hipStream_t s) {
-  const Shape h = shape_of(p.job[0].b.cols, p.job[0].c.cols);
-  return a.in_dtype == M3_BF16 ? launch_walk_bf16(p, h.kb, h.nct, states_only, s) : launch_walk_f32(p, h.kb, h.nct, states_only, s);
+hipError_t run(const m3_linear_attention_args& a, WalkPlan& p, bool states, hipStream_t s) {
+  const WalkJob& f = p.job[0];  // the others' states have its shape
+  const Shape h = states ? shape_of(a, f.b.cols, f.c.cols, units(a) * (p.segs - 1) * p.jobs, true) : walk_shape(a, f.b.cols, f.c.cols);
+  for (int i = 0; i < p.jobs; ++i) p.job[i].blocks = tiles(p.job[i].c.cols, h);
+  return a.in_dtype == M3_BF16 ? launch_walk_bf16(p, h.kb, h.nct, states, s) : launch_walk_f32(p, h.kb, h.nct, states, s);
 }
 
 // ---------------------------------------------------------------- joins
@@ -233,8 +246,8 @@ StepShape step_shape(const m3_linear_attention_step_args& a) {
 // ---------------------------------------------------------------- entry points
 bool attention_fits(const m3_linear_attention_args& a) {
   const Cut c = forward_cut(a);
-  const int64_t units = int64_t(a.Bt) * a.H;
-  return launchable(units * c.segs * tiles(a.V, shape_of(a.K, a.V)), 256) && launchable(units * ((a.K * a.V + 255) / 256), 256);
+  const int64_t u = units(a);
+  return launchable(forward_blocks(a) * c.segs * 2, 512) && launchable(u * ((a.K * a.V + 255) / 256), 256);
 }
 size_t attention_workspace(const m3_linear_attention_args& a) { return states_bytes(a, forward_cut(a).segs); }
 
@@ -278,10 +291,9 @@ hipError_t launch_attention_step(const m3_linear_attention_step_args& a, hipStre
 bool attention_backward_fits(const m3_linear_attention_backward_args& b) {
   const m3_linear_attention_args& a = b.fwd;
   const Cut c = backward_cut(a);
-  const int64_t units = int64_t(a.Bt) * a.H;
-  const int64_t walk = units * c.segs * (2 * tiles(a.K, shape_of(a.V, a.K)) + tiles(a.V, shape_of(a.K, a.V)));
+  const int64_t u = units(a);
   const int64_t most = a.K > a.V ? a.K : a.V;
-  return launchable(walk, 256) && launchable(2 * units * ((a.K * a.V + 255) / 256), 256) &&
+  return launchable(backward_blocks(a) * c.segs * 2, 512) && launchable(2 * u * ((a.K * a.V + 255) / 256), 256) &&
          launchable(int64_t(a.Bt) * a.L * a.Hk * most / 256 + 1, 256);
 }
 // Workspace: the states in front of every segment, of the forward and of the reverse walk, and
@@ -332,7 +344,7 @@ hipError_t launch_attention_backward(const m3_linear_attention_backward_args& b,
     if (e != hipSuccess) return e;
   }
   WalkPlan p = plan_of(a, c);
-  const Shape sk = shape_of(a.V, a.K), sv = shape_of(a.K, a.V);
+  const Shape sk = walk_shape(a, a.V, a.K), sv = walk_shape(a, a.K, a.V);
   p.job[0] = jk;
   p.job[1] = jq;
   p.job[2] = jv;

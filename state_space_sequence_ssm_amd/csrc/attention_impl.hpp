@@ -2,6 +2,7 @@
 // matrix cores: y, dq, dk and dv, and the states of segments.
 #pragma once
 #include <atomic>
+#include <type_traits>
 
 #include "m3ssm_internal.hpp"
 #include "mixer_internal.hpp"
@@ -25,31 +26,24 @@ struct Op<bf16_t> {
   typedef u32x2 half;  // 4 positions
   static constexpr int kWord = 8;
   // scores in 2, states read in 2 and their updates' weights in 3 bf16 parts: 16 and 24
-  // bits, so that what a product adds to the outputs' own rounding (2^-9) and to the fp32
+  // bits, so that what a product adds to the outputs' own rounding (2^-8) and to the fp32
   // state is below either
   static constexpr int kScore = 2, kState = 2, kWeight = 3;
+  // Rows of D elements, padded by 32 bytes, so that 8 bytes of 4 columns of each of 8 rows (a
+  // transposing read) meet every bank once; and every address is a lane's own plus a constant.
   template <int D>
-  static __device__ __forceinline__ int at(int r, int c) {  // 8-byte units swizzled by row, as the core's prefill
-    const int r0 = r & 1, r1 = (r >> 1) & 1, r2 = (r >> 2) & 1, r3 = (r >> 3) & 1;
-    int x;
-    if constexpr (D >= 128) x = ((r0 ^ r3) << 1) | (r1 << 2) | (r2 << 3) | (r0 << 4);
-    else if constexpr (D == 64) x = ((r0 ^ r3) << 1) | (r1 << 2) | (r2 << 3);
-    else x = ((r1 ^ r3) << 1) | (r2 << 2);
-    return r * D + (((c >> 2) ^ x) << 2);
-  }
-  template <int D>
-  static constexpr int size() { return kChunk * D * 2; }
+  static constexpr int stride() { return D + 16; }
   // row r, contracted positions of the block pair at column c
-  template <int D>
-  static __device__ __forceinline__ frag row(const elem* t, int r, int c, int g) {
-    return cat8(*reinterpret_cast<const u32x2*>(t + at<D>(r, c + 4 * g)),
-                *reinterpret_cast<const u32x2*>(t + at<D>(r, c + 16 + 4 * g)));
+  template <int S>
+  static __device__ __forceinline__ frag row(const elem* t, int r, int c, int lane) {
+    const elem* p = t + ((lane & 15) * S + (lane >> 4) * 4) + (r * S + c);
+    return cat8(*reinterpret_cast<const u32x2*>(p), *reinterpret_cast<const u32x2*>(p + 16));
   }
   // column c + l16, contracted positions: rows of the block pair at row r
-  template <int D>
+  template <int S>
   static __device__ __forceinline__ frag col(const elem* t, int r, int c, int lane) {
-    const int rr = r + (lane >> 4) * 4 + ((lane & 15) >> 2), cc = c + (lane & 3) * 4;
-    return cat8(lds_read_tr(t + at<D>(rr, cc)), lds_read_tr(t + at<D>(rr + 16, cc)));
+    const elem* p = t + (((lane >> 4) * 4 + ((lane & 15) >> 2)) * S + (lane & 3) * 4) + (r * S + c);
+    return cat8(lds_read_tr(p), lds_read_tr(p + 16 * S));
   }
   static __device__ __forceinline__ f32x4 mma(frag a, frag b, f32x4 c) { return m3::mma(a, b, c); }
   static __device__ __forceinline__ frag join(half lo, half hi) { return cat8(lo, hi); }
@@ -83,21 +77,20 @@ struct Op<float> {
   // rows 4 words apart from a multiple of 64 banks' worth: whole rows, columns and words
   // are read and written without conflicts
   template <int D>
-  static __device__ __forceinline__ int at(int r, int c) { return r * (D + 4) + c; }
-  template <int D>
-  static constexpr int size() { return kChunk * (D + 4) * 4; }
-  template <int D>
-  static __device__ __forceinline__ frag row(const elem* t, int r, int c, int g) {
-    return {*reinterpret_cast<const f32x4*>(t + at<D>(r, c + 4 * g)), *reinterpret_cast<const f32x4*>(t + at<D>(r, c + 16 + 4 * g))};
+  static constexpr int stride() { return D + 4; }
+  template <int S>
+  static __device__ __forceinline__ frag row(const elem* t, int r, int c, int lane) {
+    const elem* p = t + ((lane & 15) * S + (lane >> 4) * 4) + (r * S + c);
+    return {*reinterpret_cast<const f32x4*>(p), *reinterpret_cast<const f32x4*>(p + 16)};
   }
-  template <int D>
+  template <int S>
   static __device__ __forceinline__ frag col(const elem* t, int r, int c, int lane) {
-    const elem* q = t + at<D>(r + (lane >> 4) * 4, c + (lane & 15));
+    const elem* p = t + ((lane >> 4) * 4 * S + (lane & 15)) + (r * S + c);
     frag f;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      f.lo[i] = q[at<D>(i, 0)];
-      f.hi[i] = q[at<D>(16 + i, 0)];
+      f.lo[i] = p[i * S];
+      f.hi[i] = p[(16 + i) * S];
     }
     return f;
   }
@@ -126,47 +119,96 @@ struct Op<float> {
 // l^d for whole d >= 0: 1 at 0 also where l = 0
 __device__ __forceinline__ float power(float g2, int d) { return d == 0 ? 1.f : __builtin_amdgcn_exp2f(g2 * float(d)); }
 
-// ---------------------------------------------------------------- one tile on its way
-// 64 rows of D elements (columns past `cols` and rows past n zero) from the tokens of a
-// chunk into LDS, 16-byte words over 256 threads.
+// Tiles in LDS: where the words of 16 bytes of row r from column c on go.  Padded rows, for
+// the one-phase walk; rows swizzled by XOR as its a and as its b and c, for the two-role walk.
 template <typename T, int D>
+struct Padded {
+  typedef typename Op<T>::elem elem;
+  static constexpr int S = Op<T>::template stride<D>(), kBytes = kChunk * S * int(sizeof(elem));
+  static __device__ __forceinline__ void put(elem* t, int r, int c, u32x4 w) { *reinterpret_cast<u32x4*>(t + r * S + c) = w; }
+};
+constexpr int shift_of(int D) { return D >= 128 ? 0 : D == 64 ? 1 : 2; }
+// a: operands of 8 positions lie together, 16 bytes; 16 rows of one meet every bank once
+template <int D>
+struct SwizzledA {
+  static constexpr int kBytes = kChunk * D * 2;
+  static __device__ __forceinline__ int mix(int r) { return (r & 15) >> shift_of(D); }
+  static __device__ __forceinline__ void put(uint16_t* t, int r, int c, u32x4 w) {
+    const int u = c / 32 * 4 + (c & 8) / 4, h = (c & 16) / 4;  // units of columns c.. and c + 4..
+    *reinterpret_cast<u32x2*>(t + r * D + (u ^ mix(r)) * 8 + h) = u32x2{w[0], w[1]};
+    *reinterpret_cast<u32x2*>(t + r * D + ((u + 1) ^ mix(r)) * 8 + h) = u32x2{w[2], w[3]};
+  }
+  // a lane's element offset of the operand of row l16 at block pair R
+  static __device__ __forceinline__ int row(int R, int lane) { return (lane & 15) * D + ((4 * R + (lane >> 4)) ^ mix(lane & 15)) * 8; }
+};
+// b and c: units of 8 bytes; 16 rows of two of them, and 8 rows of four, meet every bank once
+template <int D>
+struct SwizzledB {
+  static constexpr int kBytes = kChunk * D * 2;
+  static __device__ __forceinline__ int mix(int r) { return (((r & 7) >> shift_of(D)) << 2) | ((r >> 3 & 1) << 1); }
+  static __device__ __forceinline__ void put(uint16_t* t, int r, int c, u32x4 w) {
+    *reinterpret_cast<u32x4*>(t + r * D + ((c / 4) ^ mix(r)) * 4) = w;
+  }
+  static __device__ __forceinline__ int row(int c, int lane) { return (lane & 15) * D + ((c / 4 + (lane >> 4)) ^ mix(lane & 15)) * 4; }
+  // where the lane points for a transposing read of columns c..c + 15, rows 4 g + 0..3 of 16
+  static __device__ __forceinline__ int col(int c, int lane) {
+    const int r = (lane >> 4) * 4 + ((lane & 15) >> 2);
+    return r * D + ((c / 4 + (lane & 3)) ^ mix(r)) * 4;
+  }
+};
+
+// 64 tokens' rows of D elements (columns past the head's and rows past the chunk's zero) on
+// their way through registers into LDS, 16-byte words over 256 threads.  Rows are loaded in
+// the tokens' order and stored in the walk's.
+template <typename T, int D, typename To>
 struct Tile {
-  static constexpr int W = Op<T>::kWord, kRow = D / W, N = kChunk * kRow / 256;
-  static_assert(N >= 1, "a word per thread at least");
+  typedef typename Op<T>::elem elem;
+  static constexpr int W = Op<T>::kWord, kRow = D / W, kRows = 256 / kRow, N = kChunk / kRows;
+  static_assert(N >= 1 && 256 % kRow == 0, "whole rows over the block");
   u32x4 w[N];
-  // base: head's elements of position 0 of the chunk; step: elements to the next position
-  __device__ __forceinline__ void load(const T* base, int64_t step, int n, int cols, bool words) {
+  const T* base;  // the head's elements of the chunk's first token
+  uint32_t at;    // this thread's bytes from there
+  int r0, c0;     // its first row and its column
+  __device__ __forceinline__ void place(const T* first, int64_t ld, int cols, int thread) {
+    base = first;
+    r0 = thread / kRow;
+    c0 = thread % kRow * W;
+    at = (uint32_t(r0) * uint32_t(ld) + uint32_t(c0 < cols ? c0 : 0)) * uint32_t(sizeof(T));
+  }
+  // a whole chunk of whole words; columns past the head's are others' here, and zeroed when stored
+  __device__ __forceinline__ void load(int64_t ld) {
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+      w[i] = *reinterpret_cast<const u32x4*>(reinterpret_cast<const char*>(base + int64_t(i * kRows) * ld) + at);
+  }
+  // n tokens, any words
+  __device__ __forceinline__ void load_any(int64_t ld, int n, int cols) {
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-      const int at = i * 256 + int(threadIdx.x), r = at / kRow, c = at % kRow * W;
-      const bool in = r < n && c < cols;
-      const T* p = base + (in ? r : 0) * step + (in ? c : 0);
-      if (words) {
-        w[i] = *reinterpret_cast<const u32x4*>(p);
-      } else {
-        const int left = in ? cols - c : 0;
-        Pack<T, W> q;
-        if (left >= W) q = load_loose<T, W>(p);
-        else q = load_some<T, W>(p, left);
-        __builtin_memcpy(&w[i], &q, 16);
-      }
-      if (!in) w[i] = u32x4{0, 0, 0, 0};
+      const int r = i * kRows + r0, left = r < n ? cols - c0 : 0;
+      const T* p = base + int64_t(r < n ? r : 0) * ld + (left > 0 ? c0 : 0);
+      Pack<T, W> q;
+      if (left >= W) q = load_loose<T, W>(p);
+      else q = load_some<T, W>(p, left);
+      __builtin_memcpy(&w[i], &q, 16);
     }
   }
-  __device__ __forceinline__ void store(typename Op<T>::elem* t) const {
+  __device__ __forceinline__ void store(elem* t, int n, int cols, bool rev) {
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-      const int at = i * 256 + int(threadIdx.x), r = at / kRow, c = at % kRow * W;
-      *reinterpret_cast<u32x4*>(t + Op<T>::template at<D>(r, c)) = w[i];
+      const int r = i * kRows + r0;
+      if (cols < D) w[i] = c0 < cols ? w[i] : u32x4{0, 0, 0, 0};
+      To::put(t, rev && r < n ? n - 1 - r : r, c0, w[i]);
     }
   }
 };
 
-template <typename T>
-__device__ __forceinline__ void put4(const WalkJob& j, T* out, int64_t at, f32x4 v, int n) {
-  if (j.out_f32 || sizeof(T) == 4) {
-    float* o = reinterpret_cast<float*>(out) + at;
-    if (j.out_words && n >= 4) {
+// Four consecutive columns of the output, n of them within the head.
+template <typename T, bool FAST>
+__device__ __forceinline__ void put4(bool f32, bool words, char* out, uint32_t at, f32x4 v, int n) {
+  if (sizeof(T) == 4 || f32) {
+    float* o = reinterpret_cast<float*>(out + at * 4u);
+    if (FAST || (words && n >= 4)) {
       *reinterpret_cast<f32x4*>(o) = v;
     } else {
 #pragma unroll
@@ -174,8 +216,8 @@ __device__ __forceinline__ void put4(const WalkJob& j, T* out, int64_t at, f32x4
         if (i < n) o[i] = v[i];
     }
   } else {
-    T* o = out + at;
-    if (j.out_words && n >= 4) {
+    T* o = reinterpret_cast<T*>(out + at * uint32_t(sizeof(T)));
+    if (FAST || (words && n >= 4)) {
       store4<T>(o, v[0], v[1], v[2], v[3]);
     } else {
 #pragma unroll
@@ -185,115 +227,250 @@ __device__ __forceinline__ void put4(const WalkJob& j, T* out, int64_t at, f32x4
   }
 }
 
-// One block of 4 waves walks one segment of one (item, head) for 64 NCT columns of c: wave w
-// holds columns 16 NCT w.. of the state, all 32 KB rows of it, in accumulators.
-//   A: tiles of a, b, c into LDS.  B: the triangle's 10 score tiles, dealt over the waves, weighted by
-//   l^(p-j) and handed round through LDS; a E from the state.  C: scores times c, out, the state.
+// ---------------------------------------------------------------- what a block walks
+// One segment of one (item, head) for V columns of c: 4 waves hold V / 4 columns of the state
+// each, all its rows, in accumulators.
+template <typename T, int V, bool STATES>
+struct Place {
+  const WalkPlan& plan;
+  const WalkJob& j;
+  int vt, unit, seg, item, h, n, from, to, v0, vc, chunks, rest;
+  bool rev, last_seg, idle;
+  float g2;
+  int64_t per;
+  static __device__ __forceinline__ int job_of(const WalkPlan& plan, int64_t& id) {
+    const int units = plan.Bt * plan.H, segs = STATES ? plan.segs - 1 : plan.segs;
+    int ji = 0;
+    while (ji + 1 < plan.jobs && id >= int64_t(plan.job[ji].blocks) * units * segs) {
+      id -= int64_t(plan.job[ji].blocks) * units * segs;
+      ++ji;
+    }
+    return ji;
+  }
+  __device__ __forceinline__ Place(const WalkPlan& p, int64_t id) : plan(p), j(p.job[job_of(p, id)]) {
+    const int units = plan.Bt * plan.H;
+    vt = int(id % j.blocks);
+    unit = int(id / j.blocks % units);
+    seg = int(id / j.blocks / units);
+    item = unit / plan.H;
+    h = unit % plan.H;
+    n = item_length(plan.lengths, item, plan.L);
+    from = seg * plan.seg_len;
+    to = min(n, from + plan.seg_len);
+    v0 = vt * V;
+    vc = min(j.c.cols - v0, V);
+    rev = j.rev != 0;
+    g2 = plan.log_decay[h] * 1.4426950408889634f;
+    per = int64_t(j.b.cols) * j.c.cols;
+    last_seg = from + plan.seg_len >= n;  // of this item
+    idle = STATES ? last_seg : (from >= n && seg > 0);
+    chunks = to > from ? (to - from + kChunk - 1) / kChunk : 0;
+    rest = to - from - (chunks - 1) * kChunk;
+  }
+  __device__ __forceinline__ int held(int k) const { return k + 1 < chunks ? kChunk : rest; }
+  // the first token in memory of chunk k
+  __device__ __forceinline__ int64_t token(int k) const {
+    return int64_t(item) * plan.L + (rev ? n - from - k * kChunk - held(k) : from + k * kChunk);
+  }
+  __device__ __forceinline__ const T* head(const WalkSide& s) const {
+    return static_cast<const T*>(s.p) + int64_t(h / (plan.H / s.heads)) * s.cols;
+  }
+  // zeros into the output's rows behind the item's tokens
+  __device__ __forceinline__ void zero_tail(int threads) const {
+    const int first = max(n, from), last = min(plan.L, from + plan.seg_len);
+    T* o = static_cast<T*>(j.out);
+    for (int64_t i = threadIdx.x; i < int64_t(last - first) * vc; i += threads)
+      o[((int64_t(item) * plan.L + first + i / vc) * plan.H + h) * j.c.cols + v0 + i % vc] = T{};
+  }
+  // the state's columns 16 (wave NCT + ct) + l16, rows 16 r + 4 g + i
+  template <int NR, int NCT>
+  __device__ __forceinline__ void start(f32x4 (&E)[NR][NCT], int wave, int lane) const {
+    const float* init = nullptr;
+    if constexpr (!STATES) init = plan.segs > 1 ? j.states + (int64_t(unit) * plan.segs + seg) * per : j.init == nullptr ? nullptr : j.init + unit * per;
+#pragma unroll
+    for (int r = 0; r < NR; ++r)
+#pragma unroll
+      for (int ct = 0; ct < NCT; ++ct) {
+        const int v = 16 * (wave * NCT + ct) + (lane & 15);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int row = 16 * r + 4 * (lane >> 4) + i;
+          E[r][ct][i] = init != nullptr && row < j.b.cols && v < vc ? init[row * j.sn + (v0 + v) * j.sv] : 0.f;
+        }
+      }
+  }
+  template <int NR, int NCT>
+  __device__ __forceinline__ void finish(const f32x4 (&E)[NR][NCT], int wave, int lane) const {
+    float* fin = STATES ? j.states + (int64_t(unit) * plan.segs + seg + 1) * per : last_seg && j.fin != nullptr ? j.fin + unit * per : nullptr;
+    if (fin == nullptr) return;
+#pragma unroll
+    for (int r = 0; r < NR; ++r)
+#pragma unroll
+      for (int ct = 0; ct < NCT; ++ct) {
+        const int v = 16 * (wave * NCT + ct) + (lane & 15);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int row = 16 * r + 4 * (lane >> 4) + i;
+          if (row < j.b.cols && v < vc) fin[row * j.sn + (v0 + v) * j.sv] = E[r][ct][i];
+        }
+      }
+  }
+  // chunks in front of this one are whole ones of whole words
+  __device__ __forceinline__ int quick() const {
+    const bool words = (STATES || (j.a.words && j.out_words && vc == V)) && j.b.words && j.c.words;
+    return words ? (rest == kChunk ? chunks : chunks - 1) : 0;
+  }
+};
+
+// Weights l^(p - j) s of a triangle's tiles (rows j = 4 g + i, columns p = l16), and l^(p + e) w.
+struct Powers {
+  float near[4], far[4], out[4], far2, far3;
+  __device__ __forceinline__ Powers(float g2, const WalkJob& j, int lane) {
+    const int g = lane >> 4, l16 = lane & 15;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int d = l16 - 4 * g - i;
+      near[i] = d < 0 ? 0.f : j.s * power(g2, d);
+      far[i] = j.s * power(g2, 16 + d);
+      out[i] = j.w * power(g2, 16 * i + l16 + j.e);
+    }
+    far2 = power(g2, 16);
+    far3 = power(g2, 32);
+  }
+  // scores of tiles `apart` apart
+  __device__ __forceinline__ f32x4 weigh(f32x4 s, int apart, int lane) const {
+    const float f = apart == 3 ? far3 : apart == 2 ? far2 : 1.f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float v = s[i] * (apart == 0 ? near[i] : far[i] * f);
+      s[i] = apart == 0 && (lane & 15) < 4 * (lane >> 4) + i ? 0.f : v;
+    }
+    return s;
+  }
+};
+// The triangle's 10 tiles (tt, jt <= tt) in order, and the 6 operands of 32 positions they
+// make: pair_of(tt, jt / 2); the second halves of (0, 0) and (2, 1) are empty.
+__device__ __forceinline__ int column_of(int tile) { return tile < 1 ? 0 : tile < 3 ? 1 : tile < 6 ? 2 : 3; }
+constexpr __host__ __device__ int pair_of(int tt, int m) { return (tt * (tt + 2) + 1) / 4 + m; }
+
+// u l^(n - e - i) for the tokens of a whole chunk and of the last one
+__device__ __forceinline__ void put_weights(float* sw, float g2, const WalkJob& j, int rest) {
+  if (threadIdx.x < 2 * kChunk) {
+    const int i = threadIdx.x % kChunk, nc = threadIdx.x < kChunk ? kChunk : rest;
+    sw[threadIdx.x] = j.u * power(g2, max(0, nc - j.e - i));
+  }
+}
+// c's operands of 32 tokens times their weights, in parts
+template <typename O, int NW>
+__device__ __forceinline__ void weigh_column(typename O::frag f, f32x4 wl, f32x4 wh, typename O::frag (&o)[NW]) {
+  float v[8];
+  O::values(f, v);
+  typename O::half lo[NW], hi[NW];
+  O::template split<NW>(wl * f32x4{v[0], v[1], v[2], v[3]}, lo);
+  O::template split<NW>(wh * f32x4{v[4], v[5], v[6], v[7]}, hi);
+#pragma unroll
+  for (int q = 0; q < NW; ++q) o[q] = O::join(lo[q], hi[q]);
+}
+// e(R): the state's rows of block pair R as an operand, in parts
+template <typename O, int NE>
+__device__ __forceinline__ void state_operand(f32x4 a, f32x4 b, typename O::frag (&o)[NE]) {
+  typename O::half lo[NE], hi[NE];
+  O::template split<NE>(a, lo);
+  O::template split<NE>(b, hi);
+#pragma unroll
+  for (int q = 0; q < NE; ++q) o[q] = O::join(lo[q], hi[q]);
+}
+
+// ---------------------------------------------------------------- one-phase walk
+// 4 waves, 64 NCT columns: tiles into LDS; scores, dealt over the waves, and the state's part;
+// scores times c, out, and the state behind the chunk.  For segments' states, for fp32, and for
+// a and b of more than 128 elements, whose tiles leave LDS no room for two chunks.
 template <typename T, int KB, int NCT, bool STATES>
 struct Lds {
   static constexpr int D = 32 * KB, V = 64 * NCT;
-  static constexpr int a = 0, b = STATES ? 0 : Op<T>::template size<D>(), c = b + Op<T>::template size<D>(),
-                       p = c + Op<T>::template size<V>(), end = p + (STATES ? 0 : 10 * Op<T>::kScore * 64 * int(sizeof(typename Op<T>::half)));
+  static constexpr int tD = Padded<T, D>::kBytes, tV = Padded<T, V>::kBytes;
+  static constexpr int a = 0, b = STATES ? 0 : tD, c = b + tD, p = c + tV,
+                       w = p + (STATES ? 0 : 6 * Op<T>::kScore * 64 * int(sizeof(typename Op<T>::frag))), end = w + 2 * kChunk * 4;
+  static_assert(end <= 160 * 1024, "a compute unit's LDS");
 };
 
 template <typename T, int KB, int NCT, bool STATES>
-__global__ __launch_bounds__(256) void walk_kernel(WalkPlan plan) {
+__global__ __launch_bounds__(256, (KB * NCT <= 4 ? 2 : 1)) void walk_kernel(WalkPlan plan) {
   typedef Op<T> O;
   typedef Lds<T, KB, NCT, STATES> M;
   typedef typename O::elem elem;
-  constexpr int D = M::D, V = M::V, NS = O::kScore, NE = O::kState, NW = O::kWeight;
+  typedef typename O::frag frag;
+  typedef typename O::half half;
+  constexpr int D = M::D, V = M::V, SD = Padded<T, D>::S, SV = Padded<T, V>::S, NS = O::kScore, NE = O::kState, NW = O::kWeight;
   extern __shared__ __attribute__((aligned(16))) char lds[];
   elem* sa = reinterpret_cast<elem*>(lds + M::a);
   elem* sb = reinterpret_cast<elem*>(lds + M::b);
   elem* sc = reinterpret_cast<elem*>(lds + M::c);
-  typename O::half* sp = reinterpret_cast<typename O::half*>(lds + M::p);
-
-  // which job, item, head, segment and columns
-  int64_t id = blockIdx.x;
-  const int units = plan.Bt * plan.H, segs = STATES ? plan.segs - 1 : plan.segs;
-  int ji = 0;
-  while (ji + 1 < plan.jobs && id >= int64_t(plan.job[ji].blocks) * units * segs) {
-    id -= int64_t(plan.job[ji].blocks) * units * segs;
-    ++ji;
-  }
-  const WalkJob& j = plan.job[ji];
-  const int vt = int(id % j.blocks), unit = int(id / j.blocks % units), seg = int(id / j.blocks / units);
-  const int item = unit / plan.H, h = unit % plan.H;
-  const int n = item_length(plan.lengths, item, plan.L);
-  const int from = seg * plan.seg_len, to = min(n, from + plan.seg_len);
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, g = lane >> 4, l16 = lane & 15;
-  const int v0 = vt * V, vc = min(j.c.cols - v0, V);
-  const float g2 = plan.log_decay[h] * 1.4426950408889634f;
-
+  half* sp = reinterpret_cast<half*>(lds + M::p);
+  float* sw = reinterpret_cast<float*>(lds + M::w);
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), g = lane >> 4, l16 = lane & 15;
+  const Place<T, V, STATES> at(plan, block_on_xcd());
+  const WalkJob& j = at.j;
   if constexpr (!STATES) {
-    if (j.zero_tail) {  // rows behind the item's tokens
-      const int first = max(n, from), last = min(plan.L, from + plan.seg_len);
-      T* o = static_cast<T*>(j.out);
-      for (int64_t i = threadIdx.x; i < int64_t(last - first) * vc; i += 256)
-        o[((int64_t(item) * plan.L + first + i / vc) * plan.H + h) * j.c.cols + v0 + i % vc] = T{};
-    }
+    if (j.zero_tail) at.zero_tail(256);
   }
-  const bool last_seg = from + plan.seg_len >= n;  // of this item
-  if (STATES ? last_seg : (from >= n && seg > 0)) return;
-
-  // the state: rows 16 r + 4 g + i, columns 16 (wave NCT + ct) + l16
+  if (at.idle) return;
   f32x4 E[2 * KB][NCT];
-  const int64_t per = int64_t(j.b.cols) * j.c.cols;
-  const float* init = nullptr;
-  if constexpr (!STATES) init = plan.segs > 1 ? j.states + (int64_t(unit) * plan.segs + seg) * per : j.init == nullptr ? nullptr : j.init + unit * per;
-#pragma unroll
-  for (int r = 0; r < 2 * KB; ++r)
-#pragma unroll
-    for (int ct = 0; ct < NCT; ++ct) {
-      const int v = 16 * (wave * NCT + ct) + l16;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int row = 16 * r + 4 * g + i;
-        E[r][ct][i] = init != nullptr && row < j.b.cols && v < vc ? init[row * j.sn + (v0 + v) * j.sv] : 0.f;
-      }
+  at.start(E, wave, lane);
+  put_weights(sw, at.g2, j, at.rest);
+  const float whole = power(at.g2, kChunk), whole_rest = power(at.g2, max(0, at.rest));
+  const Powers pw(at.g2, j, lane);
+  const int chunks = at.chunks;
+  const bool rev = at.rev, out_f32 = j.out_f32 != 0, out_words = j.out_words != 0;
+  const int a_cols = j.a.cols, b_cols = j.b.cols, vc = at.vc;
+  const int64_t a_ld = j.a.ld, b_ld = j.b.ld, c_ld = j.c.ld, way = rev ? -kChunk : kChunk;
+  const T *pa = STATES ? nullptr : at.head(j.a), *pb = at.head(j.b), *pc = at.head(j.c) + at.v0;
+  Tile<T, D, Padded<T, D>> ta, tb;
+  Tile<T, V, Padded<T, V>> tc;
+  if constexpr (!STATES) ta.place(pa, a_ld, a_cols, threadIdx.x);
+  tb.place(pb, b_ld, b_cols, threadIdx.x);
+  tc.place(pc, c_ld, vc, threadIdx.x);
+  auto load_any = [&](int k) {
+    const int64_t t = at.token(k);
+    if constexpr (!STATES) {
+      ta.base = pa + t * a_ld;
+      ta.load_any(a_ld, at.held(k), a_cols);
     }
-
-  const int64_t first = j.rev ? int64_t(item) * plan.L + n - 1 : int64_t(item) * plan.L;
-  const int dir = j.rev ? -1 : 1;
-  auto rows = [&](const WalkSide& s, int p) {
-    return static_cast<const T*>(s.p) + (first + int64_t(dir) * p) * s.ld + int64_t(h / (plan.H / s.heads)) * s.cols;
+    tb.base = pb + t * b_ld;
+    tb.load_any(b_ld, at.held(k), b_cols);
+    tc.base = pc + t * c_ld;
+    tc.load_any(c_ld, at.held(k), vc);
   };
-  for (int p0 = from; p0 < to; p0 += kChunk) {
-    const int nc = min(kChunk, to - p0);
-    {
-      Tile<T, D> t;
-      if constexpr (!STATES) {
-        t.load(rows(j.a, p0), dir * j.a.ld, nc, j.a.cols, j.a.words);
-        t.store(sa);
-      }
-      t.load(rows(j.b, p0), dir * j.b.ld, nc, j.b.cols, j.b.words);
-      t.store(sb);
-      Tile<T, V> tc;
-      tc.load(rows(j.c, p0) + v0, dir * j.c.ld, nc, vc, j.c.words);
-      tc.store(sc);
-    }
+  auto store = [&](int n) {
+    if constexpr (!STATES) ta.store(sa, n, a_cols, rev);
+    tb.store(sb, n, b_cols, rev);
+    tc.store(sc, n, vc, rev);
+  };
+  if constexpr (!STATES) {
+    for (int i = wave; i < 2 * NS; i += 4) sp[(pair_of(i & 1 ? 2 : 0, i & 1) * NS + i / 2) * 128 + lane * 2 + 1] = half{};
+  }
+  const uint32_t out_row = uint32_t(plan.H) * uint32_t(j.c.cols);
+  auto middle = [&](int k, auto fast) {
+    constexpr bool FAST = decltype(fast)::value;
+    const int nc = FAST ? kChunk : at.held(k);
+    const bool full = nc == kChunk;
     __syncthreads();
     f32x4 acc[4][NCT];
     if constexpr (!STATES) {
       // scores transposed: rows j, columns p
 #pragma unroll
-      for (int k = 0; k < 3; ++k) {
-        const int idx = wave + 4 * k;
-        if (idx < 10) {
-          const int tt = idx < 1 ? 0 : idx < 3 ? 1 : idx < 6 ? 2 : 3, jt = idx - tt * (tt + 1) / 2;
+      for (int x = 0; x < 3; ++x) {
+        const int tile = wave + 4 * x;
+        if (tile < 10) {
+          const int tt = column_of(tile), jt = tile - tt * (tt + 1) / 2;
           f32x4 s = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
           for (int R = 0; R < KB; ++R)
-            s = O::mma(O::template row<D>(sb, 16 * jt + l16, 32 * R, g), O::template row<D>(sa, 16 * tt + l16, 32 * R, g), s);
+            s = O::mma(O::template row<SD>(sb + 16 * jt * SD, 0, 32 * R, lane), O::template row<SD>(sa + 16 * tt * SD, 0, 32 * R, lane), s);
+          half o[NS];
+          O::template split<NS>(pw.weigh(s, tt - jt, lane), o);
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int d = 16 * (tt - jt) + l16 - 4 * g - i;
-            s[i] = d < 0 ? 0.f : s[i] * (j.s * power(g2, d));
-          }
-          typename O::half o[NS];
-          O::template split<NS>(s, o);
-#pragma unroll
-          for (int q = 0; q < NS; ++q) sp[(idx * NS + q) * 64 + lane] = o[q];
+          for (int q = 0; q < NS; ++q) sp[((pair_of(tt, jt / 2) * NS + q) * 64 + lane) * 2 + (jt & 1)] = o[q];
         }
       }
       // a E, transposed: rows v, columns p
@@ -303,18 +480,12 @@ __global__ __launch_bounds__(256) void walk_kernel(WalkPlan plan) {
         for (int ct = 0; ct < NCT; ++ct) acc[tt][ct] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
       for (int R = 0; R < KB; ++R) {
-        typename O::frag e[NCT][NE];
+        frag e[NCT][NE];
 #pragma unroll
-        for (int ct = 0; ct < NCT; ++ct) {
-          typename O::half lo[NE], hi[NE];
-          O::template split<NE>(E[2 * R][ct], lo);
-          O::template split<NE>(E[2 * R + 1][ct], hi);
-#pragma unroll
-          for (int q = 0; q < NE; ++q) e[ct][q] = O::join(lo[q], hi[q]);
-        }
+        for (int ct = 0; ct < NCT; ++ct) state_operand<O, NE>(E[2 * R][ct], E[2 * R + 1][ct], e[ct]);
 #pragma unroll
         for (int tt = 0; tt < 4; ++tt) {
-          const typename O::frag fa = O::template row<D>(sa, 16 * tt + l16, 32 * R, g);
+          const frag fa = O::template row<SD>(sa, 16 * tt, 32 * R, lane);
 #pragma unroll
           for (int ct = 0; ct < NCT; ++ct)
 #pragma unroll
@@ -322,98 +493,334 @@ __global__ __launch_bounds__(256) void walk_kernel(WalkPlan plan) {
         }
       }
 #pragma unroll
-      for (int tt = 0; tt < 4; ++tt) {
-        const float f = j.w * power(g2, 16 * tt + l16 + j.e);
+      for (int tt = 0; tt < 4; ++tt)
 #pragma unroll
-        for (int ct = 0; ct < NCT; ++ct) acc[tt][ct] *= f;
-      }
+        for (int ct = 0; ct < NCT; ++ct) acc[tt][ct] *= pw.out[tt];
       __syncthreads();
     }
-    // the chunk's part of c, as the products take it
-    typename O::frag fc[2][NCT];
+    frag fc[2][NCT];
 #pragma unroll
     for (int m = 0; m < 2; ++m)
 #pragma unroll
-      for (int ct = 0; ct < NCT; ++ct) fc[m][ct] = O::template col<V>(sc, 32 * m, 16 * (wave * NCT + ct), lane);
+      for (int ct = 0; ct < NCT; ++ct) fc[m][ct] = O::template col<SV>(sc + 16 * NCT * wave, 32 * m, 16 * ct, lane);
     if constexpr (!STATES) {
 #pragma unroll
-      for (int tt = 0; tt < 4; ++tt)
+      for (int m = 0; m < 2; ++m)
 #pragma unroll
-        for (int m = 0; m <= tt / 2; ++m)
+        for (int q = 0; q < NS; ++q)
 #pragma unroll
-          for (int q = 0; q < NS; ++q) {
-            const int i0 = tt * (tt + 1) / 2 + 2 * m;
-            const typename O::half lo = sp[(i0 * NS + q) * 64 + lane];
-            typename O::half hi{};
-            if (2 * m + 1 <= tt) hi = sp[((i0 + 1) * NS + q) * 64 + lane];
-            const typename O::frag fp = O::join(lo, hi);
+          for (int tt = 2 * m; tt < 4; ++tt) {
+            const frag fp = *reinterpret_cast<const frag*>(sp + ((pair_of(tt, m) * NS + q) * 64 + lane) * 2);
 #pragma unroll
             for (int ct = 0; ct < NCT; ++ct) acc[tt][ct] = O::mma(fc[m][ct], fp, acc[tt][ct]);
           }
+      char* out = static_cast<char*>(j.out) + (at.token(k) * plan.H * j.c.cols + int64_t(at.h) * j.c.cols + at.v0) * (sizeof(T) == 4 || out_f32 ? 4 : int(sizeof(T)));
 #pragma unroll
       for (int tt = 0; tt < 4; ++tt) {
         const int p = 16 * tt + l16;
-        if (p < nc) {
-          const int64_t token = first + int64_t(dir) * (p0 + p);
+        if (FAST || p < nc) {
+          const uint32_t row = uint32_t(rev ? nc - 1 - p : p) * out_row;
 #pragma unroll
           for (int ct = 0; ct < NCT; ++ct) {
             const int v = 16 * (wave * NCT + ct) + 4 * g;
-            if (v < vc) put4<T>(j, static_cast<T*>(j.out), (token * plan.H + h) * j.c.cols + v0 + v, acc[tt][ct], vc - v);
+            if (FAST || v < vc) put4<T, FAST>(out_f32, out_words, out, row + v, acc[tt][ct], vc - v);
           }
         }
       }
     }
     // the state behind the chunk
-    typename O::frag wc[2][NCT][NW];
+    const float f = full ? whole : whole_rest;
+    const float* W = sw + (full ? 0 : kChunk);
+#pragma unroll
+    for (int r = 0; r < 2 * KB; ++r)
+#pragma unroll
+      for (int ct = 0; ct < NCT; ++ct) E[r][ct] *= f;
 #pragma unroll
     for (int m = 0; m < 2; ++m) {
-      f32x4 wl, wh;
+      const f32x4 wl = *reinterpret_cast<const f32x4*>(W + 32 * m + 4 * g), wh = *reinterpret_cast<const f32x4*>(W + 32 * m + 16 + 4 * g);
+      frag wc[NCT][NW];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        wl[i] = j.u * power(g2, max(0, nc - j.e - (32 * m + 4 * g + i)));
-        wh[i] = j.u * power(g2, max(0, nc - j.e - (32 * m + 16 + 4 * g + i)));
-      }
+      for (int ct = 0; ct < NCT; ++ct) weigh_column<O, NW>(fc[m][ct], wl, wh, wc[ct]);
 #pragma unroll
-      for (int ct = 0; ct < NCT; ++ct) {
-        float v[8];
-        O::values(fc[m][ct], v);
-        typename O::half lo[NW], hi[NW];
-        O::template split<NW>(wl * f32x4{v[0], v[1], v[2], v[3]}, lo);
-        O::template split<NW>(wh * f32x4{v[4], v[5], v[6], v[7]}, hi);
-#pragma unroll
-        for (int q = 0; q < NW; ++q) wc[m][ct][q] = O::join(lo[q], hi[q]);
-      }
-    }
-    const float whole = power(g2, nc);
-#pragma unroll
-    for (int r = 0; r < 2 * KB; ++r) {
-#pragma unroll
-      for (int ct = 0; ct < NCT; ++ct) E[r][ct] *= whole;
-#pragma unroll
-      for (int m = 0; m < 2; ++m) {
-        const typename O::frag fb = O::template col<D>(sb, 32 * m, 16 * r, lane);
+      for (int r = 0; r < 2 * KB; ++r) {
+        const frag fb = O::template col<SD>(sb, 32 * m, 16 * r, lane);
 #pragma unroll
         for (int ct = 0; ct < NCT; ++ct)
 #pragma unroll
-          for (int q = 0; q < NW; ++q) E[r][ct] = O::mma(fb, wc[m][ct][q], E[r][ct]);
+          for (int q = 0; q < NW; ++q) E[r][ct] = O::mma(fb, wc[ct][q], E[r][ct]);
       }
     }
     __syncthreads();
+  };
+  if (chunks > 0) load_any(0);
+  const int quick = at.quick();
+  int k = 0;
+  for (; k + 1 < quick; ++k) {
+    store(kChunk);
+    if constexpr (!STATES) {
+      ta.base += way * a_ld;
+      ta.load(a_ld);
+    }
+    tb.base += way * b_ld;
+    tb.load(b_ld);
+    tc.base += way * c_ld;
+    tc.load(c_ld);
+    middle(k, std::true_type{});
+  }
+  for (; k < chunks; ++k) {
+    store(at.held(k));
+    if (k + 1 < chunks) load_any(k + 1);
+    middle(k, std::false_type{});
+  }
+  at.finish(E, wave, lane);
+}
+
+// ---------------------------------------------------------------- two-role walk
+// bf16, a and b of up to 128 elements, 64 columns: 8 waves, two on each SIMD.  The first four
+// hold the state: its part of the next chunk's outputs, handed over through LDS, and its
+// update.  The other four move tiles, form the scores and the outputs.  So matrix instructions
+// of the one run beside loads, conversions and waits of the other, and a chunk takes one
+// barrier: between two of them, for chunk k,
+//   state waves: update with k, then a E for k + 1;
+//   others: a and b of k + 2 and c of k + 1 into LDS and the next ones asked for, scores of
+//   k + 1, scores times c and out for k.
+template <int KB>
+struct PairLds {
+  static constexpr int D = 32 * KB;
+  static constexpr int tA = SwizzledA<D>::kBytes, tB = SwizzledB<D>::kBytes, tC = SwizzledB<64>::kBytes, tP = 6 * 2 * 64 * 16, tX = 16 * 64 * 16;
+  static constexpr int a = 0, b = a + 2 * tA, c = b + 3 * tB, p = c + 2 * tC, x = p + 2 * tP, w = x + 2 * tX, end = w + 2 * kChunk * 4;
+  static_assert(end <= 160 * 1024, "a compute unit's LDS");
+};
+
+template <int KB>
+__global__ __launch_bounds__(512, 1) void pair_kernel(WalkPlan plan) {
+  typedef Op<bf16_t> O;
+  typedef PairLds<KB> M;
+  typedef O::frag frag;
+  typedef O::half half;
+  constexpr int D = M::D, V = 64, NS = O::kScore, NE = O::kState, NW = O::kWeight;
+  static_assert(NS == 2, "room for the scores");
+  typedef SwizzledA<D> A;
+  typedef SwizzledB<D> B;
+  typedef SwizzledB<V> C;
+  extern __shared__ __attribute__((aligned(16))) char lds[];
+  auto sa = [&](int i) { return reinterpret_cast<uint16_t*>(lds + M::a + i * M::tA); };
+  auto sb = [&](int i) { return reinterpret_cast<uint16_t*>(lds + M::b + i * M::tB); };
+  auto sc = [&](int i) { return reinterpret_cast<uint16_t*>(lds + M::c + i * M::tC); };
+  auto sp = [&](int i) { return reinterpret_cast<half*>(lds + M::p + i * M::tP); };
+  auto sx = [&](int i) { return reinterpret_cast<f32x4*>(lds + M::x + i * M::tX); };
+  float* sw = reinterpret_cast<float*>(lds + M::w);
+  const int lane = threadIdx.x & 63, role = __builtin_amdgcn_readfirstlane(threadIdx.x >> 8), wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) & 3,
+            g = lane >> 4, l16 = lane & 15;
+  const Place<bf16_t, V, false> at(plan, block_on_xcd());
+  const WalkJob& j = at.j;
+  if (j.zero_tail) at.zero_tail(512);
+  if (at.idle) return;
+  put_weights(sw, at.g2, j, at.rest);
+  const Powers pw(at.g2, j, lane);
+  const int chunks = at.chunks;
+  // c's operands of tokens 32 m.. at this wave's columns
+  const int at_c = C::col(16 * wave, lane);
+  auto column = [&](const uint16_t* t, int m) { return cat8(lds_read_tr(t + at_c + 32 * m * V), lds_read_tr(t + at_c + (32 * m + 16) * V)); };
+
+  if (role == 0) {
+    f32x4 E[2 * KB][1];
+    at.start(E, wave, lane);
+    const float whole = power(at.g2, kChunk), whole_rest = power(at.g2, max(0, at.rest));
+    int at_a[KB], at_b[2 * KB];
+#pragma unroll
+    for (int R = 0; R < KB; ++R) at_a[R] = A::row(R, lane);
+#pragma unroll
+    for (int r = 0; r < 2 * KB; ++r) at_b[r] = B::col(16 * r, lane);
+    auto inter = [&](const uint16_t* t, f32x4* x) {
+      f32x4 acc[4] = {};
+#pragma unroll
+      for (int R = 0; R < KB; ++R) {
+        frag e[NE], fa[4];
+        state_operand<O, NE>(E[2 * R][0], E[2 * R + 1][0], e);
+#pragma unroll
+        for (int tt = 0; tt < 4; ++tt) fa[tt] = as_bf16x8(*reinterpret_cast<const u32x4*>(t + at_a[R] + 16 * tt * D));
+#pragma unroll
+        for (int q = 0; q < NE; ++q)
+#pragma unroll
+          for (int tt = 0; tt < 4; ++tt) acc[tt] = O::mma(e[q], fa[tt], acc[tt]);
+      }
+#pragma unroll
+      for (int tt = 0; tt < 4; ++tt) x[(tt * 4 + wave) * 64 + lane] = acc[tt] * pw.out[tt];
+    };
+    if (chunks > 0) {
+      __syncthreads();
+      inter(sa(0), sx(0));
+    }
+    int b0 = 0;
+    for (int k = 0; k < chunks; ++k) {
+      const bool full = at.held(k) == kChunk;
+      const float f = full ? whole : whole_rest;
+      const float* W = sw + (full ? 0 : kChunk);
+      __syncthreads();
+      const uint16_t *tb = sb(b0), *tc = sc(k & 1);
+      frag wc[2][NW];
+#pragma unroll
+      for (int m = 0; m < 2; ++m)
+        weigh_column<O, NW>(column(tc, m), *reinterpret_cast<const f32x4*>(W + 32 * m + 4 * g), *reinterpret_cast<const f32x4*>(W + 32 * m + 16 + 4 * g), wc[m]);
+#pragma unroll
+      for (int r = 0; r < 2 * KB; ++r) E[r][0] *= f;
+#pragma unroll
+      for (int m = 0; m < 2; ++m)
+#pragma unroll
+        for (int r = 0; r < 2 * KB; r += 2) {
+          frag fb[2];
+#pragma unroll
+          for (int x = 0; x < 2; ++x) fb[x] = cat8(lds_read_tr(tb + at_b[r + x] + 32 * m * D), lds_read_tr(tb + at_b[r + x] + (32 * m + 16) * D));
+#pragma unroll
+          for (int q = 0; q < NW; ++q)
+#pragma unroll
+            for (int x = 0; x < 2; ++x) E[r + x][0] = O::mma(fb[x], wc[m][q], E[r + x][0]);
+        }
+      if (k + 1 < chunks) inter(sa(~k & 1), sx(~k & 1));
+      b0 = b0 == 2 ? 0 : b0 + 1;
+    }
+    at.finish(E, wave, lane);
+    return;
   }
 
-  float* fin = STATES ? j.states + (int64_t(unit) * plan.segs + seg + 1) * per : last_seg && j.fin != nullptr ? j.fin + unit * per : nullptr;
-  if (fin == nullptr) return;
+  const bool rev = at.rev, out_f32 = j.out_f32 != 0, out_words = j.out_words != 0;
+  const int thread = threadIdx.x & 255, a_cols = j.a.cols, b_cols = j.b.cols, vc = at.vc;
+  const int64_t a_ld = j.a.ld, b_ld = j.b.ld, c_ld = j.c.ld, way = rev ? -kChunk : kChunk;
+  const bf16_t *pa = at.head(j.a), *pb = at.head(j.b), *pc = at.head(j.c) + at.v0;
+  Tile<bf16_t, D, A> ta;
+  Tile<bf16_t, D, B> tb;
+  Tile<bf16_t, V, C> tc;
+  ta.place(pa, a_ld, a_cols, thread);
+  tb.place(pb, b_ld, b_cols, thread);
+  tc.place(pc, c_ld, vc, thread);
+  auto any_ab = [&](int k) {
+    ta.base = pa + at.token(k) * a_ld;
+    ta.load_any(a_ld, at.held(k), a_cols);
+    tb.base = pb + at.token(k) * b_ld;
+    tb.load_any(b_ld, at.held(k), b_cols);
+  };
+  auto any_c = [&](int k) {
+    tc.base = pc + at.token(k) * c_ld;
+    tc.load_any(c_ld, at.held(k), vc);
+  };
+  for (int i = wave; i < 8; i += 4) sp(i >> 2)[(pair_of(i & 1 ? 2 : 0, i & 1) * NS + (i >> 1 & 1)) * 128 + lane * 2 + 1] = half{};
+  int at_a[KB], at_b[2 * KB];
 #pragma unroll
-  for (int r = 0; r < 2 * KB; ++r)
+  for (int R = 0; R < KB; ++R) {
+    at_a[R] = A::row(R, lane);
+    at_b[2 * R] = B::row(32 * R, lane);
+    at_b[2 * R + 1] = B::row(32 * R + 16, lane);
+  }
+  // scores transposed: rows j, columns p
+  auto scores = [&](const uint16_t* A_, const uint16_t* B_, half* P) {
 #pragma unroll
-    for (int ct = 0; ct < NCT; ++ct) {
-      const int v = 16 * (wave * NCT + ct) + l16;
+    for (int x = 0; x < 3; ++x) {
+      const int tile = wave + 4 * x;
+      if (tile < 10) {
+        const int tt = column_of(tile), jt = tile - tt * (tt + 1) / 2;
+        const uint16_t *At = A_ + 16 * tt * D, *Bt = B_ + 16 * jt * D;
+        f32x4 s = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int row = 16 * r + 4 * g + i;
-        if (row < j.b.cols && v < vc) fin[row * j.sn + (v0 + v) * j.sv] = E[r][ct][i];
+        for (int R = 0; R < KB; ++R)
+          s = O::mma(cat8(*reinterpret_cast<const u32x2*>(Bt + at_b[2 * R]), *reinterpret_cast<const u32x2*>(Bt + at_b[2 * R + 1])),
+                     as_bf16x8(*reinterpret_cast<const u32x4*>(At + at_a[R])), s);
+        half o[NS];
+        O::split<NS>(pw.weigh(s, tt - jt, lane), o);
+#pragma unroll
+        for (int q = 0; q < NS; ++q) P[((pair_of(tt, jt / 2) * NS + q) * 64 + lane) * 2 + (jt & 1)] = o[q];
       }
     }
+  };
+  const uint32_t out_row = uint32_t(plan.H) * uint32_t(j.c.cols), out_first = uint32_t(rev ? kChunk - 1 - l16 : l16) * out_row + 16 * wave + 4 * g;
+  const int64_t out_head = int64_t(at.h) * j.c.cols + at.v0, out_token = int64_t(plan.H) * j.c.cols;
+  const int out_size = out_f32 ? 4 : 2;
+  auto outputs = [&](int k, int nc, auto fast) {
+    constexpr bool FAST = decltype(fast)::value;
+    const half* P = sp(k & 1);
+    const uint16_t* t = sc(k & 1);
+    f32x4 acc[4];
+#pragma unroll
+    for (int tt = 0; tt < 4; ++tt) acc[tt] = sx(k & 1)[(tt * 4 + wave) * 64 + lane];
+#pragma unroll
+    for (int m = 0; m < 2; ++m) {
+      const frag fc = column(t, m);
+#pragma unroll
+      for (int q = 0; q < NS; ++q)
+#pragma unroll
+        for (int tt = 2 * m; tt < 4; ++tt) acc[tt] = O::mma(fc, *reinterpret_cast<const frag*>(P + ((pair_of(tt, m) * NS + q) * 64 + lane) * 2), acc[tt]);
+    }
+    char* out = static_cast<char*>(j.out) + (at.token(k) * out_token + out_head) * out_size;
+#pragma unroll
+    for (int tt = 0; tt < 4; ++tt) {
+      if constexpr (FAST) {
+        put4<bf16_t, true>(out_f32, true, out, out_first + uint32_t(rev ? -16 * tt : 16 * tt) * out_row, acc[tt], 4);
+      } else {
+        const int p = 16 * tt + l16, v = 16 * wave + 4 * g;
+        if (p < nc && v < vc) put4<bf16_t, false>(out_f32, out_words, out, uint32_t(rev ? nc - 1 - p : p) * out_row + v, acc[tt], vc - v);
+      }
+    }
+  };
+  if (chunks > 0) {
+    any_ab(0);
+    ta.store(sa(0), at.held(0), a_cols, rev);
+    tb.store(sb(0), at.held(0), b_cols, rev);
+    any_c(0);
+    tc.store(sc(0), at.held(0), vc, rev);
+    if (chunks > 1) {
+      any_ab(1);
+      ta.store(sa(1), at.held(1), a_cols, rev);
+      tb.store(sb(1), at.held(1), b_cols, rev);
+      any_c(1);
+    }
+    if (chunks > 2) any_ab(2);
+    __syncthreads();
+    scores(sa(0), sb(0), sp(0));
+  }
+  const int quick = at.quick();
+  int k = 0, b1 = 1, b2 = 2;  // b's tiles of chunks k + 1 and k + 2
+  for (; k + 3 < quick; ++k) {
+    __syncthreads();
+    ta.store(sa(k & 1), kChunk, a_cols, rev);
+    tb.store(sb(b2), kChunk, b_cols, rev);
+    tc.store(sc(~k & 1), kChunk, vc, rev);
+    ta.base += way * a_ld;
+    tb.base += way * b_ld;
+    tc.base += way * c_ld;
+    ta.load(a_ld);
+    tb.load(b_ld);
+    tc.load(c_ld);
+    scores(sa(~k & 1), sb(b1), sp(~k & 1));
+    outputs(k, kChunk, std::true_type{});
+    b1 = b2;
+    b2 = b2 == 2 ? 0 : b2 + 1;
+  }
+  for (; k < chunks; ++k) {
+    __syncthreads();
+    if (k + 2 < chunks) {
+      ta.store(sa(k & 1), at.held(k + 2), a_cols, rev);
+      tb.store(sb(b2), at.held(k + 2), b_cols, rev);
+    }
+    if (k + 1 < chunks) tc.store(sc(~k & 1), at.held(k + 1), vc, rev);
+    if (k + 3 < chunks) any_ab(k + 3);
+    if (k + 2 < chunks) any_c(k + 2);
+    if (k + 1 < chunks) scores(sa(~k & 1), sb(b1), sp(~k & 1));
+    outputs(k, at.held(k), std::false_type{});
+    b1 = b2;
+    b2 = b2 == 2 ? 0 : b2 + 1;
+  }
+}
+
+template <int KB>
+hipError_t launch_pair(const WalkPlan& p, hipStream_t s) {
+  int64_t blocks = 0;
+  for (int i = 0; i < p.jobs; ++i) blocks += int64_t(p.job[i].blocks) * p.Bt * p.H * p.segs;
+  constexpr int bytes = PairLds<KB>::end;
+  static std::atomic<uint64_t> cleared{0};
+  const hipError_t e = allow_lds(reinterpret_cast<const void*>(&pair_kernel<KB>), bytes, cleared);
+  if (e != hipSuccess) return e;
+  pair_kernel<KB><<<dim3(uint32_t(blocks)), dim3(512), bytes, s>>>(p);
+  return hipGetLastError();
 }
 
 template <typename T, int KB, int NCT, bool STATES>
@@ -442,7 +849,16 @@ hipError_t dispatch(const WalkPlan& p, int kb, int nct, bool states_only, hipStr
       case 81: return launch<T, 8, 1, true>(p, s);
     }
   } else {
-    switch (key) {
+    if constexpr (sizeof(T) == 2) {
+      switch (key) {
+        case 11: return launch_pair<1>(p, s);
+        case 21: return launch_pair<2>(p, s);
+        case 41: return launch_pair<4>(p, s);
+        case 81: return launch<T, 8, 1, false>(p, s);
+      }
+      return hipErrorInvalidValue;
+    }
+    if constexpr (sizeof(T) == 4) switch (key) {
       case 11: return launch<T, 1, 1, false>(p, s);
       case 12: return launch<T, 1, 2, false>(p, s);
       case 21: return launch<T, 2, 1, false>(p, s);
