@@ -131,7 +131,7 @@ constexpr int shift_of(int D) { return D >= 128 ? 0 : D == 64 ? 1 : 2; }
 // a: operands of 8 positions lie together, 16 bytes; 16 rows of one meet every bank once
 template <int D>
 struct SwizzledA {
-  static constexpr int kBytes = kChunk * D * 2;
+  static constexpr int S = D, kBytes = kChunk * D * 2;
   static __device__ __forceinline__ int mix(int r) { return (r & 15) >> shift_of(D); }
   static __device__ __forceinline__ void put(uint16_t* t, int r, int c, u32x4 w) {
     const int u = c / 32 * 4 + (c & 8) / 4, h = (c & 16) / 4;  // units of columns c.. and c + 4..
@@ -144,7 +144,7 @@ struct SwizzledA {
 // b and c: units of 8 bytes; 16 rows of two of them, and 8 rows of four, meet every bank once
 template <int D>
 struct SwizzledB {
-  static constexpr int kBytes = kChunk * D * 2;
+  static constexpr int S = D, kBytes = kChunk * D * 2;
   static __device__ __forceinline__ int mix(int r) { return (((r & 7) >> shift_of(D)) << 2) | ((r >> 3 & 1) << 1); }
   static __device__ __forceinline__ void put(uint16_t* t, int r, int c, u32x4 w) {
     *reinterpret_cast<u32x4*>(t + r * D + ((c / 4) ^ mix(r)) * 4) = w;
@@ -165,24 +165,42 @@ struct Tile {
   typedef typename Op<T>::elem elem;
   static constexpr int W = Op<T>::kWord, kRow = D / W, kRows = 256 / kRow, N = kChunk / kRows;
   static_assert(N >= 1 && 256 % kRow == 0, "whole rows over the block");
-  u32x4 w[N];
-  const T* base;  // the head's elements of the chunk's first token
-  uint32_t at;    // this thread's bytes from there
-  int r0, c0;     // its first row and its column
-  __device__ __forceinline__ void place(const T* first, int64_t ld, int cols, int thread) {
-    base = first;
+  typedef u32x4 words[N];
+  uint32_t at;  // this thread's bytes from a chunk's first element
+  int r0, c0;   // its first row and its column
+  __device__ __forceinline__ Tile(int64_t ld, int cols, int thread) {
     r0 = thread / kRow;
     c0 = thread % kRow * W;
     at = (uint32_t(r0) * uint32_t(ld) + uint32_t(c0 < cols ? c0 : 0)) * uint32_t(sizeof(T));
   }
   // a whole chunk of whole words; columns past the head's are others' here, and zeroed when stored
-  __device__ __forceinline__ void load(int64_t ld) {
+  __device__ __forceinline__ void load(words& w, const T* base, int64_t ld) const {
 #pragma unroll
     for (int i = 0; i < N; ++i)
       w[i] = *reinterpret_cast<const u32x4*>(reinterpret_cast<const char*>(base + int64_t(i * kRows) * ld) + at);
   }
+  // whole chunks: a place per thread and constant steps (rows of one are 16 apart, which the
+  // swizzles do not see)
+  __device__ __forceinline__ void store_whole(words& w, elem* t, int cols, bool rev) const {
+    if (cols < D) {
+#pragma unroll
+      for (int i = 0; i < N; ++i) w[i] = c0 < cols ? w[i] : u32x4{0, 0, 0, 0};
+    }
+    if constexpr (kRows % 16 == 0) {
+      if (rev) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) To::put(t + (N - 1 - i) * kRows * To::S, kRows - 1 - r0, c0, w[i]);
+      } else {
+#pragma unroll
+        for (int i = 0; i < N; ++i) To::put(t + i * kRows * To::S, r0, c0, w[i]);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < N; ++i) To::put(t, rev ? kChunk - 1 - i * kRows - r0 : i * kRows + r0, c0, w[i]);
+    }
+  }
   // n tokens, any words
-  __device__ __forceinline__ void load_any(int64_t ld, int n, int cols) {
+  __device__ __forceinline__ void load_any(words& w, const T* base, int64_t ld, int n, int cols) const {
 #pragma unroll
     for (int i = 0; i < N; ++i) {
       const int r = i * kRows + r0, left = r < n ? cols - c0 : 0;
@@ -193,7 +211,7 @@ struct Tile {
       __builtin_memcpy(&w[i], &q, 16);
     }
   }
-  __device__ __forceinline__ void store(elem* t, int n, int cols, bool rev) {
+  __device__ __forceinline__ void store(words& w, elem* t, int n, int cols, bool rev) const {
 #pragma unroll
     for (int i = 0; i < N; ++i) {
       const int r = i * kRows + r0;
@@ -254,13 +272,13 @@ struct Place {
     seg = int(id / j.blocks / units);
     item = unit / plan.H;
     h = unit % plan.H;
-    n = item_length(plan.lengths, item, plan.L);
+    n = __builtin_amdgcn_readfirstlane(item_length(plan.lengths, item, plan.L));  // the same for the block
     from = seg * plan.seg_len;
     to = min(n, from + plan.seg_len);
     v0 = vt * V;
     vc = min(j.c.cols - v0, V);
     rev = j.rev != 0;
-    g2 = plan.log_decay[h] * 1.4426950408889634f;
+    g2 = __builtin_bit_cast(float, __builtin_amdgcn_readfirstlane(__builtin_bit_cast(int, plan.log_decay[h] * 1.4426950408889634f)));
     per = int64_t(j.b.cols) * j.c.cols;
     last_seg = from + plan.seg_len >= n;  // of this item
     idle = STATES ? last_seg : (from >= n && seg > 0);
@@ -425,26 +443,22 @@ __global__ __launch_bounds__(256, (KB * NCT <= 4 ? 2 : 1)) void walk_kernel(Walk
   const int a_cols = j.a.cols, b_cols = j.b.cols, vc = at.vc;
   const int64_t a_ld = j.a.ld, b_ld = j.b.ld, c_ld = j.c.ld, way = rev ? -kChunk : kChunk;
   const T *pa = STATES ? nullptr : at.head(j.a), *pb = at.head(j.b), *pc = at.head(j.c) + at.v0;
-  Tile<T, D, Padded<T, D>> ta, tb;
-  Tile<T, V, Padded<T, V>> tc;
-  if constexpr (!STATES) ta.place(pa, a_ld, a_cols, threadIdx.x);
-  tb.place(pb, b_ld, b_cols, threadIdx.x);
-  tc.place(pc, c_ld, vc, threadIdx.x);
+  typedef Tile<T, D, Padded<T, D>> TD;
+  typedef Tile<T, V, Padded<T, V>> TV;
+  const TD ta(a_ld, a_cols, threadIdx.x), tb(b_ld, b_cols, threadIdx.x);
+  const TV tc(c_ld, vc, threadIdx.x);
+  typename TD::words wa, wb;
+  typename TV::words wc;
   auto load_any = [&](int k) {
     const int64_t t = at.token(k);
-    if constexpr (!STATES) {
-      ta.base = pa + t * a_ld;
-      ta.load_any(a_ld, at.held(k), a_cols);
-    }
-    tb.base = pb + t * b_ld;
-    tb.load_any(b_ld, at.held(k), b_cols);
-    tc.base = pc + t * c_ld;
-    tc.load_any(c_ld, at.held(k), vc);
+    if constexpr (!STATES) ta.load_any(wa, pa + t * a_ld, a_ld, at.held(k), a_cols);
+    tb.load_any(wb, pb + t * b_ld, b_ld, at.held(k), b_cols);
+    tc.load_any(wc, pc + t * c_ld, c_ld, at.held(k), vc);
   };
   auto store = [&](int n) {
-    if constexpr (!STATES) ta.store(sa, n, a_cols, rev);
-    tb.store(sb, n, b_cols, rev);
-    tc.store(sc, n, vc, rev);
+    if constexpr (!STATES) ta.store(wa, sa, n, a_cols, rev);
+    tb.store(wb, sb, n, b_cols, rev);
+    tc.store(wc, sc, n, vc, rev);
   };
   if constexpr (!STATES) {
     for (int i = wave; i < 2 * NS; i += 4) sp[(pair_of(i & 1 ? 2 : 0, i & 1) * NS + i / 2) * 128 + lane * 2 + 1] = half{};
@@ -538,16 +552,16 @@ __global__ __launch_bounds__(256, (KB * NCT <= 4 ? 2 : 1)) void walk_kernel(Walk
 #pragma unroll
     for (int m = 0; m < 2; ++m) {
       const f32x4 wl = *reinterpret_cast<const f32x4*>(W + 32 * m + 4 * g), wh = *reinterpret_cast<const f32x4*>(W + 32 * m + 16 + 4 * g);
-      frag wc[NCT][NW];
+      frag fw[NCT][NW];
 #pragma unroll
-      for (int ct = 0; ct < NCT; ++ct) weigh_column<O, NW>(fc[m][ct], wl, wh, wc[ct]);
+      for (int ct = 0; ct < NCT; ++ct) weigh_column<O, NW>(fc[m][ct], wl, wh, fw[ct]);
 #pragma unroll
       for (int r = 0; r < 2 * KB; ++r) {
         const frag fb = O::template col<SD>(sb, 32 * m, 16 * r, lane);
 #pragma unroll
         for (int ct = 0; ct < NCT; ++ct)
 #pragma unroll
-          for (int q = 0; q < NW; ++q) E[r][ct] = O::mma(fb, wc[ct][q], E[r][ct]);
+          for (int q = 0; q < NW; ++q) E[r][ct] = O::mma(fb, fw[ct][q], E[r][ct]);
       }
     }
     __syncthreads();
@@ -556,15 +570,14 @@ __global__ __launch_bounds__(256, (KB * NCT <= 4 ? 2 : 1)) void walk_kernel(Walk
   const int quick = at.quick();
   int k = 0;
   for (; k + 1 < quick; ++k) {
-    store(kChunk);
-    if constexpr (!STATES) {
-      ta.base += way * a_ld;
-      ta.load(a_ld);
-    }
-    tb.base += way * b_ld;
-    tb.load(b_ld);
-    tc.base += way * c_ld;
-    tc.load(c_ld);
+    const int64_t t = at.token(k) + way;
+    if constexpr (!STATES) ta.store_whole(wa, sa, a_cols, rev);
+    tb.store_whole(wb, sb, b_cols, rev);
+    tc.store_whole(wc, sc, vc, rev);
+    if constexpr (!STATES) ta.load(wa, pa + t * a_ld, a_ld);
+    tb.load(wb, pb + t * b_ld, b_ld);
+    tc.load(wc, pc + t * c_ld, c_ld);
+    __builtin_amdgcn_sched_barrier(0);  // asked for now, not where the scheduler finds a register for them
     middle(k, std::true_type{});
   }
   for (; k < chunks; ++k) {
@@ -593,7 +606,7 @@ struct PairLds {
 };
 
 template <int KB>
-__global__ __launch_bounds__(512, 1) void pair_kernel(WalkPlan plan) {
+__global__ __launch_bounds__(512, 1) __attribute__((amdgpu_waves_per_eu(2, 2))) void pair_kernel(WalkPlan plan) {
   typedef Op<bf16_t> O;
   typedef PairLds<KB> M;
   typedef O::frag frag;
@@ -632,25 +645,38 @@ __global__ __launch_bounds__(512, 1) void pair_kernel(WalkPlan plan) {
     for (int R = 0; R < KB; ++R) at_a[R] = A::row(R, lane);
 #pragma unroll
     for (int r = 0; r < 2 * KB; ++r) at_b[r] = B::col(16 * r, lane);
-    auto inter = [&](const uint16_t* t, f32x4* x) {
+    // Reads of LDS are asked for ahead of the products in front of those that need them:
+    // left to itself the scheduler waits for each (12 waits of 230 cycles made 60% of a chunk).
+    auto ahead = [] { __builtin_amdgcn_sched_barrier(0); };
+    auto rows_of_a = [&](const uint16_t* t, int R, frag (&f)[4]) {
+#pragma unroll
+      for (int tt = 0; tt < 4; ++tt) f[tt] = as_bf16x8(*reinterpret_cast<const u32x4*>(t + at_a[R] + 16 * tt * D));
+    };
+    // acc = a E: e, the state in parts
+    auto inter = [&](const uint16_t* t, f32x4* x, const frag (&e)[KB][NE], frag (&first)[4]) {
       f32x4 acc[4] = {};
+      frag fa[2][4];
+#pragma unroll
+      for (int tt = 0; tt < 4; ++tt) fa[0][tt] = first[tt];
 #pragma unroll
       for (int R = 0; R < KB; ++R) {
-        frag e[NE], fa[4];
-        state_operand<O, NE>(E[2 * R][0], E[2 * R + 1][0], e);
-#pragma unroll
-        for (int tt = 0; tt < 4; ++tt) fa[tt] = as_bf16x8(*reinterpret_cast<const u32x4*>(t + at_a[R] + 16 * tt * D));
+        if (R + 1 < KB) rows_of_a(t, R + 1, fa[(R + 1) & 1]);
+        ahead();
 #pragma unroll
         for (int q = 0; q < NE; ++q)
 #pragma unroll
-          for (int tt = 0; tt < 4; ++tt) acc[tt] = O::mma(e[q], fa[tt], acc[tt]);
+          for (int tt = 0; tt < 4; ++tt) acc[tt] = O::mma(e[R][q], fa[R & 1][tt], acc[tt]);
       }
 #pragma unroll
       for (int tt = 0; tt < 4; ++tt) x[(tt * 4 + wave) * 64 + lane] = acc[tt] * pw.out[tt];
     };
+    frag e[KB][NE], first[4];
     if (chunks > 0) {
       __syncthreads();
-      inter(sa(0), sx(0));
+      rows_of_a(sa(0), 0, first);
+#pragma unroll
+      for (int R = 0; R < KB; ++R) state_operand<O, NE>(E[2 * R][0], E[2 * R + 1][0], e[R]);
+      inter(sa(0), sx(0), e, first);
     }
     int b0 = 0;
     for (int k = 0; k < chunks; ++k) {
@@ -659,25 +685,42 @@ __global__ __launch_bounds__(512, 1) void pair_kernel(WalkPlan plan) {
       const float* W = sw + (full ? 0 : kChunk);
       __syncthreads();
       const uint16_t *tb = sb(b0), *tc = sc(k & 1);
-      frag wc[2][NW];
+      auto columns_of_b = [&](int R, frag (&o)[2][2]) {
 #pragma unroll
-      for (int m = 0; m < 2; ++m)
-        weigh_column<O, NW>(column(tc, m), *reinterpret_cast<const f32x4*>(W + 32 * m + 4 * g), *reinterpret_cast<const f32x4*>(W + 32 * m + 16 + 4 * g), wc[m]);
+        for (int m = 0; m < 2; ++m)
 #pragma unroll
-      for (int r = 0; r < 2 * KB; ++r) E[r][0] *= f;
+          for (int x = 0; x < 2; ++x)
+            o[m][x] = cat8(lds_read_tr(tb + at_b[2 * R + x] + 32 * m * D), lds_read_tr(tb + at_b[2 * R + x] + (32 * m + 16) * D));
+      };
+      frag fc[2], wc[2][NW], fb[2][2][2];
+      f32x4 wt[2][2];
 #pragma unroll
-      for (int m = 0; m < 2; ++m)
+      for (int m = 0; m < 2; ++m) {
+        fc[m] = column(tc, m);
+        wt[m][0] = *reinterpret_cast<const f32x4*>(W + 32 * m + 4 * g);
+        wt[m][1] = *reinterpret_cast<const f32x4*>(W + 32 * m + 16 + 4 * g);
+      }
+      columns_of_b(0, fb[0]);
+      ahead();
 #pragma unroll
-        for (int r = 0; r < 2 * KB; r += 2) {
-          frag fb[2];
+      for (int m = 0; m < 2; ++m) weigh_column<O, NW>(fc[m], wt[m][0], wt[m][1], wc[m]);
 #pragma unroll
-          for (int x = 0; x < 2; ++x) fb[x] = cat8(lds_read_tr(tb + at_b[r + x] + 32 * m * D), lds_read_tr(tb + at_b[r + x] + (32 * m + 16) * D));
+      for (int R = 0; R < KB; ++R) {
+        if (R + 1 < KB) columns_of_b(R + 1, fb[(R + 1) & 1]);
+        else if (k + 1 < chunks) rows_of_a(sa(~k & 1), 0, first);
+        ahead();
+        if (R > 0) state_operand<O, NE>(E[2 * R - 2][0], E[2 * R - 1][0], e[R - 1]);
+#pragma unroll
+        for (int x = 0; x < 2; ++x) E[2 * R + x][0] *= f;
+#pragma unroll
+        for (int m = 0; m < 2; ++m)
 #pragma unroll
           for (int q = 0; q < NW; ++q)
 #pragma unroll
-            for (int x = 0; x < 2; ++x) E[r + x][0] = O::mma(fb[x], wc[m][q], E[r + x][0]);
-        }
-      if (k + 1 < chunks) inter(sa(~k & 1), sx(~k & 1));
+            for (int x = 0; x < 2; ++x) E[2 * R + x][0] = O::mma(fb[R & 1][m][x], wc[m][q], E[2 * R + x][0]);
+      }
+      state_operand<O, NE>(E[2 * KB - 2][0], E[2 * KB - 1][0], e[KB - 1]);
+      if (k + 1 < chunks) inter(sa(~k & 1), sx(~k & 1), e, first);
       b0 = b0 == 2 ? 0 : b0 + 1;
     }
     at.finish(E, wave, lane);
@@ -688,22 +731,20 @@ __global__ __launch_bounds__(512, 1) void pair_kernel(WalkPlan plan) {
   const int thread = threadIdx.x & 255, a_cols = j.a.cols, b_cols = j.b.cols, vc = at.vc;
   const int64_t a_ld = j.a.ld, b_ld = j.b.ld, c_ld = j.c.ld, way = rev ? -kChunk : kChunk;
   const bf16_t *pa = at.head(j.a), *pb = at.head(j.b), *pc = at.head(j.c) + at.v0;
-  Tile<bf16_t, D, A> ta;
-  Tile<bf16_t, D, B> tb;
-  Tile<bf16_t, V, C> tc;
-  ta.place(pa, a_ld, a_cols, thread);
-  tb.place(pb, b_ld, b_cols, thread);
-  tc.place(pc, c_ld, vc, thread);
+  typedef Tile<bf16_t, D, A> TA;
+  typedef Tile<bf16_t, D, B> TB;
+  typedef Tile<bf16_t, V, C> TC;
+  const TA ta(a_ld, a_cols, thread);
+  const TB tb(b_ld, b_cols, thread);
+  const TC tc(c_ld, vc, thread);
+  typename TA::words wa;
+  typename TB::words wb;
+  TC::words wc;
   auto any_ab = [&](int k) {
-    ta.base = pa + at.token(k) * a_ld;
-    ta.load_any(a_ld, at.held(k), a_cols);
-    tb.base = pb + at.token(k) * b_ld;
-    tb.load_any(b_ld, at.held(k), b_cols);
+    ta.load_any(wa, pa + at.token(k) * a_ld, a_ld, at.held(k), a_cols);
+    tb.load_any(wb, pb + at.token(k) * b_ld, b_ld, at.held(k), b_cols);
   };
-  auto any_c = [&](int k) {
-    tc.base = pc + at.token(k) * c_ld;
-    tc.load_any(c_ld, at.held(k), vc);
-  };
+  auto any_c = [&](int k) { tc.load_any(wc, pc + at.token(k) * c_ld, c_ld, at.held(k), vc); };
   for (int i = wave; i < 8; i += 4) sp(i >> 2)[(pair_of(i & 1 ? 2 : 0, i & 1) * NS + (i >> 1 & 1)) * 128 + lane * 2 + 1] = half{};
   int at_a[KB], at_b[2 * KB];
 #pragma unroll
@@ -712,24 +753,52 @@ __global__ __launch_bounds__(512, 1) void pair_kernel(WalkPlan plan) {
     at_b[2 * R] = B::row(32 * R, lane);
     at_b[2 * R + 1] = B::row(32 * R + 16, lane);
   }
-  // scores transposed: rows j, columns p
+  // Scores transposed: rows j, columns p.  Three tiles a wave, without a branch, so that their
+  // products and what follows run beside each other; two waves' third is their first again.
+  int off_a[3], off_b[3], off_p[3];
+  float weight[3][4];
+  int keep = 0;  // a bit for each: on or below the diagonal
+#pragma unroll
+  for (int x = 0; x < 3; ++x) {
+    const int tile = wave + 4 * x < 10 ? wave + 4 * x : wave, tt = column_of(tile), jt = tile - tt * (tt + 1) / 2;
+    off_a[x] = 16 * tt * D;
+    off_b[x] = 16 * jt * D;
+    off_p[x] = pair_of(tt, jt / 2) * NS * 128 + (jt & 1);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int d = 16 * (tt - jt) + l16 - 4 * g - i;
+      keep |= (d >= 0 ? 1 : 0) << (4 * x + i);
+      weight[x][i] = j.s * power(at.g2, max(d, 0));
+    }
+  }
   auto scores = [&](const uint16_t* A_, const uint16_t* B_, half* P) {
+    f32x4 s[3] = {};
+    frag fa[2][3], fb[2][3];
+    auto operands = [&](int R) {
+#pragma unroll
+      for (int x = 0; x < 3; ++x) {
+        fb[R & 1][x] = cat8(*reinterpret_cast<const u32x2*>(B_ + off_b[x] + at_b[2 * R]), *reinterpret_cast<const u32x2*>(B_ + off_b[x] + at_b[2 * R + 1]));
+        fa[R & 1][x] = as_bf16x8(*reinterpret_cast<const u32x4*>(A_ + off_a[x] + at_a[R]));
+      }
+    };
+    operands(0);
+#pragma unroll
+    for (int R = 0; R < KB; ++R) {
+      if (R + 1 < KB) operands(R + 1);
+      __builtin_amdgcn_sched_barrier(0);  // ahead of these products
+#pragma unroll
+      for (int x = 0; x < 3; ++x) s[x] = O::mma(fb[R & 1][x], fa[R & 1][x], s[x]);
+    }
 #pragma unroll
     for (int x = 0; x < 3; ++x) {
-      const int tile = wave + 4 * x;
-      if (tile < 10) {
-        const int tt = column_of(tile), jt = tile - tt * (tt + 1) / 2;
-        const uint16_t *At = A_ + 16 * tt * D, *Bt = B_ + 16 * jt * D;
-        f32x4 s = {0.f, 0.f, 0.f, 0.f};
+      f32x4 v;
 #pragma unroll
-        for (int R = 0; R < KB; ++R)
-          s = O::mma(cat8(*reinterpret_cast<const u32x2*>(Bt + at_b[2 * R]), *reinterpret_cast<const u32x2*>(Bt + at_b[2 * R + 1])),
-                     as_bf16x8(*reinterpret_cast<const u32x4*>(At + at_a[R])), s);
-        half o[NS];
-        O::split<NS>(pw.weigh(s, tt - jt, lane), o);
+      for (int i = 0; i < 4; ++i)
+        v[i] = __builtin_bit_cast(float, __builtin_bit_cast(int, s[x][i] * weight[x][i]) & __builtin_amdgcn_sbfe(keep, 4 * x + i, 1));
+      half o[NS];
+      O::split<NS>(v, o);
 #pragma unroll
-        for (int q = 0; q < NS; ++q) P[((pair_of(tt, jt / 2) * NS + q) * 64 + lane) * 2 + (jt & 1)] = o[q];
-      }
+      for (int q = 0; q < NS; ++q) P[off_p[x] + (q * 64 + lane) * 2] = o[q];
     }
   };
   const uint32_t out_row = uint32_t(plan.H) * uint32_t(j.c.cols), out_first = uint32_t(rev ? kChunk - 1 - l16 : l16) * out_row + 16 * wave + 4 * g;
@@ -740,16 +809,22 @@ __global__ __launch_bounds__(512, 1) void pair_kernel(WalkPlan plan) {
     const half* P = sp(k & 1);
     const uint16_t* t = sc(k & 1);
     f32x4 acc[4];
+    frag fc[2], fp[6][NS];
+#pragma unroll
+    for (int m = 0; m < 2; ++m) fc[m] = column(t, m);
 #pragma unroll
     for (int tt = 0; tt < 4; ++tt) acc[tt] = sx(k & 1)[(tt * 4 + wave) * 64 + lane];
 #pragma unroll
-    for (int m = 0; m < 2; ++m) {
-      const frag fc = column(t, m);
+    for (int x = 0; x < 6; ++x)
+#pragma unroll
+      for (int q = 0; q < NS; ++q) fp[x][q] = *reinterpret_cast<const frag*>(P + ((x * NS + q) * 64 + lane) * 2);
+    __builtin_amdgcn_sched_barrier(0);  // all asked for ahead of the products
+#pragma unroll
+    for (int m = 0; m < 2; ++m)
 #pragma unroll
       for (int q = 0; q < NS; ++q)
 #pragma unroll
-        for (int tt = 2 * m; tt < 4; ++tt) acc[tt] = O::mma(fc, *reinterpret_cast<const frag*>(P + ((pair_of(tt, m) * NS + q) * 64 + lane) * 2), acc[tt]);
-    }
+        for (int tt = 2 * m; tt < 4; ++tt) acc[tt] = O::mma(fc[m], fp[pair_of(tt, m)][q], acc[tt]);
     char* out = static_cast<char*>(j.out) + (at.token(k) * out_token + out_head) * out_size;
 #pragma unroll
     for (int tt = 0; tt < 4; ++tt) {
@@ -763,14 +838,14 @@ __global__ __launch_bounds__(512, 1) void pair_kernel(WalkPlan plan) {
   };
   if (chunks > 0) {
     any_ab(0);
-    ta.store(sa(0), at.held(0), a_cols, rev);
-    tb.store(sb(0), at.held(0), b_cols, rev);
+    ta.store(wa, sa(0), at.held(0), a_cols, rev);
+    tb.store(wb, sb(0), at.held(0), b_cols, rev);
     any_c(0);
-    tc.store(sc(0), at.held(0), vc, rev);
+    tc.store(wc, sc(0), at.held(0), vc, rev);
     if (chunks > 1) {
       any_ab(1);
-      ta.store(sa(1), at.held(1), a_cols, rev);
-      tb.store(sb(1), at.held(1), b_cols, rev);
+      ta.store(wa, sa(1), at.held(1), a_cols, rev);
+      tb.store(wb, sb(1), at.held(1), b_cols, rev);
       any_c(1);
     }
     if (chunks > 2) any_ab(2);
@@ -779,17 +854,24 @@ __global__ __launch_bounds__(512, 1) void pair_kernel(WalkPlan plan) {
   }
   const int quick = at.quick();
   int k = 0, b1 = 1, b2 = 2;  // b's tiles of chunks k + 1 and k + 2
+  const bf16_t *na = pa, *nb = pb, *nc = pc;  // the next whole chunk's first token
+  if (quick > 3) {
+    na += at.token(3) * a_ld;
+    nb += at.token(3) * b_ld;
+    nc += at.token(2) * c_ld;
+  }
   for (; k + 3 < quick; ++k) {
     __syncthreads();
-    ta.store(sa(k & 1), kChunk, a_cols, rev);
-    tb.store(sb(b2), kChunk, b_cols, rev);
-    tc.store(sc(~k & 1), kChunk, vc, rev);
-    ta.base += way * a_ld;
-    tb.base += way * b_ld;
-    tc.base += way * c_ld;
-    ta.load(a_ld);
-    tb.load(b_ld);
-    tc.load(c_ld);
+    ta.store_whole(wa, sa(k & 1), a_cols, rev);
+    tb.store_whole(wb, sb(b2), b_cols, rev);
+    tc.store_whole(wc, sc(~k & 1), vc, rev);
+    ta.load(wa, na, a_ld);
+    tb.load(wb, nb, b_ld);
+    tc.load(wc, nc, c_ld);
+    na += way * a_ld;
+    nb += way * b_ld;
+    nc += way * c_ld;
+    __builtin_amdgcn_sched_barrier(0);  // asked for now, not where the scheduler finds a register for them
     scores(sa(~k & 1), sb(b1), sp(~k & 1));
     outputs(k, kChunk, std::true_type{});
     b1 = b2;
@@ -798,10 +880,10 @@ __global__ __launch_bounds__(512, 1) void pair_kernel(WalkPlan plan) {
   for (; k < chunks; ++k) {
     __syncthreads();
     if (k + 2 < chunks) {
-      ta.store(sa(k & 1), at.held(k + 2), a_cols, rev);
-      tb.store(sb(b2), at.held(k + 2), b_cols, rev);
+      ta.store(wa, sa(k & 1), at.held(k + 2), a_cols, rev);
+      tb.store(wb, sb(b2), at.held(k + 2), b_cols, rev);
     }
-    if (k + 1 < chunks) tc.store(sc(~k & 1), at.held(k + 1), vc, rev);
+    if (k + 1 < chunks) tc.store(wc, sc(~k & 1), at.held(k + 1), vc, rev);
     if (k + 3 < chunks) any_ab(k + 3);
     if (k + 2 < chunks) any_c(k + 2);
     if (k + 1 < chunks) scores(sa(~k & 1), sb(b1), sp(~k & 1));
