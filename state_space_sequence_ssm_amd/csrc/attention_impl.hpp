@@ -594,9 +594,9 @@ __global__ __launch_bounds__(256, (KB * NCT <= 4 ? 2 : 1)) void walk_kernel(Walk
 // update.  The other four move tiles, form the scores and the outputs.  So matrix instructions
 // of the one run beside loads, conversions and waits of the other, and a chunk takes one
 // barrier: between two of them, for chunk k,
-//   state waves: update with k, then a E for k + 1;
-//   others: a and b of k + 2 and c of k + 1 into LDS and the next ones asked for, scores of
-//   k + 1, scores times c and out for k.
+//   state waves: c of k + 1 into LDS and k + 3's asked for, update with k, then a E for k + 1;
+//   others: a and b of k + 2 into LDS and k + 4's asked for, scores of k + 1 (three waves, a
+//   quarter of the triangle's 2 x 2 blocks of 2 x 2 tiles each), scores times c and out for k.
 template <int KB>
 struct PairLds {
   static constexpr int D = 32 * KB;
@@ -636,9 +636,21 @@ __global__ __launch_bounds__(512, 1) __attribute__((amdgpu_waves_per_eu(2, 2))) 
   const int at_c = C::col(16 * wave, lane);
   auto column = [&](const uint16_t* t, int m) { return cat8(lds_read_tr(t + at_c + 32 * m * V), lds_read_tr(t + at_c + (32 * m + 16) * V)); };
 
+  const bool rev = at.rev;
+  const int thread = threadIdx.x & 255, vc = at.vc, quick = at.quick();
+  const int64_t way = rev ? -kChunk : kChunk;
+  std::integral_constant<int, 0> even;
+  std::integral_constant<int, 1> odd;
   if (role == 0) {
     f32x4 E[2 * KB][1];
     at.start(E, wave, lane);
+    typedef Tile<bf16_t, V, C> TC;
+    const int64_t c_ld = j.c.ld;
+    const TC tc(c_ld, vc, thread);
+    TC::words wc[2];  // of chunk k in set k & 1
+    const bf16_t *pc = at.head(j.c) + at.v0, *nc = pc;
+    auto any_c = [&](int k, auto set) { tc.load_any(wc[decltype(set)::value], pc + at.token(k) * c_ld, c_ld, at.held(k), vc); };
+    if (quick > 3) nc += at.token(3) * c_ld;
     const float whole = power(at.g2, kChunk), whole_rest = power(at.g2, max(0, at.rest));
     int at_a[KB], at_b[2 * KB];
 #pragma unroll
@@ -672,6 +684,10 @@ __global__ __launch_bounds__(512, 1) __attribute__((amdgpu_waves_per_eu(2, 2))) 
     };
     frag e[KB][NE], first[4];
     if (chunks > 0) {
+      any_c(0, even);
+      tc.store(wc[0], sc(0), at.held(0), vc, rev);
+      if (chunks > 1) any_c(1, odd);
+      if (chunks > 2) any_c(2, even);
       __syncthreads();
       rows_of_a(sa(0), 0, first);
 #pragma unroll
@@ -679,12 +695,14 @@ __global__ __launch_bounds__(512, 1) __attribute__((amdgpu_waves_per_eu(2, 2))) 
       inter(sa(0), sx(0), e, first);
     }
     int b0 = 0;
-    for (int k = 0; k < chunks; ++k) {
-      const bool full = at.held(k) == kChunk;
+    auto turn = [&](int k, auto set, auto whole_chunks) {  // k & 1 = set
+      constexpr int S = decltype(set)::value;
+      constexpr bool FAST = decltype(whole_chunks)::value;
+      const bool full = FAST || at.held(k) == kChunk, more = FAST || k + 1 < chunks;
       const float f = full ? whole : whole_rest;
       const float* W = sw + (full ? 0 : kChunk);
       __syncthreads();
-      const uint16_t *tb = sb(b0), *tc = sc(k & 1);
+      const uint16_t *tb = sb(b0), *ct = sc(S);
       auto columns_of_b = [&](int R, frag (&o)[2][2]) {
 #pragma unroll
         for (int m = 0; m < 2; ++m)
@@ -692,22 +710,30 @@ __global__ __launch_bounds__(512, 1) __attribute__((amdgpu_waves_per_eu(2, 2))) 
           for (int x = 0; x < 2; ++x)
             o[m][x] = cat8(lds_read_tr(tb + at_b[2 * R + x] + 32 * m * D), lds_read_tr(tb + at_b[2 * R + x] + (32 * m + 16) * D));
       };
-      frag fc[2], wc[2][NW], fb[2][2][2];
+      frag fc[2], fw[2][NW], fb[2][2][2];
       f32x4 wt[2][2];
 #pragma unroll
       for (int m = 0; m < 2; ++m) {
-        fc[m] = column(tc, m);
+        fc[m] = column(ct, m);
         wt[m][0] = *reinterpret_cast<const f32x4*>(W + 32 * m + 4 * g);
         wt[m][1] = *reinterpret_cast<const f32x4*>(W + 32 * m + 16 + 4 * g);
       }
       columns_of_b(0, fb[0]);
+      if constexpr (FAST) {
+        tc.store_whole(wc[1 - S], sc(1 - S), vc, rev);
+        tc.load(wc[1 - S], nc, c_ld);
+        nc += way * c_ld;
+      } else {
+        if (more) tc.store(wc[1 - S], sc(1 - S), at.held(k + 1), vc, rev);
+        if (k + 3 < chunks) any_c(k + 3, std::integral_constant<int, 1 - S>());
+      }
       ahead();
 #pragma unroll
-      for (int m = 0; m < 2; ++m) weigh_column<O, NW>(fc[m], wt[m][0], wt[m][1], wc[m]);
+      for (int m = 0; m < 2; ++m) weigh_column<O, NW>(fc[m], wt[m][0], wt[m][1], fw[m]);
 #pragma unroll
       for (int R = 0; R < KB; ++R) {
         if (R + 1 < KB) columns_of_b(R + 1, fb[(R + 1) & 1]);
-        else if (k + 1 < chunks) rows_of_a(sa(~k & 1), 0, first);
+        else if (more) rows_of_a(sa(1 - S), 0, first);
         ahead();
         if (R > 0) state_operand<O, NE>(E[2 * R - 2][0], E[2 * R - 1][0], e[R - 1]);
 #pragma unroll
@@ -717,35 +743,40 @@ __global__ __launch_bounds__(512, 1) __attribute__((amdgpu_waves_per_eu(2, 2))) 
 #pragma unroll
           for (int q = 0; q < NW; ++q)
 #pragma unroll
-            for (int x = 0; x < 2; ++x) E[2 * R + x][0] = O::mma(fb[R & 1][m][x], wc[m][q], E[2 * R + x][0]);
+            for (int x = 0; x < 2; ++x) E[2 * R + x][0] = O::mma(fb[R & 1][m][x], fw[m][q], E[2 * R + x][0]);
       }
       state_operand<O, NE>(E[2 * KB - 2][0], E[2 * KB - 1][0], e[KB - 1]);
-      if (k + 1 < chunks) inter(sa(~k & 1), sx(~k & 1), e, first);
+      if (more) inter(sa(1 - S), sx(1 - S), e, first);
       b0 = b0 == 2 ? 0 : b0 + 1;
+    };
+    int k = 0;
+    for (; k + 4 < quick; k += 2) {
+      turn(k, even, std::true_type{});
+      turn(k + 1, odd, std::true_type{});
+    }
+    for (; k < chunks; k += 2) {
+      turn(k, even, std::false_type{});
+      if (k + 1 < chunks) turn(k + 1, odd, std::false_type{});
     }
     at.finish(E, wave, lane);
     return;
   }
 
-  const bool rev = at.rev, out_f32 = j.out_f32 != 0, out_words = j.out_words != 0;
-  const int thread = threadIdx.x & 255, a_cols = j.a.cols, b_cols = j.b.cols, vc = at.vc;
-  const int64_t a_ld = j.a.ld, b_ld = j.b.ld, c_ld = j.c.ld, way = rev ? -kChunk : kChunk;
-  const bf16_t *pa = at.head(j.a), *pb = at.head(j.b), *pc = at.head(j.c) + at.v0;
+  const bool out_f32 = j.out_f32 != 0, out_words = j.out_words != 0;
+  const int a_cols = j.a.cols, b_cols = j.b.cols;
+  const int64_t a_ld = j.a.ld, b_ld = j.b.ld;
+  const bf16_t *pa = at.head(j.a), *pb = at.head(j.b), *na = pa, *nb = pb;  // n: the next whole chunk's first token
   typedef Tile<bf16_t, D, A> TA;
   typedef Tile<bf16_t, D, B> TB;
-  typedef Tile<bf16_t, V, C> TC;
   const TA ta(a_ld, a_cols, thread);
   const TB tb(b_ld, b_cols, thread);
-  const TC tc(c_ld, vc, thread);
-  typename TA::words wa;
-  typename TB::words wb;
-  TC::words wc;
-  auto any_ab = [&](int k) {
-    ta.load_any(wa, pa + at.token(k) * a_ld, a_ld, at.held(k), a_cols);
-    tb.load_any(wb, pb + at.token(k) * b_ld, b_ld, at.held(k), b_cols);
+  typename TA::words wa[2];  // of chunk k in set k & 1
+  typename TB::words wb[2];
+  auto any_ab = [&](int k, auto set) {
+    constexpr int S = decltype(set)::value;
+    ta.load_any(wa[S], pa + at.token(k) * a_ld, a_ld, at.held(k), a_cols);
+    tb.load_any(wb[S], pb + at.token(k) * b_ld, b_ld, at.held(k), b_cols);
   };
-  auto any_c = [&](int k) { tc.load_any(wc, pc + at.token(k) * c_ld, c_ld, at.held(k), vc); };
-  for (int i = wave; i < 8; i += 4) sp(i >> 2)[(pair_of(i & 1 ? 2 : 0, i & 1) * NS + (i >> 1 & 1)) * 128 + lane * 2 + 1] = half{};
   int at_a[KB], at_b[2 * KB];
 #pragma unroll
   for (int R = 0; R < KB; ++R) {
@@ -753,32 +784,30 @@ __global__ __launch_bounds__(512, 1) __attribute__((amdgpu_waves_per_eu(2, 2))) 
     at_b[2 * R] = B::row(32 * R, lane);
     at_b[2 * R + 1] = B::row(32 * R + 16, lane);
   }
-  // Scores transposed: rows j, columns p.  Three tiles a wave, without a branch, so that their
-  // products and what follows run beside each other; two waves' third is their first again.
-  int off_a[3], off_b[3], off_p[3];
-  float weight[3][4];
+  // Scores transposed: rows j, columns p.  A wave's 2 x 2 tiles share their operands; those above
+  // the diagonal are zeros.
+  const int t2 = wave < 2 ? 1 : 0, j2 = wave == 1 ? 1 : 0;
+  float weight[4][4];
   int keep = 0;  // a bit for each: on or below the diagonal
 #pragma unroll
-  for (int x = 0; x < 3; ++x) {
-    const int tile = wave + 4 * x < 10 ? wave + 4 * x : wave, tt = column_of(tile), jt = tile - tt * (tt + 1) / 2;
-    off_a[x] = 16 * tt * D;
-    off_b[x] = 16 * jt * D;
-    off_p[x] = pair_of(tt, jt / 2) * NS * 128 + (jt & 1);
+  for (int x = 0; x < 4; ++x)
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const int d = 16 * (tt - jt) + l16 - 4 * g - i;
+      const int d = 16 * (2 * (t2 - j2) + x / 2 - x % 2) + l16 - 4 * g - i;
       keep |= (d >= 0 ? 1 : 0) << (4 * x + i);
       weight[x][i] = j.s * power(at.g2, max(d, 0));
     }
-  }
   auto scores = [&](const uint16_t* A_, const uint16_t* B_, half* P) {
-    f32x4 s[3] = {};
-    frag fa[2][3], fb[2][3];
+    if (wave == 3) return;
+    A_ += 32 * t2 * D;
+    B_ += 32 * j2 * D;
+    f32x4 s[4] = {};
+    frag fa[2][2], fb[2][2];
     auto operands = [&](int R) {
 #pragma unroll
-      for (int x = 0; x < 3; ++x) {
-        fb[R & 1][x] = cat8(*reinterpret_cast<const u32x2*>(B_ + off_b[x] + at_b[2 * R]), *reinterpret_cast<const u32x2*>(B_ + off_b[x] + at_b[2 * R + 1]));
-        fa[R & 1][x] = as_bf16x8(*reinterpret_cast<const u32x4*>(A_ + off_a[x] + at_a[R]));
+      for (int x = 0; x < 2; ++x) {
+        fb[R & 1][x] = cat8(*reinterpret_cast<const u32x2*>(B_ + 16 * x * D + at_b[2 * R]), *reinterpret_cast<const u32x2*>(B_ + 16 * x * D + at_b[2 * R + 1]));
+        fa[R & 1][x] = as_bf16x8(*reinterpret_cast<const u32x4*>(A_ + 16 * x * D + at_a[R]));
       }
     };
     operands(0);
@@ -787,10 +816,10 @@ __global__ __launch_bounds__(512, 1) __attribute__((amdgpu_waves_per_eu(2, 2))) 
       if (R + 1 < KB) operands(R + 1);
       __builtin_amdgcn_sched_barrier(0);  // ahead of these products
 #pragma unroll
-      for (int x = 0; x < 3; ++x) s[x] = O::mma(fb[R & 1][x], fa[R & 1][x], s[x]);
+      for (int x = 0; x < 4; ++x) s[x] = O::mma(fb[R & 1][x % 2], fa[R & 1][x / 2], s[x]);
     }
 #pragma unroll
-    for (int x = 0; x < 3; ++x) {
+    for (int x = 0; x < 4; ++x) {
       f32x4 v;
 #pragma unroll
       for (int i = 0; i < 4; ++i)
@@ -798,7 +827,7 @@ __global__ __launch_bounds__(512, 1) __attribute__((amdgpu_waves_per_eu(2, 2))) 
       half o[NS];
       O::split<NS>(v, o);
 #pragma unroll
-      for (int q = 0; q < NS; ++q) P[off_p[x] + (q * 64 + lane) * 2] = o[q];
+      for (int q = 0; q < NS; ++q) P[((pair_of(2 * t2 + x / 2, j2) * NS + q) * 64 + lane) * 2 + x % 2] = o[q];
     }
   };
   const uint32_t out_row = uint32_t(plan.H) * uint32_t(j.c.cols), out_first = uint32_t(rev ? kChunk - 1 - l16 : l16) * out_row + 16 * wave + 4 * g;
@@ -837,59 +866,56 @@ __global__ __launch_bounds__(512, 1) __attribute__((amdgpu_waves_per_eu(2, 2))) 
     }
   };
   if (chunks > 0) {
-    any_ab(0);
-    ta.store(wa, sa(0), at.held(0), a_cols, rev);
-    tb.store(wb, sb(0), at.held(0), b_cols, rev);
-    any_c(0);
-    tc.store(wc, sc(0), at.held(0), vc, rev);
+    any_ab(0, even);
+    ta.store(wa[0], sa(0), at.held(0), a_cols, rev);
+    tb.store(wb[0], sb(0), at.held(0), b_cols, rev);
     if (chunks > 1) {
-      any_ab(1);
-      ta.store(wa, sa(1), at.held(1), a_cols, rev);
-      tb.store(wb, sb(1), at.held(1), b_cols, rev);
-      any_c(1);
+      any_ab(1, odd);
+      ta.store(wa[1], sa(1), at.held(1), a_cols, rev);
+      tb.store(wb[1], sb(1), at.held(1), b_cols, rev);
     }
-    if (chunks > 2) any_ab(2);
+    if (chunks > 2) any_ab(2, even);
+    if (chunks > 3) any_ab(3, odd);
     __syncthreads();
     scores(sa(0), sb(0), sp(0));
   }
-  const int quick = at.quick();
-  int k = 0, b1 = 1, b2 = 2;  // b's tiles of chunks k + 1 and k + 2
-  const bf16_t *na = pa, *nb = pb, *nc = pc;  // the next whole chunk's first token
-  if (quick > 3) {
-    na += at.token(3) * a_ld;
-    nb += at.token(3) * b_ld;
-    nc += at.token(2) * c_ld;
+  int b1 = 1, b2 = 2;  // b's tiles of chunks k + 1 and k + 2
+  if (quick > 4) {
+    na += at.token(4) * a_ld;
+    nb += at.token(4) * b_ld;
   }
-  for (; k + 3 < quick; ++k) {
+  auto turn = [&](int k, auto set, auto whole_chunks) {  // k & 1 = set
+    constexpr int S = decltype(set)::value;
+    constexpr bool FAST = decltype(whole_chunks)::value;
     __syncthreads();
-    ta.store_whole(wa, sa(k & 1), a_cols, rev);
-    tb.store_whole(wb, sb(b2), b_cols, rev);
-    tc.store_whole(wc, sc(~k & 1), vc, rev);
-    ta.load(wa, na, a_ld);
-    tb.load(wb, nb, b_ld);
-    tc.load(wc, nc, c_ld);
-    na += way * a_ld;
-    nb += way * b_ld;
-    nc += way * c_ld;
-    __builtin_amdgcn_sched_barrier(0);  // asked for now, not where the scheduler finds a register for them
-    scores(sa(~k & 1), sb(b1), sp(~k & 1));
-    outputs(k, kChunk, std::true_type{});
-    b1 = b2;
-    b2 = b2 == 2 ? 0 : b2 + 1;
-  }
-  for (; k < chunks; ++k) {
-    __syncthreads();
-    if (k + 2 < chunks) {
-      ta.store(wa, sa(k & 1), at.held(k + 2), a_cols, rev);
-      tb.store(wb, sb(b2), at.held(k + 2), b_cols, rev);
+    if constexpr (FAST) {
+      ta.store_whole(wa[S], sa(S), a_cols, rev);
+      tb.store_whole(wb[S], sb(b2), b_cols, rev);
+      ta.load(wa[S], na, a_ld);
+      tb.load(wb[S], nb, b_ld);
+      na += way * a_ld;
+      nb += way * b_ld;
+    } else {
+      if (k + 2 < chunks) {
+        ta.store(wa[S], sa(S), at.held(k + 2), a_cols, rev);
+        tb.store(wb[S], sb(b2), at.held(k + 2), b_cols, rev);
+      }
+      if (k + 4 < chunks) any_ab(k + 4, set);
     }
-    if (k + 1 < chunks) tc.store(wc, sc(~k & 1), at.held(k + 1), vc, rev);
-    if (k + 3 < chunks) any_ab(k + 3);
-    if (k + 2 < chunks) any_c(k + 2);
-    if (k + 1 < chunks) scores(sa(~k & 1), sb(b1), sp(~k & 1));
-    outputs(k, at.held(k), std::false_type{});
+    __builtin_amdgcn_sched_barrier(0);  // asked for now, not where the scheduler finds a register for them
+    if (FAST || k + 1 < chunks) scores(sa(1 - S), sb(b1), sp(1 - S));
+    outputs(k, at.held(k), whole_chunks);
     b1 = b2;
     b2 = b2 == 2 ? 0 : b2 + 1;
+  };
+  int k = 0;
+  for (; k + 5 < quick; k += 2) {
+    turn(k, even, std::true_type{});
+    turn(k + 1, odd, std::true_type{});
+  }
+  for (; k < chunks; k += 2) {
+    turn(k, even, std::false_type{});
+    if (k + 1 < chunks) turn(k + 1, odd, std::false_type{});
   }
 }
 
