@@ -83,8 +83,9 @@ WalkJob job_of(const WalkSide& x, const WalkSide& b, const WalkSide& c, bool rev
 void to(WalkJob& j, void* out, bool f32, size_t elem) {
   j.out = out;
   j.out_f32 = f32;
-  const size_t word = 4 * (f32 ? 4 : elem);
-  j.out_words = j.c.cols % 4 == 0 && reinterpret_cast<uintptr_t>(out) % word == 0;
+  const uintptr_t at = reinterpret_cast<uintptr_t>(out);
+  const int cols = j.c.cols, four = cols % 4 == 0 && at % (4 * (f32 ? 4 : elem)) == 0;
+  j.out_words = four && (f32 || elem == 4 || (cols % 8 == 0 && at % 16 == 0)) ? 2 : four;
 }
 hipError_t run(const m3_linear_attention_args& a, WalkPlan& p, bool states, hipStream_t s) {
   const WalkJob& f = p.job[0];  // the others' states have its shape

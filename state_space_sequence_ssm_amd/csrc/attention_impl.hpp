@@ -157,6 +157,25 @@ struct SwizzledB {
   }
 };
 
+// c of the two-role walk, 64 columns.  An operand's 16 columns are 4 of each of four words of 8 of
+// one half, so that two operands of a token are 16 bytes of each of its output's four lanes:
+// tile w's column m is 32 (w / 2) + 8 (m / 4) + 4 (w % 2) + m % 4.  Units of 8 bytes; 8 rows of
+// the four of a tile meet every bank once.
+struct SwizzledC {
+  static constexpr int S = 64, kBytes = kChunk * 64 * 2;
+  static __device__ __forceinline__ int column(int tile, int m) { return 32 * (tile >> 1) + 8 * (m >> 2) + 4 * (tile & 1) + (m & 3); }
+  static __device__ __forceinline__ int mix(int r) { return ((r >> 2 & 1) << 3) | (r >> 1 & 1); }
+  static __device__ __forceinline__ void put(uint16_t* t, int r, int c, u32x4 w) {
+    *reinterpret_cast<u32x2*>(t + r * S + ((c / 4) ^ mix(r)) * 4) = u32x2{w[0], w[1]};
+    *reinterpret_cast<u32x2*>(t + r * S + ((c / 4 + 1) ^ mix(r)) * 4) = u32x2{w[2], w[3]};
+  }
+  // where the lane points for a transposing read of a tile's columns, rows 4 g + 0..3 of 16
+  static __device__ __forceinline__ int col(int tile, int lane) {
+    const int r = (lane >> 4) * 4 + ((lane & 15) >> 2);
+    return r * S + ((column(tile, 4 * (lane & 3)) / 4) ^ mix(r)) * 4;
+  }
+};
+
 // 64 tokens' rows of D elements (columns past the head's and rows past the chunk's zero) on
 // their way through registers into LDS, 16-byte words over 256 threads.  Rows are loaded in
 // the tokens' order and stored in the walk's.
@@ -248,7 +267,7 @@ __device__ __forceinline__ void put4(bool f32, bool words, char* out, uint32_t a
 // ---------------------------------------------------------------- what a block walks
 // One segment of one (item, head) for V columns of c: 4 waves hold V / 4 columns of the state
 // each, all its rows, in accumulators.
-template <typename T, int V, bool STATES>
+template <typename T, int V, bool STATES, bool MIXED = false>
 struct Place {
   const WalkPlan& plan;
   const WalkJob& j;
@@ -300,7 +319,10 @@ struct Place {
     for (int64_t i = threadIdx.x; i < int64_t(last - first) * vc; i += threads)
       o[((int64_t(item) * plan.L + first + i / vc) * plan.H + h) * j.c.cols + v0 + i % vc] = T{};
   }
-  // the state's columns 16 (wave NCT + ct) + l16, rows 16 r + 4 g + i
+  // the state's rows 16 r + 4 g + i, columns:
+  static __device__ __forceinline__ int column(int tile, int lane) {
+    return MIXED ? SwizzledC::column(tile, lane & 15) : 16 * tile + (lane & 15);
+  }
   template <int NR, int NCT>
   __device__ __forceinline__ void start(f32x4 (&E)[NR][NCT], int wave, int lane) const {
     const float* init = nullptr;
@@ -309,7 +331,7 @@ struct Place {
     for (int r = 0; r < NR; ++r)
 #pragma unroll
       for (int ct = 0; ct < NCT; ++ct) {
-        const int v = 16 * (wave * NCT + ct) + (lane & 15);
+        const int v = column(wave * NCT + ct, lane);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const int row = 16 * r + 4 * (lane >> 4) + i;
@@ -325,7 +347,7 @@ struct Place {
     for (int r = 0; r < NR; ++r)
 #pragma unroll
       for (int ct = 0; ct < NCT; ++ct) {
-        const int v = 16 * (wave * NCT + ct) + (lane & 15);
+        const int v = column(wave * NCT + ct, lane);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const int row = 16 * r + 4 * (lane >> 4) + i;
@@ -335,7 +357,7 @@ struct Place {
   }
   // chunks in front of this one are whole ones of whole words
   __device__ __forceinline__ int quick() const {
-    const bool words = (STATES || (j.a.words && j.out_words && vc == V)) && j.b.words && j.c.words;
+    const bool words = (STATES || (j.a.words && j.out_words == 2 && vc == V)) && j.b.words && j.c.words;
     return words ? (rest == kChunk ? chunks : chunks - 1) : 0;
   }
 };
@@ -600,7 +622,7 @@ __global__ __launch_bounds__(256, (KB * NCT <= 4 ? 2 : 1)) void walk_kernel(Walk
 template <int KB>
 struct PairLds {
   static constexpr int D = 32 * KB;
-  static constexpr int tA = SwizzledA<D>::kBytes, tB = SwizzledB<D>::kBytes, tC = SwizzledB<64>::kBytes, tP = 6 * 2 * 64 * 16, tX = 16 * 64 * 16;
+  static constexpr int tA = SwizzledA<D>::kBytes, tB = SwizzledB<D>::kBytes, tC = SwizzledC::kBytes, tP = 6 * 2 * 64 * 16, tX = 16 * 64 * 16;
   static constexpr int a = 0, b = a + 2 * tA, c = b + 3 * tB, p = c + 2 * tC, x = p + 2 * tP, w = x + 2 * tX, end = w + 2 * kChunk * 4;
   static_assert(end <= 160 * 1024, "a compute unit's LDS");
 };
@@ -615,7 +637,7 @@ __global__ __launch_bounds__(512, 1) __attribute__((amdgpu_waves_per_eu(2, 2))) 
   static_assert(NS == 2, "room for the scores");
   typedef SwizzledA<D> A;
   typedef SwizzledB<D> B;
-  typedef SwizzledB<V> C;
+  typedef SwizzledC C;
   extern __shared__ __attribute__((aligned(16))) char lds[];
   auto sa = [&](int i) { return reinterpret_cast<uint16_t*>(lds + M::a + i * M::tA); };
   auto sb = [&](int i) { return reinterpret_cast<uint16_t*>(lds + M::b + i * M::tB); };
@@ -625,16 +647,15 @@ __global__ __launch_bounds__(512, 1) __attribute__((amdgpu_waves_per_eu(2, 2))) 
   float* sw = reinterpret_cast<float*>(lds + M::w);
   const int lane = threadIdx.x & 63, role = __builtin_amdgcn_readfirstlane(threadIdx.x >> 8), wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) & 3,
             g = lane >> 4, l16 = lane & 15;
-  const Place<bf16_t, V, false> at(plan, block_on_xcd());
+  const Place<bf16_t, V, false, true> at(plan, block_on_xcd());
   const WalkJob& j = at.j;
   if (j.zero_tail) at.zero_tail(512);
   if (at.idle) return;
   put_weights(sw, at.g2, j, at.rest);
   const Powers pw(at.g2, j, lane);
   const int chunks = at.chunks;
-  // c's operands of tokens 32 m.. at this wave's columns
-  const int at_c = C::col(16 * wave, lane);
-  auto column = [&](const uint16_t* t, int m) { return cat8(lds_read_tr(t + at_c + 32 * m * V), lds_read_tr(t + at_c + (32 * m + 16) * V)); };
+  // c's operand of tokens 32 m.. and a tile's columns, from where the lane points
+  auto column = [&](const uint16_t* t, int m) { return cat8(lds_read_tr(t + 32 * m * V), lds_read_tr(t + (32 * m + 16) * V)); };
 
   const bool rev = at.rev;
   const int thread = threadIdx.x & 255, vc = at.vc, quick = at.quick();
@@ -652,6 +673,7 @@ __global__ __launch_bounds__(512, 1) __attribute__((amdgpu_waves_per_eu(2, 2))) 
     auto any_c = [&](int k, auto set) { tc.load_any(wc[decltype(set)::value], pc + at.token(k) * c_ld, c_ld, at.held(k), vc); };
     if (quick > 3) nc += at.token(3) * c_ld;
     const float whole = power(at.g2, kChunk), whole_rest = power(at.g2, max(0, at.rest));
+    const int at_c = C::col(wave, lane);
     int at_a[KB], at_b[2 * KB];
 #pragma unroll
     for (int R = 0; R < KB; ++R) at_a[R] = A::row(R, lane);
@@ -714,7 +736,7 @@ __global__ __launch_bounds__(512, 1) __attribute__((amdgpu_waves_per_eu(2, 2))) 
       f32x4 wt[2][2];
 #pragma unroll
       for (int m = 0; m < 2; ++m) {
-        fc[m] = column(ct, m);
+        fc[m] = column(ct + at_c, m);
         wt[m][0] = *reinterpret_cast<const f32x4*>(W + 32 * m + 4 * g);
         wt[m][1] = *reinterpret_cast<const f32x4*>(W + 32 * m + 16 + 4 * g);
       }
@@ -830,38 +852,56 @@ __global__ __launch_bounds__(512, 1) __attribute__((amdgpu_waves_per_eu(2, 2))) 
       for (int q = 0; q < NS; ++q) P[((pair_of(2 * t2 + x / 2, j2) * NS + q) * 64 + lane) * 2 + x % 2] = o[q];
     }
   };
-  const uint32_t out_row = uint32_t(plan.H) * uint32_t(j.c.cols), out_first = uint32_t(rev ? kChunk - 1 - l16 : l16) * out_row + 16 * wave + 4 * g;
+  // Outputs: a wave takes 16 tokens, 16 wave + l16, and all 64 columns of them: a lane's are 8 g..
+  // and 32 + 8 g.., whole words of 16 bytes.
+  const uint32_t out_row = uint32_t(plan.H) * uint32_t(j.c.cols);
   const int64_t out_head = int64_t(at.h) * j.c.cols + at.v0, out_token = int64_t(plan.H) * j.c.cols;
   const int out_size = out_f32 ? 4 : 2;
+  int at_c[4];
+#pragma unroll
+  for (int ct = 0; ct < 4; ++ct) at_c[ct] = C::col(ct, lane);
   auto outputs = [&](int k, int nc, auto fast) {
     constexpr bool FAST = decltype(fast)::value;
-    const half* P = sp(k & 1);
+    const half* P = sp(k & 1) + (pair_of(wave, 0) * NS * 64 + lane) * 2;
     const uint16_t* t = sc(k & 1);
     f32x4 acc[4];
-    frag fc[2], fp[6][NS];
+    auto part = [&](int m) {
+      frag fc[4], fp[NS];
 #pragma unroll
-    for (int m = 0; m < 2; ++m) fc[m] = column(t, m);
+      for (int ct = 0; ct < 4; ++ct) fc[ct] = column(t + at_c[ct], m);
 #pragma unroll
-    for (int tt = 0; tt < 4; ++tt) acc[tt] = sx(k & 1)[(tt * 4 + wave) * 64 + lane];
+      for (int q = 0; q < NS; ++q) fp[q] = *reinterpret_cast<const frag*>(P + (m * NS + q) * 128);
+      if (m == 0) {
 #pragma unroll
-    for (int x = 0; x < 6; ++x)
-#pragma unroll
-      for (int q = 0; q < NS; ++q) fp[x][q] = *reinterpret_cast<const frag*>(P + ((x * NS + q) * 64 + lane) * 2);
-    __builtin_amdgcn_sched_barrier(0);  // all asked for ahead of the products
-#pragma unroll
-    for (int m = 0; m < 2; ++m)
+        for (int ct = 0; ct < 4; ++ct) acc[ct] = sx(k & 1)[(wave * 4 + ct) * 64 + lane];
+      }
+      __builtin_amdgcn_sched_barrier(0);  // all asked for ahead of the products
 #pragma unroll
       for (int q = 0; q < NS; ++q)
 #pragma unroll
-        for (int tt = 2 * m; tt < 4; ++tt) acc[tt] = O::mma(fc[m], fp[pair_of(tt, m)][q], acc[tt]);
+        for (int ct = 0; ct < 4; ++ct) acc[ct] = O::mma(fc[ct], fp[q], acc[ct]);
+    };
+    part(0);
+    if (wave >= 2) part(1);
     char* out = static_cast<char*>(j.out) + (at.token(k) * out_token + out_head) * out_size;
+    const int p = 16 * wave + l16;
+    const uint32_t first = uint32_t(rev ? nc - 1 - p : p) * out_row + 8 * g;
+    if constexpr (FAST) {
+      if (out_f32) {
 #pragma unroll
-    for (int tt = 0; tt < 4; ++tt) {
-      if constexpr (FAST) {
-        put4<bf16_t, true>(out_f32, true, out, out_first + uint32_t(rev ? -16 * tt : 16 * tt) * out_row, acc[tt], 4);
+        for (int ct = 0; ct < 4; ++ct) *reinterpret_cast<f32x4*>(out + (first + 32 * (ct >> 1) + 4 * (ct & 1)) * 4u) = acc[ct];
       } else {
-        const int p = 16 * tt + l16, v = 16 * wave + 4 * g;
-        if (p < nc && v < vc) put4<bf16_t, false>(out_f32, out_words, out, uint32_t(rev ? nc - 1 - p : p) * out_row + v, acc[tt], vc - v);
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          const u32x2 lo = pack4(acc[2 * x]), hi = pack4(acc[2 * x + 1]);
+          *reinterpret_cast<u32x4*>(out + (first + 32 * x) * 2u) = u32x4{lo[0], lo[1], hi[0], hi[1]};
+        }
+      }
+    } else if (p < nc) {
+#pragma unroll
+      for (int ct = 0; ct < 4; ++ct) {
+        const int v = 32 * (ct >> 1) + 4 * (ct & 1), n = vc - 8 * g - v;
+        if (n > 0) put4<bf16_t, false>(out_f32, out_words, out, first + v, acc[ct], n);
       }
     }
   };

@@ -35,7 +35,8 @@ struct WalkSide {
 struct WalkJob {
   WalkSide a, b, c;
   void* out;  // [Bt, L, H, c.cols]
-  int out_f32, out_words, zero_tail;
+  int out_f32, zero_tail;
+  int out_words;  // 1: four columns are an aligned word, 2: 16 bytes are
   const float* init;  // [Bt, H, .] or null
   float* fin;         // likewise
   int64_t sn, sv;     // a state's element (n of b, v of c) is at n sn + v sv
