@@ -616,9 +616,11 @@ __global__ __launch_bounds__(256, (KB * NCT <= 4 ? 2 : 1)) void walk_kernel(Walk
 // update.  The other four move tiles, form the scores and the outputs.  So matrix instructions
 // of the one run beside loads, conversions and waits of the other, and a chunk takes one
 // barrier: between two of them, for chunk k,
-//   state waves: c of k + 1 into LDS and k + 3's asked for, update with k, then a E for k + 1;
-//   others: a and b of k + 2 into LDS and k + 4's asked for, scores of k + 1 (three waves, a
-//   quarter of the triangle's 2 x 2 blocks of 2 x 2 tiles each), scores times c and out for k.
+//   state waves: b of k + 2 and c of k + 1 into LDS and those two further on asked for, update
+//   with k, then a E for k + 1;
+//   others: a of k + 2 into LDS and k + 4's asked for, scores of k + 1 (two waves 2 x 2 tiles
+//   of the triangle's lower half each, two 1 x 2 of its upper), scores times c and out for k
+//   (the upper half's waves have the half with more of it).
 template <int KB>
 struct PairLds {
   static constexpr int D = 32 * KB;
@@ -666,12 +668,20 @@ __global__ __launch_bounds__(512, 1) __attribute__((amdgpu_waves_per_eu(2, 2))) 
     f32x4 E[2 * KB][1];
     at.start(E, wave, lane);
     typedef Tile<bf16_t, V, C> TC;
-    const int64_t c_ld = j.c.ld;
+    typedef Tile<bf16_t, D, B> TB;
+    const int b_cols = j.b.cols;
+    const int64_t b_ld = j.b.ld, c_ld = j.c.ld;
+    const TB tb(b_ld, b_cols, thread);
     const TC tc(c_ld, vc, thread);
+    typename TB::words wb[2];
     TC::words wc[2];  // of chunk k in set k & 1
-    const bf16_t *pc = at.head(j.c) + at.v0, *nc = pc;
+    const bf16_t *pb = at.head(j.b), *nb = pb, *pc = at.head(j.c) + at.v0, *nc = pc;  // n: the next whole chunk's first token
+    auto any_b = [&](int k, auto set) { tb.load_any(wb[decltype(set)::value], pb + at.token(k) * b_ld, b_ld, at.held(k), b_cols); };
     auto any_c = [&](int k, auto set) { tc.load_any(wc[decltype(set)::value], pc + at.token(k) * c_ld, c_ld, at.held(k), vc); };
-    if (quick > 3) nc += at.token(3) * c_ld;
+    if (quick > 4) {
+      nb += at.token(4) * b_ld;
+      nc += at.token(3) * c_ld;
+    }
     const float whole = power(at.g2, kChunk), whole_rest = power(at.g2, max(0, at.rest));
     const int at_c = C::col(wave, lane);
     int at_a[KB], at_b[2 * KB];
@@ -706,17 +716,27 @@ __global__ __launch_bounds__(512, 1) __attribute__((amdgpu_waves_per_eu(2, 2))) 
     };
     frag e[KB][NE], first[4];
     if (chunks > 0) {
+      any_b(0, even);
+      tb.store(wb[0], sb(0), at.held(0), b_cols, rev);
       any_c(0, even);
       tc.store(wc[0], sc(0), at.held(0), vc, rev);
-      if (chunks > 1) any_c(1, odd);
-      if (chunks > 2) any_c(2, even);
+      if (chunks > 1) {
+        any_b(1, odd);
+        tb.store(wb[1], sb(1), at.held(1), b_cols, rev);
+        any_c(1, odd);
+      }
+      if (chunks > 2) {
+        any_b(2, even);
+        any_c(2, even);
+      }
+      if (chunks > 3) any_b(3, odd);
       __syncthreads();
       rows_of_a(sa(0), 0, first);
 #pragma unroll
       for (int R = 0; R < KB; ++R) state_operand<O, NE>(E[2 * R][0], E[2 * R + 1][0], e[R]);
       inter(sa(0), sx(0), e, first);
     }
-    int b0 = 0;
+    int b0 = 0, b2 = 2;  // b's tiles of chunks k and k + 2
     auto turn = [&](int k, auto set, auto whole_chunks) {  // k & 1 = set
       constexpr int S = decltype(set)::value;
       constexpr bool FAST = decltype(whole_chunks)::value;
@@ -724,13 +744,13 @@ __global__ __launch_bounds__(512, 1) __attribute__((amdgpu_waves_per_eu(2, 2))) 
       const float f = full ? whole : whole_rest;
       const float* W = sw + (full ? 0 : kChunk);
       __syncthreads();
-      const uint16_t *tb = sb(b0), *ct = sc(S);
+      const uint16_t *bt = sb(b0), *ct = sc(S);
       auto columns_of_b = [&](int R, frag (&o)[2][2]) {
 #pragma unroll
         for (int m = 0; m < 2; ++m)
 #pragma unroll
           for (int x = 0; x < 2; ++x)
-            o[m][x] = cat8(lds_read_tr(tb + at_b[2 * R + x] + 32 * m * D), lds_read_tr(tb + at_b[2 * R + x] + (32 * m + 16) * D));
+            o[m][x] = cat8(lds_read_tr(bt + at_b[2 * R + x] + 32 * m * D), lds_read_tr(bt + at_b[2 * R + x] + (32 * m + 16) * D));
       };
       frag fc[2], fw[2][NW], fb[2][2][2];
       f32x4 wt[2][2];
@@ -742,10 +762,15 @@ __global__ __launch_bounds__(512, 1) __attribute__((amdgpu_waves_per_eu(2, 2))) 
       }
       columns_of_b(0, fb[0]);
       if constexpr (FAST) {
+        tb.store_whole(wb[S], sb(b2), b_cols, rev);
         tc.store_whole(wc[1 - S], sc(1 - S), vc, rev);
+        tb.load(wb[S], nb, b_ld);
         tc.load(wc[1 - S], nc, c_ld);
+        nb += way * b_ld;
         nc += way * c_ld;
       } else {
+        if (k + 2 < chunks) tb.store(wb[S], sb(b2), at.held(k + 2), b_cols, rev);
+        if (k + 4 < chunks) any_b(k + 4, set);
         if (more) tc.store(wc[1 - S], sc(1 - S), at.held(k + 1), vc, rev);
         if (k + 3 < chunks) any_c(k + 3, std::integral_constant<int, 1 - S>());
       }
@@ -770,9 +795,10 @@ __global__ __launch_bounds__(512, 1) __attribute__((amdgpu_waves_per_eu(2, 2))) 
       state_operand<O, NE>(E[2 * KB - 2][0], E[2 * KB - 1][0], e[KB - 1]);
       if (more) inter(sa(1 - S), sx(1 - S), e, first);
       b0 = b0 == 2 ? 0 : b0 + 1;
+      b2 = b2 == 2 ? 0 : b2 + 1;
     };
     int k = 0;
-    for (; k + 4 < quick; k += 2) {
+    for (; k + 5 < quick; k += 2) {
       turn(k, even, std::true_type{});
       turn(k + 1, odd, std::true_type{});
     }
@@ -785,19 +811,15 @@ __global__ __launch_bounds__(512, 1) __attribute__((amdgpu_waves_per_eu(2, 2))) 
   }
 
   const bool out_f32 = j.out_f32 != 0, out_words = j.out_words != 0;
-  const int a_cols = j.a.cols, b_cols = j.b.cols;
-  const int64_t a_ld = j.a.ld, b_ld = j.b.ld;
-  const bf16_t *pa = at.head(j.a), *pb = at.head(j.b), *na = pa, *nb = pb;  // n: the next whole chunk's first token
+  const int a_cols = j.a.cols;
+  const int64_t a_ld = j.a.ld;
+  const bf16_t *pa = at.head(j.a), *na = pa;  // n: the next whole chunk's first token
   typedef Tile<bf16_t, D, A> TA;
-  typedef Tile<bf16_t, D, B> TB;
   const TA ta(a_ld, a_cols, thread);
-  const TB tb(b_ld, b_cols, thread);
   typename TA::words wa[2];  // of chunk k in set k & 1
-  typename TB::words wb[2];
-  auto any_ab = [&](int k, auto set) {
+  auto any_a = [&](int k, auto set) {
     constexpr int S = decltype(set)::value;
     ta.load_any(wa[S], pa + at.token(k) * a_ld, a_ld, at.held(k), a_cols);
-    tb.load_any(wb[S], pb + at.token(k) * b_ld, b_ld, at.held(k), b_cols);
   };
   int at_a[KB], at_b[2 * KB];
 #pragma unroll
@@ -806,31 +828,31 @@ __global__ __launch_bounds__(512, 1) __attribute__((amdgpu_waves_per_eu(2, 2))) 
     at_b[2 * R] = B::row(32 * R, lane);
     at_b[2 * R + 1] = B::row(32 * R + 16, lane);
   }
-  // Scores transposed: rows j, columns p.  A wave's 2 x 2 tiles share their operands; those above
-  // the diagonal are zeros.
-  const int t2 = wave < 2 ? 1 : 0, j2 = wave == 1 ? 1 : 0;
+  // Scores transposed: rows j, columns p.  A wave's tiles share their operands: tokens' tiles t0
+  // (and t0 + 1) by tiles j0 and j0 + 1; those above the diagonal are zeros.
+  const int t0 = wave < 2 ? 2 : 3 - wave, j0 = wave == 1 ? 2 : 0;
   float weight[4][4];
   int keep = 0;  // a bit for each: on or below the diagonal
 #pragma unroll
   for (int x = 0; x < 4; ++x)
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const int d = 16 * (2 * (t2 - j2) + x / 2 - x % 2) + l16 - 4 * g - i;
+      const int d = 16 * (t0 - j0 + x / 2 - x % 2) + l16 - 4 * g - i;
       keep |= (d >= 0 ? 1 : 0) << (4 * x + i);
       weight[x][i] = j.s * power(at.g2, max(d, 0));
     }
-  auto scores = [&](const uint16_t* A_, const uint16_t* B_, half* P) {
-    if (wave == 3) return;
-    A_ += 32 * t2 * D;
-    B_ += 32 * j2 * D;
-    f32x4 s[4] = {};
-    frag fa[2][2], fb[2][2];
+  auto scores_of = [&](const uint16_t* A_, const uint16_t* B_, half* P, auto tiles) {
+    constexpr int NT = decltype(tiles)::value;
+    A_ += 16 * t0 * D;
+    B_ += 16 * j0 * D;
+    f32x4 s[2 * NT] = {};
+    frag fa[2][NT], fb[2][2];
     auto operands = [&](int R) {
 #pragma unroll
-      for (int x = 0; x < 2; ++x) {
+      for (int x = 0; x < 2; ++x)
         fb[R & 1][x] = cat8(*reinterpret_cast<const u32x2*>(B_ + 16 * x * D + at_b[2 * R]), *reinterpret_cast<const u32x2*>(B_ + 16 * x * D + at_b[2 * R + 1]));
-        fa[R & 1][x] = as_bf16x8(*reinterpret_cast<const u32x4*>(A_ + 16 * x * D + at_a[R]));
-      }
+#pragma unroll
+      for (int x = 0; x < NT; ++x) fa[R & 1][x] = as_bf16x8(*reinterpret_cast<const u32x4*>(A_ + 16 * x * D + at_a[R]));
     };
     operands(0);
 #pragma unroll
@@ -838,10 +860,10 @@ __global__ __launch_bounds__(512, 1) __attribute__((amdgpu_waves_per_eu(2, 2))) 
       if (R + 1 < KB) operands(R + 1);
       __builtin_amdgcn_sched_barrier(0);  // ahead of these products
 #pragma unroll
-      for (int x = 0; x < 4; ++x) s[x] = O::mma(fb[R & 1][x % 2], fa[R & 1][x / 2], s[x]);
+      for (int x = 0; x < 2 * NT; ++x) s[x] = O::mma(fb[R & 1][x % 2], fa[R & 1][x / 2], s[x]);
     }
 #pragma unroll
-    for (int x = 0; x < 4; ++x) {
+    for (int x = 0; x < 2 * NT; ++x) {
       f32x4 v;
 #pragma unroll
       for (int i = 0; i < 4; ++i)
@@ -849,8 +871,12 @@ __global__ __launch_bounds__(512, 1) __attribute__((amdgpu_waves_per_eu(2, 2))) 
       half o[NS];
       O::split<NS>(v, o);
 #pragma unroll
-      for (int q = 0; q < NS; ++q) P[((pair_of(2 * t2 + x / 2, j2) * NS + q) * 64 + lane) * 2 + x % 2] = o[q];
+      for (int q = 0; q < NS; ++q) P[((pair_of(t0 + x / 2, j0 / 2) * NS + q) * 64 + lane) * 2 + x % 2] = o[q];
     }
+  };
+  auto scores = [&](const uint16_t* A_, const uint16_t* B_, half* P) {
+    if (wave < 2) scores_of(A_, B_, P, std::integral_constant<int, 2>());
+    else scores_of(A_, B_, P, std::integral_constant<int, 1>());
   };
   // Outputs: a wave takes 16 tokens, 16 wave + l16, and all 64 columns of them: a lane's are 8 g..
   // and 32 + 8 g.., whole words of 16 bytes.
@@ -906,47 +932,35 @@ __global__ __launch_bounds__(512, 1) __attribute__((amdgpu_waves_per_eu(2, 2))) 
     }
   };
   if (chunks > 0) {
-    any_ab(0, even);
+    any_a(0, even);
     ta.store(wa[0], sa(0), at.held(0), a_cols, rev);
-    tb.store(wb[0], sb(0), at.held(0), b_cols, rev);
     if (chunks > 1) {
-      any_ab(1, odd);
+      any_a(1, odd);
       ta.store(wa[1], sa(1), at.held(1), a_cols, rev);
-      tb.store(wb[1], sb(1), at.held(1), b_cols, rev);
     }
-    if (chunks > 2) any_ab(2, even);
-    if (chunks > 3) any_ab(3, odd);
+    if (chunks > 2) any_a(2, even);
+    if (chunks > 3) any_a(3, odd);
     __syncthreads();
     scores(sa(0), sb(0), sp(0));
   }
-  int b1 = 1, b2 = 2;  // b's tiles of chunks k + 1 and k + 2
-  if (quick > 4) {
-    na += at.token(4) * a_ld;
-    nb += at.token(4) * b_ld;
-  }
+  int b1 = 1;  // b's tile of chunk k + 1
+  if (quick > 4) na += at.token(4) * a_ld;
   auto turn = [&](int k, auto set, auto whole_chunks) {  // k & 1 = set
     constexpr int S = decltype(set)::value;
     constexpr bool FAST = decltype(whole_chunks)::value;
     __syncthreads();
     if constexpr (FAST) {
       ta.store_whole(wa[S], sa(S), a_cols, rev);
-      tb.store_whole(wb[S], sb(b2), b_cols, rev);
       ta.load(wa[S], na, a_ld);
-      tb.load(wb[S], nb, b_ld);
       na += way * a_ld;
-      nb += way * b_ld;
     } else {
-      if (k + 2 < chunks) {
-        ta.store(wa[S], sa(S), at.held(k + 2), a_cols, rev);
-        tb.store(wb[S], sb(b2), at.held(k + 2), b_cols, rev);
-      }
-      if (k + 4 < chunks) any_ab(k + 4, set);
+      if (k + 2 < chunks) ta.store(wa[S], sa(S), at.held(k + 2), a_cols, rev);
+      if (k + 4 < chunks) any_a(k + 4, set);
     }
     __builtin_amdgcn_sched_barrier(0);  // asked for now, not where the scheduler finds a register for them
     if (FAST || k + 1 < chunks) scores(sa(1 - S), sb(b1), sp(1 - S));
     outputs(k, at.held(k), whole_chunks);
-    b1 = b2;
-    b2 = b2 == 2 ? 0 : b2 + 1;
+    b1 = b1 == 2 ? 0 : b1 + 1;
   };
   int k = 0;
   for (; k + 5 < quick; k += 2) {
