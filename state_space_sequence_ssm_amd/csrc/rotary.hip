@@ -147,6 +147,33 @@ __device__ __forceinline__ void angles_of(const Units<V, NU, RAG, ADJ>& u, const
     for (int j = 0; j < V; ++j) o[i][j] = u.pair[i] < 0 ? float2{1.f, 0.f} : cs[u.pair[i] + j];
 }
 
+// A lane's gains (1 without them), kept in registers while a wave walks tokens: read anew for
+// each head they were half of the loads.
+template <int V, int NU>
+struct Gains {
+  float a[NU][V], b[NU][V];
+  template <bool RAG, bool ADJ>
+  __device__ __forceinline__ Gains(const float* w, const Units<V, NU, RAG, ADJ>& u) {
+#pragma unroll
+    for (int i = 0; i < NU; ++i)
+#pragma unroll
+      for (int j = 0; j < V; ++j) {
+        a[i][j] = w == nullptr ? 1.f : w[u.a[i] + j];
+        b[i][j] = w == nullptr ? 1.f : w[u.b[i] + j];
+      }
+  }
+};
+
+// Turn `it` of a wave over the heads of a token: q's first, then k's.
+struct Head {
+  int k, mine, head;
+  __device__ __forceinline__ Head(const RopeP& p, int it, int teams, int lane) {
+    k = it >= p.its[0] ? 1 : 0;
+    mine = (it - (k ? p.its[0] : 0)) * teams + (lane >> p.lgteam);
+    head = min(mine, p.heads[k] - 1);
+  }
+};
+
 template <typename T, int V, int NU, bool RAG, bool ADJ>
 __global__ __launch_bounds__(256) void rope_kernel(RopeP p) {
   extern __shared__ float2 lds[];
@@ -157,25 +184,37 @@ __global__ __launch_bounds__(256) void rope_kernel(RopeP p) {
   const int team = 1 << p.lgteam, teams = 64 >> p.lgteam;
   const Units<V, NU, RAG, ADJ> u(p, lane & (team - 1), team);
   const int all = p.its[0] + p.its[1], each = (all + p.splits - 1) / p.splits;
+  const Gains<V, NU> wq(p.w[0], u), wk(p.w[1], u);
   for (int64_t row = walker < p.walkers ? walker : p.rows; row < p.rows; row += p.walkers) {
     const int t = int(row % p.L);
     if (t >= item_length(p.lengths, int(row / p.L), p.L)) continue;
     if (p.R > 0) angles(p, cs, p.positions == nullptr ? p.start + t : p.positions[row], lane);
     float2 turn[NU][V];
     angles_of<V, NU, RAG, ADJ>(u, cs, turn);
-    for (int it = split * each; it < min(all, (split + 1) * each); ++it) {
-      const int k = it >= p.its[0] ? 1 : 0;
-      const int head = min((it - (k ? p.its[0] : 0)) * teams + (lane >> p.lgteam), p.heads[k] - 1);
-      const T* x = static_cast<const T*>(p.x[k]) + row * p.ld[k] + int64_t(head) * p.D;
-      T* y = static_cast<T*>(p.y[k]) + (row * p.heads[k] + head) * p.D;
-      const float* w = p.w[k];
+    const int last = min(all, (split + 1) * each);
+    Pack<T, V> qa[NU], qb[NU];
+    auto load = [&](int it) {
+      const Head h(p, it, teams, lane);
+      const T* x = static_cast<const T*>(p.x[h.k]) + row * p.ld[h.k] + int64_t(h.head) * p.D;
+#pragma unroll
+      for (int i = 0; i < NU; ++i) {
+        qa[i] = fetch<T, V, RAG>(x + u.a[i]);
+        qb[i] = fetch<T, V, RAG>(x + u.b[i]);
+      }
+    };
+    int it = split * each;
+    if (it < last) load(it);
+    for (; it < last; ++it) {
+      const Head h(p, it, teams, lane);
+      T* y = static_cast<T*>(p.y[h.k]) + (row * p.heads[h.k] + h.head) * p.D;
       float a[NU][V], b[NU][V];
       float s = 0.f;
 #pragma unroll
       for (int i = 0; i < NU; ++i) {
-        unpack<T, V>(fetch<T, V, RAG>(x + u.a[i]), a[i]);
-        unpack<T, V>(fetch<T, V, RAG>(x + u.b[i]), b[i]);
+        unpack<T, V>(qa[i], a[i]);
+        unpack<T, V>(qb[i], b[i]);
       }
+      if (it + 1 < last) load(it + 1);  // the next heads on their way (in place: other heads than these)
       if (p.norm) {
 #pragma unroll
         for (int i = 0; i < NU; ++i)
@@ -185,13 +224,17 @@ __global__ __launch_bounds__(256) void rope_kernel(RopeP p) {
             s = fmaf(va, va, fmaf(vb, vb, s));
           }
         const float r = rsqrtf(team_sum(s, p.lgteam) * p.inv + p.eps);
+        auto scale = [&](const Gains<V, NU>& w) {
 #pragma unroll
-        for (int i = 0; i < NU; ++i)
+          for (int i = 0; i < NU; ++i)
 #pragma unroll
-          for (int j = 0; j < V; ++j) {
-            a[i][j] *= r * (w == nullptr ? 1.f : w[u.a[i] + j]);
-            b[i][j] *= r * (w == nullptr ? 1.f : w[u.b[i] + j]);
-          }
+            for (int j = 0; j < V; ++j) {
+              a[i][j] *= r * w.a[i][j];
+              b[i][j] *= r * w.b[i][j];
+            }
+        };
+        if (h.k == 0) scale(wq);
+        else scale(wk);
       }
 #pragma unroll
       for (int i = 0; i < NU; ++i) {
@@ -217,6 +260,7 @@ __global__ __launch_bounds__(256) void rope_backward_kernel(RopeP p) {
   const int team = 1 << p.lgteam, teams = 64 >> p.lgteam;
   const Units<V, NU, RAG, ADJ> u(p, lane & (team - 1), team);
   const int all = p.its[0] + p.its[1], each = (all + p.splits - 1) / p.splits;
+  const Gains<V, NU> wq(p.w[0], u), wk(p.w[1], u);
   float dwa[2][NU][V], dwb[2][NU][V];
 #pragma unroll
   for (int k = 0; k < 2; ++k)
@@ -232,67 +276,79 @@ __global__ __launch_bounds__(256) void rope_backward_kernel(RopeP p) {
       if (p.R > 0) angles(p, cs, p.positions == nullptr ? p.start + t : p.positions[row], lane);
       angles_of<V, NU, RAG, ADJ>(u, cs, turn);
     }
+    const int last = min(all, (split + 1) * each);
+    Pack<T, V> qa[NU], qb[NU], ga[NU], gb[NU];
+    auto load = [&](int it) {
+      const Head h(p, it, teams, lane);
+      const T* x = static_cast<const T*>(p.x[h.k]) + row * p.ld[h.k] + int64_t(h.head) * p.D;
+      const T* dy = static_cast<const T*>(p.dy[h.k]) + (row * p.heads[h.k] + h.head) * p.D;
 #pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      const int first = k ? p.its[0] : 0;
-      for (int it = max(first, split * each); it < min(first + p.its[k], (split + 1) * each); ++it) {
-        const int mine = (it - first) * teams + (lane >> p.lgteam), head = min(mine, p.heads[k] - 1);
-        const T* x = static_cast<const T*>(p.x[k]) + row * p.ld[k] + int64_t(head) * p.D;
-        const int64_t at = (row * p.heads[k] + head) * p.D;
-        const T* dy = static_cast<const T*>(p.dy[k]) + at;
-        T* dx = static_cast<T*>(p.y[k]) + at;
-        const float* w = p.w[k];
-        float a[NU][V], b[NU][V], da[NU][V], db[NU][V];
-        if (!held) {
+      for (int i = 0; i < NU; ++i) {
+        qa[i] = fetch<T, V, RAG>(x + u.a[i]);
+        qb[i] = fetch<T, V, RAG>(x + u.b[i]);
+        ga[i] = fetch<T, V, RAG>(dy + u.a[i]);
+        gb[i] = fetch<T, V, RAG>(dy + u.b[i]);
+      }
+    };
+    int it = split * each;
+    if (held && it < last) load(it);
+    for (; it < last; ++it) {
+      const Head h(p, it, teams, lane);
+      T* dx = static_cast<T*>(p.y[h.k]) + (row * p.heads[h.k] + h.head) * p.D;
+      float a[NU][V], b[NU][V], da[NU][V], db[NU][V];
+      if (!held) {
 #pragma unroll
-          for (int j = 0; j < V; ++j) a[0][j] = 0.f;
-#pragma unroll
-          for (int i = 0; i < NU; ++i) {
-            put<T, V, RAG>(dx + u.a[i], a[0]);
-            put<T, V, RAG>(dx + u.b[i], a[0]);
-          }
-          continue;
-        }
-#pragma unroll
-        for (int i = 0; i < NU; ++i) {
-          unpack<T, V>(fetch<T, V, RAG>(x + u.a[i]), a[i]);
-          unpack<T, V>(fetch<T, V, RAG>(x + u.b[i]), b[i]);
-          unpack<T, V>(fetch<T, V, RAG>(dy + u.a[i]), da[i]);
-          unpack<T, V>(fetch<T, V, RAG>(dy + u.b[i]), db[i]);
-          turn_unit<V, ADJ>(da[i], db[i], turn[i], -1.f);
-        }
-        if (p.norm) {
-          float s = 0.f, m = 0.f;
-          float ea[NU][V], eb[NU][V];
-#pragma unroll
-          for (int i = 0; i < NU; ++i)
-#pragma unroll
-            for (int j = 0; j < V; ++j) {
-              const bool ca = u.in[i] && u.counts_a(i, j), cb = u.in[i] && u.counts_b(i, j);
-              ea[i][j] = da[i][j] * (w == nullptr ? 1.f : w[u.a[i] + j]);
-              eb[i][j] = db[i][j] * (w == nullptr ? 1.f : w[u.b[i] + j]);
-              s += (ca ? a[i][j] * a[i][j] : 0.f) + (cb ? b[i][j] * b[i][j] : 0.f);
-              m += (ca ? a[i][j] * ea[i][j] : 0.f) + (cb ? b[i][j] * eb[i][j] : 0.f);
-            }
-          const float r = rsqrtf(team_sum(s, p.lgteam) * p.inv + p.eps);
-          m = team_sum(m, p.lgteam) * p.inv * r * r;
-          const bool own = mine < p.heads[k];
-#pragma unroll
-          for (int i = 0; i < NU; ++i)
-#pragma unroll
-            for (int j = 0; j < V; ++j) {
-              dwa[k][i][j] += own && u.in[i] && u.counts_a(i, j) ? da[i][j] * (a[i][j] * r) : 0.f;
-              dwb[k][i][j] += own && u.in[i] && u.counts_b(i, j) ? db[i][j] * (b[i][j] * r) : 0.f;
-              da[i][j] = r * (ea[i][j] - a[i][j] * m);
-              db[i][j] = r * (eb[i][j] - b[i][j] * m);
-            }
-        }
+        for (int j = 0; j < V; ++j) a[0][j] = 0.f;
 #pragma unroll
         for (int i = 0; i < NU; ++i) {
-          if (NU == 1 || u.in[i]) {
-            put<T, V, RAG>(dx + u.a[i], da[i]);
-            put<T, V, RAG>(dx + u.b[i], db[i]);
+          put<T, V, RAG>(dx + u.a[i], a[0]);
+          put<T, V, RAG>(dx + u.b[i], a[0]);
+        }
+        continue;
+      }
+#pragma unroll
+      for (int i = 0; i < NU; ++i) {
+        unpack<T, V>(qa[i], a[i]);
+        unpack<T, V>(qb[i], b[i]);
+        unpack<T, V>(ga[i], da[i]);
+        unpack<T, V>(gb[i], db[i]);
+      }
+      if (it + 1 < last) load(it + 1);  // the next heads on their way
+#pragma unroll
+      for (int i = 0; i < NU; ++i) turn_unit<V, ADJ>(da[i], db[i], turn[i], -1.f);
+      auto gradient = [&](const Gains<V, NU>& w, float (&wa)[NU][V], float (&wb)[NU][V]) {
+        float s = 0.f, m = 0.f;
+#pragma unroll
+        for (int i = 0; i < NU; ++i)
+#pragma unroll
+          for (int j = 0; j < V; ++j) {
+            const bool ca = u.in[i] && u.counts_a(i, j), cb = u.in[i] && u.counts_b(i, j);
+            const float va = ca ? a[i][j] : 0.f, vb = cb ? b[i][j] : 0.f;
+            s = fmaf(va, va, fmaf(vb, vb, s));
+            m = fmaf(va, da[i][j] * w.a[i][j], fmaf(vb, db[i][j] * w.b[i][j], m));
           }
+        const float r = rsqrtf(team_sum(s, p.lgteam) * p.inv + p.eps);
+        m = team_sum(m, p.lgteam) * p.inv * r * r;
+        const bool own = h.mine < p.heads[h.k];
+#pragma unroll
+        for (int i = 0; i < NU; ++i)
+#pragma unroll
+          for (int j = 0; j < V; ++j) {
+            wa[i][j] += own && u.in[i] && u.counts_a(i, j) ? da[i][j] * (a[i][j] * r) : 0.f;
+            wb[i][j] += own && u.in[i] && u.counts_b(i, j) ? db[i][j] * (b[i][j] * r) : 0.f;
+            da[i][j] = r * (da[i][j] * w.a[i][j] - a[i][j] * m);
+            db[i][j] = r * (db[i][j] * w.b[i][j] - b[i][j] * m);
+          }
+      };
+      if (p.norm) {
+        if (h.k == 0) gradient(wq, dwa[0], dwb[0]);
+        else gradient(wk, dwa[1], dwb[1]);
+      }
+#pragma unroll
+      for (int i = 0; i < NU; ++i) {
+        if (NU == 1 || u.in[i]) {
+          put<T, V, RAG>(dx + u.a[i], da[i]);
+          put<T, V, RAG>(dx + u.b[i], db[i]);
         }
       }
     }
@@ -373,7 +429,7 @@ Plan plan_of(const m3_qk_norm_rope_args& a, bool backward) {
   const int all = p.its[0] + p.its[1];
   const int64_t want = (2048 + p.rows - 1) / p.rows;
   p.splits = int(want < all ? want : all);
-  const int64_t most = backward ? 4096 : 1 << 20;
+  const int64_t most = backward ? 4096 : 8192;
   p.walkers = p.rows < most ? p.rows : most;
   h.blocks = (p.walkers * p.splits + 3) / 4;
   return h;
