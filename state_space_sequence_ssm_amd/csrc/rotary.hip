@@ -134,8 +134,12 @@ __device__ __forceinline__ void put(T* p, const float (&v)[V]) {
 }
 
 // The token's cosines and sines into this wave's part of LDS; no other wave reads them.
-__device__ __forceinline__ void angles(const RopeP& p, float2* cs, int pos, int lane) {
-  for (int i = lane; i < p.R / 2; i += 64) cs[i] = turn_of(double(pos) * double(p.freqs[i]) * 0.15915494309189533577);
+// `first`: this lane's first rate in turns, kept from token to token, so that no load of it
+// waits for the heads that are on their way.
+__device__ __forceinline__ double rate_of(const RopeP& p, int i) { return i < p.R / 2 ? double(p.freqs[i]) * 0.15915494309189533577 : 0.0; }
+__device__ __forceinline__ void angles(const RopeP& p, float2* cs, int pos, int lane, double first) {
+  if (lane < p.R / 2) cs[lane] = turn_of(double(pos) * first);
+  for (int i = lane + 64; i < p.R / 2; i += 64) cs[i] = turn_of(double(pos) * rate_of(p, i));
   __builtin_amdgcn_wave_barrier();
   asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
 }
@@ -174,6 +178,20 @@ struct Head {
   }
 };
 
+// A token: whether its item holds it, and its position.  A wave looks at the next one while it
+// works on one, so that the next one's first heads are on their way too.
+struct Token {
+  int64_t row;
+  int pos;
+  bool any, held;
+  __device__ __forceinline__ Token(const RopeP& p, int64_t r) : row(r), pos(0), any(r < p.rows), held(false) {
+    if (!any) return;
+    const int t = int(row % p.L);
+    held = t < item_length(p.lengths, int(row / p.L), p.L);
+    if (held && p.R > 0) pos = p.positions == nullptr ? p.start + t : p.positions[row];
+  }
+};
+
 template <typename T, int V, int NU, bool RAG, bool ADJ>
 __global__ __launch_bounds__(256) void rope_kernel(RopeP p) {
   extern __shared__ float2 lds[];
@@ -185,26 +203,33 @@ __global__ __launch_bounds__(256) void rope_kernel(RopeP p) {
   const Units<V, NU, RAG, ADJ> u(p, lane & (team - 1), team);
   const int all = p.its[0] + p.its[1], each = (all + p.splits - 1) / p.splits;
   const Gains<V, NU> wq(p.w[0], u), wk(p.w[1], u);
-  for (int64_t row = walker < p.walkers ? walker : p.rows; row < p.rows; row += p.walkers) {
-    const int t = int(row % p.L);
-    if (t >= item_length(p.lengths, int(row / p.L), p.L)) continue;
-    if (p.R > 0) angles(p, cs, p.positions == nullptr ? p.start + t : p.positions[row], lane);
+  const double rate = rate_of(p, lane);
+  const int begin = split * each, last = min(all, begin + each);
+  if (begin >= last) return;
+  Pack<T, V> qa[NU], qb[NU];
+  auto load = [&](int64_t row, int it) {
+    const Head h(p, it, teams, lane);
+    const T* x = static_cast<const T*>(p.x[h.k]) + row * p.ld[h.k] + int64_t(h.head) * p.D;
+#pragma unroll
+    for (int i = 0; i < NU; ++i) {
+      qa[i] = fetch<T, V, RAG>(x + u.a[i]);
+      qb[i] = fetch<T, V, RAG>(x + u.b[i]);
+    }
+  };
+  Token now(p, walker < p.walkers ? walker : p.rows);
+  if (now.held) load(now.row, begin);
+  while (now.any) {
+    const int64_t row = now.row;
+    const Token next(p, row + p.walkers);
+    if (!now.held) {
+      if (next.held) load(next.row, begin);
+      now = next;
+      continue;
+    }
+    if (p.R > 0) angles(p, cs, now.pos, lane, rate);
     float2 turn[NU][V];
     angles_of<V, NU, RAG, ADJ>(u, cs, turn);
-    const int last = min(all, (split + 1) * each);
-    Pack<T, V> qa[NU], qb[NU];
-    auto load = [&](int it) {
-      const Head h(p, it, teams, lane);
-      const T* x = static_cast<const T*>(p.x[h.k]) + row * p.ld[h.k] + int64_t(h.head) * p.D;
-#pragma unroll
-      for (int i = 0; i < NU; ++i) {
-        qa[i] = fetch<T, V, RAG>(x + u.a[i]);
-        qb[i] = fetch<T, V, RAG>(x + u.b[i]);
-      }
-    };
-    int it = split * each;
-    if (it < last) load(it);
-    for (; it < last; ++it) {
+    for (int it = begin; it < last; ++it) {
       const Head h(p, it, teams, lane);
       T* y = static_cast<T*>(p.y[h.k]) + (row * p.heads[h.k] + h.head) * p.D;
       float a[NU][V], b[NU][V];
@@ -214,7 +239,9 @@ __global__ __launch_bounds__(256) void rope_kernel(RopeP p) {
         unpack<T, V>(qa[i], a[i]);
         unpack<T, V>(qb[i], b[i]);
       }
-      if (it + 1 < last) load(it + 1);  // the next heads on their way (in place: other heads than these)
+      // the next heads on their way (in place: other heads than these)
+      if (it + 1 < last) load(row, it + 1);
+      else if (next.held) load(next.row, begin);
       if (p.norm) {
 #pragma unroll
         for (int i = 0; i < NU; ++i)
@@ -245,6 +272,7 @@ __global__ __launch_bounds__(256) void rope_kernel(RopeP p) {
         }
       }
     }
+    now = next;
   }
 }
 
@@ -261,6 +289,7 @@ __global__ __launch_bounds__(256) void rope_backward_kernel(RopeP p) {
   const Units<V, NU, RAG, ADJ> u(p, lane & (team - 1), team);
   const int all = p.its[0] + p.its[1], each = (all + p.splits - 1) / p.splits;
   const Gains<V, NU> wq(p.w[0], u), wk(p.w[1], u);
+  const double rate = rate_of(p, lane);
   float dwa[2][NU][V], dwb[2][NU][V];
 #pragma unroll
   for (int k = 0; k < 2; ++k)
@@ -268,31 +297,32 @@ __global__ __launch_bounds__(256) void rope_backward_kernel(RopeP p) {
     for (int i = 0; i < NU; ++i)
 #pragma unroll
       for (int j = 0; j < V; ++j) dwa[k][i][j] = dwb[k][i][j] = 0.f;
-  for (int64_t row = walker < p.walkers ? walker : p.rows; row < p.rows; row += p.walkers) {
-    const int t = int(row % p.L);
-    const bool held = t < item_length(p.lengths, int(row / p.L), p.L);
+  const int begin = split * each, last = min(all, begin + each);
+  Pack<T, V> qa[NU], qb[NU], ga[NU], gb[NU];
+  auto load = [&](int64_t row, int it) {
+    const Head h(p, it, teams, lane);
+    const T* x = static_cast<const T*>(p.x[h.k]) + row * p.ld[h.k] + int64_t(h.head) * p.D;
+    const T* dy = static_cast<const T*>(p.dy[h.k]) + (row * p.heads[h.k] + h.head) * p.D;
+#pragma unroll
+    for (int i = 0; i < NU; ++i) {
+      qa[i] = fetch<T, V, RAG>(x + u.a[i]);
+      qb[i] = fetch<T, V, RAG>(x + u.b[i]);
+      ga[i] = fetch<T, V, RAG>(dy + u.a[i]);
+      gb[i] = fetch<T, V, RAG>(dy + u.b[i]);
+    }
+  };
+  Token now(p, walker < p.walkers && begin < last ? walker : p.rows);
+  if (now.held) load(now.row, begin);
+  while (now.any) {
+    const int64_t row = now.row;
+    const bool held = now.held;
+    const Token next(p, row + p.walkers);
     float2 turn[NU][V];
     if (held) {
-      if (p.R > 0) angles(p, cs, p.positions == nullptr ? p.start + t : p.positions[row], lane);
+      if (p.R > 0) angles(p, cs, now.pos, lane, rate);
       angles_of<V, NU, RAG, ADJ>(u, cs, turn);
     }
-    const int last = min(all, (split + 1) * each);
-    Pack<T, V> qa[NU], qb[NU], ga[NU], gb[NU];
-    auto load = [&](int it) {
-      const Head h(p, it, teams, lane);
-      const T* x = static_cast<const T*>(p.x[h.k]) + row * p.ld[h.k] + int64_t(h.head) * p.D;
-      const T* dy = static_cast<const T*>(p.dy[h.k]) + (row * p.heads[h.k] + h.head) * p.D;
-#pragma unroll
-      for (int i = 0; i < NU; ++i) {
-        qa[i] = fetch<T, V, RAG>(x + u.a[i]);
-        qb[i] = fetch<T, V, RAG>(x + u.b[i]);
-        ga[i] = fetch<T, V, RAG>(dy + u.a[i]);
-        gb[i] = fetch<T, V, RAG>(dy + u.b[i]);
-      }
-    };
-    int it = split * each;
-    if (held && it < last) load(it);
-    for (; it < last; ++it) {
+    for (int it = begin; it < last; ++it) {
       const Head h(p, it, teams, lane);
       T* dx = static_cast<T*>(p.y[h.k]) + (row * p.heads[h.k] + h.head) * p.D;
       float a[NU][V], b[NU][V], da[NU][V], db[NU][V];
@@ -304,6 +334,7 @@ __global__ __launch_bounds__(256) void rope_backward_kernel(RopeP p) {
           put<T, V, RAG>(dx + u.a[i], a[0]);
           put<T, V, RAG>(dx + u.b[i], a[0]);
         }
+        if (it + 1 == last && next.held) load(next.row, begin);
         continue;
       }
 #pragma unroll
@@ -313,7 +344,8 @@ __global__ __launch_bounds__(256) void rope_backward_kernel(RopeP p) {
         unpack<T, V>(ga[i], da[i]);
         unpack<T, V>(gb[i], db[i]);
       }
-      if (it + 1 < last) load(it + 1);  // the next heads on their way
+      if (it + 1 < last) load(row, it + 1);  // the next heads on their way
+      else if (next.held) load(next.row, begin);
 #pragma unroll
       for (int i = 0; i < NU; ++i) turn_unit<V, ADJ>(da[i], db[i], turn[i], -1.f);
       auto gradient = [&](const Gains<V, NU>& w, float (&wa)[NU][V], float (&wb)[NU][V]) {
@@ -352,6 +384,7 @@ __global__ __launch_bounds__(256) void rope_backward_kernel(RopeP p) {
         }
       }
     }
+    now = next;
   }
   if (p.part == nullptr) return;
   // over the wave's teams, then over the block's waves, in order
