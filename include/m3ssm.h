@@ -653,7 +653,10 @@ int m3_residual_norm_backward(const m3_residual_norm_backward_args* args, void* 
  * position of its queries and keys.  A learned decay, or one per token, is the
  * core's (A, A_tok).  Types, row distances, lengths, aliasing and limits of
  * launches as for the layer operators; the rows of a tensor [Bt, L, H, K] are
- * its tokens (H * K dense elements each), row distances are below 2^24.
+ * its tokens (H * K dense elements each), row distances are below 2^24 (of single
+ * tokens: 2^40).  Launches: below 2^23 blocks of 64 columns for each item, head
+ * and segment of 256 tokens or more (backward: three walks of them), 2^24 single
+ * tokens' heads and columns; larger calls are M3_ERR_UNSUPPORTED.
  */
 
 /* Linear attention with a decay for each head:
@@ -665,7 +668,9 @@ int m3_residual_norm_backward(const m3_residual_norm_backward_args* args, void* 
  *   itself): the state after the last token.
  * K and V in 1..256, Hk divides H.
  * bf16 products are formed on the matrix cores with weights and states split
- * into bf16 parts, so that the state is as good as fp32 sums make it.
+ * into bf16 parts, so that the state is as good as fp32 sums make it.  Tokens are
+ * taken 64 at a time: a value of k or v that is not finite reaches the outputs of
+ * its item and head from the first of its 64 tokens on, not only those behind it.
  * workspace: optional; with few (batch, head) pairs the token axis is cut into
  * segments whose states are found first, when a workspace of
  * m3_linear_attention_workspace_size bytes (256-byte aligned; 0: not used) is

@@ -12,7 +12,8 @@ struct Shape {
 };
 int64_t units(const m3_linear_attention_args& a) { return int64_t(a.Bt) * a.H; }
 // Columns of c per block: 64 where eight waves share a block (bf16, a and b of up to 128), and
-// otherwise 128 where such a state fits the registers and `blocks` of them fill the card.
+// otherwise 128 where such a state fits the registers and `blocks` of them fill the card (fp32,
+// Bt 16, L 1024, 32 heads of 128 x 128: 503 us, by 64 columns 650; of 64 x 128: 310 and 296).
 bool two_roles(const m3_linear_attention_args& a, int b_cols) { return a.in_dtype == M3_BF16 && b_cols <= 128; }
 Shape shape_of(const m3_linear_attention_args& a, int b_cols, int c_cols, int64_t blocks, bool states) {
   const bool wide = c_cols > 64 && b_cols <= 128 && blocks >= 256 && (states || !two_roles(a, b_cols));
@@ -26,9 +27,13 @@ int64_t backward_blocks(const m3_linear_attention_args& a) {
   return units(a) * (2 * tiles(a.K, walk_shape(a, a.V, a.K)) + tiles(a.V, walk_shape(a, a.K, a.V)));
 }
 
-// Segments of the token axis: enough blocks for the card, each of 256 tokens at least.
-void segments(int64_t blocks, int L, int& len, int& segs) {
-  int64_t want = blocks >= 256 ? 1 : (512 + blocks - 1) / blocks;
+// Segments of the token axis, each of 256 tokens at least: `want` blocks where there are fewer
+// than 256.  One a compute unit of the forward's blocks of eight waves (16 heads of 128 x 128,
+// bf16, one item of 4096 tokens: 58 us, with two 67, uncut 131; of 16384: 138, 143, 488), two of
+// four waves (fp32, 4 x 4096 tokens of 16 heads of 64 x 64: 120 us, with one 137, uncut 342),
+// and two for the backward's three walks (16384 tokens as above: 412 us, with one 489).
+void segments(int64_t blocks, int most_blocks, int L, int& len, int& segs) {
+  int64_t want = blocks >= 256 ? 1 : (most_blocks + blocks - 1) / blocks;
   const int64_t most = (L + 255) / 256;
   if (want > most) want = most;
   len = int(((L + want - 1) / want + 63) / 64 * 64);
@@ -44,12 +49,12 @@ size_t states_bytes(const m3_linear_attention_args& a, int segs) {
 }
 Cut forward_cut(const m3_linear_attention_args& a) {
   Cut c;
-  segments(forward_blocks(a), a.L, c.len, c.segs);
+  segments(forward_blocks(a), two_roles(a, a.K) ? 256 : 512, a.L, c.len, c.segs);
   return c;
 }
 Cut backward_cut(const m3_linear_attention_args& a) {
   Cut c;
-  segments(backward_blocks(a), a.L, c.len, c.segs);
+  segments(backward_blocks(a), 512, a.L, c.len, c.segs);
   return c;
 }
 
@@ -176,6 +181,7 @@ struct StepP {
 };
 // S = l S + k v^T, y = scale q^T S.  One block per (sequence, head, tile of columns): 2^lgvl
 // lanes along a row of the state, W columns each, the other groups of lanes on other rows.
+// Bound by the state's way in and out: 256 sequences of 16 heads of 128 x 128, 109 us, 4.9 TB/s.
 template <typename T, int W>
 __global__ __launch_bounds__(256) void attention_step_kernel(StepP p) {
   __shared__ float sq[256], sk[256], red[256 * W];
