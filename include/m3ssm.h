@@ -666,7 +666,7 @@ int m3_residual_norm_backward(const m3_residual_norm_backward_args* args, void* 
  *   y [Bt, L, H, V]; log_decay [H] float32 (0: no decay; -inf: each token alone);
  *   h0 [Bt, H, K, V] float32 or NULL (zeros); h_final (nullable; may be h0
  *   itself): the state after the last token.
- * K and V in 1..256, Hk divides H.
+ * K and V in 1..256, Hk divides H, H V below 2^24 (of single tokens: any).
  * bf16 products are formed on the matrix cores with weights and states split
  * into bf16 parts, so that the state is as good as fp32 sums make it.  Tokens are
  * taken 64 at a time: a value of k or v that is not finite reaches the outputs of

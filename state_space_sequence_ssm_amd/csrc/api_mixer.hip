@@ -9,6 +9,7 @@ namespace {
 constexpr double kMaxElems = 34359738368.0;  // 2^35 elements of one tensor
 constexpr double kMaxInt = 2147483647.0;
 constexpr int kMaxLength = 1 << 28;
+constexpr int kMaxRow = 1 << 24;     // elements from one token to the next: 64 of them are addressed in 32 bits
 constexpr int kMaxHeadDim = 256;   // K and V: what a block's state and tiles hold
 constexpr int kMaxRopeDim = 1024;  // D of the rotated heads: what a wave's angles hold
 
@@ -99,7 +100,7 @@ int m3_linear_attention(const m3_linear_attention_args* args, void* stream) {
   m3_linear_attention_args a = *args;
   const int rc = check_attention_inputs(a);
   if (rc != M3_OK) return rc;
-  if (!m3::attention_fits(a)) return M3_ERR_UNSUPPORTED;
+  if (!m3::attention_fits(a) || int64_t(a.H) * a.V >= kMaxRow) return M3_ERR_UNSUPPORTED;
   if (a.y == nullptr || !all_at({a.y}, elem(a.in_dtype)) || !all_at({a.h_final}, 4)) return M3_ERR_INVALID_ARG;
   if (clash({a.y, a.h_final, a.workspace}, {a.q, a.k, a.v, a.log_decay, a.lengths}) || a.y == a.h0 ||
       (a.workspace != nullptr && a.workspace == a.h0))
@@ -132,7 +133,7 @@ int m3_linear_attention_backward(const m3_linear_attention_backward_args* args, 
   m3_linear_attention_backward_args a = *args;
   const int rc = check_attention_inputs(a.fwd);
   if (rc != M3_OK) return rc;
-  if (!m3::attention_backward_fits(a) || int64_t(a.fwd.H) * a.fwd.V >= (1 << 24)) return M3_ERR_UNSUPPORTED;
+  if (!m3::attention_backward_fits(a) || int64_t(a.fwd.H) * a.fwd.V >= kMaxRow) return M3_ERR_UNSUPPORTED;
   const m3_linear_attention_args& f = a.fwd;
   if (!all_set({a.dy, a.dq, a.dk, a.dv})) return M3_ERR_INVALID_ARG;
   if (!all_at({a.dy, a.dq, a.dk, a.dv}, elem(f.in_dtype)) || !all_at({a.dh_final, a.dh0}, 4)) return M3_ERR_INVALID_ARG;

@@ -254,7 +254,7 @@ StepShape step_shape(const m3_linear_attention_step_args& a) {
 bool attention_fits(const m3_linear_attention_args& a) {
   const Cut c = forward_cut(a);
   const int64_t u = units(a);
-  return launchable(forward_blocks(a) * c.segs * 2, 512) && launchable(u * ((a.K * a.V + 255) / 256), 256);
+  return launchable(forward_blocks(a) * c.segs, 512) && launchable(u * ((a.K * a.V + 255) / 256), 256);
 }
 size_t attention_workspace(const m3_linear_attention_args& a) { return states_bytes(a, forward_cut(a).segs); }
 
@@ -300,7 +300,7 @@ bool attention_backward_fits(const m3_linear_attention_backward_args& b) {
   const Cut c = backward_cut(a);
   const int64_t u = units(a);
   const int64_t most = a.K > a.V ? a.K : a.V;
-  return launchable(backward_blocks(a) * c.segs * 2, 512) && launchable(2 * u * ((a.K * a.V + 255) / 256), 256) &&
+  return launchable(backward_blocks(a) * c.segs, 512) && launchable(2 * u * ((a.K * a.V + 255) / 256), 256) &&
          launchable(int64_t(a.Bt) * a.L * a.Hk * most / 256 + 1, 256);
 }
 // Workspace: the states in front of every segment, of the forward and of the reverse walk, and

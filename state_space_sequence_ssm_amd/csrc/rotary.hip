@@ -155,7 +155,7 @@ __device__ __forceinline__ void angles_of(const Units<V, NU, RAG, ADJ>& u, const
 }
 
 // A lane's gains (1 without them), kept in registers while a wave walks tokens: read anew for
-// each head they were half of the loads (whole words: 16 of 120 us).
+// each head they were half of the loads, and read one by one 8 us of 121.
 template <int V, int NU>
 struct Gains {
   float a[NU][V], b[NU][V];

@@ -194,6 +194,29 @@ def test_mixer_refusals(name):
 
 
 @built
+def test_rows_past_32_bits_are_refused():
+    """64 rows of an output are addressed in 32 bits: of many heads over few shared ones too."""
+    lib = _lib.load()
+    for name, make in (("m3_linear_attention", _attention), ("m3_linear_attention_backward", _backward)):
+        a = make()
+        f = a.fwd if hasattr(a, "fwd") else a
+        f.Bt, f.L, f.H, f.Hk, f.K, f.V = 1, 64, 1 << 17, 1, 1, 128
+        if hasattr(a, "fwd"):
+            a.workspace_bytes = (1 << 64) - 1
+        assert getattr(lib, name)(ctypes.byref(a), None) == UNS, name
+
+
+@built
+def test_calls_past_32_bits_of_work_items_are_refused():
+    a = _attention()
+    a.Bt, a.L, a.H, a.Hk, a.K, a.V = 1 << 19, 1, 32, 32, 8, 8
+    assert _lib.load().m3_linear_attention(ctypes.byref(a), None) == UNS
+    b = _step()
+    b.Bt, b.H, b.Hk, b.K, b.V = 1 << 19, 64, 64, 1, 1
+    assert _lib.load().m3_linear_attention_step(ctypes.byref(b), None) == UNS
+
+
+@built
 def test_rope_in_place_needs_dense_rows():
     for x, width in (("q", 64), ("k", 32)):
         a = _rope()
