@@ -325,3 +325,14 @@ def test_rope_far_angles_and_large_rates(ops):
     got = ops.m3_qk_norm_rope(q, None, freqs=freqs, positions=pos)["q"]
     want, mag = (ref.rope(q, freqs=freqs, positions=pos, mag=x) for x in (False, True))
     close("q", got, want["y"], mag["y"] + 0.0, 48 + 3e-5 / 2 ** -23)
+
+
+@pytest.mark.parametrize("D,R,adjacent,t", [(128, 128, False, BF), (80, 40, True, F32), (57, 34, False, BF), (33, 6, True, F32)])
+def test_rope_backward_in_place(ops, D, R, adjacent, t):
+    """dq and dk where dq_out and dk_out were, uneven numbers of heads over a wave's teams."""
+    m = Maker(89)
+    q, k, dq, dk, w = m(2, 37, 5, D, dtype=t), m(2, 37, 3, D, dtype=t), m(2, 37, 5, D, dtype=t), m(2, 37, 3, D, dtype=t), m(D, shift=1.0)
+    how = dict(freqs=torch.rand(R // 2, generator=m.g).cuda(), adjacent=adjacent, lengths=ilen([37, 11]))
+    want = ops.m3_qk_norm_rope_backward(q, k, w, w, dq_out=dq, dk_out=dk, **how)
+    got = ops.m3_qk_norm_rope_backward(q, k, w, w, dq_out=dq, dk_out=dk, out=dict(dq=dq, dk=dk), **how)
+    assert got["dq"] is dq and all(torch.equal(want[n], got[n]) for n in want)
