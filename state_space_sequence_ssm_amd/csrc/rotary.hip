@@ -1,9 +1,12 @@
 // Norm of queries and keys for each head and their rotation by position, forward and
 // backward.  Memory bound: every element is read and written once.
 #include "mixer_internal.hpp"
+#include "rotary_plan.hpp"
 
 namespace m3 {
 namespace {
+
+using namespace rope;
 
 // A wave takes one token: its cosines and sines, which all heads share, are formed once by
 // its 64 lanes and handed round through LDS.  Teams of 2^lgteam lanes then take a head each.
@@ -15,21 +18,6 @@ namespace {
 // 32768 tokens of 16 + 16 heads of 128 bf16: 113 us, 4.8 TB/s (one token's loads at a time and
 // gains read for each head: 157); backward of 16 + 4 heads 151 us, 3.3 TB/s: 192 registers leave
 // two waves a SIMD, which wait for memory three quarters of the time (three spill: slower).
-struct RopeP {
-  const void* x[2];   // q, k
-  void* y[2];         // outputs, or in the backward dx
-  const void* dy[2];  // backward
-  const float* w[2];
-  int64_t ld[2];
-  int heads[2], its[2];  // turns of a wave over q's and k's heads
-  const float* freqs;
-  const int32_t* positions;
-  const int32_t* lengths;
-  float* part;  // backward: [blocks][2 D], or null
-  int64_t rows, walkers;
-  int L, D, R, start, norm, lgteam, units, rot_units, splits;
-  float eps, inv;
-};
 
 // cos and sin of 2 pi r, r in turns: reduced in 64 bits to an eighth of a turn around a
 // quarter, then the series of sine and cosine to x^9 and x^10 (off by 2e-9 at pi / 4).
@@ -55,51 +43,6 @@ __device__ __forceinline__ float team_sum(float v, int lg) {
   if (lg >= 6) v = add_x32(v);
   return v;
 }
-
-template <int V, int NU, bool RAG, bool ADJ>
-struct Units {
-  int a[NU], b[NU];  // the words' columns
-  int skip[NU];      // pairs (behind R: elements) at the front that another unit counts
-  int pair[NU];      // first pair, or -1 behind R
-  bool in[NU], once[NU];  // once: b repeats a
-  __device__ __forceinline__ Units(const RopeP& p, int lane, int team) {
-#pragma unroll
-    for (int i = 0; i < NU; ++i) {
-      int u = lane + i * team;
-      in[i] = u < p.units;
-      u = in[i] ? u : 0;
-      once[i] = false;
-      if (u < p.rot_units) {
-        const int half = p.R / 2, s = RAG ? min(u * V, half - V) : u * V;
-        skip[i] = u * V - s;
-        pair[i] = s;
-        a[i] = ADJ ? 2 * s : s;
-        b[i] = ADJ ? 2 * s + V : half + s;
-      } else {
-        const int rest = p.D - p.R, at = (u - p.rot_units) * 2 * V, s = RAG || V == 1 ? max(0, min(at, rest - 2 * V)) : at;
-        skip[i] = at - s;
-        pair[i] = -1;
-        a[i] = p.R + s;
-        b[i] = a[i] + V;
-        if (V == 1 && rest == 1) {
-          b[i] = a[i];
-          once[i] = true;
-        }
-      }
-    }
-  }
-  // whether element j of word a (of word b) is this unit's to count
-  __device__ __forceinline__ bool counts_a(int i, int j) const {
-    if (V > 1 && !RAG) return true;
-    return pair[i] < 0 || !ADJ ? j >= skip[i] : j / 2 >= skip[i];
-  }
-  __device__ __forceinline__ bool counts_b(int i, int j) const {
-    if (V > 1 && !RAG) return true;
-    if (once[i]) return false;
-    if (pair[i] < 0) return V + j >= skip[i];
-    return ADJ ? (V + j) / 2 >= skip[i] : j >= skip[i];
-  }
-};
 
 // (x0, x1) turned by the angle of (c, s); the transposed turn with the other sign of s
 __device__ __forceinline__ void turn2(float& x0, float& x1, float c, float s) {
@@ -420,64 +363,7 @@ __global__ __launch_bounds__(256) void rope_backward_kernel(RopeP p) {
 }
 
 // ---------------------------------------------------------------- launches
-struct Plan {
-  int V, NU;
-  bool rag;
-  RopeP p;
-  int64_t blocks;
-};
-int lg2_up(int v) {
-  int l = 0;
-  while ((1 << l) < v) ++l;
-  return l;
-}
 bool whole(const void* p, int64_t ld, size_t e) { return p == nullptr || rows_aligned(p, ld, e, 16); }
-
-// The words: 16 bytes wherever both ranges of a head hold a unit of them, else single
-// elements.  Tokens over waves; with few tokens, their heads over several.
-Plan plan_of(const m3_qk_norm_rope_args& a, bool backward) {
-  Plan h{};
-  RopeP& p = h.p;
-  const size_t e = a.in_dtype == M3_BF16 ? 2 : 4;
-  const int word = int(16 / e), rest = a.D - a.R;
-  h.V = (a.R == 0 || a.R >= 2 * word) && (rest == 0 || rest >= 2 * word) ? word : 1;
-  h.rag = (a.R / 2) % word != 0 || rest % (2 * word) != 0;
-  p.rot_units = (a.R / 2 + h.V - 1) / h.V;
-  p.units = p.rot_units + (rest + 2 * h.V - 1) / (2 * h.V);
-  p.lgteam = lg2_up(p.units < 64 ? p.units : 64);
-  h.NU = (p.units + 63) / 64;
-  p.x[0] = a.q;
-  p.x[1] = a.k;
-  p.w[0] = a.q_w;
-  p.w[1] = a.k_w;
-  p.ld[0] = a.q_ld;
-  p.ld[1] = a.k_ld;
-  p.heads[0] = a.H;
-  p.heads[1] = a.Hk;
-  const int teams = 64 >> p.lgteam;
-  for (int i = 0; i < 2; ++i) p.its[i] = (p.heads[i] + teams - 1) / teams;
-  p.freqs = a.freqs;
-  p.positions = a.positions;
-  p.lengths = a.lengths;
-  p.rows = int64_t(a.Bt) * a.L;
-  p.L = a.L;
-  p.D = a.D;
-  p.R = a.R;
-  p.start = a.start;
-  p.norm = a.norm;
-  p.eps = a.eps;
-  p.inv = 1.f / float(a.D);
-  const int all = p.its[0] + p.its[1];
-  const int64_t want = (2048 + p.rows - 1) / p.rows;
-  p.splits = int(want < all ? want : all);
-  // A wave's start (gains, rates) is worth a few tokens' time: four tokens each where that still
-  // leaves two waves a SIMD (7685 tokens of 9 heads of 80, fp32, uneven: 13 us, one each 16).
-  const int64_t most = backward ? 4096 : 8192, few = p.rows / 4 < 2048 ? 2048 : p.rows / 4;
-  p.walkers = p.rows < few ? p.rows : few;
-  if (p.walkers > most) p.walkers = most;
-  h.blocks = (p.walkers * p.splits + 3) / 4;
-  return h;
-}
 template <typename T, int V, int NU, bool RAG, bool ADJ>
 hipError_t launch_one(const Plan& h, bool backward, hipStream_t s) {
   const dim3 grid(uint32_t(h.blocks)), block(256);
@@ -490,13 +376,17 @@ hipError_t launch_one(const Plan& h, bool backward, hipStream_t s) {
   }
   return hipGetLastError();
 }
+// The instance that holds V and NU; a plan that none does is an error, never fewer units.
 template <typename T, int W, bool ADJ>
 hipError_t launch_any(const Plan& h, bool backward, hipStream_t s) {
-  if (h.V == 1) return h.NU == 1 ? launch_one<T, 1, 1, false, ADJ>(h, backward, s) : launch_one<T, 1, 8, false, ADJ>(h, backward, s);
+  if (h.p.units > 64 * h.NU) return hipErrorInvalidValue;
+  if (h.V == 1 && h.NU == 1) return launch_one<T, 1, 1, false, ADJ>(h, backward, s);
+  if (h.V == 1 && h.NU == 8) return launch_one<T, 1, 8, false, ADJ>(h, backward, s);
   if constexpr (W == 4) {
-    if (h.NU == 2) return h.rag ? launch_one<T, W, 2, true, ADJ>(h, backward, s) : launch_one<T, W, 2, false, ADJ>(h, backward, s);
+    if (h.V == W && h.NU == 2) return h.rag ? launch_one<T, W, 2, true, ADJ>(h, backward, s) : launch_one<T, W, 2, false, ADJ>(h, backward, s);
   }
-  return h.rag ? launch_one<T, W, 1, true, ADJ>(h, backward, s) : launch_one<T, W, 1, false, ADJ>(h, backward, s);
+  if (h.V == W && h.NU == 1) return h.rag ? launch_one<T, W, 1, true, ADJ>(h, backward, s) : launch_one<T, W, 1, false, ADJ>(h, backward, s);
+  return hipErrorInvalidValue;
 }
 hipError_t launch(const m3_qk_norm_rope_args& a, const Plan& h, bool backward, hipStream_t s) {
   if (a.in_dtype == M3_BF16) return a.adjacent ? launch_any<bf16_t, 8, true>(h, backward, s) : launch_any<bf16_t, 8, false>(h, backward, s);

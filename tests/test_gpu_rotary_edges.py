@@ -1,0 +1,45 @@
+"""The norm and rotation of queries and keys at its edges: the largest heads.
+References and tolerances as in tests/test_gpu_mixer.py."""
+import pytest
+
+torch = pytest.importorskip("torch")
+
+from tests import layer_ref, mixer_ref as ref  # noqa: E402
+from tests.test_gpu_layers import NAN, ilen  # noqa: E402
+from tests.test_gpu_mixer import K_ROPE, _rope_inputs, close  # noqa: E402
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def ops():
+    if not torch.cuda.is_available():
+        pytest.fail("no GPU visible to torch")
+    from state_space_sequence_ssm_amd import ops as o
+    return o
+
+
+# Heads of which a wave's lanes hold more than their usual number of words: both ranges of the
+# head end inside a word of 16 bytes (65 words in bf16, 129 in fp32), and their neighbours.
+LARGE = [(D, R, adjacent, dt)
+         for dt, sizes in (("bf16", [(1024, 20), (1024, 1000), (1011, 18), (1023, 514), (1010, 18), (1024, 1008)]),
+                           ("f32", [(1024, 10), (1024, 510), (1019, 10), (1023, 1014), (1018, 10), (520, 10)]))
+         for D, R in sizes for adjacent in (False, True)]
+
+
+@pytest.mark.parametrize("D,R,adjacent,dt", LARGE)
+def test_rope_of_the_largest_heads(ops, D, R, adjacent, dt):
+    c = (2, 3, 3, 2, D, R, adjacent, dt, [3, 2], True, True, None, False)
+    x, d, w, how, lengths = _rope_inputs(c, 41)
+    outs = {n: torch.full(v.shape, 7.0, dtype=v.dtype, device="cuda") for n, v in x.items()}
+    got = ops.m3_qk_norm_rope(x["q"], x["k"], w["q"], w["k"], lengths=ilen(lengths), q_out=outs["q"], k_out=outs["k"], **how)
+    out = {"d" + n: torch.full(v.shape, NAN, dtype=v.dtype, device="cuda") for n, v in x.items()}
+    out.update({"d" + n + "_w": torch.full(v.shape, NAN, device="cuda") for n, v in w.items()})
+    grad = ops.m3_qk_norm_rope_backward(x["q"], x["k"], w["q"], w["k"], dq_out=d["q"], dk_out=d["k"], lengths=ilen(lengths), out=out, **how)
+    for n in "qk":
+        want, mag = (ref.rope(x[n], w[n], lengths=lengths, mag=s, dy=d[n], **how) for s in (False, True))
+        for b, held in enumerate(layer_ref.held(lengths, 2, 3)):
+            close(n, got[n][b, :held], want["y"][b, :held], mag["y"][b, :held], K_ROPE)
+            assert (got[n][b, held:] == 7).all()
+        close("d" + n, grad["d" + n], want["dx"], mag["dx"], 2 * K_ROPE)
+        close("d" + n + "_w", grad["d" + n + "_w"], want["dw"], mag["dw"], K_ROPE + 6 * x[n].shape[2])
