@@ -44,22 +44,24 @@ __device__ __forceinline__ float team_sum(float v, int lg) {
   return v;
 }
 
-// (x0, x1) turned by the angle of (c, s); the transposed turn with the other sign of s
-__device__ __forceinline__ void turn2(float& x0, float& x1, float c, float s) {
-  const float y0 = fmaf(x0, c, -(x1 * s));
-  x1 = fmaf(x1, c, x0 * s);
-  x0 = y0;
+// (x0, x1) turned by the angle of (c, s); the transposed turn with the other sign of s.  Where
+// `turned` is false they stay, and are not turned by (1, 0): an infinity times 0 is not a number.
+// A choice for each element: a branch around them takes 16 registers more and a wave a SIMD.
+__device__ __forceinline__ void turn2(float& x0, float& x1, float c, float s, bool turned) {
+  const float y0 = fmaf(x0, c, -(x1 * s)), y1 = fmaf(x1, c, x0 * s);
+  x0 = turned ? y0 : x0;
+  x1 = turned ? y1 : x1;
 }
 template <int V, bool ADJ>
-__device__ __forceinline__ void turn_unit(float (&a)[V], float (&b)[V], const float2 (&cs)[V], float sign) {
+__device__ __forceinline__ void turn_unit(float (&a)[V], float (&b)[V], const float2 (&cs)[V], float sign, bool turned) {
   if constexpr (!ADJ || V == 1) {
 #pragma unroll
-    for (int j = 0; j < V; ++j) turn2(a[j], b[j], cs[j].x, sign * cs[j].y);
+    for (int j = 0; j < V; ++j) turn2(a[j], b[j], cs[j].x, sign * cs[j].y, turned);
   } else {
 #pragma unroll
     for (int j = 0; j < V / 2; ++j) {
-      turn2(a[2 * j], a[2 * j + 1], cs[j].x, sign * cs[j].y);
-      turn2(b[2 * j], b[2 * j + 1], cs[V / 2 + j].x, sign * cs[V / 2 + j].y);
+      turn2(a[2 * j], a[2 * j + 1], cs[j].x, sign * cs[j].y, turned);
+      turn2(b[2 * j], b[2 * j + 1], cs[V / 2 + j].x, sign * cs[V / 2 + j].y, turned);
     }
   }
 }
@@ -216,7 +218,7 @@ __global__ __launch_bounds__(256) void rope_kernel(RopeP p) {
       }
 #pragma unroll
       for (int i = 0; i < NU; ++i) {
-        turn_unit<V, ADJ>(a[i], b[i], turn[i], 1.f);
+        turn_unit<V, ADJ>(a[i], b[i], turn[i], 1.f, u.pair[i] >= 0);
         if (NU == 1 || u.in[i]) {
           put<T, V, RAG>(y + u.a[i], a[i]);
           put<T, V, RAG>(y + u.b[i], b[i]);
@@ -298,7 +300,7 @@ __global__ __launch_bounds__(256) void rope_backward_kernel(RopeP p) {
       if (it + 1 < last) load(row, it + 1);  // the next heads on their way
       else if (next.held) load(next.row, begin);
 #pragma unroll
-      for (int i = 0; i < NU; ++i) turn_unit<V, ADJ>(da[i], db[i], turn[i], -1.f);
+      for (int i = 0; i < NU; ++i) turn_unit<V, ADJ>(da[i], db[i], turn[i], -1.f, u.pair[i] >= 0);
       auto gradient = [&](const Gains<V, NU>& w, float (&wa)[NU][V], float (&wb)[NU][V]) {
         float s = 0.f, m = 0.f;
 #pragma unroll

@@ -1,14 +1,16 @@
-"""The norm and rotation of queries and keys at its edges: the largest heads.
-References and tolerances as in tests/test_gpu_mixer.py."""
+"""The norm and rotation of queries and keys at its edges: the largest heads, values that
+are not finite in elements that are not rotated.  References and
+tolerances as in tests/test_gpu_mixer.py."""
 import pytest
 
 torch = pytest.importorskip("torch")
 
 from tests import layer_ref, mixer_ref as ref  # noqa: E402
-from tests.test_gpu_layers import NAN, ilen  # noqa: E402
+from tests.test_gpu_layers import BF, F32, NAN, Maker, ilen  # noqa: E402
 from tests.test_gpu_mixer import K_ROPE, _rope_inputs, close  # noqa: E402
 
 pytestmark = pytest.mark.gpu
+INF = float("inf")
 
 
 @pytest.fixture(scope="module")
@@ -43,3 +45,40 @@ def test_rope_of_the_largest_heads(ops, D, R, adjacent, dt):
             assert (got[n][b, held:] == 7).all()
         close("d" + n, grad["d" + n], want["dx"], mag["dx"], 2 * K_ROPE)
         close("d" + n + "_w", grad["d" + n + "_w"], want["dw"], mag["dw"], K_ROPE + 6 * x[n].shape[2])
+
+
+# Elements behind R, and with norm = 0 all of them, take no part in others: words in pairs of 16
+# bytes, moved back to end with the head, and single elements.
+PASSED = [(128, 64, BF), (80, 40, BF), (57, 34, BF), (72, 64, BF), (40, 0, BF), (33, 6, F32), (128, 32, F32), (60, 26, F32), (13, 4, F32)]
+
+
+def _spread(D, R, t):
+    """[1, 7, 2, D] with a value that is not finite in single elements, each in its own head, and where."""
+    bad = torch.zeros(1, 7, 2, D, dtype=torch.bool)
+    for i in range(14):
+        bad[0, i // 2, i % 2, (i * 5 + 3 * (i // 3)) % D] = i % 7 != 6
+    values = torch.tensor([INF, -INF, NAN])[torch.arange(14).view(1, 7, 2, 1) % 3]
+    return bad.cuda(), values.to(t).cuda()
+
+
+@pytest.mark.parametrize("adjacent", [False, True])
+@pytest.mark.parametrize("D,R,t", PASSED)
+def test_values_that_are_not_finite_stay_where_they_are(ops, D, R, t, adjacent):
+    m = Maker(42)
+    x = m(1, 7, 2, D, dtype=t)
+    bad, values = _spread(D, R, t)
+    dirty = torch.where(bad, values, x)
+    freqs = torch.rand(R // 2, generator=m.g).cuda() if R else None
+    # a rotated element's value reaches its partner too
+    reach = bad.clone()
+    if R:
+        lo, hi = (slice(0, R, 2), slice(1, R, 2)) if adjacent else (slice(0, R // 2), slice(R // 2, R))
+        both = bad[..., lo] | bad[..., hi]
+        reach[..., lo], reach[..., hi] = both, both
+    how = dict(freqs=freqs, norm=False, adjacent=adjacent, start=3)
+    runs = [lambda v: ops.m3_qk_norm_rope(v, None, **how)["q"], lambda v: ops.m3_qk_norm_rope_backward(x, dq_out=v, **how)["dq"]]
+    for run in runs:
+        clean, got = run(x), run(dirty)
+        assert torch.equal(got[~reach], clean[~reach])
+        assert torch.equal(got[..., R:].nan_to_num(9e9), dirty[..., R:].nan_to_num(9e9))
+        assert not torch.isfinite(got[..., :R][bad[..., :R]]).any()
