@@ -85,9 +85,10 @@ __device__ __forceinline__ void put(T* p, const float (&v)[V]) {
 // `first`: this lane's first rate in turns, kept from token to token, so that no load of it
 // waits for the heads that are on their way.
 __device__ __forceinline__ double rate_of(const RopeP& p, int i) { return i < p.R / 2 ? double(p.freqs[i]) * 0.15915494309189533577 : 0.0; }
-__device__ __forceinline__ void angles(const RopeP& p, float2* cs, int pos, int lane, double first) {
-  if (lane < p.R / 2) cs[lane] = turn_of(double(pos) * first);
-  for (int i = lane + 64; i < p.R / 2; i += 64) cs[i] = turn_of(double(pos) * rate_of(p, i));
+__device__ __forceinline__ void angles(const RopeP& p, float2* cs, int at, int lane, double first) {
+  const double pos = double(at) + (p.positions == nullptr ? double(p.start) : 0.0);  // may pass 32 bits
+  if (lane < p.R / 2) cs[lane] = turn_of(pos * first);
+  for (int i = lane + 64; i < p.R / 2; i += 64) cs[i] = turn_of(pos * rate_of(p, i));
   __builtin_amdgcn_wave_barrier();
   asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
 }
@@ -131,8 +132,9 @@ struct Head {
   }
 };
 
-// A token: whether its item holds it, and its position.  A wave looks at the next one while it
-// works on one, so that the next one's first heads are on their way too.
+// A token: whether its item holds it, and its position (without positions: behind `start`).  A
+// wave looks at the next one while it works on one, so that the next one's first heads are on
+// their way too.
 struct Token {
   int64_t row;
   int pos;
@@ -141,7 +143,7 @@ struct Token {
     if (!any) return;
     const int t = int(row % p.L);
     held = t < item_length(p.lengths, int(row / p.L), p.L);
-    if (held && p.R > 0) pos = p.positions == nullptr ? p.start + t : p.positions[row];
+    if (held && p.R > 0) pos = p.positions == nullptr ? t : p.positions[row];
   }
 };
 

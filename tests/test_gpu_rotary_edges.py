@@ -1,5 +1,5 @@
 """The norm and rotation of queries and keys at its edges: the largest heads, values that
-are not finite in elements that are not rotated.  References and
+are not finite in elements that are not rotated, positions past 32 bits.  References and
 tolerances as in tests/test_gpu_mixer.py."""
 import pytest
 
@@ -82,3 +82,17 @@ def test_values_that_are_not_finite_stay_where_they_are(ops, D, R, t, adjacent):
         assert torch.equal(got[~reach], clean[~reach])
         assert torch.equal(got[..., R:].nan_to_num(9e9), dirty[..., R:].nan_to_num(9e9))
         assert not torch.isfinite(got[..., :R][bad[..., :R]]).any()
+
+
+@pytest.mark.parametrize("start", [(1 << 31) - 3, (1 << 31) - 1, -(1 << 31) + 1])
+def test_rope_positions_past_32_bits(ops, start):
+    """Token t is at start + t, also where that is 2^31 and more.  Rates are whole multiples of
+    2^-12 and 2^-24, so that the reference's angles are exact."""
+    m = Maker(43)
+    q, dy = m(2, 6, 1, 8), m(2, 6, 1, 8)
+    freqs = torch.tensor([1.0, 3 * 2.0 ** -12, 2.0 ** -24, 0.0], device="cuda")
+    got = ops.m3_qk_norm_rope(q, None, freqs=freqs, start=start)["q"]
+    grad = ops.m3_qk_norm_rope_backward(q, dq_out=dy, freqs=freqs, start=start)["dq"]
+    want, mag = (ref.rope(q, freqs=freqs, start=start, mag=x, dy=dy) for x in (False, True))
+    close("q", got, want["y"], mag["y"], K_ROPE)
+    close("dq", grad, want["dx"], mag["dx"], 2 * K_ROPE)
