@@ -179,6 +179,21 @@ struct StepP {
   int H, Hk, K, V, lgvl, tiles;
   float scale;
 };
+// l = exp(g) as a sum of two parts of its own sign.  Of slow decays (1 - l = 2^-12 for a memory
+// of 4096 tokens) one float of l would hold 1 - l to 2^-13 of it only, the same way in every
+// step; here hi + lo is off by a few 2^-24 of 1 - l.  A lo that is above 0 keeps l times infinity.
+struct Decay {
+  float hi, lo;
+  __device__ __forceinline__ explicit Decay(float g) {
+    if (fabsf(g) < 0.5f) {
+      const float d = expm1f(g), one = 1.f + d;
+      hi = one - 0x1p-23f;  // exact
+      lo = (d - (one - 1.f)) + 0x1p-23f;
+    } else {
+      hi = lo = 0.5f * expf(g);
+    }
+  }
+};
 // S = l S + k v^T, y = scale q^T S.  One block per (sequence, head, tile of columns): 2^lgvl
 // lanes along a row of the state, W columns each, the other groups of lanes on other rows.
 // Bound by the state's way in and out: 256 sequences of 16 heads of 128 x 128, 109 us, 4.9 TB/s.
@@ -200,7 +215,7 @@ __global__ __launch_bounds__(256) void attention_step_kernel(StepP p) {
   const int lane = threadIdx.x & (lanes - 1), group = threadIdx.x >> p.lgvl;
   const int c = (tile * lanes + lane) * W;
   const bool in = c < p.V;
-  const float l = __expf(p.log_decay[h]);
+  const Decay l(p.log_decay[h]);
   float vv[W], y[W];
 #pragma unroll
   for (int i = 0; i < W; ++i) {
@@ -217,7 +232,7 @@ __global__ __launch_bounds__(256) void attention_step_kernel(StepP p) {
       const float kr = sk[r], qr = sq[r];
 #pragma unroll
       for (int i = 0; i < W; ++i) {
-        s.e[i] = fmaf(l, s.e[i], kr * vv[i]);
+        s.e[i] = fmaf(l.hi, s.e[i], fmaf(kr, vv[i], l.lo * s.e[i]));
         y[i] = fmaf(qr, s.e[i], y[i]);
       }
       *reinterpret_cast<Pack<float, W>*>(to + r * p.V) = s;
