@@ -147,20 +147,20 @@ struct ShareP {
 };
 template <typename T>
 __global__ __launch_bounds__(256) void share_kernel(ShareP p) {
-  const int64_t i = int64_t(blockIdx.x) * 256 + threadIdx.x;
-  if (i >= p.total) return;
-  const int64_t row = i / p.cols, token = row / p.Hk;
-  float s = 0.f;
-  if (int(token % p.L) < item_length(p.lengths, int(token / p.L), p.L)) {
-    const float* at = p.part + row * p.per * p.cols + i % p.cols;
-    for (int k = 0; k < p.per; ++k) s += at[int64_t(k) * p.cols];
+  for (int64_t i = int64_t(blockIdx.x) * 256 + threadIdx.x; i < p.total; i += int64_t(gridDim.x) * 256) {
+    const int64_t row = i / p.cols, token = row / p.Hk;
+    float s = 0.f;
+    if (int(token % p.L) < item_length(p.lengths, int(token / p.L), p.L)) {
+      const float* at = p.part + row * p.per * p.cols + i % p.cols;
+      for (int k = 0; k < p.per; ++k) s += at[int64_t(k) * p.cols];
+    }
+    store_scalar<T>(static_cast<T*>(p.out) + i, s);
   }
-  store_scalar<T>(static_cast<T*>(p.out) + i, s);
 }
 hipError_t share(const m3_linear_attention_args& a, const float* part, void* out, int cols, hipStream_t s) {
   const int64_t total = int64_t(a.Bt) * a.L * a.Hk * cols;
   const ShareP p{part, out, a.lengths, total, a.L, a.Hk, a.H / a.Hk, cols};
-  const dim3 grid(uint32_t((total + 255) / 256));
+  const dim3 grid(uint32_t(total < (1 << 24) ? (total + 255) / 256 : 1 << 16));
   if (a.in_dtype == M3_BF16) share_kernel<bf16_t><<<grid, dim3(256), 0, s>>>(p);
   else share_kernel<float><<<grid, dim3(256), 0, s>>>(p);
   return hipGetLastError();
@@ -266,11 +266,8 @@ StepShape step_shape(const m3_linear_attention_step_args& a) {
 }  // namespace
 
 // ---------------------------------------------------------------- entry points
-bool attention_fits(const m3_linear_attention_args& a) {
-  const Cut c = forward_cut(a);
-  const int64_t u = units(a);
-  return launchable(forward_blocks(a) * c.segs, 512) && launchable(u * ((a.K * a.V + 255) / 256), 256);
-}
+// The walks' launches; joins are of less than 256 items' heads, as only such are cut.
+bool attention_fits(const m3_linear_attention_args& a) { return launchable(forward_blocks(a) * forward_cut(a).segs, 512); }
 size_t attention_workspace(const m3_linear_attention_args& a) { return states_bytes(a, forward_cut(a).segs); }
 
 hipError_t launch_attention(const m3_linear_attention_args& a, hipStream_t s) {
@@ -311,12 +308,7 @@ hipError_t launch_attention_step(const m3_linear_attention_step_args& a, hipStre
 }
 
 bool attention_backward_fits(const m3_linear_attention_backward_args& b) {
-  const m3_linear_attention_args& a = b.fwd;
-  const Cut c = backward_cut(a);
-  const int64_t u = units(a);
-  const int64_t most = a.K > a.V ? a.K : a.V;
-  return launchable(backward_blocks(a) * c.segs, 512) && launchable(2 * u * ((a.K * a.V + 255) / 256), 256) &&
-         launchable(int64_t(a.Bt) * a.L * a.Hk * most / 256 + 1, 256);
+  return launchable(backward_blocks(b.fwd) * backward_cut(b.fwd).segs, 512);
 }
 // Workspace: the states in front of every segment, of the forward and of the reverse walk, and
 // with shared heads every head's own dk and dv in fp32.

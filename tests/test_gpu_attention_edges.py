@@ -1,12 +1,12 @@
-"""Linear attention at its edges: a token's decay over thousands of steps.
+"""Linear attention at its edges: a token's decay over thousands of steps, the largest calls.
 References and tolerances as in tests/test_gpu_mixer.py."""
 import pytest
 
 torch = pytest.importorskip("torch")
 
 from tests import mixer_ref as ref  # noqa: E402
-from tests.test_gpu_layers import Maker  # noqa: E402
-from tests.test_gpu_mixer import close  # noqa: E402
+from tests.test_gpu_layers import Maker, ilen  # noqa: E402
+from tests.test_gpu_mixer import close, k_attention, parts_of  # noqa: E402
 
 pytestmark = pytest.mark.gpu
 
@@ -51,3 +51,36 @@ def test_a_tokens_decay_of_any_size(ops):
     ops.m3_linear_attention_step(h, q, k, v, g)
     held = torch.exp(g) > 0
     assert (h[:, held] == float("inf")).all()
+
+
+def test_many_large_states(ops):
+    """65,536 items and heads of 256 x 256: within the documented limits, states apart."""
+    n, D = 65536, 256
+    gen = torch.Generator(device="cuda").manual_seed(56)
+    q, k, v, dy = (torch.randn(n, 1, 1, D, generator=gen, device="cuda").bfloat16() for _ in range(4))
+    g = torch.zeros(1, device="cuda")
+    y = ops.m3_linear_attention(q, k, v, g, want_state=False)["y"]
+    out = ops.m3_linear_attention_backward(q, k, v, g, dy=dy)
+    s = D ** -0.5
+    q, k, v, dy = (t.double() for t in (q, k, v, dy))
+    kk = k_attention(1, D, D, g.cpu(), "bf16")
+    qk, dv = (q * k).sum(-1, keepdim=True), (dy * v).sum(-1, keepdim=True)
+    mqk, mdv = (q * k).abs().sum(-1, keepdim=True), (dy * v).abs().sum(-1, keepdim=True)
+    for name, got, want, mag in (("y", y, s * qk * v, s * mqk * v.abs()), ("dq", out["dq"], s * dv * k, s * mdv * k.abs()),
+                                 ("dk", out["dk"], s * dv * q, s * mdv * q.abs()), ("dv", out["dv"], s * qk * dy, s * mqk * dy.abs())):
+        close(name, got, want.cpu(), mag.cpu(), kk, parts_of("bf16"))
+
+
+def test_gradients_of_many_shared_heads(ops):
+    """2^24 and more elements of dk and dv: the sums over the heads that share one are those of the
+    heads alone, in order."""
+    m, Bt, L, H, Hk, K, V = Maker(57), 33, 1024, 8, 4, 128, 8
+    q, k, v, dy = m(Bt, L, H, K), m(Bt, L, Hk, K), m(Bt, L, Hk, V), m(Bt, L, H, V)
+    g = -torch.linspace(0.001, 0.1, H, device="cuda")
+    n = ilen([L - 31 * b for b in range(Bt)])
+    got = ops.m3_linear_attention_backward(q, k, v, g, dy=dy, lengths=n)
+    each = ops.m3_linear_attention_backward(q, *(x.repeat_interleave(H // Hk, 2) for x in (k, v)), g, dy=dy, lengths=n)
+    assert Bt * L * Hk * K > 1 << 24 and torch.equal(got["dq"], each["dq"])
+    for x in ("dk", "dv"):
+        a, b = each[x].unflatten(2, (Hk, 2)).unbind(3)
+        assert torch.equal(got[x], a + b), x
