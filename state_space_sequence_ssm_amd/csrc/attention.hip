@@ -12,14 +12,15 @@ struct Shape {
 };
 int64_t units(const m3_linear_attention_args& a) { return int64_t(a.Bt) * a.H; }
 // Columns of c per block: 64 where eight waves share a block (bf16, a and b of up to 128), and
-// otherwise 128 where such a state fits the registers and `blocks` of them fill the card (fp32,
+// otherwise 128 where such a state fits the registers and blocks of them fill the card (fp32,
 // Bt 16, L 1024, 32 heads of 128 x 128: 503 us, by 64 columns 650; of 64 x 128: 310 and 296).
 bool two_roles(const m3_linear_attention_args& a, int b_cols) { return a.in_dtype == M3_BF16 && b_cols <= 128; }
-Shape shape_of(const m3_linear_attention_args& a, int b_cols, int c_cols, int64_t blocks, bool states) {
-  const bool wide = c_cols > 64 && b_cols <= 128 && blocks >= 256 && (states || !two_roles(a, b_cols));
+Shape walk_shape(const m3_linear_attention_args& a, int b_cols, int c_cols) {
+  const bool wide = c_cols > 64 && b_cols <= 128 && units(a) >= 256 && !two_roles(a, b_cols);
   return {blocks32(b_cols), wide ? 2 : 1};
 }
-Shape walk_shape(const m3_linear_attention_args& a, int b_cols, int c_cols) { return shape_of(a, b_cols, c_cols, units(a), false); }
+// Of segments' own states: there are never 256 items' heads to cut.
+Shape states_shape(int b_cols) { return {blocks32(b_cols), 1}; }
 int tiles(int c_cols, Shape s) { return (c_cols + 64 * s.nct - 1) / (64 * s.nct); }
 // blocks per segment of the forward, and of the backward's three walks
 int64_t forward_blocks(const m3_linear_attention_args& a) { return units(a) * tiles(a.V, walk_shape(a, a.K, a.V)); }
@@ -94,7 +95,7 @@ void to(WalkJob& j, void* out, bool f32, size_t elem) {
 }
 hipError_t run(const m3_linear_attention_args& a, WalkPlan& p, bool states, hipStream_t s) {
   const WalkJob& f = p.job[0];  // the others' states have its shape
-  const Shape h = states ? shape_of(a, f.b.cols, f.c.cols, units(a) * (p.segs - 1) * p.jobs, true) : walk_shape(a, f.b.cols, f.c.cols);
+  const Shape h = states ? states_shape(f.b.cols) : walk_shape(a, f.b.cols, f.c.cols);
   for (int i = 0; i < p.jobs; ++i) p.job[i].blocks = tiles(p.job[i].c.cols, h);
   return a.in_dtype == M3_BF16 ? launch_walk_bf16(p, h.kb, h.nct, states, s) : launch_walk_f32(p, h.kb, h.nct, states, s);
 }

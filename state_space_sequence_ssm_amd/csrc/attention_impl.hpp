@@ -1010,11 +1010,8 @@ hipError_t dispatch(const WalkPlan& p, int kb, int nct, bool states_only, hipStr
   if (states_only) {
     switch (key) {
       case 11: return launch<T, 1, 1, true>(p, s);
-      case 12: return launch<T, 1, 2, true>(p, s);
       case 21: return launch<T, 2, 1, true>(p, s);
-      case 22: return launch<T, 2, 2, true>(p, s);
       case 41: return launch<T, 4, 1, true>(p, s);
-      case 42: return launch<T, 4, 2, true>(p, s);
       case 81: return launch<T, 8, 1, true>(p, s);
     }
   } else {
