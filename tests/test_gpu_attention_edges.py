@@ -1,11 +1,11 @@
-"""Linear attention at its edges: a token's decay over thousands of steps, the largest calls.
-References and tolerances as in tests/test_gpu_mixer.py."""
+"""Linear attention at its edges: many items and heads (blocks of 128 columns), what the parts
+of bf16 products leave, a token's decay over thousands of steps, the largest calls.  References and tolerances as in tests/test_gpu_mixer.py."""
 import pytest
 
 torch = pytest.importorskip("torch")
 
-from tests import mixer_ref as ref  # noqa: E402
-from tests.test_gpu_layers import Maker, ilen  # noqa: E402
+from tests import layer_ref, mixer_ref as ref  # noqa: E402
+from tests.test_gpu_layers import BF, DT, NAN, Maker, ilen, spoil  # noqa: E402
 from tests.test_gpu_mixer import close, k_attention, parts_of  # noqa: E402
 
 pytestmark = pytest.mark.gpu
@@ -17,6 +17,94 @@ def ops():
         pytest.fail("no GPU visible to torch")
     from state_space_sequence_ssm_amd import ops as o
     return o
+
+
+# From 256 items' heads on a block of fp32 takes 128 columns: whole, part and second tiles of
+# them, both walks of the backward by the same kernel and by two, few and many chunks.
+MANY = [
+    # Bt, L, H, Hk, K, V, dtype, lengths every 4 items
+    (64, 70, 4, 2, 128, 128, "f32", None),
+    (32, 100, 8, 8, 64, 100, "f32", [100, 0, 1, 65]),
+    (16, 65, 16, 4, 32, 128, "f32", [65, 64, 63, 3]),
+    (44, 30, 6, 3, 80, 200, "f32", [30, 1, 0, 29]),
+    (64, 200, 4, 4, 64, 96, "f32", [200, 129, 128, 5]),
+    (32, 20, 8, 2, 100, 40, "f32", None),
+    (64, 70, 4, 2, 64, 128, "bf16", [70, 0, 64, 1]),
+]
+
+
+@pytest.mark.parametrize("c", MANY, ids=str)
+def test_many_items_and_heads(ops, c):
+    Bt, L, H, Hk, K, V, dt, some = c
+    lengths = None if some is None else [some[b % 4] for b in range(Bt)]
+    m, t = Maker(51), DT[dt]
+    q, k, v, dy = (spoil(m(Bt, L, h, d, dtype=t), lengths) for h, d in ((H, K), (Hk, K), (Hk, V), (H, V)))
+    h0, dh = m(Bt, H, K, V), m(Bt, H, K, V)
+    g = -torch.linspace(0.0, 0.4, H, device="cuda") ** 2
+    want, mag = (ref.attention(q, k, v, g, h0, lengths=lengths, mag=x, dy=dy, dh_final=dh) for x in (False, True))
+    kk, parts = k_attention(L, K, V, g.cpu(), dt), parts_of(dt)
+    y = torch.full((Bt, L, H, V), 7.0, dtype=t, device="cuda")
+    hf = torch.full((Bt, H, K, V), NAN, device="cuda")
+    ops.m3_linear_attention(q, k, v, g, h0, lengths=ilen(lengths), y=y, h_final=hf)
+    for b, n in enumerate(layer_ref.held(lengths, Bt, L)):
+        close("y", y[b, :n], want["y"][b, :n], mag["y"][b, :n], kk, parts)
+        assert (y[b, n:] == 7).all()
+    close("h", hf, want["h"], mag["h"], kk)
+    shapes = dict(dq=(Bt, L, H, K), dk=(Bt, L, Hk, K), dv=(Bt, L, Hk, V))
+    out = {n: torch.full(s, NAN, dtype=t, device="cuda") for n, s in shapes.items()}
+    out["dh0"] = torch.full((Bt, H, K, V), NAN, device="cuda")
+    got = ops.m3_linear_attention_backward(q, k, v, g, h0, dy=dy, dh_final=dh, lengths=ilen(lengths), out=out)
+    for n in ("dq", "dk", "dv"):
+        close(n, got[n], want[n], mag[n], kk + H // Hk, parts)
+    close("dh0", got["dh0"], want["dh0"], mag["dh0"], kk)
+
+
+# What parts leave.  One token of an item holds values, so that nothing hides it behind sums.
+# With U = 2^-24: its state is w k v^T; the power w = exp2(x), x = d log2(e) log_decay below 1 here,
+# is off by x's two roundings and its own step (4 U), w v rounds once, three parts leave 2^-24, and
+# three sums of them, counted twice as the matrix cores may drop what they round, are 6 U: 12 U;
+# every further chunk multiplies by another power, 5 U.  Two parts would leave up to 2^-16 = 256 U.
+@pytest.mark.parametrize("L,at,chunks", [(64, 20, 1), (64, 63, 1), (40, 7, 1), (200, 130, 2), (1500, 1400, 3)])
+@pytest.mark.parametrize("K,V", [(32, 32), (64, 64), (128, 96), (256, 64)])
+def test_states_keep_what_three_parts_hold(ops, K, V, L, at, chunks):
+    m = Maker(52)
+    q, k, v = (torch.zeros(1, L, 2, d, dtype=BF, device="cuda") for d in (K, K, V))
+    k[:, at], v[:, at] = m(1, 2, K, dtype=BF), m(1, 2, V, dtype=BF)
+    g = -torch.tensor([0.0061, 0.0003], device="cuda")
+    want = ref.attention(q, k, v, g)["h"]
+    bound = (12 + 5 * (chunks - 1)) * 2.0 ** -24 * want.abs()
+    for workspace in (None, False):
+        h = ops.m3_linear_attention(q, k, v, g, workspace=workspace)["h"].cpu().double()
+        assert ((h - want).abs() <= bound).all(), float(((h - want).abs() / want.abs().clamp(min=1e-30)).max() * 2 ** 24)
+    two = (w2 := (want / k[0, at].cpu().double()[..., None]).float()).bfloat16().float()
+    two = two + (w2 - two).bfloat16().float()
+    # (the last token's weight is 1 and leaves v, which one part holds)
+    assert at == L - 1 or ((two.double() * k[0, at].cpu().double()[..., None] - want).abs() > bound).any(), "two parts would pass"
+
+
+# Scores and the state read are in two parts, 2^-16 of a term.  Two terms that nearly cancel
+# show it through the rounding of the output, 2^-8 of what is left of them: s - s' is a 64th of
+# either.  One part would be off by up to 2^-8 of the terms.  Powers are 1 (no decay) and few
+# elements are not zero, so that a handful of roundings is all there is beside.
+@pytest.mark.parametrize("where", ["scores", "state"])
+@pytest.mark.parametrize("K,V", [(32, 32), (64, 64), (128, 96), (256, 64)])
+def test_outputs_keep_what_two_parts_hold(ops, K, V, where):
+    m, L = Maker(53), 64
+    q, k, v = (torch.zeros(1, L, 1, d, dtype=BF, device="cuda") for d in (K, K, V))
+    g, h0 = torch.zeros(1, device="cuda"), None
+    a = m(V)
+    q[..., 0] = m(1, L, 1, shift=2.0, scale=0.3, dtype=BF)
+    if where == "scores":  # keys equal but for a small element, values opposite
+        q[..., 5] = q[..., 0]
+        k[0, 3, 0, 0], k[0, 9, 0, 0], k[0, 9, 0, 5] = 1.3, 1.3, 1.3 / 64
+        v[0, 3, 0], v[0, 9, 0] = a.bfloat16(), -a.bfloat16()
+    else:  # two rows of the state met by queries of opposite sign
+        q[..., 1] = -q[..., 0]
+        h0 = torch.zeros(1, 1, K, V, device="cuda")
+        h0[0, 0, 0], h0[0, 0, 1] = a, a * (1 + 1 / 64)
+    want, mag = (ref.attention(q, k, v, g, h0, mag=x) for x in (False, True))
+    y = ops.m3_linear_attention(q, k, v, g, h0)["y"]
+    close("y", y, want["y"], mag["y"], 8, 2.0 ** -16)
 
 
 def test_a_tokens_decay_over_thousands_of_steps(ops):
