@@ -654,9 +654,10 @@ int m3_residual_norm_backward(const m3_residual_norm_backward_args* args, void* 
  * core's (A, A_tok).  Types, row distances, lengths, aliasing and limits of
  * launches as for the layer operators; the rows of a tensor [Bt, L, H, K] are
  * its tokens (H * K dense elements each), row distances are below 2^24 (of single
- * tokens: 2^40).  Launches: below 2^23 blocks of 64 columns for each item, head
- * and segment of 256 tokens or more (backward: three walks of them), 2^24 single
- * tokens' heads and columns; larger calls are M3_ERR_UNSUPPORTED.
+ * tokens, a rotation's with L = 1 too: 2^40).  Launches: below 2^23 blocks of 64
+ * columns for each item, head and segment of 256 tokens or more (backward: three
+ * walks of them), 2^24 single tokens' heads and columns; larger calls are
+ * M3_ERR_UNSUPPORTED.
  */
 
 /* Linear attention with a decay for each head:

@@ -82,8 +82,9 @@ int check_rope(m3_qk_norm_rope_args& f) {
   if (!(f.eps >= 0.f && f.eps <= 3.0e38f)) return M3_ERR_INVALID_ARG;
   if (f.q == nullptr || (f.k == nullptr) != (f.Hk == 0) || (f.k == nullptr && f.k_w != nullptr)) return M3_ERR_INVALID_ARG;
   if ((f.freqs == nullptr) != (f.R == 0) || (!f.norm && (f.q_w != nullptr || f.k_w != nullptr))) return M3_ERR_INVALID_ARG;
-  if (!set_ld(f.q_ld, int64_t(f.H) * f.D, 24)) return M3_ERR_INVALID_ARG;
-  if (f.k != nullptr && !set_ld(f.k_ld, int64_t(f.Hk) * f.D, 24)) return M3_ERR_INVALID_ARG;
+  const int bits = f.L == 1 ? 40 : 24;  // single tokens
+  if (!set_ld(f.q_ld, int64_t(f.H) * f.D, bits)) return M3_ERR_INVALID_ARG;
+  if (f.k != nullptr && !set_ld(f.k_ld, int64_t(f.Hk) * f.D, bits)) return M3_ERR_INVALID_ARG;
   return all_at({f.q, f.k}, elem(f.in_dtype)) && all_at({f.q_w, f.k_w, f.freqs, f.positions, f.lengths}, 4) ? M3_OK : M3_ERR_INVALID_ARG;
 }
 

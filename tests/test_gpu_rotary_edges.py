@@ -1,6 +1,6 @@
 """The norm and rotation of queries and keys at its edges: the largest heads, values that
-are not finite in elements that are not rotated, positions past 32 bits.  References and
-tolerances as in tests/test_gpu_mixer.py."""
+are not finite in elements that are not rotated, positions past 32 bits, far rows.
+References and tolerances as in tests/test_gpu_mixer.py."""
 import pytest
 
 torch = pytest.importorskip("torch")
@@ -96,3 +96,22 @@ def test_rope_positions_past_32_bits(ops, start):
     want, mag = (ref.rope(q, freqs=freqs, start=start, mag=x, dy=dy) for x in (False, True))
     close("q", got, want["y"], mag["y"], K_ROPE)
     close("dq", grad, want["dx"], mag["dx"], 2 * K_ROPE)
+
+
+def test_single_tokens_rows_further_apart_than_a_prompts(ops):
+    """One position of each sequence of a long batch: rows 2^24 elements apart and more."""
+    m, Bt, H, Hk, D, ld = Maker(44), 3, 4, 2, 64, (1 << 24) + 64
+    big = torch.empty(Bt * ld, dtype=BF, device="cuda").view(Bt, 1, ld)
+    q, k = (big[..., a * D:b * D].unflatten(-1, (b - a, D)) for a, b in ((0, H), (H, H + Hk)))
+    x, y = m(Bt, 1, H, D, dtype=BF), m(Bt, 1, Hk, D, dtype=BF)
+    q.copy_(x)
+    k.copy_(y)
+    w, freqs, pos = m(D), torch.rand(D // 2, generator=m.g).cuda(), torch.tensor([[5], [70000], [0]], dtype=torch.int32, device="cuda")
+    calls = (lambda q, k: ops.m3_qk_norm_rope(q, k, w, w, freqs=freqs, positions=pos),
+             lambda q, k: ops.m3_qk_norm_rope_backward(q, k, w, w, dq_out=x, dk_out=y, freqs=freqs, positions=pos))
+    for call in calls:
+        got, want = call(q, k), call(x, y)
+        assert all(torch.equal(got[n], want[n]) for n in want)
+    two = torch.empty(2 * ld, dtype=BF, device="cuda").view(1, 2, ld)[..., :H * D].unflatten(-1, (H, D))  # two tokens of one
+    with pytest.raises(ops.M3Error, match="invalid argument"):
+        ops.m3_qk_norm_rope(two, freqs=freqs)

@@ -1,4 +1,4 @@
-"""Linear attention at the edges of what it takes, without a GPU."""
+"""Linear attention and rotation at the edges of what they take, without a GPU."""
 import ctypes
 import os
 
@@ -18,3 +18,15 @@ def test_large_calls_have_a_workspace():
         assert need(ctypes.byref(a)) == Bt * L * H * (K + V) * 4, (Bt, L, H)
     a.fwd.Bt, a.fwd.H, a.fwd.V = 1 << 20, 16, 64  # 2^24 items' heads: past what a launch counts
     assert need(ctypes.byref(a)) == 0
+
+
+@built
+def test_rows_too_far_apart_are_refused():
+    """Below 2^24 elements for prompts, 2^40 for single tokens."""
+    lib, base = _lib.load(), 0x10000000
+    for L, ld in ((2, 1 << 24), (1, 1 << 40)):
+        for x in ("q_ld", "k_ld"):
+            f = _lib.QkNormRopeArgs(Bt=3, L=L, H=4, Hk=2, D=16, R=8, in_dtype=_lib.M3_BF16, norm=1, eps=1e-6, q=base, k=base * 2,
+                                    freqs=base * 3, q_out=base * 4, k_out=base * 5)
+            setattr(f, x, ld)
+            assert lib.m3_qk_norm_rope(ctypes.byref(f), None) == _lib.M3_ERR_INVALID_ARG, (L, x)
