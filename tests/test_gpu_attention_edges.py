@@ -1,5 +1,6 @@
 """Linear attention at its edges: many items and heads (blocks of 128 columns), what the parts
-of bf16 products leave, a token's decay over thousands of steps, the largest calls.  References and tolerances as in tests/test_gpu_mixer.py."""
+of bf16 products leave, a token's decay over thousands of steps, the largest calls, gradients
+of values that are not finite.  References and tolerances as in tests/test_gpu_mixer.py."""
 import pytest
 
 torch = pytest.importorskip("torch")
@@ -172,3 +173,36 @@ def test_gradients_of_many_shared_heads(ops):
     for x in ("dk", "dv"):
         a, b = each[x].unflatten(2, (Hk, 2)).unbind(3)
         assert torch.equal(got[x], a + b), x
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+def test_gradients_of_values_that_are_not_finite(ops, dt):
+    """They reach no other item and head, dq no more than 63 tokens in front of a k or v, dk and dv
+    no more than 63 behind a q or dy; of a token's own row only, where it is the row's factor."""
+    m, L, at = Maker(58), 200, 100
+    q, k, v, dy = (m(2, L, 2, 32, dtype=DT[dt]) for _ in range(4))
+    g = -torch.tensor([0.02, 0.1]).cuda()
+    want = ops.m3_linear_attention_backward(q, k, v, g, dy=dy, want_carry_grads=True)
+    own = {"q": "", "k": "dv", "v": "dk", "dy": "dq"}  # outputs whose row is a sum times this row
+    for name, x in (("q", q), ("k", k), ("v", v), ("dy", dy)):
+        for bad in (NAN, float("inf")):
+            kept = x[1, at, 1].clone()
+            x[1, at, 1] = bad
+            got = ops.m3_linear_attention_backward(q, k, v, g, dy=dy, want_carry_grads=True)
+            x[1, at, 1] = kept
+            for o in ("dq", "dk", "dv"):
+                assert torch.equal(got[o][0], want[o][0]) and torch.equal(got[o][1, :, 0], want[o][1, :, 0])
+                row, was = got[o][1, :, 1], want[o][1, :, 1]
+                if o == own[name]:
+                    same = torch.arange(L, device="cuda") != at
+                elif name in ("k", "v"):  # dq of its token and those behind; dk and dv of none
+                    same = torch.arange(L, device="cuda") < at - 63 if o == "dq" else torch.ones(L, dtype=torch.bool, device="cuda")
+                else:  # dk and dv of its token and those in front; dq of none
+                    same = torch.arange(L, device="cuda") > at + 63 if o != "dq" else torch.ones(L, dtype=torch.bool, device="cuda")
+                assert torch.equal(row[same], was[same]), (name, bad, o)
+                if not same.all():
+                    assert not torch.isfinite(row[at]).all(), (name, bad, o)
+            if name in ("k", "v"):
+                assert torch.equal(got["dh0"], want["dh0"])
+            else:
+                assert torch.equal(got["dh0"][0], want["dh0"][0]) and torch.equal(got["dh0"][1, 0], want["dh0"][1, 0])
