@@ -655,7 +655,7 @@ int m3_residual_norm_backward(const m3_residual_norm_backward_args* args, void* 
  * launches as for the layer operators; the rows of a tensor [Bt, L, H, K] are
  * its tokens (H * K dense elements each), row distances are below 2^24 (of single
  * tokens, a rotation's with L = 1 too: 2^40).  Launches: below 2^23 blocks of 64
- * columns for each item, head and segment of 256 tokens or more (backward: three
+ * columns for each item, head and segment of 192 tokens or more (backward: three
  * walks of them), 2^24 single tokens' heads and columns; larger calls are
  * M3_ERR_UNSUPPORTED.
  */
@@ -664,7 +664,9 @@ int m3_residual_norm_backward(const m3_residual_norm_backward_args* args, void* 
  *   S_t = exp(log_decay[h]) S_{t-1} + k_t v_t^T,   y_t = scale q_t^T S_t,
  * head h of q and y with head h / (H / Hk) of k and v.
  *   q [Bt, L, H, K] (q_ld), k [Bt, L, Hk, K] (k_ld), v [Bt, L, Hk, V] (v_ld),
- *   y [Bt, L, H, V]; log_decay [H] float32 (0: no decay; -inf: each token alone);
+ *   y [Bt, L, H, V]; log_decay [H] float32 (0: no decay; -inf: each token alone;
+ *   above 0 states grow, and a power of 64 tokens or of a segment past float32's
+ *   range leaves values that are not finite);
  *   h0 [Bt, H, K, V] float32 or NULL (zeros); h_final (nullable; may be h0
  *   itself): the state after the last token.
  * K and V in 1..256, Hk divides H, H V below 2^24 (of single tokens: any).
@@ -720,7 +722,10 @@ int m3_linear_attention_step(const m3_linear_attention_step_args* args, void* st
 /* Its gradients for dy [Bt, L, H, V] (dense) and dh_final [Bt, H, K, V]
  * (nullable): dq [Bt, L, H, K], dk [Bt, L, Hk, K], dv [Bt, L, Hk, V] in in_dtype
  * (shared heads: summed over the heads that share them, in a fixed order) and
- * dh0 [Bt, H, K, V] (nullable).  log_decay is a constant.  workspace:
+ * dh0 [Bt, H, K, V] (nullable).  log_decay is a constant.  With 64 tokens at a
+ * time, a value that is not finite reaches, beside what depends on it, of k or v
+ * the dq of its item and head up to 63 tokens in front, of q or dy their dk and dv
+ * up to 63 tokens behind.  workspace:
  * m3_linear_attention_backward_workspace_size bytes, 256-byte aligned (0: none
  * is needed). */
 typedef struct m3_linear_attention_backward_args {

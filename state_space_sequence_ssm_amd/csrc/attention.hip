@@ -28,11 +28,12 @@ int64_t backward_blocks(const m3_linear_attention_args& a) {
   return units(a) * (2 * tiles(a.K, walk_shape(a, a.V, a.K)) + tiles(a.V, walk_shape(a, a.K, a.V)));
 }
 
-// Segments of the token axis, each of 256 tokens at least: `want` blocks where there are fewer
-// than 256.  One a compute unit of the forward's blocks of eight waves (16 heads of 128 x 128,
-// bf16, one item of 4096 tokens: 58 us, with two 67, uncut 131; of 16384: 138, 143, 488), two of
-// four waves (fp32, 4 x 4096 tokens of 16 heads of 64 x 64: 120 us, with one 137, uncut 342),
-// and two for the backward's three walks (16384 tokens as above: 412 us, with one 489).
+// Segments of the token axis, at most one for each 256 tokens or part of them, in whole chunks
+// (192 tokens at least, but for the last one): `want` blocks where there are fewer than 256.  One
+// a compute unit of the forward's blocks of eight waves (16 heads of 128 x 128, bf16, one item of
+// 4096 tokens: 58 us, with two 67, uncut 131; of 16384: 138, 143, 488), two of four waves (fp32,
+// 4 x 4096 tokens of 16 heads of 64 x 64: 120 us, with one 137, uncut 342), and two for the
+// backward's three walks (16384 tokens as above: 412 us, with one 489).
 void segments(int64_t blocks, int most_blocks, int L, int& len, int& segs) {
   int64_t want = blocks >= 256 ? 1 : (most_blocks + blocks - 1) / blocks;
   const int64_t most = (L + 255) / 256;
@@ -197,7 +198,7 @@ struct Decay {
 };
 // S = l S + k v^T, y = scale q^T S.  One block per (sequence, head, tile of columns): 2^lgvl
 // lanes along a row of the state, W columns each, the other groups of lanes on other rows.
-// Bound by the state's way in and out: 256 sequences of 16 heads of 128 x 128, 109 us, 4.9 TB/s.
+// Bound by the state's way in and out: 256 sequences of 16 heads of 128 x 128, 107 us, 5.0 TB/s.
 template <typename T, int W>
 __global__ __launch_bounds__(256) void attention_step_kernel(StepP p) {
   __shared__ float sq[256], sk[256], red[256 * W];

@@ -15,8 +15,8 @@ using namespace rope;
 // RAG: words have the alignment of their elements only, and a range's last unit is moved back
 // to end with it, its first elements, which the unit before holds too, left out of the sums
 // and stored twice with the same value.
-// 32768 tokens of 16 + 16 heads of 128 bf16: 113 us, 4.8 TB/s (one token's loads at a time and
-// gains read for each head: 157); backward of 16 + 4 heads 151 us, 3.3 TB/s: 192 registers leave
+// 32768 tokens of 16 + 16 heads of 128 bf16: 104 us, 5.1 TB/s (one token's loads at a time and
+// gains read for each head: 157); backward of 16 + 4 heads 152 us, 3.3 TB/s: 198 registers leave
 // two waves a SIMD, which wait for memory three quarters of the time (three spill: slower).
 
 // cos and sin of 2 pi r, r in turns: reduced in 64 bits to an eighth of a turn around a
